@@ -251,6 +251,11 @@ def kernel_work(wl, name):
         "mhla_ln_rows": ("hbm", 2 * io), "mhla_lepe_add": ("hbm", 3 * io),
         "mhla_gemm_qkv": ("tensor", 2 * wl.tokens * (wl.H * d) * 3 * (wl.H * d)),
         "mhla_gemm_out": ("tensor", 2 * wl.tokens * (wl.H * d) * (wl.H * d)),
+        # gated recurrence: read q, k, v, write o (a backward scan: three tensors in, one out)
+        "gated_scan": ("hbm", 4 * io), "gated_gate_grad": ("hbm", BH * wl.N * (2 * 4 + wl.elem_bytes)),
+        # norm and rotation: q and k in and out; with both output gradients in
+        "qk_norm": ("hbm", 4 * io), "qk_norm_backward": ("hbm", 6 * io),
+        "qk_norm_weight_grad": ("hbm", 2 * d * 4),
     }
     return table.get(name, ("hbm", 0))
 

@@ -425,6 +425,143 @@ mhla_status_t mhla_module_forward(const void* x, void* y, int64_t B, int64_t N, 
                                   const mhla_phi_t* phi, void* workspace, size_t workspace_bytes,
                                   void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Gated causal linear attention, and what its queries and keys pass through
+ * first.  The causal form above weighs a past block by W[i][j] whatever the
+ * tokens say and needs the sequence's length in W; this form forgets by a decay
+ * that every token brings with it, takes any length, and continues one token at
+ * a time from a d x d state, which is how a language model of this kind is
+ * served.  The chain a model runs: mhla_linear (q, k, v, decays), mhla_qk_norm,
+ * mhla_gated_forward or mhla_gated_step, mhla_linear.
+ * ------------------------------------------------------------------------ */
+
+/* The recurrence, per batch b and head h, for t = 0 .. N - 1:
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T      (d x d, S_{-1} = state_in or 0)
+ *   o_t = scale * S_t^T q_t                 (o_t[c] = scale * sum_r q_t[r] S_t[r][c])
+ * No feature map and no normaliser: q and k are taken as given.  N is any
+ * length >= 1, in raster order of whatever the caller's sequence is.
+ *   q, k, v     device tensors [B, N, H, d], same shape and dtype, any strides
+ *               (a stride of 0 shares a row), d <= 128.
+ *   g           device tensor [B, N, H, 1] of the same dtype: log decays, <= 0
+ *               (a larger value grows the state and overflows as exp does).
+ *               Values below -1000, -infinity among them, count as -1000, whose
+ *               exp is 0 in float32: such a token starts from an empty state,
+ *               so sequences can be packed one behind another in a row.  A
+ *               padding token with k = 0 and g = 0 leaves the state as it is.
+ *   state_in    device float32 [B][H][d][d] (S[r][c], r of k, c of v), or NULL
+ *               for zero; finite.
+ *   out         device tensor, same shape and dtype as q.
+ *   state_out   receives S_{N-1}, layout of state_in, or NULL; may be state_in
+ *               itself, and overlaps nothing else.
+ *   scale       finite.
+ * The states and every sum are float32 or wider; bf16 results are rounded once.
+ * Both dtypes run on the tensor cores, over chunks of 64 tokens: within a chunk
+ * as a masked product, from chunk to chunk through the state, whose products
+ * enter the tensor cores as sums of bf16 terms (three where the result is
+ * float32).
+ *   out may be one of several views interleaved in a token's row (a
+ *   projection's [B, N, 3C]); it must share no element with an input.
+ *   workspace as for mhla_forward.  Asynchronous on stream; statuses as for
+ *   mhla_forward, MHLA_ERR_SHAPE when q, k, v, out or g do not agree.
+ * B == 0 or H == 0 queues nothing. */
+mhla_status_t mhla_gated_workspace_size(const mhla_tensor_t* q, size_t* bytes);
+mhla_status_t mhla_gated_forward(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v,
+                                 const mhla_tensor_t* g, float scale, const float* state_in,
+                                 const mhla_tensor_t* out, float* state_out, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Gradients of mhla_gated_forward, given dout = dL/d(out) and, when the last
+ * state goes on into the loss, dstate_out = dL/d(state_out) (NULL: zero).  With
+ * dS_{N-1} = scale q_{N-1} dout_{N-1}^T + dstate_out and, before it,
+ *   dS_t = scale q_t dout_t^T + exp(g_{t+1}) dS_{t+1}:
+ *   dq_t = scale S_t dout_t,   dk_t = dS_t v_t,   dv_t = dS_t^T k_t,
+ *   dg_t = exp(g_t) <S_{t-1}, dS_t>,   dstate_in = exp(g_0) dS_0.
+ * dg_t is taken as a running sum of q_t . dq_t - k_t . dk_t in float32 from
+ * the unrounded dq and dk, restarted with <S, dS> at the end of every span of
+ * the sequence.
+ *   q, k, v, g, scale, state_in   those of the forward.
+ *   dout, dq, dk, dv  device tensors shaped like q;  dg  shaped like g.
+ *   dstate_in    device float32 [B][H][d][d], or NULL when not wanted.
+ * The written tensors share no element with one another or with an input (views
+ * interleaved in a token's row are fine).  The states are recomputed from k, v
+ * and g.  workspace, stream, statuses and empty calls as for the forward. */
+mhla_status_t mhla_gated_backward_workspace_size(const mhla_tensor_t* q, size_t* bytes);
+mhla_status_t mhla_gated_backward(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v,
+                                  const mhla_tensor_t* g, const mhla_tensor_t* dout, float scale,
+                                  const float* state_in, const float* dstate_out, const mhla_tensor_t* dq,
+                                  const mhla_tensor_t* dk, const mhla_tensor_t* dv, const mhla_tensor_t* dg,
+                                  float* dstate_in, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of the recurrence for every (b, h), for serving: tensors of N == 1
+ * (MHLA_ERR_SHAPE otherwise), state [B][H][d][d] float32 read, updated in place
+ * and used for out; float32 arithmetic.  The same result as mhla_gated_forward
+ * with state_in == state_out == state, in one launch without a workspace.  out
+ * and state overlap nothing else. */
+mhla_status_t mhla_gated_step(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v,
+                              const mhla_tensor_t* g, float scale, float* state, const mhla_tensor_t* out,
+                              void* stream);
+
+/* Which channels of a head turn together. */
+typedef enum mhla_rotation_layout {
+    MHLA_ROTATION_HALF = 0,        /* pair i is channels i and i + pairs       */
+    MHLA_ROTATION_INTERLEAVED = 1  /* pair i is channels 2 i and 2 i + 1       */
+} mhla_rotation_layout_t;
+
+/* Builds a rotation table from token coordinates: row n, pair i holds
+ * (cos a, sin a).  The token's coordinate on axis x of the grid (raster order)
+ * turns pairs[x] pairs, axis after axis: the i-th of them by
+ * a = coordinate * base^(-i / pairs[x]).  A 1-D sequence is grid (1, N) with
+ * pairs (0, n).  Angles, cosines and sines in double, rounded once to float32.
+ *   pairs       one count per grid axis, >= 0;  base > 0, finite.
+ *   table_host  host memory the caller owns, room for table_capacity floats;
+ *               receives prod(grid) * sum(pairs) * 2 values.
+ * Host only; MHLA_ERR_INVALID_ARG / SHAPE as for mhla_init_mixing. */
+mhla_status_t mhla_init_rotation(const mhla_shape3_t* grid, const int32_t* pairs, double base, float* table_host,
+                                 int64_t table_capacity);
+
+/* The position rotation of mhla_qk_norm. */
+typedef struct mhla_rotation {
+    const float* table;        /* device float32 [rows][pairs][2]: cos, sin; 8-byte aligned; NULL: no rotation */
+    const int32_t* positions;  /* device [B][N]: row of each token, or NULL: row n for token n (rows >= N).
+                                  A negative position leaves the token unrotated (padding); one past the
+                                  table gives NaN in the rotated channels. */
+    int64_t rows;
+    int32_t pairs;             /* 2 * pairs <= d; the channels behind them are not rotated */
+    int32_t layout;            /* mhla_rotation_layout_t */
+} mhla_rotation_t;
+
+/* Norm of every query and key head, and its rotation, in one pass ([P1] section
+ * 7, MHLA.q_norm and k_norm, with the root-mean-square norm in their place):
+ *   y = x / sqrt(mean(x^2) + eps) * weight,   then pair (a, b) of y becomes
+ *   (a cos - b sin, a sin + b cos).
+ *   q, q_out   device tensors [B, N, H, d];  k, k_out  [B, N, Hk, d] of the same
+ *              B, N, d and dtype (fewer key heads are fine), any strides, d <= 128.
+ *   q_weight, k_weight  device float32 [d], or NULL for ones.
+ *   eps        finite, >= 0;  rot  the rotation, or NULL for the norm alone.
+ * q_out may be q itself (same address and strides), k_out may be k: a
+ * projection's views are normed in place.  Otherwise outputs share no element
+ * with one another, an input, a weight or the table.  float32 arithmetic,
+ * results rounded once.  Asynchronous on stream; B == 0 queues nothing. */
+mhla_status_t mhla_qk_norm(const mhla_tensor_t* q, const mhla_tensor_t* k, const float* q_weight,
+                           const float* k_weight, float eps, const mhla_rotation_t* rot,
+                           const mhla_tensor_t* q_out, const mhla_tensor_t* k_out, void* stream);
+
+/* Gradients of mhla_qk_norm: with dy the rotation's transpose applied to
+ * dq_out (dk_out), r = 1 / sqrt(mean(x^2) + eps) and u = x r,
+ *   dx = r (weight dy - u mean(u weight dy)),   dweight = sum over b, n, h of dy u.
+ *   q, k, weights, eps, rot   those of the forward (q, k before the norm).
+ *   dq_out, dk_out in; dq, dk out, shaped like q and k; dq may be dq_out itself
+ *   (same address and strides), dk may be dk_out.  Otherwise as above.
+ *   dq_weight, dk_weight  device float32 [d], overwritten, or NULL when not
+ *   wanted; summed in a fixed order (the same bits every time).
+ *   workspace as for mhla_forward; its size depends on d alone. */
+mhla_status_t mhla_qk_norm_backward_workspace_size(const mhla_tensor_t* q, size_t* bytes);
+mhla_status_t mhla_qk_norm_backward(const mhla_tensor_t* q, const mhla_tensor_t* k, const float* q_weight,
+                                    const float* k_weight, float eps, const mhla_rotation_t* rot,
+                                    const mhla_tensor_t* dq_out, const mhla_tensor_t* dk_out,
+                                    const mhla_tensor_t* dq, const mhla_tensor_t* dk, float* dq_weight,
+                                    float* dk_weight, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Reads and clears the device error words the tensor-core and fused kernels
  * set when one of their bounded waits gives up (bit 0: pipeline wait timeout;
  * bit 1: a copy or MMA still in flight when the kernel gave up did not finish

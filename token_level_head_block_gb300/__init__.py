@@ -20,7 +20,9 @@ __all__ = [
     "device_status", "profile_begin", "layer_norm", "lepe_add", "module_forward",
     "module_workspace_size",
     "profile_end", "tensor_desc", "shape3",
-    "PATHS", "TRANSFORMS",
+    "gated_forward", "gated_workspace_size", "gated_backward", "gated_backward_workspace_size", "gated_step",
+    "init_rotation", "qk_norm", "qk_norm_backward", "qk_norm_backward_workspace_size",
+    "PATHS", "TRANSFORMS", "ROTATION_LAYOUTS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -30,6 +32,7 @@ PATHS = {"auto": 0, "simt": 1, "tc": 2, "fused": 3, "tc_fused": 4}
 TRANSFORMS = {"linear": 0, "cos": 1, "exp": 2, "gaussian": 3, "local": 4}
 PHIS = {"relu": 0, "relu_eps": 1}
 DTYPES = {"bf16": 0, "f32": 1}
+ROTATION_LAYOUTS = {"half": 0, "interleaved": 1}
 
 STATUS = {
     0: "ok", 1: "invalid argument", 2: "shape mismatch", 3: "unsupported by the selected path",
@@ -71,6 +74,14 @@ class ModuleParams(ctypes.Structure):
         ("lepe_weight", ctypes.c_void_p), ("lepe_bias", ctypes.c_void_p),
         ("out_weight", ctypes.c_void_p), ("out_bias", ctypes.c_void_p),
         ("ln_eps", ctypes.c_float), ("heads", ctypes.c_int32),
+    ]
+
+
+class Rotation(ctypes.Structure):
+    """mhla_rotation_t: the table, the rows of the tokens and which channels pair up."""
+    _fields_ = [
+        ("table", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rows", ctypes.c_int64),
+        ("pairs", ctypes.c_int32), ("layout", ctypes.c_int32),
     ]
 
 
@@ -136,6 +147,22 @@ def lib():
                                       ctypes.c_int64, P(ModuleParams), ctypes.c_void_p, P(Shape3), P(Shape3),
                                       P(Phi), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     L.mhla_module_forward.restype = ctypes.c_int
+    V, T = ctypes.c_void_p, P(Tensor)
+    L.mhla_gated_workspace_size.argtypes = [T, P(ctypes.c_size_t)]
+    L.mhla_gated_backward_workspace_size.argtypes = [T, P(ctypes.c_size_t)]
+    L.mhla_gated_forward.argtypes = [T, T, T, T, ctypes.c_float, V, T, V, V, ctypes.c_size_t, V]
+    L.mhla_gated_backward.argtypes = [T, T, T, T, T, ctypes.c_float, V, V, T, T, T, T, V, V, ctypes.c_size_t, V]
+    L.mhla_gated_step.argtypes = [T, T, T, T, ctypes.c_float, V, T, V]
+    L.mhla_init_rotation.argtypes = [P(Shape3), P(ctypes.c_int32), ctypes.c_double, P(ctypes.c_float),
+                                     ctypes.c_int64]
+    L.mhla_qk_norm.argtypes = [T, T, V, V, ctypes.c_float, P(Rotation), T, T, V]
+    L.mhla_qk_norm_backward_workspace_size.argtypes = [T, P(ctypes.c_size_t)]
+    L.mhla_qk_norm_backward.argtypes = [T, T, V, V, ctypes.c_float, P(Rotation), T, T, T, T, V, V, V,
+                                        ctypes.c_size_t, V]
+    for name in ("mhla_gated_workspace_size", "mhla_gated_backward_workspace_size", "mhla_gated_forward",
+                 "mhla_gated_backward", "mhla_gated_step", "mhla_init_rotation", "mhla_qk_norm",
+                 "mhla_qk_norm_backward_workspace_size", "mhla_qk_norm_backward"):
+        getattr(L, name).restype = ctypes.c_int
     L.mhla_debug_stall_waits.argtypes = [ctypes.c_int32, ctypes.c_uint64]
     L.mhla_debug_stall_waits.restype = ctypes.c_int
     L.mhla_device_status.argtypes = [ctypes.c_void_p, P(ctypes.c_uint32)]
@@ -444,6 +471,241 @@ def module_forward(x, params, W, grid, block, heads, phi="relu_eps", eps=1e-6, l
                                    _stream_ptr(stream, x.device))
     _check(st, "mhla_module_forward")
     return out
+
+
+# --------------------------------------------------- gated recurrence, query/key norm
+
+
+def _dtype_code(x):
+    import torch
+    if x.dtype == torch.bfloat16:
+        return 0
+    if x.dtype == torch.float32:
+        return 1
+    raise ValueError(f"unsupported dtype {x.dtype}")
+
+
+def _heads(x):
+    """mhla_tensor_t of a [B, N, H, d] tensor, in one call of the constructor (serving calls this per token)."""
+    B, N, H, d = x.shape
+    sb, sn, sh, sd = x.stride()
+    if d > 1 and sd != 1:
+        raise ValueError("the d dimension must be contiguous")
+    return Tensor(x.data_ptr() or None, _dtype_code(x), 0, B, N, H, d, sb, sn, sh)
+
+
+def _gates(x):
+    """mhla_tensor_t of a [B, N, H] tensor of one value per token and head."""
+    B, N, H = x.shape
+    return Tensor(x.data_ptr() or None, _dtype_code(x), 0, B, N, H, 1, *x.stride())
+
+
+def _float_array(name, x, shape, like):
+    """Address of a contiguous float32 tensor of this shape on like's device, or None."""
+    import torch
+    if x is None:
+        return None
+    if x.dtype != torch.float32 or tuple(x.shape) != shape or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {list(shape)}")
+    if x.device != like.device:
+        raise ValueError(f"{name} is on {x.device}, not on {like.device}")
+    return x.data_ptr()
+
+
+def _same_device(like, **tensors):
+    for name, x in tensors.items():
+        if x.device != like.device:
+            raise ValueError(f"{name} is on {x.device}, not on {like.device}")
+
+
+def _on_device(fn, x, stream, workspace, need):
+    """fn(workspace address, bytes, stream) with x's device current.  Without a workspace of
+    the caller's, need() bytes come from torch's allocator on that stream."""
+    import torch
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _on_device(fn, x, stream, workspace, need)
+    if stream is None:
+        s = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if need is None:
+        return fn(None, 0, s or None)
+    if workspace is not None:
+        return fn(workspace.data_ptr(), workspace.numel() * workspace.element_size(), s or None)
+    n = need()
+    if n == 0 or s != torch.cuda.current_stream(dev).cuda_stream:
+        return fn(None, 0, s or None)   # another stream: the library's stream-ordered allocation
+    scratch = torch.empty(n, dtype=torch.uint8, device=dev)
+    return fn(scratch.data_ptr(), n, s or None)
+
+
+def _size(fn, what, desc):
+    n = ctypes.c_size_t(0)
+    _check(fn(ctypes.byref(desc), ctypes.byref(n)), what)
+    return n.value
+
+
+def gated_workspace_size(q):
+    return _size(lib().mhla_gated_workspace_size, "mhla_gated_workspace_size", _heads(q))
+
+
+def gated_backward_workspace_size(q):
+    return _size(lib().mhla_gated_backward_workspace_size, "mhla_gated_backward_workspace_size", _heads(q))
+
+
+def gated_forward(q, k, v, g, scale=1.0, state=None, out=None, state_out=None, workspace=None, stream=None):
+    """Gated causal linear attention S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
+
+    q, k, v: CUDA tensors [B, N, H, d]; g: log decays [B, N, H] of the same
+    dtype; state: float32 [B, H, d, d] before the first token (None: zero).
+    Returns (out, state_out); state_out (allocated when not given) may be state.
+    """
+    import torch
+    B, N, H, d = q.shape
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    if state_out is None:
+        state_out = torch.empty(B, H, d, d, dtype=torch.float32, device=q.device)
+    _same_device(q, k=k, v=v, g=g, out=out)
+    s_in = _float_array("state", state, (B, H, d, d), q)
+    s_out = _float_array("state_out", state_out, (B, H, d, d), q)
+    dq = _heads(q)
+    L = lib()
+    st = _on_device(
+        lambda ws, n, s: L.mhla_gated_forward(dq, _heads(k), _heads(v), _gates(g), scale, s_in, _heads(out), s_out,
+                                              ws, n, s),
+        q, stream, workspace, lambda: _size(L.mhla_gated_workspace_size, "mhla_gated_workspace_size", dq))
+    _check(st, "mhla_gated_forward")
+    return out, state_out
+
+
+def gated_backward(q, k, v, g, dout, scale=1.0, state=None, dstate_out=None, dq=None, dk=None, dv=None, dg=None,
+                   dstate=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dv, dg, dstate) of ``gated_forward`` given dout and,
+    when the last state is used, dstate_out (float32 [B, H, d, d])."""
+    import torch
+    B, N, H, d = q.shape
+    new = lambda given: torch.empty(q.shape, dtype=q.dtype, device=q.device) if given is None else given
+    dq, dk, dv = new(dq), new(dk), new(dv)
+    dg = torch.empty(B, N, H, dtype=q.dtype, device=q.device) if dg is None else dg
+    if dstate is None:
+        dstate = torch.empty(B, H, d, d, dtype=torch.float32, device=q.device)
+    _same_device(q, k=k, v=v, g=g, dout=dout, dq=dq, dk=dk, dv=dv, dg=dg)
+    s_in = _float_array("state", state, (B, H, d, d), q)
+    ds_out = _float_array("dstate_out", dstate_out, (B, H, d, d), q)
+    ds_in = _float_array("dstate", dstate, (B, H, d, d), q)
+    desc = _heads(q)
+    L = lib()
+    st = _on_device(
+        lambda ws, n, s: L.mhla_gated_backward(desc, _heads(k), _heads(v), _gates(g), _heads(dout), scale, s_in, ds_out,
+                                               _heads(dq), _heads(dk), _heads(dv), _gates(dg), ds_in, ws, n, s),
+        q, stream, workspace,
+        lambda: _size(L.mhla_gated_backward_workspace_size, "mhla_gated_backward_workspace_size", desc))
+    _check(st, "mhla_gated_backward")
+    return dq, dk, dv, dg, dstate
+
+
+def gated_step(q, k, v, g, state, scale=1.0, out=None, stream=None):
+    """One token for every sequence: tensors [B, 1, H, d], g [B, 1, H]; ``state``
+    (float32 [B, H, d, d]) is updated in place.  Returns ``out``."""
+    import torch
+    B, N, H, d = q.shape
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    _same_device(q, k=k, v=v, g=g, out=out)
+    s = _float_array("state", state, (B, H, d, d), q)
+    st = _on_device(
+        lambda ws, n, sp: lib().mhla_gated_step(_heads(q), _heads(k), _heads(v), _gates(g), scale, s, _heads(out), sp),
+        q, stream, None, None)
+    _check(st, "mhla_gated_step")
+    return out
+
+
+def init_rotation(grid, pairs, base=10000.0):
+    """Rotation table [prod(grid), sum(pairs), 2] (cos, sin; float32, host) of the token
+    coordinates on a grid; ``pairs`` gives the rotated pairs of each grid axis
+    (a sequence of N tokens: grid (1, N), pairs (0, n))."""
+    grid = tuple(int(e) for e in grid)
+    if len(pairs) != len(grid):
+        raise ValueError("pairs needs one count per grid axis")
+    n = 1
+    for e in grid:
+        n *= e
+    total = sum(int(p) for p in pairs)
+    table = np.empty((max(n, 0), max(total, 0), 2), dtype=np.float32)
+    st = lib().mhla_init_rotation(ctypes.byref(shape3(grid)), (ctypes.c_int32 * 3)(*pairs), float(base),
+                                  table.ctypes.data_as(ctypes.POINTER(ctypes.c_float)), table.size)
+    _check(st, "mhla_init_rotation")
+    return table
+
+
+def _rotation(x, table, positions, layout):
+    import torch
+    if layout not in ROTATION_LAYOUTS:
+        raise ValueError(f"unknown rotation layout {layout!r}")
+    if table is None:
+        return None
+    if table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError("the rotation table is [rows, pairs, 2]")
+    ptr = _float_array("table", table, tuple(table.shape), x)
+    pos = None
+    if positions is not None:
+        if positions.dtype != torch.int32 or tuple(positions.shape) != tuple(x.shape[:2]) \
+                or not positions.is_contiguous():
+            raise ValueError(f"positions must be a contiguous int32 tensor of shape {list(x.shape[:2])}")
+        _same_device(x, positions=positions)
+        pos = positions.data_ptr()
+    return Rotation(ptr or None, pos, table.shape[0], table.shape[1], ROTATION_LAYOUTS[layout])
+
+
+def qk_norm(q, k, q_weight=None, k_weight=None, eps=1e-6, table=None, positions=None, layout="half", q_out=None,
+            k_out=None, stream=None):
+    """Root-mean-square norm of every head of q [B, N, H, d] and k [B, N, Hk, d] (float32
+    weights [d]) and its rotation by ``table`` ([rows, pairs, 2], see ``init_rotation``) at
+    ``positions`` (int32 [B, N]; None: 0 .. N-1).  Returns (q_out, k_out), which may be q and k."""
+    import torch
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+    _same_device(q, k=k, q_out=q_out, k_out=k_out)
+    d = q.shape[3]
+    wq, wk = _float_array("q_weight", q_weight, (d,), q), _float_array("k_weight", k_weight, (d,), q)
+    rot = _rotation(q, table, positions, layout)
+    st = _on_device(
+        lambda ws, n, s: lib().mhla_qk_norm(_heads(q), _heads(k), wq, wk, eps, rot, _heads(q_out), _heads(k_out), s),
+        q, stream, None, None)
+    _check(st, "mhla_qk_norm")
+    return q_out, k_out
+
+
+def qk_norm_backward_workspace_size(q):
+    return _size(lib().mhla_qk_norm_backward_workspace_size, "mhla_qk_norm_backward_workspace_size", _heads(q))
+
+
+def qk_norm_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, eps=1e-6, table=None, positions=None,
+                     layout="half", dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dq_weight, dk_weight) of ``qk_norm`` for its inputs q, k;
+    dq may be dq_out and dk dk_out."""
+    import torch
+    d = q.shape[3]
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
+    new = lambda given: torch.empty(d, dtype=torch.float32, device=q.device) if given is None else given
+    dq_weight, dk_weight = new(dq_weight), new(dk_weight)
+    _same_device(q, k=k, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk)
+    wq, wk = _float_array("q_weight", q_weight, (d,), q), _float_array("k_weight", k_weight, (d,), q)
+    gq, gk = _float_array("dq_weight", dq_weight, (d,), q), _float_array("dk_weight", dk_weight, (d,), q)
+    rot = _rotation(q, table, positions, layout)
+    desc = _heads(q)
+    L = lib()
+    st = _on_device(
+        lambda ws, n, s: L.mhla_qk_norm_backward(desc, _heads(k), wq, wk, eps, rot, _heads(dq_out), _heads(dk_out),
+                                                 _heads(dq), _heads(dk), gq, gk, ws, n, s),
+        q, stream, workspace,
+        lambda: _size(L.mhla_qk_norm_backward_workspace_size, "mhla_qk_norm_backward_workspace_size", desc))
+    _check(st, "mhla_qk_norm_backward")
+    return dq, dk, dq_weight, dk_weight
 
 
 def profile_begin():

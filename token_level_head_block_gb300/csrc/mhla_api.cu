@@ -7,53 +7,11 @@
 #include <cmath>
 #include <cstdint>
 
+#include "api_checks.h"
 #include "mhla_internal.h"
 
 namespace mhla {
 namespace {
-
-int64_t elem_bytes(int dtype) { return dtype == MHLA_BF16 ? 2 : 4; }
-
-bool valid_dtype(int dtype) { return dtype == MHLA_BF16 || dtype == MHLA_F32; }
-
-// Byte span [lo, hi) a [B, N, H, d] tensor can touch.
-void span(const mhla_tensor_t* t, uintptr_t* lo, uintptr_t* hi) {
-  const int64_t e = elem_bytes(t->dtype);
-  const int64_t last = (t->B - 1) * t->stride_b + (t->N - 1) * t->stride_n + (t->H - 1) * t->stride_h + t->d;
-  *lo = reinterpret_cast<uintptr_t>(t->data);
-  *hi = *lo + static_cast<uintptr_t>(last * e);
-}
-
-bool overlaps(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1) { return a0 < b1 && b0 < a1; }
-
-// No two (b, n, h, c) index tuples of an output may share an address: sort the
-// three outer dimensions by stride and require each stride to clear the extent
-// of everything inside it.
-bool non_overlapping(const mhla_tensor_t* t) {
-  struct Dim { int64_t stride, extent; } dims[3] = {
-      {t->stride_b, t->B}, {t->stride_n, t->N}, {t->stride_h, t->H}};
-  std::sort(dims, dims + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
-  int64_t inner = t->d;   // elements spanned so far
-  for (const Dim& dm : dims) {
-    if (dm.extent <= 1) continue;
-    if (dm.stride < inner) return false;
-    inner = dm.stride * (dm.extent - 1) + inner;
-  }
-  return true;
-}
-
-int check_tensor(const mhla_tensor_t* t) {
-  if (!t) return MHLA_ERR_INVALID_ARG;
-  if (!valid_dtype(t->dtype)) return MHLA_ERR_INVALID_ARG;
-  if (t->B < 0 || t->N < 1 || t->H < 0 || t->d < 1 || t->d > 128) return MHLA_ERR_INVALID_ARG;
-  if (t->stride_b < 0 || t->stride_n < 0 || t->stride_h < 0) return MHLA_ERR_INVALID_ARG;
-  if (t->B > 0 && t->H > 0 && !t->data) return MHLA_ERR_INVALID_ARG;
-  return MHLA_OK;
-}
-
-bool same_shape(const mhla_tensor_t* a, const mhla_tensor_t* b) {
-  return a->B == b->B && a->N == b->N && a->H == b->H && a->d == b->d && a->dtype == b->dtype;
-}
 
 int build_problem(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v,
                   const mhla_tensor_t* o, const mhla_shape3_t* grid, const mhla_shape3_t* block,
@@ -541,8 +499,6 @@ extern "C" const char* mhla_version(void) { return "mhla-gb300 0.1.0 sm_103a"; }
 
 namespace mhla {
 namespace {
-
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 int check_grid_tokens(const mhla_shape3_t* grid, int64_t N, int64_t* T, int64_t* Y, int64_t* X) {
   if (!grid || (grid->ndim != 2 && grid->ndim != 3)) return MHLA_ERR_INVALID_ARG;

@@ -105,3 +105,41 @@ extern "C" mhla_status_t mhla_init_mixing(const mhla_shape3_t* grid, const mhla_
     for (int64_t j = 0; j < M; ++j) W_host[i * M + j] = static_cast<float>(mat[i * M + j] / col[j]);
   return MHLA_OK;
 }
+
+// Rotation table of token coordinates (the position term of mhla_qk_norm):
+// double throughout, each cosine and sine rounded once to float.
+extern "C" mhla_status_t mhla_init_rotation(const mhla_shape3_t* grid, const int32_t* pairs, double base,
+                                            float* table_host, int64_t table_capacity) {
+  if (!grid || !pairs || !table_host) return MHLA_ERR_INVALID_ARG;
+  if (grid->ndim != 2 && grid->ndim != 3) return MHLA_ERR_SHAPE;
+  if (!(base > 0.0) || !std::isfinite(base)) return MHLA_ERR_INVALID_ARG;
+  int64_t N = 1, total = 0;
+  for (int a = 0; a < grid->ndim; ++a) {
+    if (grid->extent[a] <= 0) return MHLA_ERR_SHAPE;
+    if (grid->extent[a] > (int64_t{1} << 32) / N) return MHLA_ERR_INVALID_ARG;   // 2^32 tokens at most
+    N *= grid->extent[a];
+    if (pairs[a] < 0 || pairs[a] > 64) return MHLA_ERR_INVALID_ARG;              // d <= 128
+    total += pairs[a];
+  }
+  if (table_capacity < N * total * 2) return MHLA_ERR_INVALID_ARG;
+  std::vector<double> freq;
+  freq.reserve(static_cast<size_t>(total));
+  for (int a = 0; a < grid->ndim; ++a)
+    for (int i = 0; i < pairs[a]; ++i) freq.push_back(std::pow(base, -static_cast<double>(i) / pairs[a]));
+  for (int64_t n = 0; n < N; ++n) {
+    int64_t coord[3] = {0, 0, 0}, rem = n;
+    for (int a = grid->ndim - 1; a >= 0; --a) {
+      coord[a] = rem % grid->extent[a];
+      rem /= grid->extent[a];
+    }
+    float* row = table_host + n * total * 2;
+    int64_t c = 0;
+    for (int a = 0; a < grid->ndim; ++a)
+      for (int i = 0; i < pairs[a]; ++i, ++c) {
+        const double angle = static_cast<double>(coord[a]) * freq[static_cast<size_t>(c)];
+        row[2 * c] = static_cast<float>(std::cos(angle));
+        row[2 * c + 1] = static_cast<float>(std::sin(angle));
+      }
+  }
+  return MHLA_OK;
+}

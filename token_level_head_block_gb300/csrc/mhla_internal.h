@@ -240,6 +240,47 @@ int launch_gemm(const char* name, const void* x, const void* w, const void* bias
                 int64_t n_out, void* stream);
 int read_and_clear_gemm_error(void* stream, uint32_t* flags);
 
+// Gated causal linear attention (gated_kernels.cu).
+struct GatedProblem {
+  int64_t B, N, H;
+  int32_t d;
+  int dtype;           // mhla_dtype_t
+  float scale;
+  Operand q, k, v, g;  // g: one value a token and head
+};
+struct GatedBackward {
+  Operand dout, dq, dk, dv, dg;
+  const float *state_in, *dstate_out;   // [B][H][d][d] or null
+  float* dstate_in;                     // or null
+};
+size_t gated_workspace_bytes(const GatedProblem& p);
+size_t gated_bwd_workspace_bytes(const GatedProblem& p);
+int launch_gated_forward(const GatedProblem& p, const float* state_in, const Operand& out, float* state_out,
+                         void* workspace, void* stream);
+int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* workspace, void* stream);
+int launch_gated_step(const GatedProblem& p, float* state, const Operand& out, void* stream);
+
+// Norm and rotation of query and key heads (qk_norm_kernels.cu).
+struct QkNormProblem {
+  int64_t B, N, Hq, Hk;
+  int32_t d;
+  int dtype;
+  float eps;
+  Operand q, k;             // before the norm
+  Operand q_out, k_out;     // forward: normed; backward: dq, dk
+  Operand dq_out, dk_out;   // backward only
+  const float *q_weight, *k_weight;   // [d] or null
+  float *dq_weight, *dk_weight;       // [d] or null; backward only
+  const float* table;       // [rows][pairs][2], null when pairs == 0
+  const int32_t* positions; // [B][N] or null
+  int64_t rows;
+  int32_t pairs;
+  bool interleaved;
+};
+size_t qk_norm_bwd_workspace_bytes(int32_t d);
+int launch_qk_norm(const QkNormProblem& p, void* stream);
+int launch_qk_norm_backward(const QkNormProblem& p, void* workspace, void* stream);
+
 constexpr size_t kAlign = 256;
 inline size_t align_up(size_t x, size_t a = kAlign) { return (x + a - 1) / a * a; }
 
