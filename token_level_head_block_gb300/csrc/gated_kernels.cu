@@ -6,185 +6,1104 @@
 //   dk_t = dS_t v_t               the same with (v, do, q)
 //   dg_t = exp(g_t) <S_{t-1}, dS_t>, where <S_t, dS_t> = dg_t + k_t . dk_t = dg_{t+1} + q_t . dq_t,
 // so dg is a running sum of q . dq - k . dk from the end.
+//
+// One kernel, gated_scan, does every scan.  A CTA of four warps walks a span of
+// chunks of 64 tokens with the state (d x up to 64 columns of it) in registers.  With
+// b_i the sum of the log decays of a chunk's tokens up to i and B that of all,
+//   o_i = scale (e^{b_i} S^T q_i + sum_{j <= i} e^{b_i - b_j} (q_i . k_j) v_j)
+//   S  <- e^B S + sum_j e^{B - b_j} k_j v_j^T
+// and backwards the same with b_j - b_i, B - b_i and b_j for the three exponents.
+// All four products run on mma.sync m16n8k16 with float32 accumulators; what is
+// not exact in bf16 enters as a sum of bf16 terms (Terms below).  When there are
+// fewer (b, h) than the machine has room for, the sequence is cut into spans:
+// gated_span_state forms each span's own contribution to the state,
+// gated_join carries the state from span to span, and gated_scan then runs all
+// spans at once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "mhla_internal.h"
+#include "ptx.cuh"
 
 namespace mhla {
 namespace {
 
 constexpr float kLowestGate = -1000.0f;   // exp is 0 in float32 far above this
+constexpr int kChunk = 64;
+constexpr int kSms = 152;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void from_f(float* p, float x) { *p = x; }
 __device__ __forceinline__ void from_f(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// One scan.  States are [r][c], r of k's channels, c of v's.
 struct Scan {
-  Operand q, k, v, g, out, dot;
-  const float* init;    // [B][H][d][d] or null
-  float* last;          // or null
-  float* dots;          // [B][H][N] sums of dot_t . out_t before rounding, or null
-  int64_t N, H;
-  int32_t d;
-  float out_scale, k_scale;
-  bool reverse, transposed;   // transposed: init and last hold the state's transpose
+  Operand q, k, v, out, dot;
+  const float* init;    // state entering a span, or null for zero
+  float* last;          // state after the last span [B][H][d][d], or null
+  float* local;         // gated_span_state: a span's own contribution [B][H][spans][d][d]
+  float* decay;         // and its decay [B][H][spans]
+  float* dots;          // sums of dot_t . out_t before rounding [slices][B][H][N], or null
+  float out_scale;      // of the scores
+  float state_scale;    // of what a query reads from the state
+  float k_scale;        // of what a token adds to the state
+  int32_t reverse;
+  int32_t init_transposed;
+  int32_t init_spans;   // spans per (b, h) in init: slot of a span, or 1
 };
 
-// One CTA walks one (b, h): thread (c, half) holds half of the state's column c.
+struct ScanSet {
+  Scan scan[3];
+  Operand g;
+  int64_t N, H, BH;
+  int64_t span_chunks, chunks;
+  int32_t spans, d;
+};
+
+// bf16 terms an operand enters the tensor cores with.  bf16 inputs are exact in one.
+// The scores and the state a query reads feed a result that is rounded to bf16
+// (2^-8) anyway: two terms leave 2^-16 there; what a token adds to the float32 state takes
+// three (2^-24).  float32 runs take three everywhere.
 template <typename T>
-__global__ void __launch_bounds__(256) gated_scan_simple(const Scan a) {
-  __shared__ float sq[128], sk[128], sv[128], part[128], red[8];
-  const int64_t bh = blockIdx.x, b = bh / a.H, h = bh % a.H;
-  const int c = threadIdx.x & 127, r0 = (threadIdx.x >> 7) * 64, d = a.d;
-  auto at = [&](const Operand& o, int64_t t) { return static_cast<T*>(o.data) + b * o.sb + t * o.sn + h * o.sh; };
-  float S[64];
-  for (int i = 0; i < 64; ++i) {
-    const int r = r0 + i;
-    S[i] = a.init && r < d && c < d ? a.init[bh * d * d + (a.transposed ? c * d + r : r * d + c)] : 0.0f;
-  }
-  for (int64_t i = 0; i < a.N; ++i) {
-    const int64_t t = a.reverse ? a.N - 1 - i : i;
-    __syncthreads();
-    if (threadIdx.x < 128) {
-      sq[c] = c < d ? to_f(at(a.q, t)[c]) : 0.0f;
-      sk[c] = c < d ? a.k_scale * to_f(at(a.k, t)[c]) : 0.0f;
-      sv[c] = c < d ? to_f(at(a.v, t)[c]) : 0.0f;
-    }
-    const float decay = expf(fmaxf(to_f(*at(a.g, t)), kLowestGate));
-    __syncthreads();
-    float o = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 64; ++j) {
-      S[j] = fmaf(sk[r0 + j], sv[c], a.reverse ? S[j] : decay * S[j]);
-      o = fmaf(sq[r0 + j], S[j], o);
-      if (a.reverse) S[j] *= decay;
-    }
-    if (r0) part[c] = o;
-    __syncthreads();
-    float dot = 0.0f;
-    if (!r0 && c < d) {
-      o = a.out_scale * (o + part[c]);
-      from_f(at(a.out, t) + c, o);
-      if (a.dots) dot = o * to_f(at(a.dot, t)[c]);
-    }
-    if (a.dots) {
-      for (int s = 16; s; s >>= 1) dot += __shfl_xor_sync(~0u, dot, s);
-      if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dot;
-      __syncthreads();
-      if (threadIdx.x == 0) a.dots[bh * a.N + t] = red[0] + red[1] + red[2] + red[3];
-    }
-  }
-  if (a.last)
-    for (int i = 0; i < 64; ++i) {
-      const int r = r0 + i;
-      if (r < d && c < d) a.last[bh * d * d + (a.transposed ? c * d + r : r * d + c)] = S[i];
-    }
+struct Terms;
+template <>
+struct Terms<__nv_bfloat16> {
+  static constexpr int kIn = 1, kScore = 2, kState = 2;
+};
+template <>
+struct Terms<float> {
+  static constexpr int kIn = 3, kScore = 3, kState = 3;
+};
+constexpr int kAdd = 3;
+
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// dg of one (b, h): <S, dS> at the end, then the running sum of q.dq - k.dk.
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+__device__ __forceinline__ float low(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float high(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
+
+// x, y as sums of NT bf16 terms, packed in pairs.
+template <int NT>
+__device__ __forceinline__ void split(float x, float y, uint32_t (&t)[NT]) {
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    t[i] = pack(x, y);
+    if (i + 1 < NT) {
+      x -= low(t[i]);
+      y -= high(t[i]);
+    }
+  }
+}
+
+// c += A B over the terms of both whose product is not below the last term's size.
+template <int NA, int NB>
+__device__ __forceinline__ void mma_terms(float (&c)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4],
+                                          int half) {
+  constexpr int kMost = NA > NB ? NA : NB;
+#pragma unroll
+  for (int i = 0; i < NA; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      if (i + j < kMost) mma(c, a[i], b[j][2 * half], b[j][2 * half + 1]);
+}
+
+// A sum of log decays (in powers of two) as the sum of two floats: differences of
+// far sums keep the precision of the near ones.
+struct Sum {
+  float hi, lo;
+};
+__device__ __forceinline__ Sum add(Sum a, Sum b) {
+  const float s = a.hi + b.hi, z = s - a.hi;
+  const float e = ((a.hi - (s - z)) + (b.hi - z)) + (a.lo + b.lo);
+  Sum r;
+  r.hi = s + e;
+  r.lo = e - (r.hi - s);
+  return r;
+}
+__device__ __forceinline__ Sum gate_sum(float g) {
+  constexpr float kL = 1.4426950408889634f, kLlo = static_cast<float>(1.4426950408889634 - kL);
+  g = g < kLowestGate ? kLowestGate : g;   // NaN stays
+  Sum r;
+  r.hi = g * kL;
+  r.lo = fmaf(g, kLlo, fmaf(g, kL, -r.hi));
+  return r;
+}
+
+// What a chunk needs of its gates.
+struct Gates {
+  float hi[kChunk], lo[kChunk];   // b_i
+  float read[kChunk];             // of the state, per token
+  float addw[kChunk];             // to the state, per token
+  float total;                    // of the state over the chunk
+  float pad[3];
+};
+
+// A lane's two gates of a chunk (tokens 2 lane, 2 lane + 1); 0 behind the end.
 template <typename T>
-__global__ void __launch_bounds__(128) gated_gate_grad_simple(const float* qdots, const float* kdots, const float* last,
-                                                              const float* dlast, Operand dg, int64_t N, int64_t H,
-                                                              int32_t d) {
-  __shared__ double red[128];
-  const int64_t bh = blockIdx.x, b = bh / H, h = bh % H;
-  double s = 0.0;
-  if (dlast)
-    for (int i = threadIdx.x; i < d * d; i += 128)
-      s += static_cast<double>(last[bh * d * d + i]) * static_cast<double>(dlast[bh * d * d + i]);
-  red[threadIdx.x] = s;
+__device__ __forceinline__ float2 load_gates(const ScanSet& p, int64_t b, int64_t h, int64_t chunk, int lane) {
+  const int64_t t = chunk * kChunk + 2 * lane;
+  const T* g = static_cast<const T*>(p.g.data) + b * p.g.sb + h * p.g.sh;
+  return make_float2(t < p.N ? to_f(g[t * p.g.sn]) : 0.0f, t + 1 < p.N ? to_f(g[(t + 1) * p.g.sn]) : 0.0f);
+}
+
+// One warp: the running sums and the weights of a chunk.  Returns B.
+__device__ __forceinline__ Sum chunk_gates(float2 g, Gates& out, bool reverse, float k_scale, int lane) {
+  const Sum first = gate_sum(g.x), second = gate_sum(g.y);
+  Sum run = add(first, second);
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    Sum o;
+    o.hi = __shfl_up_sync(~0u, run.hi, s);
+    o.lo = __shfl_up_sync(~0u, run.lo, s);
+    if (lane >= s) run = add(o, run);
+  }
+  Sum all;
+  all.hi = __shfl_sync(~0u, run.hi, 31);
+  all.lo = __shfl_sync(~0u, run.lo, 31);
+  Sum before;
+  before.hi = __shfl_up_sync(~0u, run.hi, 1);
+  before.lo = __shfl_up_sync(~0u, run.lo, 1);
+  if (lane == 0) before.hi = before.lo = 0.0f;
+  const Sum at[2] = {add(before, first), run};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int i = 2 * lane + e;
+    const float up = exp2f(at[e].hi + at[e].lo), rest = exp2f((all.hi - at[e].hi) + (all.lo - at[e].lo));
+    out.hi[i] = at[e].hi;
+    out.lo[i] = at[e].lo;
+    out.read[i] = reverse ? rest : up;
+    out.addw[i] = k_scale * (reverse ? up : rest);
+  }
+  if (lane == 0) out.total = exp2f(all.hi + all.lo);
+  return all;
+}
+
+template <typename T, int DK, bool ASYNC>
+struct Tile {
+  static constexpr int DV = DK < 64 ? DK : 64;     // columns of the state a CTA holds
+  static constexpr int kIn = Terms<T>::kIn;
+  static constexpr int kStages = ASYNC ? 2 : 1;
+  // rows of 16 bytes more than the channels: eight rows at one column meet all banks
+  static constexpr int kPitchK = DK + 8, kPitchV = DV + 8;   // bf16 elements
+  static constexpr int kK = kChunk * kPitchK * 2, kV = kChunk * kPitchV * 2;   // bytes of a plane
+  static constexpr int kS = DK * kPitchV * 2;
+  // warps over the state's rows (16 each) and, for 32 rows, two halves of its columns
+  static constexpr int kRowTiles = DK >= 64 ? DK / 64 : 1;
+  static constexpr int kColTiles = DK >= 64 ? DV / 8 : DV / 16;   // of eight columns
+};
+
+// Copies a chunk's rows of one operand (columns [c0, c0 + W)) into kIn planes.
+template <typename T, int W, int PITCH, bool ASYNC>
+__device__ __forceinline__ void load_rows(char* dst, const Operand& o, int64_t b, int64_t h, int64_t chunk, int64_t N,
+                                          int c0, int d) {
+  const T* src = static_cast<const T*>(o.data) + b * o.sb + h * o.sh + c0;
+  const int64_t t0 = chunk * kChunk;
+  const int rows = static_cast<int>(N - t0 < kChunk ? N - t0 : kChunk);
+  if constexpr (ASYNC) {
+    constexpr int kUnits = W / 8;
+    const uint32_t base = ptx::smem_u32(dst);
+#pragma unroll
+    for (int i = threadIdx.x; i < kChunk * kUnits; i += 128) {
+      const int r = i / kUnits, u = i % kUnits;
+      if (c0 + 8 * u >= d) continue;   // the columns behind d were zeroed at the start
+      const bool in = r < rows;
+      cp_async_16(base + (r * PITCH + 8 * u) * 2, src + (in ? (t0 + r) * o.sn + 8 * u : 0), in ? 16 : 0);
+    }
+  } else {
+    constexpr int kPlane = kChunk * PITCH;
+    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(dst);
+    for (int i = threadIdx.x; i < kChunk * W / 2; i += 128) {
+      const int r = i / (W / 2), c = 2 * (i % (W / 2));
+      const T* x = src + (t0 + r) * o.sn + c;
+      float a = r < rows && c0 + c < d ? to_f(x[0]) : 0.0f, e = r < rows && c0 + c + 1 < d ? to_f(x[1]) : 0.0f;
+#pragma unroll
+      for (int n = 0; n < Terms<T>::kIn; ++n) {
+        const uint32_t p = pack(a, e);
+        *reinterpret_cast<uint32_t*>(out + n * kPlane + r * PITCH + c) = p;
+        // an infinity is its first term alone
+        a = fabsf(low(p)) < __int_as_float(0x7F800000) ? a - low(p) : 0.0f;
+        e = fabsf(high(p)) < __int_as_float(0x7F800000) ? e - high(p) : 0.0f;
+      }
+    }
+  }
+}
+
+// Each thread's part of the state: row tile m, column tile n, the four values of
+// an mma accumulator.  `row` and `col` are those of the first.
+template <int DK>
+struct StatePlace {
+  int row, col;
+  __device__ __forceinline__ StatePlace(int warp, int lane) {
+    row = (DK >= 64 ? (DK / 4) * warp : 16 * (warp & 1)) + (lane >> 2);
+    col = (DK >= 64 ? 0 : 16 * (warp >> 1)) + 2 * (lane & 3);
+  }
+};
+
+// S <- e^B S + (addw k)^T v over one k-step of 16 tokens: the scaled, split
+// transpose of k's rows for this warp's state rows.
+template <typename T, int DK, bool ASYNC>
+__device__ __forceinline__ void add_operand(uint32_t (&a)[kAdd][4], uint32_t k_base, int row_tile, int step,
+                                            const float* addw, int lane) {
+  using L = Tile<T, DK, ASYNC>;
+  const int token = 16 * step + (lane & 7) + ((lane >> 4) & 1) * 8, r = row_tile + ((lane >> 3) & 1) * 8;
+  const float2 w0 = *reinterpret_cast<const float2*>(addw + 16 * step + 2 * (lane & 3));
+  const float2 w1 = *reinterpret_cast<const float2*>(addw + 16 * step + 8 + 2 * (lane & 3));
+  float x[4][2];
+#pragma unroll
+  for (int n = 0; n < L::kIn; ++n) {
+    uint32_t k[4];
+    ldsm_t(k, k_base + n * L::kK + (token * L::kPitchK + r) * 2);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e][0] = n == 0 ? low(k[e]) : x[e][0] + low(k[e]);
+      x[e][1] = n == 0 ? high(k[e]) : x[e][1] + high(k[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 w = e < 2 ? w0 : w1;
+    uint32_t t[kAdd];
+    split<kAdd>(x[e][0] * w.x, x[e][1] * w.y, t);
+#pragma unroll
+    for (int i = 0; i < kAdd; ++i) a[i][e] = t[i];
+  }
+}
+
+// Fragments of 16 tokens by 16 columns of a row-major plane [token][column]
+// (v, or the state with r for the token): two column tiles of B operands.
+__device__ __forceinline__ uint32_t column_address(uint32_t base, int pitch, int token0, int col0, int lane) {
+  return base + ((token0 + (lane & 7) + ((lane >> 3) & 1) * 8) * pitch + col0 + (lane >> 4) * 8) * 2;
+}
+
+template <typename T, int DK, bool ASYNC>
+__global__ void __launch_bounds__(128) gated_span_state(const __grid_constant__ ScanSet p) {
+  using L = Tile<T, DK, ASYNC>;
+  extern __shared__ __align__(16) char smem[];
+  __shared__ __align__(16) Gates gates[2];
+  constexpr int kStage = L::kIn * (L::kK + L::kV);
+  const Scan& a = p.scan[blockIdx.y];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the span last in order adds to no other
+  const int64_t nspans = p.spans - 1;
+  int64_t id = blockIdx.x;
+  const int64_t span = id % nspans + (a.reverse ? 1 : 0);
+  id /= nspans;
+  const int slices = (p.d + L::DV - 1) / L::DV;
+  const int c0 = static_cast<int>(id % slices) * L::DV;
+  const int64_t bh = id / slices, b = bh / p.H, h = bh % p.H;
+  const int64_t first = span * p.span_chunks;
+  const int count = static_cast<int>(min(p.span_chunks, p.chunks - first));
+  const bool reverse = a.reverse;
+
+  if constexpr (ASYNC) {   // columns behind d stay zero
+    for (int i = threadIdx.x; i < L::kStages * kStage / 16; i += 128)
+      reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+  }
+  auto load = [&](int i) {
+    const int64_t chunk = first + (reverse ? count - 1 - i : i);
+    char* st = smem + (i % L::kStages) * kStage;
+    load_rows<T, DK, L::kPitchK, ASYNC>(st, a.k, b, h, chunk, p.N, 0, p.d);
+    load_rows<T, L::DV, L::kPitchV, ASYNC>(st + L::kIn * L::kK, a.v, b, h, chunk, p.N, c0, p.d);
+    if (ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto gate_chunk = [&](int i) { return first + (reverse ? count - 1 - i : i); };
+
+  float S[L::kRowTiles][L::kColTiles][4] = {};
+  Sum all = {0.0f, 0.0f};
+  float2 g = make_float2(0.0f, 0.0f);
+  if (warp == 0) {
+    all = chunk_gates(load_gates<T>(p, b, h, gate_chunk(0), lane), gates[0], reverse, a.k_scale, lane);
+    if (count > 1) g = load_gates<T>(p, b, h, gate_chunk(1), lane);
+  }
+  if constexpr (ASYNC) load(0);
+  for (int i = 0; i < count; ++i) {
+    if constexpr (ASYNC) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();
+      if (i + 1 < count) load(i + 1);
+    } else {
+      __syncthreads();
+      load(i);
+      __syncthreads();
+    }
+    if (warp == 0 && i + 1 < count) {
+      all = add(all, chunk_gates(g, gates[(i + 1) & 1], reverse, a.k_scale, lane));
+      if (i + 2 < count) g = load_gates<T>(p, b, h, gate_chunk(i + 2), lane);
+    }
+    const uint32_t k_base = ptx::smem_u32(smem + (i % L::kStages) * kStage);
+    const uint32_t v_base = k_base + L::kIn * L::kK;
+    const Gates& w = gates[i & 1];
+#pragma unroll
+    for (int m = 0; m < L::kRowTiles; ++m)
+#pragma unroll
+      for (int n = 0; n < L::kColTiles; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[m][n][e] *= w.total;
+    const int row0 = DK >= 64 ? (DK / 4) * warp : 16 * (warp & 1), col0 = DK >= 64 ? 0 : 16 * (warp >> 1);
+#pragma unroll
+    for (int s = 0; s < kChunk / 16; ++s) {
+      uint32_t ka[L::kRowTiles][kAdd][4];
+#pragma unroll
+      for (int m = 0; m < L::kRowTiles; ++m)
+        add_operand<T, DK, ASYNC>(ka[m], k_base, row0 + 16 * m, s, w.addw, lane);
+#pragma unroll
+      for (int n = 0; n < L::kColTiles; n += 2) {
+        uint32_t vb[L::kIn][4];
+#pragma unroll
+        for (int t = 0; t < L::kIn; ++t)
+          ldsm_t(vb[t], column_address(v_base + t * L::kV, L::kPitchV, 16 * s, col0 + 8 * n, lane));
+#pragma unroll
+        for (int m = 0; m < L::kRowTiles; ++m) {
+          mma_terms(S[m][n], ka[m], vb, 0);
+          mma_terms(S[m][n + 1], ka[m], vb, 1);
+        }
+      }
+    }
+  }
+  const StatePlace<DK> at(warp, lane);
+  float* out = a.local + (bh * p.spans + span) * p.d * p.d;
+#pragma unroll
+  for (int m = 0; m < L::kRowTiles; ++m)
+#pragma unroll
+    for (int n = 0; n < L::kColTiles; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = at.row + 16 * m + (e >> 1) * 8, c = c0 + at.col + 8 * n + (e & 1);
+        if (r < p.d && c < p.d) out[r * p.d + c] = S[m][n][e];
+      }
+  if (c0 == 0 && threadIdx.x == 0) a.decay[bh * p.spans + span] = exp2f(all.hi + all.lo);
+}
+
+// Turns every span's own contribution into the state that enters the span, in
+// order of the scan; one thread an element of one (b, h)'s state.
+__global__ void __launch_bounds__(256) gated_join(const __grid_constant__ ScanSet p) {
+  const Scan& a = p.scan[blockIdx.y];
+  const int64_t dd = static_cast<int64_t>(p.d) * p.d;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= p.BH * dd) return;
+  const int64_t bh = i / dd, e = i % dd;
+  const int64_t r = e / p.d, c = e % p.d;
+  float S = a.init ? a.init[bh * dd + (a.init_transposed ? c * p.d + r : e)] : 0.0f;
+  const int64_t n = p.spans;
+  float* at = a.local + (bh * n + (a.reverse ? n - 1 : 0)) * dd + e;
+  const float* w = a.decay + bh * n + (a.reverse ? n - 1 : 0);
+  const int64_t step = a.reverse ? -dd : dd, wstep = a.reverse ? -1 : 1;
+  constexpr int kBatch = 8;   // loads in flight
+  for (int64_t s = 0; s < n; s += kBatch) {
+    float own[kBatch], f[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (s + j < n - 1) {
+        own[j] = at[j * step];
+        f[j] = w[j * wstep];
+      }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (s + j < n) {
+        at[j * step] = S;
+        if (s + j < n - 1) S = fmaf(f[j], S, own[j]);
+      }
+    at += kBatch * step;
+    w += kBatch * wstep;
+  }
+}
+
+// The masked 16 x 16 block of scores times its 16 rows of v without the tensor
+// core, for rows of v that hold an infinity or NaN: a row must not see those of
+// later tokens (0 times infinity).
+template <typename T, int DK, bool ASYNC>
+__device__ __noinline__ void diagonal_apart(float (&o)[Tile<T, DK, ASYNC>::DV / 8][4], const float (&pr)[2][4],
+                                            const __nv_bfloat16* v, bool reverse, int lane) {
+  using L = Tile<T, DK, ASYNC>;
+  const int row = lane >> 2;
+  for (int j = 0; j < 16; ++j) {
+    const int src = (lane & ~3) | ((j & 7) >> 1);
+    // element (row, j): accumulator of column tile j / 8, value j % 2; (row + 8, j): the next two
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __shfl_sync(~0u, j < 8 ? pr[0][e] : pr[1][e], src);
+    const float up = j & 1 ? x[1] : x[0], dn = j & 1 ? x[3] : x[2];
+    const bool sees_up = reverse ? j >= row : j <= row, sees_dn = reverse ? j >= row + 8 : j <= row + 8;
+#pragma unroll
+    for (int n = 0; n < L::DV / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float y = 0.0f;
+        for (int t = 0; t < L::kIn; ++t)
+          y += __bfloat162float(v[t * (L::kV / 2) + j * L::kPitchV + 8 * n + 2 * (lane & 3) + e]);
+        if (sees_up) o[n][e] = fmaf(up, y, o[n][e]);
+        if (sees_dn) o[n][2 + e] = fmaf(dn, y, o[n][2 + e]);
+      }
+  }
+}
+
+template <typename T, int DK, bool ASYNC>
+struct ScanShared {
+  using L = Tile<T, DK, ASYNC>;
+  static constexpr int kStage = L::kIn * (2 * L::kK + L::kV);   // q, k, v
+  static constexpr int kBytes = L::kStages * kStage + Terms<T>::kState * L::kS;
+};
+
+template <typename T, int DK, bool ASYNC>
+__global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
+    gated_scan(const __grid_constant__ ScanSet p) {
+  using L = Tile<T, DK, ASYNC>;
+  using M = ScanShared<T, DK, ASYNC>;
+  constexpr int kScore = Terms<T>::kScore, kState = Terms<T>::kState, NV = L::DV / 8;
+  extern __shared__ __align__(16) char smem[];
+  __shared__ __align__(16) Gates gates[2];
+  const Scan& a = p.scan[blockIdx.y];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t id = blockIdx.x;
+  const int64_t span = id % p.spans;
+  id /= p.spans;
+  const int slices = (p.d + L::DV - 1) / L::DV;
+  const int slice = static_cast<int>(id % slices), c0 = slice * L::DV;
+  const int64_t bh = id / slices, b = bh / p.H, h = bh % p.H;
+  const int64_t first = span * p.span_chunks;
+  const int count = static_cast<int>(min(p.span_chunks, p.chunks - first));
+  const bool reverse = a.reverse;
+  // Rows later in the order see more of the chunk: neighbouring CTAs give them
+  // to different warps, so that an SM's four schedulers get the same work.
+  const int rows0 = 16 * ((warp + static_cast<int>(blockIdx.x)) & 3);
+  char* planes = smem + L::kStages * M::kStage;
+  const uint32_t s_base = ptx::smem_u32(planes);
+
+  if constexpr (ASYNC) {
+    for (int i = threadIdx.x; i < L::kStages * M::kStage / 16; i += 128)
+      reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+  }
+  auto chunk_of = [&](int i) { return first + (reverse ? count - 1 - i : i); };
+  auto load = [&](int i) {
+    char* st = smem + (i % L::kStages) * M::kStage;
+    load_rows<T, DK, L::kPitchK, ASYNC>(st, a.q, b, h, chunk_of(i), p.N, 0, p.d);
+    load_rows<T, DK, L::kPitchK, ASYNC>(st + L::kIn * L::kK, a.k, b, h, chunk_of(i), p.N, 0, p.d);
+    load_rows<T, L::DV, L::kPitchV, ASYNC>(st + 2 * L::kIn * L::kK, a.v, b, h, chunk_of(i), p.N, c0, p.d);
+    if (ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if constexpr (ASYNC) load(0);
+
+  // the state entering the span
+  const StatePlace<DK> at(warp, lane);
+  float S[L::kRowTiles][L::kColTiles][4];
+  {
+    const float* in = a.init ? a.init + (bh * a.init_spans + (a.init_spans > 1 ? span : 0)) * p.d * p.d : nullptr;
+#pragma unroll
+    for (int m = 0; m < L::kRowTiles; ++m)
+#pragma unroll
+      for (int n = 0; n < L::kColTiles; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = at.row + 16 * m + (e >> 1) * 8, c = c0 + at.col + 8 * n + (e & 1);
+          S[m][n][e] = in && r < p.d && c < p.d ? in[a.init_transposed ? c * p.d + r : r * p.d + c] : 0.0f;
+        }
+  }
+  auto publish = [&]() {   // the state as bf16 terms for the queries
+#pragma unroll
+    for (int m = 0; m < L::kRowTiles; ++m)
+#pragma unroll
+      for (int n = 0; n < L::kColTiles; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t t[kState];
+          split<kState>(S[m][n][2 * e], S[m][n][2 * e + 1], t);
+#pragma unroll
+          for (int k = 0; k < kState; ++k)
+            *reinterpret_cast<uint32_t*>(planes + k * L::kS +
+                                         ((at.row + 16 * m + 8 * e) * L::kPitchV + at.col + 8 * n) * 2) = t[k];
+        }
+  };
+  publish();
+
+  float2 g = make_float2(0.0f, 0.0f);
+  if (warp == 0) {
+    chunk_gates(load_gates<T>(p, b, h, chunk_of(0), lane), gates[0], reverse, a.k_scale, lane);
+    if (count > 1) g = load_gates<T>(p, b, h, chunk_of(1), lane);
+  }
+
+  for (int i = 0; i < count; ++i) {
+    if constexpr (ASYNC) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();
+      if (i + 1 < count) load(i + 1);
+    } else {
+      __syncthreads();
+      load(i);
+      __syncthreads();
+    }
+    if (warp == 0 && i + 1 < count) {
+      chunk_gates(g, gates[(i + 1) & 1], reverse, a.k_scale, lane);
+      if (i + 2 < count) g = load_gates<T>(p, b, h, chunk_of(i + 2), lane);
+    }
+    char* stage = smem + (i % L::kStages) * M::kStage;
+    const uint32_t q_base = ptx::smem_u32(stage);
+    const uint32_t k_base = q_base + L::kIn * L::kK, v_base = k_base + L::kIn * L::kK;
+    const Gates& w = gates[i & 1];
+    const int row = rows0 + (lane >> 2);
+
+    // scores (this warp's 16 rows; only the 16-token steps they see) and what the rows read from the state
+    float sc[kChunk / 8][4] = {}, o[NV][4] = {};
+    const int own = rows0 / 16;
+#pragma unroll
+    for (int ks = 0; ks < DK / 16; ++ks) {
+      uint32_t qa[L::kIn][4];
+#pragma unroll
+      for (int t = 0; t < L::kIn; ++t)
+        ldsm(qa[t], q_base + t * L::kK +
+                        ((rows0 + (lane & 7) + ((lane >> 3) & 1) * 8) * L::kPitchK + 16 * ks + (lane >> 4) * 8) * 2);
+#pragma unroll
+      for (int s = 0; s < kChunk / 16; ++s) {
+        if (reverse ? s < own : s > own) continue;
+        uint32_t kb[L::kIn][4];
+#pragma unroll
+        for (int t = 0; t < L::kIn; ++t)
+          ldsm(kb[t], k_base + t * L::kK +
+                          ((16 * s + (lane & 7) + (lane >> 4) * 8) * L::kPitchK + 16 * ks + ((lane >> 3) & 1) * 8) * 2);
+        mma_terms(sc[2 * s], qa, kb, 0);
+        mma_terms(sc[2 * s + 1], qa, kb, 1);
+      }
+#pragma unroll
+      for (int n = 0; n < NV; n += 2) {
+        uint32_t sb[kState][4];
+#pragma unroll
+        for (int t = 0; t < kState; ++t)
+          ldsm_t(sb[t], column_address(s_base + t * L::kS, L::kPitchV, 16 * ks, 8 * n, lane));
+        mma_terms(o[n], qa, sb, 0);
+        mma_terms(o[n + 1], qa, sb, 1);
+      }
+    }
+    const float read0 = a.state_scale * w.read[row], read1 = a.state_scale * w.read[row + 8];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      o[n][0] *= read0; o[n][1] *= read0;
+      o[n][2] *= read1; o[n][3] *= read1;
+    }
+#pragma unroll
+    for (int m = 0; m < L::kRowTiles; ++m)
+#pragma unroll
+      for (int n = 0; n < L::kColTiles; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[m][n][e] *= w.total;
+    const float bh0 = w.hi[row], bl0 = w.lo[row], bh1 = w.hi[row + 8], bl1 = w.lo[row + 8];
+    const int srow0 = DK >= 64 ? (DK / 4) * warp : 16 * (warp & 1), scol0 = DK >= 64 ? 0 : 16 * (warp >> 1);
+    // 16 tokens at a time: their decayed scores times v, and what they add to the state
+#pragma unroll
+    for (int s = 0; s < kChunk / 16; ++s) {
+      const bool seen = reverse ? s >= own : s <= own;
+      bool apart = false;
+      float pr[2][4];
+      uint32_t pa[kScore][4];
+      if (seen) {
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int j = 16 * s + 8 * f + 2 * (lane & 3);
+          const float2 hj = *reinterpret_cast<const float2*>(w.hi + j), lj = *reinterpret_cast<const float2*>(w.lo + j);
+          const float sign = reverse ? -1.0f : 1.0f;
+          const float x[4] = {sign * ((bh0 - hj.x) + (bl0 - lj.x)), sign * ((bh0 - hj.y) + (bl0 - lj.y)),
+                              sign * ((bh1 - hj.x) + (bl1 - lj.x)), sign * ((bh1 - hj.y) + (bl1 - lj.y))};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = row + (e >> 1) * 8, c = j + (e & 1);
+            const bool keep = reverse ? c >= r : c <= r;
+            pr[f][e] = keep ? a.out_scale * sc[2 * s + f][e] * exp2_fast(x[e]) : 0.0f;
+          }
+          uint32_t t0[kScore], t1[kScore];
+          split<kScore>(pr[f][0], pr[f][1], t0);
+          split<kScore>(pr[f][2], pr[f][3], t1);
+#pragma unroll
+          for (int t = 0; t < kScore; ++t) {
+            pa[t][2 * f] = t0[t];
+            pa[t][2 * f + 1] = t1[t];
+          }
+        }
+        if (s == own) {   // rows of v that are not finite must not reach earlier tokens
+          uint32_t bad = 0;
+#pragma unroll
+          for (int n = 0; n < NV; n += 2) {
+            uint32_t vb[4];
+            ldsm_t(vb, column_address(v_base, L::kPitchV, 16 * s, 8 * n, lane));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&vb[e]),
+                                               __floats2bfloat162_rn(0.0f, 0.0f));
+              bad |= *reinterpret_cast<const uint32_t*>(&z);
+            }
+          }
+          apart = __any_sync(~0u, bad & 0x7FFF7FFFu);
+          if (apart)
+            diagonal_apart<T, DK, ASYNC>(
+                o, pr, reinterpret_cast<const __nv_bfloat16*>(stage + 2 * L::kIn * L::kK) + 16 * s * L::kPitchV, reverse,
+                lane);
+        }
+      }
+      uint32_t ka[L::kRowTiles][kAdd][4];
+#pragma unroll
+      for (int m = 0; m < L::kRowTiles; ++m)
+        add_operand<T, DK, ASYNC>(ka[m], k_base, srow0 + 16 * m, s, w.addw, lane);
+#pragma unroll
+      for (int n = 0; n < NV; n += 2) {
+        uint32_t vb[L::kIn][4];
+#pragma unroll
+        for (int t = 0; t < L::kIn; ++t)
+          ldsm_t(vb[t], column_address(v_base + t * L::kV, L::kPitchV, 16 * s, 8 * n, lane));
+        if (seen && !apart) {
+          mma_terms(o[n], pa, vb, 0);
+          mma_terms(o[n + 1], pa, vb, 1);
+        }
+        if (DK >= 64 || 8 * n == scol0) {
+#pragma unroll
+          for (int m = 0; m < L::kRowTiles; ++m) {
+            mma_terms(S[m][DK >= 64 ? n : 0], ka[m], vb, 0);
+            mma_terms(S[m][DK >= 64 ? n + 1 : 1], ka[m], vb, 1);
+          }
+        }
+      }
+    }
+    __syncthreads();   // every warp has read the state's planes
+    if (i + 1 < count) publish();
+
+    // rows out: rounded once, through this warp's own rows of q
+    const int64_t t0 = chunk_of(i) * kChunk;
+    if (a.dots) {
+      const T* dot = static_cast<const T*>(a.dot.data) + b * a.dot.sb + h * a.dot.sh + c0;
+      float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int64_t t = t0 + row + 8 * f;
+        if (t < p.N) {
+#pragma unroll
+          for (int n = 0; n < NV; ++n) {
+            const int c = 8 * n + 2 * (lane & 3);
+            const T* x = dot + t * a.dot.sn + c;
+            if (c0 + c < p.d) sum[f] = fmaf(o[n][2 * f], to_f(x[0]), sum[f]);
+            if (c0 + c + 1 < p.d) sum[f] = fmaf(o[n][2 * f + 1], to_f(x[1]), sum[f]);
+          }
+        }
+        sum[f] += __shfl_xor_sync(~0u, sum[f], 1);
+        sum[f] += __shfl_xor_sync(~0u, sum[f], 2);
+        if ((lane & 3) == 0 && t < p.N) a.dots[(slice * p.BH + bh) * p.N + t] = sum[f];
+      }
+    }
+    T* out = static_cast<T*>(a.out.data) + b * a.out.sb + h * a.out.sh + c0;
+    if constexpr (ASYNC) {
+      char* mine = stage + rows0 * L::kPitchK * 2;
+      // the columns behind d stay zero (a NaN row would put NaN there)
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          if (c0 + 8 * n < p.d) *reinterpret_cast<uint32_t*>(mine + (((lane >> 2) + 8 * f) * L::kPitchK + 8 * n + 2 * (lane & 3)) * 2) =
+              pack(o[n][2 * f], o[n][2 * f + 1]);
+      __syncwarp();
+      constexpr int kUnits = L::DV / 8;
+#pragma unroll
+      for (int u = lane; u < 16 * kUnits; u += 32) {
+        const int r = u / kUnits, c = 8 * (u % kUnits);
+        const int64_t t = t0 + rows0 + r;
+        if (t < p.N && c0 + c < p.d)
+          *reinterpret_cast<uint4*>(out + t * a.out.sn + c) =
+              *reinterpret_cast<const uint4*>(mine + (r * L::kPitchK + c) * 2);
+      }
+      __syncwarp();
+    } else {
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int64_t t = t0 + row + 8 * f;
+        if (t >= p.N) continue;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+          const int c = 8 * n + 2 * (lane & 3);
+          if (c0 + c < p.d) from_f(out + t * a.out.sn + c, o[n][2 * f]);
+          if (c0 + c + 1 < p.d) from_f(out + t * a.out.sn + c + 1, o[n][2 * f + 1]);
+        }
+      }
+    }
+  }
+  if (a.last && span == (reverse ? 0 : p.spans - 1)) {
+    float* out = a.last + bh * p.d * p.d;
+#pragma unroll
+    for (int m = 0; m < L::kRowTiles; ++m)
+#pragma unroll
+      for (int n = 0; n < L::kColTiles; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = at.row + 16 * m + (e >> 1) * 8, c = c0 + at.col + 8 * n + (e & 1);
+          if (r < p.d && c < p.d) out[r * p.d + c] = S[m][n][e];
+        }
+  }
+}
+
+// dg over one span of one (b, h), 256 tokens at a time from its end: <S, dS>
+// there, then the running sum of q.dq - k.dk.  The sums restart at every span,
+// so their rounding does not grow with the sequence.
+struct GateGrad {
+  const float *qdots, *kdots;   // [slices][B][H][N]
+  const float *enter, *leave;   // states entering each span forwards and backwards (both with v's channels as rows)
+  const float *last, *dlast;    // the state behind the last token (rows of v), its gradient (rows of k) or null
+  Operand dg;
+  int64_t N, H, BH, span_tokens;
+  int32_t spans, d, slices;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) gated_gate_grad(const __grid_constant__ GateGrad p) {
+  __shared__ float part[8];
+  __shared__ float head;
+  const int64_t span = blockIdx.x % p.spans, bh = blockIdx.x / p.spans, b = bh / p.H, h = bh % p.H;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t dd = static_cast<int64_t>(p.d) * p.d;
+  float s = 0.0f;
+  if (span + 1 < p.spans) {
+    const float *x = p.enter + (bh * p.spans + span + 1) * dd, *y = p.leave + (bh * p.spans + span) * dd;
+    for (int64_t i = threadIdx.x; i < dd; i += 256) s = fmaf(x[i], y[i], s);
+  } else if (p.dlast) {
+    const float *x = p.last + bh * dd, *y = p.dlast + bh * dd;
+    for (int64_t i = threadIdx.x; i < dd; i += 256) s = fmaf(x[i], y[i % p.d * p.d + i / p.d], s);
+  }
+#pragma unroll
+  for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(~0u, s, k);
+  if (lane == 0) part[warp] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < 128; ++i) s += red[i];
-    for (int64_t t = N - 1; t >= 0; --t) {
-      s += static_cast<double>(qdots[bh * N + t]) - static_cast<double>(kdots[bh * N + t]);
-      from_f(static_cast<T*>(dg.data) + b * dg.sb + t * dg.sn + h * dg.sh, static_cast<float>(s));
+    float t = 0.0f;
+    for (int i = 0; i < 8; ++i) t += part[i];
+    head = t;
+  }
+  __syncthreads();
+  const int64_t t0 = span * p.span_tokens, t1 = min(p.N, t0 + p.span_tokens);
+  float carry = head;
+  for (int64_t end = t1; end > t0; end -= 256) {
+    const int64_t t = end - 1 - threadIdx.x;   // thread 0 takes the last token
+    float x = 0.0f;
+    if (t >= t0)
+      for (int k = 0; k < p.slices; ++k) {
+        const int64_t i = (k * p.BH + bh) * p.N + t;
+        x += p.qdots[i] - p.kdots[i];
+      }
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const float y = __shfl_up_sync(~0u, x, k);
+      if (lane >= k) x += y;
     }
+    __syncthreads();   // the last block's totals are read
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    float before = carry, all = carry;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i < warp) before += part[i];
+      all += part[i];
+    }
+    if (t >= t0) from_f(static_cast<T*>(p.dg.data) + b * p.dg.sb + t * p.dg.sn + h * p.dg.sh, before + x);
+    carry = all;
   }
 }
 
-Scan scan_of(const GatedProblem& p) {
+// ------------------------------------------------------------------ launches
+
+int padded(int32_t d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
+
+// Spans a sequence is cut into.
+struct Cut {
+  int64_t chunks, span_chunks, spans;
+};
+
+Cut cut_for(const GatedProblem& p, int scans) {
+  Cut c;
+  c.chunks = (p.N + kChunk - 1) / kChunk;
+  const int64_t have = p.B * p.H * (p.d > 64 ? 2 : 1) * scans;
+  const int64_t room = int64_t{kSms} * 3;
+  int64_t spans = std::max<int64_t>(1, room / have);
+  c.span_chunks = std::max<int64_t>(4, (c.chunks + spans - 1) / spans);
+  c.spans = (c.chunks + c.span_chunks - 1) / c.span_chunks;
+  return c;
+}
+
+// 16-byte rows: cp.async takes them as they lie.
+bool rows_of_16(const GatedProblem& p, std::initializer_list<const Operand*> os) {
+  if (p.dtype != MHLA_BF16 || p.d % 8 != 0) return false;
+  for (const Operand* o : os)
+    if (reinterpret_cast<uintptr_t>(o->data) % 16 != 0 || o->sb % 8 != 0 || o->sn % 8 != 0 || o->sh % 8 != 0)
+      return false;
+  return true;
+}
+
+template <typename T, int DK, bool ASYNC>
+int launch_span_state(const ScanSet& set, int scans, cudaStream_t s) {
+  using L = Tile<T, DK, ASYNC>;
+  constexpr int kBytes = L::kStages * L::kIn * (L::kK + L::kV);
+  // a per-device setting: made on every call, for whichever device is current
+  if (cudaFuncSetAttribute(gated_span_state<T, DK, ASYNC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) !=
+      cudaSuccess)
+    return MHLA_ERR_CUDA;
+  const int64_t slices = (set.d + L::DV - 1) / L::DV;
+  KernelTimer timer("gated_span_state", s);
+  gated_span_state<T, DK, ASYNC>
+      <<<dim3(static_cast<unsigned>(set.BH * slices * (set.spans - 1)), scans), 128, kBytes, s>>>(set);
+  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+}
+
+template <typename T, int DK, bool ASYNC>
+int launch_scan(const ScanSet& set, int scans, cudaStream_t s) {
+  using L = Tile<T, DK, ASYNC>;
+  constexpr int kBytes = ScanShared<T, DK, ASYNC>::kBytes;
+  if (cudaFuncSetAttribute(gated_scan<T, DK, ASYNC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) !=
+      cudaSuccess)
+    return MHLA_ERR_CUDA;
+  const int64_t slices = (set.d + L::DV - 1) / L::DV;
+  KernelTimer timer("gated_scan", s);
+  gated_scan<T, DK, ASYNC><<<dim3(static_cast<unsigned>(set.BH * slices * set.spans), scans), 128, kBytes, s>>>(set);
+  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+}
+
+template <typename T, bool ASYNC>
+int run_scans_as(const ScanSet& set, int scans, bool span_state, cudaStream_t s) {
+  switch (padded(set.d)) {
+    case 32: return span_state ? launch_span_state<T, 32, ASYNC>(set, scans, s) : launch_scan<T, 32, ASYNC>(set, scans, s);
+    case 64: return span_state ? launch_span_state<T, 64, ASYNC>(set, scans, s) : launch_scan<T, 64, ASYNC>(set, scans, s);
+    default: return span_state ? launch_span_state<T, 128, ASYNC>(set, scans, s) : launch_scan<T, 128, ASYNC>(set, scans, s);
+  }
+}
+
+int run_scans(const GatedProblem& p, const ScanSet& set, int scans, bool async, bool span_state, cudaStream_t s) {
+  if (p.dtype == MHLA_F32) return run_scans_as<float, false>(set, scans, span_state, s);
+  return async ? run_scans_as<__nv_bfloat16, true>(set, scans, span_state, s)
+               : run_scans_as<__nv_bfloat16, false>(set, scans, span_state, s);
+}
+
+int run_join(const ScanSet& set, int scans, cudaStream_t s) {
+  KernelTimer timer("gated_join", s);
+  const int64_t n = set.BH * set.d * set.d;
+  gated_join<<<dim3(static_cast<unsigned>((n + 255) / 256), scans), 256, 0, s>>>(set);
+  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+}
+
+ScanSet scan_set(const GatedProblem& p, const Cut& c) {
+  ScanSet s = {};
+  s.g = p.g;
+  s.N = p.N; s.H = p.H; s.BH = p.B * p.H;
+  s.span_chunks = c.span_chunks; s.chunks = c.chunks;
+  s.spans = static_cast<int32_t>(c.spans);
+  s.d = p.d;
+  return s;
+}
+
+Scan plain_scan(const Operand& q, const Operand& k, const Operand& v, const Operand& out) {
   Scan a = {};
-  a.g = p.g;
-  a.N = p.N; a.H = p.H; a.d = p.d;
-  a.out_scale = a.k_scale = 1.0f;
+  a.q = q; a.k = k; a.v = v; a.out = out;
+  a.out_scale = a.state_scale = a.k_scale = 1.0f;
+  a.init_spans = 1;
   return a;
 }
 
-int run_scan(const GatedProblem& p, const Scan& a, void* stream) {
-  KernelTimer timer("gated_scan", stream);
-  const unsigned grid = static_cast<unsigned>(p.B * p.H);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p.dtype == MHLA_BF16)
-    gated_scan_simple<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
-  else
-    gated_scan_simple<float><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+struct SpanBuffers {
+  float *local, *decay;
+};
+
+size_t span_bytes(const GatedProblem& p, const Cut& c) {
+  if (c.spans < 2) return 0;
+  const int64_t n = p.B * p.H * c.spans;
+  return align_up(static_cast<size_t>(n * p.d * p.d) * 4) + align_up(static_cast<size_t>(n) * 4);
+}
+
+SpanBuffers carve_spans(const GatedProblem& p, const Cut& c, char** base) {
+  if (c.spans < 2) return SpanBuffers{nullptr, nullptr};
+  const int64_t n = p.B * p.H * c.spans;
+  SpanBuffers s;
+  s.local = reinterpret_cast<float*>(*base);
+  *base += align_up(static_cast<size_t>(n * p.d * p.d) * 4);
+  s.decay = reinterpret_cast<float*>(*base);
+  *base += align_up(static_cast<size_t>(n) * 4);
+  return s;
 }
 
 }  // namespace
 
-size_t gated_workspace_bytes(const GatedProblem&) { return 0; }
+size_t gated_workspace_bytes(const GatedProblem& p) { return span_bytes(p, cut_for(p, 1)); }
 
 size_t gated_bwd_workspace_bytes(const GatedProblem& p) {
-  const int64_t bh = p.B * p.H;
-  return 2 * align_up(static_cast<size_t>(bh * p.N) * 4) + align_up(static_cast<size_t>(bh * p.d * p.d) * 4);
+  const int64_t bh = p.B * p.H, slices = p.d > 64 ? 2 : 1;
+  return 2 * span_bytes(p, cut_for(p, 3)) + 2 * align_up(static_cast<size_t>(slices * bh * p.N) * 4) +
+         align_up(static_cast<size_t>(bh * p.d * p.d) * 4);
 }
 
-int launch_gated_forward(const GatedProblem& p, const float* state_in, const Operand& out, float* state_out, void*,
-                         void* stream) {
-  Scan a = scan_of(p);
-  a.q = p.q; a.k = p.k; a.v = p.v;
-  a.out = out;
+int launch_gated_forward(const GatedProblem& p, const float* state_in, const Operand& out, float* state_out,
+                         void* workspace, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const Cut c = cut_for(p, 1);
+  const bool async = rows_of_16(p, {&p.q, &p.k, &p.v, &out});
+  ScanSet set = scan_set(p, c);
+  Scan a = plain_scan(p.q, p.k, p.v, out);
+  a.out_scale = a.state_scale = p.scale;
   a.init = state_in;
   a.last = state_out;
-  a.out_scale = p.scale;
-  return run_scan(p, a, stream);
+  char* base = static_cast<char*>(workspace);
+  const SpanBuffers sb = carve_spans(p, c, &base);
+  a.local = sb.local;
+  a.decay = sb.decay;
+  set.scan[0] = a;
+  if (c.spans > 1) {
+    int rc = run_scans(p, set, 1, async, true, s);
+    if (rc == MHLA_OK) rc = run_join(set, 1, s);
+    if (rc != MHLA_OK) return rc;
+    set.scan[0].init = sb.local;
+    set.scan[0].init_spans = set.spans;
+  }
+  return run_scans(p, set, 1, async, false, s);
 }
 
 int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* workspace, void* stream) {
-  const int64_t bh = p.B * p.H;
-  char* base = static_cast<char*>(workspace);
-  float* qdots = reinterpret_cast<float*>(base);
-  base += align_up(static_cast<size_t>(bh * p.N) * 4);
-  float* kdots = reinterpret_cast<float*>(base);
-  base += align_up(static_cast<size_t>(bh * p.N) * 4);
-  float* last = reinterpret_cast<float*>(base);
-  Scan a = scan_of(p);
-  a.q = b.dout; a.k = p.v; a.v = p.k;
-  a.out = b.dq; a.dot = p.q; a.dots = qdots;
-  a.out_scale = p.scale;
-  a.init = b.state_in; a.last = last; a.transposed = true;
-  int rc = run_scan(p, a, stream);
-  a = scan_of(p);
-  a.reverse = true;
-  a.k_scale = p.scale;
-  a.q = p.k; a.k = p.q; a.v = b.dout;
-  a.out = b.dv;
-  a.init = b.dstate_out; a.last = b.dstate_in;
-  if (rc == MHLA_OK) rc = run_scan(p, a, stream);
-  a.q = p.v; a.k = b.dout; a.v = p.q;
-  a.out = b.dk; a.dot = p.k; a.dots = kdots;
-  a.last = nullptr; a.transposed = true;
-  if (rc == MHLA_OK) rc = run_scan(p, a, stream);
-  if (rc != MHLA_OK) return rc;
-  KernelTimer timer("gated_gate_grad", stream);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const Cut c = cut_for(p, 3);
+  const bool async = rows_of_16(p, {&p.q, &p.k, &p.v, &b.dout, &b.dq, &b.dk, &b.dv});
+  const int64_t bh = p.B * p.H, slices = p.d > 64 ? 2 : 1;
+  char* base = static_cast<char*>(workspace);
+  const SpanBuffers fwd = carve_spans(p, c, &base), back = carve_spans(p, c, &base);
+  float* qdots = reinterpret_cast<float*>(base);
+  base += align_up(static_cast<size_t>(slices * bh * p.N) * 4);
+  float* kdots = reinterpret_cast<float*>(base);
+  base += align_up(static_cast<size_t>(slices * bh * p.N) * 4);
+  float* last = reinterpret_cast<float*>(base);
+
+  ScanSet set = scan_set(p, c);
+  Scan dq = plain_scan(b.dout, p.v, p.k, b.dq);   // its state: S^T
+  dq.out_scale = dq.state_scale = p.scale;
+  dq.init = b.state_in;
+  dq.init_transposed = 1;
+  dq.last = last;
+  dq.dot = p.q;
+  dq.dots = qdots;
+  dq.local = fwd.local;
+  dq.decay = fwd.decay;
+  Scan dk = plain_scan(p.v, b.dout, p.q, b.dk);   // its state: dS^T
+  dk.reverse = 1;
+  dk.out_scale = dk.k_scale = p.scale;
+  dk.init = b.dstate_out;
+  dk.init_transposed = 1;
+  dk.dot = p.k;
+  dk.dots = kdots;
+  dk.local = back.local;
+  dk.decay = back.decay;
+  Scan dv = plain_scan(p.k, p.q, b.dout, b.dv);   // its state: dS
+  dv.reverse = 1;
+  dv.out_scale = dv.k_scale = p.scale;
+  dv.init = b.dstate_out;
+  dv.last = b.dstate_in;
+  set.scan[0] = dq;
+  set.scan[1] = dk;
+  set.scan[2] = dv;
+  int rc = MHLA_OK;
+  if (c.spans > 1) {
+    rc = run_scans(p, set, 2, async, true, s);
+    if (rc == MHLA_OK) rc = run_join(set, 2, s);
+    set.scan[0].init = fwd.local;
+    set.scan[1].init = set.scan[2].init = back.local;
+    set.scan[0].init_transposed = set.scan[1].init_transposed = 0;
+    set.scan[2].init_transposed = 1;
+    for (Scan& a : set.scan) a.init_spans = set.spans;
+  }
+  if (rc == MHLA_OK) rc = run_scans(p, set, 3, async, false, s);
+  if (rc != MHLA_OK) return rc;
+  GateGrad gg = {};
+  gg.qdots = qdots; gg.kdots = kdots;
+  gg.enter = fwd.local; gg.leave = back.local;
+  gg.last = last; gg.dlast = b.dstate_out;
+  gg.dg = b.dg;
+  gg.N = p.N; gg.H = p.H; gg.BH = bh;
+  gg.span_tokens = c.span_chunks * kChunk;
+  gg.spans = set.spans; gg.d = p.d; gg.slices = static_cast<int32_t>(slices);
+  KernelTimer timer("gated_gate_grad", stream);
+  const unsigned grid = static_cast<unsigned>(bh * c.spans);
   if (p.dtype == MHLA_BF16)
-    gated_gate_grad_simple<__nv_bfloat16><<<static_cast<unsigned>(bh), 128, 0, s>>>(qdots, kdots, last, b.dstate_out,
-                                                                                   b.dg, p.N, p.H, p.d);
+    gated_gate_grad<__nv_bfloat16><<<grid, 256, 0, s>>>(gg);
   else
-    gated_gate_grad_simple<float><<<static_cast<unsigned>(bh), 128, 0, s>>>(qdots, kdots, last, b.dstate_out, b.dg,
-                                                                           p.N, p.H, p.d);
+    gated_gate_grad<float><<<grid, 256, 0, s>>>(gg);
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
 
+// ------------------------------------------------------------------ one token
+
+// A CTA takes one (b, h) and 32 columns of its state: thread (row group y, column
+// x) carries every 8th row of a column.
+template <typename T>
+__global__ void __launch_bounds__(256) gated_step(const GatedProblem p, float* state, const Operand out) {
+  __shared__ float sq[128], sk[128], part[8][33];
+  const int64_t slices = (p.d + 31) / 32;
+  const int64_t bh = blockIdx.x / slices, b = bh / p.H, h = bh % p.H;
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = static_cast<int>(blockIdx.x % slices) * 32 + x;
+  auto at = [&](const Operand& o) { return static_cast<T*>(o.data) + b * o.sb + h * o.sh; };
+  if (threadIdx.x < p.d) {
+    sq[threadIdx.x] = to_f(at(p.q)[threadIdx.x]);
+    sk[threadIdx.x] = to_f(at(p.k)[threadIdx.x]);
+  }
+  const float g = to_f(*at(p.g));
+  const float decay = expf(g < kLowestGate ? kLowestGate : g);
+  const float v = c < p.d ? to_f(at(p.v)[c]) : 0.0f;
+  __syncthreads();
+  float o = 0.0f;
+  if (c < p.d) {
+    float* S = state + bh * p.d * p.d + c;
+    for (int r = y; r < p.d; r += 8) {
+      const float n = fmaf(sk[r], v, decay * S[r * p.d]);
+      S[r * p.d] = n;
+      o = fmaf(sq[r], n, o);
+    }
+  }
+  part[y][x] = o;
+  __syncthreads();
+  if (y == 0 && c < p.d) {
+    for (int i = 1; i < 8; ++i) o += part[i][x];
+    from_f(at(out) + c, p.scale * o);
+  }
+}
+
 int launch_gated_step(const GatedProblem& p, float* state, const Operand& out, void* stream) {
-  return launch_gated_forward(p, state, out, state, nullptr, stream);
+  KernelTimer timer("gated_step", stream);
+  const unsigned grid = static_cast<unsigned>(p.B * p.H * ((p.d + 31) / 32));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p.dtype == MHLA_BF16)
+    gated_step<__nv_bfloat16><<<grid, 256, 0, s>>>(p, state, out);
+  else
+    gated_step<float><<<grid, 256, 0, s>>>(p, state, out);
+  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
 
 }  // namespace mhla
