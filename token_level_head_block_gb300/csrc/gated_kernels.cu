@@ -81,8 +81,7 @@ struct Terms<float> {
 constexpr int kAdd = 3;
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -131,16 +130,46 @@ __device__ __forceinline__ void split(float x, float y, uint32_t (&t)[NT]) {
   }
 }
 
-// c += A B over the terms of both whose product is not below the last term's size.
-template <int NA, int NB>
-__device__ __forceinline__ void mma_terms(float (&c)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4],
-                                          int half) {
+// Accumulators of NT column tiles.  The tensor core truncates what it adds to an
+// accumulator, which drifts over a long chain: float32 runs keep the products of the
+// first terms, few additions, apart from the many small ones.
+template <int NT, bool APART>
+struct Accumulators {
+  float main[NT][4];
+  float small[APART ? NT : 1][4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        main[n][e] = 0.0f;
+        if (APART) small[APART ? n : 0][e] = 0.0f;
+      }
+  }
+  __device__ __forceinline__ float get(int n, int e) const {
+    return APART ? main[n][e] + small[APART ? n : 0][e] : main[n][e];
+  }
+};
+
+// acc[n0 .. n0 + 2 P) += A B over the terms of both whose product is not below the last
+// term's size; b[t][p] holds two column tiles.  Independent accumulators follow one another.
+template <int NA, int NB, int P, int NT, bool APART>
+__device__ __forceinline__ void mma_terms(Accumulators<NT, APART>& acc, int n0, const uint32_t (&a)[NA][4],
+                                          const uint32_t (&b)[NB][P][4]) {
   constexpr int kMost = NA > NB ? NA : NB;
 #pragma unroll
-  for (int i = 0; i < NA; ++i)
+  for (int i = NA - 1; i >= 0; --i)
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
-      if (i + j < kMost) mma(c, a[i], b[j][2 * half], b[j][2 * half + 1]);
+    for (int j = NB - 1; j >= 0; --j) {
+      if (i + j >= kMost) continue;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int n = n0 + 2 * p + f;
+          mma(APART && i + j > 0 ? acc.small[APART ? n : 0] : acc.main[n], a[i], b[j][p][2 * f], b[j][p][2 * f + 1]);
+        }
+    }
 }
 
 // A sum of log decays (in powers of two) as the sum of two floats: differences of
@@ -165,12 +194,18 @@ __device__ __forceinline__ Sum gate_sum(float g) {
   return r;
 }
 
-// What a chunk needs of its gates.
+// What a chunk needs of its gates.  Rows i of a block of 16 tokens see tokens j of other
+// blocks through e^{b_i - b_j} = e^{b_i - m} e^{m - b_j}, m at the edge of the
+// row's block towards them, so neither factor exceeds 1; the state, too, is read with
+// e^{b_i - m} e^m.  (Backwards every difference changes its sign.)  Within a block the
+// difference of the two sums is taken itself.
 struct Gates {
   float hi[kChunk], lo[kChunk];   // b_i
-  float read[kChunk];             // of the state, per token
-  float addw[kChunk];             // to the state, per token
-  float total;                    // of the state over the chunk
+  float row[kChunk];              // e^{b_i - m}
+  float col[4][kChunk];           // out_scale e^{m - b_j}, per block of rows
+  float addw[kChunk];             // k_scale e^{B - b_j}: to the state
+  float enter[4];                 // state_scale e^m
+  float total;                    // e^B: of the state over the chunk
   float pad[3];
 };
 
@@ -182,8 +217,10 @@ __device__ __forceinline__ float2 load_gates(const ScanSet& p, int64_t b, int64_
   return make_float2(t < p.N ? to_f(g[t * p.g.sn]) : 0.0f, t + 1 < p.N ? to_f(g[(t + 1) * p.g.sn]) : 0.0f);
 }
 
+__device__ __forceinline__ float exp2_of(Sum a, Sum b) { return exp2_fast((a.hi - b.hi) + (a.lo - b.lo)); }
+
 // One warp: the running sums and the weights of a chunk.  Returns B.
-__device__ __forceinline__ Sum chunk_gates(float2 g, Gates& out, bool reverse, float k_scale, int lane) {
+__device__ __forceinline__ Sum chunk_gates(float2 g, Gates& out, const Scan& a, int lane) {
   const Sum first = gate_sum(g.x), second = gate_sum(g.y);
   Sum run = add(first, second);
 #pragma unroll
@@ -193,24 +230,49 @@ __device__ __forceinline__ Sum chunk_gates(float2 g, Gates& out, bool reverse, f
     o.lo = __shfl_up_sync(~0u, run.lo, s);
     if (lane >= s) run = add(o, run);
   }
-  Sum all;
-  all.hi = __shfl_sync(~0u, run.hi, 31);
-  all.lo = __shfl_sync(~0u, run.lo, 31);
+  const Sum none = {0.0f, 0.0f};
+  auto of_lane = [&](int l) {
+    Sum r;
+    r.hi = __shfl_sync(~0u, run.hi, l);
+    r.lo = __shfl_sync(~0u, run.lo, l);
+    return r;
+  };
+  const Sum all = of_lane(31);
+  Sum edge[5] = {none, of_lane(7), of_lane(15), of_lane(23), all};   // between the blocks
   Sum before;
   before.hi = __shfl_up_sync(~0u, run.hi, 1);
   before.lo = __shfl_up_sync(~0u, run.lo, 1);
-  if (lane == 0) before.hi = before.lo = 0.0f;
+  if (lane == 0) before = none;
   const Sum at[2] = {add(before, first), run};
+  const int block = lane >> 3;
+  const bool reverse = a.reverse;
+  Sum m = reverse ? edge[1] : edge[0];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int i = 2 * lane + e;
-    const float up = exp2f(at[e].hi + at[e].lo), rest = exp2f((all.hi - at[e].hi) + (all.lo - at[e].lo));
-    out.hi[i] = at[e].hi;
-    out.lo[i] = at[e].lo;
-    out.read[i] = reverse ? rest : up;
-    out.addw[i] = k_scale * (reverse ? up : rest);
+  for (int i = 1; i < 4; ++i)
+    if (block == i) m = reverse ? edge[i + 1] : edge[i];
+  float2 hi, lo, row, addw;
+  hi = make_float2(at[0].hi, at[1].hi);
+  lo = make_float2(at[0].lo, at[1].lo);
+  row = reverse ? make_float2(exp2_of(m, at[0]), exp2_of(m, at[1])) : make_float2(exp2_of(at[0], m), exp2_of(at[1], m));
+  addw = reverse ? make_float2(exp2_of(at[0], none), exp2_of(at[1], none))
+                 : make_float2(exp2_of(all, at[0]), exp2_of(all, at[1]));
+  addw.x *= a.k_scale;
+  addw.y *= a.k_scale;
+  *reinterpret_cast<float2*>(out.hi + 2 * lane) = hi;
+  *reinterpret_cast<float2*>(out.lo + 2 * lane) = lo;
+  *reinterpret_cast<float2*>(out.row + 2 * lane) = row;
+  *reinterpret_cast<float2*>(out.addw + 2 * lane) = addw;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (reverse ? block <= r : block >= r) continue;   // tokens the rows of block r do not see through m
+    const Sum e = reverse ? edge[r + 1] : edge[r];
+    float2 c = reverse ? make_float2(exp2_of(at[0], e), exp2_of(at[1], e)) : make_float2(exp2_of(e, at[0]), exp2_of(e, at[1]));
+    c.x *= a.out_scale;
+    c.y *= a.out_scale;
+    *reinterpret_cast<float2*>(out.col[r] + 2 * lane) = c;
   }
-  if (lane == 0) out.total = exp2f(all.hi + all.lo);
+  if ((lane & 7) == 0) out.enter[block] = a.state_scale * (reverse ? exp2_of(all, m) : exp2_of(m, none));
+  if (lane == 0) out.total = exp2_of(all, none);
   return all;
 }
 
@@ -228,41 +290,60 @@ struct Tile {
   static constexpr int kColTiles = DK >= 64 ? DV / 8 : DV / 16;   // of eight columns
 };
 
-// Copies a chunk's rows of one operand (columns [c0, c0 + W)) into kIn planes.
+// Copies chunks of one operand (columns [c0, c0 + W)) into kIn planes.
 template <typename T, int W, int PITCH, bool ASYNC>
-__device__ __forceinline__ void load_rows(char* dst, const Operand& o, int64_t b, int64_t h, int64_t chunk, int64_t N,
-                                          int c0, int d) {
-  const T* src = static_cast<const T*>(o.data) + b * o.sb + h * o.sh + c0;
-  const int64_t t0 = chunk * kChunk;
-  const int rows = static_cast<int>(N - t0 < kChunk ? N - t0 : kChunk);
-  if constexpr (ASYNC) {
-    constexpr int kUnits = W / 8;
-    const uint32_t base = ptx::smem_u32(dst);
-#pragma unroll
-    for (int i = threadIdx.x; i < kChunk * kUnits; i += 128) {
-      const int r = i / kUnits, u = i % kUnits;
-      if (c0 + 8 * u >= d) continue;   // the columns behind d were zeroed at the start
-      const bool in = r < rows;
-      cp_async_16(base + (r * PITCH + 8 * u) * 2, src + (in ? (t0 + r) * o.sn + 8 * u : 0), in ? 16 : 0);
+struct RowLoader {
+  const T* src;
+  int64_t step;      // elements: ASYNC from pass to pass, else from token to token
+  int32_t width;     // columns in the tensor
+  __device__ __forceinline__ RowLoader(const Operand& o, int64_t b, int64_t h, int c0, int d) {
+    src = static_cast<const T*>(o.data) + b * o.sb + h * o.sh + c0;
+    width = min(W, d - c0);
+    if constexpr (ASYNC) {
+      constexpr int kUnits = W / 8, kRows = 128 / kUnits;   // 16-byte units, rows a pass
+      src += static_cast<int>(threadIdx.x) / kUnits * o.sn + 8 * (threadIdx.x % kUnits);
+      step = kRows * o.sn;
+    } else {
+      step = o.sn;
     }
-  } else {
-    constexpr int kPlane = kChunk * PITCH;
-    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(dst);
-    for (int i = threadIdx.x; i < kChunk * W / 2; i += 128) {
-      const int r = i / (W / 2), c = 2 * (i % (W / 2));
-      const T* x = src + (t0 + r) * o.sn + c;
-      float a = r < rows && c0 + c < d ? to_f(x[0]) : 0.0f, e = r < rows && c0 + c + 1 < d ? to_f(x[1]) : 0.0f;
+  }
+  __device__ __forceinline__ void load(char* dst, int64_t chunk, int64_t N) const {
+    const int rows = static_cast<int>(min(N - chunk * kChunk, static_cast<int64_t>(kChunk)));
+    if constexpr (ASYNC) {
+      constexpr int kUnits = W / 8, kRows = 128 / kUnits, kSteps = kChunk / kRows;
+      const int r = threadIdx.x / kUnits, u = threadIdx.x % kUnits;
+      if (8 * u >= width) return;   // the columns behind d were zeroed at the start
+      uint32_t at = ptx::smem_u32(dst) + (r * PITCH + 8 * u) * 2;
+      const T* x = src + chunk * (kSteps * step);
+      if (rows == kChunk) {
 #pragma unroll
-      for (int n = 0; n < Terms<T>::kIn; ++n) {
-        const uint32_t p = pack(a, e);
-        *reinterpret_cast<uint32_t*>(out + n * kPlane + r * PITCH + c) = p;
-        // an infinity is its first term alone
-        a = fabsf(low(p)) < __int_as_float(0x7F800000) ? a - low(p) : 0.0f;
-        e = fabsf(high(p)) < __int_as_float(0x7F800000) ? e - high(p) : 0.0f;
+        for (int i = 0; i < kSteps; ++i, x += step) cp_async_16(at + i * kRows * PITCH * 2, x, 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const bool in = r + i * kRows < rows;
+          cp_async_16(at + i * kRows * PITCH * 2, in ? x + i * step : static_cast<const T*>(src), in ? 16 : 0);
+        }
+      }
+    } else {
+      constexpr int kPlane = kChunk * PITCH;
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(dst);
+      for (int i = threadIdx.x; i < kChunk * W / 2; i += 128) {
+        const int r = i / (W / 2), c = 2 * (i % (W / 2));
+        const T* x = src + (chunk * kChunk + r) * step + c;
+        float a = r < rows && c < width ? to_f(x[0]) : 0.0f, e = r < rows && c + 1 < width ? to_f(x[1]) : 0.0f;
+#pragma unroll
+        for (int n = 0; n < Terms<T>::kIn; ++n) {
+          const uint32_t p = pack(a, e);
+          *reinterpret_cast<uint32_t*>(out + n * kPlane + r * PITCH + c) = p;
+          // an infinity is its first term alone
+          a = fabsf(low(p)) < __int_as_float(0x7F800000) ? a - low(p) : 0.0f;
+          e = fabsf(high(p)) < __int_as_float(0x7F800000) ? e - high(p) : 0.0f;
+        }
       }
     }
   }
-}
+};
 
 // Each thread's part of the state: row tile m, column tile n, the four values of
 // an mma accumulator.  `row` and `col` are those of the first.
@@ -311,6 +392,38 @@ __device__ __forceinline__ uint32_t column_address(uint32_t base, int pitch, int
   return base + ((token0 + (lane & 7) + ((lane >> 3) & 1) * 8) * pitch + col0 + (lane >> 4) * 8) * 2;
 }
 
+// S <- e^B S + sum over a chunk's tokens of (addw k)^T v.  The chunk's sum is formed apart
+// and added once, rounded to nearest: a long sequence must not gather the tensor
+// core's truncation.
+template <typename T, int DK, bool ASYNC>
+__device__ __forceinline__ void add_chunk(float (&S)[Tile<T, DK, ASYNC>::kRowTiles][Tile<T, DK, ASYNC>::kColTiles][4],
+                                          uint32_t k_base, uint32_t v_base, const Gates& w, int warp, int lane) {
+  using L = Tile<T, DK, ASYNC>;
+  constexpr int P = L::kColTiles / 2;
+  const int row0 = DK >= 64 ? (DK / 4) * warp : 16 * (warp & 1), col0 = DK >= 64 ? 0 : 16 * (warp >> 1);
+  const float total = w.total;
+#pragma unroll
+  for (int m = 0; m < L::kRowTiles; ++m) {
+    Accumulators<L::kColTiles, (L::kIn > 1)> sum;
+    sum.clear();
+#pragma unroll
+    for (int s = 0; s < kChunk / 16; ++s) {
+      uint32_t ka[kAdd][4], vb[L::kIn][P][4];
+#pragma unroll
+      for (int t = 0; t < L::kIn; ++t)
+#pragma unroll
+        for (int n = 0; n < P; ++n)
+          ldsm_t(vb[t][n], column_address(v_base + t * L::kV, L::kPitchV, 16 * s, col0 + 16 * n, lane));
+      add_operand<T, DK, ASYNC>(ka, k_base, row0 + 16 * m, s, w.addw, lane);
+      mma_terms(sum, 0, ka, vb);
+    }
+#pragma unroll
+    for (int n = 0; n < L::kColTiles; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[m][n][e] = fmaf(total, S[m][n][e], sum.get(n, e));
+  }
+}
+
 template <typename T, int DK, bool ASYNC>
 __global__ void __launch_bounds__(128) gated_span_state(const __grid_constant__ ScanSet p) {
   using L = Tile<T, DK, ASYNC>;
@@ -336,21 +449,22 @@ __global__ void __launch_bounds__(128) gated_span_state(const __grid_constant__ 
       reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
   }
+  const RowLoader<T, DK, L::kPitchK, ASYNC> rows_k(a.k, b, h, 0, p.d);
+  const RowLoader<T, L::DV, L::kPitchV, ASYNC> rows_v(a.v, b, h, c0, p.d);
+  auto chunk_of = [&](int i) { return first + (reverse ? count - 1 - i : i); };
   auto load = [&](int i) {
-    const int64_t chunk = first + (reverse ? count - 1 - i : i);
     char* st = smem + (i % L::kStages) * kStage;
-    load_rows<T, DK, L::kPitchK, ASYNC>(st, a.k, b, h, chunk, p.N, 0, p.d);
-    load_rows<T, L::DV, L::kPitchV, ASYNC>(st + L::kIn * L::kK, a.v, b, h, chunk, p.N, c0, p.d);
+    rows_k.load(st, chunk_of(i), p.N);
+    rows_v.load(st + L::kIn * L::kK, chunk_of(i), p.N);
     if (ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto gate_chunk = [&](int i) { return first + (reverse ? count - 1 - i : i); };
 
   float S[L::kRowTiles][L::kColTiles][4] = {};
   Sum all = {0.0f, 0.0f};
   float2 g = make_float2(0.0f, 0.0f);
   if (warp == 0) {
-    all = chunk_gates(load_gates<T>(p, b, h, gate_chunk(0), lane), gates[0], reverse, a.k_scale, lane);
-    if (count > 1) g = load_gates<T>(p, b, h, gate_chunk(1), lane);
+    all = chunk_gates(load_gates<T>(p, b, h, chunk_of(0), lane), gates[0], a, lane);
+    if (count > 1) g = load_gates<T>(p, b, h, chunk_of(1), lane);
   }
   if constexpr (ASYNC) load(0);
   for (int i = 0; i < count; ++i) {
@@ -364,38 +478,11 @@ __global__ void __launch_bounds__(128) gated_span_state(const __grid_constant__ 
       __syncthreads();
     }
     if (warp == 0 && i + 1 < count) {
-      all = add(all, chunk_gates(g, gates[(i + 1) & 1], reverse, a.k_scale, lane));
-      if (i + 2 < count) g = load_gates<T>(p, b, h, gate_chunk(i + 2), lane);
+      all = add(all, chunk_gates(g, gates[(i + 1) & 1], a, lane));
+      if (i + 2 < count) g = load_gates<T>(p, b, h, chunk_of(i + 2), lane);
     }
     const uint32_t k_base = ptx::smem_u32(smem + (i % L::kStages) * kStage);
-    const uint32_t v_base = k_base + L::kIn * L::kK;
-    const Gates& w = gates[i & 1];
-#pragma unroll
-    for (int m = 0; m < L::kRowTiles; ++m)
-#pragma unroll
-      for (int n = 0; n < L::kColTiles; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[m][n][e] *= w.total;
-    const int row0 = DK >= 64 ? (DK / 4) * warp : 16 * (warp & 1), col0 = DK >= 64 ? 0 : 16 * (warp >> 1);
-#pragma unroll
-    for (int s = 0; s < kChunk / 16; ++s) {
-      uint32_t ka[L::kRowTiles][kAdd][4];
-#pragma unroll
-      for (int m = 0; m < L::kRowTiles; ++m)
-        add_operand<T, DK, ASYNC>(ka[m], k_base, row0 + 16 * m, s, w.addw, lane);
-#pragma unroll
-      for (int n = 0; n < L::kColTiles; n += 2) {
-        uint32_t vb[L::kIn][4];
-#pragma unroll
-        for (int t = 0; t < L::kIn; ++t)
-          ldsm_t(vb[t], column_address(v_base + t * L::kV, L::kPitchV, 16 * s, col0 + 8 * n, lane));
-#pragma unroll
-        for (int m = 0; m < L::kRowTiles; ++m) {
-          mma_terms(S[m][n], ka[m], vb, 0);
-          mma_terms(S[m][n + 1], ka[m], vb, 1);
-        }
-      }
-    }
+    add_chunk<T, DK, ASYNC>(S, k_base, k_base + L::kIn * L::kK, gates[i & 1], warp, lane);
   }
   const StatePlace<DK> at(warp, lane);
   float* out = a.local + (bh * p.spans + span) * p.d * p.d;
@@ -445,35 +532,6 @@ __global__ void __launch_bounds__(256) gated_join(const __grid_constant__ ScanSe
   }
 }
 
-// The masked 16 x 16 block of scores times its 16 rows of v without the tensor
-// core, for rows of v that hold an infinity or NaN: a row must not see those of
-// later tokens (0 times infinity).
-template <typename T, int DK, bool ASYNC>
-__device__ __noinline__ void diagonal_apart(float (&o)[Tile<T, DK, ASYNC>::DV / 8][4], const float (&pr)[2][4],
-                                            const __nv_bfloat16* v, bool reverse, int lane) {
-  using L = Tile<T, DK, ASYNC>;
-  const int row = lane >> 2;
-  for (int j = 0; j < 16; ++j) {
-    const int src = (lane & ~3) | ((j & 7) >> 1);
-    // element (row, j): accumulator of column tile j / 8, value j % 2; (row + 8, j): the next two
-    float x[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = __shfl_sync(~0u, j < 8 ? pr[0][e] : pr[1][e], src);
-    const float up = j & 1 ? x[1] : x[0], dn = j & 1 ? x[3] : x[2];
-    const bool sees_up = reverse ? j >= row : j <= row, sees_dn = reverse ? j >= row + 8 : j <= row + 8;
-#pragma unroll
-    for (int n = 0; n < L::DV / 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float y = 0.0f;
-        for (int t = 0; t < L::kIn; ++t)
-          y += __bfloat162float(v[t * (L::kV / 2) + j * L::kPitchV + 8 * n + 2 * (lane & 3) + e]);
-        if (sees_up) o[n][e] = fmaf(up, y, o[n][e]);
-        if (sees_dn) o[n][2 + e] = fmaf(dn, y, o[n][2 + e]);
-      }
-  }
-}
-
 template <typename T, int DK, bool ASYNC>
 struct ScanShared {
   using L = Tile<T, DK, ASYNC>;
@@ -481,12 +539,173 @@ struct ScanShared {
   static constexpr int kBytes = L::kStages * kStage + Terms<T>::kState * L::kS;
 };
 
+// The outputs of a chunk for one warp's 16 rows: what they read from the state,
+// the tokens of other blocks, then their own block's.
+template <typename T, int DK, bool ASYNC, bool REVERSE>
+__device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::DV / 8, (Terms<T>::kIn > 1)>& o,
+                                           const char* stage, uint32_t s_base, const Gates& w, float out_scale, int own,
+                                           int lane) {
+  using L = Tile<T, DK, ASYNC>;
+  constexpr int kScore = Terms<T>::kScore, kState = Terms<T>::kState, NV = L::DV / 8, P = NV / 2, kSteps = kChunk / 16;
+  constexpr bool kApart = L::kIn > 1;
+  const uint32_t q_base = ptx::smem_u32(stage), k_base = q_base + L::kIn * L::kK, v_base = k_base + L::kIn * L::kK;
+  const int rows0 = 16 * own, row = rows0 + (lane >> 2);
+  Accumulators<2 * kSteps, kApart> sc;
+  sc.clear();
+  o.clear();
+#pragma unroll
+  for (int ks = 0; ks < DK / 16; ++ks) {
+    uint32_t qa[L::kIn][4];
+#pragma unroll
+    for (int t = 0; t < L::kIn; ++t)
+      ldsm(qa[t], q_base + t * L::kK +
+                      ((rows0 + (lane & 7) + ((lane >> 3) & 1) * 8) * L::kPitchK + 16 * ks + (lane >> 4) * 8) * 2);
+    uint32_t sb[kState][P][4];
+#pragma unroll
+    for (int t = 0; t < kState; ++t)
+#pragma unroll
+      for (int n = 0; n < P; ++n)
+        ldsm_t(sb[t][n], column_address(s_base + t * L::kS, L::kPitchV, 16 * ks, 16 * n, lane));
+    mma_terms(o, 0, qa, sb);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      if (REVERSE ? s < own : s > own) continue;
+      uint32_t kb[L::kIn][1][4];
+#pragma unroll
+      for (int t = 0; t < L::kIn; ++t)
+        ldsm(kb[t][0], k_base + t * L::kK +
+                           ((16 * s + (lane & 7) + (lane >> 4) * 8) * L::kPitchK + 16 * ks + ((lane >> 3) & 1) * 8) * 2);
+      mma_terms(sc, 2 * s, qa, kb);
+    }
+  }
+  const float enter = w.enter[own];
+#pragma unroll
+  for (int n = 0; n < NV; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      o.main[n][e] = enter * o.get(n, e);
+      if (kApart) o.small[kApart ? n : 0][e] = 0.0f;
+    }
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    if (REVERSE ? s <= own : s >= own) continue;
+    uint32_t pa[kScore][4], vb[L::kIn][P][4];
+#pragma unroll
+    for (int t = 0; t < L::kIn; ++t)
+#pragma unroll
+      for (int n = 0; n < P; ++n)
+        ldsm_t(vb[t][n], column_address(v_base + t * L::kV, L::kPitchV, 16 * s, 16 * n, lane));
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const float2 c = *reinterpret_cast<const float2*>(w.col[own] + 16 * s + 8 * f + 2 * (lane & 3));
+      uint32_t t0[kScore], t1[kScore];
+      split<kScore>(sc.get(2 * s + f, 0) * c.x, sc.get(2 * s + f, 1) * c.y, t0);
+      split<kScore>(sc.get(2 * s + f, 2) * c.x, sc.get(2 * s + f, 3) * c.y, t1);
+#pragma unroll
+      for (int t = 0; t < kScore; ++t) {
+        pa[t][2 * f] = t0[t];
+        pa[t][2 * f + 1] = t1[t];
+      }
+    }
+    mma_terms(o, 0, pa, vb);
+  }
+  const float row0 = w.row[row], row1 = w.row[row + 8];
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    o.main[n][0] *= row0; o.main[n][1] *= row0;
+    o.main[n][2] *= row1; o.main[n][3] *= row1;
+    if (kApart) {
+      float* x = o.small[kApart ? n : 0];
+      x[0] *= row0; x[1] *= row0;
+      x[2] *= row1; x[3] *= row1;
+    }
+  }
+  // the own block: the scores that a row sees
+  float own_sc[2][4] = {};
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s)
+    if (s == own)
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) own_sc[f][e] = sc.get(2 * s + f, e);
+  const float bh0 = w.hi[row], bl0 = w.lo[row], bh1 = w.hi[row + 8], bl1 = w.lo[row + 8];
+#pragma unroll
+  for (int f = 0; f < 2; ++f) {
+    const int j = rows0 + 8 * f + 2 * (lane & 3);
+    const float2 hj = *reinterpret_cast<const float2*>(w.hi + j), lj = *reinterpret_cast<const float2*>(w.lo + j);
+    float x[4] = {(bh0 - hj.x) + (bl0 - lj.x), (bh0 - hj.y) + (bl0 - lj.y), (bh1 - hj.x) + (bl1 - lj.x),
+                  (bh1 - hj.y) + (bl1 - lj.y)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = row + (e >> 1) * 8, c = j + (e & 1);
+      const bool keep = REVERSE ? c >= r : c <= r;
+      own_sc[f][e] = keep ? own_sc[f][e] * (out_scale * exp2_fast(REVERSE ? -x[e] : x[e])) : 0.0f;
+    }
+  }
+  uint32_t vb[L::kIn][P][4];
+#pragma unroll
+  for (int t = 0; t < L::kIn; ++t)
+#pragma unroll
+    for (int n = 0; n < P; ++n)
+      ldsm_t(vb[t][n], column_address(v_base + t * L::kV, L::kPitchV, rows0, 16 * n, lane));
+  // A row of v that holds an infinity or NaN must not reach the rows that do not see
+  // it (0 times infinity): such a block goes without the tensor core.
+  uint32_t bad = 0;
+#pragma unroll
+  for (int n = 0; n < P; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&vb[0][n][e]),
+                                       __floats2bfloat162_rn(0.0f, 0.0f));
+      bad |= *reinterpret_cast<const uint32_t*>(&z);
+    }
+  if (!__any_sync(~0u, bad & 0x7FFF7FFFu)) {
+    uint32_t pa[kScore][4];
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      uint32_t t0[kScore], t1[kScore];
+      split<kScore>(own_sc[f][0], own_sc[f][1], t0);
+      split<kScore>(own_sc[f][2], own_sc[f][3], t1);
+#pragma unroll
+      for (int t = 0; t < kScore; ++t) {
+        pa[t][2 * f] = t0[t];
+        pa[t][2 * f + 1] = t1[t];
+      }
+    }
+    mma_terms(o, 0, pa, vb);
+  } else {
+    const __nv_bfloat16* v =
+        reinterpret_cast<const __nv_bfloat16*>(stage + 2 * L::kIn * L::kK) + rows0 * L::kPitchV + 2 * (lane & 3);
+#pragma unroll 1
+    for (int j = 0; j < 16; ++j) {
+      const int src = (lane & ~3) | ((j & 7) >> 1);
+      float x[4];   // (row, j): column tile j / 8, value j % 2 of its lane; (row + 8, j): the two behind
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = __shfl_sync(~0u, j < 8 ? own_sc[0][e] : own_sc[1][e], src);
+      const float up = j & 1 ? x[1] : x[0], dn = j & 1 ? x[3] : x[2];
+      const int r = lane >> 2;
+      const bool sees_up = REVERSE ? j >= r : j <= r, sees_dn = REVERSE ? j >= r + 8 : j <= r + 8;
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float y = 0.0f;
+#pragma unroll
+          for (int t = 0; t < L::kIn; ++t) y += __bfloat162float(v[t * (L::kV / 2) + j * L::kPitchV + 8 * n + e]);
+          if (sees_up) o.main[n][e] = fmaf(up, y, o.main[n][e]);
+          if (sees_dn) o.main[n][2 + e] = fmaf(dn, y, o.main[n][2 + e]);
+        }
+    }
+  }
+}
+
 template <typename T, int DK, bool ASYNC>
 __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
     gated_scan(const __grid_constant__ ScanSet p) {
   using L = Tile<T, DK, ASYNC>;
   using M = ScanShared<T, DK, ASYNC>;
-  constexpr int kScore = Terms<T>::kScore, kState = Terms<T>::kState, NV = L::DV / 8;
+  constexpr int kState = Terms<T>::kState, NV = L::DV / 8;
   extern __shared__ __align__(16) char smem[];
   __shared__ __align__(16) Gates gates[2];
   const Scan& a = p.scan[blockIdx.y];
@@ -502,7 +721,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
   const bool reverse = a.reverse;
   // Rows later in the order see more of the chunk: neighbouring CTAs give them
   // to different warps, so that an SM's four schedulers get the same work.
-  const int rows0 = 16 * ((warp + static_cast<int>(blockIdx.x)) & 3);
+  const int own = (warp + static_cast<int>(blockIdx.x)) & 3, rows0 = 16 * own;
   char* planes = smem + L::kStages * M::kStage;
   const uint32_t s_base = ptx::smem_u32(planes);
 
@@ -511,12 +730,14 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
       reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
   }
+  const RowLoader<T, DK, L::kPitchK, ASYNC> rows_q(a.q, b, h, 0, p.d), rows_k(a.k, b, h, 0, p.d);
+  const RowLoader<T, L::DV, L::kPitchV, ASYNC> rows_v(a.v, b, h, c0, p.d);
   auto chunk_of = [&](int i) { return first + (reverse ? count - 1 - i : i); };
   auto load = [&](int i) {
     char* st = smem + (i % L::kStages) * M::kStage;
-    load_rows<T, DK, L::kPitchK, ASYNC>(st, a.q, b, h, chunk_of(i), p.N, 0, p.d);
-    load_rows<T, DK, L::kPitchK, ASYNC>(st + L::kIn * L::kK, a.k, b, h, chunk_of(i), p.N, 0, p.d);
-    load_rows<T, L::DV, L::kPitchV, ASYNC>(st + 2 * L::kIn * L::kK, a.v, b, h, chunk_of(i), p.N, c0, p.d);
+    rows_q.load(st, chunk_of(i), p.N);
+    rows_k.load(st + L::kIn * L::kK, chunk_of(i), p.N);
+    rows_v.load(st + 2 * L::kIn * L::kK, chunk_of(i), p.N);
     if (ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
   };
   if constexpr (ASYNC) load(0);
@@ -553,12 +774,12 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
   };
   publish();
 
+  // the warps take the gates of the chunks in turn, a chunk ahead
   float2 g = make_float2(0.0f, 0.0f);
-  if (warp == 0) {
-    chunk_gates(load_gates<T>(p, b, h, chunk_of(0), lane), gates[0], reverse, a.k_scale, lane);
-    if (count > 1) g = load_gates<T>(p, b, h, chunk_of(1), lane);
-  }
+  if (warp == 0) chunk_gates(load_gates<T>(p, b, h, chunk_of(0), lane), gates[0], a, lane);
+  if (warp == 1 && count > 1) g = load_gates<T>(p, b, h, chunk_of(1), lane);
 
+  T* const out = static_cast<T*>(a.out.data) + b * a.out.sb + h * a.out.sh + c0;
   for (int i = 0; i < count; ++i) {
     if constexpr (ASYNC) {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -569,196 +790,93 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
       load(i);
       __syncthreads();
     }
-    if (warp == 0 && i + 1 < count) {
-      chunk_gates(g, gates[(i + 1) & 1], reverse, a.k_scale, lane);
-      if (i + 2 < count) g = load_gates<T>(p, b, h, chunk_of(i + 2), lane);
-    }
+    if (i + 1 < count && warp == ((i + 1) & 3)) chunk_gates(g, gates[(i + 1) & 1], a, lane);
+    if (i + 2 < count && warp == ((i + 2) & 3)) g = load_gates<T>(p, b, h, chunk_of(i + 2), lane);
     char* stage = smem + (i % L::kStages) * M::kStage;
-    const uint32_t q_base = ptx::smem_u32(stage);
-    const uint32_t k_base = q_base + L::kIn * L::kK, v_base = k_base + L::kIn * L::kK;
     const Gates& w = gates[i & 1];
     const int row = rows0 + (lane >> 2);
+    const int64_t t0 = chunk_of(i) * kChunk;
+    {
+      Accumulators<NV, (L::kIn > 1)> o;
+      if (reverse)
+        read_chunk<T, DK, ASYNC, true>(o, stage, s_base, w, a.out_scale, own, lane);
+      else
+        read_chunk<T, DK, ASYNC, false>(o, stage, s_base, w, a.out_scale, own, lane);
 
-    // scores (this warp's 16 rows; only the 16-token steps they see) and what the rows read from the state
-    float sc[kChunk / 8][4] = {}, o[NV][4] = {};
-    const int own = rows0 / 16;
-#pragma unroll
-    for (int ks = 0; ks < DK / 16; ++ks) {
-      uint32_t qa[L::kIn][4];
-#pragma unroll
-      for (int t = 0; t < L::kIn; ++t)
-        ldsm(qa[t], q_base + t * L::kK +
-                        ((rows0 + (lane & 7) + ((lane >> 3) & 1) * 8) * L::kPitchK + 16 * ks + (lane >> 4) * 8) * 2);
-#pragma unroll
-      for (int s = 0; s < kChunk / 16; ++s) {
-        if (reverse ? s < own : s > own) continue;
-        uint32_t kb[L::kIn][4];
-#pragma unroll
-        for (int t = 0; t < L::kIn; ++t)
-          ldsm(kb[t], k_base + t * L::kK +
-                          ((16 * s + (lane & 7) + (lane >> 4) * 8) * L::kPitchK + 16 * ks + ((lane >> 3) & 1) * 8) * 2);
-        mma_terms(sc[2 * s], qa, kb, 0);
-        mma_terms(sc[2 * s + 1], qa, kb, 1);
-      }
-#pragma unroll
-      for (int n = 0; n < NV; n += 2) {
-        uint32_t sb[kState][4];
-#pragma unroll
-        for (int t = 0; t < kState; ++t)
-          ldsm_t(sb[t], column_address(s_base + t * L::kS, L::kPitchV, 16 * ks, 8 * n, lane));
-        mma_terms(o[n], qa, sb, 0);
-        mma_terms(o[n + 1], qa, sb, 1);
-      }
-    }
-    const float read0 = a.state_scale * w.read[row], read1 = a.state_scale * w.read[row + 8];
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      o[n][0] *= read0; o[n][1] *= read0;
-      o[n][2] *= read1; o[n][3] *= read1;
-    }
-#pragma unroll
-    for (int m = 0; m < L::kRowTiles; ++m)
-#pragma unroll
-      for (int n = 0; n < L::kColTiles; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[m][n][e] *= w.total;
-    const float bh0 = w.hi[row], bl0 = w.lo[row], bh1 = w.hi[row + 8], bl1 = w.lo[row + 8];
-    const int srow0 = DK >= 64 ? (DK / 4) * warp : 16 * (warp & 1), scol0 = DK >= 64 ? 0 : 16 * (warp >> 1);
-    // 16 tokens at a time: their decayed scores times v, and what they add to the state
-#pragma unroll
-    for (int s = 0; s < kChunk / 16; ++s) {
-      const bool seen = reverse ? s >= own : s <= own;
-      bool apart = false;
-      float pr[2][4];
-      uint32_t pa[kScore][4];
-      if (seen) {
+      // rows out: rounded once, through this warp's own rows of q
+      if (a.dots) {
+        const T* dot = static_cast<const T*>(a.dot.data) + b * a.dot.sb + h * a.dot.sh + c0;
+        float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          const int j = 16 * s + 8 * f + 2 * (lane & 3);
-          const float2 hj = *reinterpret_cast<const float2*>(w.hi + j), lj = *reinterpret_cast<const float2*>(w.lo + j);
-          const float sign = reverse ? -1.0f : 1.0f;
-          const float x[4] = {sign * ((bh0 - hj.x) + (bl0 - lj.x)), sign * ((bh0 - hj.y) + (bl0 - lj.y)),
-                              sign * ((bh1 - hj.x) + (bl1 - lj.x)), sign * ((bh1 - hj.y) + (bl1 - lj.y))};
+          const int64_t t = t0 + row + 8 * f;
+          if (t < p.N) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = row + (e >> 1) * 8, c = j + (e & 1);
-            const bool keep = reverse ? c >= r : c <= r;
-            pr[f][e] = keep ? a.out_scale * sc[2 * s + f][e] * exp2_fast(x[e]) : 0.0f;
-          }
-          uint32_t t0[kScore], t1[kScore];
-          split<kScore>(pr[f][0], pr[f][1], t0);
-          split<kScore>(pr[f][2], pr[f][3], t1);
-#pragma unroll
-          for (int t = 0; t < kScore; ++t) {
-            pa[t][2 * f] = t0[t];
-            pa[t][2 * f + 1] = t1[t];
-          }
-        }
-        if (s == own) {   // rows of v that are not finite must not reach earlier tokens
-          uint32_t bad = 0;
-#pragma unroll
-          for (int n = 0; n < NV; n += 2) {
-            uint32_t vb[4];
-            ldsm_t(vb, column_address(v_base, L::kPitchV, 16 * s, 8 * n, lane));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&vb[e]),
-                                               __floats2bfloat162_rn(0.0f, 0.0f));
-              bad |= *reinterpret_cast<const uint32_t*>(&z);
+            for (int n = 0; n < NV; ++n) {
+              const int c = 8 * n + 2 * (lane & 3);
+              const T* x = dot + t * a.dot.sn + c;
+              if constexpr (ASYNC) {
+                if (c0 + c < p.d) {
+                  const uint32_t xx = *reinterpret_cast<const uint32_t*>(x);
+                  sum[f] = fmaf(o.get(n, 2 * f), low(xx), fmaf(o.get(n, 2 * f + 1), high(xx), sum[f]));
+                }
+              } else {
+                if (c0 + c < p.d) sum[f] = fmaf(o.get(n, 2 * f), to_f(x[0]), sum[f]);
+                if (c0 + c + 1 < p.d) sum[f] = fmaf(o.get(n, 2 * f + 1), to_f(x[1]), sum[f]);
+              }
             }
           }
-          apart = __any_sync(~0u, bad & 0x7FFF7FFFu);
-          if (apart)
-            diagonal_apart<T, DK, ASYNC>(
-                o, pr, reinterpret_cast<const __nv_bfloat16*>(stage + 2 * L::kIn * L::kK) + 16 * s * L::kPitchV, reverse,
-                lane);
+          sum[f] += __shfl_xor_sync(~0u, sum[f], 1);
+          sum[f] += __shfl_xor_sync(~0u, sum[f], 2);
+          if ((lane & 3) == 0 && t < p.N) a.dots[(slice * p.BH + bh) * p.N + t] = sum[f];
         }
       }
-      uint32_t ka[L::kRowTiles][kAdd][4];
+      if constexpr (ASYNC) {
+        char* mine = stage + rows0 * L::kPitchK * 2;
+        __syncwarp();   // every lane has read its rows of q
+        // the columns behind d stay zero (a NaN row would put NaN there)
 #pragma unroll
-      for (int m = 0; m < L::kRowTiles; ++m)
-        add_operand<T, DK, ASYNC>(ka[m], k_base, srow0 + 16 * m, s, w.addw, lane);
+        for (int n = 0; n < NV; ++n)
 #pragma unroll
-      for (int n = 0; n < NV; n += 2) {
-        uint32_t vb[L::kIn][4];
+          for (int f = 0; f < 2; ++f)
+            if (c0 + 8 * n < p.d)
+              *reinterpret_cast<uint32_t*>(mine + (((lane >> 2) + 8 * f) * L::kPitchK + 8 * n + 2 * (lane & 3)) * 2) =
+                  pack(o.get(n, 2 * f), o.get(n, 2 * f + 1));
+        __syncwarp();
+        constexpr int kUnits = L::DV / 8;
+        const int r = lane / kUnits, c = 8 * (lane % kUnits);
+        const int64_t t = t0 + rows0 + r;
+        T* to = out + t * a.out.sn + c;
 #pragma unroll
-        for (int t = 0; t < L::kIn; ++t)
-          ldsm_t(vb[t], column_address(v_base + t * L::kV, L::kPitchV, 16 * s, 8 * n, lane));
-        if (seen && !apart) {
-          mma_terms(o[n], pa, vb, 0);
-          mma_terms(o[n + 1], pa, vb, 1);
+        for (int u = 0; u < 16 * kUnits / 32; ++u) {
+          constexpr int kStep = 32 / kUnits;   // rows a pass
+          if (t + u * kStep < p.N && c0 + c < p.d)
+            *reinterpret_cast<uint4*>(to + u * kStep * a.out.sn) =
+                *reinterpret_cast<const uint4*>(mine + ((r + u * kStep) * L::kPitchK + c) * 2);
         }
-        if (DK >= 64 || 8 * n == scol0) {
+      } else {
 #pragma unroll
-          for (int m = 0; m < L::kRowTiles; ++m) {
-            mma_terms(S[m][DK >= 64 ? n : 0], ka[m], vb, 0);
-            mma_terms(S[m][DK >= 64 ? n + 1 : 1], ka[m], vb, 1);
-          }
-        }
-      }
-    }
-    __syncthreads();   // every warp has read the state's planes
-    if (i + 1 < count) publish();
-
-    // rows out: rounded once, through this warp's own rows of q
-    const int64_t t0 = chunk_of(i) * kChunk;
-    if (a.dots) {
-      const T* dot = static_cast<const T*>(a.dot.data) + b * a.dot.sb + h * a.dot.sh + c0;
-      float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const int64_t t = t0 + row + 8 * f;
-        if (t < p.N) {
+        for (int f = 0; f < 2; ++f) {
+          const int64_t t = t0 + row + 8 * f;
+          if (t >= p.N) continue;
 #pragma unroll
           for (int n = 0; n < NV; ++n) {
             const int c = 8 * n + 2 * (lane & 3);
-            const T* x = dot + t * a.dot.sn + c;
-            if (c0 + c < p.d) sum[f] = fmaf(o[n][2 * f], to_f(x[0]), sum[f]);
-            if (c0 + c + 1 < p.d) sum[f] = fmaf(o[n][2 * f + 1], to_f(x[1]), sum[f]);
+            if (c0 + c < p.d) from_f(out + t * a.out.sn + c, o.get(n, 2 * f));
+            if (c0 + c + 1 < p.d) from_f(out + t * a.out.sn + c + 1, o.get(n, 2 * f + 1));
           }
         }
-        sum[f] += __shfl_xor_sync(~0u, sum[f], 1);
-        sum[f] += __shfl_xor_sync(~0u, sum[f], 2);
-        if ((lane & 3) == 0 && t < p.N) a.dots[(slice * p.BH + bh) * p.N + t] = sum[f];
       }
     }
-    T* out = static_cast<T*>(a.out.data) + b * a.out.sb + h * a.out.sh + c0;
-    if constexpr (ASYNC) {
-      char* mine = stage + rows0 * L::kPitchK * 2;
-      // the columns behind d stay zero (a NaN row would put NaN there)
-#pragma unroll
-      for (int n = 0; n < NV; ++n)
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-          if (c0 + 8 * n < p.d) *reinterpret_cast<uint32_t*>(mine + (((lane >> 2) + 8 * f) * L::kPitchK + 8 * n + 2 * (lane & 3)) * 2) =
-              pack(o[n][2 * f], o[n][2 * f + 1]);
-      __syncwarp();
-      constexpr int kUnits = L::DV / 8;
-#pragma unroll
-      for (int u = lane; u < 16 * kUnits; u += 32) {
-        const int r = u / kUnits, c = 8 * (u % kUnits);
-        const int64_t t = t0 + rows0 + r;
-        if (t < p.N && c0 + c < p.d)
-          *reinterpret_cast<uint4*>(out + t * a.out.sn + c) =
-              *reinterpret_cast<const uint4*>(mine + (r * L::kPitchK + c) * 2);
-      }
-      __syncwarp();
-    } else {
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const int64_t t = t0 + row + 8 * f;
-        if (t >= p.N) continue;
-#pragma unroll
-        for (int n = 0; n < NV; ++n) {
-          const int c = 8 * n + 2 * (lane & 3);
-          if (c0 + c < p.d) from_f(out + t * a.out.sn + c, o[n][2 * f]);
-          if (c0 + c + 1 < p.d) from_f(out + t * a.out.sn + c + 1, o[n][2 * f + 1]);
-        }
-      }
+    const uint32_t k_base = ptx::smem_u32(stage) + L::kIn * L::kK;
+    add_chunk<T, DK, ASYNC>(S, k_base, k_base + L::kIn * L::kK, w, warp, lane);
+    if (i + 1 < count) {
+      __syncthreads();   // every warp has read the state's planes
+      publish();
     }
   }
   if (a.last && span == (reverse ? 0 : p.spans - 1)) {
-    float* out = a.last + bh * p.d * p.d;
+    float* last = a.last + bh * p.d * p.d;
 #pragma unroll
     for (int m = 0; m < L::kRowTiles; ++m)
 #pragma unroll
@@ -766,7 +884,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = at.row + 16 * m + (e >> 1) * 8, c = c0 + at.col + 8 * n + (e & 1);
-          if (r < p.d && c < p.d) out[r * p.d + c] = S[m][n][e];
+          if (r < p.d && c < p.d) last[r * p.d + c] = S[m][n][e];
         }
   }
 }
