@@ -87,6 +87,13 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -137,15 +144,6 @@ template <int NT, bool APART>
 struct Accumulators {
   float main[NT][4];
   float small[APART ? NT : 1][4];
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        main[n][e] = 0.0f;
-        if (APART) small[APART ? n : 0][e] = 0.0f;
-      }
-  }
   __device__ __forceinline__ float get(int n, int e) const {
     return APART ? main[n][e] + small[APART ? n : 0][e] : main[n][e];
   }
@@ -153,9 +151,10 @@ struct Accumulators {
 
 // acc[n0 .. n0 + 2 P) += A B over the terms of both whose product is not below the last
 // term's size; b[t][p] holds two column tiles.  Independent accumulators follow one another.
+// first: nothing is there yet.
 template <int NA, int NB, int P, int NT, bool APART>
 __device__ __forceinline__ void mma_terms(Accumulators<NT, APART>& acc, int n0, const uint32_t (&a)[NA][4],
-                                          const uint32_t (&b)[NB][P][4]) {
+                                          const uint32_t (&b)[NB][P][4], bool first = false) {
   constexpr int kMost = NA > NB ? NA : NB;
 #pragma unroll
   for (int i = NA - 1; i >= 0; --i)
@@ -167,7 +166,13 @@ __device__ __forceinline__ void mma_terms(Accumulators<NT, APART>& acc, int n0, 
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
           const int n = n0 + 2 * p + f;
-          mma(APART && i + j > 0 ? acc.small[APART ? n : 0] : acc.main[n], a[i], b[j][p][2 * f], b[j][p][2 * f + 1]);
+          float(&c)[4] = APART && i + j > 0 ? acc.small[APART ? n : 0] : acc.main[n];
+          // the first pair of terms that goes to this accumulator
+          const bool opens = APART ? (i + j == 0 || (i == NA - 1 && j == kMost - NA)) : (i == NA - 1 && j == kMost - NA);
+          if (first && opens)
+            mma_first(c, a[i], b[j][p][2 * f], b[j][p][2 * f + 1]);
+          else
+            mma(c, a[i], b[j][p][2 * f], b[j][p][2 * f + 1]);
         }
     }
 }
@@ -276,22 +281,28 @@ __device__ __forceinline__ Sum chunk_gates(float2 g, Gates& out, const Scan& a, 
   return all;
 }
 
+// Byte offset of a 16-byte unit of a row-major bf16 tile W columns wide.  Units change
+// places with the row's number, so that eight rows read at one column (ldmatrix) or
+// written at one (accumulators) meet all banks.
+template <int W>
+__device__ __forceinline__ int unit_at(int row, int unit) {
+  return row * (2 * W) + ((unit ^ (W == 32 ? (row >> 1) & 3 : row & 7)) << 4);
+}
+
 template <typename T, int DK, bool ASYNC>
 struct Tile {
   static constexpr int DV = DK < 64 ? DK : 64;     // columns of the state a CTA holds
   static constexpr int kIn = Terms<T>::kIn;
   static constexpr int kStages = ASYNC ? 2 : 1;
-  // rows of 16 bytes more than the channels: eight rows at one column meet all banks
-  static constexpr int kPitchK = DK + 8, kPitchV = DV + 8;   // bf16 elements
-  static constexpr int kK = kChunk * kPitchK * 2, kV = kChunk * kPitchV * 2;   // bytes of a plane
-  static constexpr int kS = DK * kPitchV * 2;
+  static constexpr int kK = kChunk * DK * 2, kV = kChunk * DV * 2;   // bytes of a plane
+  static constexpr int kS = DK * DV * 2;
   // warps over the state's rows (16 each) and, for 32 rows, two halves of its columns
   static constexpr int kRowTiles = DK >= 64 ? DK / 64 : 1;
   static constexpr int kColTiles = DK >= 64 ? DV / 8 : DV / 16;   // of eight columns
 };
 
 // Copies chunks of one operand (columns [c0, c0 + W)) into kIn planes.
-template <typename T, int W, int PITCH, bool ASYNC>
+template <typename T, int W, bool ASYNC>
 struct RowLoader {
   const T* src;
   int64_t step;      // elements: ASYNC from pass to pass, else from token to token
@@ -313,21 +324,20 @@ struct RowLoader {
       constexpr int kUnits = W / 8, kRows = 128 / kUnits, kSteps = kChunk / kRows;
       const int r = threadIdx.x / kUnits, u = threadIdx.x % kUnits;
       if (8 * u >= width) return;   // the columns behind d were zeroed at the start
-      uint32_t at = ptx::smem_u32(dst) + (r * PITCH + 8 * u) * 2;
+      static_assert(kRows % 8 == 0, "a pass keeps the units' places");
+      const uint32_t at = ptx::smem_u32(dst) + unit_at<W>(r, u);
       const T* x = src + chunk * (kSteps * step);
       if (rows == kChunk) {
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i, x += step) cp_async_16(at + i * kRows * PITCH * 2, x, 16);
+        for (int i = 0; i < kSteps; ++i, x += step) cp_async_16(at + i * kRows * W * 2, x, 16);
       } else {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
           const bool in = r + i * kRows < rows;
-          cp_async_16(at + i * kRows * PITCH * 2, in ? x + i * step : static_cast<const T*>(src), in ? 16 : 0);
+          cp_async_16(at + i * kRows * W * 2, in ? x + i * step : static_cast<const T*>(src), in ? 16 : 0);
         }
       }
     } else {
-      constexpr int kPlane = kChunk * PITCH;
-      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(dst);
       for (int i = threadIdx.x; i < kChunk * W / 2; i += 128) {
         const int r = i / (W / 2), c = 2 * (i % (W / 2));
         const T* x = src + (chunk * kChunk + r) * step + c;
@@ -335,7 +345,7 @@ struct RowLoader {
 #pragma unroll
         for (int n = 0; n < Terms<T>::kIn; ++n) {
           const uint32_t p = pack(a, e);
-          *reinterpret_cast<uint32_t*>(out + n * kPlane + r * PITCH + c) = p;
+          *reinterpret_cast<uint32_t*>(dst + n * kChunk * W * 2 + unit_at<W>(r, c >> 3) + (c & 7) * 2) = p;
           // an infinity is its first term alone
           a = fabsf(low(p)) < __int_as_float(0x7F800000) ? a - low(p) : 0.0f;
           e = fabsf(high(p)) < __int_as_float(0x7F800000) ? e - high(p) : 0.0f;
@@ -369,7 +379,7 @@ __device__ __forceinline__ void add_operand(uint32_t (&a)[kAdd][4], uint32_t k_b
 #pragma unroll
   for (int n = 0; n < L::kIn; ++n) {
     uint32_t k[4];
-    ldsm_t(k, k_base + n * L::kK + (token * L::kPitchK + r) * 2);
+    ldsm_t(k, k_base + n * L::kK + unit_at<DK>(token, r >> 3));
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       x[e][0] = n == 0 ? low(k[e]) : x[e][0] + low(k[e]);
@@ -388,8 +398,9 @@ __device__ __forceinline__ void add_operand(uint32_t (&a)[kAdd][4], uint32_t k_b
 
 // Fragments of 16 tokens by 16 columns of a row-major plane [token][column]
 // (v, or the state with r for the token): two column tiles of B operands.
-__device__ __forceinline__ uint32_t column_address(uint32_t base, int pitch, int token0, int col0, int lane) {
-  return base + ((token0 + (lane & 7) + ((lane >> 3) & 1) * 8) * pitch + col0 + (lane >> 4) * 8) * 2;
+template <int W>
+__device__ __forceinline__ uint32_t column_address(uint32_t base, int token0, int col0, int lane) {
+  return base + unit_at<W>(token0 + (lane & 7) + ((lane >> 3) & 1) * 8, (col0 >> 3) + (lane >> 4));
 }
 
 // S <- e^B S + sum over a chunk's tokens of (addw k)^T v.  The chunk's sum is formed apart
@@ -405,7 +416,6 @@ __device__ __forceinline__ void add_chunk(float (&S)[Tile<T, DK, ASYNC>::kRowTil
 #pragma unroll
   for (int m = 0; m < L::kRowTiles; ++m) {
     Accumulators<L::kColTiles, (L::kIn > 1)> sum;
-    sum.clear();
 #pragma unroll
     for (int s = 0; s < kChunk / 16; ++s) {
       uint32_t ka[kAdd][4], vb[L::kIn][P][4];
@@ -413,9 +423,9 @@ __device__ __forceinline__ void add_chunk(float (&S)[Tile<T, DK, ASYNC>::kRowTil
       for (int t = 0; t < L::kIn; ++t)
 #pragma unroll
         for (int n = 0; n < P; ++n)
-          ldsm_t(vb[t][n], column_address(v_base + t * L::kV, L::kPitchV, 16 * s, col0 + 16 * n, lane));
+          ldsm_t(vb[t][n], column_address<L::DV>(v_base + t * L::kV, 16 * s, col0 + 16 * n, lane));
       add_operand<T, DK, ASYNC>(ka, k_base, row0 + 16 * m, s, w.addw, lane);
-      mma_terms(sum, 0, ka, vb);
+      mma_terms(sum, 0, ka, vb, s == 0);
     }
 #pragma unroll
     for (int n = 0; n < L::kColTiles; ++n)
@@ -449,8 +459,8 @@ __global__ void __launch_bounds__(128) gated_span_state(const __grid_constant__ 
       reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
   }
-  const RowLoader<T, DK, L::kPitchK, ASYNC> rows_k(a.k, b, h, 0, p.d);
-  const RowLoader<T, L::DV, L::kPitchV, ASYNC> rows_v(a.v, b, h, c0, p.d);
+  const RowLoader<T, DK, ASYNC> rows_k(a.k, b, h, 0, p.d);
+  const RowLoader<T, L::DV, ASYNC> rows_v(a.v, b, h, c0, p.d);
   auto chunk_of = [&](int i) { return first + (reverse ? count - 1 - i : i); };
   auto load = [&](int i) {
     char* st = smem + (i % L::kStages) * kStage;
@@ -551,31 +561,28 @@ __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::DV /
   const uint32_t q_base = ptx::smem_u32(stage), k_base = q_base + L::kIn * L::kK, v_base = k_base + L::kIn * L::kK;
   const int rows0 = 16 * own, row = rows0 + (lane >> 2);
   Accumulators<2 * kSteps, kApart> sc;
-  sc.clear();
-  o.clear();
 #pragma unroll
   for (int ks = 0; ks < DK / 16; ++ks) {
     uint32_t qa[L::kIn][4];
 #pragma unroll
     for (int t = 0; t < L::kIn; ++t)
-      ldsm(qa[t], q_base + t * L::kK +
-                      ((rows0 + (lane & 7) + ((lane >> 3) & 1) * 8) * L::kPitchK + 16 * ks + (lane >> 4) * 8) * 2);
+      ldsm(qa[t], q_base + t * L::kK + unit_at<DK>(rows0 + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * ks + (lane >> 4)));
     uint32_t sb[kState][P][4];
 #pragma unroll
     for (int t = 0; t < kState; ++t)
 #pragma unroll
       for (int n = 0; n < P; ++n)
-        ldsm_t(sb[t][n], column_address(s_base + t * L::kS, L::kPitchV, 16 * ks, 16 * n, lane));
-    mma_terms(o, 0, qa, sb);
+        ldsm_t(sb[t][n], column_address<L::DV>(s_base + t * L::kS, 16 * ks, 16 * n, lane));
+    mma_terms(o, 0, qa, sb, ks == 0);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       if (REVERSE ? s < own : s > own) continue;
       uint32_t kb[L::kIn][1][4];
 #pragma unroll
       for (int t = 0; t < L::kIn; ++t)
-        ldsm(kb[t][0], k_base + t * L::kK +
-                           ((16 * s + (lane & 7) + (lane >> 4) * 8) * L::kPitchK + 16 * ks + ((lane >> 3) & 1) * 8) * 2);
-      mma_terms(sc, 2 * s, qa, kb);
+        ldsm(kb[t][0],
+             k_base + t * L::kK + unit_at<DK>(16 * s + (lane & 7) + (lane >> 4) * 8, 2 * ks + ((lane >> 3) & 1)));
+      mma_terms(sc, 2 * s, qa, kb, ks == 0);
     }
   }
   const float enter = w.enter[own];
@@ -594,7 +601,7 @@ __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::DV /
     for (int t = 0; t < L::kIn; ++t)
 #pragma unroll
       for (int n = 0; n < P; ++n)
-        ldsm_t(vb[t][n], column_address(v_base + t * L::kV, L::kPitchV, 16 * s, 16 * n, lane));
+        ldsm_t(vb[t][n], column_address<L::DV>(v_base + t * L::kV, 16 * s, 16 * n, lane));
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
       const float2 c = *reinterpret_cast<const float2*>(w.col[own] + 16 * s + 8 * f + 2 * (lane & 3));
@@ -648,7 +655,7 @@ __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::DV /
   for (int t = 0; t < L::kIn; ++t)
 #pragma unroll
     for (int n = 0; n < P; ++n)
-      ldsm_t(vb[t][n], column_address(v_base + t * L::kV, L::kPitchV, rows0, 16 * n, lane));
+      ldsm_t(vb[t][n], column_address<L::DV>(v_base + t * L::kV, rows0, 16 * n, lane));
   // A row of v that holds an infinity or NaN must not reach the rows that do not see
   // it (0 times infinity): such a block goes without the tensor core.
   uint32_t bad = 0;
@@ -675,8 +682,7 @@ __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::DV /
     }
     mma_terms(o, 0, pa, vb);
   } else {
-    const __nv_bfloat16* v =
-        reinterpret_cast<const __nv_bfloat16*>(stage + 2 * L::kIn * L::kK) + rows0 * L::kPitchV + 2 * (lane & 3);
+    const char* v = stage + 2 * L::kIn * L::kK;
 #pragma unroll 1
     for (int j = 0; j < 16; ++j) {
       const int src = (lane & ~3) | ((j & 7) >> 1);
@@ -692,7 +698,9 @@ __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::DV /
         for (int e = 0; e < 2; ++e) {
           float y = 0.0f;
 #pragma unroll
-          for (int t = 0; t < L::kIn; ++t) y += __bfloat162float(v[t * (L::kV / 2) + j * L::kPitchV + 8 * n + e]);
+          for (int t = 0; t < L::kIn; ++t)
+            y += __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(v + t * L::kV + unit_at<L::DV>(rows0 + j, n) +
+                                                                          2 * (2 * (lane & 3) + e)));
           if (sees_up) o.main[n][e] = fmaf(up, y, o.main[n][e]);
           if (sees_dn) o.main[n][2 + e] = fmaf(dn, y, o.main[n][2 + e]);
         }
@@ -730,8 +738,8 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
       reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
   }
-  const RowLoader<T, DK, L::kPitchK, ASYNC> rows_q(a.q, b, h, 0, p.d), rows_k(a.k, b, h, 0, p.d);
-  const RowLoader<T, L::DV, L::kPitchV, ASYNC> rows_v(a.v, b, h, c0, p.d);
+  const RowLoader<T, DK, ASYNC> rows_q(a.q, b, h, 0, p.d), rows_k(a.k, b, h, 0, p.d);
+  const RowLoader<T, L::DV, ASYNC> rows_v(a.v, b, h, c0, p.d);
   auto chunk_of = [&](int i) { return first + (reverse ? count - 1 - i : i); };
   auto load = [&](int i) {
     char* st = smem + (i % L::kStages) * M::kStage;
@@ -768,8 +776,8 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
           split<kState>(S[m][n][2 * e], S[m][n][2 * e + 1], t);
 #pragma unroll
           for (int k = 0; k < kState; ++k)
-            *reinterpret_cast<uint32_t*>(planes + k * L::kS +
-                                         ((at.row + 16 * m + 8 * e) * L::kPitchV + at.col + 8 * n) * 2) = t[k];
+            *reinterpret_cast<uint32_t*>(planes + k * L::kS + unit_at<L::DV>(at.row + 16 * m + 8 * e, (at.col >> 3) + n) +
+                                         4 * (lane & 3)) = t[k];
         }
   };
   publish();
@@ -832,7 +840,6 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
         }
       }
       if constexpr (ASYNC) {
-        char* mine = stage + rows0 * L::kPitchK * 2;
         __syncwarp();   // every lane has read its rows of q
         // the columns behind d stay zero (a NaN row would put NaN there)
 #pragma unroll
@@ -840,8 +847,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
 #pragma unroll
           for (int f = 0; f < 2; ++f)
             if (c0 + 8 * n < p.d)
-              *reinterpret_cast<uint32_t*>(mine + (((lane >> 2) + 8 * f) * L::kPitchK + 8 * n + 2 * (lane & 3)) * 2) =
-                  pack(o.get(n, 2 * f), o.get(n, 2 * f + 1));
+              *reinterpret_cast<uint32_t*>(stage + unit_at<DK>(row + 8 * f, n) + 4 * (lane & 3)) = pack(o.get(n, 2 * f), o.get(n, 2 * f + 1));
         __syncwarp();
         constexpr int kUnits = L::DV / 8;
         const int r = lane / kUnits, c = 8 * (lane % kUnits);
@@ -852,7 +858,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
           constexpr int kStep = 32 / kUnits;   // rows a pass
           if (t + u * kStep < p.N && c0 + c < p.d)
             *reinterpret_cast<uint4*>(to + u * kStep * a.out.sn) =
-                *reinterpret_cast<const uint4*>(mine + ((r + u * kStep) * L::kPitchK + c) * 2);
+                *reinterpret_cast<const uint4*>(stage + unit_at<DK>(rows0 + r + u * kStep, c >> 3));
         }
       } else {
 #pragma unroll
