@@ -80,7 +80,6 @@ def test_workspace_refusals(L):
     if need:
         assert forward(L, q, k, v, g, out=out, ws=FAKE + 9 * STEP, n=need - 1) == WORKSPACE
     assert L.mhla_gated_backward_workspace_size(*ref(q), ctypes.byref(n)) == OK and n.value % 256 == 0
-    assert n.value >= need
     assert L.mhla_gated_workspace_size(*ref(q), None) == INVALID
     assert L.mhla_gated_workspace_size(None, ctypes.byref(n)) == INVALID
     assert L.mhla_qk_norm_backward_workspace_size(*ref(q), ctypes.byref(n)) == OK and n.value % 256 == 0

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -147,7 +148,7 @@ def lib():
                                       ctypes.c_int64, P(ModuleParams), ctypes.c_void_p, P(Shape3), P(Shape3),
                                       P(Phi), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     L.mhla_module_forward.restype = ctypes.c_int
-    V, T = ctypes.c_void_p, P(Tensor)
+    V = T = ctypes.c_void_p   # tensors as packed bytes or by reference
     L.mhla_gated_workspace_size.argtypes = [T, P(ctypes.c_size_t)]
     L.mhla_gated_backward_workspace_size.argtypes = [T, P(ctypes.c_size_t)]
     L.mhla_gated_forward.argtypes = [T, T, T, T, ctypes.c_float, V, T, V, V, ctypes.c_size_t, V]
@@ -476,28 +477,36 @@ def module_forward(x, params, W, grid, block, heads, phi="relu_eps", eps=1e-6, l
 # --------------------------------------------------- gated recurrence, query/key norm
 
 
+_PACK_TENSOR = struct.Struct("Pii7q").pack   # mhla_tensor_t
+_CODES = {}
+
+
 def _dtype_code(x):
     import torch
-    if x.dtype == torch.bfloat16:
-        return 0
-    if x.dtype == torch.float32:
-        return 1
-    raise ValueError(f"unsupported dtype {x.dtype}")
+    if not _CODES:
+        _CODES.update({torch.bfloat16: 0, torch.float32: 1})
+    code = _CODES.get(x.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    return code
 
 
+# These two pack the C struct directly: serving makes such a call per token, and
+# filling a ctypes structure field by field costs more than the launch.
 def _heads(x):
-    """mhla_tensor_t of a [B, N, H, d] tensor, in one call of the constructor (serving calls this per token)."""
+    """mhla_tensor_t of a [B, N, H, d] tensor."""
     B, N, H, d = x.shape
     sb, sn, sh, sd = x.stride()
     if d > 1 and sd != 1:
         raise ValueError("the d dimension must be contiguous")
-    return Tensor(x.data_ptr() or None, _dtype_code(x), 0, B, N, H, d, sb, sn, sh)
+    return _PACK_TENSOR(x.data_ptr(), _dtype_code(x), 0, B, N, H, d, sb, sn, sh)
 
 
 def _gates(x):
     """mhla_tensor_t of a [B, N, H] tensor of one value per token and head."""
     B, N, H = x.shape
-    return Tensor(x.data_ptr() or None, _dtype_code(x), 0, B, N, H, 1, *x.stride())
+    sb, sn, sh = x.stride()
+    return _PACK_TENSOR(x.data_ptr(), _dtype_code(x), 0, B, N, H, 1, sb, sn, sh)
 
 
 def _float_array(name, x, shape, like):
@@ -512,40 +521,42 @@ def _float_array(name, x, shape, like):
     return x.data_ptr()
 
 
-def _same_device(like, **tensors):
-    for name, x in tensors.items():
-        if x.device != like.device:
-            raise ValueError(f"{name} is on {x.device}, not on {like.device}")
-
-
-def _on_device(fn, x, stream, workspace, need):
-    """fn(workspace address, bytes, stream) with x's device current.  Without a workspace of
-    the caller's, need() bytes come from torch's allocator on that stream."""
-    import torch
-    dev = x.device
+def _same_device(like, *tensors):
+    dev = like.device
+    for x in tensors:
+        if x.device != dev:
+            raise ValueError(f"a tensor is on {x.device}, not on {dev}")
     if dev.type != "cuda":
         raise ValueError("expected CUDA tensors")
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
-            return _on_device(fn, x, stream, workspace, need)
+
+
+def _launch(call, x, stream, workspace=None, need=None):
+    """call(workspace address, bytes, stream) with x's device current; need() tells the
+    bytes, taken from torch's allocator on that stream when the caller brings none."""
+    import torch
+    index = x.device.index
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _launch(call, x, stream, workspace, need)
+    current = torch._C._cuda_getCurrentRawStream(index)
     if stream is None:
-        s = torch.cuda.current_stream(dev).cuda_stream
+        s = current
     else:
         s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if need is None:
-        return fn(None, 0, s or None)
+        return call(None, 0, s)
     if workspace is not None:
-        return fn(workspace.data_ptr(), workspace.numel() * workspace.element_size(), s or None)
+        return call(workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
     n = need()
-    if n == 0 or s != torch.cuda.current_stream(dev).cuda_stream:
-        return fn(None, 0, s or None)   # another stream: the library's stream-ordered allocation
-    scratch = torch.empty(n, dtype=torch.uint8, device=dev)
-    return fn(scratch.data_ptr(), n, s or None)
+    if n == 0 or s != current:
+        return call(None, 0, s)   # another stream: the library's stream-ordered allocation
+    scratch = torch.empty(n, dtype=torch.uint8, device=x.device)
+    return call(scratch.data_ptr(), n, s)
 
 
 def _size(fn, what, desc):
     n = ctypes.c_size_t(0)
-    _check(fn(ctypes.byref(desc), ctypes.byref(n)), what)
+    _check(fn(desc, ctypes.byref(n)), what)
     return n.value
 
 
@@ -569,12 +580,12 @@ def gated_forward(q, k, v, g, scale=1.0, state=None, out=None, state_out=None, w
     out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
     if state_out is None:
         state_out = torch.empty(B, H, d, d, dtype=torch.float32, device=q.device)
-    _same_device(q, k=k, v=v, g=g, out=out)
+    _same_device(q, k, v, g, out)
     s_in = _float_array("state", state, (B, H, d, d), q)
     s_out = _float_array("state_out", state_out, (B, H, d, d), q)
     dq = _heads(q)
     L = lib()
-    st = _on_device(
+    st = _launch(
         lambda ws, n, s: L.mhla_gated_forward(dq, _heads(k), _heads(v), _gates(g), scale, s_in, _heads(out), s_out,
                                               ws, n, s),
         q, stream, workspace, lambda: _size(L.mhla_gated_workspace_size, "mhla_gated_workspace_size", dq))
@@ -593,13 +604,13 @@ def gated_backward(q, k, v, g, dout, scale=1.0, state=None, dstate_out=None, dq=
     dg = torch.empty(B, N, H, dtype=q.dtype, device=q.device) if dg is None else dg
     if dstate is None:
         dstate = torch.empty(B, H, d, d, dtype=torch.float32, device=q.device)
-    _same_device(q, k=k, v=v, g=g, dout=dout, dq=dq, dk=dk, dv=dv, dg=dg)
+    _same_device(q, k, v, g, dout, dq, dk, dv, dg)
     s_in = _float_array("state", state, (B, H, d, d), q)
     ds_out = _float_array("dstate_out", dstate_out, (B, H, d, d), q)
     ds_in = _float_array("dstate", dstate, (B, H, d, d), q)
     desc = _heads(q)
     L = lib()
-    st = _on_device(
+    st = _launch(
         lambda ws, n, s: L.mhla_gated_backward(desc, _heads(k), _heads(v), _gates(g), _heads(dout), scale, s_in, ds_out,
                                                _heads(dq), _heads(dk), _heads(dv), _gates(dg), ds_in, ws, n, s),
         q, stream, workspace,
@@ -614,11 +625,11 @@ def gated_step(q, k, v, g, state, scale=1.0, out=None, stream=None):
     import torch
     B, N, H, d = q.shape
     out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
-    _same_device(q, k=k, v=v, g=g, out=out)
+    _same_device(q, k, v, g, out)
     s = _float_array("state", state, (B, H, d, d), q)
-    st = _on_device(
+    st = _launch(
         lambda ws, n, sp: lib().mhla_gated_step(_heads(q), _heads(k), _heads(v), _gates(g), scale, s, _heads(out), sp),
-        q, stream, None, None)
+        q, stream)
     _check(st, "mhla_gated_step")
     return out
 
@@ -655,7 +666,7 @@ def _rotation(x, table, positions, layout):
         if positions.dtype != torch.int32 or tuple(positions.shape) != tuple(x.shape[:2]) \
                 or not positions.is_contiguous():
             raise ValueError(f"positions must be a contiguous int32 tensor of shape {list(x.shape[:2])}")
-        _same_device(x, positions=positions)
+        _same_device(x, positions)
         pos = positions.data_ptr()
     return Rotation(ptr or None, pos, table.shape[0], table.shape[1], ROTATION_LAYOUTS[layout])
 
@@ -668,13 +679,13 @@ def qk_norm(q, k, q_weight=None, k_weight=None, eps=1e-6, table=None, positions=
     import torch
     q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
     k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-    _same_device(q, k=k, q_out=q_out, k_out=k_out)
+    _same_device(q, k, q_out, k_out)
     d = q.shape[3]
     wq, wk = _float_array("q_weight", q_weight, (d,), q), _float_array("k_weight", k_weight, (d,), q)
     rot = _rotation(q, table, positions, layout)
-    st = _on_device(
+    st = _launch(
         lambda ws, n, s: lib().mhla_qk_norm(_heads(q), _heads(k), wq, wk, eps, rot, _heads(q_out), _heads(k_out), s),
-        q, stream, None, None)
+        q, stream)
     _check(st, "mhla_qk_norm")
     return q_out, k_out
 
@@ -693,13 +704,13 @@ def qk_norm_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, eps=1e-
     dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
     new = lambda given: torch.empty(d, dtype=torch.float32, device=q.device) if given is None else given
     dq_weight, dk_weight = new(dq_weight), new(dk_weight)
-    _same_device(q, k=k, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk)
+    _same_device(q, k, dq_out, dk_out, dq, dk)
     wq, wk = _float_array("q_weight", q_weight, (d,), q), _float_array("k_weight", k_weight, (d,), q)
     gq, gk = _float_array("dq_weight", dq_weight, (d,), q), _float_array("dk_weight", dk_weight, (d,), q)
     rot = _rotation(q, table, positions, layout)
     desc = _heads(q)
     L = lib()
-    st = _on_device(
+    st = _launch(
         lambda ws, n, s: L.mhla_qk_norm_backward(desc, _heads(k), wq, wk, eps, rot, _heads(dq_out), _heads(dk_out),
                                                  _heads(dq), _heads(dk), gq, gk, ws, n, s),
         q, stream, workspace,

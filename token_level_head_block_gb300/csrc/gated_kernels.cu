@@ -895,7 +895,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
   }
 }
 
-// dg over one span of one (b, h), 256 tokens at a time from its end: <S, dS>
+// dg over one span of one (b, h), 2048 tokens at a time from its end: <S, dS>
 // there, then the running sum of q.dq - k.dk.  The sums restart at every span,
 // so their rounding does not grow with the sequence.
 struct GateGrad {
@@ -934,21 +934,28 @@ __global__ void __launch_bounds__(256) gated_gate_grad(const __grid_constant__ G
   __syncthreads();
   const int64_t t0 = span * p.span_tokens, t1 = min(p.N, t0 + p.span_tokens);
   float carry = head;
-  for (int64_t end = t1; end > t0; end -= 256) {
-    const int64_t t = end - 1 - threadIdx.x;   // thread 0 takes the last token
-    float x = 0.0f;
-    if (t >= t0)
-      for (int k = 0; k < p.slices; ++k) {
-        const int64_t i = (k * p.BH + bh) * p.N + t;
-        x += p.qdots[i] - p.kdots[i];
-      }
+  constexpr int kEach = 8;   // tokens a thread, so that a long span takes few rounds
+  for (int64_t end = t1; end > t0; end -= 256 * kEach) {
+    const int64_t t = end - 1 - kEach * static_cast<int64_t>(threadIdx.x);   // thread 0 takes the last ones
+    float x[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) x[e] = 0.0f;
+    for (int k = 0; k < p.slices; ++k) {
+      const int64_t i = (k * p.BH + bh) * p.N + t;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e)
+        if (t - e >= t0) x[e] += p.qdots[i - e] - p.kdots[i - e];
+    }
+#pragma unroll
+    for (int e = 1; e < kEach; ++e) x[e] += x[e - 1];
+    float sum = x[kEach - 1];
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
-      const float y = __shfl_up_sync(~0u, x, k);
-      if (lane >= k) x += y;
+      const float y = __shfl_up_sync(~0u, sum, k);
+      if (lane >= k) sum += y;
     }
-    __syncthreads();   // the last block's totals are read
-    if (lane == 31) part[warp] = x;
+    __syncthreads();   // the last round's totals are read
+    if (lane == 31) part[warp] = sum;
     __syncthreads();
     float before = carry, all = carry;
 #pragma unroll
@@ -956,7 +963,13 @@ __global__ void __launch_bounds__(256) gated_gate_grad(const __grid_constant__ G
       if (i < warp) before += part[i];
       all += part[i];
     }
-    if (t >= t0) from_f(static_cast<T*>(p.dg.data) + b * p.dg.sb + t * p.dg.sn + h * p.dg.sh, before + x);
+    float lower = __shfl_up_sync(~0u, sum, 1);   // of the threads in front of this one
+    if (lane == 0) lower = 0.0f;
+    before += lower;
+    T* dg = static_cast<T*>(p.dg.data) + b * p.dg.sb + h * p.dg.sh;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (t - e >= t0) from_f(dg + (t - e) * p.dg.sn, before + x[e]);
     carry = all;
   }
 }
@@ -1185,48 +1198,89 @@ int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* w
 
 // ------------------------------------------------------------------ one token
 
-// A CTA takes one (b, h) and 32 columns of its state: thread (row group y, column
-// x) carries every 8th row of a column.
-template <typename T>
+// A CTA takes one (b, h).  The state is read and written once and nothing else is of
+// size, so the loads count: VEC 4 keeps four 16-byte loads of a thread in flight (d = 64),
+// row groups meeting in shared memory for o.  VEC 1 takes any d and alignment.
+template <typename T, int VEC>
 __global__ void __launch_bounds__(256) gated_step(const GatedProblem p, float* state, const Operand out) {
-  __shared__ float sq[128], sk[128], part[8][33];
-  const int64_t slices = (p.d + 31) / 32;
-  const int64_t bh = blockIdx.x / slices, b = bh / p.H, h = bh % p.H;
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = static_cast<int>(blockIdx.x % slices) * 32 + x;
+  constexpr int kBatch = 4;
+  __shared__ float sq[128], sk[128];
+  __shared__ float part[256 * VEC];
+  const int64_t bh = blockIdx.x, b = bh / p.H, h = bh % p.H;
   auto at = [&](const Operand& o) { return static_cast<T*>(o.data) + b * o.sb + h * o.sh; };
-  if (threadIdx.x < p.d) {
+  const int d = p.d, units = d / VEC, groups = 256 / units;   // threads a row, rows at once
+  const int x = threadIdx.x % units, y = threadIdx.x / units;
+  float* S = state + bh * d * d + x * VEC;
+  float s[kBatch][VEC];
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = r0 + i * groups;
+      if (r >= d) continue;
+      if constexpr (VEC == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(S + r * d);
+        s[i][0] = f.x; s[i][1] = f.y; s[i][2] = f.z; s[i][3] = f.w;
+      } else {
+        s[i][0] = S[r * d];
+      }
+    }
+  };
+  if (y < groups) load(y);
+  if (threadIdx.x < d) {
     sq[threadIdx.x] = to_f(at(p.q)[threadIdx.x]);
     sk[threadIdx.x] = to_f(at(p.k)[threadIdx.x]);
   }
   const float g = to_f(*at(p.g));
   const float decay = expf(g < kLowestGate ? kLowestGate : g);
-  const float v = c < p.d ? to_f(at(p.v)[c]) : 0.0f;
+  float v[VEC], o[VEC] = {};
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) v[e] = to_f(at(p.v)[x * VEC + e]);
   __syncthreads();
-  float o = 0.0f;
-  if (c < p.d) {
-    float* S = state + bh * p.d * p.d + c;
-    for (int r = y; r < p.d; r += 8) {
-      const float n = fmaf(sk[r], v, decay * S[r * p.d]);
-      S[r * p.d] = n;
-      o = fmaf(sq[r], n, o);
+  if (y < groups)
+    for (int r0 = y; r0 < d; r0 += kBatch * groups) {
+      if (r0 != y) load(r0);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + i * groups;
+        if (r >= d) continue;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          s[i][e] = fmaf(sk[r], v[e], decay * s[i][e]);
+          o[e] = fmaf(sq[r], s[i][e], o[e]);
+        }
+        if constexpr (VEC == 4)
+          *reinterpret_cast<float4*>(S + r * d) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+        else
+          S[r * d] = s[i][0];
+      }
     }
-  }
-  part[y][x] = o;
+  if (y < groups)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) part[y * d + x * VEC + e] = o[e];
   __syncthreads();
-  if (y == 0 && c < p.d) {
-    for (int i = 1; i < 8; ++i) o += part[i][x];
-    from_f(at(out) + c, p.scale * o);
+  if (threadIdx.x < d) {
+    float sum = 0.0f;
+    for (int i = 0; i < groups; ++i) sum += part[i * d + threadIdx.x];
+    from_f(at(out) + threadIdx.x, p.scale * sum);
   }
 }
 
 int launch_gated_step(const GatedProblem& p, float* state, const Operand& out, void* stream) {
   KernelTimer timer("gated_step", stream);
-  const unsigned grid = static_cast<unsigned>(p.B * p.H * ((p.d + 31) / 32));
+  const unsigned grid = static_cast<unsigned>(p.B * p.H);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p.dtype == MHLA_BF16)
-    gated_step<__nv_bfloat16><<<grid, 256, 0, s>>>(p, state, out);
-  else
-    gated_step<float><<<grid, 256, 0, s>>>(p, state, out);
+  const bool vec = p.d % 4 == 0 && reinterpret_cast<uintptr_t>(state) % 16 == 0;
+  if (p.dtype == MHLA_BF16) {
+    if (vec)
+      gated_step<__nv_bfloat16, 4><<<grid, 256, 0, s>>>(p, state, out);
+    else
+      gated_step<__nv_bfloat16, 1><<<grid, 256, 0, s>>>(p, state, out);
+  } else {
+    if (vec)
+      gated_step<float, 4><<<grid, 256, 0, s>>>(p, state, out);
+    else
+      gated_step<float, 1><<<grid, 256, 0, s>>>(p, state, out);
+  }
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
 
