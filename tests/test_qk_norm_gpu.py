@@ -151,6 +151,18 @@ def test_zero_rows_and_large_values():
     check_backward(x, "half", "f32", run_backward(x, "half"))
 
 
+@pytest.mark.parametrize("d", [64, 40, 7])
+def test_no_eps(d):
+    """eps = 0: a row that is not there (the lanes behind the last one) leaves no 0 / 0 in the sums."""
+    x = draw(49, 1, 3, 3, 1, d, "f32", pairs=0)
+    got = mhla.qk_norm_backward(*(x[n].to(DEV) for n in ("q", "k", "dq_out", "dk_out", "q_weight", "k_weight")), eps=0.0)
+    torch.cuda.synchronize()
+    for i, name in enumerate("qk"):
+        dx, dw = oracle.qk_norm_backward(f64(x[name]), f64(x["d%s_out" % name]), f64(x[name + "_weight"]), 0.0)
+        assert np.abs(f64(got[i]) - dx).max() <= 1e-5 * np.abs(dx).max()
+        assert np.abs(f64(got[2 + i]) - dw).max() <= 1e-5 * np.abs(dw).max()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("extra", [0, 1])
 def test_in_place_on_a_projection(dtype, extra):

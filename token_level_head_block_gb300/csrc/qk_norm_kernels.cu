@@ -116,48 +116,40 @@ __global__ void __launch_bounds__(256) qk_norm_rows(const QkNormProblem p, float
   }
 }
 
-// ------------------------------------------------------------------ 16-byte units
+// ------------------------------------------------------------------ eight channels a lane
 //
-// A head row is read once, in 16-byte units, by a group of G lanes (G a power of two, the
-// lanes behind the head's units idle), kHeads heads of a token at a time: the rotation's
-// row is fetched once for them, and their loads are in flight together.  Every input
-// byte is read once and every output byte written once, so HBM bounds it.
+// A head row is read once by a group of G lanes (G a power of two, the lanes behind
+// the head's channels idle), each lane two runs of four channels chosen so that both
+// channels of a pair are its own: no exchange for the rotation, and four pairs of the table a lane.
+// A group takes kHeads heads of one token at a time, their loads in flight together and the
+// rotation's row fetched once.  Every input byte is read once and every output byte written
+// once: HBM bounds it.
 
+// Four channels as loaded.
 template <typename T>
-struct Units;
+struct Four;
 template <>
-struct Units<__nv_bfloat16> {
-  static constexpr int kVec = 8;
+struct Four<float> {
+  using Raw = float4;
+  static __device__ __forceinline__ void expand(const Raw& r, float* x) {
+    x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w;
+  }
+  static __device__ __forceinline__ Raw round(const float* x) { return make_float4(x[0], x[1], x[2], x[3]); }
 };
 template <>
-struct Units<float> {
-  static constexpr int kVec = 4;
+struct Four<__nv_bfloat16> {
+  using Raw = uint2;
+  static __device__ __forceinline__ void expand(const Raw& r, float* x) {
+    x[0] = __uint_as_float(r.x << 16);
+    x[1] = __uint_as_float(r.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(r.y << 16);
+    x[3] = __uint_as_float(r.y & 0xFFFF0000u);
+  }
+  static __device__ __forceinline__ Raw round(const float* x) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
 };
-
-__device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ void unpack(const uint4& u, float (&x)[4]) {
-  x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
-  x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
-}
-__device__ __forceinline__ uint4 repack(const float (&x)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&p);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ uint4 repack(const float (&x)[4]) {
-  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-}
 
 template <int G>
 __device__ __forceinline__ float group_total(float x) {
@@ -166,203 +158,207 @@ __device__ __forceinline__ float group_total(float x) {
   return x;
 }
 
-// The turn of a lane's VEC channels: y[e] -> y[e] c[e] + partner s[e].
-template <int VEC>
-struct Turns {
-  float c[VEC], s[VEC];
-  int partner;        // lane that holds the partners (half layout)
+// (a, b) of every pair of a lane's channels x[0..3], x[4..7].
+template <bool INTER>
+__device__ __forceinline__ void turn(float (&x)[8], const float (&c)[4], const float (&s)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int f = INTER ? 2 * i : i, g = INTER ? 2 * i + 1 : i + 4;
+    const float a = x[f], b = x[g];
+    x[f] = fmaf(a, c[i], -s[i] * b);
+    x[g] = fmaf(b, c[i], s[i] * a);
+  }
+}
+
+struct Walk {
+  int64_t items;            // (token, run of heads)
+  int32_t runs_q, runs_k;   // runs of a token
+  bool narrow;              // items and tokens in 32 bits
 };
 
-template <int VEC, int G>
-__device__ __forceinline__ Turns<VEC> turns_of(const QkNormProblem& p, int64_t row, int unit, int lane) {
-  Turns<VEC> t;
-  t.partner = lane;
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    t.c[e] = 1.0f;
-    t.s[e] = 0.0f;
-  }
-  if (!p.table) return t;
-  const float2* cs = reinterpret_cast<const float2*>(p.table) + (row > 0 ? row * p.pairs : 0);
-  const float nan = __int_as_float(0x7FC00000);
-  if (p.interleaved) {
-#pragma unroll
-    for (int e = 0; e < VEC; e += 2) {
-      const int pair = unit * (VEC / 2) + e / 2;
-      if (pair >= p.pairs || row == -1) continue;
-      const float2 x = row == -2 ? make_float2(nan, 0.0f) : cs[pair];
-      t.c[e] = t.c[e + 1] = x.x;
-      t.s[e] = -x.y;
-      t.s[e + 1] = x.y;
-    }
-    return t;
-  }
-  const int half = p.pairs / VEC;   // units a half
-  if (unit >= 2 * half) return t;
-  const bool second = unit >= half;
-  t.partner = second ? lane - half : lane + half;
-  if (row == -1) return t;
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    const float2 x = row == -2 ? make_float2(nan, 0.0f) : cs[(second ? unit - half : unit) * VEC + e];
-    t.c[e] = x.x;
-    t.s[e] = second ? x.y : -x.y;
-  }
-  return t;
-}
-
-template <int VEC>
-__device__ __forceinline__ void turn(float (&y)[VEC], const Turns<VEC>& t, bool interleaved, float sign) {
-  float o[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) o[e] = interleaved ? y[e ^ 1] : __shfl_sync(~0u, y[e], t.partner);
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) y[e] = fmaf(y[e], t.c[e], sign * t.s[e] * o[e]);
-}
-
-// kHeads heads of a token per group of G lanes; a grid-stride walk over (token, run of heads).
-template <typename T, int G, bool BWD>
-__global__ void __launch_bounds__(256) qk_norm_units(const QkNormProblem p, float* part) {
-  constexpr int VEC = Units<T>::kVec, kHeads = BWD ? 2 : 4, kGroups = 256 / G;
-  const int lane = threadIdx.x & 31, unit = threadIdx.x % G;
-  const bool live = unit * VEC < p.d;
-  const int64_t heads = p.Hq + p.Hk, runs = (heads + kHeads - 1) / kHeads, items = p.B * p.N * runs;
+template <typename T, int G, bool BWD, bool INTER>
+__global__ void __launch_bounds__(256, 3) qk_norm_lanes(const QkNormProblem p, const Walk walk, float* part) {
+  using R = typename Four<T>::Raw;
+  constexpr int kHeads = BWD ? 2 : 4, kGroups = 256 / G;
+  const int unit = threadIdx.x % G;
+  const bool live = unit * 8 < p.d;
+  // the lane's runs of channels; the four pairs 4 unit .. 4 unit + 3
+  const bool pairs_here = !INTER && 4 * unit < p.pairs;
+  const int c0 = pairs_here ? 4 * unit : 8 * unit, c1 = pairs_here ? 4 * unit + p.pairs : 8 * unit + 4;
   const float inv_d = 1.0f / static_cast<float>(p.d);
-  float w[2][VEC], acc[2][VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    w[0][e] = p.q_weight && live ? p.q_weight[unit * VEC + e] : 1.0f;
-    w[1][e] = p.k_weight && live ? p.k_weight[unit * VEC + e] : 1.0f;
-    acc[0][e] = acc[1][e] = 0.0f;
-  }
-  // every lane of a warp takes the same number of rounds: the shuffles need all of them
+  const int runs = walk.runs_q + walk.runs_k;
+  float acc[BWD ? 2 : 1][8] = {};
+  // every lane of a warp takes the same number of rounds: the sums need all of them
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kGroups;
-  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kGroups; i0 < items; i0 += stride) {
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kGroups; i0 < walk.items; i0 += stride) {
     const int64_t i = i0 + threadIdx.x / G;
-    const bool in = i < items && live;
-    const int64_t item = i < items ? i : items - 1;
-    const int64_t token = item / runs, b = token / p.N, n = token - b * p.N;
-    const int h0 = static_cast<int>(item - token * runs) * kHeads;
-    uint4 x[kHeads], z[BWD ? kHeads : 1];
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const bool in = i < walk.items && live;
+    const int64_t item = i < walk.items ? i : walk.items - 1;
+    int64_t token, b;
+    int run;
+    if (walk.narrow) {
+      const uint32_t t = static_cast<uint32_t>(item) / static_cast<uint32_t>(runs);
+      run = static_cast<int>(static_cast<uint32_t>(item) - t * runs);
+      b = t / static_cast<uint32_t>(p.N);
+      token = t;
+    } else {
+      token = item / runs;
+      run = static_cast<int>(item - token * runs);
+      b = token / p.N;
+    }
+    const int64_t n = token - b * p.N;
+    const bool is_k = run >= walk.runs_q;
+    const int h0 = (is_k ? run - walk.runs_q : run) * kHeads;
+    const int count = min(kHeads, static_cast<int>(is_k ? p.Hk : p.Hq) - h0);
+    auto row_of = [&](const Operand& oq, const Operand& ok, int64_t& sh) {
+      const Operand& o = is_k ? ok : oq;
+      sh = o.sh;
+      return static_cast<T*>(o.data) + b * o.sb + n * o.sn + h0 * o.sh;
+    };
+    int64_t xs, zs = 0, os;
+    const T* x = row_of(p.q, p.k, xs);
+    R xa[kHeads], xb[kHeads], za[BWD ? kHeads : 1], zb[BWD ? kHeads : 1];
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
-      const bool is_k = h0 + j >= p.Hq;
-      const int64_t h = is_k ? h0 + j - p.Hq : h0 + j;
-      const bool has = in && h0 + j < heads;
-      const Operand& src = is_k ? p.k : p.q;
-      x[j] = has ? *reinterpret_cast<const uint4*>(static_cast<const T*>(src.data) + b * src.sb + n * src.sn +
-                                                   h * src.sh + unit * VEC)
-                 : zero;
-      if (BWD) {
-        const Operand& g = is_k ? p.dk_out : p.dq_out;
-        z[j] = has ? *reinterpret_cast<const uint4*>(static_cast<const T*>(g.data) + b * g.sb + n * g.sn + h * g.sh +
-                                                     unit * VEC)
-                   : zero;
+      xa[j] = xb[j] = R{};
+      if (in && j < count) {
+        xa[j] = *reinterpret_cast<const R*>(x + j * xs + c0);
+        xb[j] = *reinterpret_cast<const R*>(x + j * xs + c1);
       }
     }
-    const Turns<VEC> t = turns_of<VEC, G>(p, rotation_row(p, token), unit, lane);
+    if (BWD) {
+      const T* z = row_of(p.dq_out, p.dk_out, zs);
+#pragma unroll
+      for (int j = 0; j < kHeads; ++j) {
+        za[BWD ? j : 0] = zb[BWD ? j : 0] = R{};
+        if (in && j < count) {
+          za[BWD ? j : 0] = *reinterpret_cast<const R*>(z + j * zs + c0);
+          zb[BWD ? j : 0] = *reinterpret_cast<const R*>(z + j * zs + c1);
+        }
+      }
+    }
+    float c[4], s[4];
+    const int64_t row = rotation_row(p, token);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      c[e] = 1.0f;
+      s[e] = 0.0f;
+      if (row != -1 && 4 * unit + e < p.pairs) {
+        const float2 cs = row == -2 ? make_float2(__int_as_float(0x7FC00000), 0.0f)
+                                    : reinterpret_cast<const float2*>(p.table)[row * p.pairs + 4 * unit + e];
+        c[e] = cs.x;
+        s[e] = BWD ? -cs.y : cs.y;
+      }
+    }
+    float w[8];
+    const float* weight = is_k ? p.k_weight : p.q_weight;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = weight && live ? weight[(e < 4 ? c0 : c1) + (e & 3)] : 1.0f;
+    T* out = row_of(p.q_out, p.k_out, os);
+    float own[8] = {};   // the heads' share of the weight's gradient
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
-      const bool is_k = h0 + j >= p.Hq;
-      const int64_t h = is_k ? h0 + j - p.Hq : h0 + j;
-      const float(&ww)[VEC] = w[0];
-      float u[VEC], ss = 0.0f;
-      unpack(x[j], u);
+      const bool real = in && j < count;
+      float u[8], ss = 0.0f;
+      Four<T>::expand(xa[j], u);
+      Four<T>::expand(xb[j], u + 4);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) ss = fmaf(u[e], u[e], ss);
+      for (int e = 0; e < 8; ++e) ss = fmaf(u[e], u[e], ss);
       const float r = rsqrtf(group_total<G>(ss) * inv_d + p.eps);
-      float y[VEC];
+      float y[8];
       if (!BWD) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) y[e] = u[e] * r * (is_k ? w[1][e] : ww[e]);
-        turn(y, t, p.interleaved, 1.0f);
+        for (int e = 0; e < 8; ++e) y[e] = u[e] * r * w[e];
+        turn<INTER>(y, c, s);
       } else {
-        unpack(z[BWD ? j : 0], y);
-        turn(y, t, p.interleaved, -1.0f);
+        Four<T>::expand(za[BWD ? j : 0], y);
+        Four<T>::expand(zb[BWD ? j : 0], y + 4);
+        turn<INTER>(y, c, s);
         float m = 0.0f;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
+        for (int e = 0; e < 8; ++e) {
           u[e] *= r;
-          const float du = y[e] * u[e];
-          if (is_k)
-            acc[1][e] += du;
-          else
-            acc[0][e] += du;
-          y[e] *= is_k ? w[1][e] : ww[e];
+          if (real) own[e] = fmaf(y[e], u[e], own[e]);   // eps 0: a row that is not there is 0 / 0
+          y[e] *= w[e];
           m = fmaf(y[e], u[e], m);
         }
         m = group_total<G>(m) * inv_d;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) y[e] = r * (y[e] - u[e] * m);
+        for (int e = 0; e < 8; ++e) y[e] = r * (y[e] - u[e] * m);
       }
-      if (in && h0 + j < heads) {
-        const Operand& dst = is_k ? p.k_out : p.q_out;
-        *reinterpret_cast<uint4*>(static_cast<T*>(dst.data) + b * dst.sb + n * dst.sn + h * dst.sh + unit * VEC) =
-            repack(y);
+      if (real) {
+        *reinterpret_cast<R*>(out + j * os + c0) = Four<T>::round(y);
+        *reinterpret_cast<R*>(out + j * os + c1) = Four<T>::round(y + 4);
       }
     }
+    if (BWD)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        acc[0][e] += is_k ? 0.0f : own[e];
+        acc[BWD ? 1 : 0][e] += is_k ? own[e] : 0.0f;
+      }
   }
   if (BWD) {   // the block's sums, its groups in a fixed order
-    __shared__ float sums[BWD ? kGroups * G * VEC : 1];
+    __shared__ float sums[BWD ? kGroups * G * 8 : 1];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       __syncthreads();
+      float* mine = sums + (threadIdx.x / G) * G * 8;
+      if (live)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) sums[(threadIdx.x / G) * G * VEC + unit * VEC + e] = acc[k][e];
+        for (int e = 0; e < 8; ++e) mine[(e < 4 ? c0 : c1) + (e & 3)] = acc[BWD ? k : 0][e];
       __syncthreads();
-      for (int c = threadIdx.x; c < 128; c += 256) {
-        float s = 0.0f;
-        if (c < G * VEC)
-          for (int g = 0; g < kGroups; ++g) s += sums[g * G * VEC + c];
-        part[static_cast<int64_t>(blockIdx.x) * 256 + k * 128 + c] = s;
+      if (threadIdx.x < p.d) {
+        float t = 0.0f;
+        for (int g = 0; g < kGroups; ++g) t += sums[g * G * 8 + threadIdx.x];
+        part[static_cast<int64_t>(blockIdx.x) * 256 + k * 128 + threadIdx.x] = t;
       }
     }
   }
 }
 
-// Whether the call's rows and their pairs fall into whole 16-byte units.
-bool in_units(const QkNormProblem& p, bool bwd) {
-  const int vec = p.dtype == MHLA_BF16 ? 8 : 4;
-  if (p.d % vec != 0 || (!p.interleaved && p.pairs % vec != 0)) return false;
+// Whether a lane's runs of four channels lie on the loads' boundaries and hold whole pairs.
+bool in_lanes(const QkNormProblem& p, bool bwd) {
+  if (p.d % 8 != 0 || (!p.interleaved && p.pairs % 4 != 0)) return false;
   const Operand* all[] = {&p.q, &p.k, &p.q_out, &p.k_out, &p.dq_out, &p.dk_out};
   const int64_t heads[] = {p.Hq, p.Hk, p.Hq, p.Hk, p.Hq, p.Hk};
+  const uintptr_t bytes = p.dtype == MHLA_BF16 ? 8 : 16;
   for (int i = 0; i < (bwd ? 6 : 4); ++i) {
     if (heads[i] == 0) continue;
     const Operand& o = *all[i];
-    if (reinterpret_cast<uintptr_t>(o.data) % 16 != 0 || o.sb % vec != 0 || o.sn % vec != 0 || o.sh % vec != 0)
-      return false;
+    if (reinterpret_cast<uintptr_t>(o.data) % bytes != 0 || o.sb % 4 != 0 || o.sn % 4 != 0 || o.sh % 4 != 0) return false;
   }
-  return p.Hq + p.Hk < (int64_t{1} << 30);
+  return true;
 }
 
-constexpr int kBwdBlocks = 608;   // four CTAs an SM
+constexpr int kBwdBlocks = 456;   // three CTAs an SM
 
-template <typename T, int G>
-void launch_units_group(const QkNormProblem& p, bool bwd, float* part, unsigned* grid, cudaStream_t s) {
-  const int64_t heads = p.Hq + p.Hk, per = bwd ? 2 : 4, groups = 256 / G;
-  const int64_t items = p.B * p.N * ((heads + per - 1) / per);
-  const int64_t blocks = std::max<int64_t>(1, (items + groups - 1) / groups);
-  if (bwd) {
-    *grid = static_cast<unsigned>(std::min<int64_t>(blocks, kBwdBlocks));
-    qk_norm_units<T, G, true><<<*grid, 256, 0, s>>>(p, part);
-  } else {
-    *grid = static_cast<unsigned>(std::min<int64_t>(blocks, int64_t{1} << 30));
-    qk_norm_units<T, G, false><<<*grid, 256, 0, s>>>(p, nullptr);
-  }
+template <typename T, int G, bool BWD>
+unsigned launch_lanes_group(const QkNormProblem& p, float* part, cudaStream_t s) {
+  constexpr int kHeads = BWD ? 2 : 4, kGroups = 256 / G;
+  Walk w;
+  w.runs_q = static_cast<int32_t>((p.Hq + kHeads - 1) / kHeads);
+  w.runs_k = static_cast<int32_t>((p.Hk + kHeads - 1) / kHeads);
+  w.items = p.B * p.N * (w.runs_q + w.runs_k);
+  w.narrow = w.items < (int64_t{1} << 31) && p.N < (int64_t{1} << 31);
+  const int64_t blocks = std::max<int64_t>(1, (w.items + kGroups - 1) / kGroups);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(blocks, BWD ? kBwdBlocks : int64_t{1} << 30));
+  if (p.interleaved)
+    qk_norm_lanes<T, G, BWD, true><<<grid, 256, 0, s>>>(p, w, part);
+  else
+    qk_norm_lanes<T, G, BWD, false><<<grid, 256, 0, s>>>(p, w, part);
+  return grid;
 }
 
-template <typename T>
-void launch_units(const QkNormProblem& p, bool bwd, float* part, unsigned* grid, cudaStream_t s) {
-  const int units = p.d / Units<T>::kVec;
-  if (units <= 4)
-    launch_units_group<T, 4>(p, bwd, part, grid, s);
-  else if (units <= 8)
-    launch_units_group<T, 8>(p, bwd, part, grid, s);
-  else if (units <= 16)
-    launch_units_group<T, 16>(p, bwd, part, grid, s);
-  else if constexpr (sizeof(T) == 4)
-    launch_units_group<T, 32>(p, bwd, part, grid, s);
+template <bool BWD>
+unsigned launch_lanes(const QkNormProblem& p, float* part, cudaStream_t s) {
+  if (p.dtype == MHLA_BF16)
+    return p.d <= 32   ? launch_lanes_group<__nv_bfloat16, 4, BWD>(p, part, s)
+           : p.d <= 64 ? launch_lanes_group<__nv_bfloat16, 8, BWD>(p, part, s)
+                       : launch_lanes_group<__nv_bfloat16, 16, BWD>(p, part, s);
+  return p.d <= 32   ? launch_lanes_group<float, 4, BWD>(p, part, s)
+         : p.d <= 64 ? launch_lanes_group<float, 8, BWD>(p, part, s)
+                     : launch_lanes_group<float, 16, BWD>(p, part, s);
 }
 
 // One warp a channel: the blocks' sums in a fixed order.
@@ -388,14 +384,11 @@ size_t qk_norm_bwd_workspace_bytes(int32_t) { return align_up(static_cast<size_t
 
 int launch_qk_norm(const QkNormProblem& p, void* stream) {
   KernelTimer timer("qk_norm", stream);
-  unsigned grid = static_cast<unsigned>(std::min<int64_t>(row_blocks(p), 152 * 64));
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(row_blocks(p), 152 * 64));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (in_units(p, false)) {
-    if (p.dtype == MHLA_BF16)
-      launch_units<__nv_bfloat16>(p, false, nullptr, &grid, s);
-    else
-      launch_units<float>(p, false, nullptr, &grid, s);
-  } else if (p.dtype == MHLA_BF16)
+  if (in_lanes(p, false))
+    launch_lanes<false>(p, nullptr, s);
+  else if (p.dtype == MHLA_BF16)
     qk_norm_rows<__nv_bfloat16, false><<<grid, 256, 0, s>>>(p, nullptr);
   else
     qk_norm_rows<float, false><<<grid, 256, 0, s>>>(p, nullptr);
@@ -408,13 +401,10 @@ int launch_qk_norm_backward(const QkNormProblem& p, void* workspace, void* strea
   float* part = static_cast<float*>(workspace);
   {
     KernelTimer timer("qk_norm_backward", stream);
-    const bool any = p.B > 0 && p.Hq + p.Hk > 0;   // the walk over units needs a row
-    if (any && in_units(p, true)) {
-      if (p.dtype == MHLA_BF16)
-        launch_units<__nv_bfloat16>(p, true, part, &grid, s);
-      else
-        launch_units<float>(p, true, part, &grid, s);
-    } else if (p.dtype == MHLA_BF16)
+    const bool any = p.B > 0 && p.Hq + p.Hk > 0;   // the walk over lanes needs a row
+    if (any && in_lanes(p, true))
+      grid = launch_lanes<true>(p, part, s);
+    else if (p.dtype == MHLA_BF16)
       qk_norm_rows<__nv_bfloat16, true><<<grid, 256, 0, s>>>(p, part);
     else
       qk_norm_rows<float, true><<<grid, 256, 0, s>>>(p, part);
