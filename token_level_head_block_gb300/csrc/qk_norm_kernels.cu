@@ -177,9 +177,9 @@ struct Walk {
 };
 
 template <typename T, int G, bool BWD, bool INTER>
-__global__ void __launch_bounds__(256, 3) qk_norm_lanes(const QkNormProblem p, const Walk walk, float* part) {
+__global__ void __launch_bounds__(256, BWD ? 2 : 4) qk_norm_lanes(const QkNormProblem p, const Walk walk, float* part) {
   using R = typename Four<T>::Raw;
-  constexpr int kHeads = BWD ? 2 : 4, kGroups = 256 / G;
+  constexpr int kHeads = BWD ? 3 : 4, kGroups = 256 / G;
   const int unit = threadIdx.x % G;
   const bool live = unit * 8 < p.d;
   // the lane's runs of channels; the four pairs 4 unit .. 4 unit + 3
@@ -331,11 +331,11 @@ bool in_lanes(const QkNormProblem& p, bool bwd) {
   return true;
 }
 
-constexpr int kBwdBlocks = 456;   // three CTAs an SM
+constexpr int kBwdBlocks = 304;   // two CTAs an SM
 
 template <typename T, int G, bool BWD>
 unsigned launch_lanes_group(const QkNormProblem& p, float* part, cudaStream_t s) {
-  constexpr int kHeads = BWD ? 2 : 4, kGroups = 256 / G;
+  constexpr int kHeads = BWD ? 3 : 4, kGroups = 256 / G;
   Walk w;
   w.runs_q = static_cast<int32_t>((p.Hq + kHeads - 1) / kHeads);
   w.runs_k = static_cast<int32_t>((p.Hk + kHeads - 1) / kHeads);
