@@ -253,7 +253,8 @@ def kernel_work(wl, name):
         "mhla_gemm_out": ("tensor", 2 * wl.tokens * (wl.H * d) * (wl.H * d)),
         # gated recurrence: read q, k, v, write o (a backward scan: three tensors in, one out)
         # (a span's state: read k, v; joining: the states of every 512 tokens or so, in and out)
-        "gated_span_state": ("hbm", 2 * io), "gated_join": ("hbm", BH * max(1, wl.N // 512) * d * d * 8),
+        "gated_span_state": ("hbm", 2 * io), "gated_tc_span_state": ("hbm", 2 * io), "gated_tc_scan": ("hbm", 4 * io),
+        "gated_join": ("hbm", BH * max(1, wl.N // 512) * d * d * 8),
         "gated_step": ("hbm", BH * d * d * 8), "gated_scan": ("hbm", 4 * io), "gated_gate_grad": ("hbm", BH * wl.N * (2 * 4 + wl.elem_bytes)),
         # norm and rotation: q and k in and out; with both output gradients in
         "qk_norm": ("hbm", 4 * io), "qk_norm_backward": ("hbm", 6 * io),

@@ -25,44 +25,17 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "gated_common.cuh"
 #include "mhla_internal.h"
 #include "ptx.cuh"
 
 namespace mhla {
+
+using namespace gated;
+
 namespace {
 
-constexpr float kLowestGate = -1000.0f;   // exp is 0 in float32 far above this
 constexpr int kChunk = 64;
-constexpr int kSms = 152;
-
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_f(float* p, float x) { *p = x; }
-__device__ __forceinline__ void from_f(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-
-// One scan.  States are [r][c], r of k's channels, c of v's.
-struct Scan {
-  Operand q, k, v, out, dot;
-  const float* init;    // state entering a span, or null for zero
-  float* last;          // state after the last span [B][H][d][d], or null
-  float* local;         // gated_span_state: a span's own contribution [B][H][spans][d][d]
-  float* decay;         // and its decay [B][H][spans]
-  float* dots;          // sums of dot_t . out_t before rounding [slices][B][H][N], or null
-  float out_scale;      // of the scores
-  float state_scale;    // of what a query reads from the state
-  float k_scale;        // of what a token adds to the state
-  int32_t reverse;
-  int32_t init_transposed;
-  int32_t init_spans;   // spans per (b, h) in init: slot of a span, or 1
-};
-
-struct ScanSet {
-  Scan scan[3];
-  Operand g;
-  int64_t N, H, BH;
-  int64_t span_chunks, chunks;
-  int32_t spans, d;
-};
 
 // bf16 terms an operand enters the tensor cores with.  bf16 inputs are exact in one.
 // The scores and the state a query reads feed a result that is rounded to bf16
@@ -111,32 +84,6 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint3
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack(float lo, float hi) {
-  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
-}
-__device__ __forceinline__ float low(uint32_t p) { return __uint_as_float(p << 16); }
-__device__ __forceinline__ float high(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
-
-// x, y as sums of NT bf16 terms, packed in pairs.
-template <int NT>
-__device__ __forceinline__ void split(float x, float y, uint32_t (&t)[NT]) {
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    t[i] = pack(x, y);
-    if (i + 1 < NT) {
-      x -= low(t[i]);
-      y -= high(t[i]);
-    }
-  }
-}
-
 // Accumulators of NT column tiles.  The tensor core truncates what it adds to an
 // accumulator, which drifts over a long chain: float32 runs keep the products of the
 // first terms, few additions, apart from the many small ones.
@@ -177,28 +124,6 @@ __device__ __forceinline__ void mma_terms(Accumulators<NT, APART>& acc, int n0, 
     }
 }
 
-// A sum of log decays (in powers of two) as the sum of two floats: differences of
-// far sums keep the precision of the near ones.
-struct Sum {
-  float hi, lo;
-};
-__device__ __forceinline__ Sum add(Sum a, Sum b) {
-  const float s = a.hi + b.hi, z = s - a.hi;
-  const float e = ((a.hi - (s - z)) + (b.hi - z)) + (a.lo + b.lo);
-  Sum r;
-  r.hi = s + e;
-  r.lo = e - (r.hi - s);
-  return r;
-}
-__device__ __forceinline__ Sum gate_sum(float g) {
-  constexpr float kL = 1.4426950408889634f, kLlo = static_cast<float>(1.4426950408889634 - kL);
-  g = g < kLowestGate ? kLowestGate : g;   // NaN stays
-  Sum r;
-  r.hi = g * kL;
-  r.lo = fmaf(g, kLlo, fmaf(g, kL, -r.hi));
-  return r;
-}
-
 // What a chunk needs of its gates.  Rows i of a block of 16 tokens see tokens j of other
 // blocks through e^{b_i - b_j} = e^{b_i - m} e^{m - b_j}, m at the edge of the
 // row's block towards them, so neither factor exceeds 1; the state, too, is read with
@@ -221,8 +146,6 @@ __device__ __forceinline__ float2 load_gates(const ScanSet& p, int64_t b, int64_
   const T* g = static_cast<const T*>(p.g.data) + b * p.g.sb + h * p.g.sh;
   return make_float2(t < p.N ? to_f(g[t * p.g.sn]) : 0.0f, t + 1 < p.N ? to_f(g[(t + 1) * p.g.sn]) : 0.0f);
 }
-
-__device__ __forceinline__ float exp2_of(Sum a, Sum b) { return exp2_fast((a.hi - b.hi) + (a.lo - b.lo)); }
 
 // One warp: the running sums and the weights of a chunk.  Returns B.
 __device__ __forceinline__ Sum chunk_gates(float2 g, Gates& out, const Scan& a, int lane) {
@@ -978,11 +901,6 @@ __global__ void __launch_bounds__(256) gated_gate_grad(const __grid_constant__ G
 
 int padded(int32_t d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
 
-// Spans a sequence is cut into.
-struct Cut {
-  int64_t chunks, span_chunks, spans;
-};
-
 Cut cut_for(const GatedProblem& p, int scans) {
   Cut c;
   c.chunks = (p.N + kChunk - 1) / kChunk;
@@ -1081,6 +999,14 @@ size_t span_bytes(const GatedProblem& p, const Cut& c) {
   return align_up(static_cast<size_t>(n * p.d * p.d) * 4) + align_up(static_cast<size_t>(n) * 4);
 }
 
+// Enough for either kernel, whichever takes the call's operands.
+size_t most_span_bytes(const GatedProblem& p, int scans) {
+  const size_t n = span_bytes(p, cut_for(p, scans));
+  return tc_supported(p) ? std::max(n, span_bytes(p, tc_cut(p, scans))) : n;
+}
+
+int64_t dot_slices(const GatedProblem& p) { return p.d > 32 ? 2 : 1; }
+
 SpanBuffers carve_spans(const GatedProblem& p, const Cut& c, char** base) {
   if (c.spans < 2) return SpanBuffers{nullptr, nullptr};
   const int64_t n = p.B * p.H * c.spans;
@@ -1092,92 +1018,110 @@ SpanBuffers carve_spans(const GatedProblem& p, const Cut& c, char** base) {
   return s;
 }
 
+// The kernels of one call: tcgen05 where the operands suit it, else mma.sync.
+struct Runner {
+  const GatedProblem& p;
+  bool tc, async;
+  TcMaps maps;
+  cudaStream_t s;
+  int run(const ScanSet& set, int scans, bool span_state) const {
+    return tc ? launch_tc_scan(set, maps, scans, span_state, s) : run_scans(p, set, scans, async, span_state, s);
+  }
+};
+
+// Short sequences leave most of a 128-token tile empty.
+bool wants_tc(const GatedProblem& p) { return tc_supported(p) && p.N >= 128; }
+
 }  // namespace
 
-size_t gated_workspace_bytes(const GatedProblem& p) { return span_bytes(p, cut_for(p, 1)); }
+size_t gated_workspace_bytes(const GatedProblem& p) { return most_span_bytes(p, 1); }
 
 size_t gated_bwd_workspace_bytes(const GatedProblem& p) {
-  const int64_t bh = p.B * p.H, slices = p.d > 64 ? 2 : 1;
-  return 2 * span_bytes(p, cut_for(p, 3)) + 2 * align_up(static_cast<size_t>(slices * bh * p.N) * 4) +
+  const int64_t bh = p.B * p.H;
+  return 2 * most_span_bytes(p, 3) + 2 * align_up(static_cast<size_t>(dot_slices(p) * bh * p.N) * 4) +
          align_up(static_cast<size_t>(bh * p.d * p.d) * 4);
 }
 
 int launch_gated_forward(const GatedProblem& p, const float* state_in, const Operand& out, float* state_out,
                          void* workspace, void* stream) {
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Cut c = cut_for(p, 1);
-  const bool async = rows_of_16(p, {&p.q, &p.k, &p.v, &out});
-  ScanSet set = scan_set(p, c);
   Scan a = plain_scan(p.q, p.k, p.v, out);
   a.out_scale = a.state_scale = p.scale;
   a.init = state_in;
   a.last = state_out;
+  Runner r{p, false, rows_of_16(p, {&p.q, &p.k, &p.v, &out}), {}, static_cast<cudaStream_t>(stream)};
+  ScanSet set = {};
+  set.scan[0] = a;
+  r.tc = r.async && wants_tc(p) && tc_maps(p, set, 1, &r.maps);
+  const Cut c = r.tc ? tc_cut(p, 1) : cut_for(p, 1);
+  set = scan_set(p, c);
   char* base = static_cast<char*>(workspace);
   const SpanBuffers sb = carve_spans(p, c, &base);
   a.local = sb.local;
   a.decay = sb.decay;
   set.scan[0] = a;
   if (c.spans > 1) {
-    int rc = run_scans(p, set, 1, async, true, s);
-    if (rc == MHLA_OK) rc = run_join(set, 1, s);
+    int rc = r.run(set, 1, true);
+    if (rc == MHLA_OK) rc = run_join(set, 1, r.s);
     if (rc != MHLA_OK) return rc;
     set.scan[0].init = sb.local;
     set.scan[0].init_spans = set.spans;
   }
-  return run_scans(p, set, 1, async, false, s);
+  return r.run(set, 1, false);
 }
 
 int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* workspace, void* stream) {
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Cut c = cut_for(p, 3);
-  const bool async = rows_of_16(p, {&p.q, &p.k, &p.v, &b.dout, &b.dq, &b.dk, &b.dv});
-  const int64_t bh = p.B * p.H, slices = p.d > 64 ? 2 : 1;
-  char* base = static_cast<char*>(workspace);
-  const SpanBuffers fwd = carve_spans(p, c, &base), back = carve_spans(p, c, &base);
-  float* qdots = reinterpret_cast<float*>(base);
-  base += align_up(static_cast<size_t>(slices * bh * p.N) * 4);
-  float* kdots = reinterpret_cast<float*>(base);
-  base += align_up(static_cast<size_t>(slices * bh * p.N) * 4);
-  float* last = reinterpret_cast<float*>(base);
-
-  ScanSet set = scan_set(p, c);
   Scan dq = plain_scan(b.dout, p.v, p.k, b.dq);   // its state: S^T
   dq.out_scale = dq.state_scale = p.scale;
   dq.init = b.state_in;
   dq.init_transposed = 1;
-  dq.last = last;
   dq.dot = p.q;
-  dq.dots = qdots;
-  dq.local = fwd.local;
-  dq.decay = fwd.decay;
   Scan dk = plain_scan(p.v, b.dout, p.q, b.dk);   // its state: dS^T
   dk.reverse = 1;
   dk.out_scale = dk.k_scale = p.scale;
   dk.init = b.dstate_out;
   dk.init_transposed = 1;
   dk.dot = p.k;
-  dk.dots = kdots;
-  dk.local = back.local;
-  dk.decay = back.decay;
   Scan dv = plain_scan(p.k, p.q, b.dout, b.dv);   // its state: dS
   dv.reverse = 1;
   dv.out_scale = dv.k_scale = p.scale;
   dv.init = b.dstate_out;
   dv.last = b.dstate_in;
-  set.scan[0] = dq;
-  set.scan[1] = dk;
-  set.scan[2] = dv;
+
+  Runner r{p, false, rows_of_16(p, {&p.q, &p.k, &p.v, &b.dout, &b.dq, &b.dk, &b.dv}), {},
+           static_cast<cudaStream_t>(stream)};
+  ScanSet set = {};
+  set.scan[0] = dq; set.scan[1] = dk; set.scan[2] = dv;
+  r.tc = r.async && wants_tc(p) && tc_maps(p, set, 3, &r.maps);
+  const Cut c = r.tc ? tc_cut(p, 3) : cut_for(p, 3);
+  const int64_t bh = p.B * p.H;
+  char* base = static_cast<char*>(workspace);
+  const SpanBuffers fwd = carve_spans(p, c, &base), back = carve_spans(p, c, &base);
+  float* qdots = reinterpret_cast<float*>(base);
+  base += align_up(static_cast<size_t>(dot_slices(p) * bh * p.N) * 4);
+  float* kdots = reinterpret_cast<float*>(base);
+  base += align_up(static_cast<size_t>(dot_slices(p) * bh * p.N) * 4);
+  float* last = reinterpret_cast<float*>(base);
+
+  set = scan_set(p, c);
+  dq.last = last;
+  dq.dots = qdots;
+  dq.local = fwd.local;
+  dq.decay = fwd.decay;
+  dk.dots = kdots;
+  dk.local = back.local;
+  dk.decay = back.decay;
+  set.scan[0] = dq; set.scan[1] = dk; set.scan[2] = dv;
   int rc = MHLA_OK;
   if (c.spans > 1) {
-    rc = run_scans(p, set, 2, async, true, s);
-    if (rc == MHLA_OK) rc = run_join(set, 2, s);
+    rc = r.run(set, 2, true);
+    if (rc == MHLA_OK) rc = run_join(set, 2, r.s);
     set.scan[0].init = fwd.local;
     set.scan[1].init = set.scan[2].init = back.local;
     set.scan[0].init_transposed = set.scan[1].init_transposed = 0;
     set.scan[2].init_transposed = 1;
     for (Scan& a : set.scan) a.init_spans = set.spans;
   }
-  if (rc == MHLA_OK) rc = run_scans(p, set, 3, async, false, s);
+  if (rc == MHLA_OK) rc = r.run(set, 3, false);
   if (rc != MHLA_OK) return rc;
   GateGrad gg = {};
   gg.qdots = qdots; gg.kdots = kdots;
@@ -1185,14 +1129,15 @@ int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* w
   gg.last = last; gg.dlast = b.dstate_out;
   gg.dg = b.dg;
   gg.N = p.N; gg.H = p.H; gg.BH = bh;
-  gg.span_tokens = c.span_chunks * kChunk;
-  gg.spans = set.spans; gg.d = p.d; gg.slices = static_cast<int32_t>(slices);
+  gg.span_tokens = c.span_chunks * (r.tc ? kTcChunk : kChunk);
+  gg.spans = set.spans; gg.d = p.d;
+  gg.slices = r.tc ? static_cast<int32_t>(dot_slices(p)) : (p.d > 64 ? 2 : 1);
   KernelTimer timer("gated_gate_grad", stream);
   const unsigned grid = static_cast<unsigned>(bh * c.spans);
   if (p.dtype == MHLA_BF16)
-    gated_gate_grad<__nv_bfloat16><<<grid, 256, 0, s>>>(gg);
+    gated_gate_grad<__nv_bfloat16><<<grid, 256, 0, r.s>>>(gg);
   else
-    gated_gate_grad<float><<<grid, 256, 0, s>>>(gg);
+    gated_gate_grad<float><<<grid, 256, 0, r.s>>>(gg);
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
 

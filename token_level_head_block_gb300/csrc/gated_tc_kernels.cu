@@ -1,0 +1,719 @@
+// The scans of gated causal linear attention (gated_kernels.cu states the recurrence)
+// on the fifth-generation tensor cores: bf16, d <= 64, chunks of 128 tokens.
+//
+// A persistent CTA per SM walks a span of chunks.  Per chunk, b_i the sum of the log
+// decays up to token i and B of all of them (backwards every difference changes sign):
+//   scores  S1 = Q K^T                                128 x 128, in tensor memory
+//   P_ij    = scale e^{b_i - b_j} S1_ij for j <= i    two bf16 terms, over S1 in tensor memory
+//   O1      = Q S                                     S the state, two bf16 terms in shared memory
+//   O2      = P V                                     A from tensor memory
+//   o_i     = scale e^{b_i} O1_i + O2_i
+//   L       = (e^{B - b_j} k_j)^T V                   three bf16 terms in shared memory
+//   S       <- e^B S + L                              float32 in registers, rounded to nearest
+// The tensor core has four times mma.sync's rate and takes its operands without
+// instructions of the warps, which leaves them the splitting into terms: that work
+// bounds the kernel, so sixteen warps share it.  Eight (score warps) turn S1 into P and
+// write the outputs, one chunk apart, so that PV of one chunk runs under P of
+// the next; eight (state warps) scale and split k and carry the state; one warp issues the MMAs, one
+// loads (TMA, three stages) and prepares the gates.  A thread of a score warp owns a row, so a
+// row's factor is a register and the columns' factors are read by broadcast.
+//
+// Every wait is bounded; one that gives up sets bit 0 of this file's error
+// word and an abort flag, the CTA drains what it issued and releases tensor memory.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "gated_common.cuh"
+#include "mhla_internal.h"
+#include "ptx.cuh"
+#include "tc_common.cuh"
+#include "tma_host.h"
+
+namespace mhla {
+
+__device__ unsigned int g_gated_error = 0;
+
+namespace gated {
+namespace {
+
+using namespace tc;
+
+constexpr int kScoreWarps = 8, kStateWarps = 8;
+constexpr int kIssuer = kScoreWarps + kStateWarps, kLoader = kIssuer + 1;
+constexpr int kThreads = 32 * (kLoader + 1);
+constexpr int kStages = 3;
+constexpr int kTileBytes = kTcChunk * 128;   // 128 rows of 64 channels, 128-byte swizzle
+constexpr int kPlane = kTileBytes;           // one term of the scaled k
+constexpr int kStatePlane = 64 * 128;        // one term of the state
+constexpr uint32_t kSbo = 1024;              // between groups of eight rows
+
+// Tensor memory columns.
+constexpr uint32_t kScores = 0;   // two buffers of 128: S1, then P
+constexpr uint32_t kO1 = 256, kO2 = 320, kL = 384;
+constexpr uint32_t kTmemColumns = 512;
+
+// What a chunk needs of its gates; blocks of 32 rows see other blocks' tokens through
+// e^{b_i - m} e^{m - b_j}, m at the block's edge towards them, neither factor above 1.
+struct ChunkGates {
+  float hi[kTcChunk], lo[kTcChunk];   // b_i
+  float row[kTcChunk];                // e^{b_i - m}
+  float col[4][kTcChunk];             // out_scale e^{m - b_j}, per block of rows
+  float addw[kTcChunk];               // k_scale e^{B - b_j}
+  float enter[4];                     // state_scale e^m
+  float total;                        // e^B
+  float pad[3];
+};
+
+struct Bars {
+  uint64_t full[kStages], gates[kStages], freed[kStages];
+  uint64_t scores[2], p_ready[2];
+  uint64_t out_done, out_read, k_ready[2], l_done, s_ready, fin;
+};
+
+struct Control {
+  Bars bars;
+  uint32_t tmem, abort;
+  uint32_t bad[4];   // chunk + 1 whose v holds an infinity or NaN
+};
+
+template <bool ONLY_STATE>
+struct Layout {
+  static constexpr int kTiles = ONLY_STATE ? 2 : 3;   // q, k, v  |  k, v
+  static constexpr int kStage = kTiles * kTileBytes;
+  static constexpr int kKp = kStages * kStage;
+  static constexpr int kS = kKp + 3 * kPlane;
+  static constexpr int kGates = kS + (ONLY_STATE ? 0 : 2 * kStatePlane);
+  static constexpr int kControl = kGates + kStages * static_cast<int>(sizeof(ChunkGates));
+  static constexpr size_t kBytes = kControl + sizeof(Control) + 1024;
+};
+static_assert(Layout<false>::kBytes <= 227 * 1024, "shared memory of one CTA");
+
+__device__ __forceinline__ bool gwait(uint64_t* bar, uint32_t parity, volatile uint32_t* abortf) {
+  return wait_bounded_on(bar, parity & 1u, abortf, &g_gated_error);
+}
+__device__ __forceinline__ bool gwarp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abortf) {
+  return warp_wait_on(bar, parity & 1u, abortf, &g_gated_error);
+}
+
+// D (+)= A[tensor memory] B[shared memory].
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 16 lanes by 32 columns, spread over the warp like an mma accumulator: value 4 n + e is
+// row lane / 4 + 8 (e / 2), column 8 n + 2 (lane % 4) + e % 2.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// Byte offset of a 16-byte unit of a 128-byte row in the 128-byte swizzle.
+__device__ __forceinline__ int unit_at(int row, int unit) { return row * 128 + ((unit ^ (row & 7)) << 4); }
+
+// A lane's four gates of a chunk (tokens 4 lane ..); 0 behind the end.
+__device__ __forceinline__ float4 load_gates(const ScanSet& p, int64_t b, int64_t h, int64_t chunk, int lane) {
+  const int64_t t = chunk * kTcChunk + 4 * lane;
+  const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(p.g.data) + b * p.g.sb + h * p.g.sh + t * p.g.sn;
+  float x[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = t + e < p.N ? to_f(g[e * p.g.sn]) : 0.0f;
+  return make_float4(x[0], x[1], x[2], x[3]);
+}
+
+__device__ __forceinline__ Sum shfl_sum(Sum s, int lane) {
+  Sum r;
+  r.hi = __shfl_sync(~0u, s.hi, lane);
+  r.lo = __shfl_sync(~0u, s.lo, lane);
+  return r;
+}
+
+// One warp: the running sums and the weights of a chunk.  Returns B.
+__device__ __forceinline__ Sum chunk_gates(float4 g, ChunkGates& out, const Scan& a, int lane) {
+  const Sum none = {0.0f, 0.0f};
+  Sum at[4];
+  at[0] = gate_sum(g.x);
+  at[1] = add(at[0], gate_sum(g.y));
+  at[2] = add(at[1], gate_sum(g.z));
+  at[3] = add(at[2], gate_sum(g.w));
+  Sum run = at[3];
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    Sum o;
+    o.hi = __shfl_up_sync(~0u, run.hi, s);
+    o.lo = __shfl_up_sync(~0u, run.lo, s);
+    if (lane >= s) run = add(o, run);
+  }
+  const Sum all = shfl_sum(run, 31);
+  const Sum edge[5] = {none, shfl_sum(run, 7), shfl_sum(run, 15), shfl_sum(run, 23), all};
+  Sum before;
+  before.hi = __shfl_up_sync(~0u, run.hi, 1);
+  before.lo = __shfl_up_sync(~0u, run.lo, 1);
+  if (lane == 0) before = none;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) at[e] = add(before, at[e]);
+  const int block = lane >> 3;
+  const bool reverse = a.reverse;
+  Sum m = reverse ? edge[1] : edge[0];
+#pragma unroll
+  for (int i = 1; i < 4; ++i)
+    if (block == i) m = reverse ? edge[i + 1] : edge[i];
+  float hi[4], lo[4], row[4], addw[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    hi[e] = at[e].hi;
+    lo[e] = at[e].lo;
+    row[e] = reverse ? exp2_of(m, at[e]) : exp2_of(at[e], m);
+    addw[e] = a.k_scale * (reverse ? exp2_of(at[e], none) : exp2_of(all, at[e]));
+  }
+  auto put = [&](float* to, const float (&x)[4]) {
+    reinterpret_cast<float4*>(to)[lane] = make_float4(x[0], x[1], x[2], x[3]);
+  };
+  put(out.hi, hi);
+  put(out.lo, lo);
+  put(out.row, row);
+  put(out.addw, addw);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (reverse ? block <= r : block >= r) continue;   // tokens the rows of block r do not see through m
+    const Sum e = reverse ? edge[r + 1] : edge[r];
+    float c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = a.out_scale * (reverse ? exp2_of(at[i], e) : exp2_of(e, at[i]));
+    put(out.col[r], c);
+  }
+  if ((lane & 7) == 0) out.enter[block] = a.state_scale * (reverse ? exp2_of(all, m) : exp2_of(m, none));
+  if (lane == 0) out.total = exp2_of(all, none);
+  return all;
+}
+
+// The outputs' second part of one row without the tensor core, for a chunk whose v
+// holds an infinity or NaN: 0 times it must not reach rows that do not see it.
+template <int DH>
+__device__ __noinline__ void row_apart(float (&o)[16], const uint8_t* stage, const ChunkGates& w, float out_scale,
+                                       int row, int c0, bool reverse) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) o[c] = 0.0f;
+  const uint8_t *q = stage, *k = stage + kTileBytes, *v = stage + 2 * kTileBytes;
+  const int j0 = reverse ? row : 0, j1 = reverse ? kTcChunk : row + 1;
+  for (int j = j0; j < j1; ++j) {
+    float s = 0.0f;
+    for (int u = 0; u < DH / 8; ++u) {
+      const uint4 a = *reinterpret_cast<const uint4*>(q + unit_at(row, u));
+      const uint4 b = *reinterpret_cast<const uint4*>(k + unit_at(j, u));
+      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s = fmaf(low(x[e]), low(y[e]), fmaf(high(x[e]), high(y[e]), s));
+    }
+    const float x = (w.hi[row] - w.hi[j]) + (w.lo[row] - w.lo[j]);
+    s *= out_scale * exp2_fast(reverse ? -x : x);
+    for (int u = 0; u < 2; ++u) {
+      const uint4 a = *reinterpret_cast<const uint4*>(v + unit_at(j, c0 / 8 + u));
+      const uint32_t y[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[8 * u + 2 * e] = fmaf(s, low(y[e]), o[8 * u + 2 * e]);
+        o[8 * u + 2 * e + 1] = fmaf(s, high(y[e]), o[8 * u + 2 * e + 1]);
+      }
+    }
+  }
+}
+
+// DH: channels the tensor core works on (32 or 64).
+template <int DH, bool ONLY_STATE>
+__global__ void __launch_bounds__(kThreads, 1)
+    gated_tc_scan(const __grid_constant__ ScanSet p, const __grid_constant__ TcMaps maps) {
+  using L = Layout<ONLY_STATE>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
+  uint8_t* kp = smem + L::kKp;
+  uint8_t* planes = smem + L::kS;
+  ChunkGates* gates = reinterpret_cast<ChunkGates*>(smem + L::kGates);
+  Control& ctl = *reinterpret_cast<Control*>(smem + L::kControl);
+  Bars& bar = ctl.bars;
+  volatile uint32_t* abortf = &ctl.abort;
+  constexpr int kKTile = ONLY_STATE ? 0 : kTileBytes, kVTile = kKTile + kTileBytes;
+
+  const Scan& a = p.scan[blockIdx.y];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool reverse = a.reverse;
+  int64_t id = blockIdx.x;
+  const int64_t nspans = ONLY_STATE ? p.spans - 1 : p.spans;   // the span last in order adds to no other
+  const int64_t span = id % nspans + (ONLY_STATE && reverse ? 1 : 0);
+  const int64_t bh = id / nspans, b = bh / p.H, h = bh % p.H;
+  const int64_t first = span * p.span_chunks;
+  const int count = static_cast<int>(min(p.span_chunks, p.chunks - first));
+  auto chunk_of = [&](int n) { return first + (reverse ? count - 1 - n : n); };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar.full + s, 1);
+      mbar_init(bar.gates + s, 1);
+      mbar_init(bar.freed + s, ONLY_STATE ? kStateWarps : kStateWarps + kScoreWarps);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar.scores + s, 1);
+      mbar_init(bar.p_ready + s, kScoreWarps);
+      mbar_init(bar.k_ready + s, kStateWarps);
+    }
+    mbar_init(&bar.out_done, 1);
+    mbar_init(&bar.out_read, kScoreWarps);
+    mbar_init(&bar.l_done, 1);
+    mbar_init(&bar.s_ready, kStateWarps);
+    mbar_init(&bar.fin, 1);
+    ctl.abort = 0u;
+    for (int i = 0; i < 4; ++i) ctl.bad[i] = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&ctl.tmem, kTmemColumns);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+
+  if (warp == kLoader) {
+    // ------------------------------------------------------------ loads and gates
+    const uint64_t policy = ONLY_STATE ? policy_evict_last() : policy_evict_first();
+    auto load = [&](int n) {
+      uint64_t* full = bar.full + n % kStages;
+      uint8_t* st = smem + (n % kStages) * L::kStage;
+      const int32_t t = static_cast<int32_t>(chunk_of(n) * kTcChunk), hh = static_cast<int32_t>(h),
+                    bb = static_cast<int32_t>(b);
+      mbar_arrive_expect_tx(full, L::kStage);
+      if (!ONLY_STATE) tma_load_4d(st, &maps.q[blockIdx.y], full, 0, hh, t, bb, policy);
+      tma_load_4d(st + kKTile, &maps.k[blockIdx.y], full, 0, hh, t, bb, policy);
+      tma_load_4d(st + kVTile, &maps.v[blockIdx.y], full, 0, hh, t, bb, policy);
+    };
+    int issued = min(count, kStages);
+    if (lane == 0)
+      for (int n = 0; n < issued; ++n) load(n);
+    Sum all = {0.0f, 0.0f};
+    float4 g = load_gates(p, b, h, chunk_of(0), lane);
+    for (int n = 0; n < count; ++n) {
+      const int s = n % kStages;
+      if (n >= kStages) {
+        if (!gwarp_wait(bar.freed + s, n / kStages - 1, abortf)) break;
+        if (lane == 0) load(n);
+        ++issued;
+      }
+      const float4 now = g;
+      if (n + 1 < count) g = load_gates(p, b, h, chunk_of(n + 1), lane);
+      all = add(all, chunk_gates(now, gates[s], a, lane));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.gates + s);
+    }
+    if (ONLY_STATE && lane == 0) a.decay[bh * p.spans + span] = exp2_of(all, Sum{0.0f, 0.0f});
+    if (lane == 0)   // every load must have landed before the CTA ends
+      for (int n = max(0, issued - kStages); n < issued; ++n)
+        drain_wait_on(bar.full + n % kStages, static_cast<uint32_t>((n / kStages) & 1), &g_gated_error);
+  } else if (warp == kIssuer) {
+    // ------------------------------------------------------------ MMAs
+    if (lane == 0) {
+      auto scores = [&](int n) {
+        constexpr uint32_t idesc = idesc_bf16_f32(128, kTcChunk, false, false);
+        const uint32_t q = smem_u32(smem + (n % kStages) * L::kStage), k = q + kKTile;
+#pragma unroll
+        for (int ks = 0; ks < DH / 16; ++ks)
+          mma_bf16(tmem + kScores + 128 * (n & 1), smem_desc(q + ks * 32, 16, kSbo, 2),
+                   smem_desc(k + ks * 32, 16, kSbo, 2), idesc, ks > 0);
+        mma_commit(bar.scores + (n & 1));
+      };
+      bool ok = true;
+      if (!ONLY_STATE) {
+        ok = gwait(bar.full, 0, abortf);
+        if (ok) scores(0);
+      }
+      for (int n = 0; ok && n < count; ++n) {
+        const int s = n % kStages;
+        uint8_t* st = smem + s * L::kStage;
+        const uint32_t v = smem_u32(st + kVTile);
+        if (!ONLY_STATE) {
+          // the scores' other buffer: P of the chunk before has been read
+          if (n > 0 && !gwait(&bar.out_done, n - 1, abortf)) break;
+          if (n + 1 < count) {
+            if (!gwait(bar.full + (n + 1) % kStages, (n + 1) / kStages, abortf)) break;
+            tc_fence_after();
+            scores(n + 1);
+          }
+          if (!gwait(&bar.s_ready, n, abortf)) break;
+          if (n > 0 && !gwait(&bar.out_read, n - 1, abortf)) break;
+          tc_fence_after();
+          constexpr uint32_t idesc = idesc_bf16_f32(128, DH, false, true);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int ks = 0; ks < DH / 16; ++ks)
+              mma_bf16(tmem + kO1, smem_desc(smem_u32(st) + ks * 32, 16, kSbo, 2),
+                       smem_desc(smem_u32(planes) + t * kStatePlane + ks * 2 * kSbo, kSbo, kSbo, 2), idesc, t + ks > 0);
+        } else if (!gwait(bar.full + s, n / kStages, abortf)) {
+          break;
+        }
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (!gwait(bar.k_ready + half, n, abortf)) { ok = false; break; }
+          tc_fence_after();
+          constexpr uint32_t idesc = idesc_bf16_f32(64, DH, true, true);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int t = 0; t < 3; ++t)
+              mma_bf16(tmem + kL, smem_desc(smem_u32(kp) + t * kPlane + (4 * half + ks) * 2 * kSbo, kSbo, kSbo, 2),
+                       smem_desc(v + (4 * half + ks) * 2 * kSbo, kSbo, kSbo, 2), idesc, half + ks + t > 0);
+        }
+        if (!ok) break;
+        mma_commit(&bar.l_done);
+        if (!ONLY_STATE) {
+          if (!gwait(bar.p_ready + (n & 1), n >> 1, abortf)) break;
+          tc_fence_after();
+          constexpr uint32_t idesc = idesc_bf16_f32(128, DH, false, true);
+          const uint32_t pt = tmem + kScores + 128 * (n & 1);
+#pragma unroll
+          for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int ks = 0; ks < 2; ++ks)
+                mma_bf16_ts(tmem + kO2, pt + 32 * cb + 16 * t + 8 * ks,
+                            smem_desc(v + (2 * cb + ks) * 2 * kSbo, kSbo, kSbo, 2), idesc, cb + t + ks > 0);
+          mma_commit(&bar.out_done);
+        }
+      }
+      mma_commit(&bar.fin);
+      drain_wait_on(&bar.fin, 0, &g_gated_error);
+    }
+  } else if (warp < kScoreWarps) {
+    // ------------------------------------------------------------ scores and outputs
+    if (!ONLY_STATE) {
+      const int q = warp & 3, half = warp >> 2, row = 32 * q + lane;
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q) << 16);
+      const int64_t slice = half;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + b * a.out.sb + h * a.out.sh + 32 * half;
+      const __nv_bfloat16* dot = static_cast<const __nv_bfloat16*>(a.dot.data) + b * a.dot.sb + h * a.dot.sh + 32 * half;
+
+      // P of chunk n: this warp's 32 rows, tokens 64 half ..
+      auto form_p = [&](int n) -> bool {
+        const int s = n % kStages;
+        if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + s, n / kStages, abortf)) return false;
+        const ChunkGates& w = gates[s];
+        // rows of v that are not finite (this warp looks at 32 of them, half a row a lane)
+        {
+          const uint8_t* v = smem + s * L::kStage + kVTile;
+          uint32_t bad = 0;
+#pragma unroll
+          for (int u = 0; u < DH / 16; ++u) {
+            const uint4 x = *reinterpret_cast<const uint4*>(v + unit_at(row, DH / 16 * half + u));
+            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 z =
+                  __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y[e]), __floats2bfloat162_rn(0.0f, 0.0f));
+              bad |= *reinterpret_cast<const uint32_t*>(&z);
+            }
+          }
+          if (bad & 0x7FFF7FFFu) *reinterpret_cast<volatile uint32_t*>(ctl.bad + (n & 3)) = n + 1;
+        }
+        if (!gwarp_wait(bar.scores + (n & 1), n >> 1, abortf)) return false;
+        tc_fence_after();
+        const float rw = w.row[row], bh0 = w.hi[row], bl0 = w.lo[row];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int cb = 2 * half + c;
+          const uint32_t at = lanes + kScores + 128 * (n & 1) + 32 * cb;
+          uint32_t t0[16], t1[16];
+          if (reverse ? cb < q : cb > q) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) t0[i] = t1[i] = 0u;
+          } else {
+            uint32_t x[32];
+            tmem_ld_x32(at, x);
+            tmem_ld_wait();
+            if (cb != q) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(w.col[q] + 32 * cb + j);
+                uint32_t t[2];
+                split<2>(__uint_as_float(x[j]) * (rw * f.x), __uint_as_float(x[j + 1]) * (rw * f.y), t);
+                t0[j / 2] = t[0];
+                t1[j / 2] = t[1];
+                split<2>(__uint_as_float(x[j + 2]) * (rw * f.z), __uint_as_float(x[j + 3]) * (rw * f.w), t);
+                t0[j / 2 + 1] = t[0];
+                t1[j / 2 + 1] = t[1];
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 hj = *reinterpret_cast<const float4*>(w.hi + 32 * cb + j);
+                const float4 lj = *reinterpret_cast<const float4*>(w.lo + 32 * cb + j);
+                const float d[4] = {(bh0 - hj.x) + (bl0 - lj.x), (bh0 - hj.y) + (bl0 - lj.y),
+                                    (bh0 - hj.z) + (bl0 - lj.z), (bh0 - hj.w) + (bl0 - lj.w)};
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const bool keep = reverse ? j + e >= lane : j + e <= lane;
+                  y[e] = keep ? __uint_as_float(x[j + e]) * (a.out_scale * exp2_fast(reverse ? -d[e] : d[e])) : 0.0f;
+                }
+                uint32_t t[2];
+                split<2>(y[0], y[1], t);
+                t0[j / 2] = t[0];
+                t1[j / 2] = t[1];
+                split<2>(y[2], y[3], t);
+                t0[j / 2 + 1] = t[0];
+                t1[j / 2 + 1] = t[1];
+              }
+            }
+          }
+          tmem_st_x16(at, t0);
+          tmem_st_x16(at + 16, t1);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.p_ready + (n & 1));
+        return true;
+      };
+
+      // Output rows of chunk n, columns 32 half ..
+      auto write_out = [&](int n) -> bool {
+        const int s = n % kStages;
+        const int64_t t = chunk_of(n) * kTcChunk + row;
+        const bool in = t < p.N;
+        const ChunkGates& w = gates[s];
+        if (!gwarp_wait(&bar.out_done, n, abortf)) return false;
+        tc_fence_after();
+        const float f = w.enter[q] * w.row[row];
+        const bool apart = *reinterpret_cast<volatile uint32_t*>(ctl.bad + (n & 3)) == static_cast<uint32_t>(n + 1);
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 32; c += 16) {
+          if (32 * half + c >= DH) continue;
+          uint32_t x[16], y[16];
+          tmem_ld_x16(lanes + kO1 + 32 * half + c, x);
+          tmem_ld_x16(lanes + kO2 + 32 * half + c, y);
+          tmem_ld_wait();
+          float o[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(y[e]);
+          if (apart)
+            row_apart<DH>(o, smem + s * L::kStage, w, a.out_scale, row, 32 * half + c, reverse);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = fmaf(f, __uint_as_float(x[e]), o[e]);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (!in || 32 * half + c + 8 * u >= p.d) continue;
+            if (a.dots) {
+              const uint4 r = *reinterpret_cast<const uint4*>(dot + t * a.dot.sn + c + 8 * u);
+              const uint32_t z[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                sum = fmaf(o[8 * u + 2 * e], low(z[e]), fmaf(o[8 * u + 2 * e + 1], high(z[e]), sum));
+            }
+            *reinterpret_cast<uint4*>(out + t * a.out.sn + c + 8 * u) =
+                make_uint4(pack(o[8 * u], o[8 * u + 1]), pack(o[8 * u + 2], o[8 * u + 3]),
+                           pack(o[8 * u + 4], o[8 * u + 5]), pack(o[8 * u + 6], o[8 * u + 7]));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar.out_read);
+          mbar_arrive(bar.freed + s);
+        }
+        if (a.dots && in && 32 * half < DH) a.dots[(slice * p.BH + bh) * p.N + t] = sum;
+        return true;
+      };
+
+      bool ok = form_p(0);
+      for (int n = 0; ok && n < count; ++n) {
+        if (n + 1 < count) ok = form_p(n + 1);
+        if (ok) ok = write_out(n);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ the state
+    const int q = warp & 3, hf = (warp - kScoreWarps) >> 2;
+    const int r0 = 16 * q + (lane >> 2), c0 = 32 * hf + 2 * (lane & 3);
+    const bool holds = 16 * q < DH && 32 * hf < DH;   // of the state
+    float S[16];
+    {
+      const float* in = !ONLY_STATE && a.init
+                            ? a.init + (bh * a.init_spans + (a.init_spans > 1 ? span : 0)) * p.d * p.d
+                            : nullptr;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int r = r0 + 8 * ((i >> 1) & 1), c = c0 + 8 * (i >> 2) + (i & 1);
+        S[i] = in && holds && r < p.d && c < p.d ? in[a.init_transposed ? c * p.d + r : r * p.d + c] : 0.0f;
+      }
+    }
+    auto publish = [&]() {
+      if (holds) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t t[2];
+            split<2>(S[4 * n + 2 * e], S[4 * n + 2 * e + 1], t);
+            uint8_t* at = planes + unit_at(r0 + 8 * e, 4 * hf + n) + 4 * (lane & 3);
+            *reinterpret_cast<uint32_t*>(at) = t[0];
+            *reinterpret_cast<uint32_t*>(at + kStatePlane) = t[1];
+          }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.s_ready);
+    };
+    if (!ONLY_STATE) publish();
+
+    // k's rows of this warp: 256 / DH... rows at once, eight channels a lane.  The score warps of a
+    // scheduler with fewer blocks of scores to form leave it more rows.
+    constexpr int kLanes = DH / 8, kRows = 32 / kLanes, kGroups = 64 / kRows;   // groups of rows a half chunk
+    const int load = ONLY_STATE ? 4 : reverse ? 3 - q : q;   // 0: lightest score work
+    // sixteenths of a half chunk per warp: 3 3 | 3 2 | 2 1 | 1 1 (or two each)
+    const int from16 = load == 4 ? 2 * (warp - kScoreWarps)
+                                 : load == 0 ? 3 * hf : load == 1 ? 6 + 3 * hf : load == 2 ? 11 + 2 * hf : 14 + hf;
+    const int many16 = load == 4 ? 2 : load == 0 ? 3 : load == 1 ? 3 - hf : load == 2 ? 2 - hf : 1;
+    const int g0 = from16 * kGroups / 16, g1 = (from16 + many16) * kGroups / 16;
+    const int kr = lane / kLanes, ku = lane % kLanes;
+    bool ok = true;
+    for (int n = 0; ok && n < count; ++n) {
+      const int s = n % kStages;
+      if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + s, n / kStages, abortf)) break;
+      const ChunkGates& w = gates[s];
+      const uint8_t* k = smem + s * L::kStage + kKTile;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll 2
+        for (int g = g0; g < g1; ++g) {
+          const int token = 64 * half + kRows * g + kr;
+          const int at = unit_at(token, ku);
+          const uint4 x = *reinterpret_cast<const uint4*>(k + at);
+          const float f = w.addw[token];
+          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+          uint32_t t[4][3];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split<3>(low(y[e]) * f, high(y[e]) * f, t[e]);
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            *reinterpret_cast<uint4*>(kp + i * kPlane + at) = make_uint4(t[0][i], t[1][i], t[2][i], t[3][i]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.k_ready + half);
+      }
+      const float total = w.total;
+      if (!gwarp_wait(&bar.l_done, n, abortf)) { ok = false; break; }
+      tc_fence_after();
+      if (holds) {
+        uint32_t l[16];
+        tmem_ld_16x32(tmem + (static_cast<uint32_t>(32 * q) << 16) + kL + 32 * hf, l);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[i] = fmaf(total, S[i], __uint_as_float(l[i]));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.freed + s);
+      if (!ONLY_STATE && n + 1 < count) publish();
+    }
+    float* to = ONLY_STATE ? a.local + (bh * p.spans + span) * p.d * p.d
+                           : a.last && span == (reverse ? 0 : p.spans - 1) ? a.last + bh * p.d * p.d : nullptr;
+    if (to && holds) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int r = r0 + 8 * ((i >> 1) & 1), c = c0 + 8 * (i >> 2) + (i & 1);
+        if (r < p.d && c < p.d) to[r * p.d + c] = S[i];
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, kTmemColumns);
+}
+
+bool operand_map(const ScanSet& set, int64_t B, const Operand& o, CUtensorMap* m) {
+  const int64_t lim = int64_t{1} << 39;   // strides in bytes below 2^40
+  const int64_t sh = set.H > 1 ? o.sh : set.d, sn = set.N > 1 ? o.sn : set.d, sb = B > 1 ? o.sb : set.d;
+  if (sh <= 0 || sn <= 0 || sb <= 0 || sh >= lim || sn >= lim || sb >= lim) return false;   // a shared row: no map
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(set.d), static_cast<cuuint64_t>(set.H),
+                              static_cast<cuuint64_t>(set.N), static_cast<cuuint64_t>(B)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(sh * 2), static_cast<cuuint64_t>(sn * 2),
+                                 static_cast<cuuint64_t>(sb * 2)};
+  const cuuint32_t box[4] = {64u, 1u, static_cast<cuuint32_t>(kTcChunk), 1u};
+  return encode_tensor_map(m, 4, o.data, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int DH, bool ONLY_STATE>
+int launch(const ScanSet& set, const TcMaps& maps, int scans, cudaStream_t s) {
+  constexpr int kBytes = static_cast<int>(Layout<ONLY_STATE>::kBytes);
+  // a per-device setting: made on every call, for whichever device is current
+  if (cudaFuncSetAttribute(gated_tc_scan<DH, ONLY_STATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) !=
+      cudaSuccess)
+    return MHLA_ERR_CUDA;
+  const unsigned grid = static_cast<unsigned>(set.BH * (ONLY_STATE ? set.spans - 1 : set.spans));
+  KernelTimer timer(ONLY_STATE ? "gated_tc_span_state" : "gated_tc_scan", s);
+  gated_tc_scan<DH, ONLY_STATE><<<dim3(grid, scans), kThreads, kBytes, s>>>(set, maps);
+  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+}
+
+}  // namespace
+
+bool tc_supported(const GatedProblem& p) {
+  return p.dtype == MHLA_BF16 && p.d <= 64 && p.d % 8 == 0 && p.N < (int64_t{1} << 31) - kTcChunk;
+}
+
+// One CTA an SM: as many spans as fill the SMs once, none shorter than two chunks.
+Cut tc_cut(const GatedProblem& p, int scans) {
+  Cut c;
+  c.chunks = (p.N + kTcChunk - 1) / kTcChunk;
+  const int64_t spans = std::max<int64_t>(1, kSms / (p.B * p.H * scans));
+  c.span_chunks = std::max<int64_t>(2, (c.chunks + spans - 1) / spans);
+  c.spans = (c.chunks + c.span_chunks - 1) / c.span_chunks;
+  return c;
+}
+
+bool tc_maps(const GatedProblem& p, const ScanSet& set, int scans, TcMaps* maps) {
+  ScanSet sizes = {};
+  sizes.N = p.N; sizes.H = p.H; sizes.d = p.d;
+  for (int i = 0; i < scans; ++i)
+    if (!operand_map(sizes, p.B, set.scan[i].q, &maps->q[i]) || !operand_map(sizes, p.B, set.scan[i].k, &maps->k[i]) ||
+        !operand_map(sizes, p.B, set.scan[i].v, &maps->v[i]))
+      return false;
+  return true;
+}
+
+int launch_tc_scan(const ScanSet& set, const TcMaps& maps, int scans, bool span_state, cudaStream_t s) {
+  if (set.d <= 32) return span_state ? launch<32, true>(set, maps, scans, s) : launch<32, false>(set, maps, scans, s);
+  return span_state ? launch<64, true>(set, maps, scans, s) : launch<64, false>(set, maps, scans, s);
+}
+
+}  // namespace gated
+
+int read_and_clear_gated_error(void* stream, uint32_t* flags) { return tc::read_and_clear_word(g_gated_error, stream, flags); }
+
+MHLA_DEFINE_STALL_SETTER(set_stall_gated)
+
+}  // namespace mhla

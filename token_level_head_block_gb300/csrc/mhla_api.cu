@@ -453,17 +453,18 @@ extern "C" mhla_status_t mhla_forward_causal(const mhla_tensor_t* q, const mhla_
 
 extern "C" mhla_status_t mhla_device_status(void* stream, uint32_t* flags) {
   if (!flags) return MHLA_ERR_INVALID_ARG;
-  uint32_t tc = 0, small = 0, bwd = 0, causal = 0, module = 0, gemm = 0;
+  uint32_t tc = 0, small = 0, bwd = 0, causal = 0, module = 0, gemm = 0, gated = 0;
   const int a = read_and_clear_device_error(stream, &tc);
   const int b = read_and_clear_small_error(stream, &small);
   const int c = read_and_clear_bwd_error(stream, &bwd);
   const int e = read_and_clear_causal_error(stream, &causal);
   const int f = read_and_clear_module_error(stream, &module);
   const int g = read_and_clear_gemm_error(stream, &gemm);
+  const int r = read_and_clear_gated_error(stream, &gated);
   if (a == MHLA_ERR_CUDA || b == MHLA_ERR_CUDA || c == MHLA_ERR_CUDA || e == MHLA_ERR_CUDA || f == MHLA_ERR_CUDA ||
-      g == MHLA_ERR_CUDA)
+      g == MHLA_ERR_CUDA || r == MHLA_ERR_CUDA)
     return MHLA_ERR_CUDA;
-  *flags = tc | small | bwd | causal | module | gemm;
+  *flags = tc | small | bwd | causal | module | gemm | gated;
   return *flags ? MHLA_ERR_TIMEOUT : MHLA_OK;
 }
 
@@ -474,7 +475,8 @@ extern "C" mhla_status_t mhla_debug_stall_waits(int32_t warp, uint64_t limit_ns)
   const uint64_t ns = warp < 0 ? 0 : limit_ns;
   int (*const setters[])(uint32_t, uint64_t) = {set_stall_summary, set_stall_mix, set_stall_output,
                                                 set_stall_fused,   set_stall_small, set_stall_bwd,
-                                                set_stall_causal,  set_stall_module, set_stall_gemm};
+                                                set_stall_causal,  set_stall_module, set_stall_gemm,
+                                                set_stall_gated};
   for (auto set : setters)
     if (set(w, ns) != MHLA_OK) return MHLA_ERR_CUDA;
   return MHLA_OK;

@@ -187,6 +187,7 @@ int set_stall_bwd(uint32_t warp_plus_1, uint64_t ns);
 int set_stall_causal(uint32_t warp_plus_1, uint64_t ns);
 int set_stall_module(uint32_t warp_plus_1, uint64_t ns);
 int set_stall_gemm(uint32_t warp_plus_1, uint64_t ns);
+int set_stall_gated(uint32_t warp_plus_1, uint64_t ns);
 
 // Brackets one kernel launch with CUDA events on its stream while
 // mhla_profile_begin/end collection is active, and always with an NVTX range
@@ -259,6 +260,7 @@ int launch_gated_forward(const GatedProblem& p, const float* state_in, const Ope
                          void* workspace, void* stream);
 int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* workspace, void* stream);
 int launch_gated_step(const GatedProblem& p, float* state, const Operand& out, void* stream);
+int read_and_clear_gated_error(void* stream, uint32_t* flags);
 
 // Norm and rotation of query and key heads (qk_norm_kernels.cu).
 struct QkNormProblem {
