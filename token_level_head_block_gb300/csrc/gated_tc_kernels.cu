@@ -14,8 +14,8 @@
 // instructions of the warps, which leaves them the splitting into terms: that work
 // bounds the kernel, so sixteen warps share it.  Eight (score warps) turn S1 into P and
 // write the outputs, one chunk apart, so that PV of one chunk runs under P of
-// the next; eight (state warps) scale and split k and carry the state; one warp issues the MMAs, one
-// loads (TMA, three stages) and prepares the gates.  A thread of a score warp owns a row, so a
+// the next; eight (state warps) scale and split k and carry the state; two warps issue the MMAs,
+// one loads (TMA, three stages) and prepares the gates.  A thread of a score warp owns a row, so a
 // row's factor is a register and the columns' factors are read by broadcast.
 //
 // Every wait is bounded; one that gives up sets bit 0 of this file's error
@@ -43,7 +43,7 @@ namespace {
 using namespace tc;
 
 constexpr int kScoreWarps = 8, kStateWarps = 8;
-constexpr int kIssuer = kScoreWarps + kStateWarps, kLoader = kIssuer + 1;
+constexpr int kIssuer = kScoreWarps + kStateWarps, kAdder = kIssuer + 1, kLoader = kIssuer + 2;
 constexpr int kThreads = 32 * (kLoader + 1);
 constexpr int kStages = 3;
 constexpr int kTileBytes = kTcChunk * 128;   // 128 rows of 64 channels, 128-byte swizzle
@@ -61,17 +61,18 @@ constexpr uint32_t kTmemColumns = 512;
 struct ChunkGates {
   float hi[kTcChunk], lo[kTcChunk];   // b_i
   float row[kTcChunk];                // e^{b_i - m}
-  float col[4][kTcChunk];             // out_scale e^{m - b_j}, per block of rows
+  float col[4][kTcChunk];             // out_scale e^{m - b_j}, per block of rows (its own tokens too)
   float addw[kTcChunk];               // k_scale e^{B - b_j}
   float enter[4];                     // state_scale e^m
   float total;                        // e^B
-  float pad[3];
+  uint32_t steep;                     // bit of a block: e^{m - b_j} of its own tokens may be large
+  float pad[2];
 };
 
 struct Bars {
   uint64_t full[kStages], gates[kStages], freed[kStages];
   uint64_t scores[2], p_ready[2];
-  uint64_t out_done, out_read, k_ready[2], l_done, s_ready, fin;
+  uint64_t state_read, out_done, out_read, k_ready[2], l_done, s_ready, fin[2];
 };
 
 struct Control {
@@ -92,11 +93,18 @@ struct Layout {
 };
 static_assert(Layout<false>::kBytes <= 227 * 1024, "shared memory of one CTA");
 
-__device__ __forceinline__ bool gwait(uint64_t* bar, uint32_t parity, volatile uint32_t* abortf) {
-  return wait_bounded_on(bar, parity & 1u, abortf, &g_gated_error);
-}
+// Every lane waits, then the warp agrees; the first look is in place.
 __device__ __forceinline__ bool gwarp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abortf) {
-  return warp_wait_on(bar, parity & 1u, abortf, &g_gated_error);
+  bool ok = mbar_try_wait(bar, parity & 1u);
+  if (!ok) ok = wait_bounded_on(bar, parity & 1u, abortf, &g_gated_error);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// One lane of the warp, the same one for as long as all take part.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 // D (+)= A[tensor memory] B[shared memory].
@@ -109,13 +117,10 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, 
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -197,7 +202,7 @@ __device__ __forceinline__ Sum chunk_gates(float4 g, ChunkGates& out, const Scan
   put(out.addw, addw);
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    if (reverse ? block <= r : block >= r) continue;   // tokens the rows of block r do not see through m
+    if (reverse ? block < r : block > r) continue;   // tokens the rows of block r do not see
     const Sum e = reverse ? edge[r + 1] : edge[r];
     float c[4];
 #pragma unroll
@@ -205,39 +210,69 @@ __device__ __forceinline__ Sum chunk_gates(float4 g, ChunkGates& out, const Scan
     put(out.col[r], c);
   }
   if ((lane & 7) == 0) out.enter[block] = a.state_scale * (reverse ? exp2_of(all, m) : exp2_of(m, none));
-  if (lane == 0) out.total = exp2_of(all, none);
+  // beyond 2^24 within a block its own scores take each difference by itself
+  bool far = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) far = far || !(fabsf((at[e].hi - m.hi) + (at[e].lo - m.lo)) <= 24.0f);
+  const uint32_t lanes = __ballot_sync(~0u, far);
+  if (lane == 0) {
+    out.total = exp2_of(all, none);
+    uint32_t steep = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) steep |= (lanes >> (8 * r) & 0xFFu) ? 1u << r : 0u;
+    out.steep = steep;
+  }
   return all;
 }
 
-// The outputs' second part of one row without the tensor core, for a chunk whose v
-// holds an infinity or NaN: 0 times it must not reach rows that do not see it.
+// 16 outputs of one row without the tensor core's P V, for a chunk whose v holds an
+// infinity or NaN: 0 times it must not reach rows that do not see it.  x: what the row
+// reads from the state, f: its factor.  Returns the row's share of dot . o.
 template <int DH>
-__device__ __noinline__ void row_apart(float (&o)[16], const uint8_t* stage, const ChunkGates& w, float out_scale,
-                                       int row, int c0, bool reverse) {
+__device__ __noinline__ float row_apart(const uint32_t (&x)[16], float f, const uint8_t* stage, const ChunkGates& w,
+                                        float out_scale, int row, int c0, bool reverse, __nv_bfloat16* out,
+                                        const __nv_bfloat16* dot, int width) {
+  float o[16];
 #pragma unroll
   for (int c = 0; c < 16; ++c) o[c] = 0.0f;
   const uint8_t *q = stage, *k = stage + kTileBytes, *v = stage + 2 * kTileBytes;
   const int j0 = reverse ? row : 0, j1 = reverse ? kTcChunk : row + 1;
+#pragma unroll 1
   for (int j = j0; j < j1; ++j) {
     float s = 0.0f;
+#pragma unroll 1
     for (int u = 0; u < DH / 8; ++u) {
       const uint4 a = *reinterpret_cast<const uint4*>(q + unit_at(row, u));
       const uint4 b = *reinterpret_cast<const uint4*>(k + unit_at(j, u));
-      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+      const uint32_t y[4] = {a.x, a.y, a.z, a.w}, z[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s = fmaf(low(x[e]), low(y[e]), fmaf(high(x[e]), high(y[e]), s));
+      for (int e = 0; e < 4; ++e) s = fmaf(low(y[e]), low(z[e]), fmaf(high(y[e]), high(z[e]), s));
     }
-    const float x = (w.hi[row] - w.hi[j]) + (w.lo[row] - w.lo[j]);
-    s *= out_scale * exp2_fast(reverse ? -x : x);
-    for (int u = 0; u < 2; ++u) {
-      const uint4 a = *reinterpret_cast<const uint4*>(v + unit_at(j, c0 / 8 + u));
-      const uint32_t y[4] = {a.x, a.y, a.z, a.w};
+    const float d = (w.hi[row] - w.hi[j]) + (w.lo[row] - w.lo[j]);
+    s *= out_scale * exp2_fast(reverse ? -d : d);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        o[8 * u + 2 * e] = fmaf(s, low(y[e]), o[8 * u + 2 * e]);
-        o[8 * u + 2 * e + 1] = fmaf(s, high(y[e]), o[8 * u + 2 * e + 1]);
-      }
-    }
+    for (int c = 0; c < 16; ++c)
+      o[c] = fmaf(s, to_f(*reinterpret_cast<const __nv_bfloat16*>(v + unit_at(j, (c0 + c) / 8) + 2 * (c & 7))), o[c]);
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    if (c >= width) continue;
+    o[c] = fmaf(f, __uint_as_float(x[c]), o[c]);
+    out[c] = __float2bfloat16_rn(o[c]);
+    if (dot) sum = fmaf(o[c], to_f(dot[c]), sum);
+  }
+  return sum;
+}
+
+// 16 scores of a row in its own block times their decays, each difference by itself.
+__device__ __noinline__ void steep_block(uint32_t (&x)[16], const ChunkGates& w, float out_scale, int row, int j0,
+                                         bool reverse) {
+  const float hi = w.hi[row], lo = w.lo[row];
+#pragma unroll 4
+  for (int j = 0; j < 16; ++j) {
+    const float d = (hi - w.hi[j0 + j]) + (lo - w.lo[j0 + j]);
+    x[j] = __float_as_uint(__uint_as_float(x[j]) * (out_scale * exp2_fast(reverse ? -d : d)));
   }
 }
 
@@ -278,11 +313,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar.p_ready + s, kScoreWarps);
       mbar_init(bar.k_ready + s, kStateWarps);
     }
+    mbar_init(&bar.state_read, 1);
     mbar_init(&bar.out_done, 1);
     mbar_init(&bar.out_read, kScoreWarps);
     mbar_init(&bar.l_done, 1);
     mbar_init(&bar.s_ready, kStateWarps);
-    mbar_init(&bar.fin, 1);
+    mbar_init(bar.fin, 1);
+    mbar_init(bar.fin + 1, 1);
     ctl.abort = 0u;
     for (int i = 0; i < 4; ++i) ctl.bad[i] = 0u;
     fence_mbar_init();
@@ -332,90 +369,113 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = max(0, issued - kStages); n < issued; ++n)
         drain_wait_on(bar.full + n % kStages, static_cast<uint32_t>((n / kStages) & 1), &g_gated_error);
   } else if (warp == kIssuer) {
-    // ------------------------------------------------------------ MMAs
-    if (lane == 0) {
+    // ------------------------------------------------------------ scores and outputs: MMAs
+    if (!ONLY_STATE) {
+      const bool leader = elect_one();
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, kTcChunk, false, false);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(128, DH, false, true);
+      const uint64_t stage0 = smem_desc(smem_u32(smem), 16, kSbo, 2);           // K-major: q, k
+      const uint64_t v0 = smem_desc(smem_u32(smem + kVTile), kSbo, kSbo, 2);    // MN-major: v
+      const uint64_t state0 = smem_desc(smem_u32(planes), kSbo, kSbo, 2);
       auto scores = [&](int n) {
-        constexpr uint32_t idesc = idesc_bf16_f32(128, kTcChunk, false, false);
-        const uint32_t q = smem_u32(smem + (n % kStages) * L::kStage), k = q + kKTile;
+        const uint64_t q = stage0 + (n % kStages) * (L::kStage >> 4), k = q + (kKTile >> 4);
+        const uint32_t d = tmem + kScores + 128 * (n & 1);
+        if (leader) {
 #pragma unroll
-        for (int ks = 0; ks < DH / 16; ++ks)
-          mma_bf16(tmem + kScores + 128 * (n & 1), smem_desc(q + ks * 32, 16, kSbo, 2),
-                   smem_desc(k + ks * 32, 16, kSbo, 2), idesc, ks > 0);
-        mma_commit(bar.scores + (n & 1));
+          for (int ks = 0; ks < DH / 16; ++ks) mma_bf16(d, q + 2 * ks, k + 2 * ks, idesc_s, ks > 0);
+          mma_commit(bar.scores + (n & 1));
+        }
+        __syncwarp();
       };
-      bool ok = true;
-      if (!ONLY_STATE) {
-        ok = gwait(bar.full, 0, abortf);
-        if (ok) scores(0);
-      }
+      bool ok = gwarp_wait(bar.full, 0, abortf);
+      if (ok) scores(0);
       for (int n = 0; ok && n < count; ++n) {
         const int s = n % kStages;
-        uint8_t* st = smem + s * L::kStage;
-        const uint32_t v = smem_u32(st + kVTile);
-        if (!ONLY_STATE) {
-          // the scores' other buffer: P of the chunk before has been read
-          if (n > 0 && !gwait(&bar.out_done, n - 1, abortf)) break;
-          if (n + 1 < count) {
-            if (!gwait(bar.full + (n + 1) % kStages, (n + 1) / kStages, abortf)) break;
-            tc_fence_after();
-            scores(n + 1);
-          }
-          if (!gwait(&bar.s_ready, n, abortf)) break;
-          if (n > 0 && !gwait(&bar.out_read, n - 1, abortf)) break;
+        // the scores' other buffer: P of the chunk before has been read
+        if (n > 0 && !gwarp_wait(&bar.out_done, n - 1, abortf)) break;
+        if (n + 1 < count) {
+          if (!gwarp_wait(bar.full + (n + 1) % kStages, (n + 1) / kStages, abortf)) break;
           tc_fence_after();
-          constexpr uint32_t idesc = idesc_bf16_f32(128, DH, false, true);
+          scores(n + 1);
+        }
+        if (!gwarp_wait(&bar.s_ready, n, abortf)) break;
+        if (n > 0 && !gwarp_wait(&bar.out_read, n - 1, abortf)) break;
+        tc_fence_after();
+        const uint64_t q = stage0 + s * (L::kStage >> 4), v = v0 + s * (L::kStage >> 4);
+        if (leader) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int ks = 0; ks < DH / 16; ++ks)
-              mma_bf16(tmem + kO1, smem_desc(smem_u32(st) + ks * 32, 16, kSbo, 2),
-                       smem_desc(smem_u32(planes) + t * kStatePlane + ks * 2 * kSbo, kSbo, kSbo, 2), idesc, t + ks > 0);
-        } else if (!gwait(bar.full + s, n / kStages, abortf)) {
-          break;
+              mma_bf16(tmem + kO1, q + 2 * ks, state0 + (t * kStatePlane + ks * 2 * kSbo) / 16, idesc_o, t + ks > 0);
+          mma_commit(&bar.state_read);
         }
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (!gwait(bar.k_ready + half, n, abortf)) { ok = false; break; }
-          tc_fence_after();
-          constexpr uint32_t idesc = idesc_bf16_f32(64, DH, true, true);
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-            for (int t = 0; t < 3; ++t)
-              mma_bf16(tmem + kL, smem_desc(smem_u32(kp) + t * kPlane + (4 * half + ks) * 2 * kSbo, kSbo, kSbo, 2),
-                       smem_desc(v + (4 * half + ks) * 2 * kSbo, kSbo, kSbo, 2), idesc, half + ks + t > 0);
-        }
-        if (!ok) break;
-        mma_commit(&bar.l_done);
-        if (!ONLY_STATE) {
-          if (!gwait(bar.p_ready + (n & 1), n >> 1, abortf)) break;
-          tc_fence_after();
-          constexpr uint32_t idesc = idesc_bf16_f32(128, DH, false, true);
-          const uint32_t pt = tmem + kScores + 128 * (n & 1);
+        __syncwarp();
+        if (!gwarp_wait(bar.p_ready + (n & 1), n >> 1, abortf)) break;
+        tc_fence_after();
+        const uint32_t pt = tmem + kScores + 128 * (n & 1);
+        if (leader) {
 #pragma unroll
           for (int cb = 0; cb < 4; ++cb)
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int ks = 0; ks < 2; ++ks)
-                mma_bf16_ts(tmem + kO2, pt + 32 * cb + 16 * t + 8 * ks,
-                            smem_desc(v + (2 * cb + ks) * 2 * kSbo, kSbo, kSbo, 2), idesc, cb + t + ks > 0);
+                mma_bf16_ts(tmem + kO2, pt + 32 * cb + 16 * t + 8 * ks, v + (2 * cb + ks) * 2 * kSbo / 16, idesc_o,
+                            cb + t + ks > 0);
           mma_commit(&bar.out_done);
         }
+        __syncwarp();
       }
-      mma_commit(&bar.fin);
-      drain_wait_on(&bar.fin, 0, &g_gated_error);
+      if (leader) {
+        mma_commit(bar.fin);
+        drain_wait_on(bar.fin, 0, &g_gated_error);
+      }
+      __syncwarp();
     }
+  } else if (warp == kAdder) {
+    // ------------------------------------------------------------ what the state gains: MMAs
+    const bool leader = elect_one();
+    constexpr uint32_t idesc = idesc_bf16_f32(64, DH, true, true);
+    const uint64_t v0 = smem_desc(smem_u32(smem + kVTile), kSbo, kSbo, 2), k0 = smem_desc(smem_u32(kp), kSbo, kSbo, 2);
+    bool ok = true;
+    for (int n = 0; ok && n < count; ++n) {
+      const int s = n % kStages;
+      if (!gwarp_wait(bar.full + s, n / kStages, abortf)) break;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        if (!gwarp_wait(bar.k_ready + half, n, abortf)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t k = k0 + half * (4 * 2 * kSbo / 16), v = v0 + s * (L::kStage >> 4) + half * (4 * 2 * kSbo / 16);
+        if (leader) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int t = 0; t < 3; ++t)
+              mma_bf16(tmem + kL, k + (t * kPlane + ks * 2 * kSbo) / 16, v + ks * 2 * kSbo / 16, idesc,
+                       half + ks + t > 0);
+          if (half) mma_commit(&bar.l_done);
+        }
+        __syncwarp();
+      }
+    }
+    if (leader) {
+      mma_commit(bar.fin + 1);
+      drain_wait_on(bar.fin + 1, 0, &g_gated_error);
+    }
+    __syncwarp();
   } else if (warp < kScoreWarps) {
     // ------------------------------------------------------------ scores and outputs
     if (!ONLY_STATE) {
       const int q = warp & 3, half = warp >> 2, row = 32 * q + lane;
       const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q) << 16);
       const int64_t slice = half;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + b * a.out.sb + h * a.out.sh + 32 * half;
-      const __nv_bfloat16* dot = static_cast<const __nv_bfloat16*>(a.dot.data) + b * a.dot.sb + h * a.dot.sh + 32 * half;
+      uint32_t kept[16];   // scores of a block's second half
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + b * a.out.sb + h * a.out.sh;
+      const __nv_bfloat16* dot = static_cast<const __nv_bfloat16*>(a.dot.data) + b * a.dot.sb + h * a.dot.sh;
 
-      // P of chunk n: this warp's 32 rows, tokens 64 half ..
+      // P of chunk n: this warp's 32 rows, tokens 64 half .., 16 tokens a round.  A row's
+      // factor e^{b_i - m} waits for the outputs, except where the row's block is steep.
       auto form_p = [&](int n) -> bool {
         const int s = n % kStages;
         if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + s, n / kStages, abortf)) return false;
@@ -437,58 +497,75 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (bad & 0x7FFF7FFFu) *reinterpret_cast<volatile uint32_t*>(ctl.bad + (n & 3)) = n + 1;
         }
+        const bool steep = w.steep >> q & 1;
         if (!gwarp_wait(bar.scores + (n & 1), n >> 1, abortf)) return false;
         tc_fence_after();
-        const float rw = w.row[row], bh0 = w.hi[row], bl0 = w.lo[row];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int cb = 2 * half + c;
-          const uint32_t at = lanes + kScores + 128 * (n & 1) + 32 * cb;
-          uint32_t t0[16], t1[16];
+#pragma unroll 1
+        for (int c = 4 * half; c < 4 * half + 4; ++c) {   // 16 tokens
+          const int cb = c >> 1;
+          const uint32_t buffer = lanes + kScores + 128 * (n & 1) + 32 * cb;
+          uint32_t t0[8], t1[8];
+          uint32_t x[16];
+          // both halves of a block are read before either is written over
           if (reverse ? cb < q : cb > q) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) t0[i] = t1[i] = 0u;
+            for (int i = 0; i < 8; ++i) t0[i] = t1[i] = 0u;
           } else {
-            uint32_t x[32];
-            tmem_ld_x32(at, x);
-            tmem_ld_wait();
-            if (cb != q) {
+            if ((c & 1) == 0) {
+              tmem_ld_x16(buffer + 16, x);
+              tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(w.col[q] + 32 * cb + j);
-                uint32_t t[2];
-                split<2>(__uint_as_float(x[j]) * (rw * f.x), __uint_as_float(x[j + 1]) * (rw * f.y), t);
-                t0[j / 2] = t[0];
-                t1[j / 2] = t[1];
-                split<2>(__uint_as_float(x[j + 2]) * (rw * f.z), __uint_as_float(x[j + 3]) * (rw * f.w), t);
-                t0[j / 2 + 1] = t[0];
-                t1[j / 2 + 1] = t[1];
-              }
+              for (int i = 0; i < 16; ++i) kept[i] = x[i];
+              tmem_ld_x16(buffer, x);
+              tmem_ld_wait();
             } else {
 #pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 hj = *reinterpret_cast<const float4*>(w.hi + 32 * cb + j);
-                const float4 lj = *reinterpret_cast<const float4*>(w.lo + 32 * cb + j);
-                const float d[4] = {(bh0 - hj.x) + (bl0 - lj.x), (bh0 - hj.y) + (bl0 - lj.y),
-                                    (bh0 - hj.z) + (bl0 - lj.z), (bh0 - hj.w) + (bl0 - lj.w)};
-                float y[4];
+              for (int i = 0; i < 16; ++i) x[i] = kept[i];
+            }
+            const int j0 = 16 * c;
+            if (cb == q && steep) {
+              uint32_t z[16];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const bool keep = reverse ? j + e >= lane : j + e <= lane;
-                  y[e] = keep ? __uint_as_float(x[j + e]) * (a.out_scale * exp2_fast(reverse ? -d[e] : d[e])) : 0.0f;
-                }
-                uint32_t t[2];
-                split<2>(y[0], y[1], t);
-                t0[j / 2] = t[0];
-                t1[j / 2] = t[1];
-                split<2>(y[2], y[3], t);
-                t0[j / 2 + 1] = t[0];
-                t1[j / 2 + 1] = t[1];
+              for (int i = 0; i < 16; ++i) z[i] = x[i];
+              steep_block(z, w, a.out_scale, row, j0, reverse);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[i] = z[i];
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(w.col[q] + j0 + j);
+                x[j] = __float_as_uint(__uint_as_float(x[j]) * f.x);
+                x[j + 1] = __float_as_uint(__uint_as_float(x[j + 1]) * f.y);
+                x[j + 2] = __float_as_uint(__uint_as_float(x[j + 2]) * f.z);
+                x[j + 3] = __float_as_uint(__uint_as_float(x[j + 3]) * f.w);
+              }
+              if (steep) {
+                const float rw = w.row[row];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * rw);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              uint32_t t[2];
+              split<2>(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), t);
+              t0[i] = t[0];
+              t1[i] = t[1];
+            }
+            if (cb == q) {   // tokens the row does not see: their bits cleared, whatever they hold
+              const int seen = reverse ? row - j0 : row - j0 + 1;   // forwards tokens below it, backwards those from it
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int k = min(max(seen - 2 * i, 0), 2);
+                uint32_t keep = k == 2 ? 0xFFFFFFFFu : k == 1 ? 0xFFFFu : 0u;
+                if (reverse) keep = ~keep;
+                t0[i] &= keep;
+                t1[i] &= keep;
               }
             }
           }
-          tmem_st_x16(at, t0);
-          tmem_st_x16(at + 16, t1);
+          tmem_st_x8(buffer + 8 * (c & 1), t0);
+          tmem_st_x8(buffer + 16 + 8 * (c & 1), t1);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -497,53 +574,80 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
 
-      // Output rows of chunk n, columns 32 half ..
+      // Output rows of chunk n, columns 32 half ..: through this warp's 2 KB of the q tile
+      // (32 rows of 64 bytes), which nothing reads any more, so that eight rows go out at once.
+      auto staged = [&](uint8_t* base, int r, int u) {
+        return reinterpret_cast<uint4*>(base + 64 * r + ((u ^ (r >> 1 & 3)) << 4));
+      };
       auto write_out = [&](int n) -> bool {
-        const int s = n % kStages;
-        const int64_t t = chunk_of(n) * kTcChunk + row;
-        const bool in = t < p.N;
+        const int s = n % kStages, part_row = lane >> 2, part = lane & 3;
+        const int64_t t0 = chunk_of(n) * kTcChunk + 32 * q;
+        const int rows = static_cast<int>(min(p.N - t0, static_cast<int64_t>(32)));   // in the sequence
+        const bool part_in = 32 * half + 8 * part < p.d;
+        uint4 z[4];
+        if (a.dots) {
+          const __nv_bfloat16* x = dot + (t0 + part_row) * a.dot.sn + 32 * half + 8 * part;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            z[i] = part_in && part_row + 8 * i < rows ? *reinterpret_cast<const uint4*>(x + 8 * i * a.dot.sn)
+                                                      : make_uint4(0u, 0u, 0u, 0u);
+        }
         const ChunkGates& w = gates[s];
         if (!gwarp_wait(&bar.out_done, n, abortf)) return false;
         tc_fence_after();
-        const float f = w.enter[q] * w.row[row];
         const bool apart = *reinterpret_cast<volatile uint32_t*>(ctl.bad + (n & 3)) == static_cast<uint32_t>(n + 1);
+        const bool steep = w.steep >> q & 1;
+        // o = f2 (f1 O1 + O2)
+        const float f1 = steep ? w.enter[q] * w.row[row] : w.enter[q], f2 = steep ? 1.0f : w.row[row];
         float sum = 0.0f;
+        uint8_t* mine = smem + s * L::kStage + 4096 * q + 2048 * half;
+        if (a.dots && !apart) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 16) {
-          if (32 * half + c >= DH) continue;
+          for (int i = 0; i < 4; ++i) *staged(mine, part_row + 8 * i, part) = z[i];
+          __syncwarp();
+        }
+#pragma unroll 1
+        for (int c = 32 * half; c < min(32 * half + 32, DH); c += 16) {
           uint32_t x[16], y[16];
-          tmem_ld_x16(lanes + kO1 + 32 * half + c, x);
-          tmem_ld_x16(lanes + kO2 + 32 * half + c, y);
+          tmem_ld_x16(lanes + kO1 + c, x);
+          tmem_ld_x16(lanes + kO2 + c, y);
           tmem_ld_wait();
-          float o[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(y[e]);
-          if (apart)
-            row_apart<DH>(o, smem + s * L::kStage, w, a.out_scale, row, 32 * half + c, reverse);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = fmaf(f, __uint_as_float(x[e]), o[e]);
+          if (apart) {
+            if (lane < rows)
+              sum += row_apart<DH>(x, f1 * f2, smem + s * L::kStage, w, a.out_scale, row, c, reverse,
+                                   out + (t0 + lane) * a.out.sn + c, a.dots ? dot + (t0 + lane) * a.dot.sn + c : nullptr,
+                                   p.d - c);
+            continue;
+          }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            if (!in || 32 * half + c + 8 * u >= p.d) continue;
-            if (a.dots) {
-              const uint4 r = *reinterpret_cast<const uint4*>(dot + t * a.dot.sn + c + 8 * u);
-              const uint32_t z[4] = {r.x, r.y, r.z, r.w};
+            float o[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                sum = fmaf(o[8 * u + 2 * e], low(z[e]), fmaf(o[8 * u + 2 * e + 1], high(z[e]), sum));
+            for (int e = 0; e < 8; ++e)
+              o[e] = f2 * fmaf(f1, __uint_as_float(x[8 * u + e]), __uint_as_float(y[8 * u + e]));
+            uint4* at = staged(mine, lane, (c & 31) / 8 + u);
+            if (a.dots) {
+              const uint4 r = *at;
+              const uint32_t zz[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sum = fmaf(o[2 * e], low(zz[e]), fmaf(o[2 * e + 1], high(zz[e]), sum));
             }
-            *reinterpret_cast<uint4*>(out + t * a.out.sn + c + 8 * u) =
-                make_uint4(pack(o[8 * u], o[8 * u + 1]), pack(o[8 * u + 2], o[8 * u + 3]),
-                           pack(o[8 * u + 4], o[8 * u + 5]), pack(o[8 * u + 6], o[8 * u + 7]));
+            *at = make_uint4(pack(o[0], o[1]), pack(o[2], o[3]), pack(o[4], o[5]), pack(o[6], o[7]));
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bar.out_read);
-          mbar_arrive(bar.freed + s);
+        if (lane == 0) mbar_arrive(&bar.out_read);
+        if (!apart && 32 * half < DH) {
+          __nv_bfloat16* to = out + (t0 + part_row) * a.out.sn + 32 * half + 8 * part;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (part_in && part_row + 8 * i < rows)
+              *reinterpret_cast<uint4*>(to + 8 * i * a.out.sn) = *staged(mine, part_row + 8 * i, part);
+          __syncwarp();
         }
-        if (a.dots && in && 32 * half < DH) a.dots[(slice * p.BH + bh) * p.N + t] = sum;
+        if (lane == 0) mbar_arrive(bar.freed + s);
+        if (a.dots && lane < rows && 32 * half < DH) a.dots[(slice * p.BH + bh) * p.N + t0 + lane] = sum;
         return true;
       };
 
@@ -637,7 +741,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.freed + s);
-      if (!ONLY_STATE && n + 1 < count) publish();
+      if (!ONLY_STATE && n + 1 < count) {
+        if (!gwarp_wait(&bar.state_read, n, abortf)) break;
+        publish();
+      }
     }
     float* to = ONLY_STATE ? a.local + (bh * p.spans + span) * p.d * p.d
                            : a.last && span == (reverse ? 0 : p.spans - 1) ? a.last + bh * p.d * p.d : nullptr;
