@@ -210,10 +210,10 @@ __device__ __forceinline__ Sum chunk_gates(float4 g, ChunkGates& out, const Scan
     put(out.col[r], c);
   }
   if ((lane & 7) == 0) out.enter[block] = a.state_scale * (reverse ? exp2_of(all, m) : exp2_of(m, none));
-  // beyond 2^24 within a block its own scores take each difference by itself
+  // beyond 2^40 within a block its own scores take each difference by itself
   bool far = false;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) far = far || !(fabsf((at[e].hi - m.hi) + (at[e].lo - m.lo)) <= 24.0f);
+  for (int e = 0; e < 4; ++e) far = far || !(fabsf((at[e].hi - m.hi) + (at[e].lo - m.lo)) <= 40.0f);
   const uint32_t lanes = __ballot_sync(~0u, far);
   if (lane == 0) {
     out.total = exp2_of(all, none);
@@ -387,10 +387,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      bool ok = gwarp_wait(bar.full, 0, abortf);
-      if (ok) scores(0);
-      for (int n = 0; ok && n < count; ++n) {
-        const int s = n % kStages;
+#pragma unroll 1
+      for (int n = -1; n < count; ++n) {
+        const int s = (n + kStages) % kStages;
         // the scores' other buffer: P of the chunk before has been read
         if (n > 0 && !gwarp_wait(&bar.out_done, n - 1, abortf)) break;
         if (n + 1 < count) {
@@ -398,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           scores(n + 1);
         }
+        if (n < 0) continue;
         if (!gwarp_wait(&bar.s_ready, n, abortf)) break;
         if (n > 0 && !gwarp_wait(&bar.out_read, n - 1, abortf)) break;
         tc_fence_after();
@@ -651,10 +651,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
 
-      bool ok = form_p(0);
-      for (int n = 0; ok && n < count; ++n) {
+      bool ok = true;
+#pragma unroll 1
+      for (int n = -1; ok && n < count; ++n) {
         if (n + 1 < count) ok = form_p(n + 1);
-        if (ok) ok = write_out(n);
+        if (ok && n >= 0) ok = write_out(n);
       }
     }
   } else {
@@ -690,8 +691,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.s_ready);
     };
-    if (!ONLY_STATE) publish();
-
     // k's rows of this warp: 256 / DH... rows at once, eight channels a lane.  The score warps of a
     // scheduler with fewer blocks of scores to form leave it more rows.
     constexpr int kLanes = DH / 8, kRows = 32 / kLanes, kGroups = 64 / kRows;   // groups of rows a half chunk
@@ -703,14 +702,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g0 = from16 * kGroups / 16, g1 = (from16 + many16) * kGroups / 16;
     const int kr = lane / kLanes, ku = lane % kLanes;
     bool ok = true;
+#pragma unroll 1
     for (int n = 0; ok && n < count; ++n) {
       const int s = n % kStages;
+      if (!ONLY_STATE) {
+        if (n > 0 && !gwarp_wait(&bar.state_read, n - 1, abortf)) break;
+        publish();
+      }
       if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + s, n / kStages, abortf)) break;
       const ChunkGates& w = gates[s];
       const uint8_t* k = smem + s * L::kStage + kKTile;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-#pragma unroll 2
+#pragma unroll 1
         for (int g = g0; g < g1; ++g) {
           const int token = 64 * half + kRows * g + kr;
           const int at = unit_at(token, ku);
@@ -741,10 +745,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.freed + s);
-      if (!ONLY_STATE && n + 1 < count) {
-        if (!gwarp_wait(&bar.state_read, n, abortf)) break;
-        publish();
-      }
     }
     float* to = ONLY_STATE ? a.local + (bh * p.spans + span) * p.d * p.d
                            : a.last && span == (reverse ? 0 : p.spans - 1) ? a.last + bh * p.d * p.d : nullptr;
