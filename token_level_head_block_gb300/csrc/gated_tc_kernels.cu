@@ -12,11 +12,11 @@
 //   S       <- e^B S + L                              float32 in registers, rounded to nearest
 // The tensor core has four times mma.sync's rate and takes its operands without
 // instructions of the warps, which leaves them the splitting into terms: that work
-// bounds the kernel, so sixteen warps share it.  Eight (score warps) turn S1 into P and
-// write the outputs, one chunk apart, so that PV of one chunk runs under P of
-// the next; eight (state warps) scale and split k and carry the state; two warps issue the MMAs,
-// one loads (TMA, three stages) and prepares the gates.  A thread of a score warp owns a row, so a
-// row's factor is a register and the columns' factors are read by broadcast.
+// bounds the kernel, so twenty-four warps share it, eight for each of three steps that
+// run on different chunks at once: S1 into P (score warps); k scaled and split, and the state
+// (state warps); the outputs (output warps).  Two warps issue the MMAs, one loads (TMA, three
+// stages) and prepares the gates.  A thread of a score or output warp
+// owns a row, so a row's factor is a register and the columns' factors are read by broadcast.
 //
 // Every wait is bounded; one that gives up sets bit 0 of this file's error
 // word and an abort flag, the CTA drains what it issued and releases tensor memory.
@@ -42,8 +42,8 @@ namespace {
 
 using namespace tc;
 
-constexpr int kScoreWarps = 8, kStateWarps = 8;
-constexpr int kIssuer = kScoreWarps + kStateWarps, kAdder = kIssuer + 1, kLoader = kIssuer + 2;
+constexpr int kScoreWarps = 8, kStateWarps = 8, kOutWarps = 8;   // in this order
+constexpr int kFirstOut = kScoreWarps + kStateWarps, kIssuer = kFirstOut + kOutWarps, kAdder = kIssuer + 1, kLoader = kIssuer + 2;
 constexpr int kThreads = 32 * (kLoader + 1);
 constexpr int kStages = 3;
 constexpr int kTileBytes = kTcChunk * 128;   // 128 rows of 64 channels, 128-byte swizzle
@@ -306,16 +306,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar.full + s, 1);
       mbar_init(bar.gates + s, 1);
-      mbar_init(bar.freed + s, ONLY_STATE ? kStateWarps : kStateWarps + kScoreWarps);
+      mbar_init(bar.freed + s, ONLY_STATE ? kStateWarps : kStateWarps + kOutWarps);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar.scores + s, 1);
       mbar_init(bar.p_ready + s, kScoreWarps);
-      mbar_init(bar.k_ready + s, kStateWarps);
+      mbar_init(bar.k_ready + s, ONLY_STATE ? kStateWarps + kScoreWarps : kStateWarps);
     }
     mbar_init(&bar.state_read, 1);
     mbar_init(&bar.out_done, 1);
-    mbar_init(&bar.out_read, kScoreWarps);
+    mbar_init(&bar.out_read, kOutWarps);
     mbar_init(&bar.l_done, 1);
     mbar_init(&bar.s_ready, kStateWarps);
     mbar_init(bar.fin, 1);
@@ -416,13 +416,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t pt = tmem + kScores + 128 * (n & 1);
         if (leader) {
 #pragma unroll
-          for (int cb = 0; cb < 4; ++cb)
+          for (int ks = 0; ks < kTcChunk / 16; ++ks)
 #pragma unroll
             for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int ks = 0; ks < 2; ++ks)
-                mma_bf16_ts(tmem + kO2, pt + 32 * cb + 16 * t + 8 * ks, v + (2 * cb + ks) * 2 * kSbo / 16, idesc_o,
-                            cb + t + ks > 0);
+              mma_bf16_ts(tmem + kO2, pt + 16 * ks + 8 * t, v + ks * 2 * kSbo / 16, idesc_o, ks + t > 0);
           mma_commit(&bar.out_done);
         }
         __syncwarp();
@@ -464,122 +461,114 @@ __global__ void __launch_bounds__(kThreads, 1)
       drain_wait_on(bar.fin + 1, 0, &g_gated_error);
     }
     __syncwarp();
-  } else if (warp < kScoreWarps) {
-    // ------------------------------------------------------------ scores and outputs
-    if (!ONLY_STATE) {
-      const int q = warp & 3, half = warp >> 2, row = 32 * q + lane;
-      const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q) << 16);
-      const int64_t slice = half;
-      uint32_t kept[16];   // scores of a block's second half
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + b * a.out.sb + h * a.out.sh;
-      const __nv_bfloat16* dot = static_cast<const __nv_bfloat16*>(a.dot.data) + b * a.dot.sb + h * a.dot.sh;
-
-      // P of chunk n: this warp's 32 rows, tokens 64 half .., 16 tokens a round.  A row's
-      // factor e^{b_i - m} waits for the outputs, except where the row's block is steep.
-      auto form_p = [&](int n) -> bool {
-        const int s = n % kStages;
-        if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + s, n / kStages, abortf)) return false;
-        const ChunkGates& w = gates[s];
-        // rows of v that are not finite (this warp looks at 32 of them, half a row a lane)
-        {
-          const uint8_t* v = smem + s * L::kStage + kVTile;
-          uint32_t bad = 0;
+  } else if (!ONLY_STATE && warp < kScoreWarps) {
+    // ------------------------------------------------------------ scores
+    const int q = warp & 3, half = warp >> 2, row = 32 * q + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    // P of a chunk: this warp's 32 rows, tokens 64 half .., 16 tokens a round, their two
+    // terms (8 columns each) over their scores.  A row's factor e^{b_i - m} waits for the
+    // outputs, except where the row's block is steep.
+#pragma unroll 1
+    for (int n = 0; n < count; ++n) {
+      const int s = n % kStages;
+      if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + s, n / kStages, abortf)) break;
+      const ChunkGates& w = gates[s];
+      // rows of v that are not finite (this warp looks at 32 of them, half a row a lane)
+      {
+        const uint8_t* v = smem + s * L::kStage + kVTile;
+        uint32_t bad = 0;
 #pragma unroll
-          for (int u = 0; u < DH / 16; ++u) {
-            const uint4 x = *reinterpret_cast<const uint4*>(v + unit_at(row, DH / 16 * half + u));
-            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+        for (int u = 0; u < DH / 16; ++u) {
+          const uint4 x = *reinterpret_cast<const uint4*>(v + unit_at(row, DH / 16 * half + u));
+          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 z =
-                  __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y[e]), __floats2bfloat162_rn(0.0f, 0.0f));
-              bad |= *reinterpret_cast<const uint32_t*>(&z);
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 z =
+                __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y[e]), __floats2bfloat162_rn(0.0f, 0.0f));
+            bad |= *reinterpret_cast<const uint32_t*>(&z);
+          }
+        }
+        if (bad & 0x7FFF7FFFu) *reinterpret_cast<volatile uint32_t*>(ctl.bad + (n & 3)) = n + 1;
+      }
+      const bool steep = w.steep >> q & 1;
+      if (!gwarp_wait(bar.scores + (n & 1), n >> 1, abortf)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 4 * half; c < 4 * half + 4; ++c) {   // 16 tokens
+        const int cb = c >> 1, j0 = 16 * c;
+        const uint32_t at = lanes + kScores + 128 * (n & 1) + j0;
+        uint32_t t0[8], t1[8];
+        if (reverse ? cb < q : cb > q) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t0[i] = t1[i] = 0u;
+        } else {
+          uint32_t x[16];
+          tmem_ld_x16(at, x);
+          tmem_ld_wait();
+          if (cb == q && steep) {
+            uint32_t z[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z[i] = x[i];
+            steep_block(z, w, a.out_scale, row, j0, reverse);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = z[i];
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(w.col[q] + j0 + j);
+              x[j] = __float_as_uint(__uint_as_float(x[j]) * f.x);
+              x[j + 1] = __float_as_uint(__uint_as_float(x[j + 1]) * f.y);
+              x[j + 2] = __float_as_uint(__uint_as_float(x[j + 2]) * f.z);
+              x[j + 3] = __float_as_uint(__uint_as_float(x[j + 3]) * f.w);
+            }
+            if (steep) {
+              const float rw = w.row[row];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * rw);
             }
           }
-          if (bad & 0x7FFF7FFFu) *reinterpret_cast<volatile uint32_t*>(ctl.bad + (n & 3)) = n + 1;
-        }
-        const bool steep = w.steep >> q & 1;
-        if (!gwarp_wait(bar.scores + (n & 1), n >> 1, abortf)) return false;
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 4 * half; c < 4 * half + 4; ++c) {   // 16 tokens
-          const int cb = c >> 1;
-          const uint32_t buffer = lanes + kScores + 128 * (n & 1) + 32 * cb;
-          uint32_t t0[8], t1[8];
-          uint32_t x[16];
-          // both halves of a block are read before either is written over
-          if (reverse ? cb < q : cb > q) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t0[i] = t1[i] = 0u;
-          } else {
-            if ((c & 1) == 0) {
-              tmem_ld_x16(buffer + 16, x);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) kept[i] = x[i];
-              tmem_ld_x16(buffer, x);
-              tmem_ld_wait();
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] = kept[i];
-            }
-            const int j0 = 16 * c;
-            if (cb == q && steep) {
-              uint32_t z[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) z[i] = x[i];
-              steep_block(z, w, a.out_scale, row, j0, reverse);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] = z[i];
-            } else {
-#pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(w.col[q] + j0 + j);
-                x[j] = __float_as_uint(__uint_as_float(x[j]) * f.x);
-                x[j + 1] = __float_as_uint(__uint_as_float(x[j + 1]) * f.y);
-                x[j + 2] = __float_as_uint(__uint_as_float(x[j + 2]) * f.z);
-                x[j + 3] = __float_as_uint(__uint_as_float(x[j + 3]) * f.w);
-              }
-              if (steep) {
-                const float rw = w.row[row];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * rw);
-              }
-            }
+          for (int i = 0; i < 8; ++i) {
+            uint32_t t[2];
+            split<2>(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), t);
+            t0[i] = t[0];
+            t1[i] = t[1];
+          }
+          if (cb == q) {   // tokens the row does not see: their bits cleared, whatever they hold
+            const int seen = reverse ? row - j0 : row - j0 + 1;   // forwards tokens below it, backwards those from it
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              uint32_t t[2];
-              split<2>(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), t);
-              t0[i] = t[0];
-              t1[i] = t[1];
-            }
-            if (cb == q) {   // tokens the row does not see: their bits cleared, whatever they hold
-              const int seen = reverse ? row - j0 : row - j0 + 1;   // forwards tokens below it, backwards those from it
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int k = min(max(seen - 2 * i, 0), 2);
-                uint32_t keep = k == 2 ? 0xFFFFFFFFu : k == 1 ? 0xFFFFu : 0u;
-                if (reverse) keep = ~keep;
-                t0[i] &= keep;
-                t1[i] &= keep;
-              }
+              const int k = min(max(seen - 2 * i, 0), 2);
+              uint32_t keep = k == 2 ? 0xFFFFFFFFu : k == 1 ? 0xFFFFu : 0u;
+              if (reverse) keep = ~keep;
+              t0[i] &= keep;
+              t1[i] &= keep;
             }
           }
-          tmem_st_x8(buffer + 8 * (c & 1), t0);
-          tmem_st_x8(buffer + 16 + 8 * (c & 1), t1);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar.p_ready + (n & 1));
-        return true;
-      };
-
+        tmem_st_x8(at, t0);
+        tmem_st_x8(at + 8, t1);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.p_ready + (n & 1));
+    }
+  } else if (warp >= kFirstOut) {
+    // ------------------------------------------------------------ outputs
+    if (!ONLY_STATE) {
+      const int q = warp & 3, half = (warp - kFirstOut) >> 2, row = 32 * q + lane;
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * q) << 16);
+      const int64_t slice = half;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out.data) + b * a.out.sb + h * a.out.sh;
+      const __nv_bfloat16* dot = static_cast<const __nv_bfloat16*>(a.dot.data) + b * a.dot.sb + h * a.dot.sh;
       // Output rows of chunk n, columns 32 half ..: through this warp's 2 KB of the q tile
       // (32 rows of 64 bytes), which nothing reads any more, so that eight rows go out at once.
       auto staged = [&](uint8_t* base, int r, int u) {
         return reinterpret_cast<uint4*>(base + 64 * r + ((u ^ (r >> 1 & 3)) << 4));
       };
-      auto write_out = [&](int n) -> bool {
+#pragma unroll 1
+      for (int n = 0; n < count; ++n) {
         const int s = n % kStages, part_row = lane >> 2, part = lane & 3;
         const int64_t t0 = chunk_of(n) * kTcChunk + 32 * q;
         const int rows = static_cast<int>(min(p.N - t0, static_cast<int64_t>(32)));   // in the sequence
@@ -593,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                       : make_uint4(0u, 0u, 0u, 0u);
         }
         const ChunkGates& w = gates[s];
-        if (!gwarp_wait(&bar.out_done, n, abortf)) return false;
+        if (!gwarp_wait(&bar.out_done, n, abortf)) break;
         tc_fence_after();
         const bool apart = *reinterpret_cast<volatile uint32_t*>(ctl.bad + (n & 3)) == static_cast<uint32_t>(n + 1);
         const bool steep = w.steep >> q & 1;
@@ -613,8 +602,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_x16(lanes + kO2 + c, y);
           tmem_ld_wait();
           if (apart) {
+            uint32_t xx[16];   // of its own: what a call is given lives in memory
+#pragma unroll
+            for (int i = 0; i < 16; ++i) xx[i] = x[i];
             if (lane < rows)
-              sum += row_apart<DH>(x, f1 * f2, smem + s * L::kStage, w, a.out_scale, row, c, reverse,
+              sum += row_apart<DH>(xx, f1 * f2, smem + s * L::kStage, w, a.out_scale, row, c, reverse,
                                    out + (t0 + lane) * a.out.sn + c, a.dots ? dot + (t0 + lane) * a.dot.sn + c : nullptr,
                                    p.d - c);
             continue;
@@ -648,21 +640,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) mbar_arrive(bar.freed + s);
         if (a.dots && lane < rows && 32 * half < DH) a.dots[(slice * p.BH + bh) * p.N + t0 + lane] = sum;
-        return true;
-      };
-
-      bool ok = true;
-#pragma unroll 1
-      for (int n = -1; ok && n < count; ++n) {
-        if (n + 1 < count) ok = form_p(n + 1);
-        if (ok && n >= 0) ok = write_out(n);
       }
     }
   } else {
     // ------------------------------------------------------------ the state
+    const bool carries = warp >= kScoreWarps;   // ONLY_STATE: the score warps help with k alone
     const int q = warp & 3, hf = (warp - kScoreWarps) >> 2;
     const int r0 = 16 * q + (lane >> 2), c0 = 32 * hf + 2 * (lane & 3);
-    const bool holds = 16 * q < DH && 32 * hf < DH;   // of the state
+    const bool holds = carries && 16 * q < DH && 32 * hf < DH;   // of the state
     float S[16];
     {
       const float* in = !ONLY_STATE && a.init
@@ -694,11 +679,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // k's rows of this warp: 256 / DH... rows at once, eight channels a lane.  The score warps of a
     // scheduler with fewer blocks of scores to form leave it more rows.
     constexpr int kLanes = DH / 8, kRows = 32 / kLanes, kGroups = 64 / kRows;   // groups of rows a half chunk
-    const int load = ONLY_STATE ? 4 : reverse ? 3 - q : q;   // 0: lightest score work
-    // sixteenths of a half chunk per warp: 3 3 | 3 2 | 2 1 | 1 1 (or two each)
-    const int from16 = load == 4 ? 2 * (warp - kScoreWarps)
-                                 : load == 0 ? 3 * hf : load == 1 ? 6 + 3 * hf : load == 2 ? 11 + 2 * hf : 14 + hf;
-    const int many16 = load == 4 ? 2 : load == 0 ? 3 : load == 1 ? 3 - hf : load == 2 ? 2 - hf : 1;
+    const int load = reverse ? 3 - q : q;   // 0: lightest score work
+    // sixteenths of a half chunk per warp: 3 3 | 3 2 | 2 1 | 1 1; ONLY_STATE: one each
+    const int from16 = ONLY_STATE ? warp : load == 0 ? 3 * hf : load == 1 ? 6 + 3 * hf : load == 2 ? 11 + 2 * hf : 14 + hf;
+    const int many16 = ONLY_STATE ? 1 : load == 0 ? 3 : load == 1 ? 3 - hf : load == 2 ? 2 - hf : 1;
     const int g0 = from16 * kGroups / 16, g1 = (from16 + many16) * kGroups / 16;
     const int kr = lane / kLanes, ku = lane % kLanes;
     bool ok = true;
@@ -734,6 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float total = w.total;
       if (!gwarp_wait(&bar.l_done, n, abortf)) { ok = false; break; }
+      if (ONLY_STATE && !carries) continue;
       tc_fence_after();
       if (holds) {
         uint32_t l[16];
