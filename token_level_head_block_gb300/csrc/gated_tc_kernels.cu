@@ -14,8 +14,8 @@
 // instructions of the warps, which leaves them the splitting into terms: that work
 // bounds the kernel, so twenty-four warps share it, eight for each of three steps that
 // run on different chunks at once: S1 into P (score warps); k scaled and split, and the state
-// (state warps); the outputs (output warps).  Two warps issue the MMAs, one loads (TMA, three
-// stages) and prepares the gates.  A thread of a score or output warp
+// (state warps); the outputs (output warps).  Two warps issue the MMAs, one the loads (TMA,
+// three stages), one prepares the gates.  A thread of a score or output warp
 // owns a row, so a row's factor is a register and the columns' factors are read by broadcast.
 //
 // Every wait is bounded; one that gives up sets bit 0 of this file's error
@@ -43,9 +43,9 @@ namespace {
 using namespace tc;
 
 constexpr int kScoreWarps = 8, kStateWarps = 8, kOutWarps = 8;   // in this order
-constexpr int kFirstOut = kScoreWarps + kStateWarps, kIssuer = kFirstOut + kOutWarps, kAdder = kIssuer + 1, kLoader = kIssuer + 2;
+constexpr int kFirstOut = kScoreWarps + kStateWarps, kIssuer = kFirstOut + kOutWarps, kAdder = kIssuer + 1, kGates = kIssuer + 2, kLoader = kIssuer + 3;
 constexpr int kThreads = 32 * (kLoader + 1);
-constexpr int kStages = 3;
+constexpr int kStages = 3, kGateRing = 4;
 constexpr int kTileBytes = kTcChunk * 128;   // 128 rows of 64 channels, 128-byte swizzle
 constexpr int kPlane = kTileBytes;           // one term of the scaled k
 constexpr int kStatePlane = 64 * 128;        // one term of the state
@@ -70,15 +70,15 @@ struct ChunkGates {
 };
 
 struct Bars {
-  uint64_t full[kStages], gates[kStages], freed[kStages];
+  uint64_t full[kStages], freed[kStages], gates[kGateRing], gates_freed[kGateRing];
   uint64_t scores[2], p_ready[2];
-  uint64_t state_read, out_done, out_read, k_ready[2], l_done, s_ready, fin[2];
+  uint64_t state_read, o1_read, out_done, out_read, k_ready[2], l_done, s_ready, fin[2];
 };
 
 struct Control {
   Bars bars;
   uint32_t tmem, abort;
-  uint32_t bad[4];   // chunk + 1 whose v holds an infinity or NaN
+  uint32_t bad;   // v held an infinity or NaN
 };
 
 template <bool ONLY_STATE>
@@ -88,14 +88,28 @@ struct Layout {
   static constexpr int kKp = kStages * kStage;
   static constexpr int kS = kKp + 3 * kPlane;
   static constexpr int kGates = kS + (ONLY_STATE ? 0 : 2 * kStatePlane);
-  static constexpr int kControl = kGates + kStages * static_cast<int>(sizeof(ChunkGates));
+  static constexpr int kControl = kGates + kGateRing * static_cast<int>(sizeof(ChunkGates));
   static constexpr size_t kBytes = kControl + sizeof(Control) + 1024;
 };
 static_assert(Layout<false>::kBytes <= 227 * 1024, "shared memory of one CTA");
 
+// A look that may suspend the thread up to `ns`: a waiting warp that does not poll leaves
+// its issue slots to the others.
+__device__ __forceinline__ bool mbar_try_wait_up_to(uint64_t* bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+
 // Every lane waits, then the warp agrees; the first look is in place.
 __device__ __forceinline__ bool gwarp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abortf) {
-  bool ok = mbar_try_wait(bar, parity & 1u);
+  bool ok = mbar_try_wait_up_to(bar, parity & 1u, 1000000u);
   if (!ok) ok = wait_bounded_on(bar, parity & 1u, abortf, &g_gated_error);
   return __all_sync(0xffffffffu, ok);
 }
@@ -225,44 +239,61 @@ __device__ __forceinline__ Sum chunk_gates(float4 g, ChunkGates& out, const Scan
   return all;
 }
 
-// 16 outputs of one row without the tensor core's P V, for a chunk whose v holds an
-// infinity or NaN: 0 times it must not reach rows that do not see it.  x: what the row
-// reads from the state, f: its factor.  Returns the row's share of dot . o.
-template <int DH>
-__device__ __noinline__ float row_apart(const uint32_t (&x)[16], float f, const uint8_t* stage, const ChunkGates& w,
-                                        float out_scale, int row, int c0, bool reverse, __nv_bfloat16* out,
-                                        const __nv_bfloat16* dot, int width) {
-  float o[16];
+// A whole span again, token by token without the tensor core: for a span whose v held an
+// infinity or NaN, which the masked products (0 times it) carried to earlier rows of its chunk.  Rare and
+// slow; called once, behind the pipeline, so that it costs that no registers.
+__device__ __noinline__ void redo_span(const ScanSet& p, const Scan& a, uint8_t* smem, int64_t bh, int64_t span,
+                                       int64_t t0, int64_t t1) {
+  float* q = reinterpret_cast<float*>(smem);
+  float *k = q + 64, *v = k + 64, *part = v + 64;   // part: [8][64]
+  const int c = threadIdx.x & 63, g = threadIdx.x >> 6, d = p.d;
+  const int64_t b = bh / p.H, h = bh % p.H;
+  auto at = [&](const Operand& o, int64_t t) {
+    return static_cast<__nv_bfloat16*>(o.data) + b * o.sb + t * o.sn + h * o.sh;
+  };
+  float S[8];   // rows 8 g .. of column c
+  const float* in = a.init ? a.init + (bh * a.init_spans + (a.init_spans > 1 ? span : 0)) * d * d : nullptr;
 #pragma unroll
-  for (int c = 0; c < 16; ++c) o[c] = 0.0f;
-  const uint8_t *q = stage, *k = stage + kTileBytes, *v = stage + 2 * kTileBytes;
-  const int j0 = reverse ? row : 0, j1 = reverse ? kTcChunk : row + 1;
+  for (int i = 0; i < 8; ++i) {
+    const int r = 8 * g + i;
+    S[i] = in && r < d && c < d ? in[a.init_transposed ? c * d + r : r * d + c] : 0.0f;
+  }
 #pragma unroll 1
-  for (int j = j0; j < j1; ++j) {
-    float s = 0.0f;
-#pragma unroll 1
-    for (int u = 0; u < DH / 8; ++u) {
-      const uint4 a = *reinterpret_cast<const uint4*>(q + unit_at(row, u));
-      const uint4 b = *reinterpret_cast<const uint4*>(k + unit_at(j, u));
-      const uint32_t y[4] = {a.x, a.y, a.z, a.w}, z[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s = fmaf(low(y[e]), low(z[e]), fmaf(high(y[e]), high(z[e]), s));
+  for (int64_t i = 0; i < t1 - t0; ++i) {
+    const int64_t t = a.reverse ? t1 - 1 - i : t0 + i;
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      q[c] = c < d ? to_f(at(a.q, t)[c]) : 0.0f;
+      k[c] = c < d ? a.k_scale * to_f(at(a.k, t)[c]) : 0.0f;
+      v[c] = c < d ? to_f(at(a.v, t)[c]) : 0.0f;
     }
-    const float d = (w.hi[row] - w.hi[j]) + (w.lo[row] - w.lo[j]);
-    s *= out_scale * exp2_fast(reverse ? -d : d);
+    const float gate = to_f(*at(p.g, t)), decay = expf(gate < kLowestGate ? kLowestGate : gate);
+    __syncthreads();
+    if (g < 8) {
+      float o = 0.0f;
 #pragma unroll
-    for (int c = 0; c < 16; ++c)
-      o[c] = fmaf(s, to_f(*reinterpret_cast<const __nv_bfloat16*>(v + unit_at(j, (c0 + c) / 8) + 2 * (c & 7))), o[c]);
-  }
-  float sum = 0.0f;
+      for (int e = 0; e < 8; ++e) {
+        S[e] = fmaf(k[8 * g + e], v[c], a.reverse ? S[e] : decay * S[e]);
+        o = fmaf(q[8 * g + e], S[e], o);
+        if (a.reverse) S[e] *= decay;
+      }
+      part[64 * g + c] = o;
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      float o = 0.0f;
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    if (c >= width) continue;
-    o[c] = fmaf(f, __uint_as_float(x[c]), o[c]);
-    out[c] = __float2bfloat16_rn(o[c]);
-    if (dot) sum = fmaf(o[c], to_f(dot[c]), sum);
+      for (int e = 0; e < 8; ++e) o += part[64 * e + c];
+      o *= a.state_scale;
+      if (c < d) at(a.out, t)[c] = __float2bfloat16_rn(o);
+      if (a.dots) {
+        float x = c < d ? o * to_f(at(a.dot, t)[c]) : 0.0f;
+#pragma unroll
+        for (int e = 16; e; e >>= 1) x += __shfl_xor_sync(~0u, x, e);
+        if ((c & 31) == 0 && (c == 0 || d > 32)) a.dots[((c >> 5) * p.BH + bh) * p.N + t] = x;
+      }
+    }
   }
-  return sum;
 }
 
 // 16 scores of a row in its own block times their decays, each difference by itself.
@@ -305,8 +336,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar.full + s, 1);
-      mbar_init(bar.gates + s, 1);
       mbar_init(bar.freed + s, ONLY_STATE ? kStateWarps : kStateWarps + kOutWarps);
+    }
+    for (int s = 0; s < kGateRing; ++s) {
+      mbar_init(bar.gates + s, 1);
+      mbar_init(bar.gates_freed + s, ONLY_STATE ? kStateWarps : kStateWarps + kOutWarps);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar.scores + s, 1);
@@ -315,13 +349,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&bar.state_read, 1);
     mbar_init(&bar.out_done, 1);
+    mbar_init(&bar.o1_read, kOutWarps);
     mbar_init(&bar.out_read, kOutWarps);
     mbar_init(&bar.l_done, 1);
     mbar_init(&bar.s_ready, kStateWarps);
     mbar_init(bar.fin, 1);
     mbar_init(bar.fin + 1, 1);
     ctl.abort = 0u;
-    for (int i = 0; i < 4; ++i) ctl.bad[i] = 0u;
+    ctl.bad = 0u;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -334,40 +369,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl.tmem;
 
   if (warp == kLoader) {
-    // ------------------------------------------------------------ loads and gates
+    // ------------------------------------------------------------ loads
     const uint64_t policy = ONLY_STATE ? policy_evict_last() : policy_evict_first();
-    auto load = [&](int n) {
-      uint64_t* full = bar.full + n % kStages;
-      uint8_t* st = smem + (n % kStages) * L::kStage;
-      const int32_t t = static_cast<int32_t>(chunk_of(n) * kTcChunk), hh = static_cast<int32_t>(h),
-                    bb = static_cast<int32_t>(b);
-      mbar_arrive_expect_tx(full, L::kStage);
-      if (!ONLY_STATE) tma_load_4d(st, &maps.q[blockIdx.y], full, 0, hh, t, bb, policy);
-      tma_load_4d(st + kKTile, &maps.k[blockIdx.y], full, 0, hh, t, bb, policy);
-      tma_load_4d(st + kVTile, &maps.v[blockIdx.y], full, 0, hh, t, bb, policy);
-    };
-    int issued = min(count, kStages);
-    if (lane == 0)
-      for (int n = 0; n < issued; ++n) load(n);
-    Sum all = {0.0f, 0.0f};
-    float4 g = load_gates(p, b, h, chunk_of(0), lane);
+    const bool leader = elect_one();
+    int issued = 0;
+#pragma unroll 1
     for (int n = 0; n < count; ++n) {
       const int s = n % kStages;
-      if (n >= kStages) {
-        if (!gwarp_wait(bar.freed + s, n / kStages - 1, abortf)) break;
-        if (lane == 0) load(n);
-        ++issued;
+      if (n >= kStages && !gwarp_wait(bar.freed + s, n / kStages - 1, abortf)) break;
+      if (leader) {
+        uint8_t* st = smem + s * L::kStage;
+        const int32_t t = static_cast<int32_t>(chunk_of(n) * kTcChunk), hh = static_cast<int32_t>(h),
+                      bb = static_cast<int32_t>(b);
+        mbar_arrive_expect_tx(bar.full + s, L::kStage);
+        if (!ONLY_STATE) tma_load_4d(st, &maps.q[blockIdx.y], bar.full + s, 0, hh, t, bb, policy);
+        tma_load_4d(st + kKTile, &maps.k[blockIdx.y], bar.full + s, 0, hh, t, bb, policy);
+        tma_load_4d(st + kVTile, &maps.v[blockIdx.y], bar.full + s, 0, hh, t, bb, policy);
       }
-      const float4 now = g;
-      if (n + 1 < count) g = load_gates(p, b, h, chunk_of(n + 1), lane);
-      all = add(all, chunk_gates(now, gates[s], a, lane));
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar.gates + s);
+      ++issued;
     }
-    if (ONLY_STATE && lane == 0) a.decay[bh * p.spans + span] = exp2_of(all, Sum{0.0f, 0.0f});
-    if (lane == 0)   // every load must have landed before the CTA ends
+    if (leader)   // every load must have landed before the CTA ends
       for (int n = max(0, issued - kStages); n < issued; ++n)
         drain_wait_on(bar.full + n % kStages, static_cast<uint32_t>((n / kStages) & 1), &g_gated_error);
+    __syncwarp();
+  } else if (warp == kGates) {
+    // ------------------------------------------------------------ gates, ahead of the loads
+    Sum all = {0.0f, 0.0f};
+    float4 g = load_gates(p, b, h, chunk_of(0), lane);
+#pragma unroll 1
+    for (int n = 0; n < count; ++n) {
+      if (n >= kGateRing && !gwarp_wait(bar.gates_freed + n % kGateRing, n / kGateRing - 1, abortf)) break;
+      const float4 now = g;
+      if (n + 1 < count) g = load_gates(p, b, h, chunk_of(n + 1), lane);
+      all = add(all, chunk_gates(now, gates[n % kGateRing], a, lane));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.gates + n % kGateRing);
+    }
+    if (ONLY_STATE && lane == 0) a.decay[bh * p.spans + span] = exp2_of(all, Sum{0.0f, 0.0f});
   } else if (warp == kIssuer) {
     // ------------------------------------------------------------ scores and outputs: MMAs
     if (!ONLY_STATE) {
@@ -399,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (n < 0) continue;
         if (!gwarp_wait(&bar.s_ready, n, abortf)) break;
-        if (n > 0 && !gwarp_wait(&bar.out_read, n - 1, abortf)) break;
+        if (n > 0 && !gwarp_wait(&bar.o1_read, n - 1, abortf)) break;
         tc_fence_after();
         const uint64_t q = stage0 + s * (L::kStage >> 4), v = v0 + s * (L::kStage >> 4);
         if (leader) {
@@ -412,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (!gwarp_wait(bar.p_ready + (n & 1), n >> 1, abortf)) break;
+        if (n > 0 && !gwarp_wait(&bar.out_read, n - 1, abortf)) break;
         tc_fence_after();
         const uint32_t pt = tmem + kScores + 128 * (n & 1);
         if (leader) {
@@ -471,24 +511,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int n = 0; n < count; ++n) {
       const int s = n % kStages;
-      if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + s, n / kStages, abortf)) break;
-      const ChunkGates& w = gates[s];
+      if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + n % kGateRing, n / kGateRing, abortf)) break;
+      const ChunkGates& w = gates[n % kGateRing];
       // rows of v that are not finite (this warp looks at 32 of them, half a row a lane)
       {
         const uint8_t* v = smem + s * L::kStage + kVTile;
-        uint32_t bad = 0;
+        const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
+        __nv_bfloat162 z = zero;   // zero as long as what it meets is finite
 #pragma unroll
         for (int u = 0; u < DH / 16; ++u) {
           const uint4 x = *reinterpret_cast<const uint4*>(v + unit_at(row, DH / 16 * half + u));
           const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 z =
-                __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y[e]), __floats2bfloat162_rn(0.0f, 0.0f));
-            bad |= *reinterpret_cast<const uint32_t*>(&z);
-          }
+          for (int e = 0; e < 4; ++e) z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&y[e]), zero, z);
         }
-        if (bad & 0x7FFF7FFFu) *reinterpret_cast<volatile uint32_t*>(ctl.bad + (n & 3)) = n + 1;
+        if (*reinterpret_cast<const uint32_t*>(&z) & 0x7FFF7FFFu) *reinterpret_cast<volatile uint32_t*>(&ctl.bad) = 1u;
       }
       const bool steep = w.steep >> q & 1;
       if (!gwarp_wait(bar.scores + (n & 1), n >> 1, abortf)) break;
@@ -581,56 +618,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             z[i] = part_in && part_row + 8 * i < rows ? *reinterpret_cast<const uint4*>(x + 8 * i * a.dot.sn)
                                                       : make_uint4(0u, 0u, 0u, 0u);
         }
-        const ChunkGates& w = gates[s];
-        if (!gwarp_wait(&bar.out_done, n, abortf)) break;
+        // the queries have read the state: O1 is there, and the q tile is free
+        if (!gwarp_wait(bar.gates + n % kGateRing, n / kGateRing, abortf) || !gwarp_wait(&bar.state_read, n, abortf)) break;
         tc_fence_after();
-        const bool apart = *reinterpret_cast<volatile uint32_t*>(ctl.bad + (n & 3)) == static_cast<uint32_t>(n + 1);
-        const bool steep = w.steep >> q & 1;
-        // o = f2 (f1 O1 + O2)
-        const float f1 = steep ? w.enter[q] * w.row[row] : w.enter[q], f2 = steep ? 1.0f : w.row[row];
-        float sum = 0.0f;
         uint8_t* mine = smem + s * L::kStage + 4096 * q + 2048 * half;
-        if (a.dots && !apart) {
+        if (a.dots) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) *staged(mine, part_row + 8 * i, part) = z[i];
           __syncwarp();
         }
-#pragma unroll 1
-        for (int c = 32 * half; c < min(32 * half + 32, DH); c += 16) {
-          uint32_t x[16], y[16];
-          tmem_ld_x16(lanes + kO1 + c, x);
-          tmem_ld_x16(lanes + kO2 + c, y);
+        const ChunkGates& w = gates[n % kGateRing];
+        const bool steep = w.steep >> q & 1;
+        // o = f2 (f1 O1 + O2)
+        const float f1 = steep ? w.enter[q] * w.row[row] : w.enter[q], f2 = steep ? 1.0f : w.row[row];
+        float x[32];
+        if (32 * half < DH) {
+          uint32_t r[32];
+          tmem_ld_x32(lanes + kO1 + 32 * half, r);
           tmem_ld_wait();
-          if (apart) {
-            uint32_t xx[16];   // of its own: what a call is given lives in memory
 #pragma unroll
-            for (int i = 0; i < 16; ++i) xx[i] = x[i];
-            if (lane < rows)
-              sum += row_apart<DH>(xx, f1 * f2, smem + s * L::kStage, w, a.out_scale, row, c, reverse,
-                                   out + (t0 + lane) * a.out.sn + c, a.dots ? dot + (t0 + lane) * a.dot.sn + c : nullptr,
-                                   p.d - c);
-            continue;
-          }
+          for (int i = 0; i < 32; ++i) x[i] = f1 * __uint_as_float(r[i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.o1_read);
+        if (!gwarp_wait(&bar.out_done, n, abortf)) break;
+        tc_fence_after();
+        float sum = 0.0f;
+        if (32 * half < DH) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            float o[8];
+          for (int c = 0; c < 32; c += 16) {
+            uint32_t y[16];
+            tmem_ld_x16(lanes + kO2 + 32 * half + c, y);
+            tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              o[e] = f2 * fmaf(f1, __uint_as_float(x[8 * u + e]), __uint_as_float(y[8 * u + e]));
-            uint4* at = staged(mine, lane, (c & 31) / 8 + u);
-            if (a.dots) {
-              const uint4 r = *at;
-              const uint32_t zz[4] = {r.x, r.y, r.z, r.w};
+            for (int u = 0; u < 2; ++u) {
+              float o[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) sum = fmaf(o[2 * e], low(zz[e]), fmaf(o[2 * e + 1], high(zz[e]), sum));
+              for (int e = 0; e < 8; ++e) o[e] = f2 * (x[c + 8 * u + e] + __uint_as_float(y[8 * u + e]));
+              uint4* at = staged(mine, lane, c / 8 + u);
+              if (a.dots) {
+                const uint4 r = *at;
+                const uint32_t zz[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum = fmaf(o[2 * e], low(zz[e]), fmaf(o[2 * e + 1], high(zz[e]), sum));
+              }
+              *at = make_uint4(pack(o[0], o[1]), pack(o[2], o[3]), pack(o[4], o[5]), pack(o[6], o[7]));
             }
-            *at = make_uint4(pack(o[0], o[1]), pack(o[2], o[3]), pack(o[4], o[5]), pack(o[6], o[7]));
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.out_read);
-        if (!apart && 32 * half < DH) {
+        if (32 * half < DH) {
           __nv_bfloat16* to = out + (t0 + part_row) * a.out.sn + 32 * half + 8 * part;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -638,7 +678,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4*>(to + 8 * i * a.out.sn) = *staged(mine, part_row + 8 * i, part);
           __syncwarp();
         }
-        if (lane == 0) mbar_arrive(bar.freed + s);
+        if (lane == 0) {
+          mbar_arrive(bar.freed + s);
+          mbar_arrive(bar.gates_freed + n % kGateRing);
+        }
         if (a.dots && lane < rows && 32 * half < DH) a.dots[(slice * p.BH + bh) * p.N + t0 + lane] = sum;
       }
     }
@@ -693,8 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n > 0 && !gwarp_wait(&bar.state_read, n - 1, abortf)) break;
         publish();
       }
-      if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + s, n / kStages, abortf)) break;
-      const ChunkGates& w = gates[s];
+      if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + n % kGateRing, n / kGateRing, abortf)) break;
+      const ChunkGates& w = gates[n % kGateRing];
       const uint8_t* k = smem + s * L::kStage + kKTile;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
@@ -729,7 +772,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar.freed + s);
+      if (lane == 0) {
+        mbar_arrive(bar.freed + s);
+        mbar_arrive(bar.gates_freed + n % kGateRing);
+      }
     }
     float* to = ONLY_STATE ? a.local + (bh * p.spans + span) * p.d * p.d
                            : a.last && span == (reverse ? 0 : p.spans - 1) ? a.last + bh * p.d * p.d : nullptr;
@@ -744,6 +790,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, kTmemColumns);
+  if (!ONLY_STATE && *reinterpret_cast<volatile uint32_t*>(&ctl.bad) && !ctl.abort)
+    redo_span(p, a, smem, bh, span, first * kTcChunk, min(p.N, (first + count) * kTcChunk));
 }
 
 bool operand_map(const ScanSet& set, int64_t B, const Operand& o, CUtensorMap* m) {
