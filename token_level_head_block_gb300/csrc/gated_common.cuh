@@ -35,6 +35,7 @@ struct Scan {
   int32_t reverse;
   int32_t init_transposed;
   int32_t init_spans;   // spans per (b, h) in init: slot of a span, or 1
+  int32_t join;         // init enters the sequence; local and decay hold what the spans add (tcgen05, forwards)
 };
 
 struct ScanSet {

@@ -1061,10 +1061,16 @@ int launch_gated_forward(const GatedProblem& p, const float* state_in, const Ope
   set.scan[0] = a;
   if (c.spans > 1) {
     int rc = r.run(set, 1, true);
-    if (rc == MHLA_OK) rc = run_join(set, 1, r.s);
+    // A few spans are joined by the scan as it starts; a launch for it costs 5 us, sixteen
+    // loads of an L2 hit each about 4.
+    const bool join = r.tc && c.spans <= 16;
+    if (rc == MHLA_OK && !join) rc = run_join(set, 1, r.s);
     if (rc != MHLA_OK) return rc;
-    set.scan[0].init = sb.local;
-    set.scan[0].init_spans = set.spans;
+    set.scan[0].join = join;
+    if (!join) {
+      set.scan[0].init = sb.local;
+      set.scan[0].init_spans = set.spans;
+    }
   }
   return r.run(set, 1, false);
 }

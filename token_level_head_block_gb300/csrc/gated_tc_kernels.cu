@@ -14,8 +14,8 @@
 // instructions of the warps, which leaves them the splitting into terms: that work
 // bounds the kernel, so twenty-four warps share it, eight for each of three steps that
 // run on different chunks at once: S1 into P (score warps); k scaled and split, and the state
-// (state warps); the outputs (output warps).  Two warps issue the MMAs, one the loads (TMA,
-// three stages), one prepares the gates.  A thread of a score or output warp
+// (state warps); the outputs (output warps).  Two warps issue the MMAs and
+// the loads (TMA, three stages), two prepare the gates.  A thread of a score or output warp
 // owns a row, so a row's factor is a register and the columns' factors are read by broadcast.
 //
 // Every wait is bounded; one that gives up sets bit 0 of this file's error
@@ -43,8 +43,8 @@ namespace {
 using namespace tc;
 
 constexpr int kScoreWarps = 8, kStateWarps = 8, kOutWarps = 8;   // in this order
-constexpr int kFirstOut = kScoreWarps + kStateWarps, kIssuer = kFirstOut + kOutWarps, kAdder = kIssuer + 1, kGates = kIssuer + 2, kLoader = kIssuer + 3;
-constexpr int kThreads = 32 * (kLoader + 1);
+constexpr int kFirstOut = kScoreWarps + kStateWarps, kIssuer = kFirstOut + kOutWarps, kAdder = kIssuer + 1, kGates = kIssuer + 2;   // two of these
+constexpr int kThreads = 32 * (kGates + 2);
 constexpr int kStages = 3, kGateRing = 4;
 constexpr int kTileBytes = kTcChunk * 128;   // 128 rows of 64 channels, 128-byte swizzle
 constexpr int kPlane = kTileBytes;           // one term of the scaled k
@@ -72,13 +72,14 @@ struct ChunkGates {
 struct Bars {
   uint64_t full[kStages], freed[kStages], gates[kGateRing], gates_freed[kGateRing];
   uint64_t scores[2], p_ready[2];
-  uint64_t state_read, o1_read, out_done, out_read, k_ready[2], l_done, s_ready, fin[2];
+  uint64_t state_read, o1_read, out_done, out_read, k_ready[2], l_done[2], s_ready, fin[2];
 };
 
 struct Control {
   Bars bars;
   uint32_t tmem, abort;
   uint32_t bad;   // v held an infinity or NaN
+  Sum decay[2];   // of the span, in two parts
 };
 
 template <bool ONLY_STATE>
@@ -86,7 +87,8 @@ struct Layout {
   static constexpr int kTiles = ONLY_STATE ? 2 : 3;   // q, k, v  |  k, v
   static constexpr int kStage = kTiles * kTileBytes;
   static constexpr int kKp = kStages * kStage;
-  static constexpr int kS = kKp + 3 * kPlane;
+  static constexpr int kSets = ONLY_STATE ? 2 : 1;     // of the scaled k's planes
+  static constexpr int kS = kKp + kSets * 3 * kPlane;
   static constexpr int kGates = kS + (ONLY_STATE ? 0 : 2 * kStatePlane);
   static constexpr int kControl = kGates + kGateRing * static_cast<int>(sizeof(ChunkGates));
   static constexpr size_t kBytes = kControl + sizeof(Control) + 1024;
@@ -169,7 +171,8 @@ __device__ __forceinline__ Sum shfl_sum(Sum s, int lane) {
   return r;
 }
 
-// One warp: the running sums and the weights of a chunk.  Returns B.
+// One warp: the running sums and the weights of a chunk (ONLY_STATE: those of the state alone).  Returns B.
+template <bool ONLY_STATE>
 __device__ __forceinline__ Sum chunk_gates(float4 g, ChunkGates& out, const Scan& a, int lane) {
   const Sum none = {0.0f, 0.0f};
   Sum at[4];
@@ -186,7 +189,6 @@ __device__ __forceinline__ Sum chunk_gates(float4 g, ChunkGates& out, const Scan
     if (lane >= s) run = add(o, run);
   }
   const Sum all = shfl_sum(run, 31);
-  const Sum edge[5] = {none, shfl_sum(run, 7), shfl_sum(run, 15), shfl_sum(run, 23), all};
   Sum before;
   before.hi = __shfl_up_sync(~0u, run.hi, 1);
   before.lo = __shfl_up_sync(~0u, run.lo, 1);
@@ -195,6 +197,18 @@ __device__ __forceinline__ Sum chunk_gates(float4 g, ChunkGates& out, const Scan
   for (int e = 0; e < 4; ++e) at[e] = add(before, at[e]);
   const int block = lane >> 3;
   const bool reverse = a.reverse;
+  auto put = [&](float* to, const float (&x)[4]) {
+    reinterpret_cast<float4*>(to)[lane] = make_float4(x[0], x[1], x[2], x[3]);
+  };
+  if constexpr (ONLY_STATE) {
+    float addw[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) addw[e] = a.k_scale * (reverse ? exp2_of(at[e], none) : exp2_of(all, at[e]));
+    put(out.addw, addw);
+    if (lane == 0) out.total = exp2_of(all, none);
+    return all;
+  }
+  const Sum edge[5] = {none, shfl_sum(run, 7), shfl_sum(run, 15), shfl_sum(run, 23), all};
   Sum m = reverse ? edge[1] : edge[0];
 #pragma unroll
   for (int i = 1; i < 4; ++i)
@@ -207,9 +221,6 @@ __device__ __forceinline__ Sum chunk_gates(float4 g, ChunkGates& out, const Scan
     row[e] = reverse ? exp2_of(m, at[e]) : exp2_of(at[e], m);
     addw[e] = a.k_scale * (reverse ? exp2_of(at[e], none) : exp2_of(all, at[e]));
   }
-  auto put = [&](float* to, const float (&x)[4]) {
-    reinterpret_cast<float4*>(to)[lane] = make_float4(x[0], x[1], x[2], x[3]);
-  };
   put(out.hi, hi);
   put(out.lo, lo);
   put(out.row, row);
@@ -239,6 +250,22 @@ __device__ __forceinline__ Sum chunk_gates(float4 g, ChunkGates& out, const Scan
   return all;
 }
 
+// Element (r, c) of the state that enters a span: init's, or (join) the state that enters the
+// sequence carried through the spans in front, whose own contributions lie in local.
+__device__ __forceinline__ float entering(const Scan& a, int64_t bh, int64_t span, int32_t spans, int d, int r, int c) {
+  const int64_t dd = static_cast<int64_t>(d) * d;
+  const int at = a.init_transposed ? c * d + r : r * d + c;
+  const float* in = a.init ? a.init + (bh * a.init_spans + (a.init_spans > 1 ? span : 0)) * dd : nullptr;
+  float x = in ? in[at] : 0.0f;
+  if (a.join) {
+    const int64_t from = bh * spans;
+#pragma unroll 4
+    for (int64_t s = 0; s < span; ++s)
+      x = fmaf(a.decay[from + s], x, a.local[(from + s) * dd + r * d + c]);
+  }
+  return x;
+}
+
 // A whole span again, token by token without the tensor core: for a span whose v held an
 // infinity or NaN, which the masked products (0 times it) carried to earlier rows of its chunk.  Rare and
 // slow; called once, behind the pipeline, so that it costs that no registers.
@@ -252,11 +279,10 @@ __device__ __noinline__ void redo_span(const ScanSet& p, const Scan& a, uint8_t*
     return static_cast<__nv_bfloat16*>(o.data) + b * o.sb + t * o.sn + h * o.sh;
   };
   float S[8];   // rows 8 g .. of column c
-  const float* in = a.init ? a.init + (bh * a.init_spans + (a.init_spans > 1 ? span : 0)) * d * d : nullptr;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = 8 * g + i;
-    S[i] = in && r < d && c < d ? in[a.init_transposed ? c * d + r : r * d + c] : 0.0f;
+    S[i] = r < d && c < d ? entering(a, bh, span, p.spans, d, r, c) : 0.0f;
   }
 #pragma unroll 1
   for (int64_t i = 0; i < t1 - t0; ++i) {
@@ -351,7 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar.out_done, 1);
     mbar_init(&bar.o1_read, kOutWarps);
     mbar_init(&bar.out_read, kOutWarps);
-    mbar_init(&bar.l_done, 1);
+    mbar_init(bar.l_done, 1);
+    mbar_init(bar.l_done + 1, 1);
     mbar_init(&bar.s_ready, kStateWarps);
     mbar_init(bar.fin, 1);
     mbar_init(bar.fin + 1, 1);
@@ -368,45 +395,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
 
-  if (warp == kLoader) {
-    // ------------------------------------------------------------ loads
-    const uint64_t policy = ONLY_STATE ? policy_evict_last() : policy_evict_first();
-    const bool leader = elect_one();
-    int issued = 0;
-#pragma unroll 1
-    for (int n = 0; n < count; ++n) {
-      const int s = n % kStages;
-      if (n >= kStages && !gwarp_wait(bar.freed + s, n / kStages - 1, abortf)) break;
-      if (leader) {
-        uint8_t* st = smem + s * L::kStage;
-        const int32_t t = static_cast<int32_t>(chunk_of(n) * kTcChunk), hh = static_cast<int32_t>(h),
-                      bb = static_cast<int32_t>(b);
-        mbar_arrive_expect_tx(bar.full + s, L::kStage);
-        if (!ONLY_STATE) tma_load_4d(st, &maps.q[blockIdx.y], bar.full + s, 0, hh, t, bb, policy);
-        tma_load_4d(st + kKTile, &maps.k[blockIdx.y], bar.full + s, 0, hh, t, bb, policy);
-        tma_load_4d(st + kVTile, &maps.v[blockIdx.y], bar.full + s, 0, hh, t, bb, policy);
-      }
-      __syncwarp();
-      ++issued;
-    }
-    if (leader)   // every load must have landed before the CTA ends
-      for (int n = max(0, issued - kStages); n < issued; ++n)
-        drain_wait_on(bar.full + n % kStages, static_cast<uint32_t>((n / kStages) & 1), &g_gated_error);
-    __syncwarp();
-  } else if (warp == kGates) {
-    // ------------------------------------------------------------ gates, ahead of the loads
+  if (warp >= kGates) {
+    // ------------------------------------------------------------ gates: the two warps take the chunks in turn
+    const int me = warp - kGates;
     Sum all = {0.0f, 0.0f};
-    float4 g = load_gates(p, b, h, chunk_of(0), lane);
+    float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (me < count) g = load_gates(p, b, h, chunk_of(me), lane);
 #pragma unroll 1
-    for (int n = 0; n < count; ++n) {
+    for (int n = me; n < count; n += 2) {
       if (n >= kGateRing && !gwarp_wait(bar.gates_freed + n % kGateRing, n / kGateRing - 1, abortf)) break;
       const float4 now = g;
-      if (n + 1 < count) g = load_gates(p, b, h, chunk_of(n + 1), lane);
-      all = add(all, chunk_gates(now, gates[n % kGateRing], a, lane));
+      if (n + 2 < count) g = load_gates(p, b, h, chunk_of(n + 2), lane);
+      all = add(all, chunk_gates<ONLY_STATE>(now, gates[n % kGateRing], a, lane));
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.gates + n % kGateRing);
     }
-    if (ONLY_STATE && lane == 0) a.decay[bh * p.spans + span] = exp2_of(all, Sum{0.0f, 0.0f});
+    if (ONLY_STATE && lane == 0) ctl.decay[me] = all;
   } else if (warp == kIssuer) {
     // ------------------------------------------------------------ scores and outputs: MMAs
     if (!ONLY_STATE) {
@@ -471,7 +475,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else if (warp == kAdder) {
-    // ------------------------------------------------------------ what the state gains: MMAs
+    // ------------------------------------------------------------ loads; what the state gains: MMAs
+    const uint64_t policy = ONLY_STATE ? policy_evict_last() : policy_evict_first();
+    int issued = 0;
+    auto load = [&](int n) {
+      const int s = n % kStages;
+      if (elect_one()) {
+        uint8_t* st = smem + s * L::kStage;
+        const int32_t t = static_cast<int32_t>(chunk_of(n) * kTcChunk), hh = static_cast<int32_t>(h),
+                      bb = static_cast<int32_t>(b);
+        mbar_arrive_expect_tx(bar.full + s, L::kStage);
+        if (!ONLY_STATE) tma_load_4d(st, &maps.q[blockIdx.y], bar.full + s, 0, hh, t, bb, policy);
+        tma_load_4d(st + kKTile, &maps.k[blockIdx.y], bar.full + s, 0, hh, t, bb, policy);
+        tma_load_4d(st + kVTile, &maps.v[blockIdx.y], bar.full + s, 0, hh, t, bb, policy);
+      }
+      __syncwarp();
+      ++issued;
+    };
+#pragma unroll 1
+    for (int n = 0; n < min(count, kStages); ++n) load(n);
     const bool leader = elect_one();
     constexpr uint32_t idesc = idesc_bf16_f32(64, DH, true, true);
     const uint64_t v0 = smem_desc(smem_u32(smem + kVTile), kSbo, kSbo, 2), k0 = smem_desc(smem_u32(kp), kSbo, kSbo, 2);
@@ -479,26 +501,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; ok && n < count; ++n) {
       const int s = n % kStages;
       if (!gwarp_wait(bar.full + s, n / kStages, abortf)) break;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        if (!gwarp_wait(bar.k_ready + half, n, abortf)) { ok = false; break; }
+      if constexpr (ONLY_STATE) {
+        // two sets of planes and two accumulators: k of one chunk is scaled while another's products run
+        if (!gwarp_wait(bar.k_ready + (n & 1), n >> 1, abortf)) break;
         tc_fence_after();
-        const uint64_t k = k0 + half * (4 * 2 * kSbo / 16), v = v0 + s * (L::kStage >> 4) + half * (4 * 2 * kSbo / 16);
+        const uint64_t k = k0 + (n & 1) * (3 * kPlane / 16), v = v0 + s * (L::kStage >> 4);
         if (leader) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
+          for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
             for (int t = 0; t < 3; ++t)
-              mma_bf16(tmem + kL, k + (t * kPlane + ks * 2 * kSbo) / 16, v + ks * 2 * kSbo / 16, idesc,
-                       half + ks + t > 0);
-          if (half) mma_commit(&bar.l_done);
+              mma_bf16(tmem + kL + 64 * (n & 1), k + (t * kPlane + ks * 2 * kSbo) / 16, v + ks * 2 * kSbo / 16, idesc,
+                       ks + t > 0);
+          mma_commit(bar.l_done + (n & 1));
         }
         __syncwarp();
+      } else {
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (!gwarp_wait(bar.k_ready + half, n, abortf)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t k = k0 + half * (4 * 2 * kSbo / 16), v = v0 + s * (L::kStage >> 4) + half * (4 * 2 * kSbo / 16);
+          if (leader) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+              for (int t = 0; t < 3; ++t)
+                mma_bf16(tmem + kL, k + (t * kPlane + ks * 2 * kSbo) / 16, v + ks * 2 * kSbo / 16, idesc,
+                         half + ks + t > 0);
+            if (half) mma_commit(bar.l_done);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+      // chunk n + 2 into the stage of chunk n - 1, once that is done with
+      if (n > 0 && n + kStages - 1 < count) {
+        if (!gwarp_wait(bar.freed + (n - 1) % kStages, (n - 1) / kStages, abortf)) break;
+        load(n + kStages - 1);
       }
     }
     if (leader) {
       mma_commit(bar.fin + 1);
       drain_wait_on(bar.fin + 1, 0, &g_gated_error);
+      for (int n = max(0, issued - kStages); n < issued; ++n)   // every load must have landed before the CTA ends
+        drain_wait_on(bar.full + n % kStages, static_cast<uint32_t>((n / kStages) & 1), &g_gated_error);
     }
     __syncwarp();
   } else if (!ONLY_STATE && warp < kScoreWarps) {
@@ -692,15 +739,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r0 = 16 * q + (lane >> 2), c0 = 32 * hf + 2 * (lane & 3);
     const bool holds = carries && 16 * q < DH && 32 * hf < DH;   // of the state
     float S[16];
-    {
-      const float* in = !ONLY_STATE && a.init
-                            ? a.init + (bh * a.init_spans + (a.init_spans > 1 ? span : 0)) * p.d * p.d
-                            : nullptr;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = r0 + 8 * ((i >> 1) & 1), c = c0 + 8 * (i >> 2) + (i & 1);
-        S[i] = in && holds && r < p.d && c < p.d ? in[a.init_transposed ? c * p.d + r : r * p.d + c] : 0.0f;
-      }
+    for (int i = 0; i < 16; ++i) {
+      const int r = r0 + 8 * ((i >> 1) & 1), c = c0 + 8 * (i >> 2) + (i & 1);
+      S[i] = !ONLY_STATE && holds && r < p.d && c < p.d ? entering(a, bh, span, p.spans, p.d, r, c) : 0.0f;
     }
     auto publish = [&]() {
       if (holds) {
@@ -719,53 +761,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.s_ready);
     };
-    // k's rows of this warp: 256 / DH... rows at once, eight channels a lane.  The score warps of a
-    // scheduler with fewer blocks of scores to form leave it more rows.
-    constexpr int kLanes = DH / 8, kRows = 32 / kLanes, kGroups = 64 / kRows;   // groups of rows a half chunk
-    const int load = reverse ? 3 - q : q;   // 0: lightest score work
-    // sixteenths of a half chunk per warp: 3 3 | 3 2 | 2 1 | 1 1; ONLY_STATE: one each
-    const int from16 = ONLY_STATE ? warp : load == 0 ? 3 * hf : load == 1 ? 6 + 3 * hf : load == 2 ? 11 + 2 * hf : 14 + hf;
-    const int many16 = ONLY_STATE ? 1 : load == 0 ? 3 : load == 1 ? 3 - hf : load == 2 ? 2 - hf : 1;
-    const int g0 = from16 * kGroups / 16, g1 = (from16 + many16) * kGroups / 16;
+    // k's rows, kRows at once, eight channels a lane: scaled and split into the planes.
+    constexpr int kLanes = DH / 8, kRows = 32 / kLanes, kGroups = kTcChunk / kRows;
     const int kr = lane / kLanes, ku = lane % kLanes;
-    bool ok = true;
+    auto scale_rows = [&](const uint8_t* k, const ChunkGates& w, uint8_t* to, int g0, int g1) {
 #pragma unroll 1
-    for (int n = 0; ok && n < count; ++n) {
-      const int s = n % kStages;
-      if (!ONLY_STATE) {
-        if (n > 0 && !gwarp_wait(&bar.state_read, n - 1, abortf)) break;
-        publish();
-      }
-      if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + n % kGateRing, n / kGateRing, abortf)) break;
-      const ChunkGates& w = gates[n % kGateRing];
-      const uint8_t* k = smem + s * L::kStage + kKTile;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-#pragma unroll 1
-        for (int g = g0; g < g1; ++g) {
-          const int token = 64 * half + kRows * g + kr;
-          const int at = unit_at(token, ku);
-          const uint4 x = *reinterpret_cast<const uint4*>(k + at);
-          const float f = w.addw[token];
-          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-          uint32_t t[4][3];
+      for (int g = g0; g < g1; ++g) {
+        const int token = kRows * g + kr, at = unit_at(token, ku);
+        const uint4 x = *reinterpret_cast<const uint4*>(k + at);
+        const float f = w.addw[token];
+        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+        uint32_t t[4][3];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) split<3>(low(y[e]) * f, high(y[e]) * f, t[e]);
+        for (int e = 0; e < 4; ++e) split<3>(low(y[e]) * f, high(y[e]) * f, t[e]);
 #pragma unroll
-          for (int i = 0; i < 3; ++i)
-            *reinterpret_cast<uint4*>(kp + i * kPlane + at) = make_uint4(t[0][i], t[1][i], t[2][i], t[3][i]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar.k_ready + half);
+        for (int i = 0; i < 3; ++i)
+          *reinterpret_cast<uint4*>(to + i * kPlane + at) = make_uint4(t[0][i], t[1][i], t[2][i], t[3][i]);
       }
-      const float total = w.total;
-      if (!gwarp_wait(&bar.l_done, n, abortf)) { ok = false; break; }
-      if (ONLY_STATE && !carries) continue;
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    // S <- e^B S + L of chunk n
+    auto gain = [&](int n, uint32_t l_columns) {
+      const float total = gates[n % kGateRing].total;
       tc_fence_after();
       if (holds) {
         uint32_t l[16];
-        tmem_ld_16x32(tmem + (static_cast<uint32_t>(32 * q) << 16) + kL + 32 * hf, l);
+        tmem_ld_16x32(tmem + (static_cast<uint32_t>(32 * q) << 16) + l_columns + 32 * hf, l);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 16; ++i) S[i] = fmaf(total, S[i], __uint_as_float(l[i]));
@@ -773,8 +795,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar.freed + s);
+        mbar_arrive(bar.freed + n % kStages);
         mbar_arrive(bar.gates_freed + n % kGateRing);
+      }
+    };
+    if constexpr (ONLY_STATE) {
+      // 16 warps scale; the gain of a chunk is taken while the next one's products run
+      const int g0 = warp * kGroups / 16, g1 = (warp + 1) * kGroups / 16;
+#pragma unroll 1
+      for (int n = 0; n <= count; ++n) {
+        if (n < count) {
+          const int s = n % kStages;
+          // the set's planes: the products of chunk n - 2 have read them
+          if (n >= 2 && !gwarp_wait(bar.l_done + (n & 1), (n >> 1) - 1, abortf)) break;
+          if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + n % kGateRing, n / kGateRing, abortf))
+            break;
+          scale_rows(smem + s * L::kStage + kKTile, gates[n % kGateRing], kp + (n & 1) * 3 * kPlane, g0, g1);
+          if (lane == 0) mbar_arrive(bar.k_ready + (n & 1));
+        }
+        if (n > 0 && carries) {
+          if (!gwarp_wait(bar.l_done + ((n - 1) & 1), (n - 1) >> 1, abortf)) break;
+          gain(n - 1, kL + 64 * ((n - 1) & 1));
+        }
+      }
+    } else {
+      // The score warps of a scheduler with fewer blocks of scores to form leave it more rows:
+      // sixteenths of a half chunk per warp 3 3 | 3 2 | 2 1 | 1 1.  (Two each: 10% slower.)
+      const int load = reverse ? 3 - q : q;   // 0: lightest score work
+      const int from16 = load == 0 ? 3 * hf : load == 1 ? 6 + 3 * hf : load == 2 ? 11 + 2 * hf : 14 + hf;
+      const int many16 = load == 0 ? 3 : load == 1 ? 3 - hf : load == 2 ? 2 - hf : 1;
+      const int g0 = from16 * kGroups / 32, g1 = (from16 + many16) * kGroups / 32;   // of a half
+#pragma unroll 1
+      for (int n = 0; n < count; ++n) {
+        const int s = n % kStages;
+        if (n > 0 && !gwarp_wait(&bar.state_read, n - 1, abortf)) break;
+        publish();
+        if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + n % kGateRing, n / kGateRing, abortf))
+          break;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          scale_rows(smem + s * L::kStage + kKTile, gates[n % kGateRing], kp, g0 + half * kGroups / 2, g1 + half * kGroups / 2);
+          if (lane == 0) mbar_arrive(bar.k_ready + half);
+        }
+        if (!gwarp_wait(bar.l_done, n, abortf)) break;
+        gain(n, kL);
       }
     }
     float* to = ONLY_STATE ? a.local + (bh * p.spans + span) * p.d * p.d
@@ -790,6 +854,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, kTmemColumns);
+  if (ONLY_STATE && threadIdx.x == 0)
+    a.decay[bh * p.spans + span] = exp2_of(add(ctl.decay[0], ctl.decay[1]), Sum{0.0f, 0.0f});
   if (!ONLY_STATE && *reinterpret_cast<volatile uint32_t*>(&ctl.bad) && !ctl.abort)
     redo_span(p, a, smem, bh, span, first * kTcChunk, min(p.N, (first + count) * kTcChunk));
 }
