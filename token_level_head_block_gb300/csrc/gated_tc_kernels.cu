@@ -72,7 +72,7 @@ struct ChunkGates {
 struct Bars {
   uint64_t full[kStages], freed[kStages], gates[kGateRing], gates_freed[kGateRing];
   uint64_t scores[2], p_ready[2];
-  uint64_t state_read, o1_read, out_done, out_read, k_ready[2], l_done[2], s_ready, fin[2];
+  uint64_t state_read, out_done, out_read, k_ready[2], l_done[2], s_ready, fin[2];
 };
 
 struct Control {
@@ -375,7 +375,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&bar.state_read, 1);
     mbar_init(&bar.out_done, 1);
-    mbar_init(&bar.o1_read, kOutWarps);
     mbar_init(&bar.out_read, kOutWarps);
     mbar_init(bar.l_done, 1);
     mbar_init(bar.l_done + 1, 1);
@@ -442,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (n < 0) continue;
         if (!gwarp_wait(&bar.s_ready, n, abortf)) break;
-        if (n > 0 && !gwarp_wait(&bar.o1_read, n - 1, abortf)) break;
+        if (n > 0 && !gwarp_wait(&bar.out_read, n - 1, abortf)) break;
         tc_fence_after();
         const uint64_t q = stage0 + s * (L::kStage >> 4), v = v0 + s * (L::kStage >> 4);
         if (leader) {
@@ -455,7 +454,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (!gwarp_wait(bar.p_ready + (n & 1), n >> 1, abortf)) break;
-        if (n > 0 && !gwarp_wait(&bar.out_read, n - 1, abortf)) break;
         tc_fence_after();
         const uint32_t pt = tmem + kScores + 128 * (n & 1);
         if (leader) {
@@ -665,53 +663,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             z[i] = part_in && part_row + 8 * i < rows ? *reinterpret_cast<const uint4*>(x + 8 * i * a.dot.sn)
                                                       : make_uint4(0u, 0u, 0u, 0u);
         }
-        // the queries have read the state: O1 is there, and the q tile is free
-        if (!gwarp_wait(bar.gates + n % kGateRing, n / kGateRing, abortf) || !gwarp_wait(&bar.state_read, n, abortf)) break;
+        const ChunkGates& w = gates[n % kGateRing];
+        if (!gwarp_wait(&bar.out_done, n, abortf)) break;
         tc_fence_after();
+        const bool steep = w.steep >> q & 1;
+        // o = f2 (f1 O1 + O2)
+        const float f1 = steep ? w.enter[q] * w.row[row] : w.enter[q], f2 = steep ? 1.0f : w.row[row];
+        float sum = 0.0f;
         uint8_t* mine = smem + s * L::kStage + 4096 * q + 2048 * half;
         if (a.dots) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) *staged(mine, part_row + 8 * i, part) = z[i];
           __syncwarp();
         }
-        const ChunkGates& w = gates[n % kGateRing];
-        const bool steep = w.steep >> q & 1;
-        // o = f2 (f1 O1 + O2)
-        const float f1 = steep ? w.enter[q] * w.row[row] : w.enter[q], f2 = steep ? 1.0f : w.row[row];
-        float x[32];
-        if (32 * half < DH) {
-          uint32_t r[32];
-          tmem_ld_x32(lanes + kO1 + 32 * half, r);
+#pragma unroll 1
+        for (int c = 32 * half; c < min(32 * half + 32, DH); c += 16) {
+          uint32_t x[16], y[16];
+          tmem_ld_x16(lanes + kO1 + c, x);
+          tmem_ld_x16(lanes + kO2 + c, y);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = f1 * __uint_as_float(r[i]);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.o1_read);
-        if (!gwarp_wait(&bar.out_done, n, abortf)) break;
-        tc_fence_after();
-        float sum = 0.0f;
-        if (32 * half < DH) {
+          for (int u = 0; u < 2; ++u) {
+            float o[8];
 #pragma unroll
-          for (int c = 0; c < 32; c += 16) {
-            uint32_t y[16];
-            tmem_ld_x16(lanes + kO2 + 32 * half + c, y);
-            tmem_ld_wait();
+            for (int e = 0; e < 8; ++e)
+              o[e] = f2 * fmaf(f1, __uint_as_float(x[8 * u + e]), __uint_as_float(y[8 * u + e]));
+            uint4* at = staged(mine, lane, (c & 31) / 8 + u);
+            if (a.dots) {
+              const uint4 r = *at;
+              const uint32_t zz[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              float o[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = f2 * (x[c + 8 * u + e] + __uint_as_float(y[8 * u + e]));
-              uint4* at = staged(mine, lane, c / 8 + u);
-              if (a.dots) {
-                const uint4 r = *at;
-                const uint32_t zz[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sum = fmaf(o[2 * e], low(zz[e]), fmaf(o[2 * e + 1], high(zz[e]), sum));
-              }
-              *at = make_uint4(pack(o[0], o[1]), pack(o[2], o[3]), pack(o[4], o[5]), pack(o[6], o[7]));
+              for (int e = 0; e < 4; ++e) sum = fmaf(o[2 * e], low(zz[e]), fmaf(o[2 * e + 1], high(zz[e]), sum));
             }
+            *at = make_uint4(pack(o[0], o[1]), pack(o[2], o[3]), pack(o[4], o[5]), pack(o[6], o[7]));
           }
         }
         tc_fence_before();
