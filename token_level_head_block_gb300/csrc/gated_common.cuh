@@ -59,17 +59,43 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 __device__ __forceinline__ float low(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float high(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
 
-// x, y as sums of NT bf16 terms, packed in pairs.
+// Two floats that one instruction works on.
+struct Two {
+  uint64_t v;
+};
+__device__ __forceinline__ Two two(float x, float y) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void apart(Two a, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// A pair as sums of NT bf16 terms, packed.
 template <int NT>
-__device__ __forceinline__ void split(float x, float y, uint32_t (&t)[NT]) {
+__device__ __forceinline__ void split(Two a, uint32_t (&t)[NT]) {
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
+    float x, y;
+    apart(a, x, y);
     t[i] = pack(x, y);
-    if (i + 1 < NT) {
-      x -= low(t[i]);
-      y -= high(t[i]);
-    }
+    if (i + 1 < NT) a = fma(two(low(t[i]), high(t[i])), two(-1.0f, -1.0f), a);
   }
+}
+template <int NT>
+__device__ __forceinline__ void split(float x, float y, uint32_t (&t)[NT]) {
+  split<NT>(two(x, y), t);
 }
 
 // A sum of log decays (in powers of two) as the sum of two floats: differences of

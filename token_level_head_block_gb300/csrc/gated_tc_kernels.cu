@@ -514,6 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(bar.l_done + (n & 1));
         }
         __syncwarp();
+        // chunk n + 2 into the stage of chunk n - 1, whose k was scaled before its products
+        if (n > 0 && n + kStages - 1 < count) {
+          if (!gwarp_wait(bar.l_done + ((n - 1) & 1), (n - 1) >> 1, abortf)) break;
+          load(n + kStages - 1);
+        }
+        continue;
       } else {
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
@@ -598,10 +604,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
               const float4 f = *reinterpret_cast<const float4*>(w.col[q] + j0 + j);
-              x[j] = __float_as_uint(__uint_as_float(x[j]) * f.x);
-              x[j + 1] = __float_as_uint(__uint_as_float(x[j + 1]) * f.y);
-              x[j + 2] = __float_as_uint(__uint_as_float(x[j + 2]) * f.z);
-              x[j + 3] = __float_as_uint(__uint_as_float(x[j + 3]) * f.w);
+              float y[4];
+              apart(mul(two(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), two(f.x, f.y)), y[0], y[1]);
+              apart(mul(two(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), two(f.z, f.w)), y[2], y[3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[j + e] = __float_as_uint(y[e]);
             }
             if (steep) {
               const float rw = w.row[row];
@@ -686,8 +693,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 0; u < 2; ++u) {
             float o[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              o[e] = f2 * fmaf(f1, __uint_as_float(x[8 * u + e]), __uint_as_float(y[8 * u + e]));
+            for (int e = 0; e < 8; e += 2)
+              apart(mul(two(f2, f2), fma(two(f1, f1), two(__uint_as_float(x[8 * u + e]), __uint_as_float(x[8 * u + e + 1])),
+                                         two(__uint_as_float(y[8 * u + e]), __uint_as_float(y[8 * u + e + 1])))),
+                    o[e], o[e + 1]);
             uint4* at = staged(mine, lane, (c & 31) / 8 + u);
             if (a.dots) {
               const uint4 r = *at;
@@ -757,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t y[4] = {x.x, x.y, x.z, x.w};
         uint32_t t[4][3];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split<3>(low(y[e]) * f, high(y[e]) * f, t[e]);
+        for (int e = 0; e < 4; ++e) split<3>(mul(two(low(y[e]), high(y[e])), two(f, f)), t[e]);
 #pragma unroll
         for (int i = 0; i < 3; ++i)
           *reinterpret_cast<uint4*>(to + i * kPlane + at) = make_uint4(t[0][i], t[1][i], t[2][i], t[3][i]);
@@ -774,7 +783,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_16x32(tmem + (static_cast<uint32_t>(32 * q) << 16) + l_columns + 32 * hf, l);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) S[i] = fmaf(total, S[i], __uint_as_float(l[i]));
+        for (int i = 0; i < 16; i += 2)
+          apart(fma(two(total, total), two(S[i], S[i + 1]), two(__uint_as_float(l[i]), __uint_as_float(l[i + 1]))), S[i],
+                S[i + 1]);
       }
       tc_fence_before();
       __syncwarp();
