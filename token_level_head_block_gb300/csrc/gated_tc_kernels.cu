@@ -26,6 +26,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "gated_common.cuh"
 #include "mhla_internal.h"
@@ -45,7 +46,6 @@ using namespace tc;
 constexpr int kScoreWarps = 8, kStateWarps = 8, kOutWarps = 8;   // in this order
 constexpr int kFirstOut = kScoreWarps + kStateWarps, kIssuer = kFirstOut + kOutWarps, kAdder = kIssuer + 1, kGates = kIssuer + 2;   // two of these
 constexpr int kThreads = 32 * (kGates + 2);
-constexpr int kStages = 3, kGateRing = 4;
 constexpr int kTileBytes = kTcChunk * 128;   // 128 rows of 64 channels, 128-byte swizzle
 constexpr int kPlane = kTileBytes;           // one term of the scaled k
 constexpr int kStatePlane = 64 * 128;        // one term of the state
@@ -69,10 +69,17 @@ struct ChunkGates {
   float pad[2];
 };
 
+// Of those, what a span's own state needs.
+struct StateGates {
+  float addw[kTcChunk];
+  float total;
+  float pad[3];
+};
+
 struct Bars {
-  uint64_t full[kStages], freed[kStages], gates[kGateRing], gates_freed[kGateRing];
+  uint64_t full[5], freed[5], gates[8], gates_freed[8];
   uint64_t scores[2], p_ready[2];
-  uint64_t state_read, out_done, out_read, k_ready[2], l_done[2], s_ready, fin[2];
+  uint64_t state_read, out_done, out_read, k_ready[2], half_done[2], l_done[2], s_ready, fin[2];
 };
 
 struct Control {
@@ -85,15 +92,16 @@ struct Control {
 template <bool ONLY_STATE>
 struct Layout {
   static constexpr int kTiles = ONLY_STATE ? 2 : 3;   // q, k, v  |  k, v
+  static constexpr int kStages = ONLY_STATE ? 5 : 3, kGateRing = ONLY_STATE ? 8 : 4;
+  using Gates = typename std::conditional<ONLY_STATE, StateGates, ChunkGates>::type;
   static constexpr int kStage = kTiles * kTileBytes;
   static constexpr int kKp = kStages * kStage;
-  static constexpr int kSets = ONLY_STATE ? 2 : 1;     // of the scaled k's planes
-  static constexpr int kS = kKp + kSets * 3 * kPlane;
+  static constexpr int kS = kKp + 3 * kPlane;
   static constexpr int kGates = kS + (ONLY_STATE ? 0 : 2 * kStatePlane);
-  static constexpr int kControl = kGates + kGateRing * static_cast<int>(sizeof(ChunkGates));
+  static constexpr int kControl = kGates + kGateRing * static_cast<int>(sizeof(Gates));
   static constexpr size_t kBytes = kControl + sizeof(Control) + 1024;
 };
-static_assert(Layout<false>::kBytes <= 227 * 1024, "shared memory of one CTA");
+static_assert(Layout<false>::kBytes <= 227 * 1024 && Layout<true>::kBytes <= 227 * 1024, "shared memory of one CTA");
 
 // A look that may suspend the thread up to `ns`: a waiting warp that does not poll leaves
 // its issue slots to the others.
@@ -173,7 +181,7 @@ __device__ __forceinline__ Sum shfl_sum(Sum s, int lane) {
 
 // One warp: the running sums and the weights of a chunk (ONLY_STATE: those of the state alone).  Returns B.
 template <bool ONLY_STATE>
-__device__ __forceinline__ Sum chunk_gates(float4 g, ChunkGates& out, const Scan& a, int lane) {
+__device__ __forceinline__ Sum chunk_gates(float4 g, typename Layout<ONLY_STATE>::Gates& out, const Scan& a, int lane) {
   const Sum none = {0.0f, 0.0f};
   Sum at[4];
   at[0] = gate_sum(g.x);
@@ -206,8 +214,7 @@ __device__ __forceinline__ Sum chunk_gates(float4 g, ChunkGates& out, const Scan
     for (int e = 0; e < 4; ++e) addw[e] = a.k_scale * (reverse ? exp2_of(at[e], none) : exp2_of(all, at[e]));
     put(out.addw, addw);
     if (lane == 0) out.total = exp2_of(all, none);
-    return all;
-  }
+  } else {
   const Sum edge[5] = {none, shfl_sum(run, 7), shfl_sum(run, 15), shfl_sum(run, 23), all};
   Sum m = reverse ? edge[1] : edge[0];
 #pragma unroll
@@ -246,6 +253,7 @@ __device__ __forceinline__ Sum chunk_gates(float4 g, ChunkGates& out, const Scan
 #pragma unroll
     for (int r = 0; r < 4; ++r) steep |= (lanes >> (8 * r) & 0xFFu) ? 1u << r : 0u;
     out.steep = steep;
+  }
   }
   return all;
 }
@@ -338,11 +346,13 @@ template <int DH, bool ONLY_STATE>
 __global__ void __launch_bounds__(kThreads, 1)
     gated_tc_scan(const __grid_constant__ ScanSet p, const __grid_constant__ TcMaps maps) {
   using L = Layout<ONLY_STATE>;
+  constexpr int kStages = L::kStages, kGateRing = L::kGateRing;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
   uint8_t* kp = smem + L::kKp;
   uint8_t* planes = smem + L::kS;
-  ChunkGates* gates = reinterpret_cast<ChunkGates*>(smem + L::kGates);
+  auto* gates = reinterpret_cast<typename L::Gates*>(smem + L::kGates);
+  const ChunkGates* chunk_gate_ring = reinterpret_cast<const ChunkGates*>(gates);   // score and output warps
   Control& ctl = *reinterpret_cast<Control*>(smem + L::kControl);
   Bars& bar = ctl.bars;
   volatile uint32_t* abortf = &ctl.abort;
@@ -376,6 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar.state_read, 1);
     mbar_init(&bar.out_done, 1);
     mbar_init(&bar.out_read, kOutWarps);
+    mbar_init(bar.half_done, 1);
+    mbar_init(bar.half_done + 1, 1);
     mbar_init(bar.l_done, 1);
     mbar_init(bar.l_done + 1, 1);
     mbar_init(&bar.s_ready, kStateWarps);
@@ -499,45 +511,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; ok && n < count; ++n) {
       const int s = n % kStages;
       if (!gwarp_wait(bar.full + s, n / kStages, abortf)) break;
-      if constexpr (ONLY_STATE) {
-        // two sets of planes and two accumulators: k of one chunk is scaled while another's products run
-        if (!gwarp_wait(bar.k_ready + (n & 1), n >> 1, abortf)) break;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        if (!gwarp_wait(bar.k_ready + half, n, abortf)) { ok = false; break; }
         tc_fence_after();
-        const uint64_t k = k0 + (n & 1) * (3 * kPlane / 16), v = v0 + s * (L::kStage >> 4);
+        const uint64_t k = k0 + half * (4 * 2 * kSbo / 16), v = v0 + s * (L::kStage >> 4) + half * (4 * 2 * kSbo / 16);
+        const uint32_t l = tmem + kL + (ONLY_STATE ? 64 * (n & 1) : 0);   // the state alone: two accumulators
         if (leader) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
+          for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
             for (int t = 0; t < 3; ++t)
-              mma_bf16(tmem + kL + 64 * (n & 1), k + (t * kPlane + ks * 2 * kSbo) / 16, v + ks * 2 * kSbo / 16, idesc,
-                       ks + t > 0);
-          mma_commit(bar.l_done + (n & 1));
+              mma_bf16(l, k + (t * kPlane + ks * 2 * kSbo) / 16, v + ks * 2 * kSbo / 16, idesc, half + ks + t > 0);
+          if (ONLY_STATE) mma_commit(bar.half_done + half);
+          if (half) mma_commit(bar.l_done + (ONLY_STATE ? n & 1 : 0));
         }
         __syncwarp();
-        // chunk n + 2 into the stage of chunk n - 1, whose k was scaled before its products
+      }
+      if (!ok) break;
+      if (ONLY_STATE) {
+        // the next chunk into the stage of chunk n - 1, whose k was scaled before its products
         if (n > 0 && n + kStages - 1 < count) {
           if (!gwarp_wait(bar.l_done + ((n - 1) & 1), (n - 1) >> 1, abortf)) break;
           load(n + kStages - 1);
         }
         continue;
-      } else {
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (!gwarp_wait(bar.k_ready + half, n, abortf)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t k = k0 + half * (4 * 2 * kSbo / 16), v = v0 + s * (L::kStage >> 4) + half * (4 * 2 * kSbo / 16);
-          if (leader) {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-              for (int t = 0; t < 3; ++t)
-                mma_bf16(tmem + kL, k + (t * kPlane + ks * 2 * kSbo) / 16, v + ks * 2 * kSbo / 16, idesc,
-                         half + ks + t > 0);
-            if (half) mma_commit(bar.l_done);
-          }
-          __syncwarp();
-        }
-        if (!ok) break;
       }
       // chunk n + 2 into the stage of chunk n - 1, once that is done with
       if (n > 0 && n + kStages - 1 < count) {
@@ -563,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; n < count; ++n) {
       const int s = n % kStages;
       if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + n % kGateRing, n / kGateRing, abortf)) break;
-      const ChunkGates& w = gates[n % kGateRing];
+      const ChunkGates& w = chunk_gate_ring[n % kGateRing];
       // rows of v that are not finite (this warp looks at 32 of them, half a row a lane)
       {
         const uint8_t* v = smem + s * L::kStage + kVTile;
@@ -670,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             z[i] = part_in && part_row + 8 * i < rows ? *reinterpret_cast<const uint4*>(x + 8 * i * a.dot.sn)
                                                       : make_uint4(0u, 0u, 0u, 0u);
         }
-        const ChunkGates& w = gates[n % kGateRing];
+        const ChunkGates& w = chunk_gate_ring[n % kGateRing];
         if (!gwarp_wait(&bar.out_done, n, abortf)) break;
         tc_fence_after();
         const bool steep = w.steep >> q & 1;
@@ -757,12 +755,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // k's rows, kRows at once, eight channels a lane: scaled and split into the planes.
     constexpr int kLanes = DH / 8, kRows = 32 / kLanes, kGroups = kTcChunk / kRows;
     const int kr = lane / kLanes, ku = lane % kLanes;
-    auto scale_rows = [&](const uint8_t* k, const ChunkGates& w, uint8_t* to, int g0, int g1) {
+    auto scale_rows = [&](const uint8_t* k, const float* addw, uint8_t* to, int g0, int g1) {
 #pragma unroll 1
       for (int g = g0; g < g1; ++g) {
         const int token = kRows * g + kr, at = unit_at(token, ku);
         const uint4 x = *reinterpret_cast<const uint4*>(k + at);
-        const float f = w.addw[token];
+        const float f = addw[token];
         const uint32_t y[4] = {x.x, x.y, x.z, x.w};
         uint32_t t[4][3];
 #pragma unroll
@@ -795,18 +793,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     if constexpr (ONLY_STATE) {
-      // 16 warps scale; the gain of a chunk is taken while the next one's products run
-      const int g0 = warp * kGroups / 16, g1 = (warp + 1) * kGroups / 16;
+      // 16 warps scale, a half of the planes as soon as the products of the chunk before have
+      // read it; the gain of a chunk is taken while the next one's products run
+      const int g0 = warp * kGroups / 32, g1 = (warp + 1) * kGroups / 32;   // of a half
+      bool ok = true;
 #pragma unroll 1
-      for (int n = 0; n <= count; ++n) {
+      for (int n = 0; ok && n <= count; ++n) {
         if (n < count) {
           const int s = n % kStages;
-          // the set's planes: the products of chunk n - 2 have read them
-          if (n >= 2 && !gwarp_wait(bar.l_done + (n & 1), (n >> 1) - 1, abortf)) break;
           if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + n % kGateRing, n / kGateRing, abortf))
             break;
-          scale_rows(smem + s * L::kStage + kKTile, gates[n % kGateRing], kp + (n & 1) * 3 * kPlane, g0, g1);
-          if (lane == 0) mbar_arrive(bar.k_ready + (n & 1));
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            if (n > 0 && !gwarp_wait(bar.half_done + half, n - 1, abortf)) { ok = false; break; }
+            scale_rows(smem + s * L::kStage + kKTile, gates[n % kGateRing].addw, kp, g0 + half * kGroups / 2,
+                       g1 + half * kGroups / 2);
+            if (lane == 0) mbar_arrive(bar.k_ready + half);
+          }
+          if (!ok) break;
         }
         if (n > 0 && carries) {
           if (!gwarp_wait(bar.l_done + ((n - 1) & 1), (n - 1) >> 1, abortf)) break;
@@ -829,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          scale_rows(smem + s * L::kStage + kKTile, gates[n % kGateRing], kp, g0 + half * kGroups / 2, g1 + half * kGroups / 2);
+          scale_rows(smem + s * L::kStage + kKTile, gates[n % kGateRing].addw, kp, g0 + half * kGroups / 2, g1 + half * kGroups / 2);
           if (lane == 0) mbar_arrive(bar.k_ready + half);
         }
         if (!gwarp_wait(bar.l_done, n, abortf)) break;
