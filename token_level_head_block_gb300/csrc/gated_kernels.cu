@@ -261,17 +261,27 @@ struct RowLoader {
         }
       }
     } else {
-      for (int i = threadIdx.x; i < kChunk * W / 2; i += 128) {
-        const int r = i / (W / 2), c = 2 * (i % (W / 2));
-        const T* x = src + (chunk * kChunk + r) * step + c;
-        float a = r < rows && c < width ? to_f(x[0]) : 0.0f, e = r < rows && c + 1 < width ? to_f(x[1]) : 0.0f;
+      constexpr int kPairs = kChunk * W / 2 / 128, kBatch = kPairs < 8 ? kPairs : 8;   // loads in flight
+      for (int i0 = 0; i0 < kPairs; i0 += kBatch) {
+        float a[kBatch], e[kBatch];
 #pragma unroll
-        for (int n = 0; n < Terms<T>::kIn; ++n) {
-          const uint32_t p = pack(a, e);
-          *reinterpret_cast<uint32_t*>(dst + n * kChunk * W * 2 + unit_at<W>(r, c >> 3) + (c & 7) * 2) = p;
-          // an infinity is its first term alone
-          a = fabsf(low(p)) < __int_as_float(0x7F800000) ? a - low(p) : 0.0f;
-          e = fabsf(high(p)) < __int_as_float(0x7F800000) ? e - high(p) : 0.0f;
+        for (int j = 0; j < kBatch; ++j) {
+          const int i = threadIdx.x + 128 * (i0 + j), r = i / (W / 2), c = 2 * (i % (W / 2));
+          const T* x = src + (chunk * kChunk + r) * step + c;
+          a[j] = r < rows && c < width ? to_f(x[0]) : 0.0f;
+          e[j] = r < rows && c + 1 < width ? to_f(x[1]) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int i = threadIdx.x + 128 * (i0 + j), r = i / (W / 2), c = 2 * (i % (W / 2));
+#pragma unroll
+          for (int n = 0; n < Terms<T>::kIn; ++n) {
+            const uint32_t p = pack(a[j], e[j]);
+            *reinterpret_cast<uint32_t*>(dst + n * kChunk * W * 2 + unit_at<W>(r, c >> 3) + (c & 7) * 2) = p;
+            // an infinity is its first term alone
+            a[j] = fabsf(low(p)) < __int_as_float(0x7F800000) ? a[j] - low(p) : 0.0f;
+            e[j] = fabsf(high(p)) < __int_as_float(0x7F800000) ? e[j] - high(p) : 0.0f;
+          }
         }
       }
     }
@@ -838,12 +848,18 @@ __global__ void __launch_bounds__(256) gated_gate_grad(const __grid_constant__ G
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t dd = static_cast<int64_t>(p.d) * p.d;
   float s = 0.0f;
+  const int d = p.d;
   if (span + 1 < p.spans) {
     const float *x = p.enter + (bh * p.spans + span + 1) * dd, *y = p.leave + (bh * p.spans + span) * dd;
-    for (int64_t i = threadIdx.x; i < dd; i += 256) s = fmaf(x[i], y[i], s);
+#pragma unroll 8
+    for (int i = threadIdx.x; i < d * d; i += 256) s = fmaf(x[i], y[i], s);
   } else if (p.dlast) {
     const float *x = p.last + bh * dd, *y = p.dlast + bh * dd;
-    for (int64_t i = threadIdx.x; i < dd; i += 256) s = fmaf(x[i], y[i % p.d * p.d + i / p.d], s);
+#pragma unroll 8
+    for (int i = threadIdx.x; i < d * d; i += 256) {
+      const uint32_t r = static_cast<uint32_t>(i) / static_cast<uint32_t>(d), c = i - r * d;
+      s = fmaf(x[i], y[c * d + r], s);
+    }
   }
 #pragma unroll
   for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(~0u, s, k);
@@ -907,7 +923,7 @@ Cut cut_for(const GatedProblem& p, int scans) {
   const int64_t have = p.B * p.H * (p.d > 64 ? 2 : 1) * scans;
   const int64_t room = int64_t{kSms} * 3;
   int64_t spans = std::max<int64_t>(1, room / have);
-  c.span_chunks = std::max<int64_t>(4, (c.chunks + spans - 1) / spans);
+  c.span_chunks = (c.chunks + spans - 1) / spans;
   c.spans = (c.chunks + c.span_chunks - 1) / c.span_chunks;
   return c;
 }
