@@ -1045,8 +1045,21 @@ struct Runner {
   }
 };
 
-// Short sequences leave most of a 128-token tile empty.
-bool wants_tc(const GatedProblem& p) { return tc_supported(p) && p.N >= 128; }
+// Which kernel takes operands that suit both.  tcgen05 runs one CTA an SM at half to a third of
+// mma.sync's time a token, but starts slowly (6 us a wave of CTAs) and cuts long sequences of
+// few heads into fewer, longer spans.  Measured, mma.sync against tcgen05 in us:
+//   up to 384 tokens, one wave         d 64, 48 heads x 256 forwards: 18.4, 10.1;   d 32: 11.5, 8.7
+//   longer, d > 32: enough tokens      16 heads x 2048: 25.6, 21.9;   1 x 16384: 35.5, 23.5;   4 x 1024: 15.5, 18.5
+//   longer, d <= 32: whole sequences   128 heads x 1024: 35.0, 20.7;   48 x 1024 (two launches): 17.8, 20.5
+//   several waves: enough chunks each  d 64, 512 x 256: 47.8, 37.9;  512 x 128: 28.2, 29.5;
+//                                      d 32, 512 x 1024: 92.0, 76.2;  512 x 512: 43.8, 47.4
+bool wants_tc(const GatedProblem& p, int scans) {
+  if (!tc_supported(p) || p.N < 128) return false;
+  const int64_t ctas = p.B * p.H * scans;
+  if (ctas > kSms) return p.N >= (p.d <= 32 ? 1024 : 256);
+  if (p.N <= 384) return true;
+  return p.d <= 32 ? 2 * ctas > kSms : ctas * p.N >= 16384;
+}
 
 }  // namespace
 
@@ -1067,7 +1080,7 @@ int launch_gated_forward(const GatedProblem& p, const float* state_in, const Ope
   Runner r{p, false, rows_of_16(p, {&p.q, &p.k, &p.v, &out}), {}, static_cast<cudaStream_t>(stream)};
   ScanSet set = {};
   set.scan[0] = a;
-  r.tc = r.async && wants_tc(p) && tc_maps(p, set, 1, &r.maps);
+  r.tc = r.async && wants_tc(p, 1) && tc_maps(p, set, 1, &r.maps);
   const Cut c = r.tc ? tc_cut(p, 1) : cut_for(p, 1);
   set = scan_set(p, c);
   char* base = static_cast<char*>(workspace);
@@ -1077,9 +1090,9 @@ int launch_gated_forward(const GatedProblem& p, const float* state_in, const Ope
   set.scan[0] = a;
   if (c.spans > 1) {
     int rc = r.run(set, 1, true);
-    // A few spans are joined by the scan as it starts; a launch for it costs 5 us, sixteen
-    // loads of an L2 hit each about 4.
-    const bool join = r.tc && c.spans <= 16;
+    // A few spans are joined by the scan as it starts: a launch for it costs 4 us, a span's
+    // loads from L2 0.7.
+    const bool join = r.tc && c.spans <= 6;
     if (rc == MHLA_OK && !join) rc = run_join(set, 1, r.s);
     if (rc != MHLA_OK) return rc;
     set.scan[0].join = join;
@@ -1113,7 +1126,7 @@ int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* w
            static_cast<cudaStream_t>(stream)};
   ScanSet set = {};
   set.scan[0] = dq; set.scan[1] = dk; set.scan[2] = dv;
-  r.tc = r.async && wants_tc(p) && tc_maps(p, set, 3, &r.maps);
+  r.tc = r.async && wants_tc(p, 3) && tc_maps(p, set, 3, &r.maps);
   const Cut c = r.tc ? tc_cut(p, 3) : cut_for(p, 3);
   const int64_t bh = p.B * p.H;
   char* base = static_cast<char*>(workspace);

@@ -103,23 +103,9 @@ struct Layout {
 };
 static_assert(Layout<false>::kBytes <= 227 * 1024 && Layout<true>::kBytes <= 227 * 1024, "shared memory of one CTA");
 
-// A look that may suspend the thread up to `ns`: a waiting warp that does not poll leaves
-// its issue slots to the others.
-__device__ __forceinline__ bool mbar_try_wait_up_to(uint64_t* bar, uint32_t parity, uint32_t ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
-      : "memory");
-  return ok != 0;
-}
-
 // Every lane waits, then the warp agrees; the first look is in place.
 __device__ __forceinline__ bool gwarp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abortf) {
-  bool ok = mbar_try_wait_up_to(bar, parity & 1u, 1000000u);
+  bool ok = mbar_try_wait(bar, parity & 1u);
   if (!ok) ok = wait_bounded_on(bar, parity & 1u, abortf, &g_gated_error);
   return __all_sync(0xffffffffu, ok);
 }
@@ -258,20 +244,33 @@ __device__ __forceinline__ Sum chunk_gates(float4 g, typename Layout<ONLY_STATE>
   return all;
 }
 
-// Element (r, c) of the state that enters a span: init's, or (join) the state that enters the
-// sequence carried through the spans in front, whose own contributions lie in local.
-__device__ __forceinline__ float entering(const Scan& a, int64_t bh, int64_t span, int32_t spans, int d, int r, int c) {
+// Elements of the state that enters a span: init's, or (join) the state that enters the sequence
+// carried through the spans in front, whose own contributions lie in local.  place(i, r, c)
+// gives the i-th element's row and column, or false; a span's loads are in flight together.
+template <int COUNT, typename Place>
+__device__ __forceinline__ void entering(float (&S)[COUNT], const Scan& a, int64_t bh, int64_t span, int32_t spans, int d,
+                                         Place place) {
   const int64_t dd = static_cast<int64_t>(d) * d;
-  const int at = a.init_transposed ? c * d + r : r * d + c;
   const float* in = a.init ? a.init + (bh * a.init_spans + (a.init_spans > 1 ? span : 0)) * dd : nullptr;
-  float x = in ? in[at] : 0.0f;
-  if (a.join) {
-    const int64_t from = bh * spans;
-#pragma unroll 4
-    for (int64_t s = 0; s < span; ++s)
-      x = fmaf(a.decay[from + s], x, a.local[(from + s) * dd + r * d + c]);
+#pragma unroll
+  for (int i = 0; i < COUNT; ++i) {
+    int r, c;
+    S[i] = place(i, r, c) && in ? in[a.init_transposed ? c * d + r : r * d + c] : 0.0f;
   }
-  return x;
+  if (!a.join) return;
+  const float* local = a.local + bh * spans * dd;
+#pragma unroll 1
+  for (int64_t s = 0; s < span; ++s, local += dd) {
+    const float decay = a.decay[bh * spans + s];
+    float l[COUNT];
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+      int r, c;
+      l[i] = place(i, r, c) ? local[r * d + c] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) S[i] = fmaf(decay, S[i], l[i]);
+  }
 }
 
 // A whole span again, token by token without the tensor core: for a span whose v held an
@@ -287,11 +286,11 @@ __device__ __noinline__ void redo_span(const ScanSet& p, const Scan& a, uint8_t*
     return static_cast<__nv_bfloat16*>(o.data) + b * o.sb + t * o.sn + h * o.sh;
   };
   float S[8];   // rows 8 g .. of column c
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 8 * g + i;
-    S[i] = r < d && c < d ? entering(a, bh, span, p.spans, d, r, c) : 0.0f;
-  }
+  entering(S, a, bh, span, p.spans, d, [&](int i, int& r, int& col) {
+    r = 8 * g + i;
+    col = c;
+    return r < d && c < d;
+  });
 #pragma unroll 1
   for (int64_t i = 0; i < t1 - t0; ++i) {
     const int64_t t = a.reverse ? t1 - 1 - i : t0 + i;
@@ -730,10 +729,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r0 = 16 * q + (lane >> 2), c0 = 32 * hf + 2 * (lane & 3);
     const bool holds = carries && 16 * q < DH && 32 * hf < DH;   // of the state
     float S[16];
+    if constexpr (ONLY_STATE) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = r0 + 8 * ((i >> 1) & 1), c = c0 + 8 * (i >> 2) + (i & 1);
-      S[i] = !ONLY_STATE && holds && r < p.d && c < p.d ? entering(a, bh, span, p.spans, p.d, r, c) : 0.0f;
+      for (int i = 0; i < 16; ++i) S[i] = 0.0f;
+    } else {
+      entering(S, a, bh, span, p.spans, p.d, [&](int i, int& r, int& c) {
+        r = r0 + 8 * ((i >> 1) & 1);
+        c = c0 + 8 * (i >> 2) + (i & 1);
+        return holds && r < p.d && c < p.d;
+      });
     }
     auto publish = [&]() {
       if (holds) {
@@ -890,12 +894,13 @@ bool tc_supported(const GatedProblem& p) {
   return p.dtype == MHLA_BF16 && p.d <= 64 && p.d % 8 == 0 && p.N < (int64_t{1} << 31) - kTcChunk;
 }
 
-// One CTA an SM: as many spans as fill the SMs once, none shorter than two chunks.
+// One CTA an SM: as many spans as fill the SMs once, none shorter than two chunks; up to four
+// chunks stay whole (a chunk takes 2.4 us; a second span's launch and start more than two of them).
 Cut tc_cut(const GatedProblem& p, int scans) {
   Cut c;
   c.chunks = (p.N + kTcChunk - 1) / kTcChunk;
   const int64_t spans = std::max<int64_t>(1, kSms / (p.B * p.H * scans));
-  c.span_chunks = std::max<int64_t>(2, (c.chunks + spans - 1) / spans);
+  c.span_chunks = c.chunks <= 4 ? c.chunks : std::max<int64_t>(2, (c.chunks + spans - 1) / spans);
   c.spans = (c.chunks + c.span_chunks - 1) / c.span_chunks;
   return c;
 }
