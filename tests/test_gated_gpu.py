@@ -86,6 +86,19 @@ SHAPES = [(1, 1, 1, 64), (2, 2, 3, 64), (1, 63, 2, 32), (2, 64, 2, 64), (1, 65, 
           (40, 70, 9, 32)]
 
 
+# bf16 on the tcgen05 kernel: more chunks than its stages, a last chunk of one token, few spans (joined by
+# the scan) and more of them (joined apart), several waves, 32 and 64 channels whole and in part
+TC_SHAPES = [(2, 769, 11, 64), (4, 1000, 6, 64), (1, 2300, 12, 40), (1, 5000, 4, 64), (10, 520, 8, 32), (10, 641, 8, 24),
+             (16, 300, 10, 64), (20, 1030, 8, 8)]
+
+
+@pytest.mark.parametrize("B,N,H,d", TC_SHAPES)
+@pytest.mark.parametrize("state", [True, False], ids=["state", "empty"])
+def test_forward_of_many_tokens(B, N, H, d, state):
+    x = draw(N + H, B, N, H, d, "bf16", state)
+    check_forward(x, "bf16", d ** -0.5, *run_forward(x, d ** -0.5))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,N,H,d", SHAPES)
 @pytest.mark.parametrize("state", [True, False], ids=["state", "empty"])
@@ -130,6 +143,13 @@ def test_backward(B, N, H, d, dtype, state):
     check_backward(x, dtype, d ** -0.5, run_backward(x, d ** -0.5))
 
 
+@pytest.mark.parametrize("B,N,H,d", [(1, 769, 4, 64), (2, 520, 6, 40), (1, 1500, 5, 64), (20, 1030, 8, 8), (7, 300, 8, 64)])
+@pytest.mark.parametrize("state", [True, False], ids=["state", "empty"])
+def test_backward_of_many_tokens(B, N, H, d, state):
+    x = draw(N + H, B, N, H, d, "bf16", state)
+    check_backward(x, "bf16", d ** -0.5, run_backward(x, d ** -0.5))
+
+
 def test_backward_against_differences_of_the_forward():
     """Central differences of the framework's own forward, float32, along a direction per input.
 
@@ -167,13 +187,14 @@ def test_closed_gates_start_afresh(dtype):
     check_backward(x, dtype, 0.125, run_backward(x, 0.125))
 
 
-@pytest.mark.parametrize("value", [0.0, -0.7, -30.0])
-def test_constant_gates_over_a_long_sequence(value):
-    """No forgetting at all, a short memory whose far pairs vanish, and almost none."""
-    x = draw(22, 1, 1500, 1, 32, "f32")
+@pytest.mark.parametrize("dtype,H,d", [("f32", 1, 32), ("bf16", 11, 64)], ids=["f32", "bf16"])
+@pytest.mark.parametrize("value", [0.0, -0.7, -2.0, -30.0])
+def test_constant_gates_over_a_long_sequence(value, dtype, H, d):
+    """No forgetting at all, short memories whose far pairs vanish, and almost none."""
+    x = draw(22, 1, 1500, H, d, dtype)
     x["g"][:] = value
-    check_forward(x, "f32", 1.0, *run_forward(x, 1.0))
-    check_backward(x, "f32", 1.0, run_backward(x, 1.0))
+    check_forward(x, dtype, 1.0, *run_forward(x, 1.0))
+    check_backward(x, dtype, 1.0, run_backward(x, 1.0))
 
 
 def test_padding_tokens_leave_the_state():
@@ -338,3 +359,75 @@ def test_nan_stays_in_its_head():
     assert np.isnan(out[0, 70:, 1, 3]).all() and np.isnan(last[0, 1, :, 3]).all()
     out[0, 70:, 1, 3] = last[0, 1, :, 3] = 0
     assert np.isfinite(out).all() and np.isfinite(last).all()   # no other channel, head or earlier token
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("N,H,d", [(60, 2, 32), (150, 2, 64), (1500, 11, 64), (150, 2, 100)])
+def test_what_is_not_finite_reaches_no_earlier_token(N, H, d, bad):
+    """One value of v: its channel from its token on; one of k: the channels of v from its token on."""
+    at = N // 2 + 5
+    for name in ("v", "k"):
+        x = draw(35, 1, N, H, d, "bf16")
+        plain, _ = run_forward(x, 0.125)
+        x[name][0, at, 1, 3] = bad
+        out, last = run_forward(x, 0.125)
+        out, last, plain = f64(out), f64(last), f64(plain)
+        touched = (slice(None), 1, 3) if name == "v" else (slice(None), 1)
+        assert not np.isfinite(out[0, at:][touched]).any() and np.isfinite(out[0, :at]).all()
+        assert np.isfinite(out[0, :, 0]).all() and np.isfinite(last[0, 0]).all() and not np.isfinite(last[0, 1, 3, 3])
+        if name == "v":
+            assert np.isfinite(np.delete(out[0, :, 1], 3, axis=1)).all() and np.isfinite(np.delete(last[0, 1], 3, axis=1)).all()
+        # earlier tokens: the plain values, each side within 2^-8 of its own and 2^-15 of A of the exact one
+        size = oracle.gated(*(np.abs(f64(x[n]))[:, :at] for n in "qkv"), f64(x["g"])[:, :at], 0.125, magnitude(f64(x["state"])))[0]
+        assert (np.abs(out[:, :at] - plain[:, :at]) <= 2.0 ** -7 * np.abs(plain[:, :at]) + 2.0 ** -13 * size).all()
+
+
+@pytest.mark.parametrize("N,H", [(150, 2), (1500, 4)])
+def test_a_gradient_that_is_not_finite_reaches_no_later_token(N, H):
+    """dout of one token: dk and dv of its token and earlier, dq of itself."""
+    x = draw(36, 1, N, H, 64, "bf16")
+    at = N // 2 + 5
+    x["dout"][0, at, 1, 3] = float("nan")
+    dq, dk, dv, dg, dstate = (f64(t) for t in run_backward(x, 0.125))
+    assert np.isfinite(dk[0, at + 1:]).all() and np.isfinite(dv[0, at + 1:]).all() and np.isfinite(dg[0, at + 1:]).all()
+    assert np.isnan(dv[0, :at + 1, 1, 3]).all() and np.isfinite(np.delete(dv[0, :, 1], 3, axis=1)).all()
+    assert np.isfinite(np.delete(dq[0, :, 1], at, axis=0)).all() and np.isnan(dq[0, at, 1]).all()
+    for t in (dq, dk, dv):
+        assert np.isfinite(t[0, :, 0]).all()
+    assert np.isfinite(dstate[0, 0]).all()
+
+
+def test_a_gate_that_is_nan_reaches_no_earlier_token():
+    for N, H in ((60, 2), (150, 2), (1500, 11)):
+        x = draw(37, 1, N, H, 64, "bf16")
+        at = N // 2 + 5
+        x["g"][0, at, 1] = float("nan")
+        out, last = (f64(t) for t in run_forward(x, 0.125))
+        assert np.isfinite(out[0, :at]).all() and np.isnan(out[0, at:, 1]).all() and np.isfinite(out[0, :, 0]).all()
+        assert np.isnan(last[0, 1]).all() and np.isfinite(last[0, 0]).all()
+
+
+def raw_status():
+    """(status, flags) of mhla_device_status without raising."""
+    import ctypes
+    flags = ctypes.c_uint32(0)
+    st = mhla.lib().mhla_device_status(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream) or None,
+                                       ctypes.byref(flags))
+    return int(st), int(flags.value)
+
+
+# the output warps: the ones whose waits outlast a first look (the hook acts on those alone)
+@pytest.mark.parametrize("warp", [16, 23])
+def test_a_wait_that_gives_up_is_reported_and_the_context_recovers(warp):
+    x = draw(38, 4, 1000, 6, 64, "bf16")
+    assert raw_status() == (0, 0)
+    mhla.debug_stall_waits(warp, 1_000_000)
+    try:
+        mhla.gated_forward(*(gpu(x[n]) for n in ("q", "k", "v", "g")), scale=0.125, state=gpu(x["state"]))
+        torch.cuda.synchronize()
+        status, flags = raw_status()
+    finally:
+        mhla.debug_stall_waits(-1)
+    assert status == 5 and flags & 1 and not flags & 2, (status, flags)
+    assert raw_status() == (0, 0)
+    check_forward(x, "bf16", 0.125, *run_forward(x, 0.125))

@@ -103,10 +103,32 @@ struct Layout {
 };
 static_assert(Layout<false>::kBytes <= 227 * 1024 && Layout<true>::kBytes <= 227 * 1024, "shared memory of one CTA");
 
+// A wait whose first look failed: bounded like tc::wait_bounded_on, the diagnostic hook
+// (stall_hook.cuh) looked at before the next poll.
+__device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, volatile uint32_t* abortf) {
+  if (stall_this_warp()) {
+    stalled_wait(abortf);
+    *abortf = 1u;
+    atomicOr(&g_gated_error, 1u);
+    return false;
+  }
+  const uint64_t t0 = globaltimer();
+  for (uint32_t it = 1; it < kWaitLimitPolls; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*abortf) return false;
+      if (globaltimer() - t0 > kWaitLimitNs) break;
+    }
+  }
+  *abortf = 1u;
+  atomicOr(&g_gated_error, 1u);
+  return false;
+}
+
 // Every lane waits, then the warp agrees; the first look is in place.
 __device__ __forceinline__ bool gwarp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abortf) {
   bool ok = mbar_try_wait(bar, parity & 1u);
-  if (!ok) ok = wait_bounded_on(bar, parity & 1u, abortf, &g_gated_error);
+  if (!ok) ok = wait_longer(bar, parity & 1u, abortf);
   return __all_sync(0xffffffffu, ok);
 }
 
