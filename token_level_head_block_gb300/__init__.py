@@ -482,22 +482,24 @@ _CODES = {}
 
 
 def _dtype_code(x):
-    import torch
-    if not _CODES:
-        _CODES.update({torch.bfloat16: 0, torch.float32: 1})
     code = _CODES.get(x.dtype)
     if code is None:
-        raise ValueError(f"unsupported dtype {x.dtype}")
+        import torch
+        _CODES.update({torch.bfloat16: 0, torch.float32: 1})
+        code = _CODES.get(x.dtype)
+        if code is None:
+            raise ValueError(f"unsupported dtype {x.dtype}")
     return code
 
 
-# These two pack the C struct directly: serving makes such a call per token, and
-# filling a ctypes structure field by field costs more than the launch.
+# These two pack the C struct directly, and _launch takes its arguments as they are: serving
+# makes such a call per token, and filling a ctypes structure field by field costs
+# more than the launch.
 def _heads(x):
     """mhla_tensor_t of a [B, N, H, d] tensor."""
     B, N, H, d = x.shape
     sb, sn, sh, sd = x.stride()
-    if d > 1 and sd != 1:
+    if sd != 1 and d > 1:
         raise ValueError("the d dimension must be contiguous")
     return _PACK_TENSOR(x.data_ptr(), _dtype_code(x), 0, B, N, H, d, sb, sn, sh)
 
@@ -511,47 +513,51 @@ def _gates(x):
 
 def _float_array(name, x, shape, like):
     """Address of a contiguous float32 tensor of this shape on like's device, or None."""
-    import torch
     if x is None:
         return None
-    if x.dtype != torch.float32 or tuple(x.shape) != shape or not x.is_contiguous():
+    if _dtype_code(x) != 1 or x.shape != shape or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of shape {list(shape)}")
-    if x.device != like.device:
+    if x.get_device() != like.get_device():
         raise ValueError(f"{name} is on {x.device}, not on {like.device}")
     return x.data_ptr()
 
 
 def _same_device(like, *tensors):
-    dev = like.device
-    for x in tensors:
-        if x.device != dev:
-            raise ValueError(f"a tensor is on {x.device}, not on {dev}")
-    if dev.type != "cuda":
+    index = like.get_device()
+    if index < 0:
         raise ValueError("expected CUDA tensors")
+    for x in tensors:
+        if x.get_device() != index:
+            raise ValueError(f"a tensor is on {x.device}, not on {like.device}")
 
 
-def _launch(call, x, stream, workspace=None, need=None):
-    """call(workspace address, bytes, stream) with x's device current; need() tells the
-    bytes, taken from torch's allocator on that stream when the caller brings none."""
+def _launch(what, fn, args, x, stream, workspace=None, need=None):
+    """fn(*args, [workspace, bytes,] stream) with x's device current.  need() tells the workspace's
+    bytes (None: the call takes none); they come from torch's allocator on that stream when the caller
+    brings no workspace."""
     import torch
-    index = x.device.index
-    if torch.cuda.current_device() != index:
+    index = x.get_device()
+    if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(index):
-            return _launch(call, x, stream, workspace, need)
+            return _launch(what, fn, args, x, stream, workspace, need)
     current = torch._C._cuda_getCurrentRawStream(index)
     if stream is None:
         s = current
     else:
         s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if need is None:
-        return call(None, 0, s)
-    if workspace is not None:
-        return call(workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
-    n = need()
-    if n == 0 or s != current:
-        return call(None, 0, s)   # another stream: the library's stream-ordered allocation
-    scratch = torch.empty(n, dtype=torch.uint8, device=x.device)
-    return call(scratch.data_ptr(), n, s)
+        st = fn(*args, s)
+    elif workspace is not None:
+        st = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+    else:
+        n = need()
+        if n == 0 or s != current:
+            st = fn(*args, None, 0, s)   # another stream: the library's stream-ordered allocation
+        else:
+            scratch = torch.empty(n, dtype=torch.uint8, device=x.device)
+            st = fn(*args, scratch.data_ptr(), n, s)
+    if st != 0:
+        raise MhlaError(st, what)
 
 
 def _size(fn, what, desc):
@@ -577,19 +583,17 @@ def gated_forward(q, k, v, g, scale=1.0, state=None, out=None, state_out=None, w
     """
     import torch
     B, N, H, d = q.shape
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    if out is None:
+        out = torch.empty_like(q)
     if state_out is None:
-        state_out = torch.empty(B, H, d, d, dtype=torch.float32, device=q.device)
-    _same_device(q, k, v, g, out)
-    s_in = _float_array("state", state, (B, H, d, d), q)
-    s_out = _float_array("state_out", state_out, (B, H, d, d), q)
+        state_out = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
     dq = _heads(q)
+    args = (dq, _heads(k), _heads(v), _gates(g), scale, _float_array("state", state, (B, H, d, d), q), _heads(out),
+            _float_array("state_out", state_out, (B, H, d, d), q))
+    _same_device(q, k, v, g, out)
     L = lib()
-    st = _launch(
-        lambda ws, n, s: L.mhla_gated_forward(dq, _heads(k), _heads(v), _gates(g), scale, s_in, _heads(out), s_out,
-                                              ws, n, s),
-        q, stream, workspace, lambda: _size(L.mhla_gated_workspace_size, "mhla_gated_workspace_size", dq))
-    _check(st, "mhla_gated_forward")
+    _launch("mhla_gated_forward", L.mhla_gated_forward, args, q, stream, workspace,
+            lambda: _size(L.mhla_gated_workspace_size, "mhla_gated_workspace_size", dq))
     return out, state_out
 
 
@@ -599,38 +603,34 @@ def gated_backward(q, k, v, g, dout, scale=1.0, state=None, dstate_out=None, dq=
     when the last state is used, dstate_out (float32 [B, H, d, d])."""
     import torch
     B, N, H, d = q.shape
-    new = lambda given: torch.empty(q.shape, dtype=q.dtype, device=q.device) if given is None else given
-    dq, dk, dv = new(dq), new(dk), new(dv)
-    dg = torch.empty(B, N, H, dtype=q.dtype, device=q.device) if dg is None else dg
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(q) if dk is None else dk
+    dv = torch.empty_like(q) if dv is None else dv
+    dg = torch.empty((B, N, H), dtype=q.dtype, device=q.device) if dg is None else dg
     if dstate is None:
-        dstate = torch.empty(B, H, d, d, dtype=torch.float32, device=q.device)
-    _same_device(q, k, v, g, dout, dq, dk, dv, dg)
-    s_in = _float_array("state", state, (B, H, d, d), q)
-    ds_out = _float_array("dstate_out", dstate_out, (B, H, d, d), q)
-    ds_in = _float_array("dstate", dstate, (B, H, d, d), q)
+        dstate = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
     desc = _heads(q)
+    square = (B, H, d, d)
+    args = (desc, _heads(k), _heads(v), _gates(g), _heads(dout), scale, _float_array("state", state, square, q),
+            _float_array("dstate_out", dstate_out, square, q), _heads(dq), _heads(dk), _heads(dv), _gates(dg),
+            _float_array("dstate", dstate, square, q))
+    _same_device(q, k, v, g, dout, dq, dk, dv, dg)
     L = lib()
-    st = _launch(
-        lambda ws, n, s: L.mhla_gated_backward(desc, _heads(k), _heads(v), _gates(g), _heads(dout), scale, s_in, ds_out,
-                                               _heads(dq), _heads(dk), _heads(dv), _gates(dg), ds_in, ws, n, s),
-        q, stream, workspace,
-        lambda: _size(L.mhla_gated_backward_workspace_size, "mhla_gated_backward_workspace_size", desc))
-    _check(st, "mhla_gated_backward")
+    _launch("mhla_gated_backward", L.mhla_gated_backward, args, q, stream, workspace,
+            lambda: _size(L.mhla_gated_backward_workspace_size, "mhla_gated_backward_workspace_size", desc))
     return dq, dk, dv, dg, dstate
 
 
 def gated_step(q, k, v, g, state, scale=1.0, out=None, stream=None):
     """One token for every sequence: tensors [B, 1, H, d], g [B, 1, H]; ``state``
     (float32 [B, H, d, d]) is updated in place.  Returns ``out``."""
-    import torch
-    B, N, H, d = q.shape
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    B, _, H, d = q.shape
+    if out is None:
+        import torch
+        out = torch.empty_like(q)
+    args = (_heads(q), _heads(k), _heads(v), _gates(g), scale, _float_array("state", state, (B, H, d, d), q), _heads(out))
     _same_device(q, k, v, g, out)
-    s = _float_array("state", state, (B, H, d, d), q)
-    st = _launch(
-        lambda ws, n, sp: lib().mhla_gated_step(_heads(q), _heads(k), _heads(v), _gates(g), scale, s, _heads(out), sp),
-        q, stream)
-    _check(st, "mhla_gated_step")
+    _launch("mhla_gated_step", lib().mhla_gated_step, args, q, stream)
     return out
 
 
@@ -660,7 +660,7 @@ def _rotation(x, table, positions, layout):
         return None
     if table.dim() != 3 or table.shape[2] != 2:
         raise ValueError("the rotation table is [rows, pairs, 2]")
-    ptr = _float_array("table", table, tuple(table.shape), x)
+    ptr = _float_array("table", table, table.shape, x)
     pos = None
     if positions is not None:
         if positions.dtype != torch.int32 or tuple(positions.shape) != tuple(x.shape[:2]) \
@@ -677,16 +677,15 @@ def qk_norm(q, k, q_weight=None, k_weight=None, eps=1e-6, table=None, positions=
     weights [d]) and its rotation by ``table`` ([rows, pairs, 2], see ``init_rotation``) at
     ``positions`` (int32 [B, N]; None: 0 .. N-1).  Returns (q_out, k_out), which may be q and k."""
     import torch
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-    _same_device(q, k, q_out, k_out)
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    if k_out is None:
+        k_out = torch.empty_like(k)
     d = q.shape[3]
-    wq, wk = _float_array("q_weight", q_weight, (d,), q), _float_array("k_weight", k_weight, (d,), q)
-    rot = _rotation(q, table, positions, layout)
-    st = _launch(
-        lambda ws, n, s: lib().mhla_qk_norm(_heads(q), _heads(k), wq, wk, eps, rot, _heads(q_out), _heads(k_out), s),
-        q, stream)
-    _check(st, "mhla_qk_norm")
+    args = (_heads(q), _heads(k), _float_array("q_weight", q_weight, (d,), q), _float_array("k_weight", k_weight, (d,), q),
+            eps, _rotation(q, table, positions, layout), _heads(q_out), _heads(k_out))
+    _same_device(q, k, q_out, k_out)
+    _launch("mhla_qk_norm", lib().mhla_qk_norm, args, q, stream)
     return q_out, k_out
 
 
@@ -700,22 +699,20 @@ def qk_norm_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, eps=1e-
     dq may be dq_out and dk dk_out."""
     import torch
     d = q.shape[3]
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
-    new = lambda given: torch.empty(d, dtype=torch.float32, device=q.device) if given is None else given
-    dq_weight, dk_weight = new(dq_weight), new(dk_weight)
-    _same_device(q, k, dq_out, dk_out, dq, dk)
-    wq, wk = _float_array("q_weight", q_weight, (d,), q), _float_array("k_weight", k_weight, (d,), q)
-    gq, gk = _float_array("dq_weight", dq_weight, (d,), q), _float_array("dk_weight", dk_weight, (d,), q)
-    rot = _rotation(q, table, positions, layout)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    if dq_weight is None:
+        dq_weight = torch.empty(d, dtype=torch.float32, device=q.device)
+    if dk_weight is None:
+        dk_weight = torch.empty(d, dtype=torch.float32, device=q.device)
     desc = _heads(q)
+    args = (desc, _heads(k), _float_array("q_weight", q_weight, (d,), q), _float_array("k_weight", k_weight, (d,), q), eps,
+            _rotation(q, table, positions, layout), _heads(dq_out), _heads(dk_out), _heads(dq), _heads(dk),
+            _float_array("dq_weight", dq_weight, (d,), q), _float_array("dk_weight", dk_weight, (d,), q))
+    _same_device(q, k, dq_out, dk_out, dq, dk)
     L = lib()
-    st = _launch(
-        lambda ws, n, s: L.mhla_qk_norm_backward(desc, _heads(k), wq, wk, eps, rot, _heads(dq_out), _heads(dk_out),
-                                                 _heads(dq), _heads(dk), gq, gk, ws, n, s),
-        q, stream, workspace,
-        lambda: _size(L.mhla_qk_norm_backward_workspace_size, "mhla_qk_norm_backward_workspace_size", desc))
-    _check(st, "mhla_qk_norm_backward")
+    _launch("mhla_qk_norm_backward", L.mhla_qk_norm_backward, args, q, stream, workspace,
+            lambda: _size(L.mhla_qk_norm_backward_workspace_size, "mhla_qk_norm_backward_workspace_size", desc))
     return dq, dk, dq_weight, dk_weight
 
 
