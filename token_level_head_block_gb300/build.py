@@ -27,7 +27,7 @@ CUDA_SOURCES = ["mhla_api.cu", "simt_kernels.cu", "tc_kernels.cu", "tc_summary.c
                 "module_kernels.cu", "gemm_kernels.cu", "sequence_api.cu", "gated_kernels.cu", "gated_tc_kernels.cu",
                 "qk_norm_kernels.cu"]
 CXX_SOURCES = ["mhla_init.cpp"]
-HEADERS = ["mhla_internal.h", "api_checks.h", "gated_common.cuh", "ptx.cuh", "tma_host.h", "tc_common.cuh", "tc_fwd_bodies.cuh", "stall_hook.cuh"]
+HEADERS = ["mhla_internal.h", "api_checks.h", "gated_common.cuh", "float_pairs.cuh", "ptx.cuh", "tma_host.h", "tc_common.cuh", "tc_fwd_bodies.cuh", "stall_hook.cuh"]
 
 
 def _nvcc():

@@ -8,6 +8,7 @@
 
 #include <cstdint>
 
+#include "float_pairs.cuh"
 #include "mhla_internal.h"
 
 namespace mhla {
@@ -58,29 +59,6 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 }
 __device__ __forceinline__ float low(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float high(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
-
-// Two floats that one instruction works on.
-struct Two {
-  uint64_t v;
-};
-__device__ __forceinline__ Two two(float x, float y) {
-  Two r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ void apart(Two a, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
-}
-__device__ __forceinline__ Two mul(Two a, Two b) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
-  Two r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
 
 // A pair as sums of NT bf16 terms, packed.
 template <int NT>
