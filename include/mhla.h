@@ -455,10 +455,18 @@ mhla_status_t mhla_module_forward(const void* x, void* y, int64_t B, int64_t N, 
  *               itself, and overlaps nothing else.
  *   scale       finite.
  * The states and every sum are float32 or wider; bf16 results are rounded once.
- * Both dtypes run on the tensor cores, over chunks of 64 tokens: within a chunk
- * as a masked product, from chunk to chunk through the state, whose products
- * enter the tensor cores as sums of bf16 terms (three where the result is
- * float32).
+ * Every call runs on the tensor cores, over chunks of tokens: within a chunk as
+ * a masked product, from chunk to chunk through the state, whose products enter
+ * the tensor cores as sums of bf16 terms (two where the result is rounded to
+ * bf16, three where it is float32).  Which kernel runs is the library's choice
+ * by type, sizes, alignment and strides: tcgen05 over chunks of 128 tokens for
+ * bf16 with d <= 64 and d % 8 == 0, 16-byte aligned rows and enough tokens, warp
+ * level products over chunks of 64 otherwise.  Few heads are spread over the
+ * machine by cutting the sequence into spans, so results depend on B, H and N in
+ * their last bits; the same call gives the same bits.
+ * An infinity or NaN in v reaches the tokens from its own on, no earlier one.
+ * The tcgen05 kernel's waits are bounded: one that gives up is reported by
+ * mhla_device_status, and the call's outputs are then not valid.
  *   out may be one of several views interleaved in a token's row (a
  *   projection's [B, N, 3C]); it must share no element with an input.
  *   workspace as for mhla_forward.  Asynchronous on stream; statuses as for

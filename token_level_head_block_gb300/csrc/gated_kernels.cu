@@ -7,7 +7,8 @@
 //   dg_t = exp(g_t) <S_{t-1}, dS_t>, where <S_t, dS_t> = dg_t + k_t . dk_t = dg_{t+1} + q_t . dq_t,
 // so dg is a running sum of q . dq - k . dk from the end.
 //
-// One kernel, gated_scan, does every scan.  A CTA of four warps walks a span of
+// gated_scan takes every type, size and alignment; bf16 with d <= 64 and enough tokens goes to
+// the tcgen05 kernels of gated_tc_kernels.cu (wants_tc below).  A CTA walks a span of
 // chunks of 64 tokens with the state (d x up to 64 columns of it) in registers.  With
 // b_i the sum of the log decays of a chunk's tokens up to i and B that of all,
 //   o_i = scale (e^{b_i} S^T q_i + sum_{j <= i} e^{b_i - b_j} (q_i . k_j) v_j)
@@ -19,11 +20,21 @@
 // gated_span_state forms each span's own contribution to the state,
 // gated_join carries the state from span to span, and gated_scan then runs all
 // spans at once.
+//
+// A chunk is a chain (scores, outputs, state, its planes) that few warps walk, so latency bounds it:
+// measured on float32 [3, 5181, 4, 64], the tensor pipe is active 25% of the scan's time and a scheduler issues in
+// one cycle of four.
+// Times, all launches of a call:
+//   bf16  [8, 2048, 16, 128]  forward  282 us      [4, 4096, 16, 80]  gradients  964 us
+//   f32   [8, 2048, 16, 128]  forward  816 us      [8, 6871, 4, 64]   gradients  826 us
+//   f32   [3, 5181, 4, 64]    forward   86 us      [8, 4096, 16, 32]  forward    272 us
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <initializer_list>
+#include <type_traits>
 
 #include "gated_common.cuh"
 #include "mhla_internal.h"
@@ -93,6 +104,15 @@ struct Accumulators {
   float small[APART ? NT : 1][4];
   __device__ __forceinline__ float get(int n, int e) const {
     return APART ? main[n][e] + small[APART ? n : 0][e] : main[n][e];
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        main[n][e] = 0.0f;
+        if (APART) small[APART ? n : 0][e] = 0.0f;
+      }
   }
 };
 
@@ -212,39 +232,96 @@ __device__ __forceinline__ int unit_at(int row, int unit) {
   return row * (2 * W) + ((unit ^ (W == 32 ? (row >> 1) & 3 : row & 7)) << 4);
 }
 
+// Warps of a CTA.  d > 64 takes eight, two to 16 rows of outputs, each with half of the columns (scores
+// twice): an SM holds one or two such CTAs, too few with four warps.  [8, 2048, 16, 128] forward, four
+// against eight: bf16 325, 282 us; float32 974, 816.
+template <int DK>
+constexpr int kWarpsOf = DK > 64 ? 8 : 4;
+
 template <typename T, int DK, bool ASYNC>
 struct Tile {
+  static constexpr int kWarps = kWarpsOf<DK>, kThreads = 32 * kWarps;
   static constexpr int DV = DK < 64 ? DK : 64;     // columns of the state a CTA holds
   static constexpr int kIn = Terms<T>::kIn;
   static constexpr int kStages = ASYNC ? 2 : 1;
   static constexpr int kK = kChunk * DK * 2, kV = kChunk * DV * 2;   // bytes of a plane
   static constexpr int kS = DK * DV * 2;
+  // Steps of 16 tokens or channels one after the other in a loop, where their unrolled code does not
+  // stay in the instruction cache (float32, six products each): scans of [8, 6871, 4, 64] gradients 835 us
+  // unrolled, 690 rolled; bf16 [8, 2048, 16, 128] 282, 293.
+  static constexpr bool kRolled = Terms<T>::kIn > 1;
   // warps over the state's rows (16 each) and, for 32 rows, two halves of its columns
-  static constexpr int kRowTiles = DK >= 64 ? DK / 64 : 1;
+  static constexpr int kRowTiles = DK >= 64 ? DK / kWarps / 16 : 1;
   static constexpr int kColTiles = DK >= 64 ? DV / 8 : DV / 16;   // of eight columns
+  static constexpr int kOutTiles = DV / 8 / (kWarps / 4);         // of a warp's outputs
 };
 
 // Copies chunks of one operand (columns [c0, c0 + W)) into kIn planes.
-template <typename T, int W, bool ASYNC>
+template <typename T, int W, int THREADS, bool ASYNC>
 struct RowLoader {
   const T* src;
   int64_t step;      // elements: ASYNC from pass to pass, else from token to token
   int32_t width;     // columns in the tensor
+  bool quads;        // float32 rows that 16-byte loads take
   __device__ __forceinline__ RowLoader(const Operand& o, int64_t b, int64_t h, int c0, int d) {
     src = static_cast<const T*>(o.data) + b * o.sb + h * o.sh + c0;
     width = min(W, d - c0);
     if constexpr (ASYNC) {
-      constexpr int kUnits = W / 8, kRows = 128 / kUnits;   // 16-byte units, rows a pass
+      constexpr int kUnits = W / 8, kRows = THREADS / kUnits;   // 16-byte units, rows a pass
       src += static_cast<int>(threadIdx.x) / kUnits * o.sn + 8 * (threadIdx.x % kUnits);
       step = kRows * o.sn;
     } else {
       step = o.sn;
     }
+    quads = sizeof(T) == 4 && reinterpret_cast<uintptr_t>(src) % 16 == 0 && o.sn % 4 == 0 && width % 4 == 0;
+  }
+
+  // float32 rows in 16-byte units: eight of a thread in flight, `part` says which of the tile's.
+  static constexpr int quads_a_part() { return kChunk * W / 4 / THREADS < 8 ? kChunk * W / 4 / THREADS : 8; }
+  static constexpr int parts() { return kChunk * W / 4 / THREADS / quads_a_part(); }
+  __device__ __forceinline__ void fetch(float4 (&x)[8], int part, int64_t chunk, int64_t N) const {
+    const int rows = static_cast<int>(min(N - chunk * kChunk, static_cast<int64_t>(kChunk)));
+    const float* from = reinterpret_cast<const float*>(src) + chunk * kChunk * step;
+    constexpr int kQuads = quads_a_part();
+#pragma unroll
+    for (int j = 0; j < kQuads; ++j) {
+      const int i = threadIdx.x + THREADS * (part * kQuads + j), r = i / (W / 4), c = 4 * (i % (W / 4));
+      x[j] = r < rows && c < width ? *reinterpret_cast<const float4*>(from + r * step + c)
+                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+  }
+  __device__ __forceinline__ void put(char* dst, const float4 (&x)[8], int part) const {
+    constexpr int kQuads = quads_a_part();
+#pragma unroll
+    for (int j = 0; j < kQuads; ++j) {
+      const int i = threadIdx.x + THREADS * (part * kQuads + j), r = i / (W / 4), c = 4 * (i % (W / 4));
+      float a[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+      for (int n = 0; n < Terms<T>::kIn; ++n) {
+        const uint32_t lo = pack(a[0], a[1]), hi = pack(a[2], a[3]);
+        *reinterpret_cast<uint2*>(dst + n * kChunk * W * 2 + unit_at<W>(r, c >> 3) + (c & 7) * 2) = make_uint2(lo, hi);
+        const float f[4] = {low(lo), high(lo), low(hi), high(hi)};
+        // an infinity is its first term alone
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = fabsf(f[e]) < __int_as_float(0x7F800000) ? a[e] - f[e] : 0.0f;
+      }
+    }
+  }
+  // Asks L2 for a later chunk's rows.
+  __device__ __forceinline__ void prefetch(int64_t chunk, int64_t N) const {
+    constexpr int kLine = 128 / sizeof(T), kLines = (W + kLine - 1) / kLine;
+    const int rows = static_cast<int>(min(N - chunk * kChunk, static_cast<int64_t>(kChunk)));
+#pragma unroll
+    for (int i0 = 0; i0 < kChunk * kLines; i0 += THREADS) {
+      const int i = i0 + threadIdx.x, r = i / kLines, c = kLine * (i % kLines);
+      if (r < rows && c < width)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(src + (chunk * kChunk + r) * step + c));
+    }
   }
   __device__ __forceinline__ void load(char* dst, int64_t chunk, int64_t N) const {
     const int rows = static_cast<int>(min(N - chunk * kChunk, static_cast<int64_t>(kChunk)));
     if constexpr (ASYNC) {
-      constexpr int kUnits = W / 8, kRows = 128 / kUnits, kSteps = kChunk / kRows;
+      constexpr int kUnits = W / 8, kRows = THREADS / kUnits, kSteps = kChunk / kRows;
       const int r = threadIdx.x / kUnits, u = threadIdx.x % kUnits;
       if (8 * u >= width) return;   // the columns behind d were zeroed at the start
       static_assert(kRows % 8 == 0, "a pass keeps the units' places");
@@ -261,19 +338,19 @@ struct RowLoader {
         }
       }
     } else {
-      constexpr int kPairs = kChunk * W / 2 / 128, kBatch = kPairs < 8 ? kPairs : 8;   // loads in flight
+      constexpr int kPairs = kChunk * W / 2 / THREADS, kBatch = kPairs < 8 ? kPairs : 8;   // loads in flight
       for (int i0 = 0; i0 < kPairs; i0 += kBatch) {
         float a[kBatch], e[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-          const int i = threadIdx.x + 128 * (i0 + j), r = i / (W / 2), c = 2 * (i % (W / 2));
+          const int i = threadIdx.x + THREADS * (i0 + j), r = i / (W / 2), c = 2 * (i % (W / 2));
           const T* x = src + (chunk * kChunk + r) * step + c;
           a[j] = r < rows && c < width ? to_f(x[0]) : 0.0f;
           e[j] = r < rows && c + 1 < width ? to_f(x[1]) : 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-          const int i = threadIdx.x + 128 * (i0 + j), r = i / (W / 2), c = 2 * (i % (W / 2));
+          const int i = threadIdx.x + THREADS * (i0 + j), r = i / (W / 2), c = 2 * (i % (W / 2));
 #pragma unroll
           for (int n = 0; n < Terms<T>::kIn; ++n) {
             const uint32_t p = pack(a[j], e[j]);
@@ -288,13 +365,56 @@ struct RowLoader {
   }
 };
 
+// One operand's chunk after the other, float32 rows in 16-byte units where all allow it: the next
+// part's loads are in flight while one is split into its terms.
+template <typename T, int W, int THREADS>
+struct PlainPart {
+  const RowLoader<T, W, THREADS, false>& rows;
+  char* dst;
+};
+template <typename... P>
+__device__ __forceinline__ void fetch_first(float4 (&x)[8], int64_t chunk, int64_t N, const P&... parts) {
+  if constexpr (sizeof...(P) > 0) {
+    auto first = [&](const auto& p, const auto&...) { p.rows.fetch(x, 0, chunk, N); };
+    first(parts...);
+  }
+}
+template <typename T, int THREADS, int W0, int... W>
+__device__ __forceinline__ void load_plain(int64_t chunk, int64_t N, PlainPart<T, W0, THREADS> one,
+                                           PlainPart<T, W, THREADS>... more) {
+  if constexpr (sizeof(T) == 4) {
+    if ((one.rows.quads && ... && more.rows.quads)) {
+      float4 x[2][8];
+      int turn = 0;
+      one.rows.fetch(x[0], 0, chunk, N);
+      auto rest = [&](auto& self, const auto& now, const auto&... next) -> void {
+        using Rows = std::remove_reference_t<decltype(now.rows)>;
+#pragma unroll
+        for (int part = 0; part < Rows::parts(); ++part) {
+          if (part + 1 < Rows::parts())
+            now.rows.fetch(x[turn ^ 1], part + 1, chunk, N);
+          else
+            fetch_first(x[turn ^ 1], chunk, N, next...);
+          now.rows.put(now.dst, x[turn], part);
+          turn ^= 1;
+        }
+        if constexpr (sizeof...(next) > 0) self(self, next...);
+      };
+      rest(rest, one, more...);
+      return;
+    }
+  }
+  one.rows.load(one.dst, chunk, N);
+  (more.rows.load(more.dst, chunk, N), ...);
+}
+
 // Each thread's part of the state: row tile m, column tile n, the four values of
 // an mma accumulator.  `row` and `col` are those of the first.
 template <int DK>
 struct StatePlace {
   int row, col;
   __device__ __forceinline__ StatePlace(int warp, int lane) {
-    row = (DK >= 64 ? (DK / 4) * warp : 16 * (warp & 1)) + (lane >> 2);
+    row = (DK >= 64 ? DK / kWarpsOf<DK> * warp : 16 * (warp & 1)) + (lane >> 2);
     col = (DK >= 64 ? 0 : 16 * (warp >> 1)) + 2 * (lane & 3);
   }
 };
@@ -344,12 +464,13 @@ __device__ __forceinline__ void add_chunk(float (&S)[Tile<T, DK, ASYNC>::kRowTil
                                           uint32_t k_base, uint32_t v_base, const Gates& w, int warp, int lane) {
   using L = Tile<T, DK, ASYNC>;
   constexpr int P = L::kColTiles / 2;
-  const int row0 = DK >= 64 ? (DK / 4) * warp : 16 * (warp & 1), col0 = DK >= 64 ? 0 : 16 * (warp >> 1);
+  const int row0 = DK >= 64 ? DK / kWarpsOf<DK> * warp : 16 * (warp & 1), col0 = DK >= 64 ? 0 : 16 * (warp >> 1);
   const float total = w.total;
 #pragma unroll
   for (int m = 0; m < L::kRowTiles; ++m) {
     Accumulators<L::kColTiles, (L::kIn > 1)> sum;
-#pragma unroll
+    if (L::kRolled) sum.clear();
+#pragma unroll(L::kRolled ? 1 : kChunk / 16)
     for (int s = 0; s < kChunk / 16; ++s) {
       uint32_t ka[kAdd][4], vb[L::kIn][P][4];
 #pragma unroll
@@ -358,7 +479,7 @@ __device__ __forceinline__ void add_chunk(float (&S)[Tile<T, DK, ASYNC>::kRowTil
         for (int n = 0; n < P; ++n)
           ldsm_t(vb[t][n], column_address<L::DV>(v_base + t * L::kV, 16 * s, col0 + 16 * n, lane));
       add_operand<T, DK, ASYNC>(ka, k_base, row0 + 16 * m, s, w.addw, lane);
-      mma_terms(sum, 0, ka, vb, s == 0);
+      mma_terms(sum, 0, ka, vb, !L::kRolled && s == 0);
     }
 #pragma unroll
     for (int n = 0; n < L::kColTiles; ++n)
@@ -368,7 +489,7 @@ __device__ __forceinline__ void add_chunk(float (&S)[Tile<T, DK, ASYNC>::kRowTil
 }
 
 template <typename T, int DK, bool ASYNC>
-__global__ void __launch_bounds__(128) gated_span_state(const __grid_constant__ ScanSet p) {
+__global__ void __launch_bounds__(32 * kWarpsOf<DK>) gated_span_state(const __grid_constant__ ScanSet p) {
   using L = Tile<T, DK, ASYNC>;
   extern __shared__ __align__(16) char smem[];
   __shared__ __align__(16) Gates gates[2];
@@ -388,18 +509,23 @@ __global__ void __launch_bounds__(128) gated_span_state(const __grid_constant__ 
   const bool reverse = a.reverse;
 
   if constexpr (ASYNC) {   // columns behind d stay zero
-    for (int i = threadIdx.x; i < L::kStages * kStage / 16; i += 128)
+    for (int i = threadIdx.x; i < L::kStages * kStage / 16; i += L::kThreads)
       reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
   }
-  const RowLoader<T, DK, ASYNC> rows_k(a.k, b, h, 0, p.d);
-  const RowLoader<T, L::DV, ASYNC> rows_v(a.v, b, h, c0, p.d);
+  const RowLoader<T, DK, L::kThreads, ASYNC> rows_k(a.k, b, h, 0, p.d);
+  const RowLoader<T, L::DV, L::kThreads, ASYNC> rows_v(a.v, b, h, c0, p.d);
   auto chunk_of = [&](int i) { return first + (reverse ? count - 1 - i : i); };
   auto load = [&](int i) {
     char* st = smem + (i % L::kStages) * kStage;
-    rows_k.load(st, chunk_of(i), p.N);
-    rows_v.load(st + L::kIn * L::kK, chunk_of(i), p.N);
-    if (ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
+    if constexpr (ASYNC) {
+      rows_k.load(st, chunk_of(i), p.N);
+      rows_v.load(st + L::kIn * L::kK, chunk_of(i), p.N);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    } else {
+      load_plain(chunk_of(i), p.N, PlainPart<T, DK, L::kThreads>{rows_k, st},
+                 PlainPart<T, L::DV, L::kThreads>{rows_v, st + L::kIn * L::kK});
+    }
   };
 
   float S[L::kRowTiles][L::kColTiles][4] = {};
@@ -418,6 +544,10 @@ __global__ void __launch_bounds__(128) gated_span_state(const __grid_constant__ 
     } else {
       __syncthreads();
       load(i);
+      if (i + 1 < count) {
+        rows_k.prefetch(chunk_of(i + 1), p.N);
+        rows_v.prefetch(chunk_of(i + 1), p.N);
+      }
       __syncthreads();
     }
     if (warp == 0 && i + 1 < count) {
@@ -442,7 +572,8 @@ __global__ void __launch_bounds__(128) gated_span_state(const __grid_constant__ 
 }
 
 // Turns every span's own contribution into the state that enters the span, in
-// order of the scan; one thread an element of one (b, h)'s state.
+// order of the scan; one thread an element of one (b, h)'s state.  The spans' values come from L2, eight loads
+// in flight: 5 us for 25 spans of 12 (b, h) with d = 64, most of it the launch.
 __global__ void __launch_bounds__(256) gated_join(const __grid_constant__ ScanSet p) {
   const Scan& a = p.scan[blockIdx.y];
   const int64_t dd = static_cast<int64_t>(p.d) * p.d;
@@ -485,16 +616,20 @@ struct ScanShared {
 // The outputs of a chunk for one warp's 16 rows: what they read from the state,
 // the tokens of other blocks, then their own block's.
 template <typename T, int DK, bool ASYNC, bool REVERSE>
-__device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::DV / 8, (Terms<T>::kIn > 1)>& o,
-                                           const char* stage, uint32_t s_base, const Gates& w, float out_scale, int own,
+__device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::kOutTiles, (Terms<T>::kIn > 1)>& o,
+                                           const char* stage, uint32_t s_base, const Gates& w, float out_scale, int own, int col0,
                                            int lane) {
   using L = Tile<T, DK, ASYNC>;
-  constexpr int kScore = Terms<T>::kScore, kState = Terms<T>::kState, NV = L::DV / 8, P = NV / 2, kSteps = kChunk / 16;
+  constexpr int kScore = Terms<T>::kScore, kState = Terms<T>::kState, NV = L::kOutTiles, P = NV / 2, kSteps = kChunk / 16;
   constexpr bool kApart = L::kIn > 1;
   const uint32_t q_base = ptx::smem_u32(stage), k_base = q_base + L::kIn * L::kK, v_base = k_base + L::kIn * L::kK;
   const int rows0 = 16 * own, row = rows0 + (lane >> 2);
   Accumulators<2 * kSteps, kApart> sc;
-#pragma unroll
+  if (L::kRolled) {
+    o.clear();
+    sc.clear();
+  }
+#pragma unroll(L::kRolled ? 1 : DK / 16)
   for (int ks = 0; ks < DK / 16; ++ks) {
     uint32_t qa[L::kIn][4];
 #pragma unroll
@@ -505,8 +640,8 @@ __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::DV /
     for (int t = 0; t < kState; ++t)
 #pragma unroll
       for (int n = 0; n < P; ++n)
-        ldsm_t(sb[t][n], column_address<L::DV>(s_base + t * L::kS, 16 * ks, 16 * n, lane));
-    mma_terms(o, 0, qa, sb, ks == 0);
+        ldsm_t(sb[t][n], column_address<L::DV>(s_base + t * L::kS, 16 * ks, col0 + 16 * n, lane));
+    mma_terms(o, 0, qa, sb, !L::kRolled && ks == 0);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       if (REVERSE ? s < own : s > own) continue;
@@ -515,7 +650,7 @@ __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::DV /
       for (int t = 0; t < L::kIn; ++t)
         ldsm(kb[t][0],
              k_base + t * L::kK + unit_at<DK>(16 * s + (lane & 7) + (lane >> 4) * 8, 2 * ks + ((lane >> 3) & 1)));
-      mma_terms(sc, 2 * s, qa, kb, ks == 0);
+      mma_terms(sc, 2 * s, qa, kb, !L::kRolled && ks == 0);
     }
   }
   const float enter = w.enter[own];
@@ -534,7 +669,7 @@ __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::DV /
     for (int t = 0; t < L::kIn; ++t)
 #pragma unroll
       for (int n = 0; n < P; ++n)
-        ldsm_t(vb[t][n], column_address<L::DV>(v_base + t * L::kV, 16 * s, 16 * n, lane));
+        ldsm_t(vb[t][n], column_address<L::DV>(v_base + t * L::kV, 16 * s, col0 + 16 * n, lane));
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
       const float2 c = *reinterpret_cast<const float2*>(w.col[own] + 16 * s + 8 * f + 2 * (lane & 3));
@@ -588,7 +723,7 @@ __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::DV /
   for (int t = 0; t < L::kIn; ++t)
 #pragma unroll
     for (int n = 0; n < P; ++n)
-      ldsm_t(vb[t][n], column_address<L::DV>(v_base + t * L::kV, rows0, 16 * n, lane));
+      ldsm_t(vb[t][n], column_address<L::DV>(v_base + t * L::kV, rows0, col0 + 16 * n, lane));
   // A row of v that holds an infinity or NaN must not reach the rows that do not see
   // it (0 times infinity): such a block goes without the tensor core.
   uint32_t bad = 0;
@@ -632,7 +767,7 @@ __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::DV /
           float y = 0.0f;
 #pragma unroll
           for (int t = 0; t < L::kIn; ++t)
-            y += __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(v + t * L::kV + unit_at<L::DV>(rows0 + j, n) +
+            y += __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(v + t * L::kV + unit_at<L::DV>(rows0 + j, col0 / 8 + n) +
                                                                           2 * (2 * (lane & 3) + e)));
           if (sees_up) o.main[n][e] = fmaf(up, y, o.main[n][e]);
           if (sees_dn) o.main[n][2 + e] = fmaf(dn, y, o.main[n][2 + e]);
@@ -642,11 +777,11 @@ __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::DV /
 }
 
 template <typename T, int DK, bool ASYNC>
-__global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
+__global__ void __launch_bounds__(32 * kWarpsOf<DK>, sizeof(T) == 2 ? (DK <= 64 ? 3 : 1) : 1)
     gated_scan(const __grid_constant__ ScanSet p) {
   using L = Tile<T, DK, ASYNC>;
   using M = ScanShared<T, DK, ASYNC>;
-  constexpr int kState = Terms<T>::kState, NV = L::DV / 8;
+  constexpr int kState = Terms<T>::kState, NV = L::kOutTiles;
   extern __shared__ __align__(16) char smem[];
   __shared__ __align__(16) Gates gates[2];
   const Scan& a = p.scan[blockIdx.y];
@@ -663,23 +798,30 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
   // Rows later in the order see more of the chunk: neighbouring CTAs give them
   // to different warps, so that an SM's four schedulers get the same work.
   const int own = (warp + static_cast<int>(blockIdx.x)) & 3, rows0 = 16 * own;
+  const int half = warp >> 2, col0 = 8 * NV * half;   // this warp's columns of the outputs
   char* planes = smem + L::kStages * M::kStage;
   const uint32_t s_base = ptx::smem_u32(planes);
 
   if constexpr (ASYNC) {
-    for (int i = threadIdx.x; i < L::kStages * M::kStage / 16; i += 128)
+    for (int i = threadIdx.x; i < L::kStages * M::kStage / 16; i += L::kThreads)
       reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
   }
-  const RowLoader<T, DK, ASYNC> rows_q(a.q, b, h, 0, p.d), rows_k(a.k, b, h, 0, p.d);
-  const RowLoader<T, L::DV, ASYNC> rows_v(a.v, b, h, c0, p.d);
+  const RowLoader<T, DK, L::kThreads, ASYNC> rows_q(a.q, b, h, 0, p.d), rows_k(a.k, b, h, 0, p.d);
+  const RowLoader<T, L::DV, L::kThreads, ASYNC> rows_v(a.v, b, h, c0, p.d);
   auto chunk_of = [&](int i) { return first + (reverse ? count - 1 - i : i); };
   auto load = [&](int i) {
     char* st = smem + (i % L::kStages) * M::kStage;
-    rows_q.load(st, chunk_of(i), p.N);
-    rows_k.load(st + L::kIn * L::kK, chunk_of(i), p.N);
-    rows_v.load(st + 2 * L::kIn * L::kK, chunk_of(i), p.N);
-    if (ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
+    if constexpr (ASYNC) {
+      rows_q.load(st, chunk_of(i), p.N);
+      rows_k.load(st + L::kIn * L::kK, chunk_of(i), p.N);
+      rows_v.load(st + 2 * L::kIn * L::kK, chunk_of(i), p.N);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    } else {
+      load_plain(chunk_of(i), p.N, PlainPart<T, DK, L::kThreads>{rows_q, st},
+                 PlainPart<T, DK, L::kThreads>{rows_k, st + L::kIn * L::kK},
+                 PlainPart<T, L::DV, L::kThreads>{rows_v, st + 2 * L::kIn * L::kK});
+    }
   };
   if constexpr (ASYNC) load(0);
 
@@ -729,6 +871,11 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
     } else {
       __syncthreads();
       load(i);
+      if (i + 1 < count) {
+        rows_q.prefetch(chunk_of(i + 1), p.N);
+        rows_k.prefetch(chunk_of(i + 1), p.N);
+        rows_v.prefetch(chunk_of(i + 1), p.N);
+      }
       __syncthreads();
     }
     if (i + 1 < count && warp == ((i + 1) & 3)) chunk_gates(g, gates[(i + 1) & 1], a, lane);
@@ -740,9 +887,9 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
     {
       Accumulators<NV, (L::kIn > 1)> o;
       if (reverse)
-        read_chunk<T, DK, ASYNC, true>(o, stage, s_base, w, a.out_scale, own, lane);
+        read_chunk<T, DK, ASYNC, true>(o, stage, s_base, w, a.out_scale, own, col0, lane);
       else
-        read_chunk<T, DK, ASYNC, false>(o, stage, s_base, w, a.out_scale, own, lane);
+        read_chunk<T, DK, ASYNC, false>(o, stage, s_base, w, a.out_scale, own, col0, lane);
 
       // rows out: rounded once, through this warp's own rows of q
       if (a.dots) {
@@ -754,7 +901,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
           if (t < p.N) {
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
-              const int c = 8 * n + 2 * (lane & 3);
+              const int c = col0 + 8 * n + 2 * (lane & 3);
               const T* x = dot + t * a.dot.sn + c;
               if constexpr (ASYNC) {
                 if (c0 + c < p.d) {
@@ -769,21 +916,25 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
           }
           sum[f] += __shfl_xor_sync(~0u, sum[f], 1);
           sum[f] += __shfl_xor_sync(~0u, sum[f], 2);
-          if ((lane & 3) == 0 && t < p.N) a.dots[(slice * p.BH + bh) * p.N + t] = sum[f];
+          if ((lane & 3) == 0 && t < p.N) a.dots[((slice * (L::kWarps / 4) + half) * p.BH + bh) * p.N + t] = sum[f];
         }
       }
       if constexpr (ASYNC) {
-        __syncwarp();   // every lane has read its rows of q
+        if (L::kWarps == 4)
+          __syncwarp();   // every lane has read its rows of q
+        else              // and every lane of the warp with the other columns
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
         // the columns behind d stay zero (a NaN row would put NaN there)
 #pragma unroll
         for (int n = 0; n < NV; ++n)
 #pragma unroll
           for (int f = 0; f < 2; ++f)
-            if (c0 + 8 * n < p.d)
-              *reinterpret_cast<uint32_t*>(stage + unit_at<DK>(row + 8 * f, n) + 4 * (lane & 3)) = pack(o.get(n, 2 * f), o.get(n, 2 * f + 1));
+            if (c0 + col0 + 8 * n < p.d)
+              *reinterpret_cast<uint32_t*>(stage + unit_at<DK>(row + 8 * f, col0 / 8 + n) + 4 * (lane & 3)) =
+                  pack(o.get(n, 2 * f), o.get(n, 2 * f + 1));
         __syncwarp();
-        constexpr int kUnits = L::DV / 8;
-        const int r = lane / kUnits, c = 8 * (lane % kUnits);
+        constexpr int kUnits = NV;
+        const int r = lane / kUnits, c = col0 + 8 * (lane % kUnits);
         const int64_t t = t0 + rows0 + r;
         T* to = out + t * a.out.sn + c;
 #pragma unroll
@@ -800,7 +951,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
           if (t >= p.N) continue;
 #pragma unroll
           for (int n = 0; n < NV; ++n) {
-            const int c = 8 * n + 2 * (lane & 3);
+            const int c = col0 + 8 * n + 2 * (lane & 3);
             if (c0 + c < p.d) from_f(out + t * a.out.sn + c, o.get(n, 2 * f));
             if (c0 + c + 1 < p.d) from_f(out + t * a.out.sn + c + 1, o.get(n, 2 * f + 1));
           }
@@ -830,7 +981,9 @@ __global__ void __launch_bounds__(128, sizeof(T) == 2 && DK <= 64 ? 3 : 1)
 
 // dg over one span of one (b, h), 2048 tokens at a time from its end: <S, dS>
 // there, then the running sum of q.dq - k.dk.  The sums restart at every span,
-// so their rounding does not grow with the sequence.
+// so their rounding does not grow with the sequence.  Two floats a token are read and one gate written
+// (with stride H), so a CTA to a span is bound by the latency of its rounds: 9 us of the 115 of gradients of
+// bf16 [4, 4096, 12, 64], 30 of the 930 of [2, 16384, 70, 32].
 struct GateGrad {
   const float *qdots, *kdots;   // [slices][B][H][N]
   const float *enter, *leave;   // states entering each span forwards and backwards (both with v's channels as rows)
@@ -842,6 +995,7 @@ struct GateGrad {
 
 template <typename T>
 __global__ void __launch_bounds__(256) gated_gate_grad(const __grid_constant__ GateGrad p) {
+  constexpr int kEach = 8;   // tokens a thread, so that a long span takes few rounds
   __shared__ float part[8];
   __shared__ float head;
   const int64_t span = blockIdx.x % p.spans, bh = blockIdx.x / p.spans, b = bh / p.H, h = bh % p.H;
@@ -851,14 +1005,34 @@ __global__ void __launch_bounds__(256) gated_gate_grad(const __grid_constant__ G
   const int d = p.d;
   if (span + 1 < p.spans) {
     const float *x = p.enter + (bh * p.spans + span + 1) * dd, *y = p.leave + (bh * p.spans + span) * dd;
+    if (d % 2 == 0) {   // d * d a multiple of four, and so is every state's start
 #pragma unroll 8
-    for (int i = threadIdx.x; i < d * d; i += 256) s = fmaf(x[i], y[i], s);
+      for (int i = threadIdx.x; i < d * d / 4; i += 256) {
+        const float4 f = reinterpret_cast<const float4*>(x)[i], g = reinterpret_cast<const float4*>(y)[i];
+        s = fmaf(f.x, g.x, fmaf(f.y, g.y, fmaf(f.z, g.z, fmaf(f.w, g.w, s))));
+      }
+    } else {
+      for (int i = threadIdx.x; i < d * d; i += 256) s = fmaf(x[i], y[i], s);
+    }
   } else if (p.dlast) {
     const float *x = p.last + bh * dd, *y = p.dlast + bh * dd;
-#pragma unroll 8
-    for (int i = threadIdx.x; i < d * d; i += 256) {
-      const uint32_t r = static_cast<uint32_t>(i) / static_cast<uint32_t>(d), c = i - r * d;
-      s = fmaf(x[i], y[c * d + r], s);
+    // a warp takes 8 rows by 16 columns of x: whole sectors of both
+    const int tiles = (d + 15) / 16, all = tiles * ((d + 7) / 8);
+    const bool quads = d % 4 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
+#pragma unroll 4
+    for (int i = warp; i < all; i += 8) {
+      const int r = i / tiles * 8 + (lane & 7), c = i % tiles * 16 + 4 * (lane >> 3);
+      if (r >= d || c >= d) continue;
+      float f[4] = {};
+      if (quads) {
+        const float4 q = *reinterpret_cast<const float4*>(x + r * d + c);
+        f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
+      } else {
+        for (int e = 0; e < 4 && c + e < d; ++e) f[e] = x[r * d + c + e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < d) s = fmaf(f[e], y[(c + e) * d + r], s);
     }
   }
 #pragma unroll
@@ -873,7 +1047,6 @@ __global__ void __launch_bounds__(256) gated_gate_grad(const __grid_constant__ G
   __syncthreads();
   const int64_t t0 = span * p.span_tokens, t1 = min(p.N, t0 + p.span_tokens);
   float carry = head;
-  constexpr int kEach = 8;   // tokens a thread, so that a long span takes few rounds
   for (int64_t end = t1; end > t0; end -= 256 * kEach) {
     const int64_t t = end - 1 - kEach * static_cast<int64_t>(threadIdx.x);   // thread 0 takes the last ones
     float x[kEach];
@@ -917,11 +1090,19 @@ __global__ void __launch_bounds__(256) gated_gate_grad(const __grid_constant__ G
 
 int padded(int32_t d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
 
+// CTAs of gated_scan an SM holds.
+int ctas_an_sm(const GatedProblem& p) {
+  if (p.d > 64) return 1;
+  return p.dtype == MHLA_BF16 ? 3 : 2;
+}
+
+// As many spans as one wave of CTAs takes: a few beyond it cost a second wave (float32 [3, 5181, 4, 64],
+// 324 CTAs on 304 places 127 us, 300 CTAs 96).
 Cut cut_for(const GatedProblem& p, int scans) {
   Cut c;
   c.chunks = (p.N + kChunk - 1) / kChunk;
   const int64_t have = p.B * p.H * (p.d > 64 ? 2 : 1) * scans;
-  const int64_t room = int64_t{kSms} * 3;
+  const int64_t room = int64_t{kSms} * ctas_an_sm(p);
   int64_t spans = std::max<int64_t>(1, room / have);
   c.span_chunks = (c.chunks + spans - 1) / spans;
   c.spans = (c.chunks + c.span_chunks - 1) / c.span_chunks;
@@ -948,7 +1129,7 @@ int launch_span_state(const ScanSet& set, int scans, cudaStream_t s) {
   const int64_t slices = (set.d + L::DV - 1) / L::DV;
   KernelTimer timer("gated_span_state", s);
   gated_span_state<T, DK, ASYNC>
-      <<<dim3(static_cast<unsigned>(set.BH * slices * (set.spans - 1)), scans), 128, kBytes, s>>>(set);
+      <<<dim3(static_cast<unsigned>(set.BH * slices * (set.spans - 1)), scans), L::kThreads, kBytes, s>>>(set);
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
 
@@ -961,7 +1142,7 @@ int launch_scan(const ScanSet& set, int scans, cudaStream_t s) {
     return MHLA_ERR_CUDA;
   const int64_t slices = (set.d + L::DV - 1) / L::DV;
   KernelTimer timer("gated_scan", s);
-  gated_scan<T, DK, ASYNC><<<dim3(static_cast<unsigned>(set.BH * slices * set.spans), scans), 128, kBytes, s>>>(set);
+  gated_scan<T, DK, ASYNC><<<dim3(static_cast<unsigned>(set.BH * slices * set.spans), scans), L::kThreads, kBytes, s>>>(set);
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
 
@@ -1021,7 +1202,9 @@ size_t most_span_bytes(const GatedProblem& p, int scans) {
   return tc_supported(p) ? std::max(n, span_bytes(p, tc_cut(p, scans))) : n;
 }
 
-int64_t dot_slices(const GatedProblem& p) { return p.d > 32 ? 2 : 1; }
+// Parts of the columns whose dots are summed apart: by gated_scan, the most of either kernel.
+int scan_dot_slices(const GatedProblem& p) { return p.d > 64 ? 4 : 1; }
+int64_t dot_slices(const GatedProblem& p) { return std::max(scan_dot_slices(p), p.d > 32 ? 2 : 1); }
 
 SpanBuffers carve_spans(const GatedProblem& p, const Cut& c, char** base) {
   if (c.spans < 2) return SpanBuffers{nullptr, nullptr};
@@ -1166,7 +1349,7 @@ int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* w
   gg.N = p.N; gg.H = p.H; gg.BH = bh;
   gg.span_tokens = c.span_chunks * (r.tc ? kTcChunk : kChunk);
   gg.spans = set.spans; gg.d = p.d;
-  gg.slices = r.tc ? static_cast<int32_t>(dot_slices(p)) : (p.d > 64 ? 2 : 1);
+  gg.slices = r.tc ? static_cast<int32_t>(dot_slices(p)) : scan_dot_slices(p);
   KernelTimer timer("gated_gate_grad", stream);
   const unsigned grid = static_cast<unsigned>(bh * c.spans);
   if (p.dtype == MHLA_BF16)
@@ -1179,8 +1362,9 @@ int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* w
 // ------------------------------------------------------------------ one token
 
 // A CTA takes one (b, h).  The state is read and written once and nothing else is of
-// size, so the loads count: VEC 4 keeps four 16-byte loads of a thread in flight (d = 64),
-// row groups meeting in shared memory for o.  VEC 1 takes any d and alignment.
+// size, so HBM bounds it and the loads count: VEC 4 keeps four 16-byte loads of a thread in flight (d = 64),
+// row groups meeting in shared memory for o.  VEC 1 takes any d and alignment.  64 sequences of 12
+// heads, d = 64 (25 MB): 5.7 us, 4.5 TB/s; one sequence 3 us, a launch.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) gated_step(const GatedProblem p, float* state, const Operand out) {
   constexpr int kBatch = 4;
