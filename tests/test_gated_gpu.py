@@ -150,6 +150,16 @@ def test_backward_of_many_tokens(B, N, H, d, state):
     check_backward(x, "bf16", d ** -0.5, run_backward(x, d ** -0.5))
 
 
+# the warp-level kernel over several spans: two slices of columns, float32 rows that 16-byte loads take and do not
+@pytest.mark.parametrize("B,N,H,d,dtype", [(1, 900, 2, 128, "bf16"), (2, 700, 3, 72, "bf16"), (1, 900, 2, 128, "f32"),
+                                           (2, 700, 3, 70, "f32"), (1, 1300, 3, 64, "f32"), (3, 600, 2, 36, "f32"),
+                                           (12, 200, 9, 128, "f32")])
+def test_spans_of_wide_heads_and_of_float32(B, N, H, d, dtype):
+    x = draw(N + d, B, N, H, d, dtype)
+    check_forward(x, dtype, d ** -0.5, *run_forward(x, d ** -0.5))
+    check_backward(x, dtype, d ** -0.5, run_backward(x, d ** -0.5))
+
+
 def test_backward_against_differences_of_the_forward():
     """Central differences of the framework's own forward, float32, along a direction per input.
 

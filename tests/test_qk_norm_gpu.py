@@ -121,6 +121,39 @@ def test_forward_and_backward(B, N, H, Hk, d, pairs, layout, dtype):
     check_backward(x, layout, dtype, run_backward(x, layout))
 
 
+# more tokens than a launch's groups hold at once (they go on from round to round, over the ends of sequences) and,
+# in the last two, more heads than it has groups
+LONG = [(7, 1999, 2, 1, 64, 32), (3, 2503, 3, 2, 128, 64), (4001, 3, 2, 1, 64, 8), (5, 2777, 1, 3, 40, 9),
+        (1, 1, 34000, 1, 64, 32), (1, 2, 50000, 3, 64, 16)]
+
+
+@pytest.mark.parametrize("dtype,layout", [("bf16", "half"), ("f32", "interleaved")])
+@pytest.mark.parametrize("B,N,H,Hk,d,pairs", LONG)
+def test_many_rounds(B, N, H, Hk, d, pairs, layout, dtype):
+    x = draw(N + H, B, N, H, Hk, d, dtype, pairs, positions=B % 2 == 1)
+    if x["positions"] is not None:
+        x["positions"][:, ::5] = -1
+    x["k"] = x["k"].transpose(1, 2).contiguous().transpose(1, 2)     # heads outside tokens
+    check_forward(x, layout, dtype, *run_forward(x, layout))
+    check_backward(x, layout, dtype, run_backward(x, layout))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_what_an_earlier_launch_left_in_shared_memory(layout, dtype):
+    """A call whose every value is NaN, then a narrower head, some of whose lanes hold no channel."""
+    nan = draw(50, 8, 1999, 3, 3, 64, dtype, positions=True)
+    for n in ("q", "k", "dq_out", "dk_out"):
+        nan[n].fill_(float("nan"))
+    nan["positions"].fill_(10 ** 6)                                  # past the table
+    x = draw(51, 3, 517, 5, 2, 40, dtype, 8)
+    for _ in range(3):
+        run_forward(nan, layout), run_backward(nan, layout)
+        check_forward(x, layout, dtype, *run_forward(x, layout))
+        run_backward(nan, layout)
+        check_backward(x, layout, dtype, run_backward(x, layout))
+
+
 @pytest.mark.parametrize("d", [64, 40])
 def test_without_weights(d):
     x = draw(41, 2, 30, 2, 3, d, "bf16")

@@ -182,6 +182,32 @@ def test_qk_norm_refusals(L):
     assert back(ws=FAKE + 9 * STEP, n=8) == WORKSPACE
 
 
+def test_elements_at_odd_addresses_are_refused(L):
+    odd = lambda i, *a: t(i, *a, base=FAKE + i * STEP + 1)
+    hk = (B, N, 1, D)
+    for i, name in enumerate(("q", "k", "v")):
+        assert forward(L, **{name: odd(i)}) == INVALID
+    assert forward(L, out=odd(4)) == INVALID
+    g = gate(3)
+    g.data = FAKE + 3 * STEP + 1
+    assert forward(L, g=g) == INVALID
+    assert norm(L, q=odd(0)) == INVALID and norm(L, k=odd(1, hk)) == INVALID and norm(L, qo=odd(2)) == INVALID
+    f32 = t(0, dtype="f32", base=FAKE + 2)
+    assert forward(L, f32, *(t(i, dtype="f32") for i in (1, 2)), g=gate(3, dtype="f32"), out=t(4, dtype="f32")) == INVALID
+
+
+def test_weight_gradients_over_the_rotation_are_refused(L):
+    hk = (B, N, 1, D)
+    back = lambda r, wq: L.mhla_qk_norm_backward(*ref(t(0), t(1, hk)), None, None, 1e-6, *ref(r),
+                                                 *ref(t(2), t(3, hk), t(4), t(5, hk)), wq, None, None, 8, None)
+    table, positions = FAKE + 20 * STEP, FAKE + 30 * STEP
+    r = rot(positions=positions)
+    assert back(r, FAKE + 40 * STEP) == WORKSPACE           # all but the workspace given here is in order
+    assert back(r, table + N * 32 * 8 - 4) == INVALID
+    assert back(r, table - 4 * D + 4) == INVALID
+    assert back(r, positions + 4 * B * N - 4) == INVALID
+
+
 def test_views_of_one_projection_pass_the_overlap_checks(L):
     """Interleaved views share no element: only the workspace given here is refused."""
     st = (N * 4 * H * D, 4 * H * D, D)

@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(256, BWD ? 2 : 3) qk_norm_lanes(const QkNormPr
     const char* const stage = shared + static_cast<int>(round % Held::kStages) * Held::kStage;
     asm volatile("cp.async.wait_group %0;" ::"n"(Held::kStages - 1) : "memory");
     float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, s[4] = {};
-    if (p.table) {
+    if (p.table && live) {   // the lanes behind the head's channels have copied none
       const float4* const turns = reinterpret_cast<const float4*>(stage + Held::kRows) + threadIdx.x;
       const float4 f = turns[0], g = turns[256];
       c[0] = f.x; s[0] = f.y; c[1] = f.z; s[1] = f.w;

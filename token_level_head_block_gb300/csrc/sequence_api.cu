@@ -14,6 +14,13 @@ namespace {
 
 bool empty(const mhla_tensor_t* t) { return t->B == 0 || t->H == 0; }
 
+// What every tensor of these calls must be: a sound description at an address its elements may have.
+int check_elements(const mhla_tensor_t* t) {
+  const int rc = check_tensor(t);
+  if (rc != MHLA_OK) return rc;
+  return reinterpret_cast<uintptr_t>(t->data) % elem_bytes(t->dtype) == 0 ? MHLA_OK : MHLA_ERR_INVALID_ARG;
+}
+
 Operand operand(const mhla_tensor_t* t) { return Operand{t->data, t->stride_b, t->stride_n, t->stride_h}; }
 
 // The [B, N, H, 1] companion of q.
@@ -23,17 +30,18 @@ bool gate_shape(const mhla_tensor_t* q, const mhla_tensor_t* g) {
 
 int64_t state_bytes(const mhla_tensor_t* q) { return q->B * q->H * q->d * q->d * int64_t{4}; }
 
-bool plain_overlap(const void* a, const void* b, int64_t bytes) {
+bool plain_overlap(const void* a, const void* b, int64_t bytes, int64_t bytes_b) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && overlaps(x, x + static_cast<uintptr_t>(bytes), y, y + static_cast<uintptr_t>(bytes));
+  return a && b && overlaps(x, x + static_cast<uintptr_t>(bytes), y, y + static_cast<uintptr_t>(bytes_b));
 }
+bool plain_overlap(const void* a, const void* b, int64_t bytes) { return plain_overlap(a, b, bytes, bytes); }
 
 // Each CTA owns (b, h) and a span of tokens; b, h and the span fit one 31-bit
 // grid axis.
 int check_gated(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v, const mhla_tensor_t* g,
                 float scale) {
   for (const mhla_tensor_t* t : {q, k, v, g}) {
-    const int rc = check_tensor(t);
+    const int rc = check_elements(t);
     if (rc != MHLA_OK) return rc;
   }
   if (!same_shape(q, k) || !same_shape(q, v) || !gate_shape(q, g)) return MHLA_ERR_SHAPE;
@@ -117,7 +125,7 @@ extern "C" mhla_status_t mhla_gated_forward(const mhla_tensor_t* q, const mhla_t
                                             const mhla_tensor_t* out, float* state_out, void* workspace,
                                             size_t workspace_bytes, void* stream) {
   int rc = check_gated(q, k, v, g, scale);
-  if (rc == MHLA_OK) rc = check_tensor(out);
+  if (rc == MHLA_OK) rc = check_elements(out);
   if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
   if (!same_shape(q, out)) return MHLA_ERR_SHAPE;
   if (empty(q)) return MHLA_OK;
@@ -145,7 +153,7 @@ extern "C" mhla_status_t mhla_gated_backward(const mhla_tensor_t* q, const mhla_
                                              size_t workspace_bytes, void* stream) {
   int rc = check_gated(q, k, v, g, scale);
   for (const mhla_tensor_t* t : {dout, dq, dk, dv, dg})
-    if (rc == MHLA_OK) rc = check_tensor(t);
+    if (rc == MHLA_OK) rc = check_elements(t);
   if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
   for (const mhla_tensor_t* t : {dout, dq, dk, dv})
     if (!same_shape(q, t)) return MHLA_ERR_SHAPE;
@@ -174,7 +182,7 @@ extern "C" mhla_status_t mhla_gated_step(const mhla_tensor_t* q, const mhla_tens
                                          const mhla_tensor_t* g, float scale, float* state,
                                          const mhla_tensor_t* out, void* stream) {
   int rc = check_gated(q, k, v, g, scale);
-  if (rc == MHLA_OK) rc = check_tensor(out);
+  if (rc == MHLA_OK) rc = check_elements(out);
   if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
   if (!same_shape(q, out) || q->N != 1) return MHLA_ERR_SHAPE;
   if (empty(q)) return MHLA_OK;
@@ -197,7 +205,7 @@ namespace {
 int qk_norm_problem(const mhla_tensor_t* q, const mhla_tensor_t* k, const float* q_weight, const float* k_weight,
                     float eps, const mhla_rotation_t* rot, QkNormProblem* p) {
   for (const mhla_tensor_t* t : {q, k}) {
-    const int rc = check_tensor(t);
+    const int rc = check_elements(t);
     if (rc != MHLA_OK) return rc;
   }
   if (q->B != k->B || q->N != k->N || q->d != k->d || q->dtype != k->dtype) return MHLA_ERR_SHAPE;
@@ -257,7 +265,7 @@ extern "C" mhla_status_t mhla_qk_norm(const mhla_tensor_t* q, const mhla_tensor_
   QkNormProblem p;
   int rc = qk_norm_problem(q, k, q_weight, k_weight, eps, rot, &p);
   for (const mhla_tensor_t* t : {q_out, k_out})
-    if (rc == MHLA_OK) rc = check_tensor(t);
+    if (rc == MHLA_OK) rc = check_elements(t);
   if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
   if (!same_shape(q, q_out) || !same_shape(k, k_out)) return MHLA_ERR_SHAPE;
   rc = check_normed(p, q_out, q, {k, k_out});
@@ -286,7 +294,7 @@ extern "C" mhla_status_t mhla_qk_norm_backward(const mhla_tensor_t* q, const mhl
   QkNormProblem p;
   int rc = qk_norm_problem(q, k, q_weight, k_weight, eps, rot, &p);
   for (const mhla_tensor_t* t : {dq_out, dk_out, dq, dk})
-    if (rc == MHLA_OK) rc = check_tensor(t);
+    if (rc == MHLA_OK) rc = check_elements(t);
   if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
   if (!same_shape(q, dq_out) || !same_shape(k, dk_out) || !same_shape(q, dq) || !same_shape(k, dk))
     return MHLA_ERR_SHAPE;
@@ -296,7 +304,9 @@ extern "C" mhla_status_t mhla_qk_norm_backward(const mhla_tensor_t* q, const mhl
   if (!states_aligned({dq_weight, dk_weight}) || plain_overlap(dq_weight, dk_weight, 4 * p.d))
     return MHLA_ERR_INVALID_ARG;
   for (const float* w : {dq_weight, dk_weight}) {
-    if (plain_overlap(w, q_weight, 4 * p.d) || plain_overlap(w, k_weight, 4 * p.d)) return MHLA_ERR_INVALID_ARG;
+    if (plain_overlap(w, q_weight, 4 * p.d) || plain_overlap(w, k_weight, 4 * p.d) ||
+        plain_overlap(w, p.table, 4 * p.d, p.rows * p.pairs * 8) || plain_overlap(w, p.positions, 4 * p.d, p.B * p.N * 4))
+      return MHLA_ERR_INVALID_ARG;
     for (const mhla_tensor_t* t : {q, k, dq_out, dk_out, dq, dk})
       if (!empty(t) && meets(t, w, 4 * p.d)) return MHLA_ERR_INVALID_ARG;
   }
