@@ -160,6 +160,20 @@ def test_spans_of_wide_heads_and_of_float32(B, N, H, d, dtype):
     check_backward(x, dtype, d ** -0.5, run_backward(x, d ** -0.5))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,N,H,d", [(2, 777, 12, 40), (1, 333, 3, 24), (3, 150, 5, 100), (10, 200, 6, 8)])
+def test_what_an_earlier_launch_left_on_the_chip(B, N, H, d, dtype):
+    """A call whose every value is NaN, then one with rows, channels and tokens behind its ends."""
+    nan = draw(60, 4, 2048, 12, 128 if d > 64 else 64, dtype)
+    nan = {n: torch.full_like(t, float("nan")) for n, t in nan.items()}
+    x = draw(61, B, N, H, d, dtype)
+    for _ in range(2):
+        run_forward(nan, 1.0), run_backward(nan, 1.0)
+        check_forward(x, dtype, d ** -0.5, *run_forward(x, d ** -0.5))
+        run_forward(nan, 1.0), run_backward(nan, 1.0)
+        check_backward(x, dtype, d ** -0.5, run_backward(x, d ** -0.5))
+
+
 def test_backward_against_differences_of_the_forward():
     """Central differences of the framework's own forward, float32, along a direction per input.
 
