@@ -522,6 +522,12 @@ def _float_array(name, x, shape, like):
     return x.data_ptr()
 
 
+def _new_float(shape, twin, like):
+    """A float32 tensor of this shape on like's device, by its twin if there is one (the shorter call)."""
+    import torch
+    return torch.empty(shape, dtype=torch.float32, device=like.device) if twin is None else torch.empty_like(twin)
+
+
 def _same_device(like, *tensors):
     index = like.get_device()
     if index < 0:
@@ -586,7 +592,7 @@ def gated_forward(q, k, v, g, scale=1.0, state=None, out=None, state_out=None, w
     if out is None:
         out = torch.empty_like(q)
     if state_out is None:
-        state_out = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
+        state_out = _new_float((B, H, d, d), state, q)
     dq = _heads(q)
     args = (dq, _heads(k), _heads(v), _gates(g), scale, _float_array("state", state, (B, H, d, d), q), _heads(out),
             _float_array("state_out", state_out, (B, H, d, d), q))
@@ -606,9 +612,9 @@ def gated_backward(q, k, v, g, dout, scale=1.0, state=None, dstate_out=None, dq=
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(q) if dk is None else dk
     dv = torch.empty_like(q) if dv is None else dv
-    dg = torch.empty((B, N, H), dtype=q.dtype, device=q.device) if dg is None else dg
+    dg = torch.empty_like(g) if dg is None else dg
     if dstate is None:
-        dstate = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
+        dstate = _new_float((B, H, d, d), state if dstate_out is None else dstate_out, q)
     desc = _heads(q)
     square = (B, H, d, d)
     args = (desc, _heads(k), _heads(v), _gates(g), _heads(dout), scale, _float_array("state", state, square, q),
@@ -702,9 +708,9 @@ def qk_norm_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, eps=1e-
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     if dq_weight is None:
-        dq_weight = torch.empty(d, dtype=torch.float32, device=q.device)
+        dq_weight = _new_float((d,), q_weight, q)
     if dk_weight is None:
-        dk_weight = torch.empty(d, dtype=torch.float32, device=q.device)
+        dk_weight = _new_float((d,), k_weight, q)
     desc = _heads(q)
     args = (desc, _heads(k), _float_array("q_weight", q_weight, (d,), q), _float_array("k_weight", k_weight, (d,), q), eps,
             _rotation(q, table, positions, layout), _heads(dq_out), _heads(dk_out), _heads(dq), _heads(dk),

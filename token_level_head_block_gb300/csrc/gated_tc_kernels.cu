@@ -432,6 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
+  // The scan behind its spans' states starts on the SMs that form none; its first loads do not depend on
+  // them.  [4, 4096, 12, 64] forward 57.1 us in turn, 54.9 so.  (Other launches of a call stay in turn: small grids
+  // that start early crowd the few SMs that are idle then: gradients of the same shape 115 us, 142 so.)
+  if (ONLY_STATE && threadIdx.x == 0) ptx::grid_dep_launch();
+  if (!ONLY_STATE && warp <= kIssuer) ptx::grid_dep_wait();
 
   if (warp >= kGates) {
     // ------------------------------------------------------------ gates: the two warps take the chunks in turn
@@ -439,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Sum all = {0.0f, 0.0f};
     float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (me < count) g = load_gates(p, b, h, chunk_of(me), lane);
+    if (!ONLY_STATE) ptx::grid_dep_wait();
 #pragma unroll 1
     for (int n = me; n < count; n += 2) {
       if (n >= kGateRing && !gwarp_wait(bar.gates_freed + n % kGateRing, n / kGateRing - 1, abortf)) break;
@@ -531,6 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 #pragma unroll 1
     for (int n = 0; n < min(count, kStages); ++n) load(n);
+    if (!ONLY_STATE) ptx::grid_dep_wait();
     const bool leader = elect_one();
     constexpr uint32_t idesc = idesc_bf16_f32(64, DH, true, true);
     const uint64_t v0 = smem_desc(smem_u32(smem + kVTile), kSbo, kSbo, 2), k0 = smem_desc(smem_u32(kp), kSbo, kSbo, 2);
@@ -912,6 +919,11 @@ int launch(const ScanSet& set, const TcMaps& maps, int scans, cudaStream_t s) {
     return MHLA_ERR_CUDA;
   const unsigned grid = static_cast<unsigned>(set.BH * (ONLY_STATE ? set.spans - 1 : set.spans));
   KernelTimer timer(ONLY_STATE ? "gated_tc_span_state" : "gated_tc_scan", s);
+  if (!ONLY_STATE && set.scan[0].join)   // directly behind the states of the spans
+    return launch_dependent(gated_tc_scan<DH, ONLY_STATE>, dim3(grid, scans), dim3(kThreads), kBytes, s, set, maps) ==
+                   cudaSuccess
+               ? MHLA_OK
+               : MHLA_ERR_CUDA;
   gated_tc_scan<DH, ONLY_STATE><<<dim3(grid, scans), kThreads, kBytes, s>>>(set, maps);
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
