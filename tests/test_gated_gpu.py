@@ -406,6 +406,28 @@ def test_what_is_not_finite_reaches_no_earlier_token(N, H, d, bad):
         assert (np.abs(out[:, :at] - plain[:, :at]) <= 2.0 ** -7 * np.abs(plain[:, :at]) + 2.0 ** -13 * size).all()
 
 
+@pytest.mark.parametrize("bad", [0.0, float("nan")])
+@pytest.mark.parametrize("N,H,d", [(150, 2, 64), (600, 40, 64), (1500, 11, 64), (700, 3, 32), (150, 2, 100), (6000, 4, 64)])
+def test_a_state_updated_in_place(N, H, d, bad):
+    """The same bits as with a state of its own, on a busy machine too (whose CTAs of one call start far apart)."""
+    x = draw(40, 2, N, H, d, "bf16")
+    x["v"][1, N // 3, 1, 3] = bad
+    args = [gpu(x[n]) for n in ("q", "k", "v", "g")]
+    out, last = mhla.gated_forward(*args, scale=0.125, state=gpu(x["state"]))
+    torch.cuda.synchronize()
+    other, load = torch.cuda.Stream(), torch.randn(4096, 4096, device=DEV)
+    for busy in (False, True, True, True):
+        state = gpu(x["state"])
+        torch.cuda.synchronize()
+        if busy:
+            with torch.cuda.stream(other):
+                for _ in range(3):
+                    load @ load
+        o, s = mhla.gated_forward(*args, scale=0.125, state=state, state_out=state)
+        torch.cuda.synchronize()
+        assert torch.equal(o.nan_to_num(7.0), out.nan_to_num(7.0)) and torch.equal(s.nan_to_num(7.0), last.nan_to_num(7.0))
+
+
 @pytest.mark.parametrize("N,H", [(150, 2), (1500, 4)])
 def test_a_gradient_that_is_not_finite_reaches_no_later_token(N, H):
     """dout of one token: dk and dv of its token and earlier, dq of itself."""

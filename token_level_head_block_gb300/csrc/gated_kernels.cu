@@ -1274,8 +1274,8 @@ int launch_gated_forward(const GatedProblem& p, const float* state_in, const Ope
   if (c.spans > 1) {
     int rc = r.run(set, 1, true);
     // A few spans are joined by the scan as it starts: a launch for it costs 4 us, a span's
-    // loads from L2 0.7.
-    const bool join = r.tc && c.spans <= 6;
+    // loads from L2 0.7.  Not when the last span's CTA writes the state that the others would read.
+    const bool join = r.tc && c.spans <= 6 && (!state_in || state_out != state_in);
     if (rc == MHLA_OK && !join) rc = run_join(set, 1, r.s);
     if (rc != MHLA_OK) return rc;
     set.scan[0].join = join;

@@ -879,13 +879,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         gain(n, kL);
       }
     }
-    float* to = ONLY_STATE ? a.local + (bh * p.spans + span) * p.d * p.d
-                           : a.last && span == (reverse ? 0 : p.spans - 1) ? a.last + bh * p.d * p.d : nullptr;
-    if (to && holds) {
+    // A scan's last state goes out behind everything else (it may lie where the first one does, which
+    // redo_span reads), from where the scaled k was.
+    float* to = ONLY_STATE ? a.local + (bh * p.spans + span) * p.d * p.d : reinterpret_cast<float*>(kp);
+    const int width = ONLY_STATE ? p.d : 64;
+    if (holds) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int r = r0 + 8 * ((i >> 1) & 1), c = c0 + 8 * (i >> 2) + (i & 1);
-        if (r < p.d && c < p.d) to[r * p.d + c] = S[i];
+        if (r < p.d && c < p.d) to[r * width + c] = S[i];
       }
     }
   }
@@ -896,6 +898,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     a.decay[bh * p.spans + span] = exp2_of(add(ctl.decay[0], ctl.decay[1]), Sum{0.0f, 0.0f});
   if (!ONLY_STATE && *reinterpret_cast<volatile uint32_t*>(&ctl.bad) && !ctl.abort)
     redo_span(p, a, smem, bh, span, first * kTcChunk, min(p.N, (first + count) * kTcChunk));
+  if (!ONLY_STATE && a.last && span == (reverse ? 0 : p.spans - 1)) {
+    const float* from = reinterpret_cast<const float*>(kp);
+    for (int i = threadIdx.x; i < p.d * p.d; i += kThreads)
+      a.last[bh * p.d * p.d + i] = from[i / p.d * 64 + i % p.d];
+  }
 }
 
 bool operand_map(const ScanSet& set, int64_t B, const Operand& o, CUtensorMap* m) {
