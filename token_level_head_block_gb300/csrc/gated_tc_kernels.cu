@@ -18,7 +18,7 @@
 // the loads (TMA, three stages), two prepare the gates.  A thread of a score or output warp
 // owns a row, so a row's factor is a register and the columns' factors are read by broadcast.
 //
-// Measured, all launches: bf16 [4, 4096, 12, 64] forward 57 us, gradients 115; [4, 65536, 6, 64] forward
+// Measured, all launches: bf16 [4, 4096, 12, 64] forward 55 us, gradients 115; [4, 65536, 6, 64] forward
 // 341 us; [2, 16384, 70, 32] gradients 930 us.  A chunk takes an SM 2.9 us where HBM would need 1.5: with
 // the splits left out the pipeline runs at HBM's rate, with them the warps issue 14,000 instructions
 // a chunk and hand over five times.  Not faster: equal shares of k's rows for two roles (1.1x), waits that sleep
@@ -144,6 +144,10 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
+
+// Lets the next grid on the stream, if it was launched with programmatic serialization, start as
+// soon as every CTA of this one has come here; it still waits (ptx::grid_dep_wait) for what this one writes.
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // D (+)= A[tensor memory] B[shared memory].
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -435,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The scan behind its spans' states starts on the SMs that form none; its first loads do not depend on
   // them.  [4, 4096, 12, 64] forward 57.1 us in turn, 54.9 so.  (Other launches of a call stay in turn: small grids
   // that start early crowd the few SMs that are idle then: gradients of the same shape 115 us, 142 so.)
-  if (ONLY_STATE && threadIdx.x == 0) ptx::grid_dep_launch();
+  if (ONLY_STATE && threadIdx.x == 0) grid_dep_launch();
   if (!ONLY_STATE && warp <= kIssuer) ptx::grid_dep_wait();
 
   if (warp >= kGates) {

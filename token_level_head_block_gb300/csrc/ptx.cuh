@@ -196,10 +196,6 @@ __device__ __forceinline__ void tma_store_5d(const void* tmap, const void* src, 
 // with programmatic serialization) have completed and their writes are visible.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Lets the next grid on the stream, if it was launched with programmatic serialization, start as
-// soon as every CTA of this one has come here; it still waits (grid_dep_wait) for what this one writes.
-__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // Drops a 128-byte L2 line without writing it back (its contents become
 // undefined): for a scratch buffer whose last reader is done with it.
 __device__ __forceinline__ void discard_l2_line(const void* p) {
