@@ -983,7 +983,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<DK>, sizeof(T) == 2 ? (DK <= 64 
 // there, then the running sum of q.dq - k.dk.  The sums restart at every span,
 // so their rounding does not grow with the sequence.  Two floats a token are read and one gate written
 // (with stride H), so a CTA to a span is bound by the latency of its rounds: 9 us of the 115 of gradients of
-// bf16 [4, 4096, 12, 64], 30 of the 930 of [2, 16384, 70, 32].
+// bf16 [4, 4096, 12, 64], 25 of the 922 of [2, 16384, 70, 32].  (1024 threads a CTA: 9, 25.)
 struct GateGrad {
   const float *qdots, *kdots;   // [slices][B][H][N]
   const float *enter, *leave;   // states entering each span forwards and backwards (both with v's channels as rows)
@@ -995,32 +995,48 @@ struct GateGrad {
 
 template <typename T>
 __global__ void __launch_bounds__(256) gated_gate_grad(const __grid_constant__ GateGrad p) {
+  constexpr int kThreads = 256, kWarps = kThreads / 32;
   constexpr int kEach = 8;   // tokens a thread, so that a long span takes few rounds
-  __shared__ float part[8];
-  __shared__ float head;
+  __shared__ float part[kWarps];
   const int64_t span = blockIdx.x % p.spans, bh = blockIdx.x / p.spans, b = bh / p.H, h = bh % p.H;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t dd = static_cast<int64_t>(p.d) * p.d;
+  const int64_t t0 = span * p.span_tokens, t1 = min(p.N, t0 + p.span_tokens);
+  // what a thread's tokens of a round add, thread 0 the last ones
+  auto load = [&](int64_t end, float (&x)[kEach]) {
+    const int64_t t = end - 1 - kEach * static_cast<int64_t>(threadIdx.x);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) x[e] = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < p.slices; ++k) {
+      const int64_t i = (k * p.BH + bh) * p.N + t;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e)
+        if (t - e >= t0) x[e] += p.qdots[i - e] - p.kdots[i - e];
+    }
+  };
+  float ahead[kEach];
+  load(t1, ahead);
   float s = 0.0f;
   const int d = p.d;
   if (span + 1 < p.spans) {
     const float *x = p.enter + (bh * p.spans + span + 1) * dd, *y = p.leave + (bh * p.spans + span) * dd;
     if (d % 2 == 0) {   // d * d a multiple of four, and so is every state's start
 #pragma unroll 8
-      for (int i = threadIdx.x; i < d * d / 4; i += 256) {
+      for (int i = threadIdx.x; i < d * d / 4; i += kThreads) {
         const float4 f = reinterpret_cast<const float4*>(x)[i], g = reinterpret_cast<const float4*>(y)[i];
         s = fmaf(f.x, g.x, fmaf(f.y, g.y, fmaf(f.z, g.z, fmaf(f.w, g.w, s))));
       }
     } else {
-      for (int i = threadIdx.x; i < d * d; i += 256) s = fmaf(x[i], y[i], s);
+      for (int i = threadIdx.x; i < d * d; i += kThreads) s = fmaf(x[i], y[i], s);
     }
   } else if (p.dlast) {
     const float *x = p.last + bh * dd, *y = p.dlast + bh * dd;
     // a warp takes 8 rows by 16 columns of x: whole sectors of both
     const int tiles = (d + 15) / 16, all = tiles * ((d + 7) / 8);
-    const bool quads = d % 4 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
+    const bool quads = d % 4 == 0;
 #pragma unroll 4
-    for (int i = warp; i < all; i += 8) {
+    for (int i = warp; i < all; i += kWarps) {
       const int r = i / tiles * 8 + (lane & 7), c = i % tiles * 16 + 4 * (lane >> 3);
       if (r >= d || c >= d) continue;
       float f[4] = {};
@@ -1039,25 +1055,15 @@ __global__ void __launch_bounds__(256) gated_gate_grad(const __grid_constant__ G
   for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(~0u, s, k);
   if (lane == 0) part[warp] = s;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float t = 0.0f;
-    for (int i = 0; i < 8; ++i) t += part[i];
-    head = t;
-  }
-  __syncthreads();
-  const int64_t t0 = span * p.span_tokens, t1 = min(p.N, t0 + p.span_tokens);
-  float carry = head;
-  for (int64_t end = t1; end > t0; end -= 256 * kEach) {
-    const int64_t t = end - 1 - kEach * static_cast<int64_t>(threadIdx.x);   // thread 0 takes the last ones
+  float carry = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) carry += part[i];
+  for (int64_t end = t1; end > t0; end -= kThreads * kEach) {
+    const int64_t t = end - 1 - kEach * static_cast<int64_t>(threadIdx.x);
     float x[kEach];
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) x[e] = 0.0f;
-    for (int k = 0; k < p.slices; ++k) {
-      const int64_t i = (k * p.BH + bh) * p.N + t;
-#pragma unroll
-      for (int e = 0; e < kEach; ++e)
-        if (t - e >= t0) x[e] += p.qdots[i - e] - p.kdots[i - e];
-    }
+    for (int e = 0; e < kEach; ++e) x[e] = ahead[e];
+    load(end - kThreads * kEach, ahead);   // the next round's loads run under this one's sums
 #pragma unroll
     for (int e = 1; e < kEach; ++e) x[e] += x[e - 1];
     float sum = x[kEach - 1];
@@ -1066,12 +1072,12 @@ __global__ void __launch_bounds__(256) gated_gate_grad(const __grid_constant__ G
       const float y = __shfl_up_sync(~0u, sum, k);
       if (lane >= k) sum += y;
     }
-    __syncthreads();   // the last round's totals are read
+    __syncthreads();   // the last totals are read
     if (lane == 31) part[warp] = sum;
     __syncthreads();
     float before = carry, all = carry;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kWarps; ++i) {
       if (i < warp) before += part[i];
       all += part[i];
     }

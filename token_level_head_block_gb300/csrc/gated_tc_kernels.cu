@@ -19,7 +19,7 @@
 // owns a row, so a row's factor is a register and the columns' factors are read by broadcast.
 //
 // Measured, all launches: bf16 [4, 4096, 12, 64] forward 55 us, gradients 115; [4, 65536, 6, 64] forward
-// 341 us; [2, 16384, 70, 32] gradients 930 us.  A chunk takes an SM 2.9 us where HBM would need 1.5: with
+// 341 us; [2, 16384, 70, 32] gradients 922 us.  A chunk takes an SM 2.9 us where HBM would need 1.5: with
 // the splits left out the pipeline runs at HBM's rate, with them the warps issue 14,000 instructions
 // a chunk and hand over five times.  Not faster: equal shares of k's rows for two roles (1.1x), waits that sleep
 // (1.0 to 1.05x), one waiting lane a warp (1.5x), terms left out (0.94x, and less exact).
