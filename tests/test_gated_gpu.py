@@ -375,6 +375,39 @@ def test_captured_and_replayed_with_new_values():
     check_backward(y, "bf16", 0.125, grads)
 
 
+@pytest.mark.parametrize("B,N,H,d", [(4, 1024, 12, 64), (1, 9000, 12, 64), (3, 900, 2, 128)])
+def test_calls_behind_one_another_that_share_a_workspace(B, N, H, d):
+    """Each reads what the one in front wrote (its v, its state), the scan's launch starting before its spans' states are
+    there; eagerly, and captured and replayed."""
+    x = {n: gpu(t) for n, t in draw(62, B, N, H, d, "bf16").items()}
+    size = max(mhla.gated_workspace_size(x["q"]), mhla.gated_backward_workspace_size(x["q"]))
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+
+    def chain(wait):
+        got, v, state = [], x["v"].clone(), x["state"].clone()
+        for _ in range(3):
+            v = v * 1.0
+            v, state = mhla.gated_forward(x["q"], x["k"], v, x["g"], scale=0.125, state=state, workspace=ws)
+            wait()
+            got += [v, state]
+            got += mhla.gated_backward(x["q"], x["k"], v, x["g"], x["dout"], scale=0.125, state=state, workspace=ws)
+            wait()
+        return got
+
+    one_by_one = chain(torch.cuda.synchronize)
+    eager = chain(lambda: None)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = chain(lambda: None)
+    for t in captured:
+        t.fill_(float("nan"))
+    graph.replay(), graph.replay()
+    torch.cuda.synchronize()
+    assert mhla.device_status() == 0
+    assert all(torch.isfinite(a).all() for a in one_by_one)
+    assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(one_by_one, eager, captured))
+
+
 def test_nan_stays_in_its_head():
     x = draw(34, 2, 150, 2, 64, "bf16")
     x["v"][0, 70, 1, 3] = float("nan")
