@@ -27,7 +27,7 @@
 // Times, all launches of a call:
 //   bf16  [8, 2048, 16, 128]  forward  282 us      [4, 4096, 16, 80]  gradients  964 us
 //   f32   [8, 2048, 16, 128]  forward  816 us      [8, 6871, 4, 64]   gradients  826 us
-//   f32   [3, 5181, 4, 64]    forward   86 us      [8, 4096, 16, 32]  forward    272 us
+//   f32   [3, 5181, 4, 64]    forward   86 us      [8, 4096, 16, 32]  forward    243 us
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -777,7 +777,7 @@ __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::kOut
 }
 
 template <typename T, int DK, bool ASYNC>
-__global__ void __launch_bounds__(32 * kWarpsOf<DK>, sizeof(T) == 2 ? (DK <= 64 ? 3 : 1) : 1)
+__global__ void __launch_bounds__(32 * kWarpsOf<DK>, DK <= (sizeof(T) == 2 ? 64 : 32) ? 3 : 1)
     gated_scan(const __grid_constant__ ScanSet p) {
   using L = Tile<T, DK, ASYNC>;
   using M = ScanShared<T, DK, ASYNC>;
@@ -1096,10 +1096,10 @@ __global__ void __launch_bounds__(256) gated_gate_grad(const __grid_constant__ G
 
 int padded(int32_t d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
 
-// CTAs of gated_scan an SM holds.
+// CTAs of gated_scan an SM holds.  (float32 [2, 3000, 10, 32] gradients: two 111 us, three 92, four 95.)
 int ctas_an_sm(const GatedProblem& p) {
   if (p.d > 64) return 1;
-  return p.dtype == MHLA_BF16 ? 3 : 2;
+  return p.dtype == MHLA_BF16 || p.d <= 32 ? 3 : 2;
 }
 
 // As many spans as one wave of CTAs takes: a few beyond it cost a second wave (float32 [3, 5181, 4, 64],
