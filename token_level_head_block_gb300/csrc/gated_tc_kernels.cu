@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rows = static_cast<int>(min(p.N - t0, static_cast<int64_t>(32)));   // in the sequence
         const bool part_in = 32 * half + 8 * part < p.d;
         uint4 z[4];
-        if (a.dots) {
+        if (a.dots && 32 * half < DH) {
           const __nv_bfloat16* x = dot + (t0 + part_row) * a.dot.sn + 32 * half + 8 * part;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f1 = steep ? w.enter[q] * w.row[row] : w.enter[q], f2 = steep ? 1.0f : w.row[row];
         float sum = 0.0f;
         uint8_t* mine = smem + s * L::kStage + 4096 * q + 2048 * half;
-        if (a.dots) {
+        if (a.dots && 32 * half < DH) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) *staged(mine, part_row + 8 * i, part) = z[i];
           __syncwarp();
@@ -752,8 +752,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i)
             if (part_in && part_row + 8 * i < rows)
               *reinterpret_cast<uint4*>(to + 8 * i * a.out.sn) = *staged(mine, part_row + 8 * i, part);
-          __syncwarp();
+          // The tile's next contents come by TMA, which these stores must be in front of: the barrier
+          // below orders ordinary accesses alone.
+          fence_proxy_async_smem();
         }
+        __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar.freed + s);
           mbar_arrive(bar.gates_freed + n % kGateRing);
