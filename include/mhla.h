@@ -484,15 +484,18 @@ mhla_status_t mhla_gated_forward(const mhla_tensor_t* q, const mhla_tensor_t* k,
  *   dS_t = scale q_t dout_t^T + exp(g_{t+1}) dS_{t+1}:
  *   dq_t = scale S_t dout_t,   dk_t = dS_t v_t,   dv_t = dS_t^T k_t,
  *   dg_t = exp(g_t) <S_{t-1}, dS_t>,   dstate_in = exp(g_0) dS_0.
- * dg_t is taken as a running sum of q_t . dq_t - k_t . dk_t in float32 from
- * the unrounded dq and dk, restarted with <S, dS> at the end of every span of
- * the sequence.
+ * dg_t is summed from what has the gate between its two tokens, every term
+ * with the gate's decay in it: its rounding is a share of exp(g_t) <|S_{t-1}|,
+ * |dS_t|> however strongly gates forget, and a closed gate has 0.
+ * An infinity or NaN in k or v of a token reaches dg of later tokens alone, one
+ * in q or dout dg of its own and of earlier ones.
  *   q, k, v, g, scale, state_in   those of the forward.
  *   dout, dq, dk, dv  device tensors shaped like q;  dg  shaped like g.
  *   dstate_in    device float32 [B][H][d][d], or NULL when not wanted.
  * The written tensors share no element with one another or with an input (views
  * interleaved in a token's row are fine).  The states are recomputed from k, v
- * and g.  workspace, stream, statuses and empty calls as for the forward. */
+ * and g.  workspace, stream, statuses and empty calls as for the forward; the
+ * workspace holds, for every 64 tokens of a head, two d x d states. */
 mhla_status_t mhla_gated_backward_workspace_size(const mhla_tensor_t* q, size_t* bytes);
 mhla_status_t mhla_gated_backward(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v,
                                   const mhla_tensor_t* g, const mhla_tensor_t* dout, float scale,

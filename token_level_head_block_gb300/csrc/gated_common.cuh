@@ -29,7 +29,8 @@ struct Scan {
   float* last;          // state after the last span [B][H][d][d], or null
   float* local;         // gated_span_state: a span's own contribution [B][H][spans][d][d]
   float* decay;         // and its decay [B][H][spans]
-  float* dots;          // sums of dot_t . out_t before rounding [slices][B][H][N], or null
+  float* dots;          // dot_t . (what out_t takes from the state that enters its chunk) [slices][B][H][N], or null
+  float* entries;       // the state that enters each chunk [B][H][chunks][d][d], or null
   float out_scale;      // of the scores
   float state_scale;    // of what a query reads from the state
   float k_scale;        // of what a token adds to the state

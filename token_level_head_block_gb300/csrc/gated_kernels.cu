@@ -4,8 +4,7 @@
 //   dq_t = scale S_t do_t         the recurrence itself with (do, v, k) for (q, k, v)
 //   dv_t = dS_t^T k_t             the recurrence run backwards with (k, q, do)
 //   dk_t = dS_t v_t               the same with (v, do, q)
-//   dg_t = exp(g_t) <S_{t-1}, dS_t>, where <S_t, dS_t> = dg_t + k_t . dk_t = dg_{t+1} + q_t . dq_t,
-// so dg is a running sum of q . dq - k . dk from the end.
+//   dg_t = exp(g_t) <S_{t-1}, dS_t>   a sum over pairs of tokens (gated_gate_grad below)
 //
 // gated_scan takes every type, size and alignment; bf16 with d <= 64 and enough tokens goes to
 // the tcgen05 kernels of gated_tc_kernels.cu (wants_tc below).  A CTA walks a span of
@@ -614,11 +613,11 @@ struct ScanShared {
 };
 
 // The outputs of a chunk for one warp's 16 rows: what they read from the state,
-// the tokens of other blocks, then their own block's.
-template <typename T, int DK, bool ASYNC, bool REVERSE>
+// the tokens of other blocks, then their own block's.  of_state(o) looks at the first of these, times its row's decay.
+template <typename T, int DK, bool ASYNC, bool REVERSE, typename OfState>
 __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::kOutTiles, (Terms<T>::kIn > 1)>& o,
                                            const char* stage, uint32_t s_base, const Gates& w, float out_scale, int own, int col0,
-                                           int lane) {
+                                           int lane, OfState of_state) {
   using L = Tile<T, DK, ASYNC>;
   constexpr int kScore = Terms<T>::kScore, kState = Terms<T>::kState, NV = L::kOutTiles, P = NV / 2, kSteps = kChunk / 16;
   constexpr bool kApart = L::kIn > 1;
@@ -661,6 +660,7 @@ __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::kOut
       o.main[n][e] = enter * o.get(n, e);
       if (kApart) o.small[kApart ? n : 0][e] = 0.0f;
     }
+  of_state(o);
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     if (REVERSE ? s <= own : s >= own) continue;
@@ -884,19 +884,33 @@ __global__ void __launch_bounds__(32 * kWarpsOf<DK>, DK <= (sizeof(T) == 2 ? 64 
     const Gates& w = gates[i & 1];
     const int row = rows0 + (lane >> 2);
     const int64_t t0 = chunk_of(i) * kChunk;
+    if (a.entries) {
+      float* to = a.entries + (bh * p.chunks + chunk_of(i)) * p.d * p.d;
+#pragma unroll
+      for (int m = 0; m < L::kRowTiles; ++m)
+#pragma unroll
+        for (int n = 0; n < L::kColTiles; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = at.row + 16 * m + 8 * e, c = c0 + at.col + 8 * n;
+            if (r >= p.d || c >= p.d) continue;
+            if (p.d % 2 == 0) {   // then whole pairs, at even places
+              *reinterpret_cast<float2*>(to + r * p.d + c) = make_float2(S[m][n][2 * e], S[m][n][2 * e + 1]);
+            } else {
+              to[r * p.d + c] = S[m][n][2 * e];
+              if (c + 1 < p.d) to[r * p.d + c + 1] = S[m][n][2 * e + 1];
+            }
+          }
+    }
     {
       Accumulators<NV, (L::kIn > 1)> o;
-      if (reverse)
-        read_chunk<T, DK, ASYNC, true>(o, stage, s_base, w, a.out_scale, own, col0, lane);
-      else
-        read_chunk<T, DK, ASYNC, false>(o, stage, s_base, w, a.out_scale, own, col0, lane);
-
-      // rows out: rounded once, through this warp's own rows of q
-      if (a.dots) {
+      // a row's dot with what it reads from the state, for the gates' gradient
+      auto of_state = [&](const Accumulators<NV, (L::kIn > 1)>& o) {
+        if (!a.dots) return;
         const T* dot = static_cast<const T*>(a.dot.data) + b * a.dot.sb + h * a.dot.sh + c0;
-        float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
+          float sum = 0.0f;
           const int64_t t = t0 + row + 8 * f;
           if (t < p.N) {
 #pragma unroll
@@ -906,19 +920,26 @@ __global__ void __launch_bounds__(32 * kWarpsOf<DK>, DK <= (sizeof(T) == 2 ? 64 
               if constexpr (ASYNC) {
                 if (c0 + c < p.d) {
                   const uint32_t xx = *reinterpret_cast<const uint32_t*>(x);
-                  sum[f] = fmaf(o.get(n, 2 * f), low(xx), fmaf(o.get(n, 2 * f + 1), high(xx), sum[f]));
+                  sum = fmaf(o.main[n][2 * f], low(xx), fmaf(o.main[n][2 * f + 1], high(xx), sum));
                 }
               } else {
-                if (c0 + c < p.d) sum[f] = fmaf(o.get(n, 2 * f), to_f(x[0]), sum[f]);
-                if (c0 + c + 1 < p.d) sum[f] = fmaf(o.get(n, 2 * f + 1), to_f(x[1]), sum[f]);
+                if (c0 + c < p.d) sum = fmaf(o.main[n][2 * f], to_f(x[0]), sum);
+                if (c0 + c + 1 < p.d) sum = fmaf(o.main[n][2 * f + 1], to_f(x[1]), sum);
               }
             }
           }
-          sum[f] += __shfl_xor_sync(~0u, sum[f], 1);
-          sum[f] += __shfl_xor_sync(~0u, sum[f], 2);
-          if ((lane & 3) == 0 && t < p.N) a.dots[((slice * (L::kWarps / 4) + half) * p.BH + bh) * p.N + t] = sum[f];
+          sum += __shfl_xor_sync(~0u, sum, 1);
+          sum += __shfl_xor_sync(~0u, sum, 2);
+          if ((lane & 3) == 0 && t < p.N)
+            a.dots[((slice * (L::kWarps / 4) + half) * p.BH + bh) * p.N + t] = w.row[row + 8 * f] * sum;
         }
-      }
+      };
+      if (reverse)
+        read_chunk<T, DK, ASYNC, true>(o, stage, s_base, w, a.out_scale, own, col0, lane, of_state);
+      else
+        read_chunk<T, DK, ASYNC, false>(o, stage, s_base, w, a.out_scale, own, col0, lane, of_state);
+
+      // rows out: rounded once, through this warp's own rows of q
       if constexpr (ASYNC) {
         if (L::kWarps == 4)
           __syncwarp();   // every lane has read its rows of q
@@ -979,116 +1000,295 @@ __global__ void __launch_bounds__(32 * kWarpsOf<DK>, DK <= (sizeof(T) == 2 ? 64 
   }
 }
 
-// dg over one span of one (b, h), 2048 tokens at a time from its end: <S, dS>
-// there, then the running sum of q.dq - k.dk.  The sums restart at every span,
-// so their rounding does not grow with the sequence.  Two floats a token are read and one gate written
-// (with stride H), so a CTA to a span is bound by the latency of its rounds: 9 us of the 115 of gradients of
-// bf16 [4, 4096, 12, 64], 25 of the 922 of [2, 16384, 70, 32].  (1024 threads a CTA: 9, 25.)
+// dg over one chunk of one (b, h).  With S the state that enters the chunk and D the gradient of the one that
+// leaves it, dg_t = e^{g_t} <S_{t-1}, dS_t> is the sum of what has the gate between its two tokens:
+//   pairs of the chunk    M_ij = scale e^{b_i - b_j} (q_i . k_j)(do_i . v_j)    j < t <= i
+//   queries and S         r_i  = scale e^{b_i} q_i . S do_i                     t <= i     (dots of the scan of dq)
+//   keys and D            c_j  = e^{B - b_j} k_j . D v_j                        j < t      (dots of the scan of dk)
+//   both states           e^B <S, D>
+// Nothing cancels: every term carries the decay of gate t, so dg is as exact as its own terms however strongly
+// gates forget, a closed gate has 0, and what is not finite stays on its side.  (A running sum of q . dq - k . dk,
+// which needs no pairs, has the error of all it has summed, however small dg itself.)
+//
+// A warp takes a block of 16 rows i and walks the blocks of columns j up to its own: both dots on mma.sync,
+// then sums over M's rows (for the gates of the rows' block) and over its columns (for the gates of the columns'
+// block); a gate in between takes whole blocks, and the pairs of one block are summed for each of its gates.
 struct GateGrad {
-  const float *qdots, *kdots;   // [slices][B][H][N]
-  const float *enter, *leave;   // states entering each span forwards and backwards (both with v's channels as rows)
-  const float *last, *dlast;    // the state behind the last token (rows of v), its gradient (rows of k) or null
-  Operand dg;
-  int64_t N, H, BH, span_tokens;
-  int32_t spans, d, slices;
+  Operand q, k, v, dout, g, dg;
+  const float *qdots, *kdots;    // r and c [slices][B][H][N]
+  const float *enter, *leave;    // S and D of every chunk, both with v's channels as rows
+  int64_t N, H, BH, chunks;      // chunks of 64 SUB tokens
+  int32_t d, slices;
+  float scale;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(256) gated_gate_grad(const __grid_constant__ GateGrad p) {
-  constexpr int kThreads = 256, kWarps = kThreads / 32;
-  constexpr int kEach = 8;   // tokens a thread, so that a long span takes few rounds
+// float32's three terms take turns in shared memory, (q, k) and then (do, v): two CTAs an SM at d = 128.
+template <typename T, int DK, int SUB>
+struct GateTile {
+  static constexpr int kIn = Terms<T>::kIn, kTokens = kChunk * SUB, kThreads = 2 * kTokens, kBlocks = kTokens / 16;
+  static constexpr int kTurns = kIn > 1 ? 2 : 1;
+  static constexpr int kPart = kChunk * DK * 2;   // bytes of a plane of 64 tokens
+  static constexpr int kOperand = SUB * kIn * kPart;
+  static constexpr int kBytes = (kTurns > 1 ? 2 : 4) * kOperand;
+};
+
+// Rows 16 own .. times columns 16 s .. of x y^T, both operands in parts of 64 tokens.
+template <typename T, int DK, int SUB>
+__device__ __forceinline__ void dots_of_block(float (&c)[2][4], uint32_t x, uint32_t y, int own, int s, int lane) {
+  using L = GateTile<T, DK, SUB>;
+  x += (own >> 2) * L::kIn * L::kPart;
+  y += (s >> 2) * L::kIn * L::kPart;
+  const int xr = 16 * (own & 3) + (lane & 7) + ((lane >> 3) & 1) * 8, yr = 16 * (s & 3) + (lane & 7) + (lane >> 4) * 8;
+  Accumulators<2, (L::kIn > 1)> acc;
+  acc.clear();
+#pragma unroll(L::kIn > 1 ? 1 : DK / 16)
+  for (int ks = 0; ks < DK / 16; ++ks) {
+    uint32_t a[L::kIn][4], b[L::kIn][1][4];
+#pragma unroll
+    for (int t = 0; t < L::kIn; ++t) {
+      ldsm(a[t], x + t * L::kPart + unit_at<DK>(xr, 2 * ks + (lane >> 4)));
+      ldsm(b[t][0], y + t * L::kPart + unit_at<DK>(yr, 2 * ks + ((lane >> 3) & 1)));
+    }
+    mma_terms(acc, 0, a, b);
+  }
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[f][e] = acc.get(f, e);
+}
+
+// Sum over a warp's eight lanes of one column.
+__device__ __forceinline__ float column_total(float x) {
+#pragma unroll
+  for (int s = 4; s < 32; s <<= 1) x += __shfl_xor_sync(~0u, x, s);
+  return x;
+}
+
+template <typename T, int DK, bool ASYNC, int SUB>
+__global__ void __launch_bounds__(2 * kChunk * SUB) gated_gate_grad(const __grid_constant__ GateGrad p) {
+  using L = GateTile<T, DK, SUB>;
+  constexpr int kTokens = L::kTokens, kBlocks = L::kBlocks, kWarps = L::kThreads / 32;
+  static_assert(kWarps == kBlocks && kBlocks * kBlocks + 2 * kBlocks <= L::kThreads, "a warp to a block of rows");
+  extern __shared__ __align__(16) char smem[];
+  __shared__ __align__(16) float hi[kTokens], lo[kTokens];   // b_i
+  __shared__ float r_dot[kTokens], c_dot[kTokens];
+  __shared__ float rows[kTokens], cols[kTokens];             // r and c, with the pairs of two blocks
+  __shared__ float within[kTokens];                          // of the pairs of the gate's own block
+  __shared__ float column[kBlocks][kTokens];                 // M's columns, summed over a block of rows
+  __shared__ float between[kBlocks][kBlocks], r_block[kBlocks], c_block[kBlocks];
   __shared__ float part[kWarps];
-  const int64_t span = blockIdx.x % p.spans, bh = blockIdx.x / p.spans, b = bh / p.H, h = bh % p.H;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t dd = static_cast<int64_t>(p.d) * p.d;
-  const int64_t t0 = span * p.span_tokens, t1 = min(p.N, t0 + p.span_tokens);
-  // what a thread's tokens of a round add, thread 0 the last ones
-  auto load = [&](int64_t end, float (&x)[kEach]) {
-    const int64_t t = end - 1 - kEach * static_cast<int64_t>(threadIdx.x);
+  __shared__ float run_hi[kTokens / 32], run_lo[kTokens / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, me = threadIdx.x, d = p.d;
+  const int64_t chunk = blockIdx.x % p.chunks, bh = blockIdx.x / p.chunks, b = bh / p.H, h = bh % p.H;
+  const int64_t t0 = chunk * kTokens;
+  const int count = static_cast<int>(min(p.N - t0, static_cast<int64_t>(kTokens)));
+
+  if constexpr (ASYNC)
+    if (d < DK) {   // columns behind d stay zero
+      for (int i = me; i < L::kBytes / 16; i += L::kThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+      __syncthreads();
+    }
+  using Rows = RowLoader<T, DK, L::kThreads, ASYNC>;
+  auto load = [&](const Operand& x, const Operand& y, char* to) {
+    const Rows of_x(x, b, h, 0, d), of_y(y, b, h, 0, d);
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) x[e] = 0.0f;
-#pragma unroll 4
-    for (int k = 0; k < p.slices; ++k) {
-      const int64_t i = (k * p.BH + bh) * p.N + t;
-#pragma unroll
-      for (int e = 0; e < kEach; ++e)
-        if (t - e >= t0) x[e] += p.qdots[i - e] - p.kdots[i - e];
+    for (int i = 0; i < SUB; ++i) {
+      char *xp = to + i * L::kIn * L::kPart, *yp = xp + L::kOperand;
+      if constexpr (ASYNC) {
+        of_x.load(xp, SUB * chunk + i, p.N);
+        of_y.load(yp, SUB * chunk + i, p.N);
+      } else {
+        load_plain(SUB * chunk + i, p.N, PlainPart<T, DK, L::kThreads>{of_x, xp}, PlainPart<T, DK, L::kThreads>{of_y, yp});
+      }
     }
   };
-  float ahead[kEach];
-  load(t1, ahead);
-  float s = 0.0f;
-  const int d = p.d;
-  if (span + 1 < p.spans) {
-    const float *x = p.enter + (bh * p.spans + span + 1) * dd, *y = p.leave + (bh * p.spans + span) * dd;
+  const uint32_t first = ptx::smem_u32(smem), second = first + (L::kTurns > 1 ? 0 : 2 * L::kOperand);
+  load(p.q, p.k, smem);
+  if (L::kTurns == 1) load(p.dout, p.v, smem + 2 * L::kOperand);
+  if constexpr (ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
+
+  // the gates' sums and the scans' dots, a token a thread
+  Sum sum = {0.0f, 0.0f};
+  if (me < kTokens) {
+    float g = 0.0f, r = 0.0f, c = 0.0f;
+    if (me < count) {
+      g = to_f((static_cast<const T*>(p.g.data) + b * p.g.sb + h * p.g.sh)[(t0 + me) * p.g.sn]);
+      for (int k = 0; k < p.slices; ++k) {
+        const int64_t i = (k * p.BH + bh) * p.N + t0 + me;
+        r += p.qdots[i];
+        c += p.kdots[i];
+      }
+    }
+    r_dot[me] = r;
+    c_dot[me] = c;
+    sum = gate_sum(g);
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      Sum o;
+      o.hi = __shfl_up_sync(~0u, sum.hi, s);
+      o.lo = __shfl_up_sync(~0u, sum.lo, s);
+      if (lane >= s) sum = add(o, sum);
+    }
+    if (lane == 31) {
+      run_hi[warp] = sum.hi;
+      run_lo[warp] = sum.lo;
+    }
+  }
+  {   // <S, D>
+    const int64_t dd = static_cast<int64_t>(d) * d;
+    const float *x = p.enter + (bh * p.chunks + chunk) * dd, *y = p.leave + (bh * p.chunks + chunk) * dd;
+    float s = 0.0f;
     if (d % 2 == 0) {   // d * d a multiple of four, and so is every state's start
-#pragma unroll 8
-      for (int i = threadIdx.x; i < d * d / 4; i += kThreads) {
+#pragma unroll 4
+      for (int i = me; i < d * d / 4; i += L::kThreads) {
         const float4 f = reinterpret_cast<const float4*>(x)[i], g = reinterpret_cast<const float4*>(y)[i];
         s = fmaf(f.x, g.x, fmaf(f.y, g.y, fmaf(f.z, g.z, fmaf(f.w, g.w, s))));
       }
     } else {
-      for (int i = threadIdx.x; i < d * d; i += kThreads) s = fmaf(x[i], y[i], s);
+      for (int i = me; i < d * d; i += L::kThreads) s = fmaf(x[i], y[i], s);
     }
-  } else if (p.dlast) {
-    const float *x = p.last + bh * dd, *y = p.dlast + bh * dd;
-    // a warp takes 8 rows by 16 columns of x: whole sectors of both
-    const int tiles = (d + 15) / 16, all = tiles * ((d + 7) / 8);
-    const bool quads = d % 4 == 0;
-#pragma unroll 4
-    for (int i = warp; i < all; i += kWarps) {
-      const int r = i / tiles * 8 + (lane & 7), c = i % tiles * 16 + 4 * (lane >> 3);
-      if (r >= d || c >= d) continue;
-      float f[4] = {};
-      if (quads) {
-        const float4 q = *reinterpret_cast<const float4*>(x + r * d + c);
-        f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
-      } else {
-        for (int e = 0; e < 4 && c + e < d; ++e) f[e] = x[r * d + c + e];
-      }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(~0u, s, k);
+    if (lane == 0) part[warp] = s;
+  }
+  if constexpr (ASYNC) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  Sum all = {run_hi[0], run_lo[0]};
+#pragma unroll
+  for (int i = 1; i <= kTokens / 32; ++i) {
+    if (i == warp) sum = add(all, sum);
+    if (i < kTokens / 32) all = add(all, Sum{run_hi[i], run_lo[i]});
+  }
+  if (me < kTokens) {
+    hi[me] = sum.hi;
+    lo[me] = sum.lo;
+  }
+  __syncthreads();
+
+  // neighbouring CTAs give the rows that see more to different warps
+  const int own = (warp + static_cast<int>(blockIdx.x)) & (kBlocks - 1), row = 16 * own + (lane >> 2);
+  float kept[L::kTurns > 1 ? kBlocks : 1][2][4];   // q . k
+  if constexpr (L::kTurns > 1) {
+#pragma unroll
+    for (int s = 0; s < kBlocks; ++s)
+      if (s <= own) dots_of_block<T, DK, SUB>(kept[s], first, first + L::kOperand, own, s, lane);
+    __syncthreads();
+    load(p.dout, p.v, smem);
+    __syncthreads();
+  }
+  const float bh0 = hi[row], bl0 = lo[row], bh1 = hi[row + 8], bl1 = lo[row + 8];
+  float of_row[2] = {0.0f, 0.0f};
+#pragma unroll(L::kTurns > 1 ? kBlocks : 1)
+  for (int s = 0; s < kBlocks; ++s) {
+    if (s > own) continue;
+    float m[2][4], z[2][4];
+    if constexpr (L::kTurns > 1) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[f][e] = kept[s][f][e];
+    } else {
+      dots_of_block<T, DK, SUB>(m, first, first + L::kOperand, own, s, lane);
+    }
+    dots_of_block<T, DK, SUB>(z, second, second + L::kOperand, own, s, lane);
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const int j = 16 * s + 8 * f + 2 * (lane & 3);
+      const float2 hj = *reinterpret_cast<const float2*>(hi + j), lj = *reinterpret_cast<const float2*>(lo + j);
+      const float x[4] = {(bh0 - hj.x) + (bl0 - lj.x), (bh0 - hj.y) + (bl0 - lj.y), (bh1 - hj.x) + (bl1 - lj.x),
+                          (bh1 - hj.y) + (bl1 - lj.y)};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (c + e < d) s = fmaf(f[e], y[(c + e) * d + r], s);
+        m[f][e] = j + (e & 1) < row + (e >> 1) * 8 ? m[f][e] * z[f][e] * (p.scale * exp2_fast(x[e])) : 0.0f;
+    }
+    if (s < own) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        of_row[0] += m[f][0] + m[f][1];
+        of_row[1] += m[f][2] + m[f][3];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = column_total(m[f][e] + m[f][e + 2]);
+          if (lane < 4) column[own][16 * s + 8 * f + 2 * lane + e] = x;
+        }
+      }
+    } else {   // gate t of the block: the sum over rows i >= t of what row i holds in front of column t
+      float x[2][2] = {};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float before[2], total[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          float y = m[f][2 * half] + m[f][2 * half + 1];
+#pragma unroll
+          for (int k = 1; k < 4; k <<= 1) {
+            const float o = __shfl_up_sync(~0u, y, k, 4);
+            if ((lane & 3) >= k) y += o;
+          }
+          const float o = __shfl_up_sync(~0u, y, 1, 4);
+          before[f] = (lane & 3) ? o : 0.0f;
+          total[f] = __shfl_sync(~0u, y, 3, 4);
+        }
+        before[1] += total[0];
+        const int i = (lane >> 2) + 8 * half, t = 2 * (lane & 3);
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          if (i >= 8 * f + t) x[f][0] += before[f];
+          if (i >= 8 * f + t + 1) x[f][1] += before[f] + m[f][2 * half];
+        }
+      }
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float y = column_total(x[f][e]);
+          if (lane < 4) within[16 * own + 8 * f + 2 * lane + e] = y;
+        }
     }
   }
 #pragma unroll
-  for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(~0u, s, k);
-  if (lane == 0) part[warp] = s;
+  for (int f = 0; f < 2; ++f) {
+    of_row[f] += __shfl_xor_sync(~0u, of_row[f], 1);
+    of_row[f] += __shfl_xor_sync(~0u, of_row[f], 2);
+    if ((lane & 3) == 0) rows[row + 8 * f] = of_row[f] + r_dot[row + 8 * f];
+  }
   __syncthreads();
-  float carry = 0.0f;
+  const int block = me / 16;   // of this thread's token
+  if (me < kBlocks * kBlocks) {
+    const int i = me / kBlocks, j = me % kBlocks;
+    float s = 0.0f;
+    if (i > j)
+      for (int e = 0; e < 16; ++e) s += column[i][16 * j + e];
+    between[i][j] = s;
+  } else if (me < kBlocks * kBlocks + 2 * kBlocks) {
+    const int i = (me - kBlocks * kBlocks) >> 1;
+    const float* x = (me & 1 ? c_dot : r_dot) + 16 * i;
+    float s = 0.0f;
+    for (int e = 0; e < 16; ++e) s += x[e];
+    (me & 1 ? c_block : r_block)[i] = s;
+  }
+  if (me < kTokens) {
+    float c = c_dot[me];
+    for (int i = block + 1; i < kBlocks; ++i) c += column[i][me];
+    cols[me] = c;
+  }
+  __syncthreads();
+  if (me < count) {
+    float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) carry += part[i];
-  for (int64_t end = t1; end > t0; end -= kThreads * kEach) {
-    const int64_t t = end - 1 - kEach * static_cast<int64_t>(threadIdx.x);
-    float x[kEach];
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) x[e] = ahead[e];
-    load(end - kThreads * kEach, ahead);   // the next round's loads run under this one's sums
-#pragma unroll
-    for (int e = 1; e < kEach; ++e) x[e] += x[e - 1];
-    float sum = x[kEach - 1];
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-      const float y = __shfl_up_sync(~0u, sum, k);
-      if (lane >= k) sum += y;
+    for (int i = 0; i < kWarps; ++i) s += part[i];
+    s = exp2_of(all, Sum{0.0f, 0.0f}) * s + within[me];
+    for (int i = block + 1; i < kBlocks; ++i) {
+      s += r_block[i];
+      for (int j = 0; j < block; ++j) s += between[i][j];
     }
-    __syncthreads();   // the last totals are read
-    if (lane == 31) part[warp] = sum;
-    __syncthreads();
-    float before = carry, all = carry;
+    for (int j = 0; j < block; ++j) s += c_block[j];
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) before += part[i];
-      all += part[i];
+    for (int e = 0; e < 16; ++e) {
+      const int i = 16 * block + e;
+      s += i < me ? cols[i] : rows[i];
     }
-    float lower = __shfl_up_sync(~0u, sum, 1);   // of the threads in front of this one
-    if (lane == 0) lower = 0.0f;
-    before += lower;
-    T* dg = static_cast<T*>(p.dg.data) + b * p.dg.sb + h * p.dg.sh;
-#pragma unroll
-    for (int e = 0; e < kEach; ++e)
-      if (t - e >= t0) from_f(dg + (t - e) * p.dg.sn, before + x[e]);
-    carry = all;
+    from_f(static_cast<T*>(p.dg.data) + b * p.dg.sb + h * p.dg.sh + (t0 + me) * p.dg.sn, s);
   }
 }
 
@@ -1174,6 +1374,33 @@ int run_join(const ScanSet& set, int scans, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
 
+template <typename T, int DK, bool ASYNC, int SUB>
+int launch_gate_grad(const GateGrad& g, cudaStream_t s) {
+  using L = GateTile<T, DK, SUB>;
+  if (cudaFuncSetAttribute(gated_gate_grad<T, DK, ASYNC, SUB>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
+      cudaSuccess)
+    return MHLA_ERR_CUDA;
+  KernelTimer timer("gated_gate_grad", s);
+  gated_gate_grad<T, DK, ASYNC, SUB><<<static_cast<unsigned>(g.BH * g.chunks), L::kThreads, L::kBytes, s>>>(g);
+  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+}
+
+template <typename T, bool ASYNC>
+int run_gate_grad_as(const GateGrad& g, cudaStream_t s) {
+  switch (padded(g.d)) {
+    case 32: return launch_gate_grad<T, 32, ASYNC, 1>(g, s);
+    case 64: return launch_gate_grad<T, 64, ASYNC, 1>(g, s);
+    default: return launch_gate_grad<T, 128, ASYNC, 1>(g, s);
+  }
+}
+
+// tc: chunks of 128 tokens, whose rows suit cp.async.
+int run_gate_grad(const GatedProblem& p, const GateGrad& g, bool tc, bool async, cudaStream_t s) {
+  if (tc) return p.d <= 32 ? launch_gate_grad<__nv_bfloat16, 32, true, 2>(g, s) : launch_gate_grad<__nv_bfloat16, 64, true, 2>(g, s);
+  if (p.dtype == MHLA_F32) return run_gate_grad_as<float, false>(g, s);
+  return async ? run_gate_grad_as<__nv_bfloat16, true>(g, s) : run_gate_grad_as<__nv_bfloat16, false>(g, s);
+}
+
 ScanSet scan_set(const GatedProblem& p, const Cut& c) {
   ScanSet s = {};
   s.g = p.g;
@@ -1211,6 +1438,13 @@ size_t most_span_bytes(const GatedProblem& p, int scans) {
 // Parts of the columns whose dots are summed apart: by gated_scan, the most of either kernel.
 int scan_dot_slices(const GatedProblem& p) { return p.d > 64 ? 4 : 1; }
 int64_t dot_slices(const GatedProblem& p) { return std::max(scan_dot_slices(p), p.d > 32 ? 2 : 1); }
+
+size_t dot_bytes(const GatedProblem& p) { return align_up(static_cast<size_t>(dot_slices(p) * p.B * p.H * p.N) * 4); }
+
+// The state that enters each chunk (chunks of 64 tokens, or 128 of the tcgen05 scan).
+size_t entry_bytes(const GatedProblem& p, int chunk) {
+  return align_up(static_cast<size_t>(p.B * p.H * ((p.N + chunk - 1) / chunk) * p.d * p.d) * 4);
+}
 
 SpanBuffers carve_spans(const GatedProblem& p, const Cut& c, char** base) {
   if (c.spans < 2) return SpanBuffers{nullptr, nullptr};
@@ -1255,9 +1489,7 @@ bool wants_tc(const GatedProblem& p, int scans) {
 size_t gated_workspace_bytes(const GatedProblem& p) { return most_span_bytes(p, 1); }
 
 size_t gated_bwd_workspace_bytes(const GatedProblem& p) {
-  const int64_t bh = p.B * p.H;
-  return 2 * most_span_bytes(p, 3) + 2 * align_up(static_cast<size_t>(dot_slices(p) * bh * p.N) * 4) +
-         align_up(static_cast<size_t>(bh * p.d * p.d) * 4);
+  return 2 * most_span_bytes(p, 3) + 2 * dot_bytes(p) + 2 * entry_bytes(p, kChunk);
 }
 
 int launch_gated_forward(const GatedProblem& p, const float* state_in, const Operand& out, float* state_out,
@@ -1317,21 +1549,21 @@ int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* w
   set.scan[0] = dq; set.scan[1] = dk; set.scan[2] = dv;
   r.tc = r.async && wants_tc(p, 3) && tc_maps(p, set, 3, &r.maps);
   const Cut c = r.tc ? tc_cut(p, 3) : cut_for(p, 3);
-  const int64_t bh = p.B * p.H;
   char* base = static_cast<char*>(workspace);
   const SpanBuffers fwd = carve_spans(p, c, &base), back = carve_spans(p, c, &base);
-  float* qdots = reinterpret_cast<float*>(base);
-  base += align_up(static_cast<size_t>(dot_slices(p) * bh * p.N) * 4);
-  float* kdots = reinterpret_cast<float*>(base);
-  base += align_up(static_cast<size_t>(dot_slices(p) * bh * p.N) * 4);
-  float* last = reinterpret_cast<float*>(base);
+  auto take = [&](size_t bytes) {
+    float* at = reinterpret_cast<float*>(base);
+    base += bytes;
+    return at;
+  };
+  dq.dots = take(dot_bytes(p));
+  dk.dots = take(dot_bytes(p));
+  dq.entries = take(entry_bytes(p, r.tc ? kTcChunk : kChunk));
+  dk.entries = take(entry_bytes(p, r.tc ? kTcChunk : kChunk));
 
   set = scan_set(p, c);
-  dq.last = last;
-  dq.dots = qdots;
   dq.local = fwd.local;
   dq.decay = fwd.decay;
-  dk.dots = kdots;
   dk.local = back.local;
   dk.decay = back.decay;
   set.scan[0] = dq; set.scan[1] = dk; set.scan[2] = dv;
@@ -1348,21 +1580,15 @@ int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* w
   if (rc == MHLA_OK) rc = r.run(set, 3, false);
   if (rc != MHLA_OK) return rc;
   GateGrad gg = {};
-  gg.qdots = qdots; gg.kdots = kdots;
-  gg.enter = fwd.local; gg.leave = back.local;
-  gg.last = last; gg.dlast = b.dstate_out;
-  gg.dg = b.dg;
-  gg.N = p.N; gg.H = p.H; gg.BH = bh;
-  gg.span_tokens = c.span_chunks * (r.tc ? kTcChunk : kChunk);
-  gg.spans = set.spans; gg.d = p.d;
+  gg.q = p.q; gg.k = p.k; gg.v = p.v; gg.dout = b.dout;
+  gg.g = p.g; gg.dg = b.dg;
+  gg.qdots = dq.dots; gg.kdots = dk.dots;
+  gg.enter = dq.entries; gg.leave = dk.entries;
+  gg.N = p.N; gg.H = p.H; gg.BH = p.B * p.H; gg.chunks = c.chunks;
+  gg.d = p.d;
   gg.slices = r.tc ? static_cast<int32_t>(dot_slices(p)) : scan_dot_slices(p);
-  KernelTimer timer("gated_gate_grad", stream);
-  const unsigned grid = static_cast<unsigned>(bh * c.spans);
-  if (p.dtype == MHLA_BF16)
-    gated_gate_grad<__nv_bfloat16><<<grid, 256, 0, r.s>>>(gg);
-  else
-    gated_gate_grad<float><<<grid, 256, 0, r.s>>>(gg);
-  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+  gg.scale = p.scale;
+  return run_gate_grad(p, gg, r.tc, r.async, r.s);
 }
 
 // ------------------------------------------------------------------ one token

@@ -306,8 +306,8 @@ __device__ __forceinline__ void entering(float (&S)[COUNT], const Scan& a, int64
 }
 
 // A whole span again, token by token without the tensor core: for a span whose v held an
-// infinity or NaN, which the masked products (0 times it) carried to earlier rows of its chunk.  Rare and
-// slow; called once, behind the pipeline, so that it costs that no registers.
+// infinity or NaN, which the masked products (0 times it) carried to earlier rows of its chunk (the states and the
+// dots do not meet them).  Rare and slow; called once, behind the pipeline, so that it costs that no registers.
 __device__ __noinline__ void redo_span(const ScanSet& p, const Scan& a, uint8_t* smem, int64_t bh, int64_t span,
                                        int64_t t0, int64_t t1) {
   float* q = reinterpret_cast<float*>(smem);
@@ -351,12 +351,6 @@ __device__ __noinline__ void redo_span(const ScanSet& p, const Scan& a, uint8_t*
       for (int e = 0; e < 8; ++e) o += part[64 * e + c];
       o *= a.state_scale;
       if (c < d) at(a.out, t)[c] = __float2bfloat16_rn(o);
-      if (a.dots) {
-        float x = c < d ? o * to_f(at(a.dot, t)[c]) : 0.0f;
-#pragma unroll
-        for (int e = 16; e; e >>= 1) x += __shfl_xor_sync(~0u, x, e);
-        if ((c & 31) == 0 && (c == 0 || d > 32)) a.dots[((c >> 5) * p.BH + bh) * p.N + t] = x;
-      }
     }
   }
 }
@@ -738,7 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint4 r = *at;
               const uint32_t zz[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) sum = fmaf(o[2 * e], low(zz[e]), fmaf(o[2 * e + 1], high(zz[e]), sum));
+              for (int e = 0; e < 4; ++e)
+                sum = fmaf(__uint_as_float(x[8 * u + 2 * e]), low(zz[e]), fmaf(__uint_as_float(x[8 * u + 2 * e + 1]), high(zz[e]), sum));
             }
             *at = make_uint4(pack(o[0], o[1]), pack(o[2], o[3]), pack(o[4], o[5]), pack(o[6], o[7]));
           }
@@ -761,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(bar.freed + s);
           mbar_arrive(bar.gates_freed + n % kGateRing);
         }
-        if (a.dots && lane < rows && 32 * half < DH) a.dots[(slice * p.BH + bh) * p.N + t0 + lane] = sum;
+        if (a.dots && lane < rows && 32 * half < DH) a.dots[(slice * p.BH + bh) * p.N + t0 + lane] = f2 * (f1 * sum);
       }
     }
   } else {
@@ -875,6 +870,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = n % kStages;
         if (n > 0 && !gwarp_wait(&bar.state_read, n - 1, abortf)) break;
         publish();
+        if (a.entries && holds) {
+          float* to = a.entries + (bh * p.chunks + chunk_of(n)) * p.d * p.d;
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const int r = r0 + 8 * ((i >> 1) & 1), c = c0 + 8 * (i >> 2);
+            if (r < p.d && c < p.d) *reinterpret_cast<float2*>(to + r * p.d + c) = make_float2(S[i], S[i + 1]);
+          }
+        }
         if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + n % kGateRing, n / kGateRing, abortf))
           break;
 #pragma unroll 1
