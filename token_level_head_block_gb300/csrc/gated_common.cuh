@@ -30,7 +30,8 @@ struct Scan {
   float* local;         // gated_span_state: a span's own contribution [B][H][spans][d][d]
   float* decay;         // and its decay [B][H][spans]
   float* dots;          // dot_t . (what out_t takes from the state that enters its chunk) [slices][B][H][N], or null
-  float* entries;       // the state that enters each chunk [B][H][chunks][d][d], or null
+  float* entries;       // the state that enters each chunk [B][H][chunks], as the kernel's threads hold it, or null
+  float* sums;          // the running sums of the gates of each chunk, high parts and low parts, or null (forwards)
   float out_scale;      // of the scores
   float state_scale;    // of what a query reads from the state
   float k_scale;        // of what a token adds to the state

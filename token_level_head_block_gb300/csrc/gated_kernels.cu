@@ -166,8 +166,8 @@ __device__ __forceinline__ float2 load_gates(const ScanSet& p, int64_t b, int64_
   return make_float2(t < p.N ? to_f(g[t * p.g.sn]) : 0.0f, t + 1 < p.N ? to_f(g[(t + 1) * p.g.sn]) : 0.0f);
 }
 
-// One warp: the running sums and the weights of a chunk.  Returns B.
-__device__ __forceinline__ Sum chunk_gates(float2 g, Gates& out, const Scan& a, int lane) {
+// One warp: the running sums and the weights of a chunk; sums: where the former go too, or null.  Returns B.
+__device__ __forceinline__ Sum chunk_gates(float2 g, Gates& out, const Scan& a, int lane, float* sums = nullptr) {
   const Sum first = gate_sum(g.x), second = gate_sum(g.y);
   Sum run = add(first, second);
 #pragma unroll
@@ -207,6 +207,10 @@ __device__ __forceinline__ Sum chunk_gates(float2 g, Gates& out, const Scan& a, 
   addw.y *= a.k_scale;
   *reinterpret_cast<float2*>(out.hi + 2 * lane) = hi;
   *reinterpret_cast<float2*>(out.lo + 2 * lane) = lo;
+  if (sums) {
+    *reinterpret_cast<float2*>(sums + 2 * lane) = hi;
+    *reinterpret_cast<float2*>(sums + kChunk + 2 * lane) = lo;
+  }
   *reinterpret_cast<float2*>(out.row + 2 * lane) = row;
   *reinterpret_cast<float2*>(out.addw + 2 * lane) = addw;
 #pragma unroll
@@ -776,7 +780,8 @@ __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::kOut
   }
 }
 
-template <typename T, int DK, bool ASYNC>
+// GRAD: what the gates' gradient needs is written too.
+template <typename T, int DK, bool ASYNC, bool GRAD>
 __global__ void __launch_bounds__(32 * kWarpsOf<DK>, DK <= (sizeof(T) == 2 ? 64 : 32) ? 3 : 1)
     gated_scan(const __grid_constant__ ScanSet p) {
   using L = Tile<T, DK, ASYNC>;
@@ -859,7 +864,10 @@ __global__ void __launch_bounds__(32 * kWarpsOf<DK>, DK <= (sizeof(T) == 2 ? 64 
 
   // the warps take the gates of the chunks in turn, a chunk ahead
   float2 g = make_float2(0.0f, 0.0f);
-  if (warp == 0) chunk_gates(load_gates<T>(p, b, h, chunk_of(0), lane), gates[0], a, lane);
+  auto sums_of = [&](int i) {
+    return GRAD && a.sums && slice == 0 ? a.sums + (bh * p.chunks + chunk_of(i)) * (2 * kChunk) : nullptr;
+  };
+  if (warp == 0) chunk_gates(load_gates<T>(p, b, h, chunk_of(0), lane), gates[0], a, lane, sums_of(0));
   if (warp == 1 && count > 1) g = load_gates<T>(p, b, h, chunk_of(1), lane);
 
   T* const out = static_cast<T*>(a.out.data) + b * a.out.sb + h * a.out.sh + c0;
@@ -878,35 +886,17 @@ __global__ void __launch_bounds__(32 * kWarpsOf<DK>, DK <= (sizeof(T) == 2 ? 64 
       }
       __syncthreads();
     }
-    if (i + 1 < count && warp == ((i + 1) & 3)) chunk_gates(g, gates[(i + 1) & 1], a, lane);
+    if (i + 1 < count && warp == ((i + 1) & 3)) chunk_gates(g, gates[(i + 1) & 1], a, lane, sums_of(i + 1));
     if (i + 2 < count && warp == ((i + 2) & 3)) g = load_gates<T>(p, b, h, chunk_of(i + 2), lane);
     char* stage = smem + (i % L::kStages) * M::kStage;
     const Gates& w = gates[i & 1];
     const int row = rows0 + (lane >> 2);
     const int64_t t0 = chunk_of(i) * kChunk;
-    if (a.entries) {
-      float* to = a.entries + (bh * p.chunks + chunk_of(i)) * p.d * p.d;
-#pragma unroll
-      for (int m = 0; m < L::kRowTiles; ++m)
-#pragma unroll
-        for (int n = 0; n < L::kColTiles; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = at.row + 16 * m + 8 * e, c = c0 + at.col + 8 * n;
-            if (r >= p.d || c >= p.d) continue;
-            if (p.d % 2 == 0) {   // then whole pairs, at even places
-              *reinterpret_cast<float2*>(to + r * p.d + c) = make_float2(S[m][n][2 * e], S[m][n][2 * e + 1]);
-            } else {
-              to[r * p.d + c] = S[m][n][2 * e];
-              if (c + 1 < p.d) to[r * p.d + c + 1] = S[m][n][2 * e + 1];
-            }
-          }
-    }
     {
       Accumulators<NV, (L::kIn > 1)> o;
       // a row's dot with what it reads from the state, for the gates' gradient
       auto of_state = [&](const Accumulators<NV, (L::kIn > 1)>& o) {
-        if (!a.dots) return;
+        if (!GRAD || !a.dots) return;
         const T* dot = static_cast<const T*>(a.dot.data) + b * a.dot.sb + h * a.dot.sh + c0;
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
@@ -979,6 +969,17 @@ __global__ void __launch_bounds__(32 * kWarpsOf<DK>, DK <= (sizeof(T) == 2 ? 64 
         }
       }
     }
+    if (GRAD && a.entries) {   // as the threads hold it, the tiles that meet the state
+      constexpr int kTiles = L::kRowTiles * L::kColTiles;
+      float4* to = reinterpret_cast<float4*>(a.entries) + (bh * p.chunks + chunk_of(i)) * (DK * DK / 4) +
+                   slice * (kTiles * L::kThreads) + threadIdx.x;
+#pragma unroll
+      for (int m = 0; m < L::kRowTiles; ++m)
+#pragma unroll
+        for (int n = 0; n < L::kColTiles; ++n)
+          if (at.row - (lane >> 2) + 16 * m < p.d && c0 + at.col - 2 * (lane & 3) + 8 * n < p.d)
+            to[(m * L::kColTiles + n) * L::kThreads] = make_float4(S[m][n][0], S[m][n][1], S[m][n][2], S[m][n][3]);
+    }
     const uint32_t k_base = ptx::smem_u32(stage) + L::kIn * L::kK;
     add_chunk<T, DK, ASYNC>(S, k_base, k_base + L::kIn * L::kK, w, warp, lane);
     if (i + 1 < count) {
@@ -1014,48 +1015,67 @@ __global__ void __launch_bounds__(32 * kWarpsOf<DK>, DK <= (sizeof(T) == 2 ? 64 
 // then sums over M's rows (for the gates of the rows' block) and over its columns (for the gates of the columns'
 // block); a gate in between takes whole blocks, and the pairs of one block are summed for each of its gates.
 struct GateGrad {
-  Operand q, k, v, dout, g, dg;
+  Operand q, k, v, dout, dg;
   const float *qdots, *kdots;    // r and c [slices][B][H][N]
-  const float *enter, *leave;    // S and D of every chunk, both with v's channels as rows
-  int64_t N, H, BH, chunks;      // chunks of 64 SUB tokens
+  const float *enter, *leave;    // S and D of every chunk, as the scans hold them
+  const float* sums;             // b of every chunk, high parts and low parts
+  int64_t N, H, BH;
+  uint32_t chunks;               // of 64 SUB tokens
   int32_t d, slices;
   float scale;
 };
 
-// float32's three terms take turns in shared memory, (q, k) and then (do, v): two CTAs an SM at d = 128.
+// bf16 operands lie in shared memory together; float32's three terms take turns, (q, k) and then (do, v).
 template <typename T, int DK, int SUB>
 struct GateTile {
   static constexpr int kIn = Terms<T>::kIn, kTokens = kChunk * SUB, kThreads = 2 * kTokens, kBlocks = kTokens / 16;
   static constexpr int kTurns = kIn > 1 ? 2 : 1;
-  static constexpr int kPart = kChunk * DK * 2;   // bytes of a plane of 64 tokens
-  static constexpr int kOperand = SUB * kIn * kPart;
+  static constexpr int kPlane = kChunk * DK * 2;   // bytes of one term of 64 tokens
+  static constexpr int kOperand = SUB * kIn * kPlane;
   static constexpr int kBytes = (kTurns > 1 ? 2 : 4) * kOperand;
+  static constexpr int kCtas = SUB == 2 ? (DK == 64 ? 3 : 4) : 1;   // an SM holds at least
 };
 
-// Rows 16 own .. times columns 16 s .. of x y^T, both operands in parts of 64 tokens.
+// A block of 16 rows as A operands; float32's three terms stay in shared memory.
 template <typename T, int DK, int SUB>
-__device__ __forceinline__ void dots_of_block(float (&c)[2][4], uint32_t x, uint32_t y, int own, int s, int lane) {
+struct BlockRows {
   using L = GateTile<T, DK, SUB>;
-  x += (own >> 2) * L::kIn * L::kPart;
-  y += (s >> 2) * L::kIn * L::kPart;
-  const int xr = 16 * (own & 3) + (lane & 7) + ((lane >> 3) & 1) * 8, yr = 16 * (s & 3) + (lane & 7) + (lane >> 4) * 8;
-  Accumulators<2, (L::kIn > 1)> acc;
-  acc.clear();
-#pragma unroll(L::kIn > 1 ? 1 : DK / 16)
-  for (int ks = 0; ks < DK / 16; ++ks) {
-    uint32_t a[L::kIn][4], b[L::kIn][1][4];
+  uint32_t at;
+  int row, lane;
+  uint32_t held[L::kIn > 1 ? 1 : DK / 16][4];
+  __device__ __forceinline__ BlockRows(uint32_t x, int own, int lane_) : lane(lane_) {
+    at = x + (own >> 2) * L::kIn * L::kPlane;
+    row = 16 * (own & 3) + (lane & 7) + ((lane >> 3) & 1) * 8;
+    if constexpr (L::kIn == 1)
 #pragma unroll
-    for (int t = 0; t < L::kIn; ++t) {
-      ldsm(a[t], x + t * L::kPart + unit_at<DK>(xr, 2 * ks + (lane >> 4)));
-      ldsm(b[t][0], y + t * L::kPart + unit_at<DK>(yr, 2 * ks + ((lane >> 3) & 1)));
-    }
-    mma_terms(acc, 0, a, b);
+      for (int ks = 0; ks < DK / 16; ++ks) ldsm(held[ks], at + unit_at<DK>(row, 2 * ks + (lane >> 4)));
   }
+  // Their dots with rows 16 s .. of y: an mma accumulator's 16 by 16.
+  __device__ __forceinline__ void dots(float (&c)[2][4], uint32_t y, int s) const {
+    y += (s >> 2) * L::kIn * L::kPlane;
+    const int yr = 16 * (s & 3) + (lane & 7) + (lane >> 4) * 8;
+    Accumulators<2, (L::kIn > 1)> acc;
+    if (L::kIn > 1) acc.clear();
+#pragma unroll(L::kIn > 1 ? 1 : DK / 16)
+    for (int ks = 0; ks < DK / 16; ++ks) {
+      uint32_t a[L::kIn][4], b[L::kIn][1][4];
 #pragma unroll
-  for (int f = 0; f < 2; ++f)
+      for (int t = 0; t < L::kIn; ++t) {
+        if constexpr (L::kIn > 1)
+          ldsm(a[t], at + t * L::kPlane + unit_at<DK>(row, 2 * ks + (lane >> 4)));
+        else
 #pragma unroll
-    for (int e = 0; e < 4; ++e) c[f][e] = acc.get(f, e);
-}
+          for (int e = 0; e < 4; ++e) a[t][e] = held[ks][e];
+        ldsm(b[t][0], y + t * L::kPlane + unit_at<DK>(yr, 2 * ks + ((lane >> 3) & 1)));
+      }
+      mma_terms(acc, 0, a, b, L::kIn == 1 && ks == 0);
+    }
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[f][e] = acc.get(f, e);
+  }
+};
 
 // Sum over a warp's eight lanes of one column.
 __device__ __forceinline__ float column_total(float x) {
@@ -1064,232 +1084,273 @@ __device__ __forceinline__ float column_total(float x) {
   return x;
 }
 
+__host__ __device__ constexpr int front(int block) { return 8 * block * (block - 1); }
+
+// This thread's share of <S, D>.  tcgen05 states are DK x DK floats in one order; the warp-level scan's lie as its
+// threads hold them, some of their tiles behind d and not written.
+template <int DK, int SUB, int THREADS>
+__device__ __forceinline__ float states_dot(const float* enter, const float* leave, int d) {
+  const float4 *x = reinterpret_cast<const float4*>(enter), *y = reinterpret_cast<const float4*>(leave);
+  float s = 0.0f;
+  auto add = [&](int i) {
+    const float4 f = x[i], g = y[i];
+    s = fmaf(f.x, g.x, fmaf(f.y, g.y, fmaf(f.z, g.z, fmaf(f.w, g.w, s))));
+  };
+  if constexpr (SUB == 2) {
+#pragma unroll
+    for (int i = 0; i < DK * DK / 4 / THREADS; ++i) add(threadIdx.x + THREADS * i);
+  } else {
+    using L = Tile<float, DK, false>;
+    constexpr int kSlices = DK / L::DV, kTiles = L::kRowTiles * L::kColTiles;
+#pragma unroll 1
+    for (int slice = 0; slice < kSlices; ++slice)
+#pragma unroll
+      for (int t = 0; t < L::kThreads / THREADS; ++t) {
+        const int thread = threadIdx.x + THREADS * t, warp = thread >> 5;
+        const StatePlace<DK> at(warp, 0);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+          if (at.row + i / L::kColTiles * 16 < d && slice * L::DV + at.col + i % L::kColTiles * 8 < d)
+            add((slice * kTiles + i) * L::kThreads + thread);
+      }
+  }
+  return s;
+}
+
 template <typename T, int DK, bool ASYNC, int SUB>
-__global__ void __launch_bounds__(2 * kChunk * SUB) gated_gate_grad(const __grid_constant__ GateGrad p) {
+__global__ void __launch_bounds__(2 * kChunk * SUB, GateTile<T, DK, SUB>::kCtas) gated_gate_grad(const __grid_constant__ GateGrad p) {
   using L = GateTile<T, DK, SUB>;
   constexpr int kTokens = L::kTokens, kBlocks = L::kBlocks, kWarps = L::kThreads / 32;
-  static_assert(kWarps == kBlocks && kBlocks * kBlocks + 2 * kBlocks <= L::kThreads, "a warp to a block of rows");
-  extern __shared__ __align__(16) char smem[];
-  __shared__ __align__(16) float hi[kTokens], lo[kTokens];   // b_i
-  __shared__ float r_dot[kTokens], c_dot[kTokens];
-  __shared__ float rows[kTokens], cols[kTokens];             // r and c, with the pairs of two blocks
-  __shared__ float within[kTokens];                          // of the pairs of the gate's own block
-  __shared__ float column[kBlocks][kTokens];                 // M's columns, summed over a block of rows
-  __shared__ float between[kBlocks][kBlocks], r_block[kBlocks], c_block[kBlocks];
-  __shared__ float part[kWarps];
-  __shared__ float run_hi[kTokens / 32], run_lo[kTokens / 32];
+  static_assert(kWarps == kBlocks && kBlocks <= 8, "a warp to a block of rows");
+  __shared__ float rows[kTokens];                          // M's rows in front of their block
+  __shared__ float within[kTokens];                        // of the pairs of the gate's own block
+  // columns in front of each block of rows, block i's from front(i) on
+  __shared__ __align__(16) float column[front(kBlocks)];   // M's, summed over the rows
+  __shared__ __align__(16) float factor[front(kBlocks)];   // scale e^{m - b_j}, m at the edge of the block of rows
+  __shared__ float r_block[kBlocks], c_block[kBlocks];     // r and c over a block
+  __shared__ float part[kWarps];                           // of <S, D>
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, me = threadIdx.x, d = p.d;
-  const int64_t chunk = blockIdx.x % p.chunks, bh = blockIdx.x / p.chunks, b = bh / p.H, h = bh % p.H;
-  const int64_t t0 = chunk * kTokens;
+  const uint32_t row_of_batch = blockIdx.x / p.chunks, H = static_cast<uint32_t>(p.H);   // 32-bit divisions
+  const uint32_t chunk = blockIdx.x - row_of_batch * p.chunks;
+  const int64_t bh = row_of_batch, b = row_of_batch / H, h = row_of_batch % H, t0 = static_cast<int64_t>(chunk) * kTokens;
   const int count = static_cast<int>(min(p.N - t0, static_cast<int64_t>(kTokens)));
+  const int block = me / 16, unit = me & 15;   // of the thread's token
+  const float *hi = p.sums + 2 * kTokens * static_cast<int64_t>(blockIdx.x), *lo = hi + kTokens;
+  auto sum_at = [&](int i) { return Sum{hi[i], lo[i]}; };
+  const Sum none = {0.0f, 0.0f};
 
+  extern __shared__ __align__(16) char smem[];
   if constexpr (ASYNC)
     if (d < DK) {   // columns behind d stay zero
       for (int i = me; i < L::kBytes / 16; i += L::kThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
       __syncthreads();
     }
-  using Rows = RowLoader<T, DK, L::kThreads, ASYNC>;
-  auto load = [&](const Operand& x, const Operand& y, char* to) {
-    const Rows of_x(x, b, h, 0, d), of_y(y, b, h, 0, d);
-#pragma unroll
-    for (int i = 0; i < SUB; ++i) {
-      char *xp = to + i * L::kIn * L::kPart, *yp = xp + L::kOperand;
-      if constexpr (ASYNC) {
-        of_x.load(xp, SUB * chunk + i, p.N);
-        of_y.load(yp, SUB * chunk + i, p.N);
-      } else {
-        load_plain(SUB * chunk + i, p.N, PlainPart<T, DK, L::kThreads>{of_x, xp}, PlainPart<T, DK, L::kThreads>{of_y, yp});
-      }
-    }
-  };
   const uint32_t first = ptx::smem_u32(smem), second = first + (L::kTurns > 1 ? 0 : 2 * L::kOperand);
-  load(p.q, p.k, smem);
-  if (L::kTurns == 1) load(p.dout, p.v, smem + 2 * L::kOperand);
-  if constexpr (ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
-
-  // the gates' sums and the scans' dots, a token a thread
-  Sum sum = {0.0f, 0.0f};
-  if (me < kTokens) {
-    float g = 0.0f, r = 0.0f, c = 0.0f;
-    if (me < count) {
-      g = to_f((static_cast<const T*>(p.g.data) + b * p.g.sb + h * p.g.sh)[(t0 + me) * p.g.sn]);
-      for (int k = 0; k < p.slices; ++k) {
-        const int64_t i = (k * p.BH + bh) * p.N + t0 + me;
-        r += p.qdots[i];
-        c += p.kdots[i];
-      }
-    }
-    r_dot[me] = r;
-    c_dot[me] = c;
-    sum = gate_sum(g);
+  if constexpr (ASYNC) {
+    constexpr int kUnits = DK / 8, kRows = L::kThreads / kUnits;   // 16-byte units of a row, rows a pass
+    static_assert(kRows % 8 == 0, "a pass keeps the units' places");
+    const int r = me / kUnits, u = me % kUnits;
+    auto fetch = [&](const Operand& o, uint32_t to) {
+      const T* base = static_cast<const T*>(o.data) + (b * o.sb + h * o.sh + t0 * o.sn);
+      const T* from = base + r * o.sn + 8 * u;
+      to += unit_at<DK>(r, u);
+      if (count == kTokens) {
 #pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      Sum o;
-      o.hi = __shfl_up_sync(~0u, sum.hi, s);
-      o.lo = __shfl_up_sync(~0u, sum.lo, s);
-      if (lane >= s) sum = add(o, sum);
+        for (int i = 0; i < kTokens / kRows; ++i, from += kRows * o.sn) cp_async_16(to + i * kRows * DK * 2, from, 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kTokens / kRows; ++i, from += kRows * o.sn) {
+          const bool in = r + i * kRows < count;
+          cp_async_16(to + i * kRows * DK * 2, in ? from : base, in ? 16 : 0);
+        }
+      }
+    };
+    if (8 * u < d) {
+      fetch(p.q, first);
+      fetch(p.k, first + L::kOperand);
+      fetch(p.dout, second);
+      fetch(p.v, second + L::kOperand);
     }
-    if (lane == 31) {
-      run_hi[warp] = sum.hi;
-      run_lo[warp] = sum.lo;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  auto load = [&](const Operand& x, const Operand& y, char* to) {   // rows that lie otherwise
+    const RowLoader<T, DK, L::kThreads, false> of_x(x, b, h, 0, d), of_y(y, b, h, 0, d);
+    load_plain(static_cast<int64_t>(chunk), p.N, PlainPart<T, DK, L::kThreads>{of_x, to},
+               PlainPart<T, DK, L::kThreads>{of_y, to + L::kOperand});
+  };
+  if constexpr (!ASYNC) {
+    static_assert(SUB == 1, "a part of 64 tokens");
+    load(p.q, p.k, smem);
+    if (L::kTurns == 1) load(p.dout, p.v, smem + 2 * L::kOperand);
+  }
+
+  // the scans' dots, a token a thread
+  float r = 0.0f, c = 0.0f;
+  if (me < count) {
+    const float *x = p.qdots + bh * p.N + t0 + me, *y = p.kdots + bh * p.N + t0 + me;
+#pragma unroll 4
+    for (int k = 0; k < p.slices; ++k, x += p.BH * p.N, y += p.BH * p.N) {
+      r += *x;
+      c += *y;
     }
   }
-  {   // <S, D>
-    const int64_t dd = static_cast<int64_t>(d) * d;
-    const float *x = p.enter + (bh * p.chunks + chunk) * dd, *y = p.leave + (bh * p.chunks + chunk) * dd;
-    float s = 0.0f;
-    if (d % 2 == 0) {   // d * d a multiple of four, and so is every state's start
-#pragma unroll 4
-      for (int i = me; i < d * d / 4; i += L::kThreads) {
-        const float4 f = reinterpret_cast<const float4*>(x)[i], g = reinterpret_cast<const float4*>(y)[i];
-        s = fmaf(f.x, g.x, fmaf(f.y, g.y, fmaf(f.z, g.z, fmaf(f.w, g.w, s))));
-      }
-    } else {
-      for (int i = me; i < d * d; i += L::kThreads) s = fmaf(x[i], y[i], s);
-    }
+  // neighbouring CTAs give the rows that see more to different warps
+  const int own = (warp + static_cast<int>(blockIdx.x)) & (kBlocks - 1), row = 16 * own + (lane >> 2);
+  {
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * DK * DK;
+    float s = states_dot<DK, SUB, L::kThreads>(p.enter + at, p.leave + at, d);
 #pragma unroll
     for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(~0u, s, k);
     if (lane == 0) part[warp] = s;
   }
+  // Pairs of two blocks: e^{b_i - m} e^{m - b_j}, m at the edge of the rows' block, each factor out of one of the sums
+  const Sum m = own ? sum_at(16 * own - 1) : none, b0 = sum_at(row), b1 = sum_at(row + 8);
+  for (int j = lane; j < 16 * own; j += 32) factor[front(own) + j] = p.scale * exp2_of(m, sum_at(j));
+  const float f0 = exp2_of(b0, m), f1 = exp2_of(b1, m);
+  __syncwarp();
+  Two sum0 = two(0.0f, 0.0f), sum1 = sum0;   // of rows row, row + 8
+  auto pairs = [&](const float (&x)[2][4], const float (&y)[2][4], int s) {
+    float z[4];
+    const float* col = factor + front(own) + 16 * s;
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const Two u0 = mul(two(x[f][0], x[f][1]), two(y[f][0], y[f][1])), u1 = mul(two(x[f][2], x[f][3]), two(y[f][2], y[f][3]));
+      const float2 w = *reinterpret_cast<const float2*>(col + 8 * f + 2 * (lane & 3));
+      sum0 = fma(u0, two(w.x, w.y), sum0);
+      sum1 = fma(u1, two(w.x, w.y), sum1);
+      apart(fma(u1, two(f1, f1), mul(u0, two(f0, f0))), z[2 * f], z[2 * f + 1]);
+    }
+    // each column over the warp's eight lanes of it: halves of the columns change hands until a lane pair has one
+    const bool up = lane & 16, right = lane & 8;
+    const float a0 = (up ? z[2] : z[0]) + __shfl_xor_sync(~0u, up ? z[0] : z[2], 16);
+    const float a1 = (up ? z[3] : z[1]) + __shfl_xor_sync(~0u, up ? z[1] : z[3], 16);
+    float a = (right ? a1 : a0) + __shfl_xor_sync(~0u, right ? a0 : a1, 8);
+    a += __shfl_xor_sync(~0u, a, 4);
+    const int j = (up ? 8 : 0) + 2 * (lane & 3) + (right ? 1 : 0);
+    if (!(lane & 4)) column[front(own) + 16 * s + j] = col[j] * a;
+  };
+  using Block = BlockRows<T, DK, SUB>;
   if constexpr (ASYNC) asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
-  Sum all = {run_hi[0], run_lo[0]};
-#pragma unroll
-  for (int i = 1; i <= kTokens / 32; ++i) {
-    if (i == warp) sum = add(all, sum);
-    if (i < kTokens / 32) all = add(all, Sum{run_hi[i], run_lo[i]});
-  }
-  if (me < kTokens) {
-    hi[me] = sum.hi;
-    lo[me] = sum.lo;
-  }
-  __syncthreads();
-
-  // neighbouring CTAs give the rows that see more to different warps
-  const int own = (warp + static_cast<int>(blockIdx.x)) & (kBlocks - 1), row = 16 * own + (lane >> 2);
-  float kept[L::kTurns > 1 ? kBlocks : 1][2][4];   // q . k
+  float x[2][4], y[2][4];
   if constexpr (L::kTurns > 1) {
+    float kept[kBlocks - 1][2][4];   // q . k
+    {
+      const Block q(first, own, lane);
 #pragma unroll
-    for (int s = 0; s < kBlocks; ++s)
-      if (s <= own) dots_of_block<T, DK, SUB>(kept[s], first, first + L::kOperand, own, s, lane);
+      for (int s = 0; s < kBlocks - 1; ++s)
+        if (s < own) q.dots(kept[s], first + L::kOperand, s);
+      q.dots(x, first + L::kOperand, own);
+    }
     __syncthreads();
     load(p.dout, p.v, smem);
     __syncthreads();
-  }
-  const float bh0 = hi[row], bl0 = lo[row], bh1 = hi[row + 8], bl1 = lo[row + 8];
-  float of_row[2] = {0.0f, 0.0f};
-#pragma unroll(L::kTurns > 1 ? kBlocks : 1)
-  for (int s = 0; s < kBlocks; ++s) {
-    if (s > own) continue;
-    float m[2][4], z[2][4];
-    if constexpr (L::kTurns > 1) {
+    const Block z(second, own, lane);
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m[f][e] = kept[s][f][e];
-    } else {
-      dots_of_block<T, DK, SUB>(m, first, first + L::kOperand, own, s, lane);
-    }
-    dots_of_block<T, DK, SUB>(z, second, second + L::kOperand, own, s, lane);
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const int j = 16 * s + 8 * f + 2 * (lane & 3);
-      const float2 hj = *reinterpret_cast<const float2*>(hi + j), lj = *reinterpret_cast<const float2*>(lo + j);
-      const float x[4] = {(bh0 - hj.x) + (bl0 - lj.x), (bh0 - hj.y) + (bl0 - lj.y), (bh1 - hj.x) + (bl1 - lj.x),
-                          (bh1 - hj.y) + (bl1 - lj.y)};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        m[f][e] = j + (e & 1) < row + (e >> 1) * 8 ? m[f][e] * z[f][e] * (p.scale * exp2_fast(x[e])) : 0.0f;
-    }
-    if (s < own) {
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        of_row[0] += m[f][0] + m[f][1];
-        of_row[1] += m[f][2] + m[f][3];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float x = column_total(m[f][e] + m[f][e + 2]);
-          if (lane < 4) column[own][16 * s + 8 * f + 2 * lane + e] = x;
-        }
+    for (int s = 0; s < kBlocks - 1; ++s)
+      if (s < own) {
+        z.dots(y, second + L::kOperand, s);
+        pairs(kept[s], y, s);
       }
-    } else {   // gate t of the block: the sum over rows i >= t of what row i holds in front of column t
-      float x[2][2] = {};
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float before[2], total[2];
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          float y = m[f][2 * half] + m[f][2 * half + 1];
-#pragma unroll
-          for (int k = 1; k < 4; k <<= 1) {
-            const float o = __shfl_up_sync(~0u, y, k, 4);
-            if ((lane & 3) >= k) y += o;
-          }
-          const float o = __shfl_up_sync(~0u, y, 1, 4);
-          before[f] = (lane & 3) ? o : 0.0f;
-          total[f] = __shfl_sync(~0u, y, 3, 4);
-        }
-        before[1] += total[0];
-        const int i = (lane >> 2) + 8 * half, t = 2 * (lane & 3);
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          if (i >= 8 * f + t) x[f][0] += before[f];
-          if (i >= 8 * f + t + 1) x[f][1] += before[f] + m[f][2 * half];
-        }
-      }
-#pragma unroll
-      for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float y = column_total(x[f][e]);
-          if (lane < 4) within[16 * own + 8 * f + 2 * lane + e] = y;
-        }
+    z.dots(y, second + L::kOperand, own);
+  } else {
+    const Block q(first, own, lane), z(second, own, lane);
+#pragma unroll 1
+    for (int s = 0; s <= own; ++s) {
+      q.dots(x, first + L::kOperand, s);
+      z.dots(y, second + L::kOperand, s);
+      if (s < own) pairs(x, y, s);
     }
   }
+  // Pairs of the own block: gate t has the sum over rows i >= t of what row i holds in front of column t.
+  float z[2][2] = {};
 #pragma unroll
   for (int f = 0; f < 2; ++f) {
-    of_row[f] += __shfl_xor_sync(~0u, of_row[f], 1);
-    of_row[f] += __shfl_xor_sync(~0u, of_row[f], 2);
-    if ((lane & 3) == 0) rows[row + 8 * f] = of_row[f] + r_dot[row + 8 * f];
+    const int j = 16 * own + 8 * f + 2 * (lane & 3);
+    const float2 hj = *reinterpret_cast<const float2*>(hi + j), lj = *reinterpret_cast<const float2*>(lo + j);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float w = exp2_of(e < 2 ? b0 : b1, e & 1 ? Sum{hj.y, lj.y} : Sum{hj.x, lj.x});
+      x[f][e] = j + (e & 1) < row + (e >> 1) * 8 ? x[f][e] * y[f][e] * w : 0.0f;
+    }
   }
-  __syncthreads();
-  const int block = me / 16;   // of this thread's token
-  if (me < kBlocks * kBlocks) {
-    const int i = me / kBlocks, j = me % kBlocks;
-    float s = 0.0f;
-    if (i > j)
-      for (int e = 0; e < 16; ++e) s += column[i][16 * j + e];
-    between[i][j] = s;
-  } else if (me < kBlocks * kBlocks + 2 * kBlocks) {
-    const int i = (me - kBlocks * kBlocks) >> 1;
-    const float* x = (me & 1 ? c_dot : r_dot) + 16 * i;
-    float s = 0.0f;
-    for (int e = 0; e < 16; ++e) s += x[e];
-    (me & 1 ? c_block : r_block)[i] = s;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    float before[2], total[2];
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      float u = x[f][2 * half] + x[f][2 * half + 1];
+#pragma unroll
+      for (int k = 1; k < 4; k <<= 1) {
+        const float o = __shfl_up_sync(~0u, u, k, 4);
+        if ((lane & 3) >= k) u += o;
+      }
+      const float o = __shfl_up_sync(~0u, u, 1, 4);
+      before[f] = (lane & 3) ? o : 0.0f;
+      total[f] = __shfl_sync(~0u, u, 3, 4);
+    }
+    before[1] += total[0];
+    const int i = (lane >> 2) + 8 * half, t = 2 * (lane & 3);
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      if (i >= 8 * f + t) z[f][0] += before[f];
+      if (i >= 8 * f + t + 1) z[f][1] += before[f] + x[f][2 * half];
+    }
+  }
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float u = column_total(z[f][e]);
+      if (lane < 4) within[16 * own + 8 * f + 2 * lane + e] = p.scale * u;
+    }
+#pragma unroll
+  for (int f = 0; f < 2; ++f) {
+    float u, w;
+    apart(f ? sum1 : sum0, u, w);
+    u += w;
+    u += __shfl_xor_sync(~0u, u, 1);
+    u += __shfl_xor_sync(~0u, u, 2);
+    if ((lane & 3) == 0) rows[row + 8 * f] = (f ? f1 : f0) * u;
   }
   if (me < kTokens) {
-    float c = c_dot[me];
-    for (int i = block + 1; i < kBlocks; ++i) c += column[i][me];
-    cols[me] = c;
+    float u = (lane & 1 ? c : r) + __shfl_xor_sync(~0u, lane & 1 ? r : c, 1);   // r in even lanes, c in odd ones
+#pragma unroll
+    for (int k = 2; k < 16; k <<= 1) u += __shfl_xor_sync(~0u, u, k);
+    if (unit < 2) (unit ? c_block : r_block)[block] = u;
   }
   __syncthreads();
-  if (me < count) {
-    float s = 0.0f;
+  if (me >= kTokens) return;
+  // rows from the gate's on and columns in front of it within the block
+  r += rows[me];
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) s += part[i];
-    s = exp2_of(all, Sum{0.0f, 0.0f}) * s + within[me];
-    for (int i = block + 1; i < kBlocks; ++i) {
-      s += r_block[i];
-      for (int j = 0; j < block; ++j) s += between[i][j];
-    }
-    for (int j = 0; j < block; ++j) s += c_block[j];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int i = 16 * block + e;
-      s += i < me ? cols[i] : rows[i];
-    }
-    from_f(static_cast<T*>(p.dg.data) + b * p.dg.sb + h * p.dg.sh + (t0 + me) * p.dg.sn, s);
+  for (int i = 1; i < kBlocks; ++i)
+    if (i > block) c += column[front(i) + me];
+  // what every gate of the block has (both states, whole blocks on both sides), a share a lane: a gate meets the
+  // shares from its lane on in r's sum, those in front in c's
+  float share = 0.0f;
+  if (unit < kBlocks) {
+    share = exp2_of(sum_at(kTokens - 1), none) * part[unit];
+    if (unit > block) share += r_block[unit];
+    if (unit < block) share += c_block[unit];
   }
+  if (unit < (kBlocks - 1 - block) * block) {   // 12 pairs of blocks at most
+    const int i = unit * ((256 + block - 1) / block) >> 8, j = unit - i * block;   // unit / block, unit % block
+    const float4* from = reinterpret_cast<const float4*>(column + front(block + 1 + i) + 16 * j);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) share += (from[e].x + from[e].y) + (from[e].z + from[e].w);
+  }
+  r += share;
+  c += share;
+#pragma unroll
+  for (int k = 1; k < 16; k <<= 1) {
+    const float u = __shfl_down_sync(~0u, r, k, 16), w = __shfl_up_sync(~0u, c, k, 16);
+    if (unit + k < 16) r += u;
+    if (unit >= k) c += w;
+  }
+  const float in_front = __shfl_up_sync(~0u, c, 1, 16);
+  const float dg = within[me] + r + (unit ? in_front : 0.0f);
+  if (me < count) from_f(static_cast<T*>(p.dg.data) + b * p.dg.sb + h * p.dg.sh + (t0 + me) * p.dg.sn, dg);
 }
 
 // ------------------------------------------------------------------ launches
@@ -1339,28 +1400,35 @@ int launch_span_state(const ScanSet& set, int scans, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
 
-template <typename T, int DK, bool ASYNC>
+template <typename T, int DK, bool ASYNC, bool GRAD>
 int launch_scan(const ScanSet& set, int scans, cudaStream_t s) {
   using L = Tile<T, DK, ASYNC>;
   constexpr int kBytes = ScanShared<T, DK, ASYNC>::kBytes;
-  if (cudaFuncSetAttribute(gated_scan<T, DK, ASYNC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) !=
+  if (cudaFuncSetAttribute(gated_scan<T, DK, ASYNC, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) !=
       cudaSuccess)
     return MHLA_ERR_CUDA;
   const int64_t slices = (set.d + L::DV - 1) / L::DV;
   KernelTimer timer("gated_scan", s);
-  gated_scan<T, DK, ASYNC><<<dim3(static_cast<unsigned>(set.BH * slices * set.spans), scans), L::kThreads, kBytes, s>>>(set);
+  gated_scan<T, DK, ASYNC, GRAD><<<dim3(static_cast<unsigned>(set.BH * slices * set.spans), scans), L::kThreads, kBytes, s>>>(set);
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+}
+
+template <typename T, int DK, bool ASYNC>
+int run_scan_kernel(const ScanSet& set, int scans, bool span_state, cudaStream_t s) {
+  if (span_state) return launch_span_state<T, DK, ASYNC>(set, scans, s);
+  return scans > 1 ? launch_scan<T, DK, ASYNC, true>(set, scans, s) : launch_scan<T, DK, ASYNC, false>(set, scans, s);
 }
 
 template <typename T, bool ASYNC>
 int run_scans_as(const ScanSet& set, int scans, bool span_state, cudaStream_t s) {
   switch (padded(set.d)) {
-    case 32: return span_state ? launch_span_state<T, 32, ASYNC>(set, scans, s) : launch_scan<T, 32, ASYNC>(set, scans, s);
-    case 64: return span_state ? launch_span_state<T, 64, ASYNC>(set, scans, s) : launch_scan<T, 64, ASYNC>(set, scans, s);
-    default: return span_state ? launch_span_state<T, 128, ASYNC>(set, scans, s) : launch_scan<T, 128, ASYNC>(set, scans, s);
+    case 32: return run_scan_kernel<T, 32, ASYNC>(set, scans, span_state, s);
+    case 64: return run_scan_kernel<T, 64, ASYNC>(set, scans, span_state, s);
+    default: return run_scan_kernel<T, 128, ASYNC>(set, scans, span_state, s);
   }
 }
 
+// One scan is the forward, three are the gradients.
 int run_scans(const GatedProblem& p, const ScanSet& set, int scans, bool async, bool span_state, cudaStream_t s) {
   if (p.dtype == MHLA_F32) return run_scans_as<float, false>(set, scans, span_state, s);
   return async ? run_scans_as<__nv_bfloat16, true>(set, scans, span_state, s)
@@ -1394,7 +1462,7 @@ int run_gate_grad_as(const GateGrad& g, cudaStream_t s) {
   }
 }
 
-// tc: chunks of 128 tokens, whose rows suit cp.async.
+// tc: behind the tcgen05 scans, whose chunks are of 128 tokens.
 int run_gate_grad(const GatedProblem& p, const GateGrad& g, bool tc, bool async, cudaStream_t s) {
   if (tc) return p.d <= 32 ? launch_gate_grad<__nv_bfloat16, 32, true, 2>(g, s) : launch_gate_grad<__nv_bfloat16, 64, true, 2>(g, s);
   if (p.dtype == MHLA_F32) return run_gate_grad_as<float, false>(g, s);
@@ -1441,9 +1509,13 @@ int64_t dot_slices(const GatedProblem& p) { return std::max(scan_dot_slices(p), 
 
 size_t dot_bytes(const GatedProblem& p) { return align_up(static_cast<size_t>(dot_slices(p) * p.B * p.H * p.N) * 4); }
 
-// The state that enters each chunk (chunks of 64 tokens, or 128 of the tcgen05 scan).
+// The state that enters each chunk (of 64 tokens, or 128 of the tcgen05 scan), and the gates' sums in each.
 size_t entry_bytes(const GatedProblem& p, int chunk) {
-  return align_up(static_cast<size_t>(p.B * p.H * ((p.N + chunk - 1) / chunk) * p.d * p.d) * 4);
+  const int64_t side = padded(p.d);
+  return align_up(static_cast<size_t>(p.B * p.H * ((p.N + chunk - 1) / chunk) * side * side) * 4);
+}
+size_t sum_bytes(const GatedProblem& p, int chunk) {
+  return align_up(static_cast<size_t>(p.B * p.H * ((p.N + chunk - 1) / chunk) * chunk) * 8);
 }
 
 SpanBuffers carve_spans(const GatedProblem& p, const Cut& c, char** base) {
@@ -1489,7 +1561,8 @@ bool wants_tc(const GatedProblem& p, int scans) {
 size_t gated_workspace_bytes(const GatedProblem& p) { return most_span_bytes(p, 1); }
 
 size_t gated_bwd_workspace_bytes(const GatedProblem& p) {
-  return 2 * most_span_bytes(p, 3) + 2 * dot_bytes(p) + 2 * entry_bytes(p, kChunk);
+  return 2 * most_span_bytes(p, 3) + 2 * dot_bytes(p) + 2 * entry_bytes(p, kChunk) +
+         std::max(sum_bytes(p, kChunk), sum_bytes(p, kTcChunk));
 }
 
 int launch_gated_forward(const GatedProblem& p, const float* state_in, const Operand& out, float* state_out,
@@ -1558,8 +1631,10 @@ int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* w
   };
   dq.dots = take(dot_bytes(p));
   dk.dots = take(dot_bytes(p));
-  dq.entries = take(entry_bytes(p, r.tc ? kTcChunk : kChunk));
-  dk.entries = take(entry_bytes(p, r.tc ? kTcChunk : kChunk));
+  const int chunk = r.tc ? kTcChunk : kChunk;
+  dq.entries = take(entry_bytes(p, chunk));
+  dk.entries = take(entry_bytes(p, chunk));
+  dq.sums = take(sum_bytes(p, chunk));
 
   set = scan_set(p, c);
   dq.local = fwd.local;
@@ -1581,10 +1656,11 @@ int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* w
   if (rc != MHLA_OK) return rc;
   GateGrad gg = {};
   gg.q = p.q; gg.k = p.k; gg.v = p.v; gg.dout = b.dout;
-  gg.g = p.g; gg.dg = b.dg;
+  gg.dg = b.dg;
+  gg.sums = dq.sums;
   gg.qdots = dq.dots; gg.kdots = dk.dots;
   gg.enter = dq.entries; gg.leave = dk.entries;
-  gg.N = p.N; gg.H = p.H; gg.BH = p.B * p.H; gg.chunks = c.chunks;
+  gg.N = p.N; gg.H = p.H; gg.BH = p.B * p.H; gg.chunks = static_cast<uint32_t>(c.chunks);
   gg.d = p.d;
   gg.slices = r.tc ? static_cast<int32_t>(dot_slices(p)) : scan_dot_slices(p);
   gg.scale = p.scale;

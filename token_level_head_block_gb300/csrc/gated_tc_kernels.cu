@@ -199,7 +199,8 @@ __device__ __forceinline__ Sum shfl_sum(Sum s, int lane) {
 
 // One warp: the running sums and the weights of a chunk (ONLY_STATE: those of the state alone).  Returns B.
 template <bool ONLY_STATE>
-__device__ __forceinline__ Sum chunk_gates(float4 g, typename Layout<ONLY_STATE>::Gates& out, const Scan& a, int lane) {
+__device__ __forceinline__ Sum chunk_gates(float4 g, typename Layout<ONLY_STATE>::Gates& out, const Scan& a, int lane,
+                                           float* sums) {
   const Sum none = {0.0f, 0.0f};
   Sum at[4];
   at[0] = gate_sum(g.x);
@@ -248,6 +249,10 @@ __device__ __forceinline__ Sum chunk_gates(float4 g, typename Layout<ONLY_STATE>
   }
   put(out.hi, hi);
   put(out.lo, lo);
+  if (sums) {
+    put(sums, hi);
+    put(sums + kTcChunk, lo);
+  }
   put(out.row, row);
   put(out.addw, addw);
 #pragma unroll
@@ -366,8 +371,8 @@ __device__ __noinline__ void steep_block(uint32_t (&x)[16], const ChunkGates& w,
   }
 }
 
-// DH: channels the tensor core works on (32 or 64).
-template <int DH, bool ONLY_STATE>
+// DH: channels the tensor core works on (32 or 64).  GRAD: what the gates' gradient needs is written too.
+template <int DH, bool ONLY_STATE, bool GRAD>
 __global__ void __launch_bounds__(kThreads, 1)
     gated_tc_scan(const __grid_constant__ ScanSet p, const __grid_constant__ TcMaps maps) {
   using L = Layout<ONLY_STATE>;
@@ -448,7 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n >= kGateRing && !gwarp_wait(bar.gates_freed + n % kGateRing, n / kGateRing - 1, abortf)) break;
       const float4 now = g;
       if (n + 2 < count) g = load_gates(p, b, h, chunk_of(n + 2), lane);
-      all = add(all, chunk_gates<ONLY_STATE>(now, gates[n % kGateRing], a, lane));
+      all = add(all, chunk_gates<ONLY_STATE>(now, gates[n % kGateRing], a, lane,
+                                             GRAD && a.sums ? a.sums + (bh * p.chunks + chunk_of(n)) * (2 * kTcChunk) : nullptr));
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.gates + n % kGateRing);
     }
@@ -693,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rows = static_cast<int>(min(p.N - t0, static_cast<int64_t>(32)));   // in the sequence
         const bool part_in = 32 * half + 8 * part < p.d;
         uint4 z[4];
-        if (a.dots && 32 * half < DH) {
+        if (GRAD && a.dots && 32 * half < DH) {
           const __nv_bfloat16* x = dot + (t0 + part_row) * a.dot.sn + 32 * half + 8 * part;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -708,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f1 = steep ? w.enter[q] * w.row[row] : w.enter[q], f2 = steep ? 1.0f : w.row[row];
         float sum = 0.0f;
         uint8_t* mine = smem + s * L::kStage + 4096 * q + 2048 * half;
-        if (a.dots && 32 * half < DH) {
+        if (GRAD && a.dots && 32 * half < DH) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) *staged(mine, part_row + 8 * i, part) = z[i];
           __syncwarp();
@@ -728,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          two(__uint_as_float(y[8 * u + e]), __uint_as_float(y[8 * u + e + 1])))),
                     o[e], o[e + 1]);
             uint4* at = staged(mine, lane, (c & 31) / 8 + u);
-            if (a.dots) {
+            if (GRAD && a.dots) {
               const uint4 r = *at;
               const uint32_t zz[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -756,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(bar.freed + s);
           mbar_arrive(bar.gates_freed + n % kGateRing);
         }
-        if (a.dots && lane < rows && 32 * half < DH) a.dots[(slice * p.BH + bh) * p.N + t0 + lane] = f2 * (f1 * sum);
+        if (GRAD && a.dots && lane < rows && 32 * half < DH) a.dots[(slice * p.BH + bh) * p.N + t0 + lane] = f2 * (f1 * sum);
       }
     }
   } else {
@@ -870,20 +876,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = n % kStages;
         if (n > 0 && !gwarp_wait(&bar.state_read, n - 1, abortf)) break;
         publish();
-        if (a.entries && holds) {
-          float* to = a.entries + (bh * p.chunks + chunk_of(n)) * p.d * p.d;
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const int r = r0 + 8 * ((i >> 1) & 1), c = c0 + 8 * (i >> 2);
-            if (r < p.d && c < p.d) *reinterpret_cast<float2*>(to + r * p.d + c) = make_float2(S[i], S[i + 1]);
-          }
-        }
         if (!gwarp_wait(bar.full + s, n / kStages, abortf) || !gwarp_wait(bar.gates + n % kGateRing, n / kGateRing, abortf))
           break;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           scale_rows(smem + s * L::kStage + kKTile, gates[n % kGateRing].addw, kp, g0 + half * kGroups / 2, g1 + half * kGroups / 2);
           if (lane == 0) mbar_arrive(bar.k_ready + half);
+        }
+        if (GRAD && a.entries && holds) {   // as the threads hold it
+          float4* to = reinterpret_cast<float4*>(a.entries) + (bh * p.chunks + chunk_of(n)) * (DH * DH / 4) +
+                       (warp - kScoreWarps) * 128 + lane;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) to[32 * i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
         }
         if (!gwarp_wait(bar.l_done, n, abortf)) break;
         gain(n, kL);
@@ -927,21 +931,21 @@ bool operand_map(const ScanSet& set, int64_t B, const Operand& o, CUtensorMap* m
   return encode_tensor_map(m, 4, o.data, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int DH, bool ONLY_STATE>
+template <int DH, bool ONLY_STATE, bool GRAD = false>
 int launch(const ScanSet& set, const TcMaps& maps, int scans, cudaStream_t s) {
   constexpr int kBytes = static_cast<int>(Layout<ONLY_STATE>::kBytes);
   // a per-device setting: made on every call, for whichever device is current
-  if (cudaFuncSetAttribute(gated_tc_scan<DH, ONLY_STATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) !=
+  if (cudaFuncSetAttribute(gated_tc_scan<DH, ONLY_STATE, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) !=
       cudaSuccess)
     return MHLA_ERR_CUDA;
   const unsigned grid = static_cast<unsigned>(set.BH * (ONLY_STATE ? set.spans - 1 : set.spans));
   KernelTimer timer(ONLY_STATE ? "gated_tc_span_state" : "gated_tc_scan", s);
   if (!ONLY_STATE && set.scan[0].join)   // directly behind the states of the spans
-    return launch_dependent(gated_tc_scan<DH, ONLY_STATE>, dim3(grid, scans), dim3(kThreads), kBytes, s, set, maps) ==
+    return launch_dependent(gated_tc_scan<DH, ONLY_STATE, GRAD>, dim3(grid, scans), dim3(kThreads), kBytes, s, set, maps) ==
                    cudaSuccess
                ? MHLA_OK
                : MHLA_ERR_CUDA;
-  gated_tc_scan<DH, ONLY_STATE><<<dim3(grid, scans), kThreads, kBytes, s>>>(set, maps);
+  gated_tc_scan<DH, ONLY_STATE, GRAD><<<dim3(grid, scans), kThreads, kBytes, s>>>(set, maps);
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
 
@@ -973,8 +977,10 @@ bool tc_maps(const GatedProblem& p, const ScanSet& set, int scans, TcMaps* maps)
 }
 
 int launch_tc_scan(const ScanSet& set, const TcMaps& maps, int scans, bool span_state, cudaStream_t s) {
-  if (set.d <= 32) return span_state ? launch<32, true>(set, maps, scans, s) : launch<32, false>(set, maps, scans, s);
-  return span_state ? launch<64, true>(set, maps, scans, s) : launch<64, false>(set, maps, scans, s);
+  const bool narrow = set.d <= 32;
+  if (span_state) return narrow ? launch<32, true>(set, maps, scans, s) : launch<64, true>(set, maps, scans, s);
+  if (scans > 1) return narrow ? launch<32, false, true>(set, maps, scans, s) : launch<64, false, true>(set, maps, scans, s);
+  return narrow ? launch<32, false>(set, maps, scans, s) : launch<64, false>(set, maps, scans, s);
 }
 
 }  // namespace gated
