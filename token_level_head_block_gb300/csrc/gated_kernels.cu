@@ -12,7 +12,7 @@
 // b_i the sum of the log decays of a chunk's tokens up to i and B that of all,
 //   o_i = scale (e^{b_i} S^T q_i + sum_{j <= i} e^{b_i - b_j} (q_i . k_j) v_j)
 //   S  <- e^B S + sum_j e^{B - b_j} k_j v_j^T
-// and backwards the same with b_j - b_i, B - b_i and b_j for the three exponents.
+// and backwards the same with b_i the sum of the gates behind token i.
 // All four products run on mma.sync m16n8k16 with float32 accumulators; what is
 // not exact in bf16 enters as a sum of bf16 terms (Terms below).  When there are
 // fewer (b, h) than the machine has room for, the sequence is cut into spans:
@@ -146,8 +146,9 @@ __device__ __forceinline__ void mma_terms(Accumulators<NT, APART>& acc, int n0, 
 // What a chunk needs of its gates.  Rows i of a block of 16 tokens see tokens j of other
 // blocks through e^{b_i - b_j} = e^{b_i - m} e^{m - b_j}, m at the edge of the
 // row's block towards them, so neither factor exceeds 1; the state, too, is read with
-// e^{b_i - m} e^m.  (Backwards every difference changes its sign.)  Within a block the
-// difference of the two sums is taken itself.
+// e^{b_i - m} e^m.  Backwards b_i is the sum of the gates behind token i, from the chunk's end, so that what a row
+// sees holds those gates alone (one that is NaN reaches no later token); all else is the same.  Within a block
+// the difference of the two sums is taken itself.
 struct Gates {
   float hi[kChunk], lo[kChunk];   // b_i
   float row[kChunk];              // e^{b_i - m}
@@ -168,41 +169,39 @@ __device__ __forceinline__ float2 load_gates(const ScanSet& p, int64_t b, int64_
 
 // One warp: the running sums and the weights of a chunk; sums: where the former go too, or null.  Returns B.
 __device__ __forceinline__ Sum chunk_gates(float2 g, Gates& out, const Scan& a, int lane, float* sums = nullptr) {
-  const Sum first = gate_sum(g.x), second = gate_sum(g.y);
+  const Sum none = {0.0f, 0.0f}, first = gate_sum(g.x), second = gate_sum(g.y);
+  const bool reverse = a.reverse;
   Sum run = add(first, second);
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
     Sum o;
-    o.hi = __shfl_up_sync(~0u, run.hi, s);
-    o.lo = __shfl_up_sync(~0u, run.lo, s);
-    if (lane >= s) run = add(o, run);
+    o.hi = reverse ? __shfl_down_sync(~0u, run.hi, s) : __shfl_up_sync(~0u, run.hi, s);
+    o.lo = reverse ? __shfl_down_sync(~0u, run.lo, s) : __shfl_up_sync(~0u, run.lo, s);
+    if (reverse ? lane + s < 32 : lane >= s) run = add(o, run);
   }
-  const Sum none = {0.0f, 0.0f};
   auto of_lane = [&](int l) {
     Sum r;
     r.hi = __shfl_sync(~0u, run.hi, l);
     r.lo = __shfl_sync(~0u, run.lo, l);
     return r;
   };
-  const Sum all = of_lane(31);
-  Sum edge[5] = {none, of_lane(7), of_lane(15), of_lane(23), all};   // between the blocks
-  Sum before;
-  before.hi = __shfl_up_sync(~0u, run.hi, 1);
-  before.lo = __shfl_up_sync(~0u, run.lo, 1);
-  if (lane == 0) before = none;
-  const Sum at[2] = {add(before, first), run};
+  const Sum all = of_lane(reverse ? 0 : 31);
+  // at the edge of each block of rows towards what it sees
+  Sum edge[4] = {of_lane(reverse ? 8 : 0), of_lane(reverse ? 16 : 7), of_lane(reverse ? 24 : 15), of_lane(23)};
+  edge[reverse ? 3 : 0] = none;
+  Sum next;   // of the lanes in front (behind)
+  next.hi = reverse ? __shfl_down_sync(~0u, run.hi, 1) : __shfl_up_sync(~0u, run.hi, 1);
+  next.lo = reverse ? __shfl_down_sync(~0u, run.lo, 1) : __shfl_up_sync(~0u, run.lo, 1);
+  if (lane == (reverse ? 31 : 0)) next = none;
+  const Sum at[2] = {reverse ? add(next, second) : add(next, first), reverse ? next : run};
   const int block = lane >> 3;
-  const bool reverse = a.reverse;
-  Sum m = reverse ? edge[1] : edge[0];
+  Sum m = edge[0];
 #pragma unroll
   for (int i = 1; i < 4; ++i)
-    if (block == i) m = reverse ? edge[i + 1] : edge[i];
-  float2 hi, lo, row, addw;
-  hi = make_float2(at[0].hi, at[1].hi);
-  lo = make_float2(at[0].lo, at[1].lo);
-  row = reverse ? make_float2(exp2_of(m, at[0]), exp2_of(m, at[1])) : make_float2(exp2_of(at[0], m), exp2_of(at[1], m));
-  addw = reverse ? make_float2(exp2_of(at[0], none), exp2_of(at[1], none))
-                 : make_float2(exp2_of(all, at[0]), exp2_of(all, at[1]));
+    if (block == i) m = edge[i];
+  const float2 hi = make_float2(at[0].hi, at[1].hi), lo = make_float2(at[0].lo, at[1].lo);
+  const float2 row = make_float2(exp2_of(at[0], m), exp2_of(at[1], m));
+  float2 addw = make_float2(exp2_of(all, at[0]), exp2_of(all, at[1]));
   addw.x *= a.k_scale;
   addw.y *= a.k_scale;
   *reinterpret_cast<float2*>(out.hi + 2 * lane) = hi;
@@ -216,13 +215,12 @@ __device__ __forceinline__ Sum chunk_gates(float2 g, Gates& out, const Scan& a, 
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     if (reverse ? block <= r : block >= r) continue;   // tokens the rows of block r do not see through m
-    const Sum e = reverse ? edge[r + 1] : edge[r];
-    float2 c = reverse ? make_float2(exp2_of(at[0], e), exp2_of(at[1], e)) : make_float2(exp2_of(e, at[0]), exp2_of(e, at[1]));
+    float2 c = make_float2(exp2_of(edge[r], at[0]), exp2_of(edge[r], at[1]));
     c.x *= a.out_scale;
     c.y *= a.out_scale;
     *reinterpret_cast<float2*>(out.col[r] + 2 * lane) = c;
   }
-  if ((lane & 7) == 0) out.enter[block] = a.state_scale * (reverse ? exp2_of(all, m) : exp2_of(m, none));
+  if ((lane & 7) == 0) out.enter[block] = a.state_scale * exp2_of(m, none);
   if (lane == 0) out.total = exp2_of(all, none);
   return all;
 }
@@ -719,7 +717,7 @@ __device__ __forceinline__ void read_chunk(Accumulators<Tile<T, DK, ASYNC>::kOut
     for (int e = 0; e < 4; ++e) {
       const int r = row + (e >> 1) * 8, c = j + (e & 1);
       const bool keep = REVERSE ? c >= r : c <= r;
-      own_sc[f][e] = keep ? own_sc[f][e] * (out_scale * exp2_fast(REVERSE ? -x[e] : x[e])) : 0.0f;
+      own_sc[f][e] = keep ? own_sc[f][e] * (out_scale * exp2_fast(x[e])) : 0.0f;
     }
   }
   uint32_t vb[L::kIn][P][4];

@@ -2,7 +2,7 @@
 // on the fifth-generation tensor cores: bf16, d <= 64, chunks of 128 tokens.
 //
 // A persistent CTA per SM walks a span of chunks.  Per chunk, b_i the sum of the log
-// decays up to token i and B of all of them (backwards every difference changes sign):
+// decays up to token i (backwards: of those behind it) and B of all of them:
 //   scores  S1 = Q K^T                                128 x 128, in tensor memory
 //   P_ij    = scale e^{b_i - b_j} S1_ij for j <= i    two bf16 terms, over S1 in tensor memory
 //   O1      = Q S                                     S the state, two bf16 terms in shared memory
@@ -201,51 +201,60 @@ __device__ __forceinline__ Sum shfl_sum(Sum s, int lane) {
 template <bool ONLY_STATE>
 __device__ __forceinline__ Sum chunk_gates(float4 g, typename Layout<ONLY_STATE>::Gates& out, const Scan& a, int lane,
                                            float* sums) {
-  const Sum none = {0.0f, 0.0f};
-  Sum at[4];
-  at[0] = gate_sum(g.x);
-  at[1] = add(at[0], gate_sum(g.y));
-  at[2] = add(at[1], gate_sum(g.z));
-  at[3] = add(at[2], gate_sum(g.w));
-  Sum run = at[3];
+  const Sum none = {0.0f, 0.0f}, gs[4] = {gate_sum(g.x), gate_sum(g.y), gate_sum(g.z), gate_sum(g.w)};
+  const bool reverse = a.reverse;
+  Sum at[4], run;
+  if (reverse) {
+    at[3] = none;
+    at[2] = gs[3];
+    at[1] = add(gs[2], at[2]);
+    at[0] = add(gs[1], at[1]);
+    run = add(gs[0], at[0]);
+  } else {
+    at[0] = gs[0];
+    at[1] = add(at[0], gs[1]);
+    at[2] = add(at[1], gs[2]);
+    run = at[3] = add(at[2], gs[3]);
+  }
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
     Sum o;
-    o.hi = __shfl_up_sync(~0u, run.hi, s);
-    o.lo = __shfl_up_sync(~0u, run.lo, s);
-    if (lane >= s) run = add(o, run);
+    o.hi = reverse ? __shfl_down_sync(~0u, run.hi, s) : __shfl_up_sync(~0u, run.hi, s);
+    o.lo = reverse ? __shfl_down_sync(~0u, run.lo, s) : __shfl_up_sync(~0u, run.lo, s);
+    if (reverse ? lane + s < 32 : lane >= s) run = add(o, run);
   }
-  const Sum all = shfl_sum(run, 31);
-  Sum before;
-  before.hi = __shfl_up_sync(~0u, run.hi, 1);
-  before.lo = __shfl_up_sync(~0u, run.lo, 1);
-  if (lane == 0) before = none;
+  const Sum all = shfl_sum(run, reverse ? 0 : 31);
+  Sum next;   // of the lanes in front (behind)
+  next.hi = reverse ? __shfl_down_sync(~0u, run.hi, 1) : __shfl_up_sync(~0u, run.hi, 1);
+  next.lo = reverse ? __shfl_down_sync(~0u, run.lo, 1) : __shfl_up_sync(~0u, run.lo, 1);
+  if (lane == (reverse ? 31 : 0)) next = none;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) at[e] = add(before, at[e]);
+  for (int e = 0; e < 4; ++e) at[e] = add(next, at[e]);
   const int block = lane >> 3;
-  const bool reverse = a.reverse;
   auto put = [&](float* to, const float (&x)[4]) {
     reinterpret_cast<float4*>(to)[lane] = make_float4(x[0], x[1], x[2], x[3]);
   };
   if constexpr (ONLY_STATE) {
     float addw[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) addw[e] = a.k_scale * (reverse ? exp2_of(at[e], none) : exp2_of(all, at[e]));
+    for (int e = 0; e < 4; ++e) addw[e] = a.k_scale * exp2_of(all, at[e]);
     put(out.addw, addw);
     if (lane == 0) out.total = exp2_of(all, none);
   } else {
-  const Sum edge[5] = {none, shfl_sum(run, 7), shfl_sum(run, 15), shfl_sum(run, 23), all};
-  Sum m = reverse ? edge[1] : edge[0];
+  // at the edge of each block of rows towards what it sees
+  Sum edge[4] = {shfl_sum(run, reverse ? 8 : 0), shfl_sum(run, reverse ? 16 : 7), shfl_sum(run, reverse ? 24 : 15), shfl_sum(run, 23)};
+  edge[reverse ? 3 : 0] = none;
+  Sum m = edge[0];
 #pragma unroll
   for (int i = 1; i < 4; ++i)
-    if (block == i) m = reverse ? edge[i + 1] : edge[i];
+    if (block == i) m = edge[i];
   float hi[4], lo[4], row[4], addw[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     hi[e] = at[e].hi;
     lo[e] = at[e].lo;
-    row[e] = reverse ? exp2_of(m, at[e]) : exp2_of(at[e], m);
-    addw[e] = a.k_scale * (reverse ? exp2_of(at[e], none) : exp2_of(all, at[e]));
+    row[e] = exp2_of(at[e], m);
+    addw[e] = a.k_scale * exp2_of(all, at[e]);
   }
   put(out.hi, hi);
   put(out.lo, lo);
@@ -258,13 +267,12 @@ __device__ __forceinline__ Sum chunk_gates(float4 g, typename Layout<ONLY_STATE>
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     if (reverse ? block < r : block > r) continue;   // tokens the rows of block r do not see
-    const Sum e = reverse ? edge[r + 1] : edge[r];
     float c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = a.out_scale * (reverse ? exp2_of(at[i], e) : exp2_of(e, at[i]));
+    for (int i = 0; i < 4; ++i) c[i] = a.out_scale * exp2_of(edge[r], at[i]);
     put(out.col[r], c);
   }
-  if ((lane & 7) == 0) out.enter[block] = a.state_scale * (reverse ? exp2_of(all, m) : exp2_of(m, none));
+  if ((lane & 7) == 0) out.enter[block] = a.state_scale * exp2_of(m, none);
   // beyond 2^40 within a block its own scores take each difference by itself
   bool far = false;
 #pragma unroll
@@ -361,13 +369,12 @@ __device__ __noinline__ void redo_span(const ScanSet& p, const Scan& a, uint8_t*
 }
 
 // 16 scores of a row in its own block times their decays, each difference by itself.
-__device__ __noinline__ void steep_block(uint32_t (&x)[16], const ChunkGates& w, float out_scale, int row, int j0,
-                                         bool reverse) {
+__device__ __noinline__ void steep_block(uint32_t (&x)[16], const ChunkGates& w, float out_scale, int row, int j0) {
   const float hi = w.hi[row], lo = w.lo[row];
 #pragma unroll 4
   for (int j = 0; j < 16; ++j) {
     const float d = (hi - w.hi[j0 + j]) + (lo - w.lo[j0 + j]);
-    x[j] = __float_as_uint(__uint_as_float(x[j]) * (out_scale * exp2_fast(reverse ? -d : d)));
+    x[j] = __float_as_uint(__uint_as_float(x[j]) * (out_scale * exp2_fast(d)));
   }
 }
 
@@ -633,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t z[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) z[i] = x[i];
-            steep_block(z, w, a.out_scale, row, j0, reverse);
+            steep_block(z, w, a.out_scale, row, j0);
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = z[i];
           } else {
