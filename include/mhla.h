@@ -488,8 +488,8 @@ mhla_status_t mhla_gated_forward(const mhla_tensor_t* q, const mhla_tensor_t* k,
  * with the gate's decay in it: its rounding is a share of exp(g_t) <|S_{t-1}|,
  * |dS_t|> however strongly gates forget, and a closed gate has 0.
  * An infinity or NaN in k or v of a token reaches dg of later tokens alone, one
- * in q or dout dg of its own and of earlier ones.
- * A NaN gate of token t * reaches dq of t and later tokens, dk and dv of earlier ones, and all of dg.
+ * in q or dout dg of its own and of earlier ones.  A NaN gate of token t reaches
+ * dq of t and later tokens, dk and dv of earlier ones, and all of dg.
  *   q, k, v, g, scale, state_in   those of the forward.
  *   dout, dq, dk, dv  device tensors shaped like q;  dg  shaped like g.
  *   dstate_in    device float32 [B][H][d][d], or NULL when not wanted.

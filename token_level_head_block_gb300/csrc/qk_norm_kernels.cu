@@ -214,6 +214,24 @@ __device__ __forceinline__ Eight turned(const Eight& x, const Angles& t) {
   return y;
 }
 
+// The first `turns` pairs turned, the others left as they are: 0 times what is not finite would reach the partner.
+template <bool INTER>
+__device__ __forceinline__ Eight turned(const Eight& x, const Angles& t, int turns) {
+  if (turns == 0) return x;
+  Eight y = turned(x, t);
+  if (INTER && turns < 4) {   // channels apart, pairs are turned by fours
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float a[2], b[2], c[2], d[2];
+      apart(x.a[i], a[0], a[1]); apart(x.b[i], b[0], b[1]);
+      apart(y.a[i], c[0], c[1]); apart(y.b[i], d[0], d[1]);
+      y.a[i] = two(2 * i < turns ? c[0] : a[0], 2 * i + 1 < turns ? c[1] : a[1]);
+      y.b[i] = two(2 * i < turns ? d[0] : b[0], 2 * i + 1 < turns ? d[1] : b[1]);
+    }
+  }
+  return y;
+}
+
 template <int G>
 __device__ __forceinline__ float group_total(float x) {
 #pragma unroll
@@ -246,6 +264,7 @@ struct Ring {
   static constexpr int kRows = kPlanes * heads_a_group<T>(BWD) * 256 * static_cast<int>(sizeof(R));
   static constexpr int kStage = kRows + 2 * 256 * 16;
   static constexpr int kBytes = kStages * kStage;
+  static_assert(kStages == 2, "one round is copied ahead");
 };
 
 template <typename R>
@@ -306,6 +325,7 @@ __global__ void __launch_bounds__(256, BWD ? 2 : 3) qk_norm_lanes(const QkNormPr
   extern __shared__ __align__(16) char shared[];
   int64_t token_ahead = token, n_ahead = n;
   int64_t position = 0;   // of the next round to be copied
+  int turns_ahead = 0;    // pairs of the lane that the last round copied turns
   auto look_up = [&]() {
     position = n_ahead;
     if (p.positions && token_ahead < walk.tokens) position = p.positions[token_ahead];
@@ -327,11 +347,12 @@ __global__ void __launch_bounds__(256, BWD ? 2 : 3) qk_norm_lanes(const QkNormPr
         }
       }
     }
-    if (p.table && there > 0) {
+    turns_ahead = p.table && position >= 0 ? max(0, min(4, p.pairs - 4 * unit)) : 0;
+    if (turns_ahead > 0 && there > 0) {
       float4* const turns = reinterpret_cast<float4*>(stage + Held::kRows) + threadIdx.x;
-      const bool turned = position >= 0 && position < p.rows;
+      const bool turned = position < p.rows;
       const float* from = p.table + 2 * (position * p.pairs + 4 * unit);
-      if (turned && walk.wide_rows && 4 * unit < p.pairs) {
+      if (turned && walk.wide_rows) {
         copy_ahead(turns, from);
         copy_ahead(turns + 256, from + 4);
       } else {
@@ -365,14 +386,14 @@ __global__ void __launch_bounds__(256, BWD ? 2 : 3) qk_norm_lanes(const QkNormPr
   for (int i = 0; i < Held::kStages - 1; ++i) copy_round(i);
   // every lane of a warp takes the same number of rounds: the sums need all of them
   for (int64_t round = 0; round < walk.rounds; ++round) {
-    const int count = token < walk.tokens ? heads : 0;
+    const int count = token < walk.tokens ? heads : 0, turns = turns_ahead;
     copy_round(round + Held::kStages - 1);
     const char* const stage = shared + static_cast<int>(round % Held::kStages) * Held::kStage;
     asm volatile("cp.async.wait_group %0;" ::"n"(Held::kStages - 1) : "memory");
     float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, s[4] = {};
-    if (p.table && live) {   // the lanes behind the head's channels have copied none
-      const float4* const turns = reinterpret_cast<const float4*>(stage + Held::kRows) + threadIdx.x;
-      const float4 f = turns[0], g = turns[256];
+    if (turns > 0) {   // else none were copied
+      const float4* const from = reinterpret_cast<const float4*>(stage + Held::kRows) + threadIdx.x;
+      const float4 f = from[0], g = from[256];
       c[0] = f.x; s[0] = f.y; c[1] = f.z; s[1] = f.w;
       c[2] = g.x; s[2] = g.y; c[3] = g.z; s[3] = g.w;
       if (BWD)
@@ -390,9 +411,9 @@ __global__ void __launch_bounds__(256, BWD ? 2 : 3) qk_norm_lanes(const QkNormPr
       const float r = rsqrtf(group_total<G>(dot(u, u)) * inv_d + p.eps);
       u = times(u, r);
       if (!BWD) {
-        y = turned(times(u, w), angles);
+        y = turned<INTER>(times(u, w), angles, turns);
       } else {
-        y = turned(expand<INTER>(row[2 * 256], row[3 * 256]), angles);
+        y = turned<INTER>(expand<INTER>(row[2 * 256], row[3 * 256]), angles, turns);
         if (real) acc = times_plus(y, u, acc);   // eps 0: a row that is not there is 0 / 0
         y = times(y, w);
         const float m = group_total<G>(dot(y, u)) * inv_d;
