@@ -537,28 +537,36 @@ def _same_device(like, *tensors):
             raise ValueError(f"a tensor is on {x.device}, not on {like.device}")
 
 
-def _launch(what, fn, args, x, stream, workspace=None, need=None):
-    """fn(*args, [workspace, bytes,] stream) with x's device current.  need() tells the workspace's
-    bytes (None: the call takes none); they come from torch's allocator on that stream when the caller
-    brings no workspace."""
+def _on(stream, x):
+    """The given stream (torch's, or a handle) as torch's current one on x's device: a call made under it allocates
+    its outputs and its workspace there, so that their memory is not handed on before that stream is through with it."""
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=x.device)
+    if stream.device != x.device:
+        raise ValueError(f"the stream is on {stream.device}, not on {x.device}")
+    return torch.cuda.stream(stream)
+
+
+def _launch(what, fn, args, x, workspace=None, need=None):
+    """fn(*args, [workspace, bytes,] stream) on torch's current stream with x's device current.  need() tells the
+    workspace's bytes (None: the call takes none); they come from torch's allocator when the caller brings
+    no workspace."""
     import torch
     index = x.get_device()
     if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(index):
-            return _launch(what, fn, args, x, stream, workspace, need)
-    current = torch._C._cuda_getCurrentRawStream(index)
-    if stream is None:
-        s = current
-    else:
-        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+            return _launch(what, fn, args, x, workspace, need)
+    s = torch._C._cuda_getCurrentRawStream(index)
     if need is None:
         st = fn(*args, s)
     elif workspace is not None:
         st = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
     else:
         n = need()
-        if n == 0 or s != current:
-            st = fn(*args, None, 0, s)   # another stream: the library's stream-ordered allocation
+        if n == 0:
+            st = fn(*args, None, 0, s)
         else:
             scratch = torch.empty(n, dtype=torch.uint8, device=x.device)
             st = fn(*args, scratch.data_ptr(), n, s)
@@ -586,8 +594,13 @@ def gated_forward(q, k, v, g, scale=1.0, state=None, out=None, state_out=None, w
     q, k, v: CUDA tensors [B, N, H, d]; g: log decays [B, N, H] of the same
     dtype; state: float32 [B, H, d, d] before the first token (None: zero).
     Returns (out, state_out); state_out (allocated when not given) may be state.
+    ``stream`` (default: torch's current one) runs the call and owns what it allocates; the
+    caller orders it behind the writers of its inputs and in front of the readers of its outputs.
     """
     import torch
+    if stream is not None:
+        with _on(stream, q):
+            return gated_forward(q, k, v, g, scale, state, out, state_out, workspace)
     B, N, H, d = q.shape
     if out is None:
         out = torch.empty_like(q)
@@ -598,7 +611,7 @@ def gated_forward(q, k, v, g, scale=1.0, state=None, out=None, state_out=None, w
             _float_array("state_out", state_out, (B, H, d, d), q))
     _same_device(q, k, v, g, out)
     L = lib()
-    _launch("mhla_gated_forward", L.mhla_gated_forward, args, q, stream, workspace,
+    _launch("mhla_gated_forward", L.mhla_gated_forward, args, q, workspace,
             lambda: _size(L.mhla_gated_workspace_size, "mhla_gated_workspace_size", dq))
     return out, state_out
 
@@ -606,8 +619,11 @@ def gated_forward(q, k, v, g, scale=1.0, state=None, out=None, state_out=None, w
 def gated_backward(q, k, v, g, dout, scale=1.0, state=None, dstate_out=None, dq=None, dk=None, dv=None, dg=None,
                    dstate=None, workspace=None, stream=None):
     """Gradients (dq, dk, dv, dg, dstate) of ``gated_forward`` given dout and,
-    when the last state is used, dstate_out (float32 [B, H, d, d])."""
+    when the last state is used, dstate_out (float32 [B, H, d, d]).  ``stream`` as for ``gated_forward``."""
     import torch
+    if stream is not None:
+        with _on(stream, q):
+            return gated_backward(q, k, v, g, dout, scale, state, dstate_out, dq, dk, dv, dg, dstate, workspace)
     B, N, H, d = q.shape
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(q) if dk is None else dk
@@ -622,21 +638,24 @@ def gated_backward(q, k, v, g, dout, scale=1.0, state=None, dstate_out=None, dq=
             _float_array("dstate", dstate, square, q))
     _same_device(q, k, v, g, dout, dq, dk, dv, dg)
     L = lib()
-    _launch("mhla_gated_backward", L.mhla_gated_backward, args, q, stream, workspace,
+    _launch("mhla_gated_backward", L.mhla_gated_backward, args, q, workspace,
             lambda: _size(L.mhla_gated_backward_workspace_size, "mhla_gated_backward_workspace_size", desc))
     return dq, dk, dv, dg, dstate
 
 
 def gated_step(q, k, v, g, state, scale=1.0, out=None, stream=None):
     """One token for every sequence: tensors [B, 1, H, d], g [B, 1, H]; ``state``
-    (float32 [B, H, d, d]) is updated in place.  Returns ``out``."""
+    (float32 [B, H, d, d]) is updated in place.  Returns ``out``.  ``stream`` as for ``gated_forward``."""
+    if stream is not None:
+        with _on(stream, q):
+            return gated_step(q, k, v, g, state, scale, out)
     B, _, H, d = q.shape
     if out is None:
         import torch
         out = torch.empty_like(q)
     args = (_heads(q), _heads(k), _heads(v), _gates(g), scale, _float_array("state", state, (B, H, d, d), q), _heads(out))
     _same_device(q, k, v, g, out)
-    _launch("mhla_gated_step", lib().mhla_gated_step, args, q, stream)
+    _launch("mhla_gated_step", lib().mhla_gated_step, args, q)
     return out
 
 
@@ -681,8 +700,12 @@ def qk_norm(q, k, q_weight=None, k_weight=None, eps=1e-6, table=None, positions=
             k_out=None, stream=None):
     """Root-mean-square norm of every head of q [B, N, H, d] and k [B, N, Hk, d] (float32
     weights [d]) and its rotation by ``table`` ([rows, pairs, 2], see ``init_rotation``) at
-    ``positions`` (int32 [B, N]; None: 0 .. N-1).  Returns (q_out, k_out), which may be q and k."""
+    ``positions`` (int32 [B, N]; None: 0 .. N-1).  Returns (q_out, k_out), which may be q and k.
+    ``stream`` as for ``gated_forward``."""
     import torch
+    if stream is not None:
+        with _on(stream, q):
+            return qk_norm(q, k, q_weight, k_weight, eps, table, positions, layout, q_out, k_out)
     if q_out is None:
         q_out = torch.empty_like(q)
     if k_out is None:
@@ -691,7 +714,7 @@ def qk_norm(q, k, q_weight=None, k_weight=None, eps=1e-6, table=None, positions=
     args = (_heads(q), _heads(k), _float_array("q_weight", q_weight, (d,), q), _float_array("k_weight", k_weight, (d,), q),
             eps, _rotation(q, table, positions, layout), _heads(q_out), _heads(k_out))
     _same_device(q, k, q_out, k_out)
-    _launch("mhla_qk_norm", lib().mhla_qk_norm, args, q, stream)
+    _launch("mhla_qk_norm", lib().mhla_qk_norm, args, q)
     return q_out, k_out
 
 
@@ -702,8 +725,12 @@ def qk_norm_backward_workspace_size(q):
 def qk_norm_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, eps=1e-6, table=None, positions=None,
                      layout="half", dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None, stream=None):
     """Gradients (dq, dk, dq_weight, dk_weight) of ``qk_norm`` for its inputs q, k;
-    dq may be dq_out and dk dk_out."""
+    dq may be dq_out and dk dk_out.  ``stream`` as for ``gated_forward``."""
     import torch
+    if stream is not None:
+        with _on(stream, q):
+            return qk_norm_backward(q, k, dq_out, dk_out, q_weight, k_weight, eps, table, positions, layout, dq, dk,
+                                    dq_weight, dk_weight, workspace)
     d = q.shape[3]
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
@@ -717,7 +744,7 @@ def qk_norm_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, eps=1e-
             _float_array("dq_weight", dq_weight, (d,), q), _float_array("dk_weight", dk_weight, (d,), q))
     _same_device(q, k, dq_out, dk_out, dq, dk)
     L = lib()
-    _launch("mhla_qk_norm_backward", L.mhla_qk_norm_backward, args, q, stream, workspace,
+    _launch("mhla_qk_norm_backward", L.mhla_qk_norm_backward, args, q, workspace,
             lambda: _size(L.mhla_qk_norm_backward_workspace_size, "mhla_qk_norm_backward_workspace_size", desc))
     return dq, dk, dq_weight, dk_weight
 
