@@ -685,6 +685,8 @@ def _rotation(x, table, positions, layout):
         return None
     if table.dim() != 3 or table.shape[2] != 2:
         raise ValueError("the rotation table is [rows, pairs, 2]")
+    if table.shape[0] == 0 and table.shape[1] > 0:   # whose address would read as no table
+        raise ValueError("the rotation table has no rows")
     ptr = _float_array("table", table, table.shape, x)
     pos = None
     if positions is not None:
