@@ -537,7 +537,7 @@ typedef struct mhla_rotation {
     const int32_t* positions;  /* device [B][N]: row of each token, or NULL: row n for token n (rows >= N).
                                   A negative position leaves the token unrotated (padding); one past the
                                   table gives NaN in the rotated channels. */
-    int64_t rows;
+    int64_t rows;              /* 2^40 at most */
     int32_t pairs;             /* 2 * pairs <= d; the channels behind them are not rotated */
     int32_t layout;            /* mhla_rotation_layout_t */
 } mhla_rotation_t;

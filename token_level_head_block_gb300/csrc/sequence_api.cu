@@ -224,6 +224,7 @@ int qk_norm_problem(const mhla_tensor_t* q, const mhla_tensor_t* k, const float*
   if (rot && rot->table) {
     if (rot->layout != MHLA_ROTATION_HALF && rot->layout != MHLA_ROTATION_INTERLEAVED) return MHLA_ERR_INVALID_ARG;
     if (rot->pairs < 0 || rot->rows < 0) return MHLA_ERR_INVALID_ARG;
+    if (rot->rows > (int64_t{1} << 40)) return MHLA_ERR_UNSUPPORTED;   // their bytes fit 64 bits below
     if (reinterpret_cast<uintptr_t>(rot->table) % 8 != 0 || reinterpret_cast<uintptr_t>(rot->positions) % 4 != 0)
       return MHLA_ERR_INVALID_ARG;
     if (2 * static_cast<int64_t>(rot->pairs) > q->d) return MHLA_ERR_SHAPE;
