@@ -1009,144 +1009,168 @@ __global__ void __launch_bounds__(32 * kWarpsOf<DK>, DK <= (sizeof(T) == 2 ? 64 
 // gates forget, a closed gate has 0, and what is not finite stays on its side.  (A running sum of q . dq - k . dk,
 // which needs no pairs, has the error of all it has summed, however small dg itself.)
 //
-// A warp takes a block of 16 rows i and walks the blocks of columns j up to its own: both dots on mma.sync,
-// then sums over M's rows (for the gates of the rows' block) and over its columns (for the gates of the columns'
-// block); a gate in between takes whole blocks, and the pairs of one block are summed for each of its gates.
+// A warp takes a group of rows i, a quarter of the chunk, and walks the tiles of 16 columns j in front of it: both dots
+// on mma.sync, then sums over M's rows (for the gates of the rows' group) and over its columns (for the gates of the
+// columns' group); a gate in between takes whole groups, and the pairs of one group are summed for each of its gates.
 struct GateGrad {
   Operand q, k, v, dout, dg;
   const float *qdots, *kdots;    // r and c [slices][B][H][N]
-  const float *enter, *leave;    // S and D of every chunk, as the scans hold them
+  const float *enter, *leave;    // S and D of every chunk, as the scans hold them; whole: [B][H][d][d] or null for zero
   const float* sums;             // b of every chunk, high parts and low parts
   int64_t N, H, BH;
-  uint32_t chunks;               // of 64 SUB tokens
+  uint32_t chunks;               // of 64 TILES tokens
   int32_t d, slices;
   float scale;
+  bool whole;                    // one chunk: the call's own states
 };
 
 // bf16 operands lie in shared memory together; float32's three terms take turns, (q, k) and then (do, v).
-template <typename T, int DK, int SUB>
+// Four warps; a warp has TILES blocks of 16 rows, one for chunks of 64 tokens and two for those of 128.
+template <typename T, int DK, int TILES>
 struct GateTile {
-  static constexpr int kIn = Terms<T>::kIn, kTokens = kChunk * SUB, kThreads = 2 * kTokens, kBlocks = kTokens / 16;
+  static constexpr int kIn = Terms<T>::kIn, kTokens = kChunk * TILES, kThreads = 128, kRows = 16 * TILES, kGroups = 4;
   static constexpr int kTurns = kIn > 1 ? 2 : 1;
   static constexpr int kPlane = kChunk * DK * 2;   // bytes of one term of 64 tokens
-  static constexpr int kOperand = SUB * kIn * kPlane;
+  static constexpr int kOperand = TILES * kIn * kPlane;
   static constexpr int kBytes = (kTurns > 1 ? 2 : 4) * kOperand;
-  static constexpr int kCtas = SUB == 2 ? (DK == 64 ? 3 : 4) : 1;   // an SM holds at least
+  // CTAs an SM holds at least: by shared memory, and by registers
+  static constexpr int kFit = 220 * 1024 / (kBytes + 8 * 1024), kMost = kTurns > 1 || DK == 128 ? 2 : DK == 64 ? 3 : 5;
+  static constexpr int kCtas = kFit < kMost ? kFit : kMost;
 };
 
-// A block of 16 rows as A operands; float32's three terms stay in shared memory.
-template <typename T, int DK, int SUB>
-struct BlockRows {
-  using L = GateTile<T, DK, SUB>;
-  uint32_t at;
-  int row, lane;
-  uint32_t held[L::kIn > 1 ? 1 : DK / 16][4];
-  __device__ __forceinline__ BlockRows(uint32_t x, int own, int lane_) : lane(lane_) {
-    at = x + (own >> 2) * L::kIn * L::kPlane;
-    row = 16 * (own & 3) + (lane & 7) + ((lane >> 3) & 1) * 8;
+// A warp's rows as A operands; float32's three terms stay in shared memory.
+template <typename T, int DK, int TILES>
+struct GroupRows {
+  using L = GateTile<T, DK, TILES>;
+  uint32_t x, y;
+  int group, lane;
+  uint32_t held[L::kIn > 1 ? 1 : TILES][L::kIn > 1 ? 1 : DK / 16][4];
+  // Byte offset of 16 rows' plane and the row in it.
+  static __device__ __forceinline__ uint32_t plane(int tile) { return (tile >> 2) * L::kIn * L::kPlane; }
+  __device__ __forceinline__ uint32_t row_of(int tile) const { return 16 * (tile & 3) + (lane & 7) + ((lane >> 3) & 1) * 8; }
+  __device__ __forceinline__ GroupRows(uint32_t x_, uint32_t y_, int group_, int lane_) : x(x_), y(y_), group(group_), lane(lane_) {
     if constexpr (L::kIn == 1)
 #pragma unroll
-      for (int ks = 0; ks < DK / 16; ++ks) ldsm(held[ks], at + unit_at<DK>(row, 2 * ks + (lane >> 4)));
+      for (int i = 0; i < TILES; ++i)
+#pragma unroll
+        for (int ks = 0; ks < DK / 16; ++ks) {
+          const int tile = TILES * group + i;
+          ldsm(held[i][ks], x + plane(tile) + unit_at<DK>(row_of(tile), 2 * ks + (lane >> 4)));
+        }
   }
-  // Their dots with rows 16 s .. of y: an mma accumulator's 16 by 16.
-  __device__ __forceinline__ void dots(float (&c)[2][4], uint32_t y, int s) const {
-    y += (s >> 2) * L::kIn * L::kPlane;
+  // Dots of tiles FROM .. TO - 1 of them with rows 16 s .. of y: mma accumulators of 16 by 16.
+  template <int FROM, int TO>
+  __device__ __forceinline__ void dots(float (&c)[TO - FROM][2][4], int s) const {
+    const uint32_t from = y + plane(s);
     const int yr = 16 * (s & 3) + (lane & 7) + (lane >> 4) * 8;
-    Accumulators<2, (L::kIn > 1)> acc;
-    if (L::kIn > 1) acc.clear();
+    Accumulators<2, (L::kIn > 1)> acc[TO - FROM];
+    if (L::kIn > 1)
+#pragma unroll
+      for (int i = 0; i < TO - FROM; ++i) acc[i].clear();
 #pragma unroll(L::kIn > 1 ? 1 : DK / 16)
     for (int ks = 0; ks < DK / 16; ++ks) {
-      uint32_t a[L::kIn][4], b[L::kIn][1][4];
+      uint32_t b[L::kIn][1][4];
 #pragma unroll
-      for (int t = 0; t < L::kIn; ++t) {
-        if constexpr (L::kIn > 1)
-          ldsm(a[t], at + t * L::kPlane + unit_at<DK>(row, 2 * ks + (lane >> 4)));
-        else
+      for (int t = 0; t < L::kIn; ++t) ldsm(b[t][0], from + t * L::kPlane + unit_at<DK>(yr, 2 * ks + ((lane >> 3) & 1)));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) a[t][e] = held[ks][e];
-        ldsm(b[t][0], y + t * L::kPlane + unit_at<DK>(yr, 2 * ks + ((lane >> 3) & 1)));
+      for (int i = 0; i < TO - FROM; ++i) {
+        uint32_t a[L::kIn][4];
+#pragma unroll
+        for (int t = 0; t < L::kIn; ++t) {
+          const int tile = TILES * group + FROM + i;
+          if constexpr (L::kIn > 1)
+            ldsm(a[t], x + plane(tile) + t * L::kPlane + unit_at<DK>(row_of(tile), 2 * ks + (lane >> 4)));
+          else
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[t][e] = held[FROM + i][ks][e];
+        }
+        mma_terms(acc[i], 0, a, b, L::kIn == 1 && ks == 0);
       }
-      mma_terms(acc, 0, a, b, L::kIn == 1 && ks == 0);
     }
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+    for (int i = 0; i < TO - FROM; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) c[f][e] = acc.get(f, e);
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[i][f][e] = acc[i].get(f, e);
   }
 };
 
-// Sum over a warp's eight lanes of one column.
-__device__ __forceinline__ float column_total(float x) {
-#pragma unroll
-  for (int s = 4; s < 32; s <<= 1) x += __shfl_xor_sync(~0u, x, s);
-  return x;
+// Sums over a warp's eight lanes of its four columns, 2 (lane % 4) and the next and those eight behind; a lane gets that
+// of column_of(lane).
+__device__ __forceinline__ float columns_total(const float (&z)[4], int lane) {   // halves change hands until a lane pair has one
+  const bool up = lane & 16, right = lane & 8;
+  const float a0 = (up ? z[2] : z[0]) + __shfl_xor_sync(~0u, up ? z[0] : z[2], 16);
+  const float a1 = (up ? z[3] : z[1]) + __shfl_xor_sync(~0u, up ? z[1] : z[3], 16);
+  const float a = (right ? a1 : a0) + __shfl_xor_sync(~0u, right ? a0 : a1, 8);
+  return a + __shfl_xor_sync(~0u, a, 4);
+}
+__device__ __forceinline__ int column_of(int lane) { return ((lane & 16) >> 1) + 2 * (lane & 3) + ((lane & 8) >> 3); }
+
+__device__ __forceinline__ float dot4(const float4& f, const float4& g, float s) {
+  return fmaf(f.x, g.x, fmaf(f.y, g.y, fmaf(f.z, g.z, fmaf(f.w, g.w, s))));
 }
 
-__host__ __device__ constexpr int front(int block) { return 8 * block * (block - 1); }
-
-// This thread's share of <S, D>.  tcgen05 states are DK x DK floats in one order; the warp-level scan's lie as its
-// threads hold them, some of their tiles behind d and not written.
-template <int DK, int SUB, int THREADS>
-__device__ __forceinline__ float states_dot(const float* enter, const float* leave, int d) {
-  const float4 *x = reinterpret_cast<const float4*>(enter), *y = reinterpret_cast<const float4*>(leave);
+// This thread's share of <S, D>: DK x DK floats in one order behind the tcgen05 scans (two tiles a warp); behind the
+// warp-level scan as its threads hold them, some of their tiles behind d and not written.
+template <int DK, int TILES>
+__device__ __forceinline__ float states_dot(const float4* enter, const float4* leave, int d) {
   float s = 0.0f;
-  auto add = [&](int i) {
-    const float4 f = x[i], g = y[i];
-    s = fmaf(f.x, g.x, fmaf(f.y, g.y, fmaf(f.z, g.z, fmaf(f.w, g.w, s))));
-  };
-  if constexpr (SUB == 2) {
+  if constexpr (TILES == 2) {
 #pragma unroll
-    for (int i = 0; i < DK * DK / 4 / THREADS; ++i) add(threadIdx.x + THREADS * i);
+    for (int i = 0; i < DK * DK / 4 / 128; ++i) s = dot4(enter[threadIdx.x + 128 * i], leave[threadIdx.x + 128 * i], s);
   } else {
     using L = Tile<float, DK, false>;
     constexpr int kSlices = DK / L::DV, kTiles = L::kRowTiles * L::kColTiles;
 #pragma unroll 1
     for (int slice = 0; slice < kSlices; ++slice)
 #pragma unroll
-      for (int t = 0; t < L::kThreads / THREADS; ++t) {
-        const int thread = threadIdx.x + THREADS * t, warp = thread >> 5;
-        const StatePlace<DK> at(warp, 0);
+      for (int t = 0; t < L::kThreads / 128; ++t) {
+        const int thread = threadIdx.x + 128 * t;
+        const StatePlace<DK> at(thread >> 5, 0);
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
-          if (at.row + i / L::kColTiles * 16 < d && slice * L::DV + at.col + i % L::kColTiles * 8 < d)
-            add((slice * kTiles + i) * L::kThreads + thread);
+          if (at.row + i / L::kColTiles * 16 < d && slice * L::DV + at.col + i % L::kColTiles * 8 < d) {
+            const int j = (slice * kTiles + i) * L::kThreads + thread;
+            s = dot4(enter[j], leave[j], s);
+          }
       }
   }
   return s;
 }
 
-template <typename T, int DK, bool ASYNC, int SUB>
-__global__ void __launch_bounds__(2 * kChunk * SUB, GateTile<T, DK, SUB>::kCtas) gated_gate_grad(const __grid_constant__ GateGrad p) {
-  using L = GateTile<T, DK, SUB>;
-  constexpr int kTokens = L::kTokens, kBlocks = L::kBlocks, kWarps = L::kThreads / 32;
-  static_assert(kWarps == kBlocks && kBlocks <= 8, "a warp to a block of rows");
-  __shared__ float rows[kTokens];                          // M's rows in front of their block
-  __shared__ float within[kTokens];                        // of the pairs of the gate's own block
-  // columns in front of each block of rows, block i's from front(i) on
-  __shared__ __align__(16) float column[front(kBlocks)];   // M's, summed over the rows
-  __shared__ __align__(16) float factor[front(kBlocks)];   // scale e^{m - b_j}, m at the edge of the block of rows
-  __shared__ float r_block[kBlocks], c_block[kBlocks];     // r and c over a block
-  __shared__ float part[kWarps];                           // of <S, D>
+template <typename T, int DK, bool ASYNC, int TILES>
+__global__ void __launch_bounds__(128, GateTile<T, DK, TILES>::kCtas) gated_gate_grad(const __grid_constant__ GateGrad p) {
+  using L = GateTile<T, DK, TILES>;
+  constexpr int kTokens = L::kTokens, kGroups = L::kGroups, kRows = L::kRows;
+  __shared__ float rows[kTokens];                       // M's rows in front of their group
+  __shared__ float within[kTokens];                     // what a gate has of the pairs of its own group
+  __shared__ float inner[TILES == 2 ? kTokens : 1];     // of a group's second tile with its first: columns, then rows
+  __shared__ float column[kGroups][kTokens - kRows];    // M's columns in front of each group of rows
+  __shared__ __align__(16) float factor[kGroups][kTokens - kRows];   // scale e^{m - b_j}, m at the group's edge
+  __shared__ float r_block[kGroups], c_block[kGroups];  // r and c over a group
+  __shared__ float part[kGroups];                       // of <S, D>
+  __shared__ __align__(16) float hi[kTokens], lo[kTokens];   // b_i
+  extern __shared__ __align__(16) char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, me = threadIdx.x, d = p.d;
-  const uint32_t row_of_batch = blockIdx.x / p.chunks, H = static_cast<uint32_t>(p.H);   // 32-bit divisions
-  const uint32_t chunk = blockIdx.x - row_of_batch * p.chunks;
-  const int64_t bh = row_of_batch, b = row_of_batch / H, h = row_of_batch % H, t0 = static_cast<int64_t>(chunk) * kTokens;
+  const int group = me / kRows, unit = me % kRows;      // of the thread's token
+  // Heads first: their rows of a token lie side by side in memory.  32-bit divisions.
+  const uint32_t H = static_cast<uint32_t>(p.H), of_batch = blockIdx.x / H, batch = of_batch / p.chunks;
+  const uint32_t chunk = of_batch - batch * p.chunks;
+  const int64_t b = batch, h = blockIdx.x - of_batch * H, bh = b * p.H + h, t0 = static_cast<int64_t>(chunk) * kTokens;
+  const int64_t slot = bh * p.chunks + chunk;   // of the chunk's states and sums
   const int count = static_cast<int>(min(p.N - t0, static_cast<int64_t>(kTokens)));
-  const int block = me / 16, unit = me & 15;   // of the thread's token
-  const float *hi = p.sums + 2 * kTokens * static_cast<int64_t>(blockIdx.x), *lo = hi + kTokens;
   auto sum_at = [&](int i) { return Sum{hi[i], lo[i]}; };
   const Sum none = {0.0f, 0.0f};
 
-  extern __shared__ __align__(16) char smem[];
-  if constexpr (ASYNC)
-    if (d < DK) {   // columns behind d stay zero
-      for (int i = me; i < L::kBytes / 16; i += L::kThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
-      __syncthreads();
-    }
   const uint32_t first = ptx::smem_u32(smem), second = first + (L::kTurns > 1 ? 0 : 2 * L::kOperand);
   if constexpr (ASYNC) {
-    constexpr int kUnits = DK / 8, kRows = L::kThreads / kUnits;   // 16-byte units of a row, rows a pass
-    static_assert(kRows % 8 == 0, "a pass keeps the units' places");
+    if (d < DK) {   // columns behind d stay zero
+      for (int i = me; i < L::kBytes / 16; i += 128) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+      __syncthreads();
+    }
+    constexpr int kUnits = DK / 8, kPass = 128 / kUnits;   // 16-byte units of a row, rows a pass
+    static_assert(kPass % 8 == 0, "a pass keeps the units' places");
     const int r = me / kUnits, u = me % kUnits;
     auto fetch = [&](const Operand& o, uint32_t to) {
       const T* base = static_cast<const T*>(o.data) + (b * o.sb + h * o.sh + t0 * o.sn);
@@ -1154,12 +1178,12 @@ __global__ void __launch_bounds__(2 * kChunk * SUB, GateTile<T, DK, SUB>::kCtas)
       to += unit_at<DK>(r, u);
       if (count == kTokens) {
 #pragma unroll
-        for (int i = 0; i < kTokens / kRows; ++i, from += kRows * o.sn) cp_async_16(to + i * kRows * DK * 2, from, 16);
+        for (int i = 0; i < kTokens / kPass; ++i, from += kPass * o.sn) cp_async_16(to + i * kPass * DK * 2, from, 16);
       } else {
 #pragma unroll
-        for (int i = 0; i < kTokens / kRows; ++i, from += kRows * o.sn) {
-          const bool in = r + i * kRows < count;
-          cp_async_16(to + i * kRows * DK * 2, in ? from : base, in ? 16 : 0);
+        for (int i = 0; i < kTokens / kPass; ++i, from += kPass * o.sn) {
+          const bool in = r + i * kPass < count;
+          cp_async_16(to + i * kPass * DK * 2, in ? from : base, in ? 16 : 0);
         }
       }
     };
@@ -1172,182 +1196,251 @@ __global__ void __launch_bounds__(2 * kChunk * SUB, GateTile<T, DK, SUB>::kCtas)
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   auto load = [&](const Operand& x, const Operand& y, char* to) {   // rows that lie otherwise
-    const RowLoader<T, DK, L::kThreads, false> of_x(x, b, h, 0, d), of_y(y, b, h, 0, d);
-    load_plain(static_cast<int64_t>(chunk), p.N, PlainPart<T, DK, L::kThreads>{of_x, to},
-               PlainPart<T, DK, L::kThreads>{of_y, to + L::kOperand});
+    const RowLoader<T, DK, 128, false> of_x(x, b, h, 0, d), of_y(y, b, h, 0, d);
+    load_plain(static_cast<int64_t>(chunk), p.N, PlainPart<T, DK, 128>{of_x, to}, PlainPart<T, DK, 128>{of_y, to + L::kOperand});
   };
   if constexpr (!ASYNC) {
-    static_assert(SUB == 1, "a part of 64 tokens");
+    static_assert(TILES == 1, "a part of 64 tokens");
     load(p.q, p.k, smem);
     if (L::kTurns == 1) load(p.dout, p.v, smem + 2 * L::kOperand);
   }
 
-  // the scans' dots, a token a thread
-  float r = 0.0f, c = 0.0f;
-  if (me < count) {
-    const float *x = p.qdots + bh * p.N + t0 + me, *y = p.kdots + bh * p.N + t0 + me;
-#pragma unroll 4
-    for (int k = 0; k < p.slices; ++k, x += p.BH * p.N, y += p.BH * p.N) {
-      r += *x;
-      c += *y;
-    }
+  // Everything else is asked for before any of it is waited for: the scans' dots and the gates' sums, a token a thread
+  constexpr int kSlices = 4;   // at most
+  float q_dot[kSlices] = {}, k_dot[kSlices] = {}, b_hi = 0.0f, b_lo = 0.0f;
+  if (me < kTokens) {
+    b_hi = p.sums[2 * kTokens * slot + me];
+    b_lo = p.sums[2 * kTokens * slot + kTokens + me];
   }
-  // neighbouring CTAs give the rows that see more to different warps
-  const int own = (warp + static_cast<int>(blockIdx.x)) & (kBlocks - 1), row = 16 * own + (lane >> 2);
-  {
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * DK * DK;
-    float s = states_dot<DK, SUB, L::kThreads>(p.enter + at, p.leave + at, d);
+  if (me < count) {
+    const int64_t at = bh * p.N + t0 + me, step = p.BH * p.N;
+#pragma unroll
+    for (int k = 0; k < kSlices; ++k)
+      if (k < p.slices) {
+        q_dot[k] = p.qdots[at + k * step];
+        k_dot[k] = p.kdots[at + k * step];
+      }
+  }
+  {   // <S, D>
+    float s = 0.0f;
+    if (p.whole) {
+      const float *x = p.enter + bh * d * d, *y = p.leave + bh * d * d;
+      if (p.enter && p.leave)
+        for (int i = me; i < d * d; i += 128) s = fmaf(x[i], y[i], s);
+    } else {
+      const int64_t at = slot * (DK * DK / 4);
+      s = states_dot<DK, TILES>(reinterpret_cast<const float4*>(p.enter) + at, reinterpret_cast<const float4*>(p.leave) + at, d);
+    }
 #pragma unroll
     for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(~0u, s, k);
     if (lane == 0) part[warp] = s;
   }
-  // Pairs of two blocks: e^{b_i - m} e^{m - b_j}, m at the edge of the rows' block, each factor out of one of the sums
-  const Sum m = own ? sum_at(16 * own - 1) : none, b0 = sum_at(row), b1 = sum_at(row + 8);
-  for (int j = lane; j < 16 * own; j += 32) factor[front(own) + j] = p.scale * exp2_of(m, sum_at(j));
-  const float f0 = exp2_of(b0, m), f1 = exp2_of(b1, m);
-  __syncwarp();
-  Two sum0 = two(0.0f, 0.0f), sum1 = sum0;   // of rows row, row + 8
-  auto pairs = [&](const float (&x)[2][4], const float (&y)[2][4], int s) {
-    float z[4];
-    const float* col = factor + front(own) + 16 * s;
+
+  if (me < kTokens) {
+    hi[me] = b_hi;
+    lo[me] = b_lo;
+  }
+  const float r_own = (q_dot[0] + q_dot[1]) + (q_dot[2] + q_dot[3]), c_own = (k_dot[0] + k_dot[1]) + (k_dot[2] + k_dot[3]);
+  if (me < kTokens) {
+    float u = (lane & 1 ? c_own : r_own) + __shfl_xor_sync(~0u, lane & 1 ? r_own : c_own, 1);   // r in even lanes, c in odd ones
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const Two u0 = mul(two(x[f][0], x[f][1]), two(y[f][0], y[f][1])), u1 = mul(two(x[f][2], x[f][3]), two(y[f][2], y[f][3]));
-      const float2 w = *reinterpret_cast<const float2*>(col + 8 * f + 2 * (lane & 3));
-      sum0 = fma(u0, two(w.x, w.y), sum0);
-      sum1 = fma(u1, two(w.x, w.y), sum1);
-      apart(fma(u1, two(f1, f1), mul(u0, two(f0, f0))), z[2 * f], z[2 * f + 1]);
-    }
-    // each column over the warp's eight lanes of it: halves of the columns change hands until a lane pair has one
-    const bool up = lane & 16, right = lane & 8;
-    const float a0 = (up ? z[2] : z[0]) + __shfl_xor_sync(~0u, up ? z[0] : z[2], 16);
-    const float a1 = (up ? z[3] : z[1]) + __shfl_xor_sync(~0u, up ? z[1] : z[3], 16);
-    float a = (right ? a1 : a0) + __shfl_xor_sync(~0u, right ? a0 : a1, 8);
-    a += __shfl_xor_sync(~0u, a, 4);
-    const int j = (up ? 8 : 0) + 2 * (lane & 3) + (right ? 1 : 0);
-    if (!(lane & 4)) column[front(own) + 16 * s + j] = col[j] * a;
-  };
-  using Block = BlockRows<T, DK, SUB>;
+    for (int k = 2; k < kRows; k <<= 1) u += __shfl_xor_sync(~0u, u, k);
+    if (unit < 2) (unit ? c_block : r_block)[group] = u;
+  }
   if constexpr (ASYNC) asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
-  float x[2][4], y[2][4];
-  if constexpr (L::kTurns > 1) {
-    float kept[kBlocks - 1][2][4];   // q . k
-    {
-      const Block q(first, own, lane);
+
+  // neighbouring CTAs give the rows that see more to different warps
+  const int own = (warp + static_cast<int>(blockIdx.x)) & (kGroups - 1), row0 = kRows * own;
+  // Pairs of two groups: e^{b_i - m} e^{m - b_j}, m at the edge of the rows' group, each factor out of one of the sums
+  const Sum m = own ? sum_at(row0 - 1) : none;
+  Sum at_row[TILES][2];   // of rows lane / 4 and eight behind it
+  float f[TILES][2];
 #pragma unroll
-      for (int s = 0; s < kBlocks - 1; ++s)
-        if (s < own) q.dots(kept[s], first + L::kOperand, s);
-      q.dots(x, first + L::kOperand, own);
+  for (int i = 0; i < TILES; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      at_row[i][e] = sum_at(row0 + 16 * i + 8 * e + (lane >> 2));
+      f[i][e] = exp2_of(at_row[i][e], m);
+    }
+  for (int j = lane; j < row0; j += 32) factor[own][j] = p.scale * exp2_of(m, sum_at(j));
+  __syncwarp();
+  Two of_row[TILES][2];   // sums over what lies in front of the group
+#pragma unroll
+  for (int i = 0; i < TILES; ++i) of_row[i][0] = of_row[i][1] = two(0.0f, 0.0f);
+  auto pairs = [&](const float (&x)[TILES][2][4], const float (&y)[TILES][2][4], int s) {
+    float z[4];
+    const float* col = factor[own] + 16 * s;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const float2 w = *reinterpret_cast<const float2*>(col + 8 * g + 2 * (lane & 3));
+      Two sum = two(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < TILES; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const Two u = mul(two(x[i][g][2 * e], x[i][g][2 * e + 1]), two(y[i][g][2 * e], y[i][g][2 * e + 1]));
+          of_row[i][e] = fma(u, two(w.x, w.y), of_row[i][e]);
+          sum = i + e ? fma(u, two(f[i][e], f[i][e]), sum) : mul(u, two(f[i][e], f[i][e]));
+        }
+      apart(sum, z[2 * g], z[2 * g + 1]);
+    }
+    const float a = columns_total(z, lane);
+    const int j = 16 * s + column_of(lane);
+    if (!(lane & 4)) column[own][j] = factor[own][j] * a;
+  };
+  // Weights within a group, from the sums themselves: tile i's rows, columns 8 g + 2 (lane % 4) and the next of tile s.
+  auto weigh = [&](float (&x)[2][4], const float (&y)[2][4], int i, int s, bool cut) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int j = 8 * g + 2 * (lane & 3);
+      const float2 hj = *reinterpret_cast<const float2*>(hi + row0 + 16 * s + j), lj = *reinterpret_cast<const float2*>(lo + row0 + 16 * s + j);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float w = p.scale * exp2_of(at_row[i][e >> 1], e & 1 ? Sum{hj.y, lj.y} : Sum{hj.x, lj.x});
+        x[g][e] = !cut || j + (e & 1) < (lane >> 2) + (e >> 1) * 8 ? x[g][e] * y[g][e] * w : 0.0f;
+      }
+    }
+  };
+  // Pairs of one tile: gate t has the sum over rows i >= t of what row i holds in front of column t.
+  auto triangle = [&](const float (&x)[2][4], int i) {
+    float z[4] = {};
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float before[2], total = 0.0f;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float u = x[g][2 * half] + x[g][2 * half + 1];
+#pragma unroll
+        for (int k = 1; k < 4; k <<= 1) {
+          const float o = __shfl_up_sync(~0u, u, k, 4);
+          if ((lane & 3) >= k) u += o;
+        }
+        const float o = __shfl_up_sync(~0u, u, 1, 4);
+        before[g] = (lane & 3) ? o : 0.0f;
+        if (g == 0) total = __shfl_sync(~0u, u, 3, 4);
+      }
+      before[1] += total;
+      const int r = (lane >> 2) + 8 * half, t = 2 * (lane & 3);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (r >= 8 * g + t) z[2 * g] += before[g];
+        if (r >= 8 * g + t + 1) z[2 * g + 1] += before[g] + x[g][2 * half];
+      }
+    }
+    const float a = columns_total(z, lane);
+    if (!(lane & 4)) within[row0 + 16 * i + column_of(lane)] = a;
+  };
+  // And of a group's second tile with its first: sums over columns and over rows.
+  auto square = [&](const float (&x)[2][4]) {
+    const float z[4] = {x[0][0] + x[0][2], x[0][1] + x[0][3], x[1][0] + x[1][2], x[1][1] + x[1][3]};
+    const float a = columns_total(z, lane);
+    if (!(lane & 4)) inner[row0 + column_of(lane)] = a;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float u = (x[0][2 * e] + x[0][2 * e + 1]) + (x[1][2 * e] + x[1][2 * e + 1]);
+      u += __shfl_xor_sync(~0u, u, 1);
+      u += __shfl_xor_sync(~0u, u, 2);
+      if ((lane & 3) == 0) inner[row0 + 16 + 8 * e + (lane >> 2)] = u;
+    }
+  };
+
+  using Rows = GroupRows<T, DK, TILES>;
+  float x[TILES][2][4], y[TILES][2][4];
+  if constexpr (L::kTurns > 1) {
+    float kept[kGroups - 1][1][2][4];   // q . k
+    {
+      const Rows q(first, first + L::kOperand, own, lane);
+#pragma unroll
+      for (int s = 0; s < kGroups - 1; ++s)
+        if (s < own) q.template dots<0, 1>(kept[s], s);
+      q.template dots<0, 1>(x, own);
     }
     __syncthreads();
     load(p.dout, p.v, smem);
     __syncthreads();
-    const Block z(second, own, lane);
+    const Rows z(second, second + L::kOperand, own, lane);
 #pragma unroll
-    for (int s = 0; s < kBlocks - 1; ++s)
+    for (int s = 0; s < kGroups - 1; ++s)
       if (s < own) {
-        z.dots(y, second + L::kOperand, s);
+        z.template dots<0, 1>(y, s);
         pairs(kept[s], y, s);
       }
-    z.dots(y, second + L::kOperand, own);
+    z.template dots<0, 1>(y, own);
+    weigh(x[0], y[0], 0, 0, true);
+    triangle(x[0], 0);
   } else {
-    const Block q(first, own, lane), z(second, own, lane);
+    const Rows q(first, first + L::kOperand, own, lane), z(second, second + L::kOperand, own, lane);
 #pragma unroll 1
-    for (int s = 0; s <= own; ++s) {
-      q.dots(x, first + L::kOperand, s);
-      z.dots(y, second + L::kOperand, s);
-      if (s < own) pairs(x, y, s);
+    for (int s = 0; s < TILES * own; ++s) {
+      q.template dots<0, TILES>(x, s);
+      z.template dots<0, TILES>(y, s);
+      pairs(x, y, s);
     }
-  }
-  // Pairs of the own block: gate t has the sum over rows i >= t of what row i holds in front of column t.
-  float z[2][2] = {};
-#pragma unroll
-  for (int f = 0; f < 2; ++f) {
-    const int j = 16 * own + 8 * f + 2 * (lane & 3);
-    const float2 hj = *reinterpret_cast<const float2*>(hi + j), lj = *reinterpret_cast<const float2*>(lo + j);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float w = exp2_of(e < 2 ? b0 : b1, e & 1 ? Sum{hj.y, lj.y} : Sum{hj.x, lj.x});
-      x[f][e] = j + (e & 1) < row + (e >> 1) * 8 ? x[f][e] * y[f][e] * w : 0.0f;
-    }
-  }
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    float before[2], total[2];
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      float u = x[f][2 * half] + x[f][2 * half + 1];
-#pragma unroll
-      for (int k = 1; k < 4; k <<= 1) {
-        const float o = __shfl_up_sync(~0u, u, k, 4);
-        if ((lane & 3) >= k) u += o;
-      }
-      const float o = __shfl_up_sync(~0u, u, 1, 4);
-      before[f] = (lane & 3) ? o : 0.0f;
-      total[f] = __shfl_sync(~0u, u, 3, 4);
-    }
-    before[1] += total[0];
-    const int i = (lane >> 2) + 8 * half, t = 2 * (lane & 3);
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      if (i >= 8 * f + t) z[f][0] += before[f];
-      if (i >= 8 * f + t + 1) z[f][1] += before[f] + x[f][2 * half];
+    q.template dots<0, TILES>(x, TILES * own);
+    z.template dots<0, TILES>(y, TILES * own);
+    weigh(x[0], y[0], 0, 0, true);
+    triangle(x[0], 0);
+    if constexpr (TILES == 2) {
+      weigh(x[1], y[1], 1, 0, false);
+      square(x[1]);
+      float u[1][2][4], w[1][2][4];
+      q.template dots<1, 2>(u, 2 * own + 1);
+      z.template dots<1, 2>(w, 2 * own + 1);
+      weigh(u[0], w[0], 1, 1, true);
+      triangle(u[0], 1);
     }
   }
 #pragma unroll
-  for (int f = 0; f < 2; ++f)
+  for (int i = 0; i < TILES; ++i)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float u = column_total(z[f][e]);
-      if (lane < 4) within[16 * own + 8 * f + 2 * lane + e] = p.scale * u;
+      float u, w;
+      apart(of_row[i][e], u, w);
+      u += w;
+      u += __shfl_xor_sync(~0u, u, 1);
+      u += __shfl_xor_sync(~0u, u, 2);
+      if ((lane & 3) == 0) rows[row0 + 16 * i + 8 * e + (lane >> 2)] = f[i][e] * u;
     }
-#pragma unroll
-  for (int f = 0; f < 2; ++f) {
-    float u, w;
-    apart(f ? sum1 : sum0, u, w);
-    u += w;
-    u += __shfl_xor_sync(~0u, u, 1);
-    u += __shfl_xor_sync(~0u, u, 2);
-    if ((lane & 3) == 0) rows[row + 8 * f] = (f ? f1 : f0) * u;
-  }
-  if (me < kTokens) {
-    float u = (lane & 1 ? c : r) + __shfl_xor_sync(~0u, lane & 1 ? r : c, 1);   // r in even lanes, c in odd ones
-#pragma unroll
-    for (int k = 2; k < 16; k <<= 1) u += __shfl_xor_sync(~0u, u, k);
-    if (unit < 2) (unit ? c_block : r_block)[block] = u;
-  }
   __syncthreads();
   if (me >= kTokens) return;
-  // rows from the gate's on and columns in front of it within the block
-  r += rows[me];
-#pragma unroll
-  for (int i = 1; i < kBlocks; ++i)
-    if (i > block) c += column[front(i) + me];
-  // what every gate of the block has (both states, whole blocks on both sides), a share a lane: a gate meets the
-  // shares from its lane on in r's sum, those in front in c's
+  // what every gate of the group has (both states, whole groups on both sides), a share a lane: a gate meets the shares
+  // from its lane on in r's sum, those in front in c's
   float share = 0.0f;
-  if (unit < kBlocks) {
+  if (unit < kGroups) {
     share = exp2_of(sum_at(kTokens - 1), none) * part[unit];
-    if (unit > block) share += r_block[unit];
-    if (unit < block) share += c_block[unit];
+    if (unit > group) share += r_block[unit];
+    if (unit < group) share += c_block[unit];
   }
-  if (unit < (kBlocks - 1 - block) * block) {   // 12 pairs of blocks at most
-    const int i = unit * ((256 + block - 1) / block) >> 8, j = unit - i * block;   // unit / block, unit % block
-    const float4* from = reinterpret_cast<const float4*>(column + front(block + 1 + i) + 16 * j);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) share += (from[e].x + from[e].y) + (from[e].z + from[e].w);
-  }
-  r += share;
-  c += share;
+  for (int i = 2; i < kGroups; ++i)
 #pragma unroll
-  for (int k = 1; k < 16; k <<= 1) {
-    const float u = __shfl_down_sync(~0u, r, k, 16), w = __shfl_up_sync(~0u, c, k, 16);
-    if (unit + k < 16) r += u;
+    for (int j = 0; j < i - 1; ++j)
+      if (i > group && group > j) share += column[i][kRows * j + unit];
+  // rows from the gate's on and columns in front of it within the group
+  float r = r_own + rows[me] + share, c = c_own + share;
+#pragma unroll
+  for (int i = 1; i < kGroups; ++i)
+    if (i > group) c += column[i][me];
+#pragma unroll
+  for (int k = 1; k < kRows; k <<= 1) {
+    const float u = __shfl_down_sync(~0u, r, k, kRows), w = __shfl_up_sync(~0u, c, k, kRows);
+    if (unit + k < kRows) r += u;
     if (unit >= k) c += w;
   }
-  const float in_front = __shfl_up_sync(~0u, c, 1, 16);
-  const float dg = within[me] + r + (unit ? in_front : 0.0f);
+  const float in_front = __shfl_up_sync(~0u, c, 1, kRows);
+  float dg = within[me] + r + (unit ? in_front : 0.0f);
+  if constexpr (TILES == 2) {   // the first tile's gates: columns in front; the second's: rows from the gate's on
+    const bool back = unit >= 16;
+    float u = inner[me];
+#pragma unroll
+    for (int k = 1; k < 16; k <<= 1) {
+      const float o = __shfl_sync(~0u, u, back ? lane + k : lane - k);
+      if (back ? lane + k < 32 : lane >= k) u += o;
+    }
+    const float o = __shfl_up_sync(~0u, u, 1);
+    dg += back ? u : lane ? o : 0.0f;
+  }
   if (me < count) from_f(static_cast<T*>(p.dg.data) + b * p.dg.sb + h * p.dg.sh + (t0 + me) * p.dg.sn, dg);
 }
 
@@ -1440,14 +1533,14 @@ int run_join(const ScanSet& set, int scans, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
 
-template <typename T, int DK, bool ASYNC, int SUB>
+template <typename T, int DK, bool ASYNC, int TILES>
 int launch_gate_grad(const GateGrad& g, cudaStream_t s) {
-  using L = GateTile<T, DK, SUB>;
-  if (cudaFuncSetAttribute(gated_gate_grad<T, DK, ASYNC, SUB>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
+  using L = GateTile<T, DK, TILES>;
+  if (cudaFuncSetAttribute(gated_gate_grad<T, DK, ASYNC, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) !=
       cudaSuccess)
     return MHLA_ERR_CUDA;
   KernelTimer timer("gated_gate_grad", s);
-  gated_gate_grad<T, DK, ASYNC, SUB><<<static_cast<unsigned>(g.BH * g.chunks), L::kThreads, L::kBytes, s>>>(g);
+  gated_gate_grad<T, DK, ASYNC, TILES><<<static_cast<unsigned>(g.BH * g.chunks), L::kThreads, L::kBytes, s>>>(g);
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
 
@@ -1508,7 +1601,9 @@ int64_t dot_slices(const GatedProblem& p) { return std::max(scan_dot_slices(p), 
 size_t dot_bytes(const GatedProblem& p) { return align_up(static_cast<size_t>(dot_slices(p) * p.B * p.H * p.N) * 4); }
 
 // The state that enters each chunk (of 64 tokens, or 128 of the tcgen05 scan), and the gates' sums in each.
+// A sequence of one chunk has the call's own states at both ends.
 size_t entry_bytes(const GatedProblem& p, int chunk) {
+  if (p.N <= chunk) return 0;
   const int64_t side = padded(p.d);
   return align_up(static_cast<size_t>(p.B * p.H * ((p.N + chunk - 1) / chunk) * side * side) * 4);
 }
@@ -1630,8 +1725,9 @@ int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* w
   dq.dots = take(dot_bytes(p));
   dk.dots = take(dot_bytes(p));
   const int chunk = r.tc ? kTcChunk : kChunk;
-  dq.entries = take(entry_bytes(p, chunk));
-  dk.entries = take(entry_bytes(p, chunk));
+  const bool whole = c.chunks == 1;
+  if (!whole) dq.entries = take(entry_bytes(p, chunk));
+  if (!whole) dk.entries = take(entry_bytes(p, chunk));
   dq.sums = take(sum_bytes(p, chunk));
 
   set = scan_set(p, c);
@@ -1657,7 +1753,9 @@ int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* w
   gg.dg = b.dg;
   gg.sums = dq.sums;
   gg.qdots = dq.dots; gg.kdots = dk.dots;
-  gg.enter = dq.entries; gg.leave = dk.entries;
+  gg.whole = whole;
+  gg.enter = whole ? b.state_in : dq.entries;
+  gg.leave = whole ? b.dstate_out : dk.entries;
   gg.N = p.N; gg.H = p.H; gg.BH = p.B * p.H; gg.chunks = static_cast<uint32_t>(c.chunks);
   gg.d = p.d;
   gg.slices = r.tc ? static_cast<int32_t>(dot_slices(p)) : scan_dot_slices(p);

@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kAdder) {
     // ------------------------------------------------------------ loads; what the state gains: MMAs
-    const uint64_t policy = ONLY_STATE ? policy_evict_last() : policy_evict_first();
+    const uint64_t policy = ONLY_STATE || GRAD ? policy_evict_last() : policy_evict_first();
     int issued = 0;
     auto load = [&](int n) {
       const int s = n % kStages;
