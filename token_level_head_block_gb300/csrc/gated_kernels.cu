@@ -1024,17 +1024,17 @@ struct GateGrad {
   bool whole;                    // one chunk: the call's own states
 };
 
-// bf16 operands lie in shared memory together; float32's three terms take turns, (q, k) and then (do, v).
-// Four warps; a warp has TILES blocks of 16 rows, one for chunks of 64 tokens and two for those of 128.
+// A warp has TILES blocks of 16 rows, one for chunks of 64 tokens and two for those of 128.  Four warps; float32, with
+// six products a term, takes four for q . k and four for do . v, which hand theirs over through shared memory.
 template <typename T, int DK, int TILES>
 struct GateTile {
-  static constexpr int kIn = Terms<T>::kIn, kTokens = kChunk * TILES, kThreads = 128, kRows = 16 * TILES, kGroups = 4;
-  static constexpr int kTurns = kIn > 1 ? 2 : 1;
+  static constexpr int kIn = Terms<T>::kIn, kTokens = kChunk * TILES, kRows = 16 * TILES, kGroups = 4;
+  static constexpr int kRoles = kIn > 1 ? 2 : 1, kThreads = 128 * kRoles;
   static constexpr int kPlane = kChunk * DK * 2;   // bytes of one term of 64 tokens
   static constexpr int kOperand = TILES * kIn * kPlane;
-  static constexpr int kBytes = (kTurns > 1 ? 2 : 4) * kOperand;
+  static constexpr int kBytes = 4 * kOperand + (kRoles > 1 ? kGroups * (kGroups + 1) / 2 * 1024 : 0);
   // CTAs an SM holds at least: by shared memory, and by registers
-  static constexpr int kFit = 220 * 1024 / (kBytes + 8 * 1024), kMost = kTurns > 1 || DK == 128 ? 2 : DK == 64 ? 3 : 5;
+  static constexpr int kFit = 227 * 1024 / (kBytes + 4608 * TILES), kMost = DK == 128 ? 2 : DK == 64 ? 4 - kRoles : kRoles > 1 ? 3 : 5;
   static constexpr int kCtas = kFit < kMost ? kFit : kMost;
 };
 
@@ -1113,20 +1113,19 @@ __device__ __forceinline__ float dot4(const float4& f, const float4& g, float s)
 
 // This thread's share of <S, D>: DK x DK floats in one order behind the tcgen05 scans (two tiles a warp); behind the
 // warp-level scan as its threads hold them, some of their tiles behind d and not written.
-template <int DK, int TILES>
+template <int DK, int TILES, int THREADS>
 __device__ __forceinline__ float states_dot(const float4* enter, const float4* leave, int d) {
   float s = 0.0f;
   if constexpr (TILES == 2) {
 #pragma unroll
-    for (int i = 0; i < DK * DK / 4 / 128; ++i) s = dot4(enter[threadIdx.x + 128 * i], leave[threadIdx.x + 128 * i], s);
+    for (int i = 0; i < DK * DK / 4 / THREADS; ++i) s = dot4(enter[threadIdx.x + THREADS * i], leave[threadIdx.x + THREADS * i], s);
   } else {
     using L = Tile<float, DK, false>;
     constexpr int kSlices = DK / L::DV, kTiles = L::kRowTiles * L::kColTiles;
 #pragma unroll 1
     for (int slice = 0; slice < kSlices; ++slice)
 #pragma unroll
-      for (int t = 0; t < L::kThreads / 128; ++t) {
-        const int thread = threadIdx.x + 128 * t;
+      for (int thread = threadIdx.x; thread < L::kThreads; thread += THREADS) {
         const StatePlace<DK> at(thread >> 5, 0);
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
@@ -1140,16 +1139,17 @@ __device__ __forceinline__ float states_dot(const float4* enter, const float4* l
 }
 
 template <typename T, int DK, bool ASYNC, int TILES>
-__global__ void __launch_bounds__(128, GateTile<T, DK, TILES>::kCtas) gated_gate_grad(const __grid_constant__ GateGrad p) {
+__global__ void __launch_bounds__(GateTile<T, DK, TILES>::kThreads, GateTile<T, DK, TILES>::kCtas)
+    gated_gate_grad(const __grid_constant__ GateGrad p) {
   using L = GateTile<T, DK, TILES>;
-  constexpr int kTokens = L::kTokens, kGroups = L::kGroups, kRows = L::kRows;
+  constexpr int kTokens = L::kTokens, kGroups = L::kGroups, kRows = L::kRows, kThreads = L::kThreads;
   __shared__ float rows[kTokens];                       // M's rows in front of their group
   __shared__ float within[kTokens];                     // what a gate has of the pairs of its own group
   __shared__ float inner[TILES == 2 ? kTokens : 1];     // of a group's second tile with its first: columns, then rows
   __shared__ float column[kGroups][kTokens - kRows];    // M's columns in front of each group of rows
   __shared__ __align__(16) float factor[kGroups][kTokens - kRows];   // scale e^{m - b_j}, m at the group's edge
   __shared__ float r_block[kGroups], c_block[kGroups];  // r and c over a group
-  __shared__ float part[kGroups];                       // of <S, D>
+  __shared__ float part[kThreads / 32];                 // of <S, D>
   __shared__ __align__(16) float hi[kTokens], lo[kTokens];   // b_i
   extern __shared__ __align__(16) char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, me = threadIdx.x, d = p.d;
@@ -1163,13 +1163,13 @@ __global__ void __launch_bounds__(128, GateTile<T, DK, TILES>::kCtas) gated_gate
   auto sum_at = [&](int i) { return Sum{hi[i], lo[i]}; };
   const Sum none = {0.0f, 0.0f};
 
-  const uint32_t first = ptx::smem_u32(smem), second = first + (L::kTurns > 1 ? 0 : 2 * L::kOperand);
+  const uint32_t first = ptx::smem_u32(smem), second = first + 2 * L::kOperand;
   if constexpr (ASYNC) {
     if (d < DK) {   // columns behind d stay zero
-      for (int i = me; i < L::kBytes / 16; i += 128) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int i = me; i < L::kBytes / 16; i += kThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
       __syncthreads();
     }
-    constexpr int kUnits = DK / 8, kPass = 128 / kUnits;   // 16-byte units of a row, rows a pass
+    constexpr int kUnits = DK / 8, kPass = kThreads / kUnits;   // 16-byte units of a row, rows a pass
     static_assert(kPass % 8 == 0, "a pass keeps the units' places");
     const int r = me / kUnits, u = me % kUnits;
     auto fetch = [&](const Operand& o, uint32_t to) {
@@ -1196,15 +1196,10 @@ __global__ void __launch_bounds__(128, GateTile<T, DK, TILES>::kCtas) gated_gate
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   auto load = [&](const Operand& x, const Operand& y, char* to) {   // rows that lie otherwise
-    const RowLoader<T, DK, 128, false> of_x(x, b, h, 0, d), of_y(y, b, h, 0, d);
-    load_plain(static_cast<int64_t>(chunk), p.N, PlainPart<T, DK, 128>{of_x, to}, PlainPart<T, DK, 128>{of_y, to + L::kOperand});
+    const RowLoader<T, DK, kThreads, false> of_x(x, b, h, 0, d), of_y(y, b, h, 0, d);
+    load_plain(static_cast<int64_t>(chunk), p.N, PlainPart<T, DK, kThreads>{of_x, to},
+               PlainPart<T, DK, kThreads>{of_y, to + L::kOperand});
   };
-  if constexpr (!ASYNC) {
-    static_assert(TILES == 1, "a part of 64 tokens");
-    load(p.q, p.k, smem);
-    if (L::kTurns == 1) load(p.dout, p.v, smem + 2 * L::kOperand);
-  }
-
   // Everything else is asked for before any of it is waited for: the scans' dots and the gates' sums, a token a thread
   constexpr int kSlices = 4;   // at most
   float q_dot[kSlices] = {}, k_dot[kSlices] = {}, b_hi = 0.0f, b_lo = 0.0f;
@@ -1226,16 +1221,21 @@ __global__ void __launch_bounds__(128, GateTile<T, DK, TILES>::kCtas) gated_gate
     if (p.whole) {
       const float *x = p.enter + bh * d * d, *y = p.leave + bh * d * d;
       if (p.enter && p.leave)
-        for (int i = me; i < d * d; i += 128) s = fmaf(x[i], y[i], s);
+        for (int i = me; i < d * d; i += kThreads) s = fmaf(x[i], y[i], s);
     } else {
       const int64_t at = slot * (DK * DK / 4);
-      s = states_dot<DK, TILES>(reinterpret_cast<const float4*>(p.enter) + at, reinterpret_cast<const float4*>(p.leave) + at, d);
+      s = states_dot<DK, TILES, kThreads>(reinterpret_cast<const float4*>(p.enter) + at, reinterpret_cast<const float4*>(p.leave) + at, d);
     }
 #pragma unroll
     for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(~0u, s, k);
     if (lane == 0) part[warp] = s;
   }
 
+  if constexpr (!ASYNC) {
+    static_assert(TILES == 1, "a part of 64 tokens");
+    load(p.q, p.k, smem);
+    load(p.dout, p.v, smem + 2 * L::kOperand);
+  }
   if (me < kTokens) {
     hi[me] = b_hi;
     lo[me] = b_lo;
@@ -1251,7 +1251,7 @@ __global__ void __launch_bounds__(128, GateTile<T, DK, TILES>::kCtas) gated_gate
   __syncthreads();
 
   // neighbouring CTAs give the rows that see more to different warps
-  const int own = (warp + static_cast<int>(blockIdx.x)) & (kGroups - 1), row0 = kRows * own;
+  const int own = (warp + static_cast<int>(blockIdx.x)) & (kGroups - 1), row0 = kRows * own, role = warp / kGroups;
   // Pairs of two groups: e^{b_i - m} e^{m - b_j}, m at the edge of the rows' group, each factor out of one of the sums
   const Sum m = own ? sum_at(row0 - 1) : none;
   Sum at_row[TILES][2];   // of rows lane / 4 and eight behind it
@@ -1263,7 +1263,7 @@ __global__ void __launch_bounds__(128, GateTile<T, DK, TILES>::kCtas) gated_gate
       at_row[i][e] = sum_at(row0 + 16 * i + 8 * e + (lane >> 2));
       f[i][e] = exp2_of(at_row[i][e], m);
     }
-  for (int j = lane; j < row0; j += 32) factor[own][j] = p.scale * exp2_of(m, sum_at(j));
+  for (int j = lane; role == 0 && j < row0; j += 32) factor[own][j] = p.scale * exp2_of(m, sum_at(j));
   __syncwarp();
   Two of_row[TILES][2];   // sums over what lies in front of the group
 #pragma unroll
@@ -1347,28 +1347,43 @@ __global__ void __launch_bounds__(128, GateTile<T, DK, TILES>::kCtas) gated_gate
 
   using Rows = GroupRows<T, DK, TILES>;
   float x[TILES][2][4], y[TILES][2][4];
-  if constexpr (L::kTurns > 1) {
+  if constexpr (L::kRoles > 1) {
     float kept[kGroups - 1][1][2][4];   // q . k
-    {
+    float4* const handed = reinterpret_cast<float4*>(smem + 4 * L::kOperand) + 32 * own * (own + 1) + lane;   // do . v
+    if (role == 0) {
       const Rows q(first, first + L::kOperand, own, lane);
 #pragma unroll
       for (int s = 0; s < kGroups - 1; ++s)
         if (s < own) q.template dots<0, 1>(kept[s], s);
       q.template dots<0, 1>(x, own);
+    } else {
+      const Rows z(second, second + L::kOperand, own, lane);
+#pragma unroll 1
+      for (int s = 0; s <= own; ++s) {
+        z.template dots<0, 1>(y, s);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) handed[64 * s + 32 * g] = make_float4(y[0][g][0], y[0][g][1], y[0][g][2], y[0][g][3]);
+      }
     }
     __syncthreads();
-    load(p.dout, p.v, smem);
-    __syncthreads();
-    const Rows z(second, second + L::kOperand, own, lane);
+    auto take = [&](int s) {
 #pragma unroll
-    for (int s = 0; s < kGroups - 1; ++s)
-      if (s < own) {
-        z.template dots<0, 1>(y, s);
-        pairs(kept[s], y, s);
+      for (int g = 0; g < 2; ++g) {
+        const float4 u = handed[64 * s + 32 * g];
+        y[0][g][0] = u.x; y[0][g][1] = u.y; y[0][g][2] = u.z; y[0][g][3] = u.w;
       }
-    z.template dots<0, 1>(y, own);
-    weigh(x[0], y[0], 0, 0, true);
-    triangle(x[0], 0);
+    };
+    if (role == 0) {
+#pragma unroll
+      for (int s = 0; s < kGroups - 1; ++s)
+        if (s < own) {
+          take(s);
+          pairs(kept[s], y, s);
+        }
+      take(own);
+      weigh(x[0], y[0], 0, 0, true);
+      triangle(x[0], 0);
+    }
   } else {
     const Rows q(first, first + L::kOperand, own, lane), z(second, second + L::kOperand, own, lane);
 #pragma unroll 1
@@ -1391,6 +1406,7 @@ __global__ void __launch_bounds__(128, GateTile<T, DK, TILES>::kCtas) gated_gate
       triangle(u[0], 1);
     }
   }
+  if (role == 0)
 #pragma unroll
   for (int i = 0; i < TILES; ++i)
 #pragma unroll
@@ -1408,7 +1424,7 @@ __global__ void __launch_bounds__(128, GateTile<T, DK, TILES>::kCtas) gated_gate
   // from its lane on in r's sum, those in front in c's
   float share = 0.0f;
   if (unit < kGroups) {
-    share = exp2_of(sum_at(kTokens - 1), none) * part[unit];
+    share = exp2_of(sum_at(kTokens - 1), none) * (L::kRoles > 1 ? part[unit] + part[kGroups + unit] : part[unit]);
     if (unit > group) share += r_block[unit];
     if (unit < group) share += c_block[unit];
   }
