@@ -255,7 +255,9 @@ def kernel_work(wl, name):
         # (a span's state: read k, v; joining: the states of every 512 tokens or so, in and out)
         "gated_span_state": ("hbm", 2 * io), "gated_tc_span_state": ("hbm", 2 * io), "gated_tc_scan": ("hbm", 4 * io),
         "gated_join": ("hbm", BH * max(1, wl.N // 512) * d * d * 8),
-        "gated_step": ("hbm", BH * d * d * 8), "gated_scan": ("hbm", 4 * io), "gated_gate_grad": ("hbm", BH * wl.N * (2 * 4 + wl.elem_bytes)),
+        "gated_step": ("hbm", BH * d * d * 8), "gated_scan": ("hbm", 4 * io),
+        # (the gates' gradient: q, k, v and dout again, two states of every 128 tokens)
+        "gated_gate_grad": ("hbm", 4 * io + BH * max(1, wl.N // 128) * d * d * 8),
         # norm and rotation: q and k in and out; with both output gradients in
         "qk_norm": ("hbm", 4 * io), "qk_norm_backward": ("hbm", 6 * io),
         "qk_norm_weight_grad": ("hbm", 2 * d * 4),

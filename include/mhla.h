@@ -460,8 +460,8 @@ mhla_status_t mhla_module_forward(const void* x, void* y, int64_t B, int64_t N, 
  * the tensor cores as sums of bf16 terms (two where the result is rounded to
  * bf16, three where it is float32).  Which kernel runs is the library's choice
  * by type, sizes, alignment and strides: tcgen05 over chunks of 128 tokens for
- * bf16 with d <= 64 and d % 8 == 0, 16-byte aligned rows and enough tokens, warp
- * level products over chunks of 64 otherwise.  Few heads are spread over the
+ * bf16 with d <= 64 and d % 8 == 0, 16-byte aligned rows, no stride of 0 and enough
+ * tokens, warp level products over chunks of 64 otherwise.  Few heads are spread over the
  * machine by cutting the sequence into spans, so results depend on B, H and N in
  * their last bits; the same call gives the same bits.
  * An infinity or NaN in v reaches the tokens from its own on, no earlier one.

@@ -24,9 +24,10 @@
 // measured on float32 [3, 5181, 4, 64], the tensor pipe is active 25% of the scan's time and a scheduler issues in
 // one cycle of four.
 // Times, all launches of a call:
-//   bf16  [8, 2048, 16, 128]  forward  282 us      [4, 4096, 16, 80]  gradients  964 us
-//   f32   [8, 2048, 16, 128]  forward  816 us      [8, 6871, 4, 64]   gradients  826 us
-//   f32   [3, 5181, 4, 64]    forward   86 us      [8, 4096, 16, 32]  forward    243 us
+//   bf16  [8, 2048, 16, 128]  forward  277 us      [4, 4096, 16, 80]  gradients 1105 us
+//   f32   [8, 2048, 16, 128]  forward  816 us      [8, 6871, 4, 64]   gradients  937 us
+//   f32   [3, 5181, 4, 64]    forward   86 us      [8, 4096, 16, 32]  forward    245 us
+// (gated_gate_grad has 93 and 112 us of the two gradients, and the scans write 210 and 113 MB of states for it.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -1012,6 +1013,12 @@ __global__ void __launch_bounds__(32 * kWarpsOf<DK>, DK <= (sizeof(T) == 2 ? 64 
 // A warp takes a group of rows i, a quarter of the chunk, and walks the tiles of 16 columns j in front of it: both dots
 // on mma.sync, then sums over M's rows (for the gates of the rows' group) and over its columns (for the gates of the
 // columns' group); a gate in between takes whole groups, and the pairs of one group are summed for each of its gates.
+//
+// q, k, v, dout and both states are read once more, so memory bounds it: bf16 gradients of [2, 16384, 70, 32] 183 us
+// for 0.77 GB (4.2 TB/s), of [4, 4096, 12, 64] 45 us for 0.16 GB (3.4 TB/s): there 3.4 waves of CTAs load together, at 5 to
+// 6 TB/s, and then compute together.  Not faster: chunks fetched one ahead by CTAs that stay (two stages leave an SM
+// eight warps: 65 us), rows straight from memory to registers (99), eight warps of one tile (53; 229), the next wave's
+// rows asked for in L2 (0.92 of the time here, 1.05 with 70 heads).
 struct GateGrad {
   Operand q, k, v, dout, dg;
   const float *qdots, *kdots;    // r and c [slices][B][H][N]

@@ -18,10 +18,10 @@
 // the loads (TMA, three stages), two prepare the gates.  A thread of a score or output warp
 // owns a row, so a row's factor is a register and the columns' factors are read by broadcast.
 //
-// Measured, all launches: bf16 [4, 4096, 12, 64] forward 55 us, gradients 115; [4, 65536, 6, 64] forward
-// 341 us; [2, 16384, 70, 32] gradients 922 us.  A chunk takes an SM 2.9 us where HBM would need 1.5: with
-// the splits left out the pipeline runs at HBM's rate, with them the warps issue 14,000 instructions
-// a chunk and hand over five times.  Not faster: equal shares of k's rows for two roles (1.1x), waits that sleep
+// Measured, all launches: bf16 [4, 4096, 12, 64] forward 54 us, gradients 153; [4, 65536, 6, 64] forward
+// 330 us; [2, 16384, 70, 32] gradients 1113 us.  A chunk takes an SM 2.6 us (forward) to 3.4 (gradients) where HBM would
+// need 1.5, and no rate is reached (issue slots 50 to 60%, tensor pipe 25%, HBM 30%): five hand-overs a
+// chunk, each with a split into terms behind it, are a chain.  Not faster: equal shares of k's rows for two roles (1.1x), waits that sleep
 // (1.0 to 1.05x), one waiting lane a warp (1.5x), terms left out (0.94x, and less exact).
 //
 // Every wait is bounded; one that gives up sets bit 0 of this file's error
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl.tmem;
   // The scan behind its spans' states starts on the SMs that form none; its first loads do not depend on
   // them.  [4, 4096, 12, 64] forward 57.1 us in turn, 54.9 so.  (Other launches of a call stay in turn: small grids
-  // that start early crowd the few SMs that are idle then: gradients of the same shape 115 us, 142 so.)
+  // that start early crowd the few SMs that are idle then: gradients of the same shape 1.2 times as long.)
   if (ONLY_STATE && threadIdx.x == 0) grid_dep_launch();
   if (!ONLY_STATE && warp <= kIssuer) ptx::grid_dep_wait();
 
@@ -530,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kAdder) {
     // ------------------------------------------------------------ loads; what the state gains: MMAs
+    // what another launch of the call, or another scan, reads again stays in L2 (gradients of [4, 4096, 12, 64] 158, 153 us)
     const uint64_t policy = ONLY_STATE || GRAD ? policy_evict_last() : policy_evict_first();
     int issued = 0;
     auto load = [&](int n) {
@@ -963,7 +964,7 @@ bool tc_supported(const GatedProblem& p) {
 }
 
 // One CTA an SM: as many spans as fill the SMs once, none shorter than two chunks; up to four
-// chunks stay whole (a chunk takes 2.4 us; a second span's launch and start more than two of them).
+// chunks stay whole (a chunk takes 2.6 us; a second span's launch and start more than two of them).
 Cut tc_cut(const GatedProblem& p, int scans) {
   Cut c;
   c.chunks = (p.N + kTcChunk - 1) / kTcChunk;

@@ -127,9 +127,9 @@ __global__ void __launch_bounds__(256) qk_norm_rows(const QkNormProblem p, float
 // and the rotation's come by asynchronous copies a round ahead, every lane's into shared memory of
 // its own: no barrier, no registers held while they are on their way.  Arithmetic works on pairs of
 // channels (mul.f32x2, fma.f32x2).  Every input byte is read once and every output byte written once,
-// so HBM bounds it; measured, bf16 [4, 65536, 6 + 6, 64]: forward 140 us (5.9 TB/s), gradients 204 us
+// so HBM bounds it; measured, bf16 [4, 65536, 6 + 6, 64]: forward 140 us (5.9 TB/s), gradients 207 us
 // (6.0 TB/s), where one channel an instruction took 238 and loads without copies ahead 275; float32
-// gradients [4, 16384, 8 + 2, 128] 155 us (6.6 TB/s).
+// gradients [4, 16384, 8 + 2, 128] 158 us (6.4 TB/s).
 
 // Four channels as they lie in memory.
 template <typename T>
