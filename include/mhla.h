@@ -496,7 +496,8 @@ mhla_status_t mhla_gated_forward(const mhla_tensor_t* q, const mhla_tensor_t* k,
  * The written tensors share no element with one another or with an input (views
  * interleaved in a token's row are fine).  The states are recomputed from k, v
  * and g.  workspace, stream, statuses and empty calls as for the forward; the
- * workspace holds, for every 64 tokens of a head, two d x d states. */
+ * workspace holds, for every 64 tokens of a head (where there are more), two
+ * states of d x d float32, d rounded up. */
 mhla_status_t mhla_gated_backward_workspace_size(const mhla_tensor_t* q, size_t* bytes);
 mhla_status_t mhla_gated_backward(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v,
                                   const mhla_tensor_t* g, const mhla_tensor_t* dout, float scale,

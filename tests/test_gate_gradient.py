@@ -208,3 +208,18 @@ def test_nothing_beside_the_gradients_is_written():
     assert got[3].data_ptr() == dg.data_ptr()
     check(x, "bf16", 0.125, dg)
     assert (buf[:, 333:] == 5).all() and (buf[:, :, :2] == 5).all() and (buf[:, :, 5:] == 5).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype,B,N,H,d", [("bf16", 2, 300, 3, 80), ("bf16", 2, 300, 3, 100), ("f32", 1, 300, 2, 72), ("f32", 2, 130, 3, 40),
+                                           ("f32", 1, 200, 2, 17), ("bf16", 6, 1100, 10, 24), ("bf16", 1, 1500, 11, 40), ("f32", 2, 64, 3, 64)])
+def test_the_workspace_is_what_was_asked_for(dtype, B, N, H, d):
+    """Stale contents in it, a guard behind it; the same bits as with the library's own."""
+    import token_level_head_block_gb300 as mhla
+    x = draw(12, B, N, H, d, dtype)
+    size = mhla.gated_backward_workspace_size(x["q"].cuda())
+    buf = torch.full((size + 4096,), 0xFF, dtype=torch.uint8, device="cuda")      # NaN as floats
+    got, plain = run(x, 0.125, workspace=buf[:size]), run(x, 0.125)
+    assert (buf[size:] == 0xFF).all()
+    assert all(torch.equal(a, b) for a, b in zip(got, plain))
+    check(x, dtype, 0.125, got[3])

@@ -410,6 +410,17 @@ __device__ __forceinline__ void load_plain(int64_t chunk, int64_t N, PlainPart<T
   (more.rows.load(more.dst, chunk, N), ...);
 }
 
+// A state as gated_scan's threads hold it: for each tile of eight columns that the state meets, 16 bytes of every thread
+// whose rows it meets.
+struct Held {
+  int threads, quads;   // a tile's, a state's
+};
+template <int DK>
+__host__ __device__ constexpr Held held_state(int d) {
+  const int threads = DK > 32 ? 32 * ((d + 15) / 16) : 128;
+  return Held{threads, threads * (DK > 32 ? (d + 7) / 8 : 2)};
+}
+
 // Each thread's part of the state: row tile m, column tile n, the four values of
 // an mma accumulator.  `row` and `col` are those of the first.
 template <int DK>
@@ -968,16 +979,14 @@ __global__ void __launch_bounds__(32 * kWarpsOf<DK>, DK <= (sizeof(T) == 2 ? 64 
         }
       }
     }
-    if (GRAD && a.entries) {   // as the threads hold it, the tiles that meet the state
-      constexpr int kTiles = L::kRowTiles * L::kColTiles;
-      float4* to = reinterpret_cast<float4*>(a.entries) + (bh * p.chunks + chunk_of(i)) * (DK * DK / 4) +
-                   slice * (kTiles * L::kThreads) + threadIdx.x;
+    if (GRAD && a.entries) {
+      static_assert(L::kRowTiles == 1, "16 rows a warp");
+      const Held held = held_state<DK>(p.d);
+      float4* to = reinterpret_cast<float4*>(a.entries) + (bh * p.chunks + chunk_of(i)) * held.quads +
+                   slice * L::kColTiles * held.threads + threadIdx.x;
 #pragma unroll
-      for (int m = 0; m < L::kRowTiles; ++m)
-#pragma unroll
-        for (int n = 0; n < L::kColTiles; ++n)
-          if (at.row - (lane >> 2) + 16 * m < p.d && c0 + at.col - 2 * (lane & 3) + 8 * n < p.d)
-            to[(m * L::kColTiles + n) * L::kThreads] = make_float4(S[m][n][0], S[m][n][1], S[m][n][2], S[m][n][3]);
+      for (int n = 0; n < L::kColTiles; ++n, to += held.threads)
+        if (DK == 32 || (at.row - (lane >> 2) < p.d && c0 + 8 * n < p.d)) *to = make_float4(S[0][n][0], S[0][n][1], S[0][n][2], S[0][n][3]);
     }
     const uint32_t k_base = ptx::smem_u32(stage) + L::kIn * L::kK;
     add_chunk<T, DK, ASYNC>(S, k_base, k_base + L::kIn * L::kK, w, warp, lane);
@@ -1118,8 +1127,7 @@ __device__ __forceinline__ float dot4(const float4& f, const float4& g, float s)
   return fmaf(f.x, g.x, fmaf(f.y, g.y, fmaf(f.z, g.z, fmaf(f.w, g.w, s))));
 }
 
-// This thread's share of <S, D>: DK x DK floats in one order behind the tcgen05 scans (two tiles a warp); behind the
-// warp-level scan as its threads hold them, some of their tiles behind d and not written.
+// This thread's share of <S, D>, both in the order in which a scan's threads hold them (tcgen05: two tiles a warp here).
 template <int DK, int TILES, int THREADS>
 __device__ __forceinline__ float states_dot(const float4* enter, const float4* leave, int d) {
   float s = 0.0f;
@@ -1127,20 +1135,9 @@ __device__ __forceinline__ float states_dot(const float4* enter, const float4* l
 #pragma unroll
     for (int i = 0; i < DK * DK / 4 / THREADS; ++i) s = dot4(enter[threadIdx.x + THREADS * i], leave[threadIdx.x + THREADS * i], s);
   } else {
-    using L = Tile<float, DK, false>;
-    constexpr int kSlices = DK / L::DV, kTiles = L::kRowTiles * L::kColTiles;
-#pragma unroll 1
-    for (int slice = 0; slice < kSlices; ++slice)
-#pragma unroll
-      for (int thread = threadIdx.x; thread < L::kThreads; thread += THREADS) {
-        const StatePlace<DK> at(thread >> 5, 0);
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i)
-          if (at.row + i / L::kColTiles * 16 < d && slice * L::DV + at.col + i % L::kColTiles * 8 < d) {
-            const int j = (slice * kTiles + i) * L::kThreads + thread;
-            s = dot4(enter[j], leave[j], s);
-          }
-      }
+    const int quads = held_state<DK>(d).quads;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < quads; i += THREADS) s = dot4(enter[i], leave[i], s);
   }
   return s;
 }
@@ -1230,7 +1227,7 @@ __global__ void __launch_bounds__(GateTile<T, DK, TILES>::kThreads, GateTile<T, 
       if (p.enter && p.leave)
         for (int i = me; i < d * d; i += kThreads) s = fmaf(x[i], y[i], s);
     } else {
-      const int64_t at = slot * (DK * DK / 4);
+      const int64_t at = slot * (TILES == 2 ? DK * DK / 4 : held_state<DK>(d).quads);
       s = states_dot<DK, TILES, kThreads>(reinterpret_cast<const float4*>(p.enter) + at, reinterpret_cast<const float4*>(p.leave) + at, d);
     }
 #pragma unroll
@@ -1625,10 +1622,11 @@ size_t dot_bytes(const GatedProblem& p) { return align_up(static_cast<size_t>(do
 
 // The state that enters each chunk (of 64 tokens, or 128 of the tcgen05 scan), and the gates' sums in each.
 // A sequence of one chunk has the call's own states at both ends.
-size_t entry_bytes(const GatedProblem& p, int chunk) {
+size_t entry_bytes(const GatedProblem& p, bool tc) {
+  const int chunk = tc ? kTcChunk : kChunk, side = padded(p.d);
   if (p.N <= chunk) return 0;
-  const int64_t side = padded(p.d);
-  return align_up(static_cast<size_t>(p.B * p.H * ((p.N + chunk - 1) / chunk) * side * side) * 4);
+  const int quads = tc ? side * side / 4 : side == 32 ? held_state<32>(p.d).quads : held_state<64>(p.d).quads;
+  return align_up(static_cast<size_t>(p.B * p.H * ((p.N + chunk - 1) / chunk)) * quads * 16);
 }
 size_t sum_bytes(const GatedProblem& p, int chunk) {
   return align_up(static_cast<size_t>(p.B * p.H * ((p.N + chunk - 1) / chunk) * chunk) * 8);
@@ -1677,7 +1675,8 @@ bool wants_tc(const GatedProblem& p, int scans) {
 size_t gated_workspace_bytes(const GatedProblem& p) { return most_span_bytes(p, 1); }
 
 size_t gated_bwd_workspace_bytes(const GatedProblem& p) {
-  return 2 * most_span_bytes(p, 3) + 2 * dot_bytes(p) + 2 * entry_bytes(p, kChunk) +
+  return 2 * most_span_bytes(p, 3) + 2 * dot_bytes(p) +
+         2 * std::max(entry_bytes(p, false), tc_supported(p) ? entry_bytes(p, true) : 0) +
          std::max(sum_bytes(p, kChunk), sum_bytes(p, kTcChunk));
 }
 
@@ -1749,8 +1748,8 @@ int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* w
   dk.dots = take(dot_bytes(p));
   const int chunk = r.tc ? kTcChunk : kChunk;
   const bool whole = c.chunks == 1;
-  if (!whole) dq.entries = take(entry_bytes(p, chunk));
-  if (!whole) dk.entries = take(entry_bytes(p, chunk));
+  if (!whole) dq.entries = take(entry_bytes(p, r.tc));
+  if (!whole) dk.entries = take(entry_bytes(p, r.tc));
   dq.sums = take(sum_bytes(p, chunk));
 
   set = scan_set(p, c);
