@@ -514,6 +514,68 @@ mhla_status_t mhla_gated_step(const mhla_tensor_t* q, const mhla_tensor_t* k, co
                               const mhla_tensor_t* g, float scale, float* state, const mhla_tensor_t* out,
                               void* stream);
 
+/* The gated delta rule, per batch b and head h: the recurrence above with every
+ * token correcting what the state already holds for its key instead of adding to it,
+ *   S'_t = exp(g_t) S_{t-1},   w_t = beta_t (v_t - S'_t^T k_t),
+ *   S_t = S'_t + k_t w_t^T,    o_t = scale * S_t^T q_t.
+ * Keys are taken as given; the state stays bounded for |k_t| <= 1 and beta_t in
+ * [0, 2] (mhla_qk_norm without weights and a factor d^-1/2 norms them so).
+ *   q, k        device tensors [B, N, Hk, d], same shape and dtype, any strides,
+ *               d <= 128.
+ *   v, out      device tensors [B, N, H, d] of the same dtype; H a multiple of
+ *               Hk: head h reads key head h / (H / Hk).
+ *   g, beta     device tensors [B, N, H, 1] of the same dtype; g as for
+ *               mhla_gated_forward.
+ *   state_in, state_out, scale, workspace, stream, statuses and empty calls as
+ *   for mhla_gated_forward.  A padding token with beta = 0 and g = 0 leaves
+ *   the state as it is.
+ * The states and every sum are float32 or wider; bf16 results are rounded once.
+ * Chunks of 64 tokens (float32: 32) on the tensor cores.  A chunk is a
+ * triangular solve and products, and enters the tensor cores as sums of bf16 terms:
+ * bf16 calls use two (2^-16) and one for the scores within a chunk, which reach
+ * bf16 outputs alone; float32 calls three (2^-24).  The same call gives the same bits.
+ * From the first token whose k, g or beta is not finite (g: but for -infinity),
+ * out and the state are NaN; one in v does this to its channel alone, one in q to
+ * its token's out.  Earlier tokens are as they would be without it.
+ * The workspace holds about 0.9 KB a token and head in bf16 with d = 64
+ * (proportional to d), twice to three times that in float32. */
+mhla_status_t mhla_delta_workspace_size(const mhla_tensor_t* q, const mhla_tensor_t* v, size_t* bytes);
+mhla_status_t mhla_delta_forward(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v,
+                                 const mhla_tensor_t* g, const mhla_tensor_t* beta, float scale,
+                                 const float* state_in, const mhla_tensor_t* out, float* state_out,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of mhla_delta_forward, given dout = dL/d(out) and dstate_out =
+ * dL/d(state_out) (NULL: zero).  With dS_t = scale q_t dout_t^T + dS'_{t+1} (dS_{N-1}:
+ * + dstate_out), dw_t = dS_t^T k_t, e_t = v_t - S'_t^T k_t:
+ *   dq_t = scale S_t dout_t,   dv_t = beta_t dw_t,   dbeta_t = dw_t . e_t,
+ *   dk_t = dS_t w_t - beta_t S'_t dw_t,
+ *   dS'_t = exp(g_t) (dS_t - beta_t k_t dw_t^T),   dg_t = <S_{t-1}, dS'_t>,   dstate_in = dS'_0.
+ *   q, k, v, g, beta, scale, state_in   those of the forward, finite (g: or -infinity);
+ *   what is not leaves the gradients of its sequence and head without a meaning.
+ *   dout, dv     device tensors shaped like v;  dq, dk  like q (summed over the
+ *                heads that share them, in float32);  dg, dbeta  like g.
+ *   dstate_in    device float32 [B][H][d][d], or NULL when not wanted.
+ * dg_t is summed from what has the gate between its two tokens, as in
+ * mhla_gated_backward.  The states are recomputed.  The written tensors share no
+ * element with one another or with an input (views interleaved in a token's row
+ * are fine).  workspace, stream, statuses and empty calls as for the forward. */
+mhla_status_t mhla_delta_backward_workspace_size(const mhla_tensor_t* q, const mhla_tensor_t* v, size_t* bytes);
+mhla_status_t mhla_delta_backward(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v,
+                                  const mhla_tensor_t* g, const mhla_tensor_t* beta, const mhla_tensor_t* dout,
+                                  float scale, const float* state_in, const float* dstate_out,
+                                  const mhla_tensor_t* dq, const mhla_tensor_t* dk, const mhla_tensor_t* dv,
+                                  const mhla_tensor_t* dg, const mhla_tensor_t* dbeta, float* dstate_in,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of the delta rule for every (b, h): tensors of N == 1
+ * (MHLA_ERR_SHAPE otherwise), state [B][H][d][d] float32 read, updated in place
+ * and used for out; float32 arithmetic, one launch, no workspace.  out and state
+ * overlap nothing else. */
+mhla_status_t mhla_delta_step(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v,
+                              const mhla_tensor_t* g, const mhla_tensor_t* beta, float scale, float* state,
+                              const mhla_tensor_t* out, void* stream);
+
 /* Which channels of a head turn together. */
 typedef enum mhla_rotation_layout {
     MHLA_ROTATION_HALF = 0,        /* pair i is channels i and i + pairs       */

@@ -29,6 +29,14 @@ from .mhla_backward import backward, phi_derivative  # noqa: F401,E402
 from .mhla_causal import blocks_are_contiguous, forward_causal, forward_causal_dense  # noqa: F401,E402
 from .mhla_causal_backward import backward_causal, backward_causal_dense  # noqa: F401,E402
 from .mhla_module import LEPE_K, LN_EPS, layer_norm, lepe, linear, module_forward  # noqa: F401,E402
+from .delta import (  # noqa: F401,E402
+    activation,
+    delta,
+    delta_backward,
+    delta_dense,
+    linear_act,
+    linear_act_backward,
+)
 from .gated import (  # noqa: F401,E402
     gated,
     gated_backward,

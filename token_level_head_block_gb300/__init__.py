@@ -22,6 +22,7 @@ __all__ = [
     "module_workspace_size",
     "profile_end", "tensor_desc", "shape3",
     "gated_forward", "gated_workspace_size", "gated_backward", "gated_backward_workspace_size", "gated_step",
+    "delta_forward", "delta_workspace_size", "delta_backward", "delta_backward_workspace_size", "delta_step",
     "init_rotation", "qk_norm", "qk_norm_backward", "qk_norm_backward_workspace_size",
     "PATHS", "TRANSFORMS", "ROTATION_LAYOUTS",
 ]
@@ -154,6 +155,11 @@ def lib():
     L.mhla_gated_forward.argtypes = [T, T, T, T, ctypes.c_float, V, T, V, V, ctypes.c_size_t, V]
     L.mhla_gated_backward.argtypes = [T, T, T, T, T, ctypes.c_float, V, V, T, T, T, T, V, V, ctypes.c_size_t, V]
     L.mhla_gated_step.argtypes = [T, T, T, T, ctypes.c_float, V, T, V]
+    L.mhla_delta_workspace_size.argtypes = [T, T, P(ctypes.c_size_t)]
+    L.mhla_delta_backward_workspace_size.argtypes = [T, T, P(ctypes.c_size_t)]
+    L.mhla_delta_forward.argtypes = [T, T, T, T, T, ctypes.c_float, V, T, V, V, ctypes.c_size_t, V]
+    L.mhla_delta_backward.argtypes = [T, T, T, T, T, T, ctypes.c_float, V, V, T, T, T, T, T, V, V, ctypes.c_size_t, V]
+    L.mhla_delta_step.argtypes = [T, T, T, T, T, ctypes.c_float, V, T, V]
     L.mhla_init_rotation.argtypes = [P(Shape3), P(ctypes.c_int32), ctypes.c_double, P(ctypes.c_float),
                                      ctypes.c_int64]
     L.mhla_qk_norm.argtypes = [T, T, V, V, ctypes.c_float, P(Rotation), T, T, V]
@@ -161,7 +167,9 @@ def lib():
     L.mhla_qk_norm_backward.argtypes = [T, T, V, V, ctypes.c_float, P(Rotation), T, T, T, T, V, V, V,
                                         ctypes.c_size_t, V]
     for name in ("mhla_gated_workspace_size", "mhla_gated_backward_workspace_size", "mhla_gated_forward",
-                 "mhla_gated_backward", "mhla_gated_step", "mhla_init_rotation", "mhla_qk_norm",
+                 "mhla_gated_backward", "mhla_gated_step", "mhla_delta_workspace_size",
+                 "mhla_delta_backward_workspace_size", "mhla_delta_forward", "mhla_delta_backward", "mhla_delta_step",
+                 "mhla_init_rotation", "mhla_qk_norm",
                  "mhla_qk_norm_backward_workspace_size", "mhla_qk_norm_backward"):
         getattr(L, name).restype = ctypes.c_int
     L.mhla_debug_stall_waits.argtypes = [ctypes.c_int32, ctypes.c_uint64]
@@ -574,9 +582,9 @@ def _launch(what, fn, args, x, workspace=None, need=None):
         raise MhlaError(st, what)
 
 
-def _size(fn, what, desc):
+def _size(fn, what, *descs):
     n = ctypes.c_size_t(0)
-    _check(fn(desc, ctypes.byref(n)), what)
+    _check(fn(*descs, ctypes.byref(n)), what)
     return n.value
 
 
@@ -656,6 +664,89 @@ def gated_step(q, k, v, g, state, scale=1.0, out=None, stream=None):
     args = (_heads(q), _heads(k), _heads(v), _gates(g), scale, _float_array("state", state, (B, H, d, d), q), _heads(out))
     _same_device(q, k, v, g, out)
     _launch("mhla_gated_step", lib().mhla_gated_step, args, q)
+    return out
+
+
+def delta_workspace_size(q, v):
+    return _size(lib().mhla_delta_workspace_size, "mhla_delta_workspace_size", _heads(q), _heads(v))
+
+
+def delta_backward_workspace_size(q, v):
+    return _size(lib().mhla_delta_backward_workspace_size, "mhla_delta_backward_workspace_size", _heads(q), _heads(v))
+
+
+def delta_forward(q, k, v, g, beta, scale=1.0, state=None, out=None, state_out=None, workspace=None, stream=None):
+    """The gated delta rule S' = exp(g_t) S_{t-1}, w = beta_t (v_t - S'^T k_t), S_t = S' + k_t w^T, o_t = scale S_t^T q_t.
+
+    q, k: CUDA tensors [B, N, Hk, d]; v: [B, N, H, d], H a multiple of Hk (head h reads key
+    head h // (H // Hk)); g, beta: log decays and strengths [B, N, H], all of one dtype; state: float32
+    [B, H, d, d] before the first token (None: zero).  Returns (out, state_out); state_out
+    (allocated when not given) may be state.  ``stream`` as for ``gated_forward``.
+    """
+    import torch
+    if stream is not None:
+        with _on(stream, q):
+            return delta_forward(q, k, v, g, beta, scale, state, out, state_out, workspace)
+    B, N, H, d = v.shape
+    if out is None:
+        out = torch.empty_like(v)
+    if state_out is None:
+        state_out = _new_float((B, H, d, d), state, v)
+    keys, values = _heads(q), _heads(v)
+    square = (B, H, d, d)
+    args = (keys, _heads(k), values, _gates(g), _gates(beta), scale, _float_array("state", state, square, v), _heads(out),
+            _float_array("state_out", state_out, square, v))
+    _same_device(v, q, k, g, beta, out)
+    L = lib()
+    _launch("mhla_delta_forward", L.mhla_delta_forward, args, v, workspace,
+            lambda: _size(L.mhla_delta_workspace_size, "mhla_delta_workspace_size", keys, values))
+    return out, state_out
+
+
+def delta_backward(q, k, v, g, beta, dout, scale=1.0, state=None, dstate_out=None, dq=None, dk=None, dv=None, dg=None,
+                   dbeta=None, dstate=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dv, dg, dbeta, dstate) of ``delta_forward`` given dout and, when the
+    last state is used, dstate_out (float32 [B, H, d, d]).  ``stream`` as for ``gated_forward``."""
+    import torch
+    if stream is not None:
+        with _on(stream, q):
+            return delta_backward(q, k, v, g, beta, dout, scale, state, dstate_out, dq, dk, dv, dg, dbeta, dstate,
+                                  workspace)
+    B, N, H, d = v.shape
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    dg = torch.empty_like(g) if dg is None else dg
+    dbeta = torch.empty_like(beta) if dbeta is None else dbeta
+    square = (B, H, d, d)
+    if dstate is None:
+        dstate = _new_float(square, state if dstate_out is None else dstate_out, v)
+    keys, values = _heads(q), _heads(v)
+    args = (keys, _heads(k), values, _gates(g), _gates(beta), _heads(dout), scale,
+            _float_array("state", state, square, v), _float_array("dstate_out", dstate_out, square, v), _heads(dq),
+            _heads(dk), _heads(dv), _gates(dg), _gates(dbeta), _float_array("dstate", dstate, square, v))
+    _same_device(v, q, k, g, beta, dout, dq, dk, dv, dg, dbeta)
+    L = lib()
+    _launch("mhla_delta_backward", L.mhla_delta_backward, args, v, workspace,
+            lambda: _size(L.mhla_delta_backward_workspace_size, "mhla_delta_backward_workspace_size", keys, values))
+    return dq, dk, dv, dg, dbeta, dstate
+
+
+def delta_step(q, k, v, g, beta, state, scale=1.0, out=None, stream=None):
+    """One token of the delta rule for every sequence: q, k [B, 1, Hk, d], v [B, 1, H, d], g and beta
+    [B, 1, H]; ``state`` (float32 [B, H, d, d]) is updated in place.  Returns ``out``.  ``stream`` as
+    for ``gated_forward``."""
+    if stream is not None:
+        with _on(stream, q):
+            return delta_step(q, k, v, g, beta, state, scale, out)
+    B, _, H, d = v.shape
+    if out is None:
+        import torch
+        out = torch.empty_like(v)
+    args = (_heads(q), _heads(k), _heads(v), _gates(g), _gates(beta), scale,
+            _float_array("state", state, (B, H, d, d), v), _heads(out))
+    _same_device(v, q, k, g, beta, out)
+    _launch("mhla_delta_step", lib().mhla_delta_step, args, v)
     return out
 
 

@@ -1,0 +1,771 @@
+// Gradients of the gated delta rule (delta_forward.cu has the notation).  With S the state that enters a chunk, D the gradient
+// of the one that leaves it, P = scale tril(Q K^T . D_ij) and do the gradient of the outputs,
+//   dW = P^T do + (e^{B-b} K) D          dR = T^T dW
+//   D' = e^B D + (scale e^b Q)^T do - K^^T dW      of the state that enters
+// so the gradient of the state runs backwards through a chunk in two products, as the state itself runs forwards: delta_back is
+// delta_scan's chain turned round, its second warps a chunk ahead with P^T do and Q^T do.  What is left,
+//   A = scale (do W^T) . D_ij  (i >= j),   L = -beta (dR W^T) . D_ij  (i > j)
+//   dq = scale e^b do S^T + A K
+//   dk = A^T Q + L K + L^T K - beta e^b dR S^T + e^{B-b} W D^T
+//   dv = beta dR,   dbeta = dR . (V - e^b K S) - rows of (dR W^T . G)
+// and the gates', a sum over what has the gate between its two tokens (pairs A (q k) + L (k k), what reads the state behind
+// it, what writes D in front of it, and e^B <S, D>; nothing cancels), every chunk does by itself: delta_grads.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "delta_common.cuh"
+
+namespace mhla {
+
+using namespace delta;
+
+namespace {
+
+struct BackArgs {
+  Common c;
+  const float* last;    // gradient of the last state, or null for zero
+  float* first;         // of the first one, or null
+};
+
+template <typename T, int DK, int NW>
+struct BackLay {
+  using L = Lay<T, DK>;
+  static constexpr int kThreads = 64 * NW, kWide = 16 * NW;   // columns of dout a CTA reads
+  static constexpr int kDoutPlane = L::C * kWide * 2;
+  static constexpr int kK = 0, kKeys = kK + L::kInput, kMarks = kKeys + L::kKeys, kStage = kMarks + L::kMarks;
+  static constexpr int kQ = 0, kScores = kQ + L::kInput, kDout = kScores + L::kScores, kMarksAhead = kDout + L::kIn * kDoutPlane;
+  static constexpr int kAhead = kMarksAhead + L::kMarks;
+  static constexpr int kHand = L::kState + L::kTokens;
+  static constexpr int kAheads = 2 * kStage, kHands = kAheads + 2 * kAhead, kBytes = kHands + 2 * NW * kHand;
+};
+
+template <typename T, int DK, int NW>
+__global__ void __launch_bounds__(BackLay<T, DK, NW>::kThreads) delta_back(const __grid_constant__ BackArgs a) {
+  using W = BackLay<T, DK, NW>;
+  using L = Lay<T, DK>;
+  constexpr int C = L::C, NT = C / 8, NS = DK / 8, THREADS = W::kThreads, WIDE = W::kWide;
+  extern __shared__ __align__(128) char smem[];
+  const Common& p = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int groups = (p.d + WIDE - 1) / WIDE;
+  const int64_t bh = blockIdx.x / groups, b = bh / p.H, h = bh % p.H, key = b * p.Hk + h / (p.H / p.Hk);
+  const int tile0 = static_cast<int>(blockIdx.x % groups) * NW;
+  const uint32_t base = ptx::smem_u32(smem);
+  const int count = static_cast<int>(p.chunks);
+  const int own = warp % NW, tile = tile0 + own, c0 = 16 * tile + (lane >> 2);
+  const bool chain = warp < NW;
+  auto chunk_of = [&](int i) { return count - 1 - i; };
+
+  auto load = [&](int i) {
+    const uint32_t st = base + (i & 1) * W::kStage;
+    const int64_t at = bh * p.chunks + chunk_of(i);
+    copy_async(st + W::kK, p.im.k + (key * p.chunks + chunk_of(i)) * L::kInput, L::kInput, threadIdx.x, THREADS);
+    copy_async(st + W::kKeys, p.im.keys + at * L::kKeys, L::kKeys, threadIdx.x, THREADS);
+    copy_async(st + W::kMarks, p.im.marks + at * L::kMarks, L::kMarks, threadIdx.x, THREADS);
+  };
+  auto load_ahead = [&](int i) {
+    const uint32_t st = base + W::kAheads + (i & 1) * W::kAhead;
+    const int64_t at = bh * p.chunks + chunk_of(i);
+    copy_async(st + W::kQ, p.im.q + (key * p.chunks + chunk_of(i)) * L::kInput, L::kInput, threadIdx.x, THREADS);
+    copy_async(st + W::kScores, p.im.scores + at * L::kScores, L::kScores, threadIdx.x, THREADS);
+    copy_async(st + W::kMarksAhead, p.im.marks + at * L::kMarks, L::kMarks, threadIdx.x, THREADS);
+    const char* src = p.im.dout + at * L::kInput;
+    constexpr int kUnits = WIDE / 8;
+    for (int j = threadIdx.x; j < L::kIn * C * kUnits; j += THREADS) {
+      const int n = j / (C * kUnits), r = j / kUnits % C, u = j % kUnits;
+      cp_async_16(st + W::kDout + n * W::kDoutPlane + unit_at<WIDE>(r, u), src + n * L::kRows + unit_at<DK>(r, 2 * tile0 + u), 16);
+    }
+  };
+  load_ahead(0);
+  commit();
+
+  // D^T: rows c0, c0 + 8 (columns of the state)
+  float D[NS][4];
+  if (chain) {
+    const float* in = a.last ? a.last + bh * p.d * p.d : nullptr;
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 8 * n + 2 * (lane & 3) + (e & 1), c = c0 + 8 * (e >> 1);
+        D[n][e] = in && r < p.d && c < p.d ? in[static_cast<int64_t>(r) * p.d + c] : 0.0f;
+      }
+  }
+
+  for (int i = 0; i <= count; ++i) {
+    wait_all();
+    __syncthreads();
+    if (i + 1 < count) load_ahead(i + 1);
+    if (i < count) load(i);
+    commit();
+    if (!chain) {
+      if (i >= count) continue;
+      // (P^T do)^T and ((scale e^b Q)^T do)^T
+      const char* stage = smem + W::kAheads + (i & 1) * W::kAhead;
+      const uint32_t st = base + W::kAheads + (i & 1) * W::kAhead;
+      const auto& m = *reinterpret_cast<const typename L::M*>(stage + W::kMarksAhead);
+      char* hand = smem + W::kHands + ((i & 1) * NW + own) * W::kHand;
+      float4 *to_x = reinterpret_cast<float4*>(hand) + lane, *to_y = reinterpret_cast<float4*>(hand + L::kState) + lane;
+      {
+        Accumulators<NT, L::kApart> acc;
+        acc.clear();
+#pragma unroll
+        for (int ks = 0; ks < C / 16; ++ks) {
+          uint32_t o[L::kIn][4];
+#pragma unroll
+          for (int n = 0; n < L::kIn; ++n) a_cols<WIDE>(o[n], st + W::kDout + n * W::kDoutPlane, 16 * own, 16 * ks, lane);
+#pragma unroll
+          for (int s = 0; s <= ks; ++s) {
+            uint32_t x[L::kScore][1][4];
+#pragma unroll
+            for (int n = 0; n < L::kScore; ++n) b_cols<C>(x[n][0], st + W::kScores + n * L::kSquare, 16 * s, 16 * ks, lane);
+            mma_terms(acc, 2 * s, o, x);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) to_y[32 * n] = make_float4(acc.get(n, 0), acc.get(n, 1), acc.get(n, 2), acc.get(n, 3));
+      }
+      uint32_t oa[C / 16][L::kOwn][4];
+#pragma unroll
+      for (int ks = 0; ks < C / 16; ++ks) {
+        float x[4][2];
+#pragma unroll
+        for (int n = 0; n < L::kIn; ++n) {
+          uint32_t o[4];
+          a_cols<WIDE>(o, st + W::kDout + n * W::kDoutPlane, 16 * own, 16 * ks, lane);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e][0] = n == 0 ? low(o[e]) : x[e][0] + low(o[e]);
+            x[e][1] = n == 0 ? high(o[e]) : x[e][1] + high(o[e]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = *reinterpret_cast<const float2*>(m.inside + 16 * ks + 8 * (e >> 1) + 2 * (lane & 3));
+          uint32_t t[L::kOwn];
+          split<L::kOwn>(x[e][0] * (p.scale * f.x), x[e][1] * (p.scale * f.y), t);
+#pragma unroll
+          for (int n = 0; n < L::kOwn; ++n) oa[ks][n][e] = t[n];
+        }
+      }
+      constexpr int G = 2;
+#pragma unroll
+      for (int n0 = 0; n0 < NS; n0 += 2 * G) {
+        Accumulators<2 * G, L::kApart> acc;
+        acc.clear();
+#pragma unroll
+        for (int ks = 0; ks < C / 16; ++ks) {
+          uint32_t x[L::kIn][G][4];
+#pragma unroll
+          for (int n = 0; n < L::kIn; ++n)
+#pragma unroll
+            for (int j = 0; j < G; ++j) b_cols<DK>(x[n][j], st + W::kQ + n * L::kRows, 8 * n0 + 16 * j, 16 * ks, lane);
+          mma_terms(acc, 0, oa[ks], x);
+        }
+#pragma unroll
+        for (int n = 0; n < 2 * G; ++n)
+          to_x[32 * (n0 + n)] = make_float4(acc.get(n, 0), acc.get(n, 1), acc.get(n, 2), acc.get(n, 3));
+      }
+    } else if (i > 0) {
+      const int now = i - 1;
+      const char* stage = smem + (now & 1) * W::kStage;
+      const uint32_t st = base + (now & 1) * W::kStage;
+      const auto& m = *reinterpret_cast<const typename L::M*>(stage + W::kMarks);
+      const char* hand = smem + W::kHands + ((now & 1) * NW + own) * W::kHand;
+      const float4 *of_x = reinterpret_cast<const float4*>(hand) + lane,
+                   *of_y = reinterpret_cast<const float4*>(hand + L::kState) + lane;
+      const int64_t at = (bh * p.chunks + chunk_of(now)) * (DK / 16) + tile;
+      const bool in = 16 * tile < p.d;
+      if (in) {
+        float4* to = reinterpret_cast<float4*>(p.im.ds + at * L::kState) + lane;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) to[32 * n] = make_float4(D[n][0], D[n][1], D[n][2], D[n][3]);
+      }
+      // dW^T = (P^T do)^T + D^T (e^{B-b} K)^T
+      Accumulators<NT, L::kApart> acc;
+      acc.clear();
+#pragma unroll
+      for (int ks = 0; ks < DK / 16; ++ks) {
+        uint32_t s[L::kOwn][4], x[L::kIn][NT / 2][4];
+        as_rows<L::kOwn>(s, D[2 * ks], D[2 * ks + 1]);
+#pragma unroll
+        for (int n = 0; n < L::kIn; ++n)
+#pragma unroll
+          for (int j = 0; j < NT / 2; ++j) b_rows<DK>(x[n][j], st + W::kK + n * L::kRows, 16 * j, 16 * ks, lane);
+        mma_terms(acc, 0, s, x);
+      }
+      float w[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float4 y = of_y[32 * n];
+        const float2 f = *reinterpret_cast<const float2*>(m.after + 8 * n + 2 * (lane & 3));
+        w[n][0] = fmaf(f.x, acc.get(n, 0), y.x); w[n][1] = fmaf(f.y, acc.get(n, 1), y.y);
+        w[n][2] = fmaf(f.x, acc.get(n, 2), y.z); w[n][3] = fmaf(f.y, acc.get(n, 3), y.w);
+      }
+      if (in) {
+        float4* to = reinterpret_cast<float4*>(p.im.dw + at * L::kTokens) + lane;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) to[32 * n] = make_float4(w[n][0], w[n][1], w[n][2], w[n][3]);
+      }
+      // D^T <- e^B D^T + (Q^T do)^T - dW^T K^, the chunk's part formed apart
+      uint32_t wa[C / 16][L::kOwn][4];
+#pragma unroll
+      for (int ks = 0; ks < C / 16; ++ks) as_rows<L::kOwn>(wa[ks], w[2 * ks], w[2 * ks + 1]);
+      const float total = m.total;
+      constexpr int G = DK / 16 < 4 ? DK / 16 : 4;
+#pragma unroll
+      for (int n0 = 0; n0 < NS; n0 += 2 * G) {
+        Accumulators<2 * G, L::kApart> sum;
+        sum.clear();
+#pragma unroll
+        for (int ks = 0; ks < C / 16; ++ks) {
+          uint32_t x[L::kOwn][G][4];
+#pragma unroll
+          for (int n = 0; n < L::kOwn; ++n)
+#pragma unroll
+            for (int j = 0; j < G; ++j) b_cols<DK>(x[n][j], st + W::kKeys + n * L::kRows, 8 * n0 + 16 * j, 16 * ks, lane);
+          mma_terms(sum, 0, wa[ks], x);
+        }
+#pragma unroll
+        for (int n = 0; n < 2 * G; ++n) {
+          const float4 x = of_x[32 * (n0 + n)];
+          const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) D[n0 + n][e] = fmaf(total, D[n0 + n][e], xs[e] - sum.get(n, e));
+        }
+      }
+    }
+  }
+  if (chain && a.first) {
+    float* first = a.first + bh * p.d * p.d;
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 8 * n + 2 * (lane & 3) + (e & 1), c = c0 + 8 * (e >> 1);
+        if (r < p.d && c < p.d) first[static_cast<int64_t>(r) * p.d + c] = D[n][e];
+      }
+  }
+}
+
+struct GradArgs {
+  Common c;
+  Operand dq, dk, dv, dg, dbeta;   // dq, dk: of every value head when they are shared, float32 then
+  uint32_t pairs;                  // stores of two values: 1 dq, 2 dk, 4 dv
+};
+
+template <typename T, int DK>
+struct GradLay {
+  using L = Lay<T, DK>;
+  static constexpr int C = L::C, kStrips = C / 16, kWarps = 2 * kStrips, kThreads = 32 * kWarps;
+  static constexpr int kSlice = DK < 64 ? DK : 64;                     // columns of the values of a state at once
+  static constexpr int kTurned = L::kOwn * DK * C * 2;                 // planes [column][token]
+  static constexpr int kSliceBytes = L::kOwn * kSlice * DK * 2, kPairs = C * (C + 1) * 4, kSum = C * DK * 4;
+  static constexpr int kK = 0, kQ = kK + L::kInput, kDout = kQ + L::kInput, kW = kDout + L::kInput, kR = kW + kTurned;
+  static constexpr int kA = kR + kTurned;                              // T before it is A
+  static constexpr int kL = kA + L::kInverse, kState = kL + L::kInverse;
+  static constexpr int kBytes = kState + std::max(kSliceBytes, std::max(kPairs, kSum));
+};
+
+// One chunk of one (b, h).  A pair of warps has 16 rows: one the products with dout (dq, A), the other those with dR (L, dk).
+template <typename T, int DK, typename O>
+__global__ void __launch_bounds__(GradLay<T, DK>::kThreads) delta_grads(const __grid_constant__ GradArgs a) {
+  using G = GradLay<T, DK>;
+  using L = Lay<T, DK>;
+  constexpr int C = L::C, THREADS = G::kThreads, STRIPS = G::kStrips, NS = DK / 8, TILES = DK / 16;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ __align__(16) typename L::M m;
+  __shared__ float vdot[TILES][C], rows_g[C], zk[C], enters[2][C], leaves[C], crossing[C], both[G::kWarps];
+  const Common& p = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t chunk = blockIdx.x % p.chunks;
+  const int64_t bh = blockIdx.x / p.chunks, b = bh / p.H, h = bh % p.H;
+  const int64_t at = bh * p.chunks + chunk, at_key = (b * p.Hk + h / (p.H / p.Hk)) * p.chunks + chunk;
+  const int64_t t0 = static_cast<int64_t>(chunk) * C;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(C), p.N - t0));
+  const uint32_t base = ptx::smem_u32(smem);
+  const int strip = warp % STRIPS, m0 = 16 * strip, row = m0 + (lane >> 2);
+  const bool second = warp >= STRIPS;
+
+  copy_async(base + G::kK, p.im.k + at_key * L::kInput, L::kInput, threadIdx.x, THREADS);
+  copy_async(base + G::kQ, p.im.q + at_key * L::kInput, L::kInput, threadIdx.x, THREADS);
+  copy_async(base + G::kDout, p.im.dout + at * L::kInput, L::kInput, threadIdx.x, THREADS);
+  copy_async(base + G::kA, p.im.inverse + at * L::kInverse, L::kInverse, threadIdx.x, THREADS);
+  copy_async(ptx::smem_u32(&m), p.im.marks + at * L::kMarks, L::kMarks, threadIdx.x, THREADS);
+  commit();
+  // two values of one row of planes W columns wide
+  auto put = [&](int where, int width, int plane, int r, int n, float x, float y) {
+    uint32_t t[L::kOwn];
+    split<L::kOwn>(x, y, t);
+#pragma unroll
+    for (int k = 0; k < L::kOwn; ++k) {
+      const int u = width == C ? unit_at<C>(r, n) : unit_at<DK>(r, n);
+      *reinterpret_cast<uint32_t*>(smem + where + k * plane + u + 4 * (lane & 3)) = t[k];
+    }
+  };
+  // W^T from its fragments
+  for (int tile = warp; tile < TILES; tile += G::kWarps) {
+    const float4* from = reinterpret_cast<const float4*>(p.im.w + (at * TILES + tile) * L::kTokens) + lane;
+#pragma unroll
+    for (int n = 0; n < C / 8; ++n) {
+      const float4 x = 16 * tile < p.d ? from[32 * n] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      put(G::kW, C, DK * C * 2, 16 * tile + (lane >> 2), n, x.x, x.y);
+      put(G::kW, C, DK * C * 2, 16 * tile + (lane >> 2) + 8, n, x.z, x.w);
+    }
+  }
+  wait_all();
+  __syncthreads();
+
+  // dR^T = dW^T T; dv; dR . V
+  for (int tile = warp; tile < TILES; tile += G::kWarps) {
+    Accumulators<C / 8, L::kApart> acc;
+    acc.clear();
+    if (16 * tile < p.d) {
+      const float4* from = reinterpret_cast<const float4*>(p.im.dw + (at * TILES + tile) * L::kTokens) + lane;
+#pragma unroll
+      for (int ks = 0; ks < STRIPS; ++ks) {
+        const float4 x = from[64 * ks], y = from[64 * ks + 32];
+        const float lo[4] = {x.x, x.y, x.z, x.w}, hi[4] = {y.x, y.y, y.z, y.w};
+        uint32_t wa[L::kOwn][4];
+        as_rows<L::kOwn>(wa, lo, hi);
+#pragma unroll
+        for (int s = 0; s <= ks; ++s) {
+          uint32_t t[L::kOwn][1][4];
+#pragma unroll
+          for (int n = 0; n < L::kOwn; ++n) b_cols<C>(t[n][0], base + G::kA + n * L::kSquare, 16 * s, 16 * ks, lane);
+          mma_terms(acc, 2 * s, wa, t);
+        }
+      }
+    }
+    const T* v = static_cast<const T*>(p.v.data) + b * p.v.sb + h * p.v.sh + t0 * p.v.sn;
+    T* dv = static_cast<T*>(a.dv.data) + b * a.dv.sb + h * a.dv.sh + t0 * a.dv.sn;
+#pragma unroll
+    for (int n = 0; n < C / 8; ++n) {
+      float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int c = 16 * tile + (lane >> 2) + 8 * f;
+        put(G::kR, C, DK * C * 2, c, n, acc.get(n, 2 * f), acc.get(n, 2 * f + 1));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = 8 * n + 2 * (lane & 3) + e;
+          if (t < rows && c < p.d) {
+            const float x = acc.get(n, 2 * f + e);
+            sum[e] = fmaf(x, to_f(v[t * p.v.sn + c]), sum[e]);
+            from_f(dv + t * a.dv.sn + c, m.beta[t] * x);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sum[e] += __shfl_xor_sync(~0u, sum[e], 4);
+        sum[e] += __shfl_xor_sync(~0u, sum[e], 8);
+        sum[e] += __shfl_xor_sync(~0u, sum[e], 16);
+        if (lane < 4) vdot[tile][8 * n + 2 * lane + e] = sum[e];
+      }
+    }
+  }
+  __syncthreads();
+
+  // do W^T and Q K^T (first), dR W^T and K K^T (second), up to the diagonal: A and L, and the pairs of the gates
+  float pairs[2 * STRIPS][4];
+  {
+    Accumulators<2 * STRIPS, L::kApart> x, y;
+    x.clear();
+    y.clear();
+#pragma unroll 1
+    for (int ks = 0; ks < TILES; ++ks) {
+      uint32_t l[L::kIn][4], r[L::kOwn][4];
+      uint32_t key[L::kIn][4];
+#pragma unroll
+      for (int n = 0; n < L::kIn; ++n) a_rows<DK>(key[n], base + (second ? G::kK : G::kQ) + n * L::kRows, m0, 16 * ks, lane);
+      if (second)
+#pragma unroll
+        for (int n = 0; n < L::kOwn; ++n) a_cols<C>(r[n], base + G::kR + n * DK * C * 2, m0, 16 * ks, lane);
+      else
+#pragma unroll
+        for (int n = 0; n < L::kIn; ++n) a_rows<DK>(l[n], base + G::kDout + n * L::kRows, m0, 16 * ks, lane);
+#pragma unroll
+      for (int s = 0; s < STRIPS; ++s) {
+        if (s > strip) continue;
+        uint32_t w[L::kOwn][1][4], k[L::kIn][1][4];
+#pragma unroll
+        for (int n = 0; n < L::kOwn; ++n) b_cols<C>(w[n][0], base + G::kW + n * DK * C * 2, 16 * s, 16 * ks, lane);
+#pragma unroll
+        for (int n = 0; n < L::kIn; ++n) b_rows<DK>(k[n][0], base + G::kK + n * L::kRows, 16 * s, 16 * ks, lane);
+        if (second)
+          mma_terms(x, 2 * s, r, w);
+        else
+          mma_terms(x, 2 * s, l, w);
+        mma_terms(y, 2 * s, key, k);
+      }
+    }
+    const Sum br[2] = {{m.hi[row], m.lo[row]}, {m.hi[row + 8], m.lo[row + 8]}};
+    const float beta_r[2] = {m.beta[row], m.beta[row + 8]};
+    float sum[2] = {0.0f, 0.0f};
+    // T's planes, where A goes, were last read in front of the barrier
+#pragma unroll
+    for (int n = 0; n < 2 * STRIPS; ++n) {
+      if (n >= 2 * strip + 2) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pairs[n][e] = 0.0f;
+        continue;
+      }
+      const int c = 8 * n + 2 * (lane & 3);
+      float f[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = row + 8 * (e >> 1), s = c + (e & 1);
+        const Sum bc = {m.hi[s], m.lo[s]};
+        const float decay = s <= r ? exp2_of(br[e >> 1], bc) : 0.0f;
+        const float g = s <= r ? x.get(n, e) * decay : 0.0f, k = y.get(n, e);
+        if (second) {
+          f[e] = s < r ? -beta_r[e >> 1] * g : 0.0f;
+          if (s < r) sum[e >> 1] = fmaf(g, k, sum[e >> 1]);
+        } else {
+          f[e] = p.scale * g;
+        }
+        pairs[n][e] = s < r ? f[e] * k : 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) put(second ? G::kL : G::kA, C, L::kSquare, row + 8 * e, n, f[2 * e], f[2 * e + 1]);
+    }
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      sum[f] += __shfl_xor_sync(~0u, sum[f], 1);
+      sum[f] += __shfl_xor_sync(~0u, sum[f], 2);
+      if (second && (lane & 3) == 0) rows_g[row + 8 * f] = sum[f];
+    }
+  }
+  // pairs that a gate lies between: sums over the rows from the gate on, then over the columns in front of it
+  float* grid = reinterpret_cast<float*>(smem + G::kState);
+#pragma unroll
+  for (int turn = 0; turn < 2; ++turn) {
+    if (second == (turn == 1))
+#pragma unroll
+      for (int n = 0; n < 2 * STRIPS; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float* to = grid + (row + 8 * (e >> 1)) * (C + 1) + 8 * n + 2 * (lane & 3) + (e & 1);
+          *to = turn ? *to + pairs[n][e] : pairs[n][e];
+        }
+    __syncthreads();
+  }
+  if (threadIdx.x < C) {
+    float run = 0.0f;
+    for (int t = C - 1; t >= 0; --t) {
+      run += grid[t * (C + 1) + threadIdx.x];
+      grid[t * (C + 1) + threadIdx.x] = run;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < C) {
+    float run = 0.0f;
+    for (int s = 0; s < static_cast<int>(threadIdx.x); ++s) run += grid[threadIdx.x * (C + 1) + s];
+    crossing[threadIdx.x] = run;
+  }
+  __syncthreads();
+
+  float through = 0.0f;   // <S, D>
+  // rows of S^T or D^T of a slice of the values' columns
+  auto fill = [&](const char* from, int slice, bool dot) {
+    for (int j = warp; j < G::kSlice / 16 * NS; j += G::kWarps) {
+      const int tile = slice * (G::kSlice / 16) + j / NS, n = j % NS;
+      const bool in = 16 * tile < p.d;
+      const int64_t off = (at * TILES + tile) * L::kState;
+      const float4 x = in ? reinterpret_cast<const float4*>(from + off)[32 * n + lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const int r = 16 * (j / NS) + (lane >> 2);
+      put(G::kState, DK, G::kSlice * DK * 2, r, n, x.x, x.y);
+      put(G::kState, DK, G::kSlice * DK * 2, r + 8, n, x.z, x.w);
+      if (dot && in) {
+        const float4 y = reinterpret_cast<const float4*>(p.im.s + off)[32 * n + lane];
+        through = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, through))));
+      }
+    }
+  };
+  // a row's sum of acc times the rows of a plane
+  auto dot_rows = [&](const Accumulators<NS, L::kApart>& acc, int where, float (&sum)[2]) {
+    sum[0] = sum[1] = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        float x = 0.0f, y = 0.0f;
+#pragma unroll
+        for (int k = L::kIn - 1; k >= 0; --k) {
+          const uint32_t t = *reinterpret_cast<const uint32_t*>(smem + where + k * L::kRows + unit_at<DK>(row + 8 * f, n) + 4 * (lane & 3));
+          x += low(t);
+          y += high(t);
+        }
+        sum[f] = fmaf(acc.get(n, 2 * f), x, fmaf(acc.get(n, 2 * f + 1), y, sum[f]));
+      }
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      sum[f] += __shfl_xor_sync(~0u, sum[f], 1);
+      sum[f] += __shfl_xor_sync(~0u, sum[f], 2);
+    }
+  };
+  auto weigh = [&](Accumulators<NS, L::kApart>& acc, float f0, float f1) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc.main[n][e] = acc.get(n, e) * (e < 2 ? f0 : f1);
+        if (L::kApart) acc.small[L::kApart ? n : 0][e] = 0.0f;
+      }
+  };
+  // acc += rows of a square plane, or of its transpose, times the rows of an input
+  auto add_square = [&](Accumulators<NS, L::kApart>& acc, int square, bool turned, int where) {
+#pragma unroll 1
+    for (int ks = turned ? strip : 0; ks < (turned ? STRIPS : strip + 1); ++ks) {
+      uint32_t l[L::kOwn][4];
+#pragma unroll
+      for (int n = 0; n < L::kOwn; ++n) {
+        if (turned)
+          a_cols<C>(l[n], base + square + n * L::kSquare, m0, 16 * ks, lane);
+        else
+          a_rows<C>(l[n], base + square + n * L::kSquare, m0, 16 * ks, lane);
+      }
+#pragma unroll
+      for (int j = 0; j < NS / 2; ++j) {
+        uint32_t x[L::kIn][1][4];
+#pragma unroll
+        for (int n = 0; n < L::kIn; ++n) b_cols<DK>(x[n][0], base + where + n * L::kRows, 16 * j, 16 * ks, lane);
+        mma_terms(acc, 2 * j, l, x);
+      }
+    }
+  };
+  // acc += rows of dout (of inputs) or of the transposes of dR, W, times the state's slice
+  auto add_state = [&](Accumulators<NS, L::kApart>& acc, int slice, int turned) {
+#pragma unroll 1
+    for (int ks = 0; ks < G::kSlice / 16; ++ks) {
+      uint32_t in[L::kIn][4], l[L::kOwn][4];
+      const int k0 = slice * G::kSlice + 16 * ks;
+      if (turned)
+#pragma unroll
+        for (int n = 0; n < L::kOwn; ++n) a_cols<C>(l[n], base + turned + n * DK * C * 2, m0, k0, lane);
+      else
+#pragma unroll
+        for (int n = 0; n < L::kIn; ++n) a_rows<DK>(in[n], base + G::kDout + n * L::kRows, m0, k0, lane);
+#pragma unroll
+      for (int j = 0; j < NS / 2; ++j) {
+        uint32_t x[L::kOwn][1][4];
+#pragma unroll
+        for (int n = 0; n < L::kOwn; ++n) b_cols<DK>(x[n][0], base + G::kState + n * G::kSlice * DK * 2, 16 * j, 16 * ks, lane);
+        if (turned)
+          mma_terms(acc, 2 * j, l, x);
+        else
+          mma_terms(acc, 2 * j, in, x);
+      }
+    }
+  };
+  auto store = [&](const Accumulators<NS, L::kApart>& acc, const Operand& to, bool two) {
+    O* out = static_cast<O*>(to.data) + b * to.sb + h * to.sh + t0 * to.sn;
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const int r = row + 8 * f;
+      if (r >= rows) continue;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        const int c = 8 * n + 2 * (lane & 3);
+        if (c < p.d) store_pair<O>(out + r * to.sn + c, acc.get(n, 2 * f), acc.get(n, 2 * f + 1), two, c + 1 < p.d);
+      }
+    }
+  };
+
+  Accumulators<NS, L::kApart> acc;
+  acc.clear();
+  for (int slice = 0; slice < DK / G::kSlice; ++slice) {
+    fill(p.im.s, slice, false);
+    __syncthreads();
+    add_state(acc, slice, second ? G::kR : 0);
+    __syncthreads();
+  }
+  {
+    const float in0 = m.inside[row], in1 = m.inside[row + 8];
+    float sum[2];
+    if (second) {
+      dot_rows(acc, G::kK, sum);
+      weigh(acc, -m.beta[row] * in0, -m.beta[row + 8] * in1);
+      if ((lane & 3) == 0) {
+        zk[row] = in0 * sum[0];
+        zk[row + 8] = in1 * sum[1];
+        enters[1][row] = -m.beta[row] * in0 * sum[0];
+        enters[1][row + 8] = -m.beta[row + 8] * in1 * sum[1];
+      }
+      add_square(acc, G::kL, false, G::kK);
+      add_square(acc, G::kL, true, G::kK);
+    } else {
+      weigh(acc, p.scale * in0, p.scale * in1);
+      dot_rows(acc, G::kQ, sum);
+      if ((lane & 3) == 0) {
+        enters[0][row] = sum[0];
+        enters[0][row + 8] = sum[1];
+      }
+      add_square(acc, G::kA, false, G::kK);
+      store(acc, a.dq, a.pairs & 1);
+      acc.clear();
+    }
+  }
+  for (int slice = 0; slice < DK / G::kSlice; ++slice) {
+    fill(p.im.ds, slice, true);
+    __syncthreads();
+    if (!second) add_state(acc, slice, G::kW);
+    __syncthreads();
+  }
+  through += __shfl_xor_sync(~0u, through, 16);
+  through += __shfl_xor_sync(~0u, through, 8);
+  through += __shfl_xor_sync(~0u, through, 4);
+  through += __shfl_xor_sync(~0u, through, 2);
+  through += __shfl_xor_sync(~0u, through, 1);
+  if (lane == 0) both[warp] = through;
+  float4* half = reinterpret_cast<float4*>(smem + G::kState) + strip * NS * 32 + lane;
+  if (!second) {
+    weigh(acc, m.after[row], m.after[row + 8]);
+    float sum[2];
+    dot_rows(acc, G::kK, sum);
+    if ((lane & 3) == 0) {
+      leaves[row] = sum[0];
+      leaves[row + 8] = sum[1];
+    }
+    add_square(acc, G::kA, true, G::kQ);
+#pragma unroll
+    for (int n = 0; n < NS; ++n) half[32 * n] = make_float4(acc.get(n, 0), acc.get(n, 1), acc.get(n, 2), acc.get(n, 3));
+  }
+  __syncthreads();
+  if (second) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      const float4 x = half[32 * n];
+      acc.main[n][0] += x.x; acc.main[n][1] += x.y; acc.main[n][2] += x.z; acc.main[n][3] += x.w;
+    }
+    store(acc, a.dk, a.pairs & 2);
+  } else if (threadIdx.x < C && static_cast<int>(threadIdx.x) < rows) {
+    const int t = threadIdx.x;
+    float dbeta = 0.0f, dg = crossing[t], all = 0.0f;
+#pragma unroll
+    for (int n = 0; n < TILES; ++n) dbeta += vdot[n][t];
+    dbeta -= zk[t] + rows_g[t];
+    float sum = 0.0f;
+    for (int s = C - 1; s >= t; --s) sum += enters[0][s] + enters[1][s];
+    dg += sum;
+    sum = 0.0f;
+    for (int s = 0; s < t; ++s) sum += leaves[s];
+    dg += sum;
+#pragma unroll
+    for (int n = 0; n < G::kWarps; ++n) all += both[n];
+    dg = fmaf(m.total, all, dg);
+    from_f(static_cast<T*>(a.dg.data) + b * a.dg.sb + h * a.dg.sh + (t0 + t) * a.dg.sn, dg);
+    from_f(static_cast<T*>(a.dbeta.data) + b * a.dbeta.sb + h * a.dbeta.sh + (t0 + t) * a.dbeta.sn, dbeta);
+  }
+}
+
+// Gradients of shared heads: the sum over the value heads of each, in their order.
+struct Shared {
+  const float* part[2];   // [B][N][H][d]
+  Operand to[2];
+  int64_t N, total;       // elements of one of them
+  int32_t Hk, times, d;
+};
+template <typename T>
+__global__ void __launch_bounds__(256) delta_shared(const __grid_constant__ Shared a) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= a.total) return;
+  const int c = static_cast<int>(i % a.d);
+  const int64_t head = i / a.d, hk = head % a.Hk, token = head / a.Hk, n = token % a.N, b = token / a.N;
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    const float* x = a.part[o] + head * a.times * a.d + c;
+    float sum = 0.0f;
+    for (int j = 0; j < a.times; ++j) sum += x[static_cast<int64_t>(j) * a.d];
+    from_f(static_cast<T*>(a.to[o].data) + b * a.to[o].sb + n * a.to[o].sn + hk * a.to[o].sh + c, sum);
+  }
+}
+
+template <typename T, int DK>
+int back_as(const BackArgs& a, int64_t BH, cudaStream_t s) {
+  constexpr int NW = 2;
+  using W = BackLay<T, DK, NW>;
+  static_assert(W::kBytes <= 227 * 1024, "shared memory");
+  if (cudaFuncSetAttribute(delta_back<T, DK, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kBytes) != cudaSuccess)
+    return MHLA_ERR_CUDA;
+  const int groups = (a.c.d + 16 * NW - 1) / (16 * NW);
+  KernelTimer timer("delta_back", s);
+  delta_back<T, DK, NW><<<static_cast<unsigned>(BH * groups), W::kThreads, W::kBytes, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+}
+
+template <typename T, int DK, typename O>
+int grads_as(const GradArgs& a, int64_t BH, cudaStream_t s) {
+  using G = GradLay<T, DK>;
+  static_assert(G::kBytes <= 220 * 1024, "shared memory");
+  if (cudaFuncSetAttribute(delta_grads<T, DK, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kBytes) != cudaSuccess)
+    return MHLA_ERR_CUDA;
+  KernelTimer timer("delta_grads", s);
+  delta_grads<T, DK, O><<<static_cast<unsigned>(BH * a.c.chunks), G::kThreads, G::kBytes, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+}
+
+template <typename T, int DK>
+int run_as(const BackArgs& b, const GradArgs& g, int64_t BH, bool shared, cudaStream_t s) {
+  const int rc = back_as<T, DK>(b, BH, s);
+  if (rc != MHLA_OK) return rc;
+  return shared && sizeof(T) == 2 ? grads_as<T, DK, float>(g, BH, s) : grads_as<T, DK, T>(g, BH, s);
+}
+
+template <typename T>
+int run_type(const BackArgs& b, const GradArgs& g, int64_t BH, bool shared, cudaStream_t s) {
+  switch (padded(b.c.d)) {
+    case 32: return run_as<T, 32>(b, g, BH, shared, s);
+    case 64: return run_as<T, 64>(b, g, BH, shared, s);
+    default: return run_as<T, 128>(b, g, BH, shared, s);
+  }
+}
+
+size_t shared_bytes(const DeltaProblem& p) { return p.H == p.Hk ? 0 : align_up(static_cast<size_t>(p.B * p.N * p.H * p.d) * 4); }
+
+}  // namespace
+
+size_t delta_bwd_workspace_bytes(const DeltaProblem& p) {
+  Images im;
+  return lay_out(p, true, nullptr, &im) + 2 * shared_bytes(p);
+}
+
+int launch_delta_backward(const DeltaProblem& p, const DeltaBackward& d, void* workspace, void* stream) {
+  ScanArgs a = {};
+  a.c = common(p, &d.dout);
+  char* rest = static_cast<char*>(workspace);
+  rest += lay_out(p, true, rest, &a.c.im);
+  a.init = d.state_in;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t BH = p.B * p.H;
+  int rc = launch_prepare(a.c, BH, p.dtype, true, s);
+  if (rc == MHLA_OK) rc = launch_scan(a, BH, p.dtype, true, s);
+  if (rc != MHLA_OK) return rc;
+  const BackArgs b = {a.c, d.dstate_out, d.dstate_in};
+  GradArgs g = {a.c, d.dq, d.dk, d.dv, d.dg, d.dbeta, 0};
+  const bool shared = p.H != p.Hk;
+  float* part[2] = {reinterpret_cast<float*>(rest), reinterpret_cast<float*>(rest + shared_bytes(p))};
+  if (shared) {
+    g.dq = Operand{part[0], p.N * p.H * p.d, p.H * p.d, p.d};
+    g.dk = Operand{part[1], p.N * p.H * p.d, p.H * p.d, p.d};
+  }
+  const int dtype = shared ? MHLA_F32 : p.dtype;
+  g.pairs = (pairs_fit(g.dq, p.d, dtype) ? 1u : 0u) | (pairs_fit(g.dk, p.d, dtype) ? 2u : 0u);
+  rc = p.dtype == MHLA_BF16 ? run_type<__nv_bfloat16>(b, g, BH, shared, s) : run_type<float>(b, g, BH, shared, s);
+  if (rc != MHLA_OK || !shared) return rc;
+  Shared sh = {{part[0], part[1]}, {d.dq, d.dk}, p.N, p.B * p.N * p.Hk * p.d, static_cast<int32_t>(p.Hk),
+               static_cast<int32_t>(p.H / p.Hk), p.d};
+  KernelTimer timer("delta_shared", s);
+  const unsigned grid = static_cast<unsigned>((sh.total + 255) / 256);
+  if (p.dtype == MHLA_BF16)
+    delta_shared<__nv_bfloat16><<<grid, 256, 0, s>>>(sh);
+  else
+    delta_shared<float><<<grid, 256, 0, s>>>(sh);
+  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+}
+
+}  // namespace mhla

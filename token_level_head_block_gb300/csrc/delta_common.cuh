@@ -1,0 +1,144 @@
+// What the kernels of the gated delta rule share: sizes, the layout of what one kernel leaves for the
+// next in the workspace, and fragments.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "gated_common.cuh"
+#include "mhla_internal.h"
+#include "ptx.cuh"
+#include "warp_mma.cuh"
+
+namespace mhla {
+namespace delta {
+
+using namespace gated;
+
+// Terms of bf16 that a value enters the tensor cores with: an input, a value formed on the way (two leave
+// 2^-16, under the error that the float32 state is allowed; three 2^-24), and a score, which only feeds an output: with
+// bf16 outputs its own rounding (2^-9) stays under theirs.
+// Tokens a chunk: three planes of float32 rows of 128 channels leave room for 32.
+template <typename T>
+struct Form;
+template <>
+struct Form<__nv_bfloat16> {
+  static constexpr int kIn = 1, kOwn = 2, kScore = 1, kChunk = 64;
+};
+template <>
+struct Form<float> {
+  static constexpr int kIn = 3, kOwn = 3, kScore = 3, kChunk = 32;
+};
+
+// A chunk's values a token, then whether any is not finite and each column's first such token.
+template <int C, int DK>
+struct Marks {
+  float hi[C], lo[C];      // sum b of the log decays up to the token, in powers of two
+  float inside[C];         // e^b
+  float after[C];          // e^(B - b), B that of the whole chunk
+  float beta[C];
+  float total;             // e^B
+  int32_t any, pad[2];
+  int32_t first[DK];
+};
+
+template <typename T, int DK>
+struct Lay {
+  static constexpr int C = Form<T>::kChunk, kIn = Form<T>::kIn, kOwn = Form<T>::kOwn, kScore = Form<T>::kScore;
+  static constexpr bool kApart = kIn > 1;
+  static constexpr int kRows = C * DK * 2, kSquare = C * C * 2;   // bytes of a plane
+  static constexpr int kInput = kIn * kRows, kKeys = kOwn * kRows, kScores = kScore * kSquare, kInverse = kOwn * kSquare;
+  static constexpr int kTokens = C / 8 * 512, kState = DK / 8 * 512;   // bytes of a warp's 16 columns, float32 fragments
+  using M = Marks<C, DK>;
+  static constexpr int kMarks = sizeof(M);
+  static_assert(kMarks % 16 == 0, "copied in 16-byte units");
+};
+
+// Where a call's images lie.  Those of key heads [B][Hk][chunks], the others [B][H][chunks]; fragments of
+// tokens [DK / 16][C / 8][32] and of states [DK / 16][DK / 8][32], 16 columns of the values apart.
+struct Images {
+  char *k, *q;          // planes of rows
+  char* keys;           // T beta e^b K
+  char* scores;         // scale tril(Q K^T . decay)
+  char* u;              // fragments of (T beta V)^T
+  char* marks;
+  char *inverse, *dout; // gradients: T, planes of rows of dout
+  char *s, *w;          // gradients: the state entering the chunk and what its tokens write, fragments
+  char *ds, *dw;        // gradients: of the state leaving the chunk and of w
+};
+
+struct Common {
+  Operand q, k, v, g, beta, dout;
+  int64_t N, H, Hk;
+  uint32_t chunks;
+  int32_t d;
+  float scale;
+  uint32_t wide;        // operands whose rows 16-byte accesses take, a bit each in the order above
+  Images im;
+};
+enum : uint32_t { kWideQ = 1, kWideK = 2, kWideV = 4, kWideDout = 8 };
+
+struct ScanArgs {
+  Common c;
+  const float* init;
+  float* last;
+  Operand out;
+  bool out_pairs;       // 4-byte stores of two bf16 (8-byte of two float32) take the output
+};
+
+__device__ __forceinline__ float nan_value() { return __int_as_float(0x7FFFFFFF); }
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7F800000); }
+
+// float32 fragments of a transposed product [m][n] as A operands: 16 of k from column tiles 2 ks, 2 ks + 1.
+template <int NT>
+__device__ __forceinline__ void as_rows(uint32_t (&a)[NT][4], const float (&lo)[4], const float (&hi)[4]) {
+  uint32_t t[NT];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float(&x)[4] = e < 2 ? lo : hi;
+    split<NT>(x[2 * (e & 1)], x[2 * (e & 1) + 1], t);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) a[i][e] = t[i];
+  }
+}
+
+__device__ __forceinline__ void copy_async(uint32_t dst, const char* src, int bytes, int thread, int threads) {
+  for (int i = 16 * thread; i < bytes; i += 16 * threads) cp_async_16(dst + i, src + i, 16);
+}
+__device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+template <typename T>
+__device__ __forceinline__ void store_pair(T* p, float x, float y, bool pairs, bool both);
+template <>
+__device__ __forceinline__ void store_pair<__nv_bfloat16>(__nv_bfloat16* p, float x, float y, bool pairs, bool both) {
+  if (pairs) {
+    *reinterpret_cast<uint32_t*>(p) = pack(x, y);
+  } else {
+    from_f(p, x);
+    if (both) from_f(p + 1, y);
+  }
+}
+template <>
+__device__ __forceinline__ void store_pair<float>(float* p, float x, float y, bool pairs, bool both) {
+  if (pairs) {
+    *reinterpret_cast<float2*>(p) = make_float2(x, y);
+  } else {
+    p[0] = x;
+    if (both) p[1] = y;
+  }
+}
+
+inline int padded(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : 128; }
+
+// Launches of delta_forward.cu that both directions make.
+int launch_prepare(const Common& c, int64_t BH, int dtype, bool grad, cudaStream_t s);
+int launch_scan(const ScanArgs& a, int64_t BH, int dtype, bool keep, cudaStream_t s);
+size_t lay_out(const DeltaProblem& p, bool grad, char* base, Images* im);
+Common common(const DeltaProblem& p, const Operand* dout);
+bool pairs_fit(const Operand& o, int d, int dtype);
+
+}  // namespace delta
+}  // namespace mhla

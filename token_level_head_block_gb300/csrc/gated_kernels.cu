@@ -39,6 +39,7 @@
 #include "gated_common.cuh"
 #include "mhla_internal.h"
 #include "ptx.cuh"
+#include "warp_mma.cuh"
 
 namespace mhla {
 
@@ -63,86 +64,6 @@ struct Terms<float> {
   static constexpr int kIn = 3, kScore = 3, kState = 3;
 };
 constexpr int kAdd = 3;
-
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
-}
-
-__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
-// Accumulators of NT column tiles.  The tensor core truncates what it adds to an
-// accumulator, which drifts over a long chain: float32 runs keep the products of the
-// first terms, few additions, apart from the many small ones.
-template <int NT, bool APART>
-struct Accumulators {
-  float main[NT][4];
-  float small[APART ? NT : 1][4];
-  __device__ __forceinline__ float get(int n, int e) const {
-    return APART ? main[n][e] + small[APART ? n : 0][e] : main[n][e];
-  }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        main[n][e] = 0.0f;
-        if (APART) small[APART ? n : 0][e] = 0.0f;
-      }
-  }
-};
-
-// acc[n0 .. n0 + 2 P) += A B over the terms of both whose product is not below the last
-// term's size; b[t][p] holds two column tiles.  Independent accumulators follow one another.
-// first: nothing is there yet.
-template <int NA, int NB, int P, int NT, bool APART>
-__device__ __forceinline__ void mma_terms(Accumulators<NT, APART>& acc, int n0, const uint32_t (&a)[NA][4],
-                                          const uint32_t (&b)[NB][P][4], bool first = false) {
-  constexpr int kMost = NA > NB ? NA : NB;
-#pragma unroll
-  for (int i = NA - 1; i >= 0; --i)
-#pragma unroll
-    for (int j = NB - 1; j >= 0; --j) {
-      if (i + j >= kMost) continue;
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const int n = n0 + 2 * p + f;
-          float(&c)[4] = APART && i + j > 0 ? acc.small[APART ? n : 0] : acc.main[n];
-          // the first pair of terms that goes to this accumulator
-          const bool opens = APART ? (i + j == 0 || (i == NA - 1 && j == kMost - NA)) : (i == NA - 1 && j == kMost - NA);
-          if (first && opens)
-            mma_first(c, a[i], b[j][p][2 * f], b[j][p][2 * f + 1]);
-          else
-            mma(c, a[i], b[j][p][2 * f], b[j][p][2 * f + 1]);
-        }
-    }
-}
 
 // What a chunk needs of its gates.  Rows i of a block of 16 tokens see tokens j of other
 // blocks through e^{b_i - b_j} = e^{b_i - m} e^{m - b_j}, m at the edge of the
@@ -224,14 +145,6 @@ __device__ __forceinline__ Sum chunk_gates(float2 g, Gates& out, const Scan& a, 
   if ((lane & 7) == 0) out.enter[block] = a.state_scale * exp2_of(m, none);
   if (lane == 0) out.total = exp2_of(all, none);
   return all;
-}
-
-// Byte offset of a 16-byte unit of a row-major bf16 tile W columns wide.  Units change
-// places with the row's number, so that eight rows read at one column (ldmatrix) or
-// written at one (accumulators) meet all banks.
-template <int W>
-__device__ __forceinline__ int unit_at(int row, int unit) {
-  return row * (2 * W) + ((unit ^ (W == 32 ? (row >> 1) & 3 : row & 7)) << 4);
 }
 
 // Warps of a CTA.  d > 64 takes eight, two to 16 rows of outputs, each with half of the columns (scores

@@ -262,6 +262,27 @@ int launch_gated_backward(const GatedProblem& p, const GatedBackward& b, void* w
 int launch_gated_step(const GatedProblem& p, float* state, const Operand& out, void* stream);
 int read_and_clear_gated_error(void* stream, uint32_t* flags);
 
+// The gated delta rule (delta_forward.cu, delta_backward.cu).  q and k have Hk heads, each shared by H / Hk of the others.
+struct DeltaProblem {
+  int64_t B, N, H, Hk;
+  int32_t d;
+  int dtype;                 // mhla_dtype_t
+  float scale;
+  Operand q, k, v, g, beta;  // g, beta: one value a token and head
+};
+struct DeltaBackward {
+  Operand dout, dq, dk, dv, dg, dbeta;
+  const float *state_in, *dstate_out;   // [B][H][d][d] or null
+  float* dstate_in;                     // or null
+};
+int64_t delta_chunks(const DeltaProblem& p);
+size_t delta_workspace_bytes(const DeltaProblem& p);
+size_t delta_bwd_workspace_bytes(const DeltaProblem& p);
+int launch_delta_forward(const DeltaProblem& p, const float* state_in, const Operand& out, float* state_out, void* workspace,
+                         void* stream);
+int launch_delta_backward(const DeltaProblem& p, const DeltaBackward& b, void* workspace, void* stream);
+int launch_delta_step(const DeltaProblem& p, float* state, const Operand& out, void* stream);
+
 // Norm and rotation of query and key heads (qk_norm_kernels.cu).
 struct QkNormProblem {
   int64_t B, N, Hq, Hk;

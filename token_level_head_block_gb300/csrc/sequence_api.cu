@@ -1,4 +1,4 @@
-// extern "C" entry points of the gated recurrence and of the query/key norm
+// extern "C" entry points of the gated recurrence, of the gated delta rule and of the query/key norm
 // with rotation: argument checks, workspace handling, launches.  Every check
 // runs on the host before anything is queued on the stream.
 #include <cuda_runtime.h>
@@ -195,6 +195,147 @@ extern "C" mhla_status_t mhla_gated_step(const mhla_tensor_t* q, const mhla_tens
   for (const mhla_tensor_t* t : in)
     if (meets(t, state, sb)) return MHLA_ERR_INVALID_ARG;
   return static_cast<mhla_status_t>(launch_gated_step(gated_problem(q, k, v, g, scale), state, operand(out), stream));
+}
+
+// ----------------------------------------------------------------- delta rule
+
+namespace mhla {
+namespace {
+
+// [B, N, H, d] of the values beside [B, N, Hk, d] of the keys.
+bool value_shape(const mhla_tensor_t* q, const mhla_tensor_t* v) {
+  return q->B == v->B && q->N == v->N && q->d == v->d && q->dtype == v->dtype &&
+         (q->H == 0 ? v->H == 0 : v->H % q->H == 0);
+}
+
+DeltaProblem delta_problem(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v, const mhla_tensor_t* g,
+                           const mhla_tensor_t* beta, float scale) {
+  DeltaProblem p = {};
+  p.B = v->B; p.N = v->N; p.H = v->H; p.Hk = q->H; p.d = static_cast<int32_t>(v->d);
+  p.dtype = v->dtype;
+  p.scale = scale;
+  p.q = operand(q); p.k = operand(k); p.v = operand(v); p.g = operand(g); p.beta = operand(beta);
+  return p;
+}
+
+// Each CTA owns a chunk of a (b, h): their number fits a 31-bit grid axis.
+bool delta_fits(const mhla_tensor_t* v) {
+  const int64_t heads = v->B > (int64_t{1} << 24) || v->H > (int64_t{1} << 24) ? int64_t{1} << 25 : v->B * v->H;
+  return heads <= (int64_t{1} << 24) && v->N <= (int64_t{1} << 36) &&
+         heads * ((v->N + 31) / 32) < (int64_t{1} << 31);   // the shorter of both types' chunks
+}
+
+int check_delta(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v, const mhla_tensor_t* g,
+                const mhla_tensor_t* beta, float scale) {
+  for (const mhla_tensor_t* t : {q, k, v, g, beta}) {
+    const int rc = check_elements(t);
+    if (rc != MHLA_OK) return rc;
+  }
+  if (!same_shape(q, k) || !value_shape(q, v) || !gate_shape(v, g) || !gate_shape(v, beta)) return MHLA_ERR_SHAPE;
+  if (!std::isfinite(scale)) return MHLA_ERR_INVALID_ARG;
+  return delta_fits(v) ? MHLA_OK : MHLA_ERR_UNSUPPORTED;
+}
+
+template <typename Bytes>
+int delta_size(const mhla_tensor_t* q, const mhla_tensor_t* v, size_t* bytes, Bytes need) {
+  if (!bytes) return MHLA_ERR_INVALID_ARG;
+  for (const mhla_tensor_t* t : {q, v}) {
+    const int rc = check_tensor(t);
+    if (rc != MHLA_OK) return rc;
+  }
+  if (!value_shape(q, v)) return MHLA_ERR_SHAPE;
+  if (!delta_fits(v)) return MHLA_ERR_UNSUPPORTED;
+  *bytes = empty(v) ? 0 : need(delta_problem(q, q, v, v, v, 1.0f));
+  return MHLA_OK;
+}
+
+}  // namespace
+}  // namespace mhla
+
+extern "C" mhla_status_t mhla_delta_workspace_size(const mhla_tensor_t* q, const mhla_tensor_t* v, size_t* bytes) {
+  return static_cast<mhla_status_t>(delta_size(q, v, bytes, delta_workspace_bytes));
+}
+
+extern "C" mhla_status_t mhla_delta_backward_workspace_size(const mhla_tensor_t* q, const mhla_tensor_t* v, size_t* bytes) {
+  return static_cast<mhla_status_t>(delta_size(q, v, bytes, delta_bwd_workspace_bytes));
+}
+
+extern "C" mhla_status_t mhla_delta_forward(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v,
+                                            const mhla_tensor_t* g, const mhla_tensor_t* beta, float scale,
+                                            const float* state_in, const mhla_tensor_t* out, float* state_out,
+                                            void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_delta(q, k, v, g, beta, scale);
+  if (rc == MHLA_OK) rc = check_elements(out);
+  if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
+  if (!same_shape(v, out)) return MHLA_ERR_SHAPE;
+  if (empty(v)) return MHLA_OK;
+  const mhla_tensor_t* in[] = {q, k, v, g, beta};
+  const float* states[] = {state_in, state_out};
+  const int64_t sb = state_bytes(v);
+  if (!states_aligned({state_in, state_out})) return MHLA_ERR_INVALID_ARG;
+  rc = check_written(out, in, 5, states, 2, sb);
+  if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
+  for (const mhla_tensor_t* t : in)
+    if (meets(t, state_out, sb)) return MHLA_ERR_INVALID_ARG;
+  if (state_out != state_in && plain_overlap(state_in, state_out, sb)) return MHLA_ERR_INVALID_ARG;
+  const DeltaProblem p = delta_problem(q, k, v, g, beta, scale);
+  return static_cast<mhla_status_t>(
+      with_workspace(delta_workspace_bytes(p), workspace, workspace_bytes, stream, [&](void* ws) {
+        return launch_delta_forward(p, state_in, operand(out), state_out, ws, stream);
+      }));
+}
+
+extern "C" mhla_status_t mhla_delta_backward(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v,
+                                             const mhla_tensor_t* g, const mhla_tensor_t* beta, const mhla_tensor_t* dout,
+                                             float scale, const float* state_in, const float* dstate_out,
+                                             const mhla_tensor_t* dq, const mhla_tensor_t* dk, const mhla_tensor_t* dv,
+                                             const mhla_tensor_t* dg, const mhla_tensor_t* dbeta, float* dstate_in,
+                                             void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_delta(q, k, v, g, beta, scale);
+  for (const mhla_tensor_t* t : {dout, dq, dk, dv, dg, dbeta})
+    if (rc == MHLA_OK) rc = check_elements(t);
+  if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
+  if (!same_shape(v, dout) || !same_shape(v, dv) || !same_shape(q, dq) || !same_shape(q, dk) || !gate_shape(v, dg) ||
+      !gate_shape(v, dbeta))
+    return MHLA_ERR_SHAPE;
+  if (empty(v)) return MHLA_OK;
+  const mhla_tensor_t* all[] = {q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta};
+  constexpr int kInputs = 6, kAll = 11;
+  const float* states[] = {state_in, dstate_out, dstate_in};
+  const int64_t sb = state_bytes(v);
+  if (!states_aligned({state_in, dstate_out, dstate_in})) return MHLA_ERR_INVALID_ARG;
+  for (int i = kInputs; i < kAll; ++i) {
+    rc = check_written(all[i], all, i, states, 3, sb);
+    if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
+  }
+  for (int i = 0; i < kInputs; ++i)
+    if (meets(all[i], dstate_in, sb)) return MHLA_ERR_INVALID_ARG;
+  if (plain_overlap(dstate_in, state_in, sb) || plain_overlap(dstate_in, dstate_out, sb)) return MHLA_ERR_INVALID_ARG;
+  const DeltaProblem p = delta_problem(q, k, v, g, beta, scale);
+  const DeltaBackward b = {operand(dout), operand(dq), operand(dk), operand(dv), operand(dg), operand(dbeta), state_in,
+                           dstate_out, dstate_in};
+  return static_cast<mhla_status_t>(
+      with_workspace(delta_bwd_workspace_bytes(p), workspace, workspace_bytes, stream,
+                     [&](void* ws) { return launch_delta_backward(p, b, ws, stream); }));
+}
+
+extern "C" mhla_status_t mhla_delta_step(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v,
+                                         const mhla_tensor_t* g, const mhla_tensor_t* beta, float scale, float* state,
+                                         const mhla_tensor_t* out, void* stream) {
+  int rc = check_delta(q, k, v, g, beta, scale);
+  if (rc == MHLA_OK) rc = check_elements(out);
+  if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
+  if (!same_shape(v, out) || v->N != 1) return MHLA_ERR_SHAPE;
+  if (empty(v)) return MHLA_OK;
+  if (!state || !states_aligned({state})) return MHLA_ERR_INVALID_ARG;
+  const mhla_tensor_t* in[] = {q, k, v, g, beta};
+  const float* states[] = {state};
+  const int64_t sb = state_bytes(v);
+  rc = check_written(out, in, 5, states, 1, sb);
+  if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
+  for (const mhla_tensor_t* t : in)
+    if (meets(t, state, sb)) return MHLA_ERR_INVALID_ARG;
+  return static_cast<mhla_status_t>(launch_delta_step(delta_problem(q, k, v, g, beta, scale), state, operand(out), stream));
 }
 
 // ----------------------------------------------------------------- norm and rotation
