@@ -30,224 +30,268 @@ struct BackArgs {
   float* first;         // of the first one, or null
 };
 
-template <typename T, int DK, int NW>
+// A CTA walks the chunks backwards with 16 MT columns of the state's gradient, as delta_scan does forwards; the warps beside
+// the chain's form, a chunk ahead, what of it does not wait for the chain.
+template <typename T, int DK, int MT>
 struct BackLay {
   using L = Lay<T, DK>;
-  static constexpr int kThreads = 64 * NW, kWide = 16 * NW;   // columns of dout a CTA reads
-  static constexpr int kDoutPlane = L::C * kWide * 2;
-  static constexpr int kK = 0, kKeys = kK + L::kInput, kMarks = kKeys + L::kKeys, kStage = kMarks + L::kMarks;
-  static constexpr int kQ = 0, kScores = kQ + L::kInput, kDout = kScores + L::kScores, kMarksAhead = kDout + L::kIn * kDoutPlane;
-  static constexpr int kAhead = kMarksAhead + L::kMarks;
-  static constexpr int kHand = L::kState + L::kTokens;
-  static constexpr int kAheads = 2 * kStage, kHands = kAheads + 2 * kAhead, kBytes = kHands + 2 * NW * kHand;
+  static constexpr int kWarps = L::kTiles, kThreads = 64 * kWarps;
+  static constexpr int kShare = DK / 16 < kWarps ? 1 : DK / 16 / kWarps;   // blocks of the state's rows a warp
+  static constexpr int kK = 0, kKeys = kK + L::kSides * L::kIn * kBlock, kStage = kKeys + kShare * L::kTiles * kChain * kBlock;
+  static constexpr int kDout = 0, kScores = kDout + MT * L::kTiles * L::kIn * kBlock, kQ = kScores + L::kTiles * kChain * kBlock;
+  static constexpr int kAhead = kQ + kShare * L::kTiles * L::kIn * kBlock;
+  static constexpr int kHand = MT * (2 + 2 * kShare) * kBlock;           // a warp's part of P^T do and Q^T do
+  static constexpr int kStatePlane = 16 * MT * DK * 2, kTokenPlane = 16 * MT * L::C * 2;
+  static constexpr int kState = 0, kW = kState + kChain * kStatePlane, kHands = kW + kChain * kTokenPlane;
+  static constexpr int kRing = kHands + 2 * kWarps * kHand, kRingAhead = kRing + kWarps * kStage;
+  static constexpr int kBytes = kRingAhead + kWarps * kAhead;
 };
 
-template <typename T, int DK, int NW>
-__global__ void __launch_bounds__(BackLay<T, DK, NW>::kThreads) delta_back(const __grid_constant__ BackArgs a) {
-  using W = BackLay<T, DK, NW>;
+template <typename T, int DK, int MT>
+__global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const __grid_constant__ BackArgs a) {
+  using W = BackLay<T, DK, MT>;
   using L = Lay<T, DK>;
-  constexpr int C = L::C, NT = C / 8, NS = DK / 8, THREADS = W::kThreads, WIDE = W::kWide;
+  constexpr int C = L::C, TILES = L::kTiles, SIDES = L::kSides, SHARE = W::kShare;
   extern __shared__ __align__(128) char smem[];
   const Common& p = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = (p.d + WIDE - 1) / WIDE;
+  const int groups = (p.d + 16 * MT - 1) / (16 * MT);
   const int64_t bh = blockIdx.x / groups, b = bh / p.H, h = bh % p.H, key = b * p.Hk + h / (p.H / p.Hk);
-  const int tile0 = static_cast<int>(blockIdx.x % groups) * NW;
+  const int tile0 = static_cast<int>(blockIdx.x % groups) * MT;
   const uint32_t base = ptx::smem_u32(smem);
   const int count = static_cast<int>(p.chunks);
-  const int own = warp % NW, tile = tile0 + own, c0 = 16 * tile + (lane >> 2);
-  const bool chain = warp < NW;
-  auto chunk_of = [&](int i) { return count - 1 - i; };
+  const int own = warp % TILES;
+  const bool chain = warp < TILES, has_share = own * SHARE < SIDES;
+  const int g = lane >> 2, t = 2 * (lane & 3);
+  auto chunk_of = [&](int i) { return bh * p.chunks + (count - 1 - i); };
+  auto key_chunk_of = [&](int i) { return key * p.chunks + (count - 1 - i); };
+  auto marks = [&](int i) { return reinterpret_cast<const typename L::M*>(p.im.marks + chunk_of(i) * L::kMarks); };
 
-  auto load = [&](int i) {
-    const uint32_t st = base + (i & 1) * W::kStage;
-    const int64_t at = bh * p.chunks + chunk_of(i);
-    copy_async(st + W::kK, p.im.k + (key * p.chunks + chunk_of(i)) * L::kInput, L::kInput, threadIdx.x, THREADS);
-    copy_async(st + W::kKeys, p.im.keys + at * L::kKeys, L::kKeys, threadIdx.x, THREADS);
-    copy_async(st + W::kMarks, p.im.marks + at * L::kMarks, L::kMarks, threadIdx.x, THREADS);
+  // each lane's own blocks, asked for as in delta_scan
+  const uint32_t ring = base + (chain ? W::kRing + own * W::kStage : W::kRingAhead + own * W::kAhead);
+  const char* st = smem + (ring - base);
+  auto load_first = [&](int i) {
+    if (i < count) copy_blocks<SIDES * L::kIn>(ring + W::kK, p.im.k_rows + key_chunk_of(i) * L::kInput + own * SIDES * L::kIn * kBlock, lane);
+    commit();
+  };
+  auto load_second = [&](int i) {
+    if (i < count && has_share)
+      copy_blocks<SHARE * TILES * kChain>(ring + W::kKeys, p.im.keys_add + chunk_of(i) * L::kKeys + own * SHARE * TILES * kChain * kBlock, lane);
+    commit();
   };
   auto load_ahead = [&](int i) {
-    const uint32_t st = base + W::kAheads + (i & 1) * W::kAhead;
-    const int64_t at = bh * p.chunks + chunk_of(i);
-    copy_async(st + W::kQ, p.im.q + (key * p.chunks + chunk_of(i)) * L::kInput, L::kInput, threadIdx.x, THREADS);
-    copy_async(st + W::kScores, p.im.scores + at * L::kScores, L::kScores, threadIdx.x, THREADS);
-    copy_async(st + W::kMarksAhead, p.im.marks + at * L::kMarks, L::kMarks, threadIdx.x, THREADS);
-    const char* src = p.im.dout + at * L::kInput;
-    constexpr int kUnits = WIDE / 8;
-    for (int j = threadIdx.x; j < L::kIn * C * kUnits; j += THREADS) {
-      const int n = j / (C * kUnits), r = j / kUnits % C, u = j % kUnits;
-      cp_async_16(st + W::kDout + n * W::kDoutPlane + unit_at<WIDE>(r, u), src + n * L::kRows + unit_at<DK>(r, 2 * tile0 + u), 16);
+    if (i < count) {
+      copy_blocks<MT * TILES * L::kIn>(ring + W::kDout, p.im.dout_cols + chunk_of(i) * L::kInput + tile0 * TILES * L::kIn * kBlock, lane);
+#pragma unroll
+      for (int ks = 0; ks < TILES; ++ks)
+        if (ks >= own)
+          copy_blocks<kChain>(ring + W::kScores + ks * kChain * kBlock,
+                              p.im.scores_back + chunk_of(i) * L::kScoresBack + (own * TILES + ks) * kChain * kBlock, lane);
+      if (has_share)
+        copy_blocks<SHARE * TILES * L::kIn>(ring + W::kQ, p.im.q_add + key_chunk_of(i) * L::kInput + own * SHARE * TILES * L::kIn * kBlock, lane);
     }
-  };
-  load_ahead(0);
-  commit();
-
-  // D^T: rows c0, c0 + 8 (columns of the state)
-  float D[NS][4];
-  if (chain) {
-    const float* in = a.last ? a.last + bh * p.d * p.d : nullptr;
-#pragma unroll
-    for (int n = 0; n < NS; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = 8 * n + 2 * (lane & 3) + (e & 1), c = c0 + 8 * (e >> 1);
-        D[n][e] = in && r < p.d && c < p.d ? in[static_cast<int64_t>(r) * p.d + c] : 0.0f;
-      }
-  }
-
-  for (int i = 0; i <= count; ++i) {
-    wait_all();
-    __syncthreads();
-    if (i + 1 < count) load_ahead(i + 1);
-    if (i < count) load(i);
     commit();
-    if (!chain) {
-      if (i >= count) continue;
-      // (P^T do)^T and ((scale e^b Q)^T do)^T
-      const char* stage = smem + W::kAheads + (i & 1) * W::kAhead;
-      const uint32_t st = base + W::kAheads + (i & 1) * W::kAhead;
-      const auto& m = *reinterpret_cast<const typename L::M*>(stage + W::kMarksAhead);
-      char* hand = smem + W::kHands + ((i & 1) * NW + own) * W::kHand;
-      float4 *to_x = reinterpret_cast<float4*>(hand) + lane, *to_y = reinterpret_cast<float4*>(hand + L::kState) + lane;
-      {
-        Accumulators<NT, L::kApart> acc;
-        acc.clear();
+  };
+  // (P^T do)^T of this warp's 16 tokens and ((scale e^b Q)^T do)^T of its share of the state's rows
+  auto ahead = [&](int i) {
+    float4* hand = reinterpret_cast<float4*>(smem + W::kHands + ((i & 1) * TILES + own) * W::kHand) + lane;
+    const auto* m = marks(i);
 #pragma unroll
-        for (int ks = 0; ks < C / 16; ++ks) {
-          uint32_t o[L::kIn][4];
+    for (int n = 0; n < MT; ++n) {
+      Accumulators<2, true> y;
+      Accumulators<2 * SHARE, true> x;
+      y.clear();
+      x.clear();
 #pragma unroll
-          for (int n = 0; n < L::kIn; ++n) a_cols<WIDE>(o[n], st + W::kDout + n * W::kDoutPlane, 16 * own, 16 * ks, lane);
+      for (int ks = 0; ks < TILES; ++ks) {
+        uint32_t o[L::kIn][4];
+        float f[4][2];
 #pragma unroll
-          for (int s = 0; s <= ks; ++s) {
-            uint32_t x[L::kScore][1][4];
-#pragma unroll
-            for (int n = 0; n < L::kScore; ++n) b_cols<C>(x[n][0], st + W::kScores + n * L::kSquare, 16 * s, 16 * ks, lane);
-            mma_terms(acc, 2 * s, o, x);
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) to_y[32 * n] = make_float4(acc.get(n, 0), acc.get(n, 1), acc.get(n, 2), acc.get(n, 3));
-      }
-      uint32_t oa[C / 16][L::kOwn][4];
-#pragma unroll
-      for (int ks = 0; ks < C / 16; ++ks) {
-        float x[4][2];
-#pragma unroll
-        for (int n = 0; n < L::kIn; ++n) {
-          uint32_t o[4];
-          a_cols<WIDE>(o, st + W::kDout + n * W::kDoutPlane, 16 * own, 16 * ks, lane);
+        for (int k = 0; k < L::kIn; ++k) {
+          load_block(o[k], st + W::kDout, (n * TILES + ks) * L::kIn + k, lane);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[e][0] = n == 0 ? low(o[e]) : x[e][0] + low(o[e]);
-            x[e][1] = n == 0 ? high(o[e]) : x[e][1] + high(o[e]);
+            f[e][0] = k == 0 ? low(o[k][e]) : f[e][0] + low(o[k][e]);
+            f[e][1] = k == 0 ? high(o[k][e]) : f[e][1] + high(o[k][e]);
+          }
+        }
+        if (ks >= own) {
+          uint32_t s[kChain][1][4];
+#pragma unroll
+          for (int k = 0; k < kChain; ++k) load_block(s[k][0], st + W::kScores, ks * kChain + k, lane);
+          mma_terms(y, 0, o, s);
+        }
+        if (has_share) {
+          uint32_t oa[kChain][4], q[L::kIn][SHARE][4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 in = *reinterpret_cast<const float2*>(m->inside + 16 * ks + 8 * (e >> 1) + t);
+            uint32_t z[kChain];
+            split<kChain>(f[e][0] * (p.scale * in.x), f[e][1] * (p.scale * in.y), z);
+#pragma unroll
+            for (int k = 0; k < kChain; ++k) oa[k][e] = z[k];
+          }
+#pragma unroll
+          for (int k = 0; k < L::kIn; ++k)
+#pragma unroll
+            for (int j = 0; j < SHARE; ++j) load_block(q[k][j], st + W::kQ, (j * TILES + ks) * L::kIn + k, lane);
+          mma_terms(x, 0, oa, q);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        hand[32 * (n * (2 + 2 * SHARE) + j)] = make_float4(y.get(j, 0), y.get(j, 1), y.get(j, 2), y.get(j, 3));
+#pragma unroll
+      for (int j = 0; j < 2 * SHARE; ++j)
+        hand[32 * (n * (2 + 2 * SHARE) + 2 + j)] = make_float4(x.get(j, 0), x.get(j, 1), x.get(j, 2), x.get(j, 3));
+    }
+  };
+
+  if (chain) {
+    load_first(0);
+    load_second(0);
+  } else {
+    load_ahead(0);
+  }
+  // D^T as delta_scan holds S^T
+  float D[MT][2 * SHARE][4];
+  const bool shares = chain && has_share;
+  auto publish = [&]() {
+#pragma unroll
+    for (int n = 0; n < MT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2 * SHARE; ++j)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          uint32_t x[kChain];
+          split<kChain>(D[n][j][2 * f], D[n][j][2 * f + 1], x);
+#pragma unroll
+          for (int k = 0; k < kChain; ++k)
+            *reinterpret_cast<uint32_t*>(smem + W::kState + k * W::kStatePlane + unit_at<DK>(16 * n + g + 8 * f, 2 * own * SHARE + j) + 2 * t) = x[k];
+        }
+  };
+  if (shares) {
+    const float* in = a.last ? a.last + bh * p.d * p.d : nullptr;
+#pragma unroll
+    for (int n = 0; n < MT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2 * SHARE; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 16 * own * SHARE + 8 * j + t + (e & 1), c = 16 * (tile0 + n) + g + 8 * (e >> 1);
+          D[n][j][e] = in && r < p.d && c < p.d ? in[static_cast<int64_t>(r) * p.d + c] : 0.0f;
+        }
+    publish();
+  }
+  if (!chain) {
+    wait_all();
+    ahead(0);
+    load_ahead(1);
+  }
+
+  for (int i = 0; i < count; ++i) {
+    if (chain) {
+      wait_older();
+      const float4* hand = reinterpret_cast<const float4*>(smem + W::kHands + ((i & 1) * TILES + own) * W::kHand) + lane;
+      const auto* m = marks(i);
+      const float2 after[2] = {*reinterpret_cast<const float2*>(m->after + 16 * own + t),
+                               *reinterpret_cast<const float2*>(m->after + 16 * own + 8 + t)};
+      const float total = m->total;
+      __syncthreads();   // the planes of D and the parts formed ahead are there
+      Accumulators<2, true> acc[MT];
+#pragma unroll
+      for (int n = 0; n < MT; ++n) acc[n].clear();
+#pragma unroll
+      for (int ks = 0; ks < SIDES; ++ks) {
+        uint32_t x[L::kIn][1][4];
+#pragma unroll
+        for (int k = 0; k < L::kIn; ++k) load_block(x[k][0], st + W::kK, ks * L::kIn + k, lane);
+#pragma unroll
+        for (int n = 0; n < MT; ++n) {
+          uint32_t s[kChain][4];
+#pragma unroll
+          for (int k = 0; k < kChain; ++k) a_rows<DK>(s[k], base + W::kState + k * W::kStatePlane, 16 * n, 16 * ks, lane);
+          mma_terms(acc[n], 0, s, x);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < MT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float4 y = hand[32 * (n * (2 + 2 * SHARE) + j)];
+          const float w[4] = {fmaf(after[j].x, acc[n].get(j, 0), y.x), fmaf(after[j].y, acc[n].get(j, 1), y.y),
+                              fmaf(after[j].x, acc[n].get(j, 2), y.z), fmaf(after[j].y, acc[n].get(j, 3), y.w)};
+          if (16 * (tile0 + n) < p.d)
+            *reinterpret_cast<float4*>(p.im.dw + (chunk_of(i) * SIDES + tile0 + n) * L::kTokens + (2 * own + j) * kBlock + 16 * lane) =
+                make_float4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            uint32_t x[kChain];
+            split<kChain>(w[2 * f], w[2 * f + 1], x);
+#pragma unroll
+            for (int k = 0; k < kChain; ++k)
+              *reinterpret_cast<uint32_t*>(smem + W::kW + k * W::kTokenPlane + unit_at<C>(16 * n + g + 8 * f, 2 * own + j) + 2 * t) = x[k];
+          }
+        }
+      load_first(i + 1);
+      __syncthreads();   // the planes of dW are there, those of D are read
+      wait_older();
+      if (shares) {
+        // D^T <- e^B D^T + (Q^T do)^T - dW^T K^, the chunk's part formed apart
+        Accumulators<2 * SHARE, true> sum[MT];
+#pragma unroll
+        for (int n = 0; n < MT; ++n) sum[n].clear();
+#pragma unroll
+        for (int ks = 0; ks < TILES; ++ks) {
+          uint32_t x[kChain][SHARE][4];
+#pragma unroll
+          for (int k = 0; k < kChain; ++k)
+#pragma unroll
+            for (int j = 0; j < SHARE; ++j) load_block(x[k][j], st + W::kKeys, (j * TILES + ks) * kChain + k, lane);
+#pragma unroll
+          for (int n = 0; n < MT; ++n) {
+            uint32_t w[kChain][4];
+#pragma unroll
+            for (int k = 0; k < kChain; ++k) a_rows<C>(w[k], base + W::kW + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
+            mma_terms(sum[n], 0, w, x);
           }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = *reinterpret_cast<const float2*>(m.inside + 16 * ks + 8 * (e >> 1) + 2 * (lane & 3));
-          uint32_t t[L::kOwn];
-          split<L::kOwn>(x[e][0] * (p.scale * f.x), x[e][1] * (p.scale * f.y), t);
+        for (int n = 0; n < MT; ++n)
 #pragma unroll
-          for (int n = 0; n < L::kOwn; ++n) oa[ks][n][e] = t[n];
-        }
+          for (int j = 0; j < 2 * SHARE; ++j) {
+            if (16 * (tile0 + n) < p.d)
+              *reinterpret_cast<float4*>(p.im.ds + (chunk_of(i) * SIDES + tile0 + n) * L::kState + (2 * own * SHARE + j) * kBlock + 16 * lane) =
+                  make_float4(D[n][j][0], D[n][j][1], D[n][j][2], D[n][j][3]);
+            const float4 x = hand[32 * (n * (2 + 2 * SHARE) + 2 + j)];
+            const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) D[n][j][e] = fmaf(total, D[n][j][e], xs[e] - sum[n].get(j, e));
+          }
+        publish();
       }
-      constexpr int G = 2;
-#pragma unroll
-      for (int n0 = 0; n0 < NS; n0 += 2 * G) {
-        Accumulators<2 * G, L::kApart> acc;
-        acc.clear();
-#pragma unroll
-        for (int ks = 0; ks < C / 16; ++ks) {
-          uint32_t x[L::kIn][G][4];
-#pragma unroll
-          for (int n = 0; n < L::kIn; ++n)
-#pragma unroll
-            for (int j = 0; j < G; ++j) b_cols<DK>(x[n][j], st + W::kQ + n * L::kRows, 8 * n0 + 16 * j, 16 * ks, lane);
-          mma_terms(acc, 0, oa[ks], x);
-        }
-#pragma unroll
-        for (int n = 0; n < 2 * G; ++n)
-          to_x[32 * (n0 + n)] = make_float4(acc.get(n, 0), acc.get(n, 1), acc.get(n, 2), acc.get(n, 3));
+      load_second(i + 1);
+    } else {
+      __syncthreads();
+      if (i + 1 < count) {
+        wait_all();
+        ahead(i + 1);
+        load_ahead(i + 2);
       }
-    } else if (i > 0) {
-      const int now = i - 1;
-      const char* stage = smem + (now & 1) * W::kStage;
-      const uint32_t st = base + (now & 1) * W::kStage;
-      const auto& m = *reinterpret_cast<const typename L::M*>(stage + W::kMarks);
-      const char* hand = smem + W::kHands + ((now & 1) * NW + own) * W::kHand;
-      const float4 *of_x = reinterpret_cast<const float4*>(hand) + lane,
-                   *of_y = reinterpret_cast<const float4*>(hand + L::kState) + lane;
-      const int64_t at = (bh * p.chunks + chunk_of(now)) * (DK / 16) + tile;
-      const bool in = 16 * tile < p.d;
-      if (in) {
-        float4* to = reinterpret_cast<float4*>(p.im.ds + at * L::kState) + lane;
-#pragma unroll
-        for (int n = 0; n < NS; ++n) to[32 * n] = make_float4(D[n][0], D[n][1], D[n][2], D[n][3]);
-      }
-      // dW^T = (P^T do)^T + D^T (e^{B-b} K)^T
-      Accumulators<NT, L::kApart> acc;
-      acc.clear();
-#pragma unroll
-      for (int ks = 0; ks < DK / 16; ++ks) {
-        uint32_t s[L::kOwn][4], x[L::kIn][NT / 2][4];
-        as_rows<L::kOwn>(s, D[2 * ks], D[2 * ks + 1]);
-#pragma unroll
-        for (int n = 0; n < L::kIn; ++n)
-#pragma unroll
-          for (int j = 0; j < NT / 2; ++j) b_rows<DK>(x[n][j], st + W::kK + n * L::kRows, 16 * j, 16 * ks, lane);
-        mma_terms(acc, 0, s, x);
-      }
-      float w[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float4 y = of_y[32 * n];
-        const float2 f = *reinterpret_cast<const float2*>(m.after + 8 * n + 2 * (lane & 3));
-        w[n][0] = fmaf(f.x, acc.get(n, 0), y.x); w[n][1] = fmaf(f.y, acc.get(n, 1), y.y);
-        w[n][2] = fmaf(f.x, acc.get(n, 2), y.z); w[n][3] = fmaf(f.y, acc.get(n, 3), y.w);
-      }
-      if (in) {
-        float4* to = reinterpret_cast<float4*>(p.im.dw + at * L::kTokens) + lane;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) to[32 * n] = make_float4(w[n][0], w[n][1], w[n][2], w[n][3]);
-      }
-      // D^T <- e^B D^T + (Q^T do)^T - dW^T K^, the chunk's part formed apart
-      uint32_t wa[C / 16][L::kOwn][4];
-#pragma unroll
-      for (int ks = 0; ks < C / 16; ++ks) as_rows<L::kOwn>(wa[ks], w[2 * ks], w[2 * ks + 1]);
-      const float total = m.total;
-      constexpr int G = DK / 16 < 4 ? DK / 16 : 4;
-#pragma unroll
-      for (int n0 = 0; n0 < NS; n0 += 2 * G) {
-        Accumulators<2 * G, L::kApart> sum;
-        sum.clear();
-#pragma unroll
-        for (int ks = 0; ks < C / 16; ++ks) {
-          uint32_t x[L::kOwn][G][4];
-#pragma unroll
-          for (int n = 0; n < L::kOwn; ++n)
-#pragma unroll
-            for (int j = 0; j < G; ++j) b_cols<DK>(x[n][j], st + W::kKeys + n * L::kRows, 8 * n0 + 16 * j, 16 * ks, lane);
-          mma_terms(sum, 0, wa[ks], x);
-        }
-#pragma unroll
-        for (int n = 0; n < 2 * G; ++n) {
-          const float4 x = of_x[32 * (n0 + n)];
-          const float xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) D[n0 + n][e] = fmaf(total, D[n0 + n][e], xs[e] - sum.get(n, e));
-        }
-      }
+      __syncthreads();
     }
   }
-  if (chain && a.first) {
+  if (shares && a.first) {
     float* first = a.first + bh * p.d * p.d;
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
+    for (int n = 0; n < MT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = 8 * n + 2 * (lane & 3) + (e & 1), c = c0 + 8 * (e >> 1);
-        if (r < p.d && c < p.d) first[static_cast<int64_t>(r) * p.d + c] = D[n][e];
-      }
+      for (int j = 0; j < 2 * SHARE; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 16 * own * SHARE + 8 * j + t + (e & 1), c = 16 * (tile0 + n) + g + 8 * (e >> 1);
+          if (r < p.d && c < p.d) first[static_cast<int64_t>(r) * p.d + c] = D[n][j][e];
+        }
   }
 }
 
@@ -685,16 +729,15 @@ __global__ void __launch_bounds__(256) delta_shared(const __grid_constant__ Shar
   }
 }
 
-template <typename T, int DK>
+template <typename T, int DK, int MT>
 int back_as(const BackArgs& a, int64_t BH, cudaStream_t s) {
-  constexpr int NW = 2;
-  using W = BackLay<T, DK, NW>;
+  using W = BackLay<T, DK, MT>;
   static_assert(W::kBytes <= 227 * 1024, "shared memory");
-  if (cudaFuncSetAttribute(delta_back<T, DK, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kBytes) != cudaSuccess)
+  if (cudaFuncSetAttribute(delta_back<T, DK, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kBytes) != cudaSuccess)
     return MHLA_ERR_CUDA;
-  const int groups = (a.c.d + 16 * NW - 1) / (16 * NW);
+  const int groups = (a.c.d + 16 * MT - 1) / (16 * MT);
   KernelTimer timer("delta_back", s);
-  delta_back<T, DK, NW><<<static_cast<unsigned>(BH * groups), W::kThreads, W::kBytes, s>>>(a);
+  delta_back<T, DK, MT><<<static_cast<unsigned>(BH * groups), W::kThreads, W::kBytes, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
 
@@ -711,7 +754,7 @@ int grads_as(const GradArgs& a, int64_t BH, cudaStream_t s) {
 
 template <typename T, int DK>
 int run_as(const BackArgs& b, const GradArgs& g, int64_t BH, bool shared, cudaStream_t s) {
-  const int rc = back_as<T, DK>(b, BH, s);
+  const int rc = two_tiles(BH, b.c.d) ? back_as<T, DK, 2>(b, BH, s) : back_as<T, DK, 1>(b, BH, s);
   if (rc != MHLA_OK) return rc;
   return shared && sizeof(T) == 2 ? grads_as<T, DK, float>(g, BH, s) : grads_as<T, DK, T>(g, BH, s);
 }

@@ -17,9 +17,9 @@ namespace delta {
 
 using namespace gated;
 
-// Terms of bf16 that a value enters the tensor cores with: an input, a value formed on the way (two leave
-// 2^-16, under the error that the float32 state is allowed; three 2^-24), and a score, which only feeds an output: with
-// bf16 outputs its own rounding (2^-9) stays under theirs.
+// Terms of bf16 that a value enters the tensor cores with: an input; a value that reaches the float32 state (kChain,
+// 2^-24); a value that reaches outputs alone (kOwn: two leave 2^-16 with bf16 outputs); and a score of the forward pass, whose one
+// rounding (2^-8) stays beside that of bf16 outputs.
 // Tokens a chunk: three planes of float32 rows of 128 channels leave room for 32.
 template <typename T>
 struct Form;
@@ -31,6 +31,7 @@ template <>
 struct Form<float> {
   static constexpr int kIn = 3, kOwn = 3, kScore = 3, kChunk = 32;
 };
+constexpr int kChain = 3;
 
 // A chunk's values a token, then whether any is not finite and each column's first such token.
 template <int C, int DK>
@@ -44,28 +45,41 @@ struct Marks {
   int32_t first[DK];
 };
 
+// One 16 x 16 block of an operand as the 32 lanes hold it, 16 bytes a lane.  What one kernel forms the next takes block by
+// block, each lane its own bytes, with no shuffling in between.
+constexpr int kBlock = 512;
+
 template <typename T, int DK>
 struct Lay {
   static constexpr int C = Form<T>::kChunk, kIn = Form<T>::kIn, kOwn = Form<T>::kOwn, kScore = Form<T>::kScore;
+  static constexpr int kTiles = C / 16, kSides = DK / 16;          // blocks of a chunk's tokens, of the channels
   static constexpr bool kApart = kIn > 1;
   static constexpr int kRows = C * DK * 2, kSquare = C * C * 2;   // bytes of a plane
-  static constexpr int kInput = kIn * kRows, kKeys = kOwn * kRows, kScores = kScore * kSquare, kInverse = kOwn * kSquare;
-  static constexpr int kTokens = C / 8 * 512, kState = DK / 8 * 512;   // bytes of a warp's 16 columns, float32 fragments
+  static constexpr int kInput = kIn * kRows, kKeys = kChain * kRows, kInverse = kOwn * kSquare;
+  static constexpr int kScores = kScore * kSquare, kScoresBack = kChain * kSquare;
+  static constexpr int kTokens = C / 8 * kBlock, kState = DK / 8 * kBlock;   // of 16 columns, float32 fragments
   using M = Marks<C, DK>;
   static constexpr int kMarks = sizeof(M);
   static_assert(kMarks % 16 == 0, "copied in 16-byte units");
 };
 
-// Where a call's images lie.  Those of key heads [B][Hk][chunks], the others [B][H][chunks]; fragments of
-// tokens [DK / 16][C / 8][32] and of states [DK / 16][DK / 8][32], 16 columns of the values apart.
+// Where a call's images lie, of every chunk [B][Hk][chunks] (inputs of key heads) or [B][H][chunks].  Blocks of an operand with
+// its terms side by side; k runs fastest, after the terms.  tok: blocks of tokens, ch: of channels.
 struct Images {
-  char *k, *q;          // planes of rows
-  char* keys;           // T beta e^b K
-  char* scores;         // scale tril(Q K^T . decay)
-  char* u;              // fragments of (T beta V)^T
+  char* k_add;          // K as [k = tok][n = ch], blocks [ch][tok]
+  char* q_rows;         // Q as [m = tok][k = ch], blocks [tok][ch]
+  char* keys;           // T beta e^b K as [n = tok][k = ch], blocks [tok][ch]
+  char* scores;         // scale tril(Q K^T . decay) as [m = tok][k = tok], blocks [tok][tok]
+  char* u;              // (T beta V)^T, float32 fragments [ch][C / 8][32]
   char* marks;
-  char *inverse, *dout; // gradients: T, planes of rows of dout
-  char *s, *w;          // gradients: the state entering the chunk and what its tokens write, fragments
+  // gradients
+  char *k, *q, *dout, *inverse;   // planes of rows; T
+  char* k_rows;         // K as [n = tok][k = ch], blocks [tok][ch]
+  char* keys_add;       // T beta e^b K as [k = tok][n = ch], blocks [ch][tok]
+  char* q_add;          // Q as [k = tok][n = ch], blocks [ch][tok]
+  char* scores_back;    // the scores as [k = tok][n = tok], blocks [n][k]
+  char* dout_cols;      // dout^T as [m = ch][k = tok], blocks [ch][tok]
+  char *s, *w;          // the state entering the chunk and what its tokens write, float32 fragments
   char *ds, *dw;        // gradients: of the state leaving the chunk and of w
 };
 
@@ -107,7 +121,24 @@ __device__ __forceinline__ void as_rows(uint32_t (&a)[NT][4], const float (&lo)[
 __device__ __forceinline__ void copy_async(uint32_t dst, const char* src, int bytes, int thread, int threads) {
   for (int i = 16 * thread; i < bytes; i += 16 * threads) cp_async_16(dst + i, src + i, 16);
 }
+// N blocks, each lane its own bytes: no other lane's copies are waited for.
+template <int N>
+__device__ __forceinline__ void copy_blocks(uint32_t dst, const char* src, int lane) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) cp_async_16(dst + i * kBlock + 16 * lane, src + i * kBlock + 16 * lane, 16);
+}
+__device__ __forceinline__ void load_block(uint32_t (&r)[4], const char* smem, int block, int lane) {
+  const uint4 x = *reinterpret_cast<const uint4*>(smem + block * kBlock + 16 * lane);
+  r[0] = x.x; r[1] = x.y; r[2] = x.z; r[3] = x.w;
+}
+// The transpose of an 8 x 8 tile, a pair of its row a lane.
+__device__ __forceinline__ uint32_t turn(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void wait_older() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }   // all but the last group
 __device__ __forceinline__ void wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 template <typename T>
@@ -138,6 +169,8 @@ int launch_prepare(const Common& c, int64_t BH, int dtype, bool grad, cudaStream
 int launch_scan(const ScanArgs& a, int64_t BH, int dtype, bool keep, cudaStream_t s);
 size_t lay_out(const DeltaProblem& p, bool grad, char* base, Images* im);
 Common common(const DeltaProblem& p, const Operand* dout);
+// Whether a scan's CTA takes 32 columns of the state or 16: 16 where all of them run at once.
+bool two_tiles(int64_t BH, int d);
 bool pairs_fit(const Operand& o, int d, int dtype);
 
 }  // namespace delta

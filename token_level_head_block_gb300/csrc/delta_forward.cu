@@ -90,92 +90,96 @@ __device__ __forceinline__ void load_rows(char* dst, const T* src, int64_t sn, i
   }
 }
 
-template <typename T, int DK, bool GRAD>
+template <typename T, int DK>
 struct Prepare {
   using L = Lay<T, DK>;
-  static constexpr int C = L::C, kStrips = C / 16, kThreads = 64 * kStrips;
-  static constexpr int kPitch = C + 4, kHalf = C / 2 + 4;   // floats a row of T, of a product on the way
-  static constexpr int kSum = 0, kTmp = kSum + C * kPitch * 4, kK = (kTmp + C / 2 * kHalf * 4 + 127) / 128 * 128;
-  static constexpr int kV = kK + L::kInput, kQ = kV + L::kInput, kPlanes = kQ;   // T's planes where Q was
-  static constexpr int kBytes = std::max(kQ + L::kInput, kPlanes + 2 * L::kInverse);
+  static constexpr int C = L::C, kStrips = L::kTiles, kThreads = 64 * kStrips;
+  static constexpr int kPitch = C + 8;   // floats a row of T: a lane's pairs of eight rows meet all banks
+  static constexpr int kK = (C * kPitch * 4 + 127) / 128 * 128, kV = kK + L::kInput, kQ = kV + L::kInput, kBytes = kQ + L::kInput;
 };
 
-// T = (1 + L)^-1 of the strictly lower triangular L in place, float32: the diagonal blocks of 16 by columns, then
-// blocks of twice the size, T21 = -T22 L21 T11.  All threads.
-template <int C, int PITCH, int HALF, int THREADS>
-__device__ __forceinline__ void invert(float* L, float* tmp) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp < C / 16 && lane < 16) {
-    float* block = L + 16 * warp * (PITCH + 1);
-    float x[16];
+// Decays between the tokens of a chunk: D_ij = e^{b_i - b_j} = row_i col_j for j in front of i's block of 16, with
+// row_i = e^{b_i - m}, col_j = e^{m - b_j}, m the sum in front of the block; neither exceeds 1.
+template <int C>
+struct Decays {
+  float row[C], col[C / 16][C];
+  float key[C], value[C];   // beta e^b, beta: weights of T's columns
+};
+
+// A pair of T's columns c, c + 1 in row r.
+template <int PITCH>
+__device__ __forceinline__ float2 pair_at(const float* m, int r, int c) {
+  return *reinterpret_cast<const float2*>(m + r * PITCH + c);
+}
+
+// Blocks T_ij = -T_ii sum_{j <= m < i} L_im T_mj (j < i) from the inverses T_ii of the diagonal blocks, one warp a
+// block column j.  It works on the transposes, Z_i = -(sum Z_m L_im^T) T_ii^T, whose accumulators are the next product's A operand
+// as they are; float32 in three terms.
+template <int TILES, int PITCH>
+__device__ __forceinline__ void invert_column(const float* L, float (&Z)[TILES][2][4], int j, int lane) {
+  const int g = lane >> 2, t = 2 * (lane & 3);
+  uint32_t za[TILES][3][4];
+  auto turned = [&](int i, uint32_t (&b)[3][1][4], const float* at) {   // at [n][k] as a B operand
+    const float2 x[4] = {pair_at<PITCH>(at, g, t), pair_at<PITCH>(at, g, t + 8), pair_at<PITCH>(at, g + 8, t), pair_at<PITCH>(at, g + 8, t + 8)};
 #pragma unroll
-    for (int r = 0; r < 16; ++r) x[r] = r == lane ? 1.0f : 0.0f;
+    for (int e = 0; e < 4; ++e) {
+      uint32_t s[3];
+      split<3>(x[e].x, x[e].y, s);
 #pragma unroll
-    for (int j = 0; j < 15; ++j)
-#pragma unroll
-      for (int r = j + 1; r < 16; ++r) x[r] = fmaf(-block[r * PITCH + j], x[j], x[r]);
-    __syncwarp(0xFFFFu);
-#pragma unroll
-    for (int r = 0; r < 16; ++r) block[r * PITCH + lane] = x[r];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int H = 16; H < C; H *= 2) {
-    const int quads = H / 4, each = H * quads, n = C / (2 * H) * each;   // outputs in fours
-    for (int i = threadIdx.x; i < n; i += THREADS) {
-      const int pair = i / each, r = i % each / quads, c = 4 * (i % quads);
-      const float *a = L + (2 * H * pair + H + r) * PITCH + 2 * H * pair, *b = L + 2 * H * pair * (PITCH + 1) + c;
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-      for (int k = 0; k < H; ++k) {
-        const float x = a[k];
-        const float4 y = *reinterpret_cast<const float4*>(b + k * PITCH);
-        s.x = fmaf(x, y.x, s.x); s.y = fmaf(x, y.y, s.y); s.z = fmaf(x, y.z, s.z); s.w = fmaf(x, y.w, s.w);
-      }
-      *reinterpret_cast<float4*>(tmp + (H * pair + r) * HALF + c) = s;
+      for (int n = 0; n < 3; ++n) b[n][0][e] = s[n];
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += THREADS) {
-      const int pair = i / each, r = i % each / quads, c = 4 * (i % quads);
-      const float *a = L + (2 * H * pair + H + r) * PITCH + 2 * H * pair + H, *b = tmp + H * pair * HALF + c;
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-      for (int k = 0; k < H; ++k) {
-        const float x = a[k];
-        const float4 y = *reinterpret_cast<const float4*>(b + k * HALF);
-        s.x = fmaf(-x, y.x, s.x); s.y = fmaf(-x, y.y, s.y); s.z = fmaf(-x, y.z, s.z); s.w = fmaf(-x, y.w, s.w);
+  };
+#pragma unroll
+  for (int i = 0; i < TILES; ++i) {
+    if (i < j) continue;
+    const float* diagonal = L + 16 * i * (PITCH + 1);
+    if (i == j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = g + 8 * (e & 1), k = t + 8 * (e >> 1);
+        uint32_t s[3];
+        split<3>(diagonal[k * PITCH + r], diagonal[(k + 1) * PITCH + r], s);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) za[i][n][e] = s[n];
       }
-      *reinterpret_cast<float4*>(L + (2 * H * pair + H + r) * PITCH + 2 * H * pair + c) = s;
+      continue;
     }
-    __syncthreads();
+    Accumulators<2, true> acc;
+    acc.clear();
+    uint32_t b[3][1][4];
+#pragma unroll
+    for (int m = 0; m < TILES; ++m) {
+      if (m < j || m >= i) continue;
+      turned(i, b, L + 16 * i * PITCH + 16 * m);
+      mma_terms(acc, 0, za[m], b);
+    }
+    float x[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[n][e] = -acc.get(n, e);
+    uint32_t xa[3][4];
+    as_rows<3>(xa, x[0], x[1]);
+    turned(i, b, diagonal);
+    acc.clear();
+    mma_terms(acc, 0, xa, b);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) Z[i][n][e] = acc.get(n, e);
+    as_rows<3>(za[i], Z[i][0], Z[i][1]);
   }
 }
 
-// T with its columns weighed, as planes of terms, lower blocks of 16.
-template <typename T, int DK, typename Weight>
-__device__ __forceinline__ void put_inverse(char* dst, const float* inv, int pitch, int threads, Weight weight) {
-  using L = Lay<T, DK>;
-  constexpr int C = L::C;
-  for (int i = threadIdx.x; i < C * C / 2; i += threads) {
-    const int r = i / (C / 2), c = 2 * (i % (C / 2));
-    if (c > (r | 15)) continue;
-    const float2 x = *reinterpret_cast<const float2*>(inv + r * pitch + c);
-    uint32_t t[L::kOwn];
-    split<L::kOwn>(weight(x.x, c), weight(x.y, c + 1), t);
-#pragma unroll
-    for (int n = 0; n < L::kOwn; ++n)
-      *reinterpret_cast<uint32_t*>(dst + n * L::kSquare + unit_at<C>(r, c >> 3) + (c & 7) * 2) = t[n];
-  }
-}
-
-// One chunk of one (b, h).
+// One chunk of one (b, h).  Half of the warps have what reads T from the left (K K^T, K^), the others the rest.
 template <typename T, int DK, bool GRAD>
-__global__ void __launch_bounds__(Prepare<T, DK, GRAD>::kThreads) delta_prepare(const __grid_constant__ Common p) {
-  using P = Prepare<T, DK, GRAD>;
+__global__ void __launch_bounds__(Prepare<T, DK>::kThreads) delta_prepare(const __grid_constant__ Common p) {
+  using P = Prepare<T, DK>;
   using L = Lay<T, DK>;
-  constexpr int C = L::C, THREADS = P::kThreads, PITCH = P::kPitch;
+  constexpr int C = L::C, TILES = L::kTiles, SIDES = L::kSides, THREADS = P::kThreads, PITCH = P::kPitch;
   extern __shared__ __align__(128) char smem[];
   __shared__ __align__(16) typename L::M m;
+  __shared__ __align__(16) Decays<C> w;
   __shared__ int32_t bad_key, bad;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t chunk = blockIdx.x % p.chunks;
@@ -184,8 +188,10 @@ __global__ void __launch_bounds__(Prepare<T, DK, GRAD>::kThreads) delta_prepare(
   const int64_t t0 = static_cast<int64_t>(chunk) * C;
   const int rows = static_cast<int>(min(static_cast<int64_t>(C), p.N - t0));
   auto from = [&](const Operand& o, int64_t head) { return static_cast<const T*>(o.data) + b * o.sb + head * o.sh + t0 * o.sn; };
-  float* inv = reinterpret_cast<float*>(smem + P::kSum);
+  float* inv = reinterpret_cast<float*>(smem);
   const uint32_t base = ptx::smem_u32(smem);
+  const int strip = warp % TILES, m0 = 16 * strip, row = m0 + (lane >> 2);
+  const bool second = warp >= TILES;
 
   for (int i = threadIdx.x; i < DK; i += THREADS) m.first[i] = C;
   if (threadIdx.x == 0) bad_key = bad = C;
@@ -231,38 +237,60 @@ __global__ void __launch_bounds__(Prepare<T, DK, GRAD>::kThreads) delta_prepare(
     before.hi = __shfl_up_sync(~0u, all.hi, 1);
     before.lo = __shfl_up_sync(~0u, all.lo, 1);
     if (lane == 0) before.hi = before.lo = 0.0f;
-    Sum end;
-    end.hi = __shfl_sync(~0u, all.hi, 31);
-    end.lo = __shfl_sync(~0u, all.lo, 31);
-    const Sum none = {0.0f, 0.0f};
+    auto of_lane = [&](int l) {
+      Sum r;
+      r.hi = __shfl_sync(~0u, all.hi, l);
+      r.lo = __shfl_sync(~0u, all.lo, l);
+      return r;
+    };
+    const Sum end = of_lane(31), none = {0.0f, 0.0f};
+    Sum edge[TILES];
+    edge[0] = none;
+#pragma unroll
+    for (int r = 1; r < TILES; ++r) edge[r] = of_lane(16 * r / E - 1);
+    const int block = E * lane / 16;
+    Sum mine = none;
+#pragma unroll
+    for (int r = 1; r < TILES; ++r)
+      if (block == r) mine = edge[r];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int t = E * lane + e;
       const Sum s = add(before, run[e]);
       m.hi[t] = s.hi;
       m.lo[t] = s.lo;
-      m.inside[t] = exp2_of(s, none);
+      const float in = exp2_of(s, none);
+      m.inside[t] = in;
       m.after[t] = exp2_of(end, s);
       m.beta[t] = beta[e];
+      w.row[t] = exp2_of(s, mine);
+      w.key[t] = t < stop ? beta[e] * in : 0.0f;
+      w.value[t] = beta[e];
+#pragma unroll
+      for (int r = 1; r < TILES; ++r)
+        if (r > block) w.col[r][t] = exp2_of(edge[r], s);
     }
     if (lane == 0) m.total = exp2_of(end, none);
   }
   __syncthreads();
 
-  // K K^T (first half of the warps) and Q K^T (second half), 16 rows each, up to the diagonal
+  // K K^T (first) and Q K^T (second), 16 rows each, up to the diagonal
   {
-    const int strip = warp % P::kStrips, m0 = 16 * strip, row = m0 + (lane >> 2);
-    const bool scores = warp >= P::kStrips;
-    const uint32_t a_base = base + (scores ? P::kQ : P::kK), b_base = base + P::kK;
-    Accumulators<2 * P::kStrips, L::kApart> acc;
+    const uint32_t a_base = base + (second ? P::kQ : P::kK), b_base = base + P::kK;
+    Accumulators<2 * TILES, L::kApart> acc;
     acc.clear();
-#pragma unroll(L::kIn > 1 ? 1 : DK / 16)
-    for (int ks = 0; ks < DK / 16; ++ks) {
+#pragma unroll(L::kIn > 1 ? 1 : SIDES)
+    for (int ks = 0; ks < SIDES; ++ks) {
       uint32_t a[L::kIn][4];
 #pragma unroll
       for (int n = 0; n < L::kIn; ++n) a_rows<DK>(a[n], a_base + n * L::kRows, m0, 16 * ks, lane);
+      if (second && !GRAD && h % times == 0)
 #pragma unroll
-      for (int s = 0; s < P::kStrips; ++s) {
+        for (int n = 0; n < L::kIn; ++n)
+          *reinterpret_cast<uint4*>(p.im.q_rows + at_key * L::kInput + ((strip * SIDES + ks) * L::kIn + n) * kBlock + 16 * lane) =
+              make_uint4(a[n][0], a[n][1], a[n][2], a[n][3]);
+#pragma unroll
+      for (int s = 0; s < TILES; ++s) {
         if (s > strip) continue;
         uint32_t x[L::kIn][1][4];
 #pragma unroll
@@ -270,39 +298,60 @@ __global__ void __launch_bounds__(Prepare<T, DK, GRAD>::kThreads) delta_prepare(
         mma_terms(acc, 2 * s, a, x);
       }
     }
-    const Sum br[2] = {{m.hi[row], m.lo[row]}, {m.hi[row + 8], m.lo[row + 8]}};
-    const float beta_r[2] = {m.beta[row], m.beta[row + 8]};
-    char* img = p.im.scores + at * L::kScores;
+    const float f[2] = {w.row[row] * (second ? p.scale : m.beta[row]), w.row[row + 8] * (second ? p.scale : m.beta[row + 8])};
 #pragma unroll
-    for (int n = 0; n < 2 * P::kStrips; ++n) {
-      const int c = 8 * n + 2 * (lane & 3);
-      float y[4] = {};
-      if (n < 2 * strip + 2) {
-        const float2 h2 = *reinterpret_cast<const float2*>(m.hi + c), l2 = *reinterpret_cast<const float2*>(m.lo + c);
-        const Sum bc[2] = {{h2.x, l2.x}, {h2.y, l2.y}};
+    for (int s = 0; s < TILES; ++s) {
+      float y[2][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = row + 8 * (e >> 1), s = c + (e & 1);
-          if (scores ? s <= r : s < r) {
-            y[e] = acc.get(n, e) * exp2_of(br[e >> 1], bc[e & 1]) * (scores ? p.scale : beta_r[e >> 1]);
-            if (!scores && !finite(y[e])) atomicMin(&bad, r);
+      for (int n = 0; n < 2; ++n) {
+        const int c = 16 * s + 8 * n + 2 * (lane & 3);
+        if (s < strip) {
+          const float2 x = *reinterpret_cast<const float2*>(w.col[strip] + c);
+          y[n][0] = acc.get(2 * s + n, 0) * f[0] * x.x; y[n][1] = acc.get(2 * s + n, 1) * f[0] * x.y;
+          y[n][2] = acc.get(2 * s + n, 2) * f[1] * x.x; y[n][3] = acc.get(2 * s + n, 3) * f[1] * x.y;
+        } else if (s == strip) {
+          const float2 h2 = *reinterpret_cast<const float2*>(m.hi + c), l2 = *reinterpret_cast<const float2*>(m.lo + c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = row + 8 * (e >> 1), j = c + (e & 1);
+            const Sum mine = {m.hi[r], m.lo[r]}, other = {e & 1 ? h2.y : h2.x, e & 1 ? l2.y : l2.x};
+            const bool sees = second ? j <= r : j < r;
+            y[n][e] = sees ? acc.get(2 * s + n, e) * exp2_of(mine, other) * (second ? p.scale : m.beta[r]) : 0.0f;
           }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[n][e] = 0.0f;
         }
       }
-      if (scores) {
-        if (n < 2 * strip + 2) {
+      if (!second) {
+        bool fine = true;
 #pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            uint32_t t[L::kScore];
-            split<L::kScore>(y[2 * f], y[2 * f + 1], t);
+        for (int n = 0; n < 2; ++n) {
+          const int c = 16 * s + 8 * n + 2 * (lane & 3);
 #pragma unroll
-            for (int k = 0; k < L::kScore; ++k)
-              *reinterpret_cast<uint32_t*>(img + k * L::kSquare + unit_at<C>(row + 8 * f, n) + 4 * (lane & 3)) = t[k];
-          }
+          for (int e = 0; e < 4; ++e) fine &= finite(y[n][e]);
+          *reinterpret_cast<float2*>(inv + row * PITCH + c) = make_float2(y[n][0], y[n][1]);
+          *reinterpret_cast<float2*>(inv + (row + 8) * PITCH + c) = make_float2(y[n][2], y[n][3]);
         }
-      } else {
+        if (!fine)
 #pragma unroll
-        for (int f = 0; f < 2; ++f) *reinterpret_cast<float2*>(inv + (row + 8 * f) * PITCH + c) = make_float2(y[2 * f], y[2 * f + 1]);
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!finite(y[n][e])) atomicMin(&bad, row + 8 * (e >> 1));
+      } else if (s <= strip) {
+        constexpr int NT = GRAD ? kChain : L::kScore;
+        uint32_t a[NT][4];
+        as_rows<NT>(a, y[0], y[1]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (GRAD)   // columns in front of rows
+            *reinterpret_cast<uint4*>(p.im.scores_back + at * L::kScoresBack + ((s * TILES + strip) * NT + n) * kBlock + 16 * lane) =
+                make_uint4(turn(a[n][0]), turn(a[n][1]), turn(a[n][2]), turn(a[n][3]));
+          else
+            *reinterpret_cast<uint4*>(p.im.scores + at * L::kScores + ((strip * TILES + s) * NT + n) * kBlock + 16 * lane) =
+                make_uint4(a[n][0], a[n][1], a[n][2], a[n][3]);
+        }
       }
     }
   }
@@ -312,88 +361,158 @@ __global__ void __launch_bounds__(Prepare<T, DK, GRAD>::kThreads) delta_prepare(
     for (int i = threadIdx.x; i < C * C; i += THREADS)
       if (i / C >= stop) inv[i / C * PITCH + i % C] = 0.0f;
     for (int i = threadIdx.x; i < C; i += THREADS)
-      if (i >= stop) m.beta[i] = 0.0f;
+      if (i >= stop) w.key[i] = w.value[i] = m.beta[i] = 0.0f;
+    __syncthreads();
+  }
+
+  // T = (1 + L)^-1 in place: the diagonal blocks by columns, the others block by block
+  if (!second && lane < 16) {
+    float* block = inv + m0 * (PITCH + 1);
+    float x[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) x[r] = r == lane ? 1.0f : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 15; ++j)
+#pragma unroll
+      for (int r = j + 1; r < 16; ++r) x[r] = fmaf(-block[r * PITCH + j], x[j], x[r]);
+    __syncwarp(0xFFFFu);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) block[r * PITCH + lane] = x[r];
+  }
+  if (second && h % times == 0) {   // the key head's images, by its first head
+    char* to = p.im.k_add + at_key * L::kInput;
+#pragma unroll 2
+    for (int i = strip; i < SIDES * TILES; i += TILES) {
+      const int side = i / TILES, ks = i % TILES;
+#pragma unroll
+      for (int n = 0; n < L::kIn; ++n) {
+        uint32_t x[4];
+        b_cols<DK>(x, base + P::kK + n * L::kRows, 16 * side, 16 * ks, lane);
+        *reinterpret_cast<uint4*>(to + (i * L::kIn + n) * kBlock + 16 * lane) = make_uint4(x[0], x[1], x[2], x[3]);
+        if (GRAD) {
+          b_cols<DK>(x, base + P::kQ + n * L::kRows, 16 * side, 16 * ks, lane);
+          *reinterpret_cast<uint4*>(p.im.q_add + at_key * L::kInput + (i * L::kIn + n) * kBlock + 16 * lane) =
+              make_uint4(x[0], x[1], x[2], x[3]);
+          b_rows<DK>(x, base + P::kK + n * L::kRows, 16 * ks, 16 * side, lane);
+          *reinterpret_cast<uint4*>(p.im.k_rows + at_key * L::kInput + ((ks * SIDES + side) * L::kIn + n) * kBlock + 16 * lane) =
+              make_uint4(x[0], x[1], x[2], x[3]);
+        }
+      }
+    }
+    if (GRAD)
+      for (int i = 16 * (threadIdx.x - THREADS / 2); i < L::kInput; i += 8 * THREADS) {
+        *reinterpret_cast<uint4*>(p.im.k + at_key * L::kInput + i) = *reinterpret_cast<const uint4*>(smem + P::kK + i);
+        *reinterpret_cast<uint4*>(p.im.q + at_key * L::kInput + i) = *reinterpret_cast<const uint4*>(smem + P::kQ + i);
+      }
+  }
+  __syncthreads();
+  {
+    float Z[TILES][2][4];
+    if (!second) invert_column<TILES, PITCH>(inv, Z, strip, lane);
+    __syncthreads();   // every warp has read L
+    if (!second)
+#pragma unroll
+      for (int i = 1; i < TILES; ++i)
+        if (i > strip)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) inv[(16 * i + 8 * n + 2 * (lane & 3) + (e & 1)) * PITCH + row + 8 * (e >> 1)] = Z[i][n][e];
   }
   __syncthreads();
 
-  // images of the rows, by the key head's first head
-  if (h % times == 0) {
-    for (int i = 16 * threadIdx.x; i < L::kInput; i += 16 * THREADS) {
-      *reinterpret_cast<uint4*>(p.im.k + at_key * L::kInput + i) = *reinterpret_cast<const uint4*>(smem + P::kK + i);
-      *reinterpret_cast<uint4*>(p.im.q + at_key * L::kInput + i) = *reinterpret_cast<const uint4*>(smem + P::kQ + i);
+  // T's rows of this strip with weighed columns: the A operand of K^ (first), the B operand of U^T (second)
+  uint32_t a[TILES][kChain][4];
+#pragma unroll
+  for (int ks = 0; ks < TILES; ++ks) {
+    if (ks > strip) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = row + 8 * (second ? e >> 1 : e & 1), c = 16 * ks + 2 * (lane & 3) + 8 * (second ? e & 1 : e >> 1);
+      const float2 x = pair_at<PITCH>(inv, r, c), f = *reinterpret_cast<const float2*>((second ? w.value : w.key) + c);
+      uint32_t t[kChain];
+      split<kChain>(x.x * f.x, x.y * f.y, t);
+#pragma unroll
+      for (int n = 0; n < kChain; ++n) a[ks][n][e] = t[n];
     }
   }
-  invert<C, PITCH, P::kHalf, THREADS>(inv, reinterpret_cast<float*>(smem + P::kTmp));
-
-  // the planes of T beta e^b and T beta take the place of Q, which every warp is through with
-  char *with_decay = smem + P::kPlanes, *with_beta = with_decay + L::kInverse;
-  put_inverse<T, DK>(with_decay, inv, PITCH, THREADS, [&](float x, int c) { return c < stop ? x * (m.beta[c] * m.inside[c]) : 0.0f; });
-  put_inverse<T, DK>(with_beta, inv, PITCH, THREADS, [&](float x, int c) { return x * m.beta[c]; });
-  if (GRAD) put_inverse<T, DK>(p.im.inverse + at * L::kInverse, inv, PITCH, THREADS, [&](float x, int) { return x; });
-  __syncthreads();
-
-  if (warp < P::kStrips) {   // K^ rows
-    const int m0 = 16 * warp, row = m0 + (lane >> 2);
-    char* img = p.im.keys + at * L::kKeys;
-    constexpr int G = 2;   // pairs of column tiles at once
 #pragma unroll 1
-    for (int n0 = 0; n0 < DK; n0 += 16 * G) {
-      Accumulators<2 * G, L::kApart> acc;
-      acc.clear();
+  for (int side = 0; side < SIDES; ++side) {
+    Accumulators<2, true> acc;
+    acc.clear();
 #pragma unroll
-      for (int ks = 0; ks < P::kStrips; ++ks) {
-        if (ks > warp) continue;
-        uint32_t a[L::kOwn][4], x[L::kIn][G][4];
+    for (int ks = 0; ks < TILES; ++ks) {
+      if (ks > strip) continue;
+      uint32_t x[L::kIn][4];
 #pragma unroll
-        for (int n = 0; n < L::kOwn; ++n) a_rows<C>(a[n], base + P::kPlanes + n * L::kSquare, m0, 16 * ks, lane);
+      for (int n = 0; n < L::kIn; ++n) {
+        if (second)
+          a_cols<DK>(x[n], base + P::kV + n * L::kRows, 16 * side, 16 * ks, lane);
+        else
+          b_cols<DK>(x[n], base + P::kK + n * L::kRows, 16 * side, 16 * ks, lane);
+      }
+      if (second) {
+        uint32_t y[kChain][1][4];
+#pragma unroll
+        for (int n = 0; n < kChain; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[n][0][e] = a[ks][n][e];
+        mma_terms(acc, 0, x, y);
+      } else {
+        uint32_t y[L::kIn][1][4];
 #pragma unroll
         for (int n = 0; n < L::kIn; ++n)
 #pragma unroll
-          for (int j = 0; j < G; ++j) b_cols<DK>(x[n][j], base + P::kK + n * L::kRows, n0 + 16 * j, 16 * ks, lane);
-        mma_terms(acc, 0, a, x);
+          for (int e = 0; e < 4; ++e) y[n][0][e] = x[n][e];
+        mma_terms(acc, 0, a[ks], y);
       }
-#pragma unroll
-      for (int n = 0; n < 2 * G; ++n)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          uint32_t t[L::kOwn];
-          split<L::kOwn>(acc.get(n, 2 * f), acc.get(n, 2 * f + 1), t);
-#pragma unroll
-          for (int k = 0; k < L::kOwn; ++k)
-            *reinterpret_cast<uint32_t*>(img + k * L::kRows + unit_at<DK>(row + 8 * f, n0 / 8 + n) + 4 * (lane & 3)) = t[k];
-        }
     }
-  } else {                   // U^T, 16 columns of the values at a time
-    const uint32_t with_beta_at = base + P::kPlanes + L::kInverse;
-#pragma unroll 1
-    for (int tile = warp - P::kStrips; tile < DK / 16; tile += P::kStrips) {
-      if (16 * tile >= p.d) break;
-      Accumulators<2 * P::kStrips, L::kApart> acc;
-      acc.clear();
+    float y[2][4];
 #pragma unroll
-      for (int ks = 0; ks < P::kStrips; ++ks) {
-        uint32_t a[L::kIn][4];
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int n = 0; n < L::kIn; ++n) a_cols<DK>(a[n], base + P::kV + n * L::kRows, 16 * tile, 16 * ks, lane);
+      for (int e = 0; e < 4; ++e) y[n][e] = acc.get(n, e);
+    if (second) {
+      float4* to = reinterpret_cast<float4*>(p.im.u + (at * SIDES + side) * L::kTokens + 2 * strip * kBlock) + lane;
+      to[0] = make_float4(y[0][0], y[0][1], y[0][2], y[0][3]);
+      to[32] = make_float4(y[1][0], y[1][1], y[1][2], y[1][3]);
+    } else {
+      uint32_t t[kChain][4];   // rows of 16 tokens as A would have them; B takes the middle two the other way round
+      as_rows<kChain>(t, y[0], y[1]);
 #pragma unroll
-        for (int s = ks; s < P::kStrips; ++s) {
-          uint32_t x[L::kOwn][1][4];
-#pragma unroll
-          for (int n = 0; n < L::kOwn; ++n) b_rows<C>(x[n][0], with_beta_at + n * L::kSquare, 16 * s, 16 * ks, lane);
-          mma_terms(acc, 2 * s, a, x);
-        }
+      for (int n = 0; n < kChain; ++n) {
+        *reinterpret_cast<uint4*>(p.im.keys + at * L::kKeys + ((strip * SIDES + side) * kChain + n) * kBlock + 16 * lane) =
+            make_uint4(t[n][0], t[n][2], t[n][1], t[n][3]);
+        if (GRAD)
+          *reinterpret_cast<uint4*>(p.im.keys_add + at * L::kKeys + ((side * TILES + strip) * kChain + n) * kBlock + 16 * lane) =
+              make_uint4(turn(t[n][0]), turn(t[n][1]), turn(t[n][2]), turn(t[n][3]));
       }
-      float4* to = reinterpret_cast<float4*>(p.im.u + (at * (DK / 16) + tile) * L::kTokens) + lane;
-#pragma unroll
-      for (int n = 0; n < 2 * P::kStrips; ++n) to[32 * n] = make_float4(acc.get(n, 0), acc.get(n, 1), acc.get(n, 2), acc.get(n, 3));
     }
   }
-  if (GRAD) {   // rows of dout, in V's place
+  if (GRAD) {   // T, and the rows of dout in V's place
+    for (int i = threadIdx.x; i < C * C / 2; i += THREADS) {
+      const int r = i / (C / 2), c = 2 * (i % (C / 2));
+      if (c > (r | 15)) continue;
+      const float2 x = pair_at<PITCH>(inv, r, c);
+      uint32_t t[L::kOwn];
+      split<L::kOwn>(x.x, x.y, t);
+#pragma unroll
+      for (int n = 0; n < L::kOwn; ++n)
+        *reinterpret_cast<uint32_t*>(p.im.inverse + at * L::kInverse + n * L::kSquare + unit_at<C>(r, c >> 3) + (c & 7) * 2) = t[n];
+    }
     __syncthreads();
     load_rows<T, DK, THREADS, 0>(smem + P::kV, from(p.dout, h), p.dout.sn, rows, p.d, p.wide & kWideDout, nullptr);
     __syncthreads();
     for (int i = 16 * threadIdx.x; i < L::kInput; i += 16 * THREADS)
       *reinterpret_cast<uint4*>(p.im.dout + at * L::kInput + i) = *reinterpret_cast<const uint4*>(smem + P::kV + i);
+    for (int i = warp; i < SIDES * TILES; i += 2 * TILES)
+#pragma unroll
+      for (int n = 0; n < L::kIn; ++n) {
+        uint32_t x[4];
+        a_cols<DK>(x, base + P::kV + n * L::kRows, 16 * (i / TILES), 16 * (i % TILES), lane);
+        *reinterpret_cast<uint4*>(p.im.dout_cols + at * L::kInput + (i * L::kIn + n) * kBlock + 16 * lane) =
+            make_uint4(x[0], x[1], x[2], x[3]);
+      }
   }
   // marks
   bool any = false;
@@ -408,248 +527,282 @@ __global__ void __launch_bounds__(Prepare<T, DK, GRAD>::kThreads) delta_prepare(
     *reinterpret_cast<uint4*>(p.im.marks + at * L::kMarks + i) = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(&m) + i);
 }
 
-// NW warps of the chain (16 columns of the state each) and, unless KEEP, as many for the outputs.  KEEP leaves
-// the states and the w of every chunk for the gradients instead.
-template <typename T, int DK, int NW, bool KEEP>
+// A CTA walks the chunks with 16 MT columns of the state.  TILES warps make the chain: each forms the W of 16 tokens, and then its
+// share of the state's rows; as many warps beside them, unless KEEP, read 16 tokens' outputs.  KEEP leaves the states and
+// the w of every chunk for the gradients instead.
+template <typename T, int DK, int MT, bool KEEP>
 struct ScanLay {
   using L = Lay<T, DK>;
-  static constexpr int kThreads = (KEEP ? 32 : 64) * NW;
-  static constexpr int kK = 0, kKeys = kK + L::kInput, kU = kKeys + L::kKeys, kMarks = kU + NW * L::kTokens;
-  static constexpr int kStage = kMarks + L::kMarks;
-  static constexpr int kQ = 0, kScores = kQ + L::kInput, kMarksOut = kScores + L::kScores, kStageOut = kMarksOut + L::kMarks;
-  static constexpr int kHand = L::kState + L::kTokens;   // a warp's S and W of one chunk
-  static constexpr int kOut = 2 * kStage, kHands = kOut + 2 * kStageOut;
-  static constexpr int kBytes = KEEP ? 2 * kStage : kHands + 2 * NW * kHand;
+  static constexpr int kWarps = L::kTiles, kThreads = (KEEP ? 32 : 64) * kWarps;
+  static constexpr int kShare = DK / 16 < kWarps ? 1 : DK / 16 / kWarps;   // blocks of the state's rows a warp
+  static constexpr int kKeys = 0, kAdd = kKeys + L::kSides * kChain * kBlock, kU = kAdd + kShare * L::kTiles * L::kIn * kBlock;
+  static constexpr int kStage = kU + MT * 2 * kBlock;
+  static constexpr int kQ = 0, kScores = kQ + L::kSides * L::kIn * kBlock, kStageOut = kScores + L::kTiles * L::kScore * kBlock;
+  static constexpr int kStatePlane = 16 * MT * DK * 2, kTokenPlane = 16 * MT * L::C * 2;
+  static constexpr int kState = 0, kAfter = kState + 2 * kChain * kStatePlane, kW = kAfter + kChain * kTokenPlane;
+  static constexpr int kRing = kW + (KEEP ? 0 : L::kOwn * kTokenPlane), kRingOut = kRing + kWarps * kStage;
+  static constexpr int kBytes = kRingOut + (KEEP ? 0 : kWarps * kStageOut);
 };
 
-template <typename T, int DK, int NW, bool KEEP>
-__global__ void __launch_bounds__(ScanLay<T, DK, NW, KEEP>::kThreads) delta_scan(const __grid_constant__ ScanArgs a) {
-  using W = ScanLay<T, DK, NW, KEEP>;
+template <typename T, int DK, int MT, bool KEEP>
+__global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan(const __grid_constant__ ScanArgs a) {
+  using W = ScanLay<T, DK, MT, KEEP>;
   using L = Lay<T, DK>;
-  constexpr int C = L::C, NT = C / 8, NS = DK / 8, THREADS = W::kThreads;
+  constexpr int C = L::C, TILES = L::kTiles, SIDES = L::kSides, SHARE = W::kShare;
   extern __shared__ __align__(128) char smem[];
   const Common& p = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = (p.d + 16 * NW - 1) / (16 * NW);
+  const int groups = (p.d + 16 * MT - 1) / (16 * MT);
   const int64_t bh = blockIdx.x / groups, b = bh / p.H, h = bh % p.H, key = b * p.Hk + h / (p.H / p.Hk);
-  const int tile0 = static_cast<int>(blockIdx.x % groups) * NW;
+  const int tile0 = static_cast<int>(blockIdx.x % groups) * MT;
   const uint32_t base = ptx::smem_u32(smem);
   const int count = static_cast<int>(p.chunks);
-  const int own = warp % NW, tile = tile0 + own, c0 = 16 * tile + (lane >> 2);
-  const bool chain = KEEP || warp < NW;
+  const int own = warp % TILES;
+  const bool chain = KEEP || warp < TILES;
+  const int g = lane >> 2, t = 2 * (lane & 3);
 
-  auto load = [&](int i) {
-    const uint32_t st = base + (i & 1) * W::kStage;
-    const int64_t at = bh * p.chunks + i;
-    copy_async(st + W::kK, p.im.k + (key * p.chunks + i) * L::kInput, L::kInput, threadIdx.x, THREADS);
-    copy_async(st + W::kKeys, p.im.keys + at * L::kKeys, L::kKeys, threadIdx.x, THREADS);
-    copy_async(st + W::kU, p.im.u + (at * (DK / 16) + tile0) * L::kTokens, NW * L::kTokens, threadIdx.x, THREADS);
-    copy_async(st + W::kMarks, p.im.marks + at * L::kMarks, L::kMarks, threadIdx.x, THREADS);
-  };
-  auto load_out = [&](int i) {
-    const uint32_t st = base + W::kOut + (i & 1) * W::kStageOut;
-    const int64_t at = bh * p.chunks + i;
-    copy_async(st + W::kQ, p.im.q + (key * p.chunks + i) * L::kInput, L::kInput, threadIdx.x, THREADS);
-    copy_async(st + W::kScores, p.im.scores + at * L::kScores, L::kScores, threadIdx.x, THREADS);
-    copy_async(st + W::kMarksOut, p.im.marks + at * L::kMarks, L::kMarks, threadIdx.x, THREADS);
-  };
-  load(0);
-  commit();
-
-  // S^T: rows c0, c0 + 8 (columns of the state), columns 8 n + 2 (lane % 4) and the next
-  float S[NS][4];
-  if (chain) {
-    const float* in = a.init ? a.init + bh * p.d * p.d : nullptr;
+  auto marks = [&](int i) { return reinterpret_cast<const typename L::M*>(p.im.marks + (bh * p.chunks + i) * L::kMarks); };
+  // Each lane's own blocks of a chunk, in two groups: what the chunk's first half reads, and what its second half does.  A group
+  // is asked for anew as soon as its half is done with it, so it has the other half's time to come.
+  const uint32_t ring = base + (chain ? W::kRing + own * W::kStage : W::kRingOut + own * W::kStageOut);
+  const char* st = smem + (ring - base);
+  auto load_first = [&](int i) {
+    const int64_t at = bh * p.chunks + i, at_key = key * p.chunks + i;
+    if (i >= count) {
+    } else if (chain) {
+      copy_blocks<SIDES * kChain>(ring + W::kKeys, p.im.keys + at * L::kKeys + own * SIDES * kChain * kBlock, lane);
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = 8 * n + 2 * (lane & 3) + (e & 1), c = c0 + 8 * (e >> 1);
-        S[n][e] = in && r < p.d && c < p.d ? in[static_cast<int64_t>(r) * p.d + c] : 0.0f;
-      }
-  }
-
-  for (int i = 0; i < count + (KEEP ? 0 : 1); ++i) {
-    wait_all();
-    __syncthreads();
-    if (i + 1 < count) load(i + 1);
-    if (!KEEP && i < count) load_out(i);
+      for (int n = 0; n < MT; ++n)
+        if (tile0 + n < SIDES) copy_blocks<2>(ring + W::kU + 2 * n * kBlock, p.im.u + (at * SIDES + tile0 + n) * L::kTokens + 2 * own * kBlock, lane);
+    } else {
+      copy_blocks<SIDES * L::kIn>(ring + W::kQ, p.im.q_rows + at_key * L::kInput + own * SIDES * L::kIn * kBlock, lane);
+    }
     commit();
-    if (chain) {
-      if (i >= count) continue;
-      const char* stage = smem + (i & 1) * W::kStage;
-      const uint32_t st = base + (i & 1) * W::kStage;
-      const auto& m = *reinterpret_cast<const typename L::M*>(stage + W::kMarks);
-      // W^T = U^T - S^T K^^T
-      Accumulators<NT, L::kApart> acc;
-      acc.clear();
+  };
+  auto load_second = [&](int i) {
+    const int64_t at = bh * p.chunks + i, at_key = key * p.chunks + i;
+    if (i >= count) {
+    } else if (chain) {
+      if (own * SHARE < SIDES)
+        copy_blocks<SHARE * TILES * L::kIn>(ring + W::kAdd, p.im.k_add + at_key * L::kInput + own * SHARE * TILES * L::kIn * kBlock, lane);
+    } else {
 #pragma unroll
-      for (int ks = 0; ks < DK / 16; ++ks) {
-        uint32_t s[L::kOwn][4], x[L::kOwn][NT / 2][4];
-        as_rows<L::kOwn>(s, S[2 * ks], S[2 * ks + 1]);
+      for (int ks = 0; ks < TILES; ++ks)
+        if (ks <= own)
+          copy_blocks<L::kScore>(ring + W::kScores + ks * L::kScore * kBlock,
+                                 p.im.scores + at * L::kScores + (own * TILES + ks) * L::kScore * kBlock, lane);
+    }
+    commit();
+  };
+  load_first(0);
+  load_second(0);
+
+  // S^T: rows the state's columns 16 (tile0 + n) + g, + 8; columns this warp's share of its rows
+  float S[MT][2 * SHARE][4];
+  const bool shares = chain && own * SHARE < SIDES;
+  auto publish = [&](int i) {   // as planes of terms
 #pragma unroll
-        for (int n = 0; n < L::kOwn; ++n)
+    for (int n = 0; n < MT; ++n)
 #pragma unroll
-          for (int j = 0; j < NT / 2; ++j) b_rows<DK>(x[n][j], st + W::kKeys + n * L::kRows, 16 * j, 16 * ks, lane);
-        mma_terms(acc, 0, s, x);
-      }
-      float w[NT][4];
-      {
-        const float4* u = reinterpret_cast<const float4*>(stage + W::kU + own * L::kTokens) + lane;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float4 x = u[32 * n];
-          w[n][0] = x.x - acc.get(n, 0); w[n][1] = x.y - acc.get(n, 1);
-          w[n][2] = x.z - acc.get(n, 2); w[n][3] = x.w - acc.get(n, 3);
-        }
-      }
-      {
-        float4 *to_s, *to_w;
-        if (KEEP) {
-          const int64_t at = (bh * p.chunks + i) * (DK / 16) + tile;
-          to_s = reinterpret_cast<float4*>(p.im.s + at * L::kState) + lane;
-          to_w = reinterpret_cast<float4*>(p.im.w + at * L::kTokens) + lane;
-        } else {
-          char* hand = smem + W::kHands + ((i & 1) * NW + own) * W::kHand;
-          to_s = reinterpret_cast<float4*>(hand) + lane;
-          to_w = reinterpret_cast<float4*>(hand + L::kState) + lane;
-        }
-        if (!KEEP || 16 * tile < p.d) {
-#pragma unroll
-          for (int n = 0; n < NS; ++n) to_s[32 * n] = make_float4(S[n][0], S[n][1], S[n][2], S[n][3]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) to_w[32 * n] = make_float4(w[n][0], w[n][1], w[n][2], w[n][3]);
-        }
-      }
-      // S^T <- e^B S^T + (e^{B-b} W)^T K.  The chunk's sum is formed apart and added once, rounded to nearest: a long
-      // sequence must not gather the tensor core's truncation.
-      uint32_t wa[C / 16][L::kOwn][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float2 f = *reinterpret_cast<const float2*>(m.after + 8 * n + 2 * (lane & 3));
-        w[n][0] *= f.x; w[n][1] *= f.y; w[n][2] *= f.x; w[n][3] *= f.y;
-      }
-#pragma unroll
-      for (int ks = 0; ks < C / 16; ++ks) as_rows<L::kOwn>(wa[ks], w[2 * ks], w[2 * ks + 1]);
-      const float total = m.total;
-      constexpr int G = DK / 16 < 4 ? DK / 16 : 4;
-#pragma unroll
-      for (int n0 = 0; n0 < NS; n0 += 2 * G) {
-        Accumulators<2 * G, L::kApart> sum;
-        sum.clear();
-#pragma unroll
-        for (int ks = 0; ks < C / 16; ++ks) {
-          uint32_t x[L::kIn][G][4];
-#pragma unroll
-          for (int n = 0; n < L::kIn; ++n)
-#pragma unroll
-            for (int j = 0; j < G; ++j) b_cols<DK>(x[n][j], st + W::kK + n * L::kRows, 8 * n0 + 16 * j, 16 * ks, lane);
-          mma_terms(sum, 0, wa[ks], x);
-        }
-#pragma unroll
-        for (int n = 0; n < 2 * G; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) S[n0 + n][e] = fmaf(total, S[n0 + n][e], sum.get(n, e));
-      }
-      if (m.any) {
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-          if (c0 + 8 * f < p.d && m.first[c0 + 8 * f] < C)
-#pragma unroll
-            for (int n = 0; n < NS; ++n) S[n][2 * f] = S[n][2 * f + 1] = nan_value();
-      }
-    } else if (!KEEP && i > 0) {
-      // O = scale e^b Q S + scores W: rows of tokens, this warp's 16 columns
-      const int done = i - 1;
-      const char* stage = smem + W::kOut + (done & 1) * W::kStageOut;
-      const uint32_t st = base + W::kOut + (done & 1) * W::kStageOut;
-      const auto& m = *reinterpret_cast<const typename L::M*>(stage + W::kMarksOut);
-      const char* hand = smem + W::kHands + ((done & 1) * NW + own) * W::kHand;
-      const float4 *of_s = reinterpret_cast<const float4*>(hand) + lane,
-                   *of_w = reinterpret_cast<const float4*>(hand + L::kState) + lane;
-      Accumulators<2, L::kApart> o[C / 16];
-#pragma unroll
-      for (int s = 0; s < C / 16; ++s) o[s].clear();
-#pragma unroll(L::kIn > 1 ? 1 : DK / 16)
-      for (int ks = 0; ks < DK / 16; ++ks) {
-        // a transposed accumulator is a B operand as it is: rows its columns, columns its k
-        const float4 x = of_s[64 * ks], y = of_s[64 * ks + 32];
-        uint32_t sb[L::kOwn][1][4], t[L::kOwn];
-        auto put = [&](int e, float f, float g) {
-          split<L::kOwn>(f, g, t);
-#pragma unroll
-          for (int n = 0; n < L::kOwn; ++n) sb[n][0][e] = t[n];
-        };
-        put(0, x.x, x.y); put(1, y.x, y.y); put(2, x.z, x.w); put(3, y.z, y.w);
-#pragma unroll
-        for (int s = 0; s < C / 16; ++s) {
-          uint32_t q[L::kIn][4];
-#pragma unroll
-          for (int n = 0; n < L::kIn; ++n) a_rows<DK>(q[n], st + W::kQ + n * L::kRows, 16 * s, 16 * ks, lane);
-          mma_terms(o[s], 0, q, sb);
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < C / 16; ++s) {
-        const float f0 = p.scale * m.inside[16 * s + (lane >> 2)], f1 = p.scale * m.inside[16 * s + (lane >> 2) + 8];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            o[s].main[n][e] = o[s].get(n, e) * (e < 2 ? f0 : f1);
-            if (L::kApart) o[s].small[L::kApart ? n : 0][e] = 0.0f;
-          }
-        }
-      }
-#pragma unroll
-      for (int ks = 0; ks < C / 16; ++ks) {
-        const float4 x = of_w[64 * ks], y = of_w[64 * ks + 32];
-        uint32_t wb[L::kOwn][1][4], t[L::kOwn];
-        auto put = [&](int e, float f, float g) {
-          split<L::kOwn>(f, g, t);
-#pragma unroll
-          for (int n = 0; n < L::kOwn; ++n) wb[n][0][e] = t[n];
-        };
-        put(0, x.x, x.y); put(1, y.x, y.y); put(2, x.z, x.w); put(3, y.z, y.w);
-#pragma unroll
-        for (int s = ks; s < C / 16; ++s) {
-          uint32_t q[L::kScore][4];
-#pragma unroll
-          for (int n = 0; n < L::kScore; ++n) a_rows<C>(q[n], st + W::kScores + n * L::kSquare, 16 * s, 16 * ks, lane);
-          mma_terms(o[s], 0, q, wb);
-        }
-      }
-      const int64_t t0 = static_cast<int64_t>(done) * C;
-      T* out = static_cast<T*>(a.out.data) + b * a.out.sb + h * a.out.sh;
-#pragma unroll
-      for (int s = 0; s < C / 16; ++s)
+      for (int j = 0; j < 2 * SHARE; ++j)
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          const int r = 16 * s + (lane >> 2) + 8 * f;
-          if (t0 + r >= p.N) continue;
+          uint32_t x[kChain];
+          split<kChain>(S[n][j][2 * f], S[n][j][2 * f + 1], x);
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int c = 16 * tile + 8 * n + 2 * (lane & 3);
-            if (c >= p.d) continue;
-            float y[2] = {o[s].get(n, 2 * f), o[s].get(n, 2 * f + 1)};
-            if (m.any)
+          for (int k = 0; k < kChain; ++k)
+            *reinterpret_cast<uint32_t*>(smem + W::kState + ((i & 1) * kChain + k) * W::kStatePlane +
+                                         unit_at<DK>(16 * n + g + 8 * f, 2 * own * SHARE + j) + 2 * t) = x[k];
+        }
+  };
+  if (shares) {
+    const float* in = a.init ? a.init + bh * p.d * p.d : nullptr;
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (r >= m.first[c + e]) y[e] = nan_value();
-            store_pair<T>(out + (t0 + r) * a.out.sn + c, y[0], y[1], a.out_pairs, c + 1 < p.d);
+    for (int n = 0; n < MT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2 * SHARE; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 16 * own * SHARE + 8 * j + t + (e & 1), c = 16 * (tile0 + n) + g + 8 * (e >> 1);
+          S[n][j][e] = in && r < p.d && c < p.d ? in[static_cast<int64_t>(r) * p.d + c] : 0.0f;
+        }
+    publish(0);
+  }
+
+  for (int i = 0; i < count; ++i) {
+    const auto* m = marks(i);
+    wait_older();
+    const uint32_t state = base + W::kState + (i & 1) * kChain * W::kStatePlane;
+    if (chain) {
+      const float2 after[2] = {*reinterpret_cast<const float2*>(m->after + 16 * own + t),
+                               *reinterpret_cast<const float2*>(m->after + 16 * own + 8 + t)};
+      const float total = m->total;
+      const int any = m->any;
+      __syncthreads();   // the state's planes are there; the outputs of the chunk before are read
+      // W^T = U^T - S^T K^^T, this warp's 16 tokens
+      Accumulators<2, true> acc[MT];
+#pragma unroll
+      for (int n = 0; n < MT; ++n) acc[n].clear();
+#pragma unroll
+      for (int ks = 0; ks < SIDES; ++ks) {
+        uint32_t x[kChain][1][4];
+#pragma unroll
+        for (int k = 0; k < kChain; ++k) load_block(x[k][0], st + W::kKeys, ks * kChain + k, lane);
+#pragma unroll
+        for (int n = 0; n < MT; ++n) {
+          uint32_t s[kChain][4];
+#pragma unroll
+          for (int k = 0; k < kChain; ++k) a_rows<DK>(s[k], state + k * W::kStatePlane, 16 * n, 16 * ks, lane);
+          mma_terms(acc[n], 0, s, x);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < MT; ++n) {
+        float w[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float4 u = *reinterpret_cast<const float4*>(st + W::kU + (2 * n + j) * kBlock + 16 * lane);
+          w[j][0] = u.x - acc[n].get(j, 0); w[j][1] = u.y - acc[n].get(j, 1);
+          w[j][2] = u.z - acc[n].get(j, 2); w[j][3] = u.w - acc[n].get(j, 3);
+          if (KEEP && 16 * (tile0 + n) < p.d)
+            *reinterpret_cast<float4*>(p.im.w + ((bh * p.chunks + i) * SIDES + tile0 + n) * L::kTokens + (2 * own + j) * kBlock + 16 * lane) =
+                make_float4(w[j][0], w[j][1], w[j][2], w[j][3]);
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const int to = unit_at<C>(16 * n + g + 8 * f, 2 * own + j) + 2 * t;
+            if (!KEEP) {
+              uint32_t x[L::kOwn];
+              split<L::kOwn>(w[j][2 * f], w[j][2 * f + 1], x);
+#pragma unroll
+              for (int k = 0; k < L::kOwn; ++k) *reinterpret_cast<uint32_t*>(smem + W::kW + k * W::kTokenPlane + to) = x[k];
+            }
+            uint32_t x[kChain];
+            split<kChain>(w[j][2 * f] * after[j].x, w[j][2 * f + 1] * after[j].y, x);
+#pragma unroll
+            for (int k = 0; k < kChain; ++k) *reinterpret_cast<uint32_t*>(smem + W::kAfter + k * W::kTokenPlane + to) = x[k];
           }
         }
+      }
+      load_first(i + 1);
+      __syncthreads();   // W's planes are there
+      wait_older();
+      if (shares) {
+        // S^T <- e^B S^T + (e^{B-b} W)^T K.  The chunk's sum is formed apart and added once, rounded to nearest: a long
+        // sequence must not gather the tensor core's truncation.
+        Accumulators<2 * SHARE, true> sum[MT];
+#pragma unroll
+        for (int n = 0; n < MT; ++n) sum[n].clear();
+#pragma unroll
+        for (int ks = 0; ks < TILES; ++ks) {
+          uint32_t x[L::kIn][SHARE][4];
+#pragma unroll
+          for (int k = 0; k < L::kIn; ++k)
+#pragma unroll
+            for (int j = 0; j < SHARE; ++j) load_block(x[k][j], st + W::kAdd, (j * TILES + ks) * L::kIn + k, lane);
+#pragma unroll
+          for (int n = 0; n < MT; ++n) {
+            uint32_t w[kChain][4];
+#pragma unroll
+            for (int k = 0; k < kChain; ++k) a_rows<C>(w[k], base + W::kAfter + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
+            mma_terms(sum[n], 0, w, x);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < MT; ++n)
+#pragma unroll
+          for (int j = 0; j < 2 * SHARE; ++j) {
+            if (KEEP && 16 * (tile0 + n) < p.d)
+              *reinterpret_cast<float4*>(p.im.s + ((bh * p.chunks + i) * SIDES + tile0 + n) * L::kState + (2 * own * SHARE + j) * kBlock +
+                                         16 * lane) = make_float4(S[n][j][0], S[n][j][1], S[n][j][2], S[n][j][3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[n][j][e] = fmaf(total, S[n][j][e], sum[n].get(j, e));
+          }
+        if (any) {
+#pragma unroll
+          for (int n = 0; n < MT; ++n)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const int c = 16 * (tile0 + n) + g + 8 * f;
+              if (c < p.d && m->first[c] < C)
+#pragma unroll
+                for (int j = 0; j < 2 * SHARE; ++j) S[n][j][2 * f] = S[n][j][2 * f + 1] = nan_value();
+            }
+        }
+        publish(i + 1);
+      }
+      load_second(i + 1);
+    } else {
+      // O = scale e^b Q S + scores W, this warp's 16 tokens
+      const float in[2] = {p.scale * m->inside[16 * own + g], p.scale * m->inside[16 * own + g + 8]};
+      const int any = m->any;
+      __syncthreads();
+      Accumulators<2 * MT, L::kApart> o;
+      o.clear();
+#pragma unroll
+      for (int ks = 0; ks < SIDES; ++ks) {
+        uint32_t q[L::kIn][4], x[L::kOwn][MT][4];
+#pragma unroll
+        for (int k = 0; k < L::kIn; ++k) load_block(q[k], st + W::kQ, ks * L::kIn + k, lane);
+#pragma unroll
+        for (int k = 0; k < L::kOwn; ++k)
+#pragma unroll
+          for (int n = 0; n < MT; ++n) b_rows<DK>(x[k][n], state + k * W::kStatePlane, 16 * n, 16 * ks, lane);
+        mma_terms(o, 0, q, x);
+      }
+#pragma unroll
+      for (int n = 0; n < 2 * MT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o.main[n][e] = o.get(n, e) * in[e >> 1];
+          if (L::kApart) o.small[L::kApart ? n : 0][e] = 0.0f;
+        }
+      load_first(i + 1);
+      __syncthreads();
+      wait_older();
+#pragma unroll
+      for (int ks = 0; ks < TILES; ++ks) {
+        if (ks > own) continue;
+        uint32_t q[L::kScore][4], x[L::kOwn][MT][4];
+#pragma unroll
+        for (int k = 0; k < L::kScore; ++k) load_block(q[k], st + W::kScores, ks * L::kScore + k, lane);
+#pragma unroll
+        for (int k = 0; k < L::kOwn; ++k)
+#pragma unroll
+          for (int n = 0; n < MT; ++n) b_rows<C>(x[k][n], base + W::kW + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
+        mma_terms(o, 0, q, x);
+      }
+      load_second(i + 1);
+      const int64_t t0 = static_cast<int64_t>(i) * C;
+      T* out = static_cast<T*>(a.out.data) + b * a.out.sb + h * a.out.sh;
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int r = 16 * own + g + 8 * f;
+        if (t0 + r >= p.N) continue;
+#pragma unroll
+        for (int n = 0; n < 2 * MT; ++n) {
+          const int c = 16 * tile0 + 8 * n + t;
+          if (c >= p.d) continue;
+          float y[2] = {o.get(n, 2 * f), o.get(n, 2 * f + 1)};
+          if (any)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (r >= m->first[c + e]) y[e] = nan_value();
+          store_pair<T>(out + (t0 + r) * a.out.sn + c, y[0], y[1], a.out_pairs, c + 1 < p.d);
+        }
+      }
     }
   }
-  if (chain && a.last) {
+  if (shares && a.last) {
     float* last = a.last + bh * p.d * p.d;
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
+    for (int n = 0; n < MT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = 8 * n + 2 * (lane & 3) + (e & 1), c = c0 + 8 * (e >> 1);
-        if (r < p.d && c < p.d) last[static_cast<int64_t>(r) * p.d + c] = S[n][e];
-      }
+      for (int j = 0; j < 2 * SHARE; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 16 * own * SHARE + 8 * j + t + (e & 1), c = 16 * (tile0 + n) + g + 8 * (e >> 1);
+          if (r < p.d && c < p.d) last[static_cast<int64_t>(r) * p.d + c] = S[n][j][e];
+        }
   }
 }
 
@@ -660,7 +813,7 @@ bool wide_rows(const Operand& o, int d, int dtype) {
 
 template <typename T, int DK, bool GRAD>
 int prepare_as(const Common& c, int64_t BH, cudaStream_t s) {
-  using P = Prepare<T, DK, GRAD>;
+  using P = Prepare<T, DK>;
   if (cudaFuncSetAttribute(delta_prepare<T, DK, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes) != cudaSuccess)
     return MHLA_ERR_CUDA;
   KernelTimer timer("delta_prepare", s);
@@ -668,17 +821,22 @@ int prepare_as(const Common& c, int64_t BH, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
 
-template <typename T, int DK, bool KEEP>
+template <typename T, int DK, int MT, bool KEEP>
 int scan_as(const ScanArgs& a, int64_t BH, cudaStream_t s) {
-  constexpr int NW = 2;
-  using W = ScanLay<T, DK, NW, KEEP>;
+  using W = ScanLay<T, DK, MT, KEEP>;
   static_assert(W::kBytes <= 227 * 1024, "shared memory");
-  if (cudaFuncSetAttribute(delta_scan<T, DK, NW, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kBytes) != cudaSuccess)
+  if (cudaFuncSetAttribute(delta_scan<T, DK, MT, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kBytes) != cudaSuccess)
     return MHLA_ERR_CUDA;
-  const int groups = (a.c.d + 16 * NW - 1) / (16 * NW);
+  const int groups = (a.c.d + 16 * MT - 1) / (16 * MT);
   KernelTimer timer(KEEP ? "delta_states" : "delta_scan", s);
-  delta_scan<T, DK, NW, KEEP><<<static_cast<unsigned>(BH * groups), W::kThreads, W::kBytes, s>>>(a);
+  delta_scan<T, DK, MT, KEEP><<<static_cast<unsigned>(BH * groups), W::kThreads, W::kBytes, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+}
+
+template <typename T, int DK>
+int scan_for(const ScanArgs& a, int64_t BH, bool keep, cudaStream_t s) {
+  if (two_tiles(BH, a.c.d)) return keep ? scan_as<T, DK, 2, true>(a, BH, s) : scan_as<T, DK, 2, false>(a, BH, s);
+  return keep ? scan_as<T, DK, 1, true>(a, BH, s) : scan_as<T, DK, 1, false>(a, BH, s);
 }
 
 template <typename T>
@@ -693,9 +851,9 @@ int prepare_type(const Common& c, int64_t BH, bool grad, cudaStream_t s) {
 template <typename T>
 int scan_type(const ScanArgs& a, int64_t BH, bool keep, cudaStream_t s) {
   switch (padded(a.c.d)) {
-    case 32: return keep ? scan_as<T, 32, true>(a, BH, s) : scan_as<T, 32, false>(a, BH, s);
-    case 64: return keep ? scan_as<T, 64, true>(a, BH, s) : scan_as<T, 64, false>(a, BH, s);
-    default: return keep ? scan_as<T, 128, true>(a, BH, s) : scan_as<T, 128, false>(a, BH, s);
+    case 32: return scan_for<T, 32>(a, BH, keep, s);
+    case 64: return scan_for<T, 64>(a, BH, keep, s);
+    default: return scan_for<T, 128>(a, BH, keep, s);
   }
 }
 
@@ -708,20 +866,28 @@ size_t lay_out_as(int64_t heads, int64_t keys, bool grad, char* base, Images* im
     used += align_up(static_cast<size_t>(bytes));
     return at;
   };
+  im->k_add = take(keys * L::kInput);
+  im->keys = take(heads * L::kKeys);
+  im->u = take(heads * L::kSides * L::kTokens);
+  im->marks = take(heads * L::kMarks);
+  if (!grad) {
+    im->q_rows = take(keys * L::kInput);
+    im->scores = take(heads * L::kScores);
+    return used;
+  }
   im->k = take(keys * L::kInput);
   im->q = take(keys * L::kInput);
-  im->keys = take(heads * L::kKeys);
-  im->scores = take(heads * L::kScores);
-  im->u = take(heads * (DK / 16) * L::kTokens);
-  im->marks = take(heads * L::kMarks);
-  if (grad) {
-    im->inverse = take(heads * L::kInverse);
-    im->dout = take(heads * L::kInput);
-    im->s = take(heads * (DK / 16) * L::kState);
-    im->ds = take(heads * (DK / 16) * L::kState);
-    im->w = take(heads * (DK / 16) * L::kTokens);
-    im->dw = take(heads * (DK / 16) * L::kTokens);
-  }
+  im->dout = take(heads * L::kInput);
+  im->inverse = take(heads * L::kInverse);
+  im->k_rows = take(keys * L::kInput);
+  im->keys_add = take(heads * L::kKeys);
+  im->q_add = take(keys * L::kInput);
+  im->scores_back = take(heads * L::kScoresBack);
+  im->dout_cols = take(heads * L::kInput);
+  im->s = take(heads * L::kSides * L::kState);
+  im->ds = take(heads * L::kSides * L::kState);
+  im->w = take(heads * L::kSides * L::kTokens);
+  im->dw = take(heads * L::kSides * L::kTokens);
   return used;
 }
 
@@ -743,6 +909,8 @@ int64_t delta_chunks(const DeltaProblem& p) {
 }
 
 namespace delta {
+
+bool two_tiles(int64_t BH, int d) { return BH * ((d + 15) / 16) > kSms; }
 
 int launch_prepare(const Common& c, int64_t BH, int dtype, bool grad, cudaStream_t s) {
   return dtype == MHLA_BF16 ? prepare_type<__nv_bfloat16>(c, BH, grad, s) : prepare_type<float>(c, BH, grad, s);
