@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
                                *reinterpret_cast<const float2*>(m->after + 16 * own + 8 + t)};
       const float total = m->total;
       __syncthreads();   // the planes of D and the parts formed ahead are there
-      Accumulators<2, true> acc[MT];
+      ChainSum<2> acc[MT];
 #pragma unroll
       for (int n = 0; n < MT; ++n) acc[n].clear();
 #pragma unroll
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
           uint32_t s[kChain][4];
 #pragma unroll
           for (int k = 0; k < kChain; ++k) a_rows<DK>(s[k], base + W::kState + k * W::kStatePlane, 16 * n, 16 * ks, lane);
-          mma_terms(acc[n], 0, s, x);
+          acc[n].add(s, x);
         }
       }
 #pragma unroll
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
       wait_older();
       if (shares) {
         // D^T <- e^B D^T + (Q^T do)^T - dW^T K^, the chunk's part formed apart
-        Accumulators<2 * SHARE, true> sum[MT];
+        ChainSum<2 * SHARE> sum[MT];
 #pragma unroll
         for (int n = 0; n < MT; ++n) sum[n].clear();
 #pragma unroll
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
             uint32_t w[kChain][4];
 #pragma unroll
             for (int k = 0; k < kChain; ++k) a_rows<C>(w[k], base + W::kW + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
-            mma_terms(sum[n], 0, w, x);
+            sum[n].add(w, x);
           }
         }
 #pragma unroll

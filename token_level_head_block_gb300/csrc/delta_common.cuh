@@ -94,6 +94,36 @@ struct Common {
 };
 enum : uint32_t { kWideQ = 1, kWideK = 2, kWideV = 4, kWideDout = 8 };
 
+// Sums of products of three terms each with their own accumulators for what is of one size: the chain of additions to one is a third
+// as long, and small products are not truncated against large ones.
+template <int NT>
+struct ChainSum {
+  float part[3][NT][4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[s][n][e] = 0.0f;
+  }
+  __device__ __forceinline__ float get(int n, int e) const { return part[0][n][e] + (part[1][n][e] + part[2][n][e]); }
+  template <int NA, int NB, int P>
+  __device__ __forceinline__ void add(const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][P][4]) {
+    constexpr int kMost = NA > NB ? NA : NB;
+#pragma unroll
+    for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+      for (int j = NB - 1; j >= 0; --j) {
+        if (i + j >= kMost) continue;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) mma(part[i + j][2 * p + f], a[i], b[j][p][2 * f], b[j][p][2 * f + 1]);
+      }
+  }
+};
+
 struct ScanArgs {
   Common c;
   const float* init;

@@ -173,7 +173,7 @@ __device__ __forceinline__ void invert_column(const float* L, float (&Z)[TILES][
 
 // One chunk of one (b, h).  Half of the warps have what reads T from the left (K K^T, K^), the others the rest.
 template <typename T, int DK, bool GRAD>
-__global__ void __launch_bounds__(Prepare<T, DK>::kThreads) delta_prepare(const __grid_constant__ Common p) {
+__global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) delta_prepare(const __grid_constant__ Common p) {
   using P = Prepare<T, DK>;
   using L = Lay<T, DK>;
   constexpr int C = L::C, TILES = L::kTiles, SIDES = L::kSides, THREADS = P::kThreads, PITCH = P::kPitch;
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
       const int any = m->any;
       __syncthreads();   // the state's planes are there; the outputs of the chunk before are read
       // W^T = U^T - S^T K^^T, this warp's 16 tokens
-      Accumulators<2, true> acc[MT];
+      ChainSum<2> acc[MT];
 #pragma unroll
       for (int n = 0; n < MT; ++n) acc[n].clear();
 #pragma unroll
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
           uint32_t s[kChain][4];
 #pragma unroll
           for (int k = 0; k < kChain; ++k) a_rows<DK>(s[k], state + k * W::kStatePlane, 16 * n, 16 * ks, lane);
-          mma_terms(acc[n], 0, s, x);
+          acc[n].add(s, x);
         }
       }
 #pragma unroll
@@ -689,7 +689,7 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
       if (shares) {
         // S^T <- e^B S^T + (e^{B-b} W)^T K.  The chunk's sum is formed apart and added once, rounded to nearest: a long
         // sequence must not gather the tensor core's truncation.
-        Accumulators<2 * SHARE, true> sum[MT];
+        ChainSum<2 * SHARE> sum[MT];
 #pragma unroll
         for (int n = 0; n < MT; ++n) sum[n].clear();
 #pragma unroll
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
             uint32_t w[kChain][4];
 #pragma unroll
             for (int k = 0; k < kChain; ++k) a_rows<C>(w[k], base + W::kAfter + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
-            mma_terms(sum[n], 0, w, x);
+            sum[n].add(w, x);
           }
         }
 #pragma unroll
@@ -910,7 +910,7 @@ int64_t delta_chunks(const DeltaProblem& p) {
 
 namespace delta {
 
-bool two_tiles(int64_t BH, int d) { return BH * ((d + 15) / 16) > kSms; }
+bool two_tiles(int64_t BH, int d) { return BH * ((d + 15) / 16) > 2 * kSms; }
 
 int launch_prepare(const Common& c, int64_t BH, int dtype, bool grad, cudaStream_t s) {
   return dtype == MHLA_BF16 ? prepare_type<__nv_bfloat16>(c, BH, grad, s) : prepare_type<float>(c, BH, grad, s);
