@@ -364,6 +364,51 @@ mhla_status_t mhla_forward_noalloc(const mhla_tensor_t* q, const mhla_tensor_t* 
 mhla_status_t mhla_linear(const void* x, const void* w, const void* bias, void* y, int64_t rows, int64_t k,
                           int64_t n_out, void* stream);
 
+/* What a linear layer's result passes through. */
+typedef enum mhla_activation {
+    MHLA_ACT_NONE = 0,
+    MHLA_ACT_RELU = 1,       /* max(z, 0)                                                  */
+    MHLA_ACT_GELU = 2,       /* z (1 + erf(z / sqrt 2)) / 2                                */
+    MHLA_ACT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2          */
+    MHLA_ACT_SILU = 4        /* z / (1 + e^-z)                                             */
+} mhla_activation_t;
+
+/* A linear layer with its activation and residual in one pass over its result:
+ *   z = x w^T + bias,   out = act(z) + residual.
+ *   x         device [rows][k] of dtype (mhla_dtype_t), row-major;  w  device
+ *             [n][k] of the same dtype;  bias  device [n], or NULL.
+ *   residual  device [rows][n], or NULL; may be out itself (added in place).
+ *   pre       receives z [rows][n] (mhla_linear_act_backward takes it), or NULL.
+ *   out       device [rows][n].
+ * Any k >= 1 and n >= 1 up to 2^20, rows < 2^31; every pointer 16-byte aligned
+ * (MHLA_ERR_INVALID_ARG otherwise).  out and pre overlap neither one another nor
+ * an input (out as residual aside).  float32 accumulation, results rounded once;
+ * float32 operands enter the tensor cores as three bf16 terms (2^-24).  rows <= 64
+ * (bf16 with k % 8 == 0; 8 otherwise) run in a kernel of their own that reads w
+ * once.  Operands that TMA does not take as they lie (float32, k % 8 != 0) are laid
+ * out in the workspace.  workspace as for mhla_forward.  Asynchronous on stream;
+ * rows == 0 queues nothing.  The waits are bounded (mhla_device_status). */
+mhla_status_t mhla_linear_act_workspace_size(int64_t rows, int64_t k, int64_t n, int32_t dtype, size_t* bytes);
+mhla_status_t mhla_linear_act(const void* x, const void* w, const void* bias, int32_t activation,
+                              const void* residual, void* pre, void* out, int64_t rows, int64_t k, int64_t n,
+                              int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of mhla_linear_act, given dout = dL/d(out): with dz = dout * act'(pre)
+ * (at 0 the slope of MHLA_ACT_RELU is 0),
+ *   dx = dz w,   dw = dz^T x,   dbias = sum of dz over the rows;
+ * the residual's gradient is dout itself.  pre is z as the forward wrote it
+ * (unused, may be NULL, with MHLA_ACT_NONE).  dz enters both products rounded to
+ * dtype, as the layer's own result does; dbias is summed in float32 before that,
+ * in a fixed order.  dx [rows][k], dw [n][k], dbias [n] of dtype; each may be
+ * NULL when not wanted, none overlaps another or an input.  rows == 0 sets dw
+ * and dbias to zero.  All else as for mhla_linear_act. */
+mhla_status_t mhla_linear_act_backward_workspace_size(int64_t rows, int64_t k, int64_t n, int32_t dtype,
+                                                      int32_t activation, size_t* bytes);
+mhla_status_t mhla_linear_act_backward(const void* x, const void* w, const void* dout, const void* pre,
+                                       int32_t activation, void* dx, void* dw, void* dbias, int64_t rows, int64_t k,
+                                       int64_t n, int32_t dtype, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
 /* LayerNorm over the last axis of a row-major [rows, C] bf16 device array:
  * y = (x - mean) / sqrt(var + eps) * weight + bias with the biased variance and
  * float32 statistics, rounded to bf16 ([P1] section 7, MHLA.norm, an
@@ -431,8 +476,9 @@ mhla_status_t mhla_module_forward(const void* x, void* y, int64_t B, int64_t N, 
  * tokens say and needs the sequence's length in W; this form forgets by a decay
  * that every token brings with it, takes any length, and continues one token at
  * a time from a d x d state, which is how a language model of this kind is
- * served.  The chain a model runs: mhla_linear (q, k, v, decays), mhla_qk_norm,
- * mhla_gated_forward or mhla_gated_step, mhla_linear.
+ * served.  The chain a model runs: mhla_linear or mhla_linear_act (q, k, v,
+ * decays), mhla_qk_norm, mhla_gated_forward or mhla_gated_step (mhla_delta_*),
+ * mhla_linear_act with the residual.
  * ------------------------------------------------------------------------ */
 
 /* The recurrence, per batch b and head h, for t = 0 .. N - 1:

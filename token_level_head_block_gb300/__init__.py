@@ -23,6 +23,7 @@ __all__ = [
     "profile_end", "tensor_desc", "shape3",
     "gated_forward", "gated_workspace_size", "gated_backward", "gated_backward_workspace_size", "gated_step",
     "delta_forward", "delta_workspace_size", "delta_backward", "delta_backward_workspace_size", "delta_step",
+    "linear_act", "linear_act_workspace_size", "linear_act_backward", "linear_act_backward_workspace_size", "ACTIVATIONS",
     "init_rotation", "qk_norm", "qk_norm_backward", "qk_norm_backward_workspace_size",
     "PATHS", "TRANSFORMS", "ROTATION_LAYOUTS",
 ]
@@ -160,6 +161,11 @@ def lib():
     L.mhla_delta_forward.argtypes = [T, T, T, T, T, ctypes.c_float, V, T, V, V, ctypes.c_size_t, V]
     L.mhla_delta_backward.argtypes = [T, T, T, T, T, T, ctypes.c_float, V, V, T, T, T, T, T, V, V, ctypes.c_size_t, V]
     L.mhla_delta_step.argtypes = [T, T, T, T, T, ctypes.c_float, V, T, V]
+    I, Z = ctypes.c_int64, ctypes.c_int32
+    L.mhla_linear_act_workspace_size.argtypes = [I, I, I, Z, P(ctypes.c_size_t)]
+    L.mhla_linear_act_backward_workspace_size.argtypes = [I, I, I, Z, Z, P(ctypes.c_size_t)]
+    L.mhla_linear_act.argtypes = [V, V, V, Z, V, V, V, I, I, I, Z, V, ctypes.c_size_t, V]
+    L.mhla_linear_act_backward.argtypes = [V, V, V, V, Z, V, V, V, I, I, I, Z, V, ctypes.c_size_t, V]
     L.mhla_init_rotation.argtypes = [P(Shape3), P(ctypes.c_int32), ctypes.c_double, P(ctypes.c_float),
                                      ctypes.c_int64]
     L.mhla_qk_norm.argtypes = [T, T, V, V, ctypes.c_float, P(Rotation), T, T, V]
@@ -169,6 +175,8 @@ def lib():
     for name in ("mhla_gated_workspace_size", "mhla_gated_backward_workspace_size", "mhla_gated_forward",
                  "mhla_gated_backward", "mhla_gated_step", "mhla_delta_workspace_size",
                  "mhla_delta_backward_workspace_size", "mhla_delta_forward", "mhla_delta_backward", "mhla_delta_step",
+                 "mhla_linear_act_workspace_size", "mhla_linear_act_backward_workspace_size", "mhla_linear_act",
+                 "mhla_linear_act_backward",
                  "mhla_init_rotation", "mhla_qk_norm",
                  "mhla_qk_norm_backward_workspace_size", "mhla_qk_norm_backward"):
         getattr(L, name).restype = ctypes.c_int
@@ -748,6 +756,98 @@ def delta_step(q, k, v, g, beta, state, scale=1.0, out=None, stream=None):
     _same_device(v, q, k, g, beta, out)
     _launch("mhla_delta_step", lib().mhla_delta_step, args, v)
     return out
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def linear_act_workspace_size(rows, k, n, dtype):
+    """dtype: "bf16" or "f32"."""
+    n_bytes = ctypes.c_size_t(0)
+    _check(lib().mhla_linear_act_workspace_size(rows, k, n, DTYPES[dtype], ctypes.byref(n_bytes)),
+           "mhla_linear_act_workspace_size")
+    return n_bytes.value
+
+
+def linear_act_backward_workspace_size(rows, k, n, dtype, activation="none"):
+    n_bytes = ctypes.c_size_t(0)
+    _check(lib().mhla_linear_act_backward_workspace_size(rows, k, n, DTYPES[dtype], ACTIVATIONS[activation],
+                                                         ctypes.byref(n_bytes)), "mhla_linear_act_backward_workspace_size")
+    return n_bytes.value
+
+
+def _dense(name, x, shape, like, code):
+    """Address of a contiguous tensor of this shape, of like's type and device; None for None."""
+    if x is None:
+        return None
+    if tuple(x.shape) != shape or not x.is_contiguous() or _dtype_code(x) != code:
+        raise ValueError(f"{name} must be a contiguous {like.dtype} tensor of shape {list(shape)}")
+    if x.get_device() != like.get_device():
+        raise ValueError(f"{name} is on {x.device}, not on {like.device}")
+    return x.data_ptr()
+
+
+def _linear_sizes(x, w, activation):
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}")
+    if w.dim() != 2 or x.dim() < 1 or x.shape[-1] != w.shape[1]:
+        raise ValueError(f"x {list(x.shape)} does not meet w {list(w.shape)}")
+    if x.get_device() < 0:
+        raise ValueError("expected CUDA tensors")
+    n, k = w.shape
+    return x.numel() // k if k else 0, k, n, _dtype_code(x)
+
+
+def linear_act(x, w, bias=None, activation="none", residual=None, out=None, pre=None, workspace=None, stream=None):
+    """act(x w^T + bias) + residual for a contiguous CUDA tensor x [..., k] (bf16 or float32) and
+    w [n, k], bias [n], residual [..., n] of its type.  ``activation``: none, relu, gelu, gelu_tanh
+    or silu.  ``pre`` ([..., n]), when given, receives x w^T + bias.  Returns ``out``, which may be
+    residual.  ``stream`` as for ``gated_forward``."""
+    import torch
+    if stream is not None:
+        with _on(stream, x):
+            return linear_act(x, w, bias, activation, residual, out, pre, workspace)
+    rows, k, n, code = _linear_sizes(x, w, activation)
+    shape = (*x.shape[:-1], n)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    args = (_dense("x", x, tuple(x.shape), x, code), _dense("w", w, (n, k), x, code), _dense("bias", bias, (n,), x, code),
+            ACTIVATIONS[activation], _dense("residual", residual, shape, x, code), _dense("pre", pre, shape, x, code),
+            _dense("out", out, shape, x, code), rows, k, n, code)
+    L = lib()
+    _launch("mhla_linear_act", L.mhla_linear_act, args, x, workspace,
+            lambda: _size(L.mhla_linear_act_workspace_size, "mhla_linear_act_workspace_size", rows, k, n, code))
+    return out
+
+
+def linear_act_backward(x, w, dout, activation="none", pre=None, bias=True, dx=None, dw=None, dbias=None, workspace=None,
+                        stream=None):
+    """Gradients (dx, dw, dbias) of ``linear_act`` given dout [..., n] and, with an activation, ``pre`` as
+    the forward left it; the residual's gradient is dout.  bias False: dbias is None.  ``stream`` as
+    for ``gated_forward``."""
+    import torch
+    if stream is not None:
+        with _on(stream, x):
+            return linear_act_backward(x, w, dout, activation, pre, bias, dx, dw, dbias, workspace)
+    rows, k, n, code = _linear_sizes(x, w, activation)
+    shape = (*x.shape[:-1], n)
+    if activation == "none":
+        pre = None
+    elif pre is None:
+        raise ValueError(f"{activation} needs pre")
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx
+    dw = torch.empty(w.shape, dtype=w.dtype, device=x.device) if dw is None else dw
+    if bias and dbias is None:
+        dbias = torch.empty((n,), dtype=x.dtype, device=x.device)
+    act = ACTIVATIONS[activation]
+    args = (_dense("x", x, tuple(x.shape), x, code), _dense("w", w, (n, k), x, code), _dense("dout", dout, shape, x, code),
+            _dense("pre", pre, shape, x, code), act, _dense("dx", dx, tuple(x.shape), x, code), _dense("dw", dw, (n, k), x, code),
+            _dense("dbias", dbias, (n,), x, code) if bias else None, rows, k, n, code)
+    L = lib()
+    _launch("mhla_linear_act_backward", L.mhla_linear_act_backward, args, x, workspace,
+            lambda: _size(L.mhla_linear_act_backward_workspace_size, "mhla_linear_act_backward_workspace_size", rows, k, n,
+                          code, act))
+    return dx, dw, dbias if bias else None
 
 
 def init_rotation(grid, pairs, base=10000.0):

@@ -25,6 +25,7 @@ CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-ffp-contract=off", f"-I{INCLUDE}"]
 CUDA_SOURCES = ["mhla_api.cu", "simt_kernels.cu", "tc_kernels.cu", "tc_summary.cu", "tc_mix.cu", "tc_output.cu", "tc_fused.cu",
                 "small_kernels.cu", "bwd_tc_kernels.cu", "causal_tc_kernels.cu", "profile.cu", "noalloc.cu",
                 "module_kernels.cu", "gemm_kernels.cu", "sequence_api.cu", "gated_kernels.cu", "gated_tc_kernels.cu", "delta_forward.cu", "delta_backward.cu",
+                "linear_kernels.cu",
                 "qk_norm_kernels.cu"]
 CXX_SOURCES = ["mhla_init.cpp"]
 HEADERS = ["mhla_internal.h", "api_checks.h", "gated_common.cuh", "warp_mma.cuh", "delta_common.cuh", "float_pairs.cuh", "ptx.cuh", "tma_host.h", "tc_common.cuh", "tc_fwd_bodies.cuh", "stall_hook.cuh"]

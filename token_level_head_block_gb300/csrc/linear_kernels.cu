@@ -1,0 +1,830 @@
+// A linear layer with its activation and residual, and its gradients:
+//   out = act(z) + residual,  z = x w^T + bias         x [rows][k], w [n][k]
+//   dz = dout act'(z),  dx = dz w,  dw = dz^T x,  dbias = sum of dz's rows
+// All three products are one kernel, linear_gemm, C [M][N] = A B over tcgen05:
+//   out   A = x    [M][K]     B = w  [N][K]
+//   dx    A = dz   [M][K]     B = w  [K][N]   (read as it lies: N-major)
+//   dw    A = dz   [K][M]     B = x  [K][N]   (both read as they lie)
+// bf16 matrices whose rows are a multiple of 16 bytes go to TMA as they are.  Others, and float32 ones, are laid out
+// first (linear_planes): rows padded to 16 bytes, float32 as the sum of three bf16 terms (2^-24), of whose products the six
+// that are not below 2^-24 are formed.  The tensor core truncates what it adds to an accumulator, so float32 keeps
+// its small products apart and its large ones in three accumulators, a third of K each, added in the epilogue.
+//
+// Few rows (serving) read w once and compute next to nothing: linear_rows gives every CTA 16 of w's rows and
+// its warps a part of K each.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "gated_common.cuh"
+#include "mhla_internal.h"
+#include "ptx.cuh"
+#include "tc_common.cuh"
+#include "tma_host.h"
+#include "warp_mma.cuh"
+
+namespace mhla {
+
+__device__ unsigned int g_linear_error = 0;
+
+namespace {
+
+using namespace ptx;
+using namespace tc;
+
+using gated::from_f;
+using gated::low;
+using gated::high;
+using gated::to_f;
+
+// ----------------------------------------------------------------- activations
+
+// 1 / (1 + e^-z); FAST for results that are rounded to bf16 (2^-8; ex2 and the reciprocal are good to 2^-21).
+template <bool FAST>
+__device__ __forceinline__ float over_sigmoid(float z) { return 1.0f + (FAST ? __expf(-z) : expf(-z)); }
+
+constexpr float kTanhScale = 0.7978845608028654f, kTanhCube = 0.044715f;   // sqrt(2 / pi)
+
+template <bool FAST>
+__device__ __forceinline__ float activate(float z, int act) {
+  switch (act) {
+    case MHLA_ACT_RELU: return z < 0.0f ? 0.0f : z;   // NaN stays
+    case MHLA_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
+    case MHLA_ACT_GELU_TANH: {   // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+      const float u = kTanhScale * fmaf(kTanhCube * z * z, z, z);
+      return FAST ? __fdividef(z, over_sigmoid<true>(2.0f * u)) : z / over_sigmoid<false>(2.0f * u);
+    }
+    case MHLA_ACT_SILU: return FAST ? __fdividef(z, over_sigmoid<true>(z)) : z / over_sigmoid<false>(z);
+    default: return z;
+  }
+}
+
+__device__ __forceinline__ float slope(float z, int act) {
+  switch (act) {
+    case MHLA_ACT_RELU: return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
+    case MHLA_ACT_GELU:
+      return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) + z * 0.3989422804014327f * expf(-0.5f * z * z);
+    case MHLA_ACT_GELU_TANH: {
+      z = z > 30.0f ? 30.0f : z < -30.0f ? -30.0f : z;   // 1 and 0 there; the cube stays finite
+      const float u = kTanhScale * fmaf(kTanhCube * z * z, z, z), p = 1.0f / over_sigmoid<false>(2.0f * u);
+      return p + z * p * (1.0f - p) * (2.0f * kTanhScale) * fmaf(3.0f * kTanhCube * z, z, 1.0f);
+    }
+    case MHLA_ACT_SILU: {
+      const float p = 1.0f / over_sigmoid<false>(z);
+      return p * fmaf(z, 1.0f - p, 1.0f);
+    }
+    default: return 1.0f;
+  }
+}
+
+// ----------------------------------------------------------------- epilogue
+
+struct Finish {
+  void* out;             // [M][N] of the call's type
+  void* pre;             // z, or null
+  const void* residual;  // [M][N], or null; may be out
+  const void* bias;      // [N], or null
+  int64_t M, N;
+  int32_t act, f32;
+  int32_t quads;         // N % 4 == 0: four values an access
+};
+
+__device__ __forceinline__ float4 load_quad(const void* p, int64_t i, int f32) {
+  if (f32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+  const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
+  return make_float4(low(x.x), high(x.x), low(x.y), high(x.y));
+}
+__device__ __forceinline__ void store_quad(void* p, int64_t i, int f32, float4 x) {
+  if (f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = x;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) = make_uint2(gated::pack(x.x, x.y), gated::pack(x.z, x.w));
+}
+__device__ __forceinline__ float load_one(const void* p, int64_t i, int f32) {
+  return f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void store_one(void* p, int64_t i, int f32, float x) {
+  if (f32)
+    static_cast<float*>(p)[i] = x;
+  else
+    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+}
+
+// Four sums of row r, columns c .. c + 3 (r < M, c < N).
+template <bool FAST>
+__device__ __forceinline__ void finish_quad(const Finish& f, int64_t r, int64_t c, float4 z, float4 bias) {
+  const int64_t i = r * f.N + c;
+  z.x += bias.x; z.y += bias.y; z.z += bias.z; z.w += bias.w;
+  if (f.quads) {
+    if (f.pre) store_quad(f.pre, i, f.f32, z);
+    float4 y = make_float4(activate<FAST>(z.x, f.act), activate<FAST>(z.y, f.act), activate<FAST>(z.z, f.act), activate<FAST>(z.w, f.act));
+    if (f.residual) {
+      const float4 s = load_quad(f.residual, i, f.f32);
+      y.x += s.x; y.y += s.y; y.z += s.z; y.w += s.w;
+    }
+    store_quad(f.out, i, f.f32, y);
+  } else {
+    const float zs[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (c + e >= f.N) break;
+      if (f.pre) store_one(f.pre, i + e, f.f32, zs[e]);
+      float y = activate<FAST>(zs[e], f.act);
+      if (f.residual) y += load_one(f.residual, i + e, f.f32);
+      store_one(f.out, i + e, f.f32, y);
+    }
+  }
+}
+
+__device__ __forceinline__ float4 bias_quad(const Finish& f, int64_t c) {
+  float b[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b[e] = f.bias && c + e < f.N ? load_one(f.bias, c + e, f.f32) : 0.0f;
+  return make_float4(b[0], b[1], b[2], b[3]);
+}
+
+// ----------------------------------------------------------------- product
+
+struct Product {
+  CUtensorMap a, b;
+  Finish f;
+  float* parts;          // [splits][M][pitch] sums of parts of K, or null
+  int64_t pitch, units;
+  int32_t a_major, b_major;   // 1: the operand lies [K][M] ([K][N])
+  int32_t BN, tiles_n, chunks, splits, split_chunks;
+};
+
+template <int TERMS>
+struct GemmLay {
+  static constexpr int BM = 128, BK = 64;
+  static constexpr int MOST_N = TERMS == 1 ? 256 : 128;
+  static constexpr int A_BYTES = BM * BK * 2, B_BYTES = MOST_N * BK * 2;
+  static constexpr int STAGE = TERMS * (A_BYTES + B_BYTES), NS = TERMS == 1 ? 4 : 2;
+  static constexpr int ACCS = TERMS == 1 ? 2 : 1;        // tiles whose sums tensor memory holds
+  static constexpr int MAINS = TERMS == 1 ? 1 : 3;       // accumulators of the large products
+  static constexpr int PITCH = 20, STAGING = 32 * PITCH * 4;   // a warp's 32 rows of 16 columns
+  static constexpr int WARPS = 8, THREADS = 64 + 32 * WARPS;
+  static constexpr size_t SMEM = static_cast<size_t>(NS) * STAGE + WARPS * STAGING + 1024 + 1024;
+};
+
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  return wait_bounded_on(bar, parity, abort_flag, &g_linear_error);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  return warp_wait_on(bar, parity, abort_flag, &g_linear_error);
+}
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) { drain_wait_on(bar, parity, &g_linear_error); }
+
+// Unit u: a tile and a part of K.
+struct Unit {
+  int32_t m0, n0, first, count, split;
+};
+__device__ __forceinline__ Unit unit_of(const Product& p, int64_t u) {
+  Unit r;
+  r.split = static_cast<int32_t>(u % p.splits);
+  const int64_t t = u / p.splits;
+  r.n0 = static_cast<int32_t>(t % p.tiles_n) * p.BN;
+  r.m0 = static_cast<int32_t>(t / p.tiles_n) * 128;
+  r.first = r.split * p.split_chunks;
+  r.count = min(p.split_chunks, p.chunks - r.first);
+  return r;
+}
+
+// Persistent CTAs walk the units, neighbours sharing A's rows in L2.  Warp 0 loads K chunks of 64 (a ring of
+// stages), warp 1 issues the MMAs, eight warps turn the sums round through shared memory, so that a row's columns lie in
+// neighbouring lanes, and finish them.
+template <int TERMS>
+__global__ void __launch_bounds__(GemmLay<TERMS>::THREADS, 1) linear_gemm(const __grid_constant__ Product p) {
+  using L = GemmLay<TERMS>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
+  uint8_t* staging = smem + L::NS * L::STAGE;
+  uint8_t* ctrl = staging + L::WARPS * L::STAGING;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
+  uint64_t* empty = full + L::NS;
+  uint64_t* tfull = empty + L::NS;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* fin = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 512);
+  volatile uint32_t* abortf = tmem_slot + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::NS; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull + a, 1);
+      mbar_init(tempty + a, 32 * L::WARPS);
+    }
+    mbar_init(fin, 1);
+    *abortf = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&p.a);
+    prefetch_tmap(&p.b);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t policy = policy_evict_last();
+      int s = 0;
+      uint32_t ph = 0;
+      uint64_t fills = 0;
+      bool ok = true;
+      const uint32_t bytes = TERMS * (L::A_BYTES + p.BN * L::BK * 2);
+      for (int64_t u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
+        const Unit un = unit_of(p, u);
+        for (int kc = 0; kc < un.count; ++kc) {
+          if (!wait_bounded(empty + s, ph ^ 1u, abortf)) { ok = false; break; }
+          mbar_arrive_expect_tx(full + s, bytes);
+          uint8_t* st = smem + s * L::STAGE;
+          const int32_t k0 = (un.first + kc) * L::BK;
+#pragma unroll
+          for (int t = 0; t < TERMS; ++t) {
+            uint8_t* at = st + t * L::A_BYTES;
+            if (p.a_major) {
+              tma_load_3d(at, &p.a, full + s, un.m0, k0, t, policy);
+              tma_load_3d(at + 8192, &p.a, full + s, un.m0 + 64, k0, t, policy);
+            } else {
+              tma_load_3d(at, &p.a, full + s, k0, un.m0, t, policy);
+            }
+            at = st + TERMS * L::A_BYTES + t * L::B_BYTES;
+            if (p.b_major) {
+              for (int j = 0; j < p.BN / 64; ++j) tma_load_3d(at + 8192 * j, &p.b, full + s, un.n0 + 64 * j, k0, t, policy);
+            } else {
+              tma_load_3d(at, &p.b, full + s, k0, un.n0, t, policy);
+            }
+          }
+          ++fills;
+          if (++s == L::NS) { s = 0; ph ^= 1u; }
+        }
+      }
+      for (int st = 0; st < L::NS; ++st) {
+        const uint64_t n = fills / L::NS + (static_cast<uint64_t>(st) < fills % L::NS ? 1 : 0);
+        if (n > 0) drain_wait(full + st, static_cast<uint32_t>((n - 1) & 1));
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(L::BM, p.BN, p.a_major != 0, p.b_major != 0);
+      // steps of 16 of K: 32 bytes along swizzled rows, or 16 rows of 128 bytes
+      const uint32_t a_step = p.a_major ? 2048 : 32, b_step = p.b_major ? 2048 : 32;
+      const uint32_t a_lbo = p.a_major ? 8192 : 16, b_lbo = p.b_major ? 8192 : 16;
+      int s = 0;
+      uint32_t ph = 0, local = 0;
+      bool ok = true;
+      for (int64_t u = blockIdx.x; ok && u < p.units; u += gridDim.x, ++local) {
+        const Unit un = unit_of(p, u);
+        const uint32_t acc = local % L::ACCS, aph = (local / L::ACCS) & 1u;
+        if (!wait_bounded(tempty + acc, aph ^ 1u, abortf)) break;
+        tc_fence_after();
+        const uint32_t dt = tmem + acc * 256;
+        for (int kc = 0; kc < un.count; ++kc) {
+          if (!wait_bounded(full + s, ph, abortf)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a_base = smem_u32(smem + s * L::STAGE), b_base = a_base + TERMS * L::A_BYTES;
+          // the accumulator of this part of K, and whether it is empty yet
+          const int main = L::MAINS * kc / un.count;
+          const bool opens = kc == (main * un.count + L::MAINS - 1) / L::MAINS;
+#pragma unroll
+          for (int ks = 0; ks < L::BK / 16; ++ks)
+#pragma unroll
+            for (int i = TERMS - 1; i >= 0; --i)
+#pragma unroll
+              for (int j = TERMS - 1 - i; j >= 0; --j) {
+                const bool large = i + j == 0;
+                const uint64_t a = smem_desc(a_base + i * L::A_BYTES + ks * a_step, a_lbo, 1024, 2);
+                const uint64_t b = smem_desc(b_base + j * L::B_BYTES + ks * b_step, b_lbo, 1024, 2);
+                const bool first = large ? opens && ks == 0 : kc == 0 && ks == 0 && i == TERMS - 1;
+                mma_bf16(dt + (large ? 128 * main : 128 * L::MAINS), a, b, idesc, first ? 0u : 1u);
+              }
+          mma_commit(empty + s);
+          if (++s == L::NS) { s = 0; ph ^= 1u; }
+        }
+        if (!ok) break;
+        mma_commit(tfull + acc);
+      }
+      mma_commit(fin);
+      drain_wait(fin, 0);
+    }
+  } else {
+    const int q4 = warp & 3, half = (warp - 2) >> 2;   // TMEM lane quarter this warp may read; its half of the columns
+    float* stage = reinterpret_cast<float*>(staging + (warp - 2) * L::STAGING);
+    uint32_t local = 0;
+    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x, ++local) {
+      const Unit un = unit_of(p, u);
+      const uint32_t acc = local % L::ACCS, aph = (local / L::ACCS) & 1u;
+      if (!warp_wait(tfull + acc, aph, abortf)) break;
+      tc_fence_after();
+      const uint32_t tb = tmem + acc * 256 + (static_cast<uint32_t>(32 * q4) << 16);
+      const int groups = p.BN / 16, mine = groups / 2;   // BN is a multiple of 64
+      const int mains = TERMS == 1 ? 1 : min(un.count, L::MAINS);
+#pragma unroll 1
+      for (int gi = 0; gi < mine; ++gi) {
+        const int col = 16 * (half * mine + gi);
+        uint32_t v[16];
+        tmem_ld_x16(tb + col, v);
+        if (TERMS > 1) {
+          uint32_t x[16], y[16], z[16];
+          tmem_ld_x16(tb + 128 * L::MAINS + col, z);
+          if (mains > 1) tmem_ld_x16(tb + 128 + col, x);
+          if (mains > 2) tmem_ld_x16(tb + 256 + col, y);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float sum = __uint_as_float(z[e]);
+            if (mains > 2) sum += __uint_as_float(y[e]);
+            if (mains > 1) sum += __uint_as_float(x[e]);
+            v[e] = __float_as_uint(__uint_as_float(v[e]) + sum);
+          }
+        } else {
+          tmem_ld_wait();
+        }
+        if (gi + 1 == mine) {   // the sums are read out
+          tc_fence_before();
+          mbar_arrive(tempty + acc);
+        }
+        if (un.n0 + col >= p.f.N) continue;   // the same for every lane
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4*>(stage + lane * L::PITCH + 4 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        __syncwarp();
+        const int64_t c = un.n0 + col + 4 * (lane & 3);
+        if (c < p.f.N) {
+          const float4 bias = p.parts ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : bias_quad(p.f, c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2);
+            const int64_t row = un.m0 + 32 * q4 + r;
+            if (row < p.f.M) {
+              const float4 z = *reinterpret_cast<const float4*>(stage + r * L::PITCH + 4 * (lane & 3));
+              if (p.parts)
+                *reinterpret_cast<float4*>(p.parts + (un.split * p.f.M + row) * p.pitch + c) = z;
+              else
+                finish_quad<TERMS == 1>(p.f, row, c, z, bias);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Sums of the parts of K, finished.
+struct Join {
+  Finish f;
+  const float* parts;
+  int64_t pitch;
+  int32_t splits;
+};
+template <bool FAST>
+__global__ void __launch_bounds__(256) linear_join(const __grid_constant__ Join p) {
+  const int64_t i = 4 * (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x), total = p.f.M * p.pitch;
+  if (i >= total) return;
+  const int64_t r = i / p.pitch, c = i % p.pitch;
+  if (c >= p.f.N) return;
+  float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int s = 0; s < p.splits; ++s) {
+    const float4 x = *reinterpret_cast<const float4*>(p.parts + s * total + i);
+    z.x += x.x; z.y += x.y; z.z += x.z; z.w += x.w;
+  }
+  finish_quad<FAST>(p.f, r, c, z, bias_quad(p.f, c));
+}
+
+// ----------------------------------------------------------------- planes
+
+// [rows][cols] as TERMS planes of bf16 rows `pitch` apart; with `pre`, times the activation's slope there.  Column sums
+// of what is laid out (in float32) by blocks of rows to `sums` [blocks][cols], or null; dst null: the sums alone.
+struct Planes {
+  const void* src;
+  const void* pre;
+  __nv_bfloat16* dst;
+  float* sums;
+  int64_t rows, cols, pitch, block_rows;
+  int32_t act, f32;
+};
+
+// A thread has VEC columns; 32 threads side by side, eight rows at once.
+template <int TERMS, int VEC>
+__global__ void __launch_bounds__(256) linear_planes(const __grid_constant__ Planes p) {
+  __shared__ float part[8][32 * VEC];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + x) * VEC;
+  const int64_t first = blockIdx.y * p.block_rows, last = min(p.rows, first + p.block_rows);
+  float sum[VEC] = {};
+  if (c < p.cols) {
+#pragma unroll 2
+    for (int64_t r = first + y; r < last; r += 8) {
+      const int64_t i = r * p.cols + c;
+      float v[VEC], z[VEC];
+      if constexpr (VEC == 4) {
+        const float4 q = load_quad(p.src, i, p.f32);
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+        if (p.pre) {
+          const float4 w = load_quad(p.pre, i, p.f32);
+          z[0] = w.x; z[1] = w.y; z[2] = w.z; z[3] = w.w;
+        }
+      } else {
+        v[0] = load_one(p.src, i, p.f32);
+        if (p.pre) z[0] = load_one(p.pre, i, p.f32);
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        if (p.pre) v[e] *= slope(z[e], p.act);
+        sum[e] += v[e];
+      }
+      if (!p.dst) continue;
+#pragma unroll
+      for (int t = 0; t < TERMS; ++t) {
+        __nv_bfloat16* to = p.dst + (t * p.rows + r) * p.pitch + c;
+        float h[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) h[e] = __bfloat162float(__float2bfloat16_rn(v[e]));
+        if constexpr (VEC == 4) {
+          *reinterpret_cast<uint2*>(to) = make_uint2(gated::pack(h[0], h[1]), gated::pack(h[2], h[3]));
+        } else {
+          from_f(to, h[0]);
+        }
+        // an infinity is its first term alone
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] = fabsf(h[e]) < __int_as_float(0x7F800000) ? v[e] - h[e] : 0.0f;
+      }
+    }
+  }
+  if (!p.sums) return;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) part[y][x * VEC + e] = sum[e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * VEC; i += 256) {
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 * VEC + i;
+    if (col >= p.cols) continue;
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += part[j][i];
+    p.sums[blockIdx.y * p.cols + col] = s;
+  }
+}
+
+// Column sums of the blocks, in their order: one warp a column.
+__global__ void __launch_bounds__(256) linear_column_sums(const float* sums, void* out, int64_t cols, int32_t blocks, int32_t f32) {
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (c >= cols) return;
+  const int lane = threadIdx.x & 31;
+  float s = 0.0f;
+  for (int b = lane; b < blocks; b += 32) s += sums[b * cols + c];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+  if (lane == 0) store_one(out, c, f32, s);
+}
+
+// ----------------------------------------------------------------- few rows
+
+// 16 of w's rows and ROWS (a multiple of 8) of x's.  Each of eight warps takes every eighth step of K and holds its operands straight from
+// memory: a lane's 16 bytes of a row are k = 8 (lane % 4) .. + 7 of a step of 32, and enter two MMAs as the k that its
+// place stands for; w and x agree on which, so the sum is the same.
+template <int GROUPS>   // of eight rows
+__global__ void __launch_bounds__(256) linear_rows(const __nv_bfloat16* x, const __nv_bfloat16* w, int64_t rows, int32_t k, const Finish f) {
+  __shared__ float part[8][16][8 * GROUPS + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16, r0 = static_cast<int64_t>(blockIdx.y) * 8 * GROUPS;
+  float acc[GROUPS][4] = {};
+  const __nv_bfloat16 *w0 = w + (n0 + g) * k + 8 * t, *w1 = w0 + 8 * static_cast<int64_t>(k);
+  const bool in0 = n0 + g < f.N, in1 = n0 + g + 8 < f.N;
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 2
+  for (int k0 = 32 * warp; k0 < k; k0 += 256) {
+    const bool in = k0 + 8 * t < k;   // k % 8 == 0
+    const uint4 a0 = in && in0 ? __ldg(reinterpret_cast<const uint4*>(w0 + k0)) : none;
+    const uint4 a1 = in && in1 ? __ldg(reinterpret_cast<const uint4*>(w1 + k0)) : none;
+    const uint32_t first[4] = {a0.x, a1.x, a0.y, a1.y}, second[4] = {a0.z, a1.z, a0.w, a1.w};
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) {
+      const int64_t r = r0 + 8 * i + g;
+      const uint4 b = in && r < rows ? __ldg(reinterpret_cast<const uint4*>(x + r * k + k0 + 8 * t)) : none;
+      gated::mma(acc[i], first, b.x, b.y);
+      gated::mma(acc[i], second, b.z, b.w);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < GROUPS; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[warp][g + 8 * (e >> 1)][8 * i + 2 * t + (e & 1)] = acc[i][e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 4 * 8 * GROUPS; i += 256) {
+    const int r = i / 4, c = 4 * (i % 4);
+    if (r0 + r >= rows || n0 + c >= f.N) continue;
+    float z[4] = {};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[e] += part[j][c + e][r];
+    finish_quad<true>(f, r0 + r, n0 + c, make_float4(z[0], z[1], z[2], z[3]), bias_quad(f, n0 + c));
+  }
+}
+
+// Float32 and rows that 16-byte loads do not take: a warp has one of w's rows and eight of x's.
+template <typename T>
+__global__ void __launch_bounds__(256) linear_dots(const T* x, const T* w, int64_t rows, int32_t k, const Finish f) {
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5), r0 = static_cast<int64_t>(blockIdx.y) * 8;
+  const int lane = threadIdx.x & 31;
+  if (n >= f.N) return;
+  float acc[8] = {};
+  const int m = static_cast<int>(min(rows - r0, int64_t{8}));
+#pragma unroll 4
+  for (int i = lane; i < k; i += 32) {
+    const float a = to_f(w[n * k + i]);
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      if (r < m) acc[r] = fmaf(a, to_f(x[(r0 + r) * k + i]), acc[r]);
+  }
+  float mine = 0.0f;
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc[r] += __shfl_xor_sync(~0u, acc[r], o);
+    if (lane == r) mine = acc[r];
+  }
+  if (lane >= m) return;
+  const int64_t i = (r0 + lane) * f.N + n;
+  const float z = mine + (f.bias ? load_one(f.bias, n, f.f32) : 0.0f);
+  if (f.pre) store_one(f.pre, i, f.f32, z);
+  float y = activate<false>(z, f.act);
+  if (f.residual) y += load_one(f.residual, i, f.f32);
+  store_one(f.out, i, f.f32, y);
+}
+
+// ----------------------------------------------------------------- host
+
+constexpr int kSms = 152;
+
+struct Matrix {          // [terms][rows][pitch] of bf16, cols of them used
+  const void* data;
+  int64_t rows, cols, pitch;
+};
+
+bool direct(int64_t cols, int dtype) { return dtype == MHLA_BF16 && cols % 8 == 0; }
+int64_t plane_pitch(int64_t cols) { return (cols + 7) / 8 * 8; }
+size_t plane_bytes(int64_t rows, int64_t cols, int dtype) {
+  return align_up(static_cast<size_t>(rows * plane_pitch(cols)) * 2 * (dtype == MHLA_BF16 ? 1 : 3));
+}
+
+bool encode_planes(CUtensorMap* m, const Matrix& x, int terms, int box_cols, int box_rows) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(x.cols), static_cast<cuuint64_t>(x.rows), static_cast<cuuint64_t>(terms)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(x.pitch * 2), static_cast<cuuint64_t>(x.rows * x.pitch * 2)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+  return encode_tensor_map(m, 3, const_cast<void*>(x.data), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// How C [M][N] over K is cut.  Time of a unit: its chunks, by the operand bytes of one (a chunk of 128 + 256 rows takes about
+// 0.55 us under full load), and what its epilogue leaves uncovered.  K is split where there are few tiles.
+struct Cutting {
+  int BN, tiles_n, chunks, splits, split_chunks;
+  int64_t tiles;
+};
+Cutting cut_product(int64_t M, int64_t N, int64_t K, int dtype) {
+  const bool f32 = dtype != MHLA_BF16;
+  Cutting best = {};
+  double least = 0;
+  const int chunks = static_cast<int>((K + 63) / 64);
+  for (int BN : {64, 128, 192, 256}) {
+    if (f32 && BN > 128) break;
+    Cutting c = {};
+    c.BN = BN;
+    c.chunks = chunks;
+    c.tiles_n = static_cast<int>((N + BN - 1) / BN);
+    c.tiles = (M + 127) / 128 * c.tiles_n;
+    const double chunk_us = (f32 ? 3.0 : 1.0) * 0.55 * (128 + BN) / 384, tail_us = 1.5 + 0.01 * BN;
+    for (int splits = 1; splits <= 64; splits = splits < 8 ? splits + 1 : 2 * splits) {
+      if (splits > 1 && (splits > chunks || c.tiles * (splits - 1) >= 2 * kSms)) break;
+      const int each = (chunks + splits - 1) / splits, used = (chunks + each - 1) / each;
+      const int64_t waves = (c.tiles * used + kSms - 1) / kSms;
+      // the parts are written and read: 8 bytes a value at 4 bytes a ns and part, and a launch
+      const double us = waves * (each * chunk_us) + tail_us * (waves > 1 ? 1.3 : 1.0) +
+                        (used > 1 ? 3.0 + 8e-6 * static_cast<double>(used) * M * N / 4 : 0.0);
+      if (best.BN == 0 || us < least) {
+        least = us;
+        best = c;
+        best.splits = used;
+        best.split_chunks = each;
+      }
+    }
+  }
+  return best;
+}
+size_t part_bytes(int64_t M, int64_t N, const Cutting& c) {
+  return c.splits < 2 ? 0 : align_up(static_cast<size_t>(c.splits) * M * ((N + 3) / 4 * 4) * 4);
+}
+
+int run_product(const char* name, const Matrix& a, bool a_major, const Matrix& b, bool b_major, int64_t M, int64_t N, int64_t K,
+                int dtype, const Finish& f, char* parts, cudaStream_t s) {
+  const int terms = dtype == MHLA_BF16 ? 1 : 3;
+  const Cutting c = cut_product(M, N, K, dtype);
+  Product p = {};
+  if (!encode_planes(&p.a, a, terms, 64, a_major ? 64 : 128) || !encode_planes(&p.b, b, terms, 64, b_major ? 64 : c.BN))
+    return MHLA_ERR_CUDA;
+  p.f = f;
+  p.parts = c.splits > 1 ? reinterpret_cast<float*>(parts) : nullptr;
+  p.pitch = (N + 3) / 4 * 4;
+  p.units = c.tiles * c.splits;
+  p.a_major = a_major; p.b_major = b_major;
+  p.BN = c.BN; p.tiles_n = c.tiles_n; p.chunks = c.chunks; p.splits = c.splits; p.split_chunks = c.split_chunks;
+  const int sms = device_sm_count();
+  if (sms <= 0) return MHLA_ERR_CUDA;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.units, sms));
+  {
+    KernelTimer timer(name, s);
+    if (terms == 1) {
+      using L = GemmLay<1>;
+      if (cudaFuncSetAttribute(linear_gemm<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L::SMEM)) != cudaSuccess)
+        return MHLA_ERR_CUDA;
+      linear_gemm<1><<<grid, L::THREADS, L::SMEM, s>>>(p);
+    } else {
+      using L = GemmLay<3>;
+      if (cudaFuncSetAttribute(linear_gemm<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L::SMEM)) != cudaSuccess)
+        return MHLA_ERR_CUDA;
+      linear_gemm<3><<<grid, L::THREADS, L::SMEM, s>>>(p);
+    }
+    if (cudaGetLastError() != cudaSuccess) return MHLA_ERR_CUDA;
+  }
+  if (c.splits < 2) return MHLA_OK;
+  const Join j = {f, p.parts, p.pitch, c.splits};
+  KernelTimer timer("linear_join", s);
+  const unsigned blocks = static_cast<unsigned>((M * p.pitch / 4 + 255) / 256);
+  if (terms == 1)
+    linear_join<true><<<blocks, 256, 0, s>>>(j);
+  else
+    linear_join<false><<<blocks, 256, 0, s>>>(j);
+  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+}
+
+int run_planes(Planes p, int dtype, int64_t row_blocks, cudaStream_t s) {
+  p.f32 = dtype != MHLA_BF16;
+  p.block_rows = (p.rows + row_blocks - 1) / row_blocks;
+  const bool quads = p.cols % 4 == 0;
+  const int64_t wide = quads ? 128 : 32;
+  const dim3 grid(static_cast<unsigned>((p.cols + wide - 1) / wide), static_cast<unsigned>(row_blocks));
+  KernelTimer timer("linear_planes", s);
+  if (dtype == MHLA_BF16) {
+    if (quads) linear_planes<1, 4><<<grid, 256, 0, s>>>(p);
+    else linear_planes<1, 1><<<grid, 256, 0, s>>>(p);
+  } else {
+    if (quads) linear_planes<3, 4><<<grid, 256, 0, s>>>(p);
+    else linear_planes<3, 1><<<grid, 256, 0, s>>>(p);
+  }
+  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+}
+
+// Blocks of rows of the planes' kernel: enough CTAs for the machine, 32 rows each at least.
+int64_t blocks_of_rows(int64_t rows, int64_t cols) {
+  const int64_t wide = cols % 4 == 0 ? 128 : 32, across = (cols + wide - 1) / wide;
+  int64_t n = std::max<int64_t>(1, std::min<int64_t>((rows + 31) / 32, (8 * kSms + across - 1) / across));
+  const int64_t each = (rows + n - 1) / n;
+  return (rows + each - 1) / each;
+}
+
+// The matrix as the product reads it: as it lies, or laid out at *ws.
+int lay_matrix(const void* x, int64_t rows, int64_t cols, int dtype, char** ws, Matrix* m, cudaStream_t s) {
+  if (direct(cols, dtype)) {
+    *m = Matrix{x, rows, cols, cols};
+    return MHLA_OK;
+  }
+  Planes p = {};
+  p.src = x;
+  p.dst = reinterpret_cast<__nv_bfloat16*>(*ws);
+  p.rows = rows; p.cols = cols; p.pitch = plane_pitch(cols);
+  *m = Matrix{*ws, rows, cols, p.pitch};
+  *ws += plane_bytes(rows, cols, dtype);
+  return run_planes(p, dtype, blocks_of_rows(rows, cols), s);
+}
+size_t lay_bytes(int64_t rows, int64_t cols, int dtype) { return direct(cols, dtype) ? 0 : plane_bytes(rows, cols, dtype); }
+
+// Rows that linear_rows and linear_dots take.
+constexpr int64_t kFewRows = 64, kFewDots = 8;
+bool few_rows(const LinearProblem& p) { return p.rows <= (direct(p.k, p.dtype) ? kFewRows : kFewDots); }
+
+template <int GROUPS>
+int run_rows(const LinearProblem& p, const Finish& f, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((p.n + 15) / 16), static_cast<unsigned>((p.rows + 8 * GROUPS - 1) / (8 * GROUPS)));
+  linear_rows<GROUPS><<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(p.x), static_cast<const __nv_bfloat16*>(p.w), p.rows,
+                                           static_cast<int32_t>(p.k), f);
+  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t linear_act_workspace_bytes(const LinearProblem& p) {
+  if (few_rows(p)) return 0;
+  return lay_bytes(p.rows, p.k, p.dtype) + lay_bytes(p.n, p.k, p.dtype) +
+         part_bytes(p.rows, p.n, cut_product(p.rows, p.n, p.k, p.dtype));
+}
+
+int launch_linear_act(const LinearProblem& p, const void* bias, const void* residual, void* pre, void* out, void* workspace,
+                      void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const Finish f = {out, pre, residual, bias, p.rows, p.n, p.act, p.dtype != MHLA_BF16, p.n % 4 == 0};
+  if (few_rows(p)) {
+    KernelTimer timer("linear_rows", s);
+    if (direct(p.k, p.dtype)) {
+      if (p.rows <= 8) return run_rows<1>(p, f, s);
+      return p.rows <= 16 ? run_rows<2>(p, f, s) : run_rows<4>(p, f, s);
+    }
+    const dim3 grid(static_cast<unsigned>((p.n + 7) / 8), static_cast<unsigned>((p.rows + 7) / 8));
+    if (p.dtype == MHLA_BF16)
+      linear_dots<__nv_bfloat16><<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(p.x), static_cast<const __nv_bfloat16*>(p.w),
+                                                      p.rows, static_cast<int32_t>(p.k), f);
+    else
+      linear_dots<float><<<grid, 256, 0, s>>>(static_cast<const float*>(p.x), static_cast<const float*>(p.w), p.rows,
+                                              static_cast<int32_t>(p.k), f);
+    return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+  }
+  char* ws = static_cast<char*>(workspace);
+  Matrix x, w;
+  int rc = lay_matrix(p.x, p.rows, p.k, p.dtype, &ws, &x, s);
+  if (rc == MHLA_OK) rc = lay_matrix(p.w, p.n, p.k, p.dtype, &ws, &w, s);
+  return rc == MHLA_OK ? run_product("linear_gemm", x, false, w, false, p.rows, p.n, p.k, p.dtype, f, ws, s) : rc;
+}
+
+size_t linear_act_bwd_workspace_bytes(const LinearProblem& p) {
+  // dz (where it is not dout as it lies), x, w, the parts of either product, the sums of dz's columns
+  const bool plain = p.act == MHLA_ACT_NONE && direct(p.n, p.dtype);
+  const size_t parts = std::max(part_bytes(p.rows, p.k, cut_product(p.rows, p.k, p.n, p.dtype)),
+                                part_bytes(p.n, p.k, cut_product(p.n, p.k, p.rows, p.dtype)));
+  return (plain ? 0 : plane_bytes(p.rows, p.n, p.dtype)) + lay_bytes(p.rows, p.k, p.dtype) + lay_bytes(p.n, p.k, p.dtype) + parts +
+         align_up(static_cast<size_t>(blocks_of_rows(p.rows, p.n) * p.n) * 4);
+}
+
+int launch_linear_act_backward(const LinearProblem& p, const void* dout, const void* pre, void* dx, void* dw, void* dbias,
+                               void* workspace, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool f32 = p.dtype != MHLA_BF16, plain = p.act == MHLA_ACT_NONE && direct(p.n, p.dtype);
+  char* ws = static_cast<char*>(workspace);
+  Matrix dz = {dout, p.rows, p.n, p.n}, x, w;
+  const int64_t blocks = blocks_of_rows(p.rows, p.n);
+  float* sums = reinterpret_cast<float*>(ws);
+  ws += align_up(static_cast<size_t>(blocks * p.n) * 4);
+  int rc = MHLA_OK;
+  if (!plain || dbias) {
+    Planes z = {};
+    z.src = dout;
+    z.pre = p.act == MHLA_ACT_NONE ? nullptr : pre;
+    z.act = p.act;
+    z.rows = p.rows; z.cols = p.n; z.pitch = plane_pitch(p.n);
+    z.sums = dbias ? sums : nullptr;
+    if (!plain) {
+      z.dst = reinterpret_cast<__nv_bfloat16*>(ws);
+      dz = Matrix{ws, p.rows, p.n, z.pitch};
+      ws += plane_bytes(p.rows, p.n, p.dtype);
+    }
+    rc = run_planes(z, p.dtype, blocks, s);
+    if (rc == MHLA_OK && dbias) {
+      KernelTimer timer("linear_column_sums", s);
+      linear_column_sums<<<static_cast<unsigned>((p.n + 7) / 8), 256, 0, s>>>(sums, dbias, p.n, static_cast<int32_t>(blocks), f32);
+      if (cudaGetLastError() != cudaSuccess) rc = MHLA_ERR_CUDA;
+    }
+  }
+  if (rc == MHLA_OK && dw) rc = lay_matrix(p.x, p.rows, p.k, p.dtype, &ws, &x, s);
+  if (rc == MHLA_OK && dx) rc = lay_matrix(p.w, p.n, p.k, p.dtype, &ws, &w, s);
+  Finish f = {};
+  f.act = MHLA_ACT_NONE;
+  f.f32 = f32;
+  f.quads = p.k % 4 == 0;
+  f.N = p.k;
+  if (rc == MHLA_OK && dx) {
+    f.out = dx;
+    f.M = p.rows;
+    rc = run_product("linear_gemm_dx", dz, false, w, true, p.rows, p.k, p.n, p.dtype, f, ws, s);
+  }
+  if (rc == MHLA_OK && dw) {
+    f.out = dw;
+    f.M = p.n;
+    rc = run_product("linear_gemm_dw", dz, true, x, true, p.n, p.k, p.rows, p.dtype, f, ws, s);
+  }
+  return rc;
+}
+
+int read_and_clear_linear_error(void* stream, uint32_t* flags) { return read_and_clear_word(g_linear_error, stream, flags); }
+
+MHLA_DEFINE_STALL_SETTER(set_stall_linear)
+
+}  // namespace mhla

@@ -187,6 +187,7 @@ int set_stall_bwd(uint32_t warp_plus_1, uint64_t ns);
 int set_stall_causal(uint32_t warp_plus_1, uint64_t ns);
 int set_stall_module(uint32_t warp_plus_1, uint64_t ns);
 int set_stall_gemm(uint32_t warp_plus_1, uint64_t ns);
+int set_stall_linear(uint32_t warp_plus_1, uint64_t ns);
 int set_stall_gated(uint32_t warp_plus_1, uint64_t ns);
 
 // Brackets one kernel launch with CUDA events on its stream while
@@ -240,6 +241,20 @@ bool gemm_supported(int64_t rows, int64_t k, int64_t n_out);
 int launch_gemm(const char* name, const void* x, const void* w, const void* bias, void* y, int64_t rows, int64_t k,
                 int64_t n_out, void* stream);
 int read_and_clear_gemm_error(void* stream, uint32_t* flags);
+
+// The linear layer with activation and residual (linear_kernels.cu).
+struct LinearProblem {
+  const void *x, *w;   // [rows][k], [n][k]
+  int64_t rows, k, n;
+  int dtype, act;      // mhla_dtype_t, mhla_activation_t
+};
+size_t linear_act_workspace_bytes(const LinearProblem& p);
+size_t linear_act_bwd_workspace_bytes(const LinearProblem& p);
+int launch_linear_act(const LinearProblem& p, const void* bias, const void* residual, void* pre, void* out, void* workspace,
+                      void* stream);
+int launch_linear_act_backward(const LinearProblem& p, const void* dout, const void* pre, void* dx, void* dw, void* dbias,
+                               void* workspace, void* stream);
+int read_and_clear_linear_error(void* stream, uint32_t* flags);
 
 // Gated causal linear attention (gated_kernels.cu).
 struct GatedProblem {

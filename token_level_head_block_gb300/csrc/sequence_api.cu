@@ -1,5 +1,5 @@
-// extern "C" entry points of the gated recurrence, of the gated delta rule and of the query/key norm
-// with rotation: argument checks, workspace handling, launches.  Every check
+// extern "C" entry points of the gated recurrence, of the gated delta rule, of the query/key norm
+// with rotation and of the linear layer around them: argument checks, workspace handling, launches.  Every check
 // runs on the host before anything is queued on the stream.
 #include <cuda_runtime.h>
 
@@ -461,4 +461,94 @@ extern "C" mhla_status_t mhla_qk_norm_backward(const mhla_tensor_t* q, const mhl
   return static_cast<mhla_status_t>(with_workspace(qk_norm_bwd_workspace_bytes(p.d), workspace, workspace_bytes,
                                                    stream,
                                                    [&](void* ws) { return launch_qk_norm_backward(p, ws, stream); }));
+}
+
+// ----------------------------------------------------------------- linear layer
+
+namespace mhla {
+namespace {
+
+int check_linear(int64_t rows, int64_t k, int64_t n, int32_t dtype, int32_t act) {
+  if (rows < 0 || k < 1 || n < 1 || !valid_dtype(dtype) || act < MHLA_ACT_NONE || act > MHLA_ACT_SILU) return MHLA_ERR_INVALID_ARG;
+  if (rows >= (int64_t{1} << 31) || k > (int64_t{1} << 20) || n > (int64_t{1} << 20)) return MHLA_ERR_UNSUPPORTED;
+  return MHLA_OK;
+}
+
+struct Block {
+  const void* p;
+  int64_t bytes;
+};
+bool apart(const Block& w, std::initializer_list<Block> others) {
+  for (const Block& o : others)
+    if (plain_overlap(w.p, o.p, w.bytes, o.bytes)) return false;
+  return true;
+}
+bool all_aligned(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!aligned16(p)) return false;
+  return true;
+}
+
+}  // namespace
+}  // namespace mhla
+
+extern "C" mhla_status_t mhla_linear_act_workspace_size(int64_t rows, int64_t k, int64_t n, int32_t dtype, size_t* bytes) {
+  if (!bytes) return MHLA_ERR_INVALID_ARG;
+  const int rc = check_linear(rows, k, n, dtype, MHLA_ACT_NONE);
+  if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
+  *bytes = rows == 0 ? 0 : linear_act_workspace_bytes(LinearProblem{nullptr, nullptr, rows, k, n, dtype, MHLA_ACT_NONE});
+  return MHLA_OK;
+}
+
+extern "C" mhla_status_t mhla_linear_act_backward_workspace_size(int64_t rows, int64_t k, int64_t n, int32_t dtype,
+                                                                 int32_t activation, size_t* bytes) {
+  if (!bytes) return MHLA_ERR_INVALID_ARG;
+  const int rc = check_linear(rows, k, n, dtype, activation);
+  if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
+  *bytes = rows == 0 ? 0 : linear_act_bwd_workspace_bytes(LinearProblem{nullptr, nullptr, rows, k, n, dtype, activation});
+  return MHLA_OK;
+}
+
+extern "C" mhla_status_t mhla_linear_act(const void* x, const void* w, const void* bias, int32_t activation,
+                                         const void* residual, void* pre, void* out, int64_t rows, int64_t k, int64_t n,
+                                         int32_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = check_linear(rows, k, n, dtype, activation);
+  if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
+  if (rows == 0) return MHLA_OK;
+  if (!x || !w || !out || !all_aligned({x, w, bias, residual, pre, out})) return MHLA_ERR_INVALID_ARG;
+  const int64_t e = elem_bytes(dtype);
+  const Block o = {out, rows * n * e}, z = {pre, rows * n * e};
+  const Block bx = {x, rows * k * e}, bw = {w, n * k * e}, bb = {bias, n * e}, br = {residual, rows * n * e};
+  if (!apart(o, {z, bx, bw, bb}) || (residual != out && !apart(o, {br})) || !apart(z, {bx, bw, bb, br})) return MHLA_ERR_INVALID_ARG;
+  const LinearProblem p = {x, w, rows, k, n, dtype, activation};
+  return static_cast<mhla_status_t>(
+      with_workspace(linear_act_workspace_bytes(p), workspace, workspace_bytes, stream,
+                     [&](void* ws) { return launch_linear_act(p, bias, residual, pre, out, ws, stream); }));
+}
+
+extern "C" mhla_status_t mhla_linear_act_backward(const void* x, const void* w, const void* dout, const void* pre,
+                                                  int32_t activation, void* dx, void* dw, void* dbias, int64_t rows, int64_t k,
+                                                  int64_t n, int32_t dtype, void* workspace, size_t workspace_bytes,
+                                                  void* stream) {
+  const int rc = check_linear(rows, k, n, dtype, activation);
+  if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
+  if (!all_aligned({x, w, dout, pre, dx, dw, dbias})) return MHLA_ERR_INVALID_ARG;
+  const int64_t e = elem_bytes(dtype);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if (dw && cudaMemsetAsync(dw, 0, static_cast<size_t>(n * k * e), s) != cudaSuccess) return MHLA_ERR_CUDA;
+    if (dbias && cudaMemsetAsync(dbias, 0, static_cast<size_t>(n * e), s) != cudaSuccess) return MHLA_ERR_CUDA;
+    return MHLA_OK;
+  }
+  if (!x || !w || !dout || (activation != MHLA_ACT_NONE && !pre)) return MHLA_ERR_INVALID_ARG;
+  const Block in[] = {{x, rows * k * e}, {w, n * k * e}, {dout, rows * n * e}, {pre, rows * n * e}};
+  const Block bx = {dx, rows * k * e}, bw = {dw, n * k * e}, bb = {dbias, n * e};
+  for (const Block& o : {bx, bw, bb})
+    if (!apart(o, {in[0], in[1], in[2], in[3]})) return MHLA_ERR_INVALID_ARG;
+  if (!apart(bx, {bw, bb}) || !apart(bw, {bb})) return MHLA_ERR_INVALID_ARG;
+  if (!dx && !dw && !dbias) return MHLA_OK;
+  const LinearProblem p = {x, w, rows, k, n, dtype, activation};
+  return static_cast<mhla_status_t>(
+      with_workspace(linear_act_bwd_workspace_bytes(p), workspace, workspace_bytes, stream,
+                     [&](void* ws) { return launch_linear_act_backward(p, dout, pre, dx, dw, dbias, ws, stream); }));
 }
