@@ -19,6 +19,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "gated_common.cuh"
 #include "mhla_internal.h"
@@ -49,32 +50,50 @@ __device__ __forceinline__ float over_sigmoid(float z) { return 1.0f + (FAST ? _
 
 constexpr float kTanhScale = 0.7978845608028654f, kTanhCube = 0.044715f;   // sqrt(2 / pi)
 
-template <bool FAST>
-__device__ __forceinline__ float activate(float z, int act) {
+template <bool FAST, int ACT>
+__device__ __forceinline__ float activate(float z) {
+  if (ACT == MHLA_ACT_RELU) return z < 0.0f ? 0.0f : z;   // NaN stays
+  if (ACT == MHLA_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
+  if (ACT == MHLA_ACT_GELU_TANH) {   // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+    const float u = kTanhScale * fmaf(kTanhCube * z * z, z, z);
+    return FAST ? __fdividef(z, over_sigmoid<true>(2.0f * u)) : z / over_sigmoid<false>(2.0f * u);
+  }
+  if (ACT == MHLA_ACT_SILU) return FAST ? __fdividef(z, over_sigmoid<true>(z)) : z / over_sigmoid<false>(z);
+  return z;
+}
+
+// One branch for all of them, so that each activation's code stands once.
+template <bool FAST, int N>
+__device__ __forceinline__ void activate_all(float (&z)[N], int act) {
+  auto all = [&](auto one) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = one(z[i]);
+  };
   switch (act) {
-    case MHLA_ACT_RELU: return z < 0.0f ? 0.0f : z;   // NaN stays
-    case MHLA_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
-    case MHLA_ACT_GELU_TANH: {   // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
-      const float u = kTanhScale * fmaf(kTanhCube * z * z, z, z);
-      return FAST ? __fdividef(z, over_sigmoid<true>(2.0f * u)) : z / over_sigmoid<false>(2.0f * u);
-    }
-    case MHLA_ACT_SILU: return FAST ? __fdividef(z, over_sigmoid<true>(z)) : z / over_sigmoid<false>(z);
-    default: return z;
+    case MHLA_ACT_RELU: all([](float x) { return activate<FAST, MHLA_ACT_RELU>(x); }); break;
+    case MHLA_ACT_GELU: all([](float x) { return activate<FAST, MHLA_ACT_GELU>(x); }); break;
+    case MHLA_ACT_GELU_TANH: all([](float x) { return activate<FAST, MHLA_ACT_GELU_TANH>(x); }); break;
+    case MHLA_ACT_SILU: all([](float x) { return activate<FAST, MHLA_ACT_SILU>(x); }); break;
+    default: break;
   }
 }
 
+template <bool FAST>
+__device__ __forceinline__ float sigmoid(float z) { return FAST ? __fdividef(1.0f, over_sigmoid<true>(z)) : 1.0f / over_sigmoid<false>(z); }
+
+template <bool FAST>
 __device__ __forceinline__ float slope(float z, int act) {
   switch (act) {
     case MHLA_ACT_RELU: return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
     case MHLA_ACT_GELU:
-      return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) + z * 0.3989422804014327f * expf(-0.5f * z * z);
+      return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) + z * 0.3989422804014327f * (FAST ? __expf(-0.5f * z * z) : expf(-0.5f * z * z));
     case MHLA_ACT_GELU_TANH: {
       z = z > 30.0f ? 30.0f : z < -30.0f ? -30.0f : z;   // 1 and 0 there; the cube stays finite
-      const float u = kTanhScale * fmaf(kTanhCube * z * z, z, z), p = 1.0f / over_sigmoid<false>(2.0f * u);
+      const float u = kTanhScale * fmaf(kTanhCube * z * z, z, z), p = sigmoid<FAST>(2.0f * u);
       return p + z * p * (1.0f - p) * (2.0f * kTanhScale) * fmaf(3.0f * kTanhCube * z, z, 1.0f);
     }
     case MHLA_ACT_SILU: {
-      const float p = 1.0f / over_sigmoid<false>(z);
+      const float p = sigmoid<FAST>(z);
       return p * fmaf(z, 1.0f - p, 1.0f);
     }
     default: return 1.0f;
@@ -89,62 +108,113 @@ struct Finish {
   const void* residual;  // [M][N], or null; may be out
   const void* bias;      // [N], or null
   int64_t M, N;
-  int32_t act, f32;
+  int32_t act;
   int32_t quads;         // N % 4 == 0: four values an access
 };
 
-__device__ __forceinline__ float4 load_quad(const void* p, int64_t i, int f32) {
-  if (f32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-  const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
-  return make_float4(low(x.x), high(x.x), low(x.y), high(x.y));
+template <bool F32>
+__device__ __forceinline__ float load_one(const void* p, int64_t i) {
+  return F32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
-__device__ __forceinline__ void store_quad(void* p, int64_t i, int f32, float4 x) {
-  if (f32)
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = x;
-  else
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) = make_uint2(gated::pack(x.x, x.y), gated::pack(x.z, x.w));
-}
-__device__ __forceinline__ float load_one(const void* p, int64_t i, int f32) {
-  return f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-__device__ __forceinline__ void store_one(void* p, int64_t i, int f32, float x) {
-  if (f32)
+template <bool F32>
+__device__ __forceinline__ void store_one(void* p, int64_t i, float x) {
+  if (F32)
     static_cast<float*>(p)[i] = x;
   else
     static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
 }
 
-// Four sums of row r, columns c .. c + 3 (r < M, c < N).
-template <bool FAST>
-__device__ __forceinline__ void finish_quad(const Finish& f, int64_t r, int64_t c, float4 z, float4 bias) {
-  const int64_t i = r * f.N + c;
-  z.x += bias.x; z.y += bias.y; z.z += bias.z; z.w += bias.w;
-  if (f.quads) {
-    if (f.pre) store_quad(f.pre, i, f.f32, z);
-    float4 y = make_float4(activate<FAST>(z.x, f.act), activate<FAST>(z.y, f.act), activate<FAST>(z.z, f.act), activate<FAST>(z.w, f.act));
-    if (f.residual) {
-      const float4 s = load_quad(f.residual, i, f.f32);
-      y.x += s.x; y.y += s.y; y.z += s.z; y.w += s.w;
+// Four values as they lie, asked for ahead of their use.
+template <bool F32>
+struct Quad {
+  typename std::conditional<F32, float4, uint2>::type x;
+  __device__ __forceinline__ void fetch(const void* p, int64_t i) {
+    if constexpr (F32)
+      x = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    else
+      x = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
+  }
+  __device__ __forceinline__ float4 value() const {
+    if constexpr (F32)
+      return x;
+    else
+      return make_float4(low(x.x), high(x.x), low(x.y), high(x.y));
+  }
+  __device__ __forceinline__ void set(float4 v) {
+    if constexpr (F32)
+      x = v;
+    else
+      x = make_uint2(gated::pack(v.x, v.y), gated::pack(v.z, v.w));
+  }
+  __device__ __forceinline__ void store(void* p, int64_t i) const {
+    if constexpr (F32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = x;
+    else
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) = x;
+  }
+};
+
+__device__ __forceinline__ float4 plus(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+
+// ROWS times four sums with the bias, those of row r from element i + r step on, N % 4 == 0; rows behind `rows` are left out.
+template <bool F32, int ROWS>
+__device__ __forceinline__ void finish_quads(const Finish& f, int64_t i, int64_t step, int rows, float (&z)[4 * ROWS],
+                                             const Quad<F32> (&residual)[ROWS]) {
+  Quad<F32> q;
+  if (f.pre)
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+      if (r < rows) {
+        q.set(make_float4(z[4 * r], z[4 * r + 1], z[4 * r + 2], z[4 * r + 3]));
+        q.store(f.pre, i + r * step);
+      }
+  activate_all<!F32>(z, f.act);
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r)
+    if (r < rows) {
+      float4 y = make_float4(z[4 * r], z[4 * r + 1], z[4 * r + 2], z[4 * r + 3]);
+      if (f.residual) y = plus(y, residual[r].value());
+      q.set(y);
+      q.store(f.out, i + r * step);
     }
-    store_quad(f.out, i, f.f32, y);
+}
+
+template <bool F32>
+__device__ __forceinline__ float4 bias_quad(const Finish& f, int64_t c) {
+  if (!f.bias) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (f.quads) {
+    Quad<F32> q;
+    q.fetch(f.bias, c);
+    return q.value();
+  }
+  float b[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b[e] = c + e < f.N ? load_one<F32>(f.bias, c + e) : 0.0f;
+  return make_float4(b[0], b[1], b[2], b[3]);
+}
+
+// Four sums of row r, columns c .. c + 3 (r < M, c < N), any N.
+template <bool F32>
+__device__ __forceinline__ void finish_quad(const Finish& f, int64_t r, int64_t c, float4 z) {
+  const int64_t i = r * f.N + c;
+  z = plus(z, bias_quad<F32>(f, c));
+  float zs[4] = {z.x, z.y, z.z, z.w};
+  if (f.quads) {
+    Quad<F32> s[1] = {};
+    if (f.residual) s[0].fetch(f.residual, i);
+    finish_quads<F32, 1>(f, i, 0, 1, zs, s);
   } else {
-    const float zs[4] = {z.x, z.y, z.z, z.w};
+    if (f.pre)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < f.N) store_one<F32>(f.pre, i + e, zs[e]);
+    activate_all<!F32>(zs, f.act);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (c + e >= f.N) break;
-      if (f.pre) store_one(f.pre, i + e, f.f32, zs[e]);
-      float y = activate<FAST>(zs[e], f.act);
-      if (f.residual) y += load_one(f.residual, i + e, f.f32);
-      store_one(f.out, i + e, f.f32, y);
+      store_one<F32>(f.out, i + e, f.residual ? zs[e] + load_one<F32>(f.residual, i + e) : zs[e]);
     }
   }
-}
-
-__device__ __forceinline__ float4 bias_quad(const Finish& f, int64_t c) {
-  float b[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) b[e] = f.bias && c + e < f.N ? load_one(f.bias, c + e, f.f32) : 0.0f;
-  return make_float4(b[0], b[1], b[2], b[3]);
 }
 
 // ----------------------------------------------------------------- product
@@ -324,25 +394,43 @@ __global__ void __launch_bounds__(GemmLay<TERMS>::THREADS, 1) linear_gemm(const 
   } else {
     const int q4 = warp & 3, half = (warp - 2) >> 2;   // TMEM lane quarter this warp may read; its half of the columns
     float* stage = reinterpret_cast<float*>(staging + (warp - 2) * L::STAGING);
+    constexpr bool F32 = TERMS > 1;
+    const int mine = p.BN / 32;                        // BN is a multiple of 64
+    const bool whole = p.f.quads && !p.parts;
     uint32_t local = 0;
     for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x, ++local) {
       const Unit un = unit_of(p, u);
       const uint32_t acc = local % L::ACCS, aph = (local / L::ACCS) & 1u;
+      const int64_t row0 = un.m0 + 32 * q4 + (lane >> 2), c0 = un.n0 + 16 * half * mine + 4 * (lane & 3);
+      const int64_t i0 = row0 * p.f.N + c0;
+      const int rows = static_cast<int>(max(int64_t{0}, min(int64_t{4}, (p.f.M - row0 + 7) / 8)));   // of this lane's four
+      // what the finish reads of memory: the first group's while the products run, then a group ahead
+      Quad<F32> residual[4] = {}, bias = {};
+      auto fetch = [&](int gi) {
+        if (!whole || c0 + 16 * gi >= p.f.N) return;
+        if (p.f.bias) bias.fetch(p.f.bias, c0 + 16 * gi);
+        if (p.f.residual)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < rows) residual[i].fetch(p.f.residual, i0 + 8 * i * p.f.N + 16 * gi);
+      };
+      fetch(0);
       if (!warp_wait(tfull + acc, aph, abortf)) break;
       tc_fence_after();
-      const uint32_t tb = tmem + acc * 256 + (static_cast<uint32_t>(32 * q4) << 16);
-      const int groups = p.BN / 16, mine = groups / 2;   // BN is a multiple of 64
+      const uint32_t tb = tmem + acc * 256 + (static_cast<uint32_t>(32 * q4) << 16) + 16 * half * mine;
       const int mains = TERMS == 1 ? 1 : min(un.count, L::MAINS);
+      const int used = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(mine), (p.f.N - un.n0 - 16 * half * mine + 15) / 16)));
+      uint32_t next[16];
+      if (TERMS == 1 && used > 0) tmem_ld_x16(tb, next);
 #pragma unroll 1
-      for (int gi = 0; gi < mine; ++gi) {
-        const int col = 16 * (half * mine + gi);
+      for (int gi = 0; gi < used; ++gi) {
         uint32_t v[16];
-        tmem_ld_x16(tb + col, v);
         if (TERMS > 1) {
           uint32_t x[16], y[16], z[16];
-          tmem_ld_x16(tb + 128 * L::MAINS + col, z);
-          if (mains > 1) tmem_ld_x16(tb + 128 + col, x);
-          if (mains > 2) tmem_ld_x16(tb + 256 + col, y);
+          tmem_ld_x16(tb + 16 * gi, v);
+          tmem_ld_x16(tb + 128 * L::MAINS + 16 * gi, z);
+          if (mains > 1) tmem_ld_x16(tb + 128 + 16 * gi, x);
+          if (mains > 2) tmem_ld_x16(tb + 256 + 16 * gi, y);
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -353,34 +441,48 @@ __global__ void __launch_bounds__(GemmLay<TERMS>::THREADS, 1) linear_gemm(const 
           }
         } else {
           tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = next[e];
         }
-        if (gi + 1 == mine) {   // the sums are read out
-          tc_fence_before();
-          mbar_arrive(tempty + acc);
-        }
-        if (un.n0 + col >= p.f.N) continue;   // the same for every lane
+        // a row of 16 columns a lane becomes four columns of four rows
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           *reinterpret_cast<uint4*>(stage + lane * L::PITCH + 4 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         __syncwarp();
-        const int64_t c = un.n0 + col + 4 * (lane & 3);
-        if (c < p.f.N) {
-          const float4 bias = p.parts ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : bias_quad(p.f, c);
+        if (TERMS == 1 && gi + 1 < used) tmem_ld_x16(tb + 16 * (gi + 1), next);
+        float z[16];
+        const float4 add = p.f.bias ? bias.value() : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(stage + (8 * i + (lane >> 2)) * L::PITCH + 4 * (lane & 3));
+          z[4 * i] = x.x; z[4 * i + 1] = x.y; z[4 * i + 2] = x.z; z[4 * i + 3] = x.w;
+        }
+        __syncwarp();
+        const int64_t c = c0 + 16 * gi;
+        if (whole) {
+          Quad<F32> now[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + (lane >> 2);
-            const int64_t row = un.m0 + 32 * q4 + r;
-            if (row < p.f.M) {
-              const float4 z = *reinterpret_cast<const float4*>(stage + r * L::PITCH + 4 * (lane & 3));
-              if (p.parts)
-                *reinterpret_cast<float4*>(p.parts + (un.split * p.f.M + row) * p.pitch + c) = z;
-              else
-                finish_quad<TERMS == 1>(p.f, row, c, z, bias);
-            }
+            now[i] = residual[i];
+            z[4 * i] += add.x; z[4 * i + 1] += add.y; z[4 * i + 2] += add.z; z[4 * i + 3] += add.w;
+          }
+          if (gi + 1 < used) fetch(gi + 1);
+          if (c < p.f.N) finish_quads<F32, 4>(p.f, i0 + 16 * gi, 8 * p.f.N, rows, z, now);
+        } else if (c < p.f.N) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i >= rows) break;
+            const float4 x = make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
+            if (p.parts)
+              *reinterpret_cast<float4*>(p.parts + (un.split * p.f.M + row0 + 8 * i) * p.pitch + c) = x;
+            else
+              finish_quad<F32>(p.f, row0 + 8 * i, c, x);
           }
         }
         __syncwarp();
       }
+      tc_fence_before();
+      mbar_arrive(tempty + acc);   // the sums are read out
     }
   }
   tc_fence_before();
@@ -398,7 +500,7 @@ struct Join {
   int64_t pitch;
   int32_t splits;
 };
-template <bool FAST>
+template <bool F32>
 __global__ void __launch_bounds__(256) linear_join(const __grid_constant__ Join p) {
   const int64_t i = 4 * (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x), total = p.f.M * p.pitch;
   if (i >= total) return;
@@ -409,7 +511,7 @@ __global__ void __launch_bounds__(256) linear_join(const __grid_constant__ Join 
     const float4 x = *reinterpret_cast<const float4*>(p.parts + s * total + i);
     z.x += x.x; z.y += x.y; z.z += x.z; z.w += x.w;
   }
-  finish_quad<FAST>(p.f, r, c, z, bias_quad(p.f, c));
+  finish_quad<F32>(p.f, r, c, z);
 }
 
 // ----------------------------------------------------------------- planes
@@ -422,7 +524,7 @@ struct Planes {
   __nv_bfloat16* dst;
   float* sums;
   int64_t rows, cols, pitch, block_rows;
-  int32_t act, f32;
+  int32_t act;
 };
 
 // A thread has VEC columns; 32 threads side by side, eight rows at once.
@@ -433,42 +535,66 @@ __global__ void __launch_bounds__(256) linear_planes(const __grid_constant__ Pla
   const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + x) * VEC;
   const int64_t first = blockIdx.y * p.block_rows, last = min(p.rows, first + p.block_rows);
   float sum[VEC] = {};
+  constexpr int BATCH = 4;   // rows in flight
+  using Wide = typename std::conditional<VEC == 8, uint4, typename std::conditional<VEC == 4, uint4, uint32_t>::type>::type;
+  auto fetch = [&](const void* q, int64_t i) {
+    Wide x;
+    if constexpr (VEC == 1)
+      x = __float_as_uint(load_one<(TERMS > 1)>(q, i));
+    else if constexpr (TERMS > 1)
+      x = *reinterpret_cast<const uint4*>(static_cast<const float*>(q) + i);
+    else
+      x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(q) + i);
+    return x;
+  };
+  auto open = [&](const Wide& x, float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+      v[0] = __uint_as_float(x);
+    } else if constexpr (VEC == 4) {
+      v[0] = __uint_as_float(x.x); v[1] = __uint_as_float(x.y); v[2] = __uint_as_float(x.z); v[3] = __uint_as_float(x.w);
+    } else {
+      v[0] = low(x.x); v[1] = high(x.x); v[2] = low(x.y); v[3] = high(x.y);
+      v[4] = low(x.z); v[5] = high(x.z); v[6] = low(x.w); v[7] = high(x.w);
+    }
+  };
   if (c < p.cols) {
-#pragma unroll 2
-    for (int64_t r = first + y; r < last; r += 8) {
-      const int64_t i = r * p.cols + c;
-      float v[VEC], z[VEC];
-      if constexpr (VEC == 4) {
-        const float4 q = load_quad(p.src, i, p.f32);
-        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-        if (p.pre) {
-          const float4 w = load_quad(p.pre, i, p.f32);
-          z[0] = w.x; z[1] = w.y; z[2] = w.z; z[3] = w.w;
+    for (int64_t r0 = first + y; r0 < last; r0 += 8 * BATCH) {
+      Wide a[BATCH], w[BATCH];
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j)
+        if (r0 + 8 * j < last) {
+          a[j] = fetch(p.src, (r0 + 8 * j) * p.cols + c);
+          if (p.pre) w[j] = fetch(p.pre, (r0 + 8 * j) * p.cols + c);
         }
-      } else {
-        v[0] = load_one(p.src, i, p.f32);
-        if (p.pre) z[0] = load_one(p.pre, i, p.f32);
-      }
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        if (p.pre) v[e] *= slope(z[e], p.act);
-        sum[e] += v[e];
-      }
-      if (!p.dst) continue;
+      for (int j = 0; j < BATCH; ++j) {
+        const int64_t r = r0 + 8 * j;
+        if (r >= last) break;
+        float v[VEC], z[VEC];
+        open(a[j], v);
+        if (p.pre) open(w[j], z);
 #pragma unroll
-      for (int t = 0; t < TERMS; ++t) {
-        __nv_bfloat16* to = p.dst + (t * p.rows + r) * p.pitch + c;
-        float h[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) h[e] = __bfloat162float(__float2bfloat16_rn(v[e]));
-        if constexpr (VEC == 4) {
-          *reinterpret_cast<uint2*>(to) = make_uint2(gated::pack(h[0], h[1]), gated::pack(h[2], h[3]));
-        } else {
-          from_f(to, h[0]);
+        for (int e = 0; e < VEC; ++e) {
+          if (p.pre) v[e] *= slope<TERMS == 1>(z[e], p.act);
+          sum[e] += v[e];
         }
-        // an infinity is its first term alone
+        if (!p.dst) continue;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = fabsf(h[e]) < __int_as_float(0x7F800000) ? v[e] - h[e] : 0.0f;
+        for (int t = 0; t < TERMS; ++t) {
+          __nv_bfloat16* to = p.dst + (t * p.rows + r) * p.pitch + c;
+          float h[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) h[e] = __bfloat162float(__float2bfloat16_rn(v[e]));
+          if constexpr (VEC == 8)
+            *reinterpret_cast<uint4*>(to) = make_uint4(gated::pack(h[0], h[1]), gated::pack(h[2], h[3]), gated::pack(h[4], h[5]), gated::pack(h[6], h[7]));
+          else if constexpr (VEC == 4)
+            *reinterpret_cast<uint2*>(to) = make_uint2(gated::pack(h[0], h[1]), gated::pack(h[2], h[3]));
+          else
+            from_f(to, h[0]);
+          // an infinity is its first term alone
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) v[e] = fabsf(h[e]) < __int_as_float(0x7F800000) ? v[e] - h[e] : 0.0f;
+        }
       }
     }
   }
@@ -487,7 +613,8 @@ __global__ void __launch_bounds__(256) linear_planes(const __grid_constant__ Pla
 }
 
 // Column sums of the blocks, in their order: one warp a column.
-__global__ void __launch_bounds__(256) linear_column_sums(const float* sums, void* out, int64_t cols, int32_t blocks, int32_t f32) {
+template <bool F32>
+__global__ void __launch_bounds__(256) linear_column_sums(const float* sums, void* out, int64_t cols, int32_t blocks) {
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (c >= cols) return;
   const int lane = threadIdx.x & 31;
@@ -495,7 +622,7 @@ __global__ void __launch_bounds__(256) linear_column_sums(const float* sums, voi
   for (int b = lane; b < blocks; b += 32) s += sums[b * cols + c];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-  if (lane == 0) store_one(out, c, f32, s);
+  if (lane == 0) store_one<F32>(out, c, s);
 }
 
 // ----------------------------------------------------------------- few rows
@@ -539,7 +666,7 @@ __global__ void __launch_bounds__(256) linear_rows(const __nv_bfloat16* x, const
     for (int e = 0; e < 4; ++e)
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[e] += part[j][c + e][r];
-    finish_quad<true>(f, r0 + r, n0 + c, make_float4(z[0], z[1], z[2], z[3]), bias_quad(f, n0 + c));
+    finish_quad<false>(f, r0 + r, n0 + c, make_float4(z[0], z[1], z[2], z[3]));
   }
 }
 
@@ -567,11 +694,12 @@ __global__ void __launch_bounds__(256) linear_dots(const T* x, const T* w, int64
   }
   if (lane >= m) return;
   const int64_t i = (r0 + lane) * f.N + n;
-  const float z = mine + (f.bias ? load_one(f.bias, n, f.f32) : 0.0f);
-  if (f.pre) store_one(f.pre, i, f.f32, z);
-  float y = activate<false>(z, f.act);
-  if (f.residual) y += load_one(f.residual, i, f.f32);
-  store_one(f.out, i, f.f32, y);
+  constexpr bool F32 = sizeof(T) == 4;
+  const float z = mine + (f.bias ? load_one<F32>(f.bias, n) : 0.0f);
+  if (f.pre) store_one<F32>(f.pre, i, z);
+  float y[1] = {z};
+  activate_all<!F32>(y, f.act);
+  store_one<F32>(f.out, i, f.residual ? y[0] + load_one<F32>(f.residual, i) : y[0]);
 }
 
 // ----------------------------------------------------------------- host
@@ -672,32 +800,34 @@ int run_product(const char* name, const Matrix& a, bool a_major, const Matrix& b
   KernelTimer timer("linear_join", s);
   const unsigned blocks = static_cast<unsigned>((M * p.pitch / 4 + 255) / 256);
   if (terms == 1)
-    linear_join<true><<<blocks, 256, 0, s>>>(j);
-  else
     linear_join<false><<<blocks, 256, 0, s>>>(j);
+  else
+    linear_join<true><<<blocks, 256, 0, s>>>(j);
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
 
+// Columns a thread of the planes' kernel has: 16 bytes where rows are a multiple of that.
+int plane_vec(int64_t cols, int dtype) { return dtype == MHLA_BF16 ? (cols % 8 == 0 ? 8 : 1) : cols % 4 == 0 ? 4 : 1; }
+
 int run_planes(Planes p, int dtype, int64_t row_blocks, cudaStream_t s) {
-  p.f32 = dtype != MHLA_BF16;
   p.block_rows = (p.rows + row_blocks - 1) / row_blocks;
-  const bool quads = p.cols % 4 == 0;
-  const int64_t wide = quads ? 128 : 32;
+  const int vec = plane_vec(p.cols, dtype);
+  const int64_t wide = 32 * vec;
   const dim3 grid(static_cast<unsigned>((p.cols + wide - 1) / wide), static_cast<unsigned>(row_blocks));
   KernelTimer timer("linear_planes", s);
   if (dtype == MHLA_BF16) {
-    if (quads) linear_planes<1, 4><<<grid, 256, 0, s>>>(p);
+    if (vec > 1) linear_planes<1, 8><<<grid, 256, 0, s>>>(p);
     else linear_planes<1, 1><<<grid, 256, 0, s>>>(p);
   } else {
-    if (quads) linear_planes<3, 4><<<grid, 256, 0, s>>>(p);
+    if (vec > 1) linear_planes<3, 4><<<grid, 256, 0, s>>>(p);
     else linear_planes<3, 1><<<grid, 256, 0, s>>>(p);
   }
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
 
 // Blocks of rows of the planes' kernel: enough CTAs for the machine, 32 rows each at least.
-int64_t blocks_of_rows(int64_t rows, int64_t cols) {
-  const int64_t wide = cols % 4 == 0 ? 128 : 32, across = (cols + wide - 1) / wide;
+int64_t blocks_of_rows(int64_t rows, int64_t cols, int dtype) {
+  const int64_t wide = 32 * plane_vec(cols, dtype), across = (cols + wide - 1) / wide;
   int64_t n = std::max<int64_t>(1, std::min<int64_t>((rows + 31) / 32, (8 * kSms + across - 1) / across));
   const int64_t each = (rows + n - 1) / n;
   return (rows + each - 1) / each;
@@ -715,7 +845,7 @@ int lay_matrix(const void* x, int64_t rows, int64_t cols, int dtype, char** ws, 
   p.rows = rows; p.cols = cols; p.pitch = plane_pitch(cols);
   *m = Matrix{*ws, rows, cols, p.pitch};
   *ws += plane_bytes(rows, cols, dtype);
-  return run_planes(p, dtype, blocks_of_rows(rows, cols), s);
+  return run_planes(p, dtype, blocks_of_rows(rows, cols, dtype), s);
 }
 size_t lay_bytes(int64_t rows, int64_t cols, int dtype) { return direct(cols, dtype) ? 0 : plane_bytes(rows, cols, dtype); }
 
@@ -742,7 +872,7 @@ size_t linear_act_workspace_bytes(const LinearProblem& p) {
 int launch_linear_act(const LinearProblem& p, const void* bias, const void* residual, void* pre, void* out, void* workspace,
                       void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Finish f = {out, pre, residual, bias, p.rows, p.n, p.act, p.dtype != MHLA_BF16, p.n % 4 == 0};
+  const Finish f = {out, pre, residual, bias, p.rows, p.n, p.act, p.n % 4 == 0};
   if (few_rows(p)) {
     KernelTimer timer("linear_rows", s);
     if (direct(p.k, p.dtype)) {
@@ -771,7 +901,7 @@ size_t linear_act_bwd_workspace_bytes(const LinearProblem& p) {
   const size_t parts = std::max(part_bytes(p.rows, p.k, cut_product(p.rows, p.k, p.n, p.dtype)),
                                 part_bytes(p.n, p.k, cut_product(p.n, p.k, p.rows, p.dtype)));
   return (plain ? 0 : plane_bytes(p.rows, p.n, p.dtype)) + lay_bytes(p.rows, p.k, p.dtype) + lay_bytes(p.n, p.k, p.dtype) + parts +
-         align_up(static_cast<size_t>(blocks_of_rows(p.rows, p.n) * p.n) * 4);
+         align_up(static_cast<size_t>(blocks_of_rows(p.rows, p.n, p.dtype) * p.n) * 4);
 }
 
 int launch_linear_act_backward(const LinearProblem& p, const void* dout, const void* pre, void* dx, void* dw, void* dbias,
@@ -780,7 +910,7 @@ int launch_linear_act_backward(const LinearProblem& p, const void* dout, const v
   const bool f32 = p.dtype != MHLA_BF16, plain = p.act == MHLA_ACT_NONE && direct(p.n, p.dtype);
   char* ws = static_cast<char*>(workspace);
   Matrix dz = {dout, p.rows, p.n, p.n}, x, w;
-  const int64_t blocks = blocks_of_rows(p.rows, p.n);
+  const int64_t blocks = blocks_of_rows(p.rows, p.n, p.dtype);
   float* sums = reinterpret_cast<float*>(ws);
   ws += align_up(static_cast<size_t>(blocks * p.n) * 4);
   int rc = MHLA_OK;
@@ -799,7 +929,11 @@ int launch_linear_act_backward(const LinearProblem& p, const void* dout, const v
     rc = run_planes(z, p.dtype, blocks, s);
     if (rc == MHLA_OK && dbias) {
       KernelTimer timer("linear_column_sums", s);
-      linear_column_sums<<<static_cast<unsigned>((p.n + 7) / 8), 256, 0, s>>>(sums, dbias, p.n, static_cast<int32_t>(blocks), f32);
+      const unsigned grid = static_cast<unsigned>((p.n + 7) / 8);
+      if (f32)
+        linear_column_sums<true><<<grid, 256, 0, s>>>(sums, dbias, p.n, static_cast<int32_t>(blocks));
+      else
+        linear_column_sums<false><<<grid, 256, 0, s>>>(sums, dbias, p.n, static_cast<int32_t>(blocks));
       if (cudaGetLastError() != cudaSuccess) rc = MHLA_ERR_CUDA;
     }
   }
@@ -807,7 +941,6 @@ int launch_linear_act_backward(const LinearProblem& p, const void* dout, const v
   if (rc == MHLA_OK && dx) rc = lay_matrix(p.w, p.n, p.k, p.dtype, &ws, &w, s);
   Finish f = {};
   f.act = MHLA_ACT_NONE;
-  f.f32 = f32;
   f.quads = p.k % 4 == 0;
   f.N = p.k;
   if (rc == MHLA_OK && dx) {
