@@ -23,7 +23,8 @@ ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
 
 # rows, k, n: one of each, few rows (a kernel of their own) to its limits, around the tiles of 128 and 64, odd sizes, K in parts
 SHAPES = [(1, 1, 1), (1, 768, 520), (3, 7, 5), (8, 40, 33), (9, 264, 64), (33, 72, 50), (64, 136, 200), (65, 136, 200), (65, 77, 130),
-          (128, 64, 64), (129, 65, 65), (300, 200, 136), (1000, 33, 17), (257, 1032, 72), (70, 2000, 260), (520, 192, 640)]
+          (128, 64, 64), (129, 65, 65), (300, 200, 136), (1000, 33, 17), (257, 1032, 72), (70, 2000, 260), (520, 192, 640), (1500, 264, 520),
+          (700, 4100, 136), (3000, 72, 1288)]
 
 
 def draw(seed, rows, k, n, dtype):

@@ -81,22 +81,33 @@ __device__ __forceinline__ void activate_all(float (&z)[N], int act) {
 template <bool FAST>
 __device__ __forceinline__ float sigmoid(float z) { return FAST ? __fdividef(1.0f, over_sigmoid<true>(z)) : 1.0f / over_sigmoid<false>(z); }
 
-template <bool FAST>
-__device__ __forceinline__ float slope(float z, int act) {
+template <bool FAST, int ACT>
+__device__ __forceinline__ float slope(float z) {
+  if (ACT == MHLA_ACT_RELU) return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
+  if (ACT == MHLA_ACT_GELU)
+    return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) +
+           z * 0.3989422804014327f * (FAST ? __expf(-0.5f * z * z) : expf(-0.5f * z * z));
+  if (ACT == MHLA_ACT_GELU_TANH) {
+    z = z > 30.0f ? 30.0f : z < -30.0f ? -30.0f : z;   // 1 and 0 there; the cube stays finite
+    const float u = kTanhScale * fmaf(kTanhCube * z * z, z, z), p = sigmoid<FAST>(2.0f * u);
+    return p + z * p * (1.0f - p) * (2.0f * kTanhScale) * fmaf(3.0f * kTanhCube * z, z, 1.0f);
+  }
+  const float p = sigmoid<FAST>(z);
+  return p * fmaf(z, 1.0f - p, 1.0f);
+}
+
+// v *= act'(z)
+template <bool FAST, int N>
+__device__ __forceinline__ void times_slope(float (&v)[N], const float (&z)[N], int act) {
+  auto all = [&](auto one) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] *= one(z[i]);
+  };
   switch (act) {
-    case MHLA_ACT_RELU: return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
-    case MHLA_ACT_GELU:
-      return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) + z * 0.3989422804014327f * (FAST ? __expf(-0.5f * z * z) : expf(-0.5f * z * z));
-    case MHLA_ACT_GELU_TANH: {
-      z = z > 30.0f ? 30.0f : z < -30.0f ? -30.0f : z;   // 1 and 0 there; the cube stays finite
-      const float u = kTanhScale * fmaf(kTanhCube * z * z, z, z), p = sigmoid<FAST>(2.0f * u);
-      return p + z * p * (1.0f - p) * (2.0f * kTanhScale) * fmaf(3.0f * kTanhCube * z, z, 1.0f);
-    }
-    case MHLA_ACT_SILU: {
-      const float p = sigmoid<FAST>(z);
-      return p * fmaf(z, 1.0f - p, 1.0f);
-    }
-    default: return 1.0f;
+    case MHLA_ACT_RELU: all([](float x) { return slope<FAST, MHLA_ACT_RELU>(x); }); break;
+    case MHLA_ACT_GELU: all([](float x) { return slope<FAST, MHLA_ACT_GELU>(x); }); break;
+    case MHLA_ACT_GELU_TANH: all([](float x) { return slope<FAST, MHLA_ACT_GELU_TANH>(x); }); break;
+    default: all([](float x) { return slope<FAST, MHLA_ACT_SILU>(x); }); break;
   }
 }
 
@@ -228,16 +239,18 @@ struct Product {
   int32_t BN, tiles_n, chunks, splits, split_chunks;
 };
 
-template <int TERMS>
+// PAIR: two CTAs with one tile of 256 rows (cta_group::2), each loading its rows of A and half of B's.
+template <int TERMS, bool PAIR>
 struct GemmLay {
-  static constexpr int BM = 128, BK = 64;
+  static constexpr int BM = 128, BK = 64;                // rows of a CTA
   static constexpr int MOST_N = TERMS == 1 ? 256 : 128;
-  static constexpr int A_BYTES = BM * BK * 2, B_BYTES = MOST_N * BK * 2;
-  static constexpr int STAGE = TERMS * (A_BYTES + B_BYTES), NS = TERMS == 1 ? 4 : 2;
+  static constexpr int A_BYTES = BM * BK * 2, B_BYTES = MOST_N / (PAIR ? 2 : 1) * BK * 2;
+  static constexpr int STAGE = TERMS * (A_BYTES + B_BYTES), NS = PAIR ? 5 : TERMS == 1 ? 4 : 2;
   static constexpr int ACCS = TERMS == 1 ? 2 : 1;        // tiles whose sums tensor memory holds
   static constexpr int MAINS = TERMS == 1 ? 1 : 3;       // accumulators of the large products
   static constexpr int PITCH = 20, STAGING = 32 * PITCH * 4;   // a warp's 32 rows of 16 columns
-  static constexpr int WARPS = 8, THREADS = 64 + 32 * WARPS;
+  static constexpr int SIDE = PAIR ? 3 : 2;              // finishing warps beside one another
+  static constexpr int WARPS = 4 * SIDE, THREADS = 64 + 32 * WARPS;
   static constexpr size_t SMEM = static_cast<size_t>(NS) * STAGE + WARPS * STAGING + 1024 + 1024;
 };
 
@@ -253,12 +266,13 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) { dra
 struct Unit {
   int32_t m0, n0, first, count, split;
 };
-__device__ __forceinline__ Unit unit_of(const Product& p, int64_t u) {
+template <bool PAIR>
+__device__ __forceinline__ Unit unit_of(const Product& p, int64_t u, uint32_t rank) {
   Unit r;
   r.split = static_cast<int32_t>(u % p.splits);
   const int64_t t = u / p.splits;
   r.n0 = static_cast<int32_t>(t % p.tiles_n) * p.BN;
-  r.m0 = static_cast<int32_t>(t / p.tiles_n) * 128;
+  r.m0 = static_cast<int32_t>(t / p.tiles_n) * (PAIR ? 256 : 128) + (PAIR ? 128 * static_cast<int32_t>(rank) : 0);
   r.first = r.split * p.split_chunks;
   r.count = min(p.split_chunks, p.chunks - r.first);
   return r;
@@ -267,9 +281,9 @@ __device__ __forceinline__ Unit unit_of(const Product& p, int64_t u) {
 // Persistent CTAs walk the units, neighbours sharing A's rows in L2.  Warp 0 loads K chunks of 64 (a ring of
 // stages), warp 1 issues the MMAs, eight warps turn the sums round through shared memory, so that a row's columns lie in
 // neighbouring lanes, and finish them.
-template <int TERMS>
-__global__ void __launch_bounds__(GemmLay<TERMS>::THREADS, 1) linear_gemm(const __grid_constant__ Product p) {
-  using L = GemmLay<TERMS>;
+template <int TERMS, bool PAIR>
+__global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(const __grid_constant__ Product p) {
+  using L = GemmLay<TERMS, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
   uint8_t* staging = smem + L::NS * L::STAGE;
@@ -289,7 +303,7 @@ __global__ void __launch_bounds__(GemmLay<TERMS>::THREADS, 1) linear_gemm(const 
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull + a, 1);
-      mbar_init(tempty + a, 32 * L::WARPS);
+      mbar_init(tempty + a, (PAIR ? 64 : 32) * L::WARPS);
     }
     mbar_init(fin, 1);
     *abortf = 0u;
@@ -300,13 +314,21 @@ __global__ void __launch_bounds__(GemmLay<TERMS>::THREADS, 1) linear_gemm(const 
     prefetch_tmap(&p.b);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(tmem_slot, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  if (PAIR) cluster_sync();   // both CTAs' barriers and tensor memory are there
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const int64_t first_unit = PAIR ? blockIdx.x / 2 : blockIdx.x, stride = PAIR ? gridDim.x / 2 : gridDim.x;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -315,50 +337,66 @@ __global__ void __launch_bounds__(GemmLay<TERMS>::THREADS, 1) linear_gemm(const 
       uint32_t ph = 0;
       uint64_t fills = 0;
       bool ok = true;
-      const uint32_t bytes = TERMS * (L::A_BYTES + p.BN * L::BK * 2);
-      for (int64_t u = blockIdx.x; ok && u < p.units; u += gridDim.x) {
-        const Unit un = unit_of(p, u);
+      const int b_rows = PAIR ? p.BN / 2 : p.BN;
+      const uint32_t bytes = TERMS * (L::A_BYTES + b_rows * L::BK * 2);
+      auto load = [&](uint8_t* at, const CUtensorMap* map, int st, int32_t x, int32_t y, int32_t z) {
+        if (PAIR)
+          tma_load_3d_pair(at, map, full + st, x, y, z, policy);
+        else
+          tma_load_3d(at, map, full + st, x, y, z, policy);
+      };
+      for (int64_t u = first_unit; ok && u < p.units; u += stride) {
+        const Unit un = unit_of<PAIR>(p, u, rank);
+        const int32_t n0 = un.n0 + static_cast<int32_t>(rank) * b_rows;
         for (int kc = 0; kc < un.count; ++kc) {
           if (!wait_bounded(empty + s, ph ^ 1u, abortf)) { ok = false; break; }
-          mbar_arrive_expect_tx(full + s, bytes);
+          // rank 0's barrier counts both CTAs' bytes
+          if (rank == 0) mbar_arrive_expect_tx(full + s, (PAIR ? 2 : 1) * bytes);
           uint8_t* st = smem + s * L::STAGE;
           const int32_t k0 = (un.first + kc) * L::BK;
 #pragma unroll
           for (int t = 0; t < TERMS; ++t) {
             uint8_t* at = st + t * L::A_BYTES;
             if (p.a_major) {
-              tma_load_3d(at, &p.a, full + s, un.m0, k0, t, policy);
-              tma_load_3d(at + 8192, &p.a, full + s, un.m0 + 64, k0, t, policy);
+              load(at, &p.a, s, un.m0, k0, t);
+              load(at + 8192, &p.a, s, un.m0 + 64, k0, t);
             } else {
-              tma_load_3d(at, &p.a, full + s, k0, un.m0, t, policy);
+              load(at, &p.a, s, k0, un.m0, t);
             }
             at = st + TERMS * L::A_BYTES + t * L::B_BYTES;
             if (p.b_major) {
-              for (int j = 0; j < p.BN / 64; ++j) tma_load_3d(at + 8192 * j, &p.b, full + s, un.n0 + 64 * j, k0, t, policy);
+              for (int j = 0; j < b_rows / 64; ++j) load(at + 8192 * j, &p.b, s, n0 + 64 * j, k0, t);
             } else {
-              tma_load_3d(at, &p.b, full + s, k0, un.n0, t, policy);
+              load(at, &p.b, s, k0, n0, t);
             }
           }
           ++fills;
           if (++s == L::NS) { s = 0; ph ^= 1u; }
         }
       }
-      for (int st = 0; st < L::NS; ++st) {
-        const uint64_t n = fills / L::NS + (static_cast<uint64_t>(st) < fills % L::NS ? 1 : 0);
-        if (n > 0) drain_wait(full + st, static_cast<uint32_t>((n - 1) & 1));
-      }
+      if (rank == 0)
+        for (int st = 0; st < L::NS; ++st) {
+          const uint64_t n = fills / L::NS + (static_cast<uint64_t>(st) < fills % L::NS ? 1 : 0);
+          if (n > 0) drain_wait(full + st, static_cast<uint32_t>((n - 1) & 1));
+        }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(L::BM, p.BN, p.a_major != 0, p.b_major != 0);
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = idesc_bf16_f32(PAIR ? 256 : 128, p.BN, p.a_major != 0, p.b_major != 0);
       // steps of 16 of K: 32 bytes along swizzled rows, or 16 rows of 128 bytes
       const uint32_t a_step = p.a_major ? 2048 : 32, b_step = p.b_major ? 2048 : 32;
       const uint32_t a_lbo = p.a_major ? 8192 : 16, b_lbo = p.b_major ? 8192 : 16;
+      auto commit = [&](uint64_t* bar) {
+        if (PAIR)
+          mma_commit_pair(bar);
+        else
+          mma_commit(bar);
+      };
       int s = 0;
       uint32_t ph = 0, local = 0;
       bool ok = true;
-      for (int64_t u = blockIdx.x; ok && u < p.units; u += gridDim.x, ++local) {
-        const Unit un = unit_of(p, u);
+      for (int64_t u = first_unit; ok && u < p.units; u += stride, ++local) {
+        const Unit un = unit_of<PAIR>(p, u, rank);
         const uint32_t acc = local % L::ACCS, aph = (local / L::ACCS) & 1u;
         if (!wait_bounded(tempty + acc, aph ^ 1u, abortf)) break;
         tc_fence_after();
@@ -380,28 +418,31 @@ __global__ void __launch_bounds__(GemmLay<TERMS>::THREADS, 1) linear_gemm(const 
                 const uint64_t a = smem_desc(a_base + i * L::A_BYTES + ks * a_step, a_lbo, 1024, 2);
                 const uint64_t b = smem_desc(b_base + j * L::B_BYTES + ks * b_step, b_lbo, 1024, 2);
                 const bool first = large ? opens && ks == 0 : kc == 0 && ks == 0 && i == TERMS - 1;
-                mma_bf16(dt + (large ? 128 * main : 128 * L::MAINS), a, b, idesc, first ? 0u : 1u);
+                const uint32_t to = dt + (large ? 128 * main : 128 * L::MAINS);
+                if (PAIR)
+                  mma_bf16_pair(to, a, b, idesc, first ? 0u : 1u);
+                else
+                  mma_bf16(to, a, b, idesc, first ? 0u : 1u);
               }
-          mma_commit(empty + s);
+          commit(empty + s);
           if (++s == L::NS) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
-        mma_commit(tfull + acc);
+        commit(tfull + acc);
       }
-      mma_commit(fin);
+      commit(fin);
       drain_wait(fin, 0);
     }
   } else {
-    const int q4 = warp & 3, half = (warp - 2) >> 2;   // TMEM lane quarter this warp may read; its half of the columns
+    const int q4 = warp & 3, side = (warp - 2) >> 2;   // TMEM lane quarter this warp may read; every SIDE-th group of 16 columns is its own
     float* stage = reinterpret_cast<float*>(staging + (warp - 2) * L::STAGING);
     constexpr bool F32 = TERMS > 1;
-    const int mine = p.BN / 32;                        // BN is a multiple of 64
     const bool whole = p.f.quads && !p.parts;
     uint32_t local = 0;
-    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x, ++local) {
-      const Unit un = unit_of(p, u);
+    for (int64_t u = first_unit; u < p.units; u += stride, ++local) {
+      const Unit un = unit_of<PAIR>(p, u, rank);
       const uint32_t acc = local % L::ACCS, aph = (local / L::ACCS) & 1u;
-      const int64_t row0 = un.m0 + 32 * q4 + (lane >> 2), c0 = un.n0 + 16 * half * mine + 4 * (lane & 3);
+      const int64_t row0 = un.m0 + 32 * q4 + (lane >> 2), c0 = un.n0 + 4 * (lane & 3);
       const int64_t i0 = row0 * p.f.N + c0;
       const int rows = static_cast<int>(max(int64_t{0}, min(int64_t{4}, (p.f.M - row0 + 7) / 8)));   // of this lane's four
       // what the finish reads of memory: the first group's while the products run, then a group ahead
@@ -414,16 +455,16 @@ __global__ void __launch_bounds__(GemmLay<TERMS>::THREADS, 1) linear_gemm(const 
           for (int i = 0; i < 4; ++i)
             if (i < rows) residual[i].fetch(p.f.residual, i0 + 8 * i * p.f.N + 16 * gi);
       };
-      fetch(0);
+      fetch(side);
       if (!warp_wait(tfull + acc, aph, abortf)) break;
       tc_fence_after();
-      const uint32_t tb = tmem + acc * 256 + (static_cast<uint32_t>(32 * q4) << 16) + 16 * half * mine;
+      const uint32_t tb = tmem + acc * 256 + (static_cast<uint32_t>(32 * q4) << 16);
       const int mains = TERMS == 1 ? 1 : min(un.count, L::MAINS);
-      const int used = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(mine), (p.f.N - un.n0 - 16 * half * mine + 15) / 16)));
+      const int used = static_cast<int>(min(static_cast<int64_t>(p.BN / 16), (p.f.N - un.n0 + 15) / 16));
       uint32_t next[16];
-      if (TERMS == 1 && used > 0) tmem_ld_x16(tb, next);
+      if (TERMS == 1 && side < used) tmem_ld_x16(tb + 16 * side, next);
 #pragma unroll 1
-      for (int gi = 0; gi < used; ++gi) {
+      for (int gi = side; gi < used; gi += L::SIDE) {
         uint32_t v[16];
         if (TERMS > 1) {
           uint32_t x[16], y[16], z[16];
@@ -449,7 +490,7 @@ __global__ void __launch_bounds__(GemmLay<TERMS>::THREADS, 1) linear_gemm(const 
         for (int e = 0; e < 4; ++e)
           *reinterpret_cast<uint4*>(stage + lane * L::PITCH + 4 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         __syncwarp();
-        if (TERMS == 1 && gi + 1 < used) tmem_ld_x16(tb + 16 * (gi + 1), next);
+        if (TERMS == 1 && gi + L::SIDE < used) tmem_ld_x16(tb + 16 * (gi + L::SIDE), next);
         float z[16];
         const float4 add = p.f.bias ? bias.value() : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -466,7 +507,7 @@ __global__ void __launch_bounds__(GemmLay<TERMS>::THREADS, 1) linear_gemm(const 
             now[i] = residual[i];
             z[4 * i] += add.x; z[4 * i + 1] += add.y; z[4 * i + 2] += add.z; z[4 * i + 3] += add.w;
           }
-          if (gi + 1 < used) fetch(gi + 1);
+          if (gi + L::SIDE < used) fetch(gi + L::SIDE);
           if (c < p.f.N) finish_quads<F32, 4>(p.f, i0 + 16 * gi, 8 * p.f.N, rows, z, now);
         } else if (c < p.f.N) {
 #pragma unroll
@@ -482,14 +523,25 @@ __global__ void __launch_bounds__(GemmLay<TERMS>::THREADS, 1) linear_gemm(const 
         __syncwarp();
       }
       tc_fence_before();
-      mbar_arrive(tempty + acc);   // the sums are read out
+      if (PAIR)
+        mbar_arrive_at(tempty + acc, 0);   // the sums are read out
+      else
+        mbar_arrive(tempty + acc);
     }
   }
   tc_fence_before();
+  // neither CTA leaves while the other's MMAs read its shared memory or their commits arrive there
   __syncthreads();
+  if (PAIR) {
+    if (rank == 1 && threadIdx.x == 32) drain_wait(fin, 0);   // the last of rank 0's commits, behind those this CTA waited for
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if (PAIR)
+      tmem_dealloc_pair(tmem, 512);
+    else
+      tmem_dealloc(tmem, 512);
   }
 }
 
@@ -567,17 +619,17 @@ __global__ void __launch_bounds__(256) linear_planes(const __grid_constant__ Pla
           if (p.pre) w[j] = fetch(p.pre, (r0 + 8 * j) * p.cols + c);
         }
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
+      for (int j = 0; j < BATCH; ++j) {   // one branch an activation: the rest of the code is small
         const int64_t r = r0 + 8 * j;
         if (r >= last) break;
         float v[VEC], z[VEC];
         open(a[j], v);
-        if (p.pre) open(w[j], z);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          if (p.pre) v[e] *= slope<TERMS == 1>(z[e], p.act);
-          sum[e] += v[e];
+        if (p.pre) {
+          open(w[j], z);
+          times_slope<TERMS == 1>(v, z, p.act);
         }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum[e] += v[e];
         if (!p.dst) continue;
 #pragma unroll
         for (int t = 0; t < TERMS; ++t) {
@@ -724,52 +776,93 @@ bool encode_planes(CUtensorMap* m, const Matrix& x, int terms, int box_cols, int
   return encode_tensor_map(m, 3, const_cast<void*>(x.data), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// How C [M][N] over K is cut.  Time of a unit: its chunks, by the operand bytes of one (a chunk of 128 + 256 rows takes about
-// 0.55 us under full load), and what its epilogue leaves uncovered.  K is split where there are few tiles.
+// How C [M][N] over K is cut.  Time of a unit: its chunks, by the operand bytes that an SM takes in (a chunk of 128 + 256 rows is
+// about 0.55 us under full load), and what its finish leaves uncovered.  K is split where there are few tiles.
 struct Cutting {
   int BN, tiles_n, chunks, splits, split_chunks;
   int64_t tiles;
+  bool pair;
 };
-Cutting cut_product(int64_t M, int64_t N, int64_t K, int dtype) {
+Cutting cut_product(int64_t M, int64_t N, int64_t K, int dtype, bool b_major) {
   const bool f32 = dtype != MHLA_BF16;
   Cutting best = {};
   double least = 0;
   const int chunks = static_cast<int>((K + 63) / 64);
-  for (int BN : {64, 128, 192, 256}) {
-    if (f32 && BN > 128) break;
-    Cutting c = {};
-    c.BN = BN;
-    c.chunks = chunks;
-    c.tiles_n = static_cast<int>((N + BN - 1) / BN);
-    c.tiles = (M + 127) / 128 * c.tiles_n;
-    const double chunk_us = (f32 ? 3.0 : 1.0) * 0.55 * (128 + BN) / 384, tail_us = 1.5 + 0.01 * BN;
-    for (int splits = 1; splits <= 64; splits = splits < 8 ? splits + 1 : 2 * splits) {
-      if (splits > 1 && (splits > chunks || c.tiles * (splits - 1) >= 2 * kSms)) break;
-      const int each = (chunks + splits - 1) / splits, used = (chunks + each - 1) / each;
-      const int64_t waves = (c.tiles * used + kSms - 1) / kSms;
-      // the parts are written and read: 8 bytes a value at 4 bytes a ns and part, and a launch
-      const double us = waves * (each * chunk_us) + tail_us * (waves > 1 ? 1.3 : 1.0) +
-                        (used > 1 ? 3.0 + 8e-6 * static_cast<double>(used) * M * N / 4 : 0.0);
-      if (best.BN == 0 || us < least) {
-        least = us;
-        best = c;
-        best.splits = used;
-        best.split_chunks = each;
+  for (int pair = 0; pair < (f32 || M <= 128 ? 1 : 2); ++pair)
+    for (int BN : {64, 128, 192, 256}) {
+      if (f32 && BN > 128) break;
+      if (pair && (BN == 64 || (BN == 192 && b_major))) continue;   // halves of B in whole boxes of 64
+      Cutting c = {};
+      c.BN = BN;
+      c.pair = pair;
+      c.chunks = chunks;
+      c.tiles_n = static_cast<int>((N + BN - 1) / BN);
+      const int64_t m = pair ? 256 : 128;
+      c.tiles = (M + m - 1) / m * c.tiles_n;
+      const int64_t machine = pair ? kSms / 2 : kSms;
+      const double chunk_us = (f32 ? 3.0 : 1.0) * 0.55 * (128 + (pair ? BN / 2 : BN)) / 384, tail_us = 1.5 + 0.01 * BN;
+      for (int splits = 1; splits <= 64; splits = splits < 8 ? splits + 1 : 2 * splits) {
+        if (splits > 1 && (splits > chunks || c.tiles * (splits - 1) >= 2 * machine)) break;
+        const int each = (chunks + splits - 1) / splits, used = (chunks + each - 1) / each;
+        const int64_t waves = (c.tiles * used + machine - 1) / machine;
+        // the parts are written and read: 8 bytes a value at 4 bytes a ns and part, and a launch
+        const double us = waves * (each * chunk_us) + tail_us * (waves > 1 ? 1.3 : 1.0) +
+                          (used > 1 ? 3.0 + 8e-6 * static_cast<double>(used) * M * N / 4 : 0.0);
+        if (best.BN == 0 || us < least) {
+          least = us;
+          best = c;
+          best.splits = used;
+          best.split_chunks = each;
+        }
       }
     }
-  }
   return best;
 }
 size_t part_bytes(int64_t M, int64_t N, const Cutting& c) {
   return c.splits < 2 ? 0 : align_up(static_cast<size_t>(c.splits) * M * ((N + 3) / 4 * 4) * 4);
 }
 
+template <int TERMS, bool PAIR>
+int launch_product(const char* name, const Product& p, cudaStream_t s) {
+  using L = GemmLay<TERMS, PAIR>;
+  auto kernel = linear_gemm<TERMS, PAIR>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L::SMEM)) != cudaSuccess)
+    return MHLA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(L::THREADS);
+  cfg.dynamicSmemBytes = L::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  int64_t grid = 0;
+  if (PAIR) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    cfg.gridDim = dim3(2);
+    if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters < 1) return MHLA_ERR_CUDA;
+    grid = 2 * std::min<int64_t>(p.units, clusters);
+  } else {
+    const int sms = device_sm_count();
+    if (sms <= 0) return MHLA_ERR_CUDA;
+    grid = std::min<int64_t>(p.units, sms);
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  KernelTimer timer(name, s);
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return MHLA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
+}
+
 int run_product(const char* name, const Matrix& a, bool a_major, const Matrix& b, bool b_major, int64_t M, int64_t N, int64_t K,
                 int dtype, const Finish& f, char* parts, cudaStream_t s) {
   const int terms = dtype == MHLA_BF16 ? 1 : 3;
-  const Cutting c = cut_product(M, N, K, dtype);
+  const Cutting c = cut_product(M, N, K, dtype, b_major);
   Product p = {};
-  if (!encode_planes(&p.a, a, terms, 64, a_major ? 64 : 128) || !encode_planes(&p.b, b, terms, 64, b_major ? 64 : c.BN))
+  if (!encode_planes(&p.a, a, terms, 64, a_major ? 64 : 128) ||
+      !encode_planes(&p.b, b, terms, 64, b_major ? 64 : c.pair ? c.BN / 2 : c.BN))
     return MHLA_ERR_CUDA;
   p.f = f;
   p.parts = c.splits > 1 ? reinterpret_cast<float*>(parts) : nullptr;
@@ -777,24 +870,8 @@ int run_product(const char* name, const Matrix& a, bool a_major, const Matrix& b
   p.units = c.tiles * c.splits;
   p.a_major = a_major; p.b_major = b_major;
   p.BN = c.BN; p.tiles_n = c.tiles_n; p.chunks = c.chunks; p.splits = c.splits; p.split_chunks = c.split_chunks;
-  const int sms = device_sm_count();
-  if (sms <= 0) return MHLA_ERR_CUDA;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(p.units, sms));
-  {
-    KernelTimer timer(name, s);
-    if (terms == 1) {
-      using L = GemmLay<1>;
-      if (cudaFuncSetAttribute(linear_gemm<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L::SMEM)) != cudaSuccess)
-        return MHLA_ERR_CUDA;
-      linear_gemm<1><<<grid, L::THREADS, L::SMEM, s>>>(p);
-    } else {
-      using L = GemmLay<3>;
-      if (cudaFuncSetAttribute(linear_gemm<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L::SMEM)) != cudaSuccess)
-        return MHLA_ERR_CUDA;
-      linear_gemm<3><<<grid, L::THREADS, L::SMEM, s>>>(p);
-    }
-    if (cudaGetLastError() != cudaSuccess) return MHLA_ERR_CUDA;
-  }
+  const int rc = terms > 1 ? launch_product<3, false>(name, p, s) : c.pair ? launch_product<1, true>(name, p, s) : launch_product<1, false>(name, p, s);
+  if (rc != MHLA_OK) return rc;
   if (c.splits < 2) return MHLA_OK;
   const Join j = {f, p.parts, p.pitch, c.splits};
   KernelTimer timer("linear_join", s);
@@ -866,7 +943,7 @@ int run_rows(const LinearProblem& p, const Finish& f, cudaStream_t s) {
 size_t linear_act_workspace_bytes(const LinearProblem& p) {
   if (few_rows(p)) return 0;
   return lay_bytes(p.rows, p.k, p.dtype) + lay_bytes(p.n, p.k, p.dtype) +
-         part_bytes(p.rows, p.n, cut_product(p.rows, p.n, p.k, p.dtype));
+         part_bytes(p.rows, p.n, cut_product(p.rows, p.n, p.k, p.dtype, false));
 }
 
 int launch_linear_act(const LinearProblem& p, const void* bias, const void* residual, void* pre, void* out, void* workspace,
@@ -898,8 +975,8 @@ int launch_linear_act(const LinearProblem& p, const void* bias, const void* resi
 size_t linear_act_bwd_workspace_bytes(const LinearProblem& p) {
   // dz (where it is not dout as it lies), x, w, the parts of either product, the sums of dz's columns
   const bool plain = p.act == MHLA_ACT_NONE && direct(p.n, p.dtype);
-  const size_t parts = std::max(part_bytes(p.rows, p.k, cut_product(p.rows, p.k, p.n, p.dtype)),
-                                part_bytes(p.n, p.k, cut_product(p.n, p.k, p.rows, p.dtype)));
+  const size_t parts = std::max(part_bytes(p.rows, p.k, cut_product(p.rows, p.k, p.n, p.dtype, true)),
+                                part_bytes(p.n, p.k, cut_product(p.n, p.k, p.rows, p.dtype, true)));
   return (plain ? 0 : plane_bytes(p.rows, p.n, p.dtype)) + lay_bytes(p.rows, p.k, p.dtype) + lay_bytes(p.n, p.k, p.dtype) + parts +
          align_up(static_cast<size_t>(blocks_of_rows(p.rows, p.n, p.dtype) * p.n) * 4);
 }
