@@ -248,10 +248,12 @@ struct GemmLay {
   static constexpr int STAGE = TERMS * (A_BYTES + B_BYTES), NS = PAIR ? 5 : TERMS == 1 ? 4 : 2;
   static constexpr int ACCS = TERMS == 1 ? 2 : 1;        // tiles whose sums tensor memory holds
   static constexpr int MAINS = TERMS == 1 ? 1 : 3;       // accumulators of the large products
-  static constexpr int PITCH = 20, STAGING = 32 * PITCH * 4;   // a warp's 32 rows of 16 columns
+  static constexpr int GROUP = PAIR ? 32 : 16;           // columns a warp finishes at once
+  static constexpr int PITCH = GROUP + 4, STAGING = 32 * PITCH * 4;   // a warp's 32 rows of them
   static constexpr int SIDE = PAIR ? 3 : 2;              // finishing warps beside one another
   static constexpr int WARPS = 4 * SIDE, THREADS = 64 + 32 * WARPS;
   static constexpr size_t SMEM = static_cast<size_t>(NS) * STAGE + WARPS * STAGING + 1024 + 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
@@ -434,39 +436,39 @@ __global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(
       drain_wait(fin, 0);
     }
   } else {
-    const int q4 = warp & 3, side = (warp - 2) >> 2;   // TMEM lane quarter this warp may read; every SIDE-th group of 16 columns is its own
+    const int q4 = warp & 3, side = (warp - 2) >> 2;   // TMEM lane quarter this warp may read; every SIDE-th group of columns is its own
     float* stage = reinterpret_cast<float*>(staging + (warp - 2) * L::STAGING);
     constexpr bool F32 = TERMS > 1;
+    constexpr int GROUP = L::GROUP, LANES = GROUP / 4, STEP = 32 / LANES, ROWS = 32 / STEP;   // lanes a row, rows at once, rows a lane
     const bool whole = p.f.quads && !p.parts;
+    const int lane_row = lane / LANES, lane_col = 4 * (lane % LANES);
     uint32_t local = 0;
     for (int64_t u = first_unit; u < p.units; u += stride, ++local) {
       const Unit un = unit_of<PAIR>(p, u, rank);
       const uint32_t acc = local % L::ACCS, aph = (local / L::ACCS) & 1u;
-      const int64_t row0 = un.m0 + 32 * q4 + (lane >> 2), c0 = un.n0 + 4 * (lane & 3);
+      const int64_t row0 = un.m0 + 32 * q4 + lane_row, c0 = un.n0 + lane_col;
       const int64_t i0 = row0 * p.f.N + c0;
-      const int rows = static_cast<int>(max(int64_t{0}, min(int64_t{4}, (p.f.M - row0 + 7) / 8)));   // of this lane's four
+      const int rows = static_cast<int>(max(int64_t{0}, min(int64_t{ROWS}, (p.f.M - row0 + STEP - 1) / STEP)));   // of this lane's
       // what the finish reads of memory: the first group's while the products run, then a group ahead
-      Quad<F32> residual[4] = {}, bias = {};
+      Quad<F32> residual[ROWS] = {}, bias = {};
       auto fetch = [&](int gi) {
-        if (!whole || c0 + 16 * gi >= p.f.N) return;
-        if (p.f.bias) bias.fetch(p.f.bias, c0 + 16 * gi);
+        if (!whole || c0 + GROUP * gi >= p.f.N) return;
+        if (p.f.bias) bias.fetch(p.f.bias, c0 + GROUP * gi);
         if (p.f.residual)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < rows) residual[i].fetch(p.f.residual, i0 + 8 * i * p.f.N + 16 * gi);
+          for (int i = 0; i < ROWS; ++i)
+            if (i < rows) residual[i].fetch(p.f.residual, i0 + STEP * i * p.f.N + GROUP * gi);
       };
       fetch(side);
       if (!warp_wait(tfull + acc, aph, abortf)) break;
       tc_fence_after();
       const uint32_t tb = tmem + acc * 256 + (static_cast<uint32_t>(32 * q4) << 16);
       const int mains = TERMS == 1 ? 1 : min(un.count, L::MAINS);
-      const int used = static_cast<int>(min(static_cast<int64_t>(p.BN / 16), (p.f.N - un.n0 + 15) / 16));
-      uint32_t next[16];
-      if (TERMS == 1 && side < used) tmem_ld_x16(tb + 16 * side, next);
+      const int used = static_cast<int>(min(static_cast<int64_t>(p.BN / GROUP), (p.f.N - un.n0 + GROUP - 1) / GROUP));
 #pragma unroll 1
       for (int gi = side; gi < used; gi += L::SIDE) {
-        uint32_t v[16];
-        if (TERMS > 1) {
+        uint32_t v[GROUP];
+        if constexpr (TERMS > 1) {
           uint32_t x[16], y[16], z[16];
           tmem_ld_x16(tb + 16 * gi, v);
           tmem_ld_x16(tb + 128 * L::MAINS + 16 * gi, z);
@@ -481,43 +483,44 @@ __global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(
             v[e] = __float_as_uint(__uint_as_float(v[e]) + sum);
           }
         } else {
+          if constexpr (GROUP == 32)
+            tmem_ld_x32(tb + 32 * gi, v);
+          else
+            tmem_ld_x16(tb + 16 * gi, v);
           tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = next[e];
         }
-        // a row of 16 columns a lane becomes four columns of four rows
+        // a row of the group a lane becomes four columns of ROWS rows
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < LANES; ++e)
           *reinterpret_cast<uint4*>(stage + lane * L::PITCH + 4 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         __syncwarp();
-        if (TERMS == 1 && gi + L::SIDE < used) tmem_ld_x16(tb + 16 * (gi + L::SIDE), next);
-        float z[16];
+        float z[4 * ROWS];
         const float4 add = p.f.bias ? bias.value() : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 x = *reinterpret_cast<const float4*>(stage + (8 * i + (lane >> 2)) * L::PITCH + 4 * (lane & 3));
+        for (int i = 0; i < ROWS; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(stage + (STEP * i + lane_row) * L::PITCH + lane_col);
           z[4 * i] = x.x; z[4 * i + 1] = x.y; z[4 * i + 2] = x.z; z[4 * i + 3] = x.w;
         }
         __syncwarp();
-        const int64_t c = c0 + 16 * gi;
+        const int64_t c = c0 + GROUP * gi;
         if (whole) {
-          Quad<F32> now[4];
+          Quad<F32> now[ROWS];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < ROWS; ++i) {
             now[i] = residual[i];
             z[4 * i] += add.x; z[4 * i + 1] += add.y; z[4 * i + 2] += add.z; z[4 * i + 3] += add.w;
           }
           if (gi + L::SIDE < used) fetch(gi + L::SIDE);
-          if (c < p.f.N) finish_quads<F32, 4>(p.f, i0 + 16 * gi, 8 * p.f.N, rows, z, now);
+          if (c < p.f.N) finish_quads<F32, ROWS>(p.f, i0 + GROUP * gi, STEP * p.f.N, rows, z, now);
         } else if (c < p.f.N) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < ROWS; ++i) {
             if (i >= rows) break;
             const float4 x = make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
             if (p.parts)
-              *reinterpret_cast<float4*>(p.parts + (un.split * p.f.M + row0 + 8 * i) * p.pitch + c) = x;
+              *reinterpret_cast<float4*>(p.parts + (un.split * p.f.M + row0 + STEP * i) * p.pitch + c) = x;
             else
-              finish_quad<F32>(p.f, row0 + 8 * i, c, x);
+              finish_quad<F32>(p.f, row0 + STEP * i, c, x);
           }
         }
         __syncwarp();
