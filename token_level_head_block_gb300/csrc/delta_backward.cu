@@ -14,11 +14,15 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstddef>
 #include <cstdint>
 
 #include "delta_common.cuh"
+#include "tc_common.cuh"
 
 namespace mhla {
+
+__device__ unsigned int g_delta_back_error = 0;
 
 using namespace delta;
 
@@ -30,21 +34,31 @@ struct BackArgs {
   float* first;         // of the first one, or null
 };
 
-// A CTA walks the chunks backwards with 16 MT columns of the state's gradient, as delta_scan does forwards; the warps beside
-// the chain's form, a chunk ahead, what of it does not wait for the chain.
+// A CTA walks the chunks backwards with 16 MT columns of the state's gradient, as delta_scan does forwards; the warps beside the
+// chain's fetch what both read and form, a chunk ahead, what of it does not wait for the chain.
 template <typename T, int DK, int MT>
 struct BackLay {
   using L = Lay<T, DK>;
+  using M = typename L::M;
   static constexpr int kWarps = L::kTiles, kThreads = 64 * kWarps;
   static constexpr int kShare = DK / 16 < kWarps ? 1 : DK / 16 / kWarps;   // blocks of the state's rows a warp
-  static constexpr int kK = 0, kKeys = kK + L::kSides * L::kIn * kBlock, kStage = kKeys + kShare * L::kTiles * kChain * kBlock;
-  static constexpr int kDout = 0, kScores = kDout + MT * L::kTiles * L::kIn * kBlock, kQ = kScores + L::kTiles * kChain * kBlock;
-  static constexpr int kAhead = kQ + kShare * L::kTiles * L::kIn * kBlock;
   static constexpr int kHand = MT * (2 + 2 * kShare) * kBlock;           // a warp's part of P^T do and Q^T do
   static constexpr int kStatePlane = 16 * MT * DK * 2, kTokenPlane = 16 * MT * L::C * 2;
   static constexpr int kState = 0, kW = kState + kChain * kStatePlane, kHands = kW + kChain * kTokenPlane;
-  static constexpr int kRing = kHands + 2 * kWarps * kHand, kRingAhead = kRing + kWarps * kStage;
-  static constexpr int kBytes = kRingAhead + kWarps * kAhead;
+  static constexpr int kRing = kHands + 2 * kWarps * kHand;
+  // of a chunk, the chain's: blocks of K, of K^
+  static constexpr int kKBytes = L::kSides * L::kIn * kBlock, kKeysBytes = kShare * L::kTiles * kChain * kBlock;
+  static constexpr int kKeys = kKBytes, kPair = kKeys + kKeysBytes;
+  static constexpr int kMarkFrom = offsetof(M, after), kMarkBytes = offsetof(M, first) - kMarkFrom;
+  static constexpr int kMarks = kWarps * kPair, kStage = kMarks + (kMarkBytes + 127) / 128 * 128;
+  // and of the next chunk, what is formed ahead: of dout, of the scores, of Q, e^b
+  static constexpr int kDoutBytes = MT * L::kTiles * L::kIn * kBlock, kScoreBytes = L::kTiles * kChain * kBlock;
+  static constexpr int kQBytes = kShare * L::kTiles * L::kIn * kBlock, kInsideBytes = L::C * 4;
+  static constexpr int kScores = kDoutBytes, kQ = kScores + kScoreBytes, kInside = kQ + kQBytes, kAhead = kInside + kInsideBytes;
+  static constexpr int kAheads = kRing + 2 * kStage;   // one a warp
+  static constexpr int kBytes = kAheads + kWarps * kAhead;
+  static_assert(kBytes <= 226 * 1024, "shared memory");
+  static_assert(kMarkFrom % 16 == 0 && kMarkBytes % 16 == 0 && kPair % 128 == 0 && kAhead % 128 == 0, "copied in units of 16 bytes");
 };
 
 template <typename T, int DK, int MT>
@@ -53,6 +67,7 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
   using L = Lay<T, DK>;
   constexpr int C = L::C, TILES = L::kTiles, SIDES = L::kSides, SHARE = W::kShare;
   extern __shared__ __align__(128) char smem[];
+  __shared__ uint64_t bars[TILES][3];   // of either stage of the chain's operands, of what is formed ahead
   const Common& p = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = (p.d + 16 * MT - 1) / (16 * MT);
@@ -61,101 +76,120 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
   const uint32_t base = ptx::smem_u32(smem);
   const int count = static_cast<int>(p.chunks);
   const int own = warp % TILES;
-  const bool chain = warp < TILES, has_share = own * SHARE < SIDES;
   const int g = lane >> 2, t = 2 * (lane & 3);
+  const bool shares = own * SHARE < SIDES;   // a warp of the chain has rows of the state
+  auto sync = [&]() { ptx::named_bar_sync(1, W::kThreads); };   // of the CTA, from several places in the code
   auto chunk_of = [&](int i) { return bh * p.chunks + (count - 1 - i); };
   auto key_chunk_of = [&](int i) { return key * p.chunks + (count - 1 - i); };
-  auto marks = [&](int i) { return reinterpret_cast<const typename L::M*>(p.im.marks + chunk_of(i) * L::kMarks); };
 
-  // each lane's own blocks, asked for as in delta_scan
-  const uint32_t ring = base + (chain ? W::kRing + own * W::kStage : W::kRingAhead + own * W::kAhead);
-  const char* st = smem + (ring - base);
-  auto load_first = [&](int i) {
-    if (i < count) copy_blocks<SIDES * L::kIn>(ring + W::kK, p.im.k_rows + key_chunk_of(i) * L::kInput + own * SIDES * L::kIn * kBlock, lane);
-    commit();
-  };
-  auto load_second = [&](int i) {
-    if (i < count && has_share)
-      copy_blocks<SHARE * TILES * kChain>(ring + W::kKeys, p.im.keys_add + chunk_of(i) * L::kKeys + own * SHARE * TILES * kChain * kBlock, lane);
-    commit();
-  };
-  auto load_ahead = [&](int i) {
-    if (i < count) {
-      copy_blocks<MT * TILES * L::kIn>(ring + W::kDout, p.im.dout_cols + chunk_of(i) * L::kInput + tile0 * TILES * L::kIn * kBlock, lane);
+  if (warp >= TILES) {
+    uint64_t* bar = bars[own];
+    if (lane == 0) {
 #pragma unroll
-      for (int ks = 0; ks < TILES; ++ks)
-        if (ks >= own)
-          copy_blocks<kChain>(ring + W::kScores + ks * kChain * kBlock,
-                              p.im.scores_back + chunk_of(i) * L::kScoresBack + (own * TILES + ks) * kChain * kBlock, lane);
-      if (has_share)
-        copy_blocks<SHARE * TILES * L::kIn>(ring + W::kQ, p.im.q_add + key_chunk_of(i) * L::kInput + own * SHARE * TILES * L::kIn * kBlock, lane);
+      for (int n = 0; n < 3; ++n) ptx::mbar_init(bar + n, 1);
+      ptx::fence_mbar_init();
     }
-    commit();
-  };
-  // (P^T do)^T of this warp's 16 tokens and ((scale e^b Q)^T do)^T of its share of the state's rows
-  auto ahead = [&](int i) {
-    float4* hand = reinterpret_cast<float4*>(smem + W::kHands + ((i & 1) * TILES + own) * W::kHand) + lane;
-    const auto* m = marks(i);
+    __syncwarp();
+    bool alive = true;   // no wait has given up
+    char* const st = smem + W::kAheads + own * W::kAhead;
+    auto load = [&](int i) {   // the chain's
+      if (lane != 0 || i >= count || !alive) return;
+      char* stage = smem + W::kRing + (i & 1) * W::kStage;
+      char* to = stage + own * W::kPair;
+      uint64_t* on = bar + (i & 1);
+      ptx::mbar_arrive_expect_tx(on, W::kKBytes + (shares ? W::kKeysBytes : 0) + (own == 0 ? W::kMarkBytes : 0));
+      ptx::bulk_load_plain(to, p.im.k_rows + key_chunk_of(i) * L::kInput + own * W::kKBytes, W::kKBytes, on);
+      if (shares) ptx::bulk_load_plain(to + W::kKeys, p.im.keys_add + chunk_of(i) * L::kKeys + own * W::kKeysBytes, W::kKeysBytes, on);
+      if (own == 0) ptx::bulk_load_plain(stage + W::kMarks, p.im.marks + chunk_of(i) * L::kMarks + W::kMarkFrom, W::kMarkBytes, on);
+    };
+    const uint32_t seen = (TILES - own) * kChain * kBlock;   // scores from the diagonal on
+    auto load_ahead = [&](int i) {
+      if (lane != 0 || i >= count || !alive) return;
+      uint64_t* on = bar + 2;
+      ptx::mbar_arrive_expect_tx(on, W::kDoutBytes + seen + (shares ? W::kQBytes : 0) + W::kInsideBytes);
+      ptx::bulk_load_plain(st, p.im.dout_cols + chunk_of(i) * L::kInput + tile0 * TILES * L::kIn * kBlock, W::kDoutBytes, on);
+      ptx::bulk_load_plain(st + W::kScores + own * kChain * kBlock,
+                           p.im.scores_back + chunk_of(i) * L::kScoresBack + own * (TILES + 1) * kChain * kBlock, seen, on);
+      if (shares) ptx::bulk_load_plain(st + W::kQ, p.im.q_add + key_chunk_of(i) * L::kInput + own * W::kQBytes, W::kQBytes, on);
+      ptx::bulk_load_plain(st + W::kInside, p.im.marks + chunk_of(i) * L::kMarks + offsetof(typename L::M, inside), W::kInsideBytes, on);
+    };
+    // (P^T do)^T of 16 tokens and ((scale e^b Q)^T do)^T of a share of the state's rows
+    auto ahead = [&](int i) {
+      float4* hand = reinterpret_cast<float4*>(smem + W::kHands + ((i & 1) * TILES + own) * W::kHand) + lane;
+      const float* inside = reinterpret_cast<const float*>(st + W::kInside);
 #pragma unroll
-    for (int n = 0; n < MT; ++n) {
-      Accumulators<2, true> y;
-      Accumulators<2 * SHARE, true> x;
-      y.clear();
-      x.clear();
+      for (int n = 0; n < MT; ++n) {
+        Accumulators<2, true> y;
+        Accumulators<2 * SHARE, true> x;
+        y.clear();
+        x.clear();
 #pragma unroll
-      for (int ks = 0; ks < TILES; ++ks) {
-        uint32_t o[L::kIn][4];
-        float f[4][2];
+        for (int ks = 0; ks < TILES; ++ks) {
+          uint32_t o[L::kIn][4];
+          float f[4][2];
 #pragma unroll
-        for (int k = 0; k < L::kIn; ++k) {
-          load_block(o[k], st + W::kDout, (n * TILES + ks) * L::kIn + k, lane);
+          for (int k = 0; k < L::kIn; ++k) {
+            load_block(o[k], st, (n * TILES + ks) * L::kIn + k, lane);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[e][0] = k == 0 ? low(o[k][e]) : f[e][0] + low(o[k][e]);
-            f[e][1] = k == 0 ? high(o[k][e]) : f[e][1] + high(o[k][e]);
+            for (int e = 0; e < 4; ++e) {
+              f[e][0] = k == 0 ? low(o[k][e]) : f[e][0] + low(o[k][e]);
+              f[e][1] = k == 0 ? high(o[k][e]) : f[e][1] + high(o[k][e]);
+            }
+          }
+          if (ks >= own) {
+            uint32_t s[kChain][1][4];
+#pragma unroll
+            for (int k = 0; k < kChain; ++k) load_block(s[k][0], st + W::kScores, ks * kChain + k, lane);
+            mma_terms(y, 0, o, s);
+          }
+          if (shares) {
+            uint32_t oa[kChain][4], q[L::kIn][SHARE][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 in = *reinterpret_cast<const float2*>(inside + 16 * ks + 8 * (e >> 1) + t);
+              uint32_t z[kChain];
+              split<kChain>(f[e][0] * (p.scale * in.x), f[e][1] * (p.scale * in.y), z);
+#pragma unroll
+              for (int k = 0; k < kChain; ++k) oa[k][e] = z[k];
+            }
+#pragma unroll
+            for (int k = 0; k < L::kIn; ++k)
+#pragma unroll
+              for (int j = 0; j < SHARE; ++j) load_block(q[k][j], st + W::kQ, (j * TILES + ks) * L::kIn + k, lane);
+            mma_terms(x, 0, oa, q);
           }
         }
-        if (ks >= own) {
-          uint32_t s[kChain][1][4];
 #pragma unroll
-          for (int k = 0; k < kChain; ++k) load_block(s[k][0], st + W::kScores, ks * kChain + k, lane);
-          mma_terms(y, 0, o, s);
-        }
-        if (has_share) {
-          uint32_t oa[kChain][4], q[L::kIn][SHARE][4];
+        for (int j = 0; j < 2; ++j)
+          hand[32 * (n * (2 + 2 * SHARE) + j)] = make_float4(y.get(j, 0), y.get(j, 1), y.get(j, 2), y.get(j, 3));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 in = *reinterpret_cast<const float2*>(m->inside + 16 * ks + 8 * (e >> 1) + t);
-            uint32_t z[kChain];
-            split<kChain>(f[e][0] * (p.scale * in.x), f[e][1] * (p.scale * in.y), z);
-#pragma unroll
-            for (int k = 0; k < kChain; ++k) oa[k][e] = z[k];
-          }
-#pragma unroll
-          for (int k = 0; k < L::kIn; ++k)
-#pragma unroll
-            for (int j = 0; j < SHARE; ++j) load_block(q[k][j], st + W::kQ, (j * TILES + ks) * L::kIn + k, lane);
-          mma_terms(x, 0, oa, q);
-        }
+        for (int j = 0; j < 2 * SHARE; ++j)
+          hand[32 * (n * (2 + 2 * SHARE) + 2 + j)] = make_float4(x.get(j, 0), x.get(j, 1), x.get(j, 2), x.get(j, 3));
       }
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        hand[32 * (n * (2 + 2 * SHARE) + j)] = make_float4(y.get(j, 0), y.get(j, 1), y.get(j, 2), y.get(j, 3));
-#pragma unroll
-      for (int j = 0; j < 2 * SHARE; ++j)
-        hand[32 * (n * (2 + 2 * SHARE) + 2 + j)] = make_float4(x.get(j, 0), x.get(j, 1), x.get(j, 2), x.get(j, 3));
-    }
-  };
-
-  if (chain) {
-    load_first(0);
-    load_second(0);
-  } else {
+    };
     load_ahead(0);
+    load(0);
+    alive = wait_copies(bar + 2, 0, &g_delta_back_error);
+    ahead(0);
+    __syncwarp();
+    load_ahead(1);
+    for (int i = 0; i < count; ++i) {
+      alive = alive && wait_copies(bar + (i & 1), i >> 1 & 1, &g_delta_back_error);
+      sync();   // the chunk's operands, what was formed ahead and the planes of D are there; the chunk before is done with
+      load(i + 1);
+      if (i + 1 < count) {
+        alive = alive && wait_copies(bar + 2, i + 1 & 1, &g_delta_back_error);
+        ahead(i + 1);
+        __syncwarp();
+        load_ahead(i + 2);
+      }
+      sync();
+    }
+    return;
   }
+
   // D^T as delta_scan holds S^T
   float D[MT][2 * SHARE][4];
-  const bool shares = chain && has_share;
   auto publish = [&]() {
 #pragma unroll
     for (int n = 0; n < MT; ++n)
@@ -183,103 +217,99 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
         }
     publish();
   }
-  if (!chain) {
-    wait_all();
-    ahead(0);
-    load_ahead(1);
-  }
-
   for (int i = 0; i < count; ++i) {
-    if (chain) {
-      wait_older();
-      const float4* hand = reinterpret_cast<const float4*>(smem + W::kHands + ((i & 1) * TILES + own) * W::kHand) + lane;
-      const auto* m = marks(i);
-      const float2 after[2] = {*reinterpret_cast<const float2*>(m->after + 16 * own + t),
-                               *reinterpret_cast<const float2*>(m->after + 16 * own + 8 + t)};
-      const float total = m->total;
-      __syncthreads();   // the planes of D and the parts formed ahead are there
-      ChainSum<2> acc[MT];
+    const char* stage = smem + W::kRing + (i & 1) * W::kStage;
+    const char* st = stage + own * W::kPair;
+    const auto* m = reinterpret_cast<const typename L::M*>(stage + W::kMarks - W::kMarkFrom);
+    const float4* hand = reinterpret_cast<const float4*>(smem + W::kHands + ((i & 1) * TILES + own) * W::kHand) + lane;
+    sync();
+    float w[MT][2][4];
+    {
+      // dW^T = (P^T do)^T + D^T (e^{B-b} K)^T
+      ChainSum<MT, 2> acc;
+      acc.clear();
+      uint32_t x[2][L::kIn][1][4], s[2][MT][kChain][4];
+      auto fetch = [&](int ks) {
 #pragma unroll
-      for (int n = 0; n < MT; ++n) acc[n].clear();
+        for (int n = 0; n < MT; ++n)
+#pragma unroll
+          for (int k = 0; k < kChain; ++k) a_rows<DK>(s[ks & 1][n][k], base + W::kState + k * W::kStatePlane, 16 * n, 16 * ks, lane);
+#pragma unroll
+        for (int k = 0; k < L::kIn; ++k) load_block(x[ks & 1][k][0], st, ks * L::kIn + k, lane);
+      };
+      fetch(0);
 #pragma unroll
       for (int ks = 0; ks < SIDES; ++ks) {
-        uint32_t x[L::kIn][1][4];
-#pragma unroll
-        for (int k = 0; k < L::kIn; ++k) load_block(x[k][0], st + W::kK, ks * L::kIn + k, lane);
-#pragma unroll
-        for (int n = 0; n < MT; ++n) {
-          uint32_t s[kChain][4];
-#pragma unroll
-          for (int k = 0; k < kChain; ++k) a_rows<DK>(s[k], base + W::kState + k * W::kStatePlane, 16 * n, 16 * ks, lane);
-          acc[n].add(s, x);
-        }
+        if (ks + 1 < SIDES) fetch(ks + 1);
+        acc.add(s[ks & 1], x[ks & 1], ks & 1);
       }
+      const float2 after[2] = {*reinterpret_cast<const float2*>(m->after + 16 * own + t), *reinterpret_cast<const float2*>(m->after + 16 * own + 8 + t)};
 #pragma unroll
       for (int n = 0; n < MT; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float4 y = hand[32 * (n * (2 + 2 * SHARE) + j)];
-          const float w[4] = {fmaf(after[j].x, acc[n].get(j, 0), y.x), fmaf(after[j].y, acc[n].get(j, 1), y.y),
-                              fmaf(after[j].x, acc[n].get(j, 2), y.z), fmaf(after[j].y, acc[n].get(j, 3), y.w)};
-          if (16 * (tile0 + n) < p.d)
-            *reinterpret_cast<float4*>(p.im.dw + (chunk_of(i) * SIDES + tile0 + n) * L::kTokens + (2 * own + j) * kBlock + 16 * lane) =
-                make_float4(w[0], w[1], w[2], w[3]);
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            uint32_t x[kChain];
-            split<kChain>(w[2 * f], w[2 * f + 1], x);
-#pragma unroll
-            for (int k = 0; k < kChain; ++k)
-              *reinterpret_cast<uint32_t*>(smem + W::kW + k * W::kTokenPlane + unit_at<C>(16 * n + g + 8 * f, 2 * own + j) + 2 * t) = x[k];
-          }
+          w[n][j][0] = fmaf(after[j].x, acc.get(n, j, 0), y.x); w[n][j][1] = fmaf(after[j].y, acc.get(n, j, 1), y.y);
+          w[n][j][2] = fmaf(after[j].x, acc.get(n, j, 2), y.z); w[n][j][3] = fmaf(after[j].y, acc.get(n, j, 3), y.w);
         }
-      load_first(i + 1);
-      __syncthreads();   // the planes of dW are there, those of D are read
-      wait_older();
-      if (shares) {
-        // D^T <- e^B D^T + (Q^T do)^T - dW^T K^, the chunk's part formed apart
-        ChainSum<2 * SHARE> sum[MT];
+    }
 #pragma unroll
-        for (int n = 0; n < MT; ++n) sum[n].clear();
+    for (int n = 0; n < MT; ++n)
 #pragma unroll
-        for (int ks = 0; ks < TILES; ++ks) {
-          uint32_t x[kChain][SHARE][4];
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          uint32_t x[kChain];
+          split<kChain>(w[n][j][2 * f], w[n][j][2 * f + 1], x);
 #pragma unroll
           for (int k = 0; k < kChain; ++k)
-#pragma unroll
-            for (int j = 0; j < SHARE; ++j) load_block(x[k][j], st + W::kKeys, (j * TILES + ks) * kChain + k, lane);
-#pragma unroll
-          for (int n = 0; n < MT; ++n) {
-            uint32_t w[kChain][4];
-#pragma unroll
-            for (int k = 0; k < kChain; ++k) a_rows<C>(w[k], base + W::kW + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
-            sum[n].add(w, x);
-          }
+            *reinterpret_cast<uint32_t*>(smem + W::kW + k * W::kTokenPlane + unit_at<C>(16 * n + g + 8 * f, 2 * own + j) + 2 * t) = x[k];
         }
+    const float total = m->total;
+    sync();   // the planes of dW are there, those of D are read
+#pragma unroll
+    for (int n = 0; n < MT; ++n)
+      if (16 * (tile0 + n) < p.d) {
+        float4* to = reinterpret_cast<float4*>(p.im.dw + (chunk_of(i) * SIDES + tile0 + n) * L::kTokens + 2 * own * kBlock) + lane;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) to[32 * j] = make_float4(w[n][j][0], w[n][j][1], w[n][j][2], w[n][j][3]);
+      }
+    if (!shares) continue;
+    // D^T <- e^B D^T + (Q^T do)^T - dW^T K^, the chunk's part formed apart
+    ChainSum<MT, 2 * SHARE> sum;
+    sum.clear();
+    {
+      uint32_t x[2][kChain][SHARE][4], v[2][MT][kChain][4];
+      auto fetch = [&](int ks) {
 #pragma unroll
         for (int n = 0; n < MT; ++n)
 #pragma unroll
-          for (int j = 0; j < 2 * SHARE; ++j) {
-            if (16 * (tile0 + n) < p.d)
-              *reinterpret_cast<float4*>(p.im.ds + (chunk_of(i) * SIDES + tile0 + n) * L::kState + (2 * own * SHARE + j) * kBlock + 16 * lane) =
-                  make_float4(D[n][j][0], D[n][j][1], D[n][j][2], D[n][j][3]);
-            const float4 x = hand[32 * (n * (2 + 2 * SHARE) + 2 + j)];
-            const float xs[4] = {x.x, x.y, x.z, x.w};
+          for (int k = 0; k < kChain; ++k) a_rows<C>(v[ks & 1][n][k], base + W::kW + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) D[n][j][e] = fmaf(total, D[n][j][e], xs[e] - sum[n].get(j, e));
-          }
-        publish();
+        for (int k = 0; k < kChain; ++k)
+#pragma unroll
+          for (int j = 0; j < SHARE; ++j) load_block(x[ks & 1][k][j], st + W::kKeys, (j * TILES + ks) * kChain + k, lane);
+      };
+      fetch(0);
+#pragma unroll
+      for (int ks = 0; ks < TILES; ++ks) {
+        if (ks + 1 < TILES) fetch(ks + 1);
+        sum.add(v[ks & 1], x[ks & 1], ks & 1);
       }
-      load_second(i + 1);
-    } else {
-      __syncthreads();
-      if (i + 1 < count) {
-        wait_all();
-        ahead(i + 1);
-        load_ahead(i + 2);
-      }
-      __syncthreads();
     }
+#pragma unroll
+    for (int n = 0; n < MT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2 * SHARE; ++j) {
+        if (16 * (tile0 + n) < p.d)
+          *reinterpret_cast<float4*>(p.im.ds + (chunk_of(i) * SIDES + tile0 + n) * L::kState + (2 * own * SHARE + j) * kBlock + 16 * lane) =
+              make_float4(D[n][j][0], D[n][j][1], D[n][j][2], D[n][j][3]);
+        const float4 x = hand[32 * (n * (2 + 2 * SHARE) + 2 + j)];
+        const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) D[n][j][e] = fmaf(total, D[n][j][e], xs[e] - sum.get(n, j, e));
+      }
+    publish();
   }
   if (shares && a.first) {
     float* first = a.first + bh * p.d * p.d;
@@ -754,7 +784,11 @@ int grads_as(const GradArgs& a, int64_t BH, cudaStream_t s) {
 
 template <typename T, int DK>
 int run_as(const BackArgs& b, const GradArgs& g, int64_t BH, bool shared, cudaStream_t s) {
-  const int rc = two_tiles(BH, b.c.d) ? back_as<T, DK, 2>(b, BH, s) : back_as<T, DK, 1>(b, BH, s);
+  int rc;
+  if constexpr (DK <= 64)
+    rc = two_tiles(BH, b.c.d) ? back_as<T, DK, 2>(b, BH, s) : back_as<T, DK, 1>(b, BH, s);
+  else
+    rc = back_as<T, DK, 1>(b, BH, s);
   if (rc != MHLA_OK) return rc;
   return shared && sizeof(T) == 2 ? grads_as<T, DK, float>(g, BH, s) : grads_as<T, DK, T>(g, BH, s);
 }
@@ -810,5 +844,11 @@ int launch_delta_backward(const DeltaProblem& p, const DeltaBackward& d, void* w
     delta_shared<float><<<grid, 256, 0, s>>>(sh);
   return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
 }
+
+int read_and_clear_delta_back_error(void* stream, uint32_t* flags) {
+  return tc::read_and_clear_word(g_delta_back_error, stream, flags);
+}
+
+MHLA_DEFINE_STALL_SETTER(set_stall_delta_back)
 
 }  // namespace mhla

@@ -10,6 +10,7 @@
 #include "gated_common.cuh"
 #include "mhla_internal.h"
 #include "ptx.cuh"
+#include "stall_hook.cuh"
 #include "warp_mma.cuh"
 
 namespace mhla {
@@ -94,33 +95,48 @@ struct Common {
 };
 enum : uint32_t { kWideQ = 1, kWideK = 2, kWideV = 4, kWideDout = 8 };
 
-// Sums of products of three terms each with their own accumulators for what is of one size: the chain of additions to one is a third
-// as long, and small products are not truncated against large ones.
-template <int NT>
+// MT x NT tiles of sums of products of terms.  Products of one size have accumulators of their own, the smallest two sets in
+// turn, and follow one another in an order that keeps two additions to one accumulator four MMAs apart: one warp's chain
+// of them is as long as it takes to issue.  Many tiles are apart enough with two sets.
+template <int MT, int NT>
 struct ChainSum {
-  float part[3][NT][4];
+  static constexpr int kParts = MT * NT <= 4 ? 4 : 2;
+  float part[kParts][MT][NT][4];
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int s = 0; s < 3; ++s)
+    for (int s = 0; s < kParts; ++s)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) part[s][n][e] = 0.0f;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) part[s][m][n][e] = 0.0f;
   }
-  __device__ __forceinline__ float get(int n, int e) const { return part[0][n][e] + (part[1][n][e] + part[2][n][e]); }
-  template <int NA, int NB, int P>
-  __device__ __forceinline__ void add(const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][P][4]) {
-    constexpr int kMost = NA > NB ? NA : NB;
+  __device__ __forceinline__ float get(int m, int n, int e) const {
+    if (kParts == 4) return part[0][m][n][e] + (part[1][m][n][e] + (part[kParts - 2][m][n][e] + part[kParts - 1][m][n][e]));
+    return part[0][m][n][e] + part[1][m][n][e];
+  }
+  template <int NB, int P>
+  __device__ __forceinline__ void one(const uint32_t (&a)[MT][kChain][4], const uint32_t (&b)[NB][P][4], int i, int j, int turn) {
+    const int s = i + j == 0 ? 0 : kParts == 2 || i + j == 1 ? 1 : 2 + turn;
 #pragma unroll
-    for (int i = NA - 1; i >= 0; --i)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int j = NB - 1; j >= 0; --j) {
-        if (i + j >= kMost) continue;
+      for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-          for (int f = 0; f < 2; ++f) mma(part[i + j][2 * p + f], a[i], b[j][p][2 * f], b[j][p][2 * f + 1]);
-      }
+        for (int f = 0; f < 2; ++f) mma(part[s < kParts ? s : 0][m][2 * p + f], a[m][i], b[j][p][2 * f], b[j][p][2 * f + 1]);
+  }
+  template <int NB, int P>
+  __device__ __forceinline__ void add(const uint32_t (&a)[MT][kChain][4], const uint32_t (&b)[NB][P][4], int turn) {
+    static_assert(NB == 1 || NB == kChain, "an input, or three terms");
+    one(a, b, 2, 0, turn);
+    one(a, b, 1, 0, turn);
+    if constexpr (NB > 1) {
+      one(a, b, 1, 1, turn);
+      one(a, b, 0, 1, turn);
+      one(a, b, 0, 2, turn);
+    }
+    one(a, b, 0, 0, turn);
   }
 };
 
@@ -151,12 +167,6 @@ __device__ __forceinline__ void as_rows(uint32_t (&a)[NT][4], const float (&lo)[
 __device__ __forceinline__ void copy_async(uint32_t dst, const char* src, int bytes, int thread, int threads) {
   for (int i = 16 * thread; i < bytes; i += 16 * threads) cp_async_16(dst + i, src + i, 16);
 }
-// N blocks, each lane its own bytes: no other lane's copies are waited for.
-template <int N>
-__device__ __forceinline__ void copy_blocks(uint32_t dst, const char* src, int lane) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) cp_async_16(dst + i * kBlock + 16 * lane, src + i * kBlock + 16 * lane, 16);
-}
 __device__ __forceinline__ void load_block(uint32_t (&r)[4], const char* smem, int block, int lane) {
   const uint4 x = *reinterpret_cast<const uint4*>(smem + block * kBlock + 16 * lane);
   r[0] = x.x; r[1] = x.y; r[2] = x.z; r[3] = x.w;
@@ -168,8 +178,27 @@ __device__ __forceinline__ uint32_t turn(uint32_t x) {
   return y;
 }
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void wait_older() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }   // all but the last group
 __device__ __forceinline__ void wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// Waits for a phase of a barrier that copies complete on.  Bounded: one that gives up is reported in *error and false for the
+// whole warp, which then asks for no more.
+static __device__ __noinline__ bool wait_copies_long(uint64_t* bar, uint32_t parity, unsigned int* error) {
+  if (stall_this_warp()) {   // a test's: it gives up, and the copies in flight are waited for behind it
+    volatile uint32_t none = 0;
+    stalled_wait(&none);
+    atomicOr(error, 1u);
+  }
+  const uint64_t t0 = ptx::globaltimer();
+  for (uint32_t it = 1; it < (1u << 28); ++it) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0 && ptx::globaltimer() - t0 > 2000000000ull) break;
+  }
+  atomicOr(error, 1u);
+  return false;
+}
+__device__ __forceinline__ bool wait_copies(uint64_t* bar, uint32_t parity, unsigned int* error) {
+  return __all_sync(~0u, ptx::mbar_try_wait(bar, parity) || wait_copies_long(bar, parity, error));
+}
 
 template <typename T>
 __device__ __forceinline__ void store_pair(T* p, float x, float y, bool pairs, bool both);
@@ -199,7 +228,7 @@ int launch_prepare(const Common& c, int64_t BH, int dtype, bool grad, cudaStream
 int launch_scan(const ScanArgs& a, int64_t BH, int dtype, bool keep, cudaStream_t s);
 size_t lay_out(const DeltaProblem& p, bool grad, char* base, Images* im);
 Common common(const DeltaProblem& p, const Operand* dout);
-// Whether a scan's CTA takes 32 columns of the state or 16: 16 where all of them run at once.
+// Whether a scan's CTA takes 32 columns of the state or 16 (wider heads always do): 16 where all of them run at once.
 bool two_tiles(int64_t BH, int d);
 bool pairs_fit(const Operand& o, int d, int dtype);
 

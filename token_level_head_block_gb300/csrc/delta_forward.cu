@@ -17,12 +17,16 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstddef>
 #include <cstdint>
 #include <initializer_list>
 
 #include "delta_common.cuh"
+#include "tc_common.cuh"
 
 namespace mhla {
+
+__device__ unsigned int g_delta_error = 0;
 
 using namespace delta;
 
@@ -528,79 +532,165 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
 }
 
 // A CTA walks the chunks with 16 MT columns of the state.  TILES warps make the chain: each forms the W of 16 tokens, and then its
-// share of the state's rows; as many warps beside them, unless KEEP, read 16 tokens' outputs.  KEEP leaves the states and
-// the w of every chunk for the gradients instead.
+// share of the state's rows.  As many warps beside them fetch what both read, chunks ahead, and (unless KEEP) read 16 tokens'
+// outputs, so nothing stands between the chain's products: it waits for two barriers a chunk.  KEEP leaves the states and the
+// w of every chunk for the gradients instead of outputs.
 template <typename T, int DK, int MT, bool KEEP>
 struct ScanLay {
   using L = Lay<T, DK>;
-  static constexpr int kWarps = L::kTiles, kThreads = (KEEP ? 32 : 64) * kWarps;
+  using M = typename L::M;
+  static constexpr int kWarps = L::kTiles, kThreads = 64 * kWarps;
   static constexpr int kShare = DK / 16 < kWarps ? 1 : DK / 16 / kWarps;   // blocks of the state's rows a warp
-  static constexpr int kKeys = 0, kAdd = kKeys + L::kSides * kChain * kBlock, kU = kAdd + kShare * L::kTiles * L::kIn * kBlock;
-  static constexpr int kStage = kU + MT * 2 * kBlock;
-  static constexpr int kQ = 0, kScores = kQ + L::kSides * L::kIn * kBlock, kStageOut = kScores + L::kTiles * L::kScore * kBlock;
   static constexpr int kStatePlane = 16 * MT * DK * 2, kTokenPlane = 16 * MT * L::C * 2;
-  static constexpr int kState = 0, kAfter = kState + 2 * kChain * kStatePlane, kW = kAfter + kChain * kTokenPlane;
-  static constexpr int kRing = kW + (KEEP ? 0 : L::kOwn * kTokenPlane), kRingOut = kRing + kWarps * kStage;
-  static constexpr int kBytes = kRingOut + (KEEP ? 0 : kWarps * kStageOut);
+  static constexpr int kState = 0, kAfter = kState + kChain * kStatePlane, kW = kAfter + kChain * kTokenPlane;
+  static constexpr int kRing = kW + (KEEP ? 0 : L::kOwn * kTokenPlane);
+  // of a chunk, a pair of warps': blocks of K^, U, K, and of Q and the scores
+  static constexpr int kKeysBytes = L::kSides * kChain * kBlock, kUBytes = 2 * kBlock, kAddBytes = kShare * L::kTiles * L::kIn * kBlock;
+  static constexpr int kQBytes = KEEP ? 0 : L::kSides * L::kIn * kBlock, kScoreBytes = KEEP ? 0 : L::kTiles * L::kScore * kBlock;
+  static constexpr int kU = kKeysBytes, kAdd = kU + MT * kUBytes, kQ = kAdd + kAddBytes, kScores = kQ + kQBytes, kPair = kScores + kScoreBytes;
+  static constexpr int kMarkFrom = offsetof(M, inside), kMarkBytes = offsetof(M, first) - kMarkFrom;
+  static constexpr int kMarks = kWarps * kPair, kStage = kMarks + (kMarkBytes + 127) / 128 * 128;
+  static constexpr int kStages = (227 * 1024 - 1024 - kRing) / kStage < 3 ? 2 : 3;
+  static constexpr int kBytes = kRing + kStages * kStage;
+  static_assert(kBytes <= 226 * 1024, "shared memory");
+  static_assert(kMarkFrom % 16 == 0 && kMarkBytes % 16 == 0 && kPair % 128 == 0, "copied in units of 16 bytes");
 };
 
 template <typename T, int DK, int MT, bool KEEP>
 __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan(const __grid_constant__ ScanArgs a) {
   using W = ScanLay<T, DK, MT, KEEP>;
   using L = Lay<T, DK>;
-  constexpr int C = L::C, TILES = L::kTiles, SIDES = L::kSides, SHARE = W::kShare;
+  constexpr int C = L::C, TILES = L::kTiles, SIDES = L::kSides, SHARE = W::kShare, STAGES = W::kStages;
   extern __shared__ __align__(128) char smem[];
+  __shared__ uint64_t bars[TILES][STAGES];
   const Common& p = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = (p.d + 16 * MT - 1) / (16 * MT);
   const int64_t bh = blockIdx.x / groups, b = bh / p.H, h = bh % p.H, key = b * p.Hk + h / (p.H / p.Hk);
   const int tile0 = static_cast<int>(blockIdx.x % groups) * MT;
-  const uint32_t base = ptx::smem_u32(smem);
+  const uint32_t base = ptx::smem_u32(smem), state = base + W::kState;
   const int count = static_cast<int>(p.chunks);
   const int own = warp % TILES;
-  const bool chain = KEEP || warp < TILES;
   const int g = lane >> 2, t = 2 * (lane & 3);
+  const bool shares = own * SHARE < SIDES;   // a warp of the chain has rows of the state
+  auto sync = [&]() { ptx::named_bar_sync(1, W::kThreads); };   // of the CTA, from several places in the code
+  // a chunk's marks from `inside` on
+  auto marks_at = [&](const char* stage) { return reinterpret_cast<const typename L::M*>(stage + W::kMarks - W::kMarkFrom); };
+  // each column's first token that is not finite, where there is one
+  auto first_of = [&](int i) { return reinterpret_cast<const typename L::M*>(p.im.marks + (bh * p.chunks + i) * L::kMarks)->first; };
 
-  auto marks = [&](int i) { return reinterpret_cast<const typename L::M*>(p.im.marks + (bh * p.chunks + i) * L::kMarks); };
-  // Each lane's own blocks of a chunk, in two groups: what the chunk's first half reads, and what its second half does.  A group
-  // is asked for anew as soon as its half is done with it, so it has the other half's time to come.
-  const uint32_t ring = base + (chain ? W::kRing + own * W::kStage : W::kRingOut + own * W::kStageOut);
-  const char* st = smem + (ring - base);
-  auto load_first = [&](int i) {
-    const int64_t at = bh * p.chunks + i, at_key = key * p.chunks + i;
-    if (i >= count) {
-    } else if (chain) {
-      copy_blocks<SIDES * kChain>(ring + W::kKeys, p.im.keys + at * L::kKeys + own * SIDES * kChain * kBlock, lane);
+  if (warp >= TILES) {
+    uint64_t* bar = bars[own];
+    if (lane == 0) {
 #pragma unroll
-      for (int n = 0; n < MT; ++n)
-        if (tile0 + n < SIDES) copy_blocks<2>(ring + W::kU + 2 * n * kBlock, p.im.u + (at * SIDES + tile0 + n) * L::kTokens + 2 * own * kBlock, lane);
-    } else {
-      copy_blocks<SIDES * L::kIn>(ring + W::kQ, p.im.q_rows + at_key * L::kInput + own * SIDES * L::kIn * kBlock, lane);
+      for (int n = 0; n < STAGES; ++n) ptx::mbar_init(bar + n, 1);
+      ptx::fence_mbar_init();
     }
-    commit();
-  };
-  auto load_second = [&](int i) {
-    const int64_t at = bh * p.chunks + i, at_key = key * p.chunks + i;
-    if (i >= count) {
-    } else if (chain) {
-      if (own * SHARE < SIDES)
-        copy_blocks<SHARE * TILES * L::kIn>(ring + W::kAdd, p.im.k_add + at_key * L::kInput + own * SHARE * TILES * L::kIn * kBlock, lane);
-    } else {
+    __syncwarp();
+    bool alive = true;   // no wait has given up
+    const char* keys = p.im.keys + bh * p.chunks * L::kKeys + own * W::kKeysBytes;
+    const char* u = p.im.u + (bh * p.chunks * SIDES + tile0) * L::kTokens + own * W::kUBytes;
+    const char* add = p.im.k_add + key * p.chunks * L::kInput + own * W::kAddBytes;
+    const char* q_rows = KEEP ? nullptr : p.im.q_rows + key * p.chunks * L::kInput + own * W::kQBytes;
+    const char* scores = KEEP ? nullptr : p.im.scores + bh * p.chunks * L::kScores + own * W::kScoreBytes;
+    const char* marks = p.im.marks + bh * p.chunks * L::kMarks + W::kMarkFrom;
+    const uint32_t seen = KEEP ? 0 : (own + 1) * L::kScore * kBlock;   // scores up to the diagonal
+    const uint32_t bytes = W::kKeysBytes + MT * W::kUBytes + (shares ? W::kAddBytes : 0) + W::kQBytes + seen + (own == 0 ? W::kMarkBytes : 0);
+    auto load = [&](int i) {
+      if (lane != 0 || i >= count || !alive) return;
+      char* stage = smem + W::kRing + i % STAGES * W::kStage;
+      char* to = stage + own * W::kPair;
+      uint64_t* on = bar + i % STAGES;
+      ptx::mbar_arrive_expect_tx(on, bytes);
+      ptx::bulk_load_plain(to, keys, W::kKeysBytes, on);
 #pragma unroll
-      for (int ks = 0; ks < TILES; ++ks)
-        if (ks <= own)
-          copy_blocks<L::kScore>(ring + W::kScores + ks * L::kScore * kBlock,
-                                 p.im.scores + at * L::kScores + (own * TILES + ks) * L::kScore * kBlock, lane);
+      for (int n = 0; n < MT; ++n) ptx::bulk_load_plain(to + W::kU + n * W::kUBytes, u + n * L::kTokens, W::kUBytes, on);
+      if (shares) ptx::bulk_load_plain(to + W::kAdd, add, W::kAddBytes, on);
+      if (!KEEP) {
+        ptx::bulk_load_plain(to + W::kQ, q_rows, W::kQBytes, on);
+        ptx::bulk_load_plain(to + W::kScores, scores, seen, on);
+        q_rows += L::kInput;
+        scores += L::kScores;
+      }
+      if (own == 0) ptx::bulk_load_plain(stage + W::kMarks, marks, W::kMarkBytes, on);
+      keys += L::kKeys;
+      u += SIDES * L::kTokens;
+      add += L::kInput;
+      marks += L::kMarks;
+    };
+    for (int i = 0; i < STAGES - 1; ++i) load(i);
+    T* const out = static_cast<T*>(a.out.data) + b * a.out.sb + h * a.out.sh;
+    for (int i = 0; i < count; ++i) {
+      const char* stage = smem + W::kRing + i % STAGES * W::kStage;
+      const char* st = stage + own * W::kPair;
+      alive = alive && wait_copies(bar + i % STAGES, i / STAGES & 1, &g_delta_error);
+      sync();   // the chunk's operands and the state's planes are there; the chunk before is done with
+      load(i + STAGES - 1);
+      if constexpr (KEEP) {
+        sync();
+      } else {
+        // O = scale e^b Q S + scores W, this warp's 16 tokens
+        const auto* m = marks_at(stage);
+        const float in[2] = {p.scale * m->inside[16 * own + g], p.scale * m->inside[16 * own + g + 8]};
+        const int any = m->any;
+        Accumulators<2 * MT, L::kApart> o;
+        o.clear();
+#pragma unroll
+        for (int ks = 0; ks < SIDES; ++ks) {
+          uint32_t q[L::kIn][4], x[L::kOwn][MT][4];
+#pragma unroll
+          for (int k = 0; k < L::kIn; ++k) load_block(q[k], st + W::kQ, ks * L::kIn + k, lane);
+#pragma unroll
+          for (int k = 0; k < L::kOwn; ++k)
+#pragma unroll
+            for (int n = 0; n < MT; ++n) b_rows<DK>(x[k][n], state + k * W::kStatePlane, 16 * n, 16 * ks, lane);
+          mma_terms(o, 0, q, x);
+        }
+#pragma unroll
+        for (int n = 0; n < 2 * MT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o.main[n][e] = o.get(n, e) * in[e >> 1];
+            if (L::kApart) o.small[L::kApart ? n : 0][e] = 0.0f;
+          }
+        sync();   // W's planes are there, the state's are read
+#pragma unroll
+        for (int ks = 0; ks < TILES; ++ks) {
+          if (ks > own) continue;
+          uint32_t q[L::kScore][4], x[L::kOwn][MT][4];
+#pragma unroll
+          for (int k = 0; k < L::kScore; ++k) load_block(q[k], st + W::kScores, ks * L::kScore + k, lane);
+#pragma unroll
+          for (int k = 0; k < L::kOwn; ++k)
+#pragma unroll
+            for (int n = 0; n < MT; ++n) b_rows<C>(x[k][n], base + W::kW + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
+          mma_terms(o, 0, q, x);
+        }
+        const int64_t t0 = static_cast<int64_t>(i) * C;
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int r = 16 * own + g + 8 * f;
+          if (t0 + r >= p.N) continue;
+#pragma unroll
+          for (int n = 0; n < 2 * MT; ++n) {
+            const int c = 16 * tile0 + 8 * n + t;
+            if (c >= p.d) continue;
+            float y[2] = {o.get(n, 2 * f), o.get(n, 2 * f + 1)};
+            if (any)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (r >= first_of(i)[c + e]) y[e] = nan_value();
+            store_pair<T>(out + (t0 + r) * a.out.sn + c, y[0], y[1], a.out_pairs, c + 1 < p.d);
+          }
+        }
+      }
     }
-    commit();
-  };
-  load_first(0);
-  load_second(0);
+    return;
+  }
 
   // S^T: rows the state's columns 16 (tile0 + n) + g, + 8; columns this warp's share of its rows
   float S[MT][2 * SHARE][4];
-  const bool shares = chain && own * SHARE < SIDES;
-  auto publish = [&](int i) {   // as planes of terms
+  auto publish = [&]() {   // as planes of terms
 #pragma unroll
     for (int n = 0; n < MT; ++n)
 #pragma unroll
@@ -611,8 +701,7 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
           split<kChain>(S[n][j][2 * f], S[n][j][2 * f + 1], x);
 #pragma unroll
           for (int k = 0; k < kChain; ++k)
-            *reinterpret_cast<uint32_t*>(smem + W::kState + ((i & 1) * kChain + k) * W::kStatePlane +
-                                         unit_at<DK>(16 * n + g + 8 * f, 2 * own * SHARE + j) + 2 * t) = x[k];
+            *reinterpret_cast<uint32_t*>(smem + W::kState + k * W::kStatePlane + unit_at<DK>(16 * n + g + 8 * f, 2 * own * SHARE + j) + 2 * t) = x[k];
         }
   };
   if (shares) {
@@ -626,171 +715,117 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
           const int r = 16 * own * SHARE + 8 * j + t + (e & 1), c = 16 * (tile0 + n) + g + 8 * (e >> 1);
           S[n][j][e] = in && r < p.d && c < p.d ? in[static_cast<int64_t>(r) * p.d + c] : 0.0f;
         }
-    publish(0);
+    publish();
   }
-
   for (int i = 0; i < count; ++i) {
-    const auto* m = marks(i);
-    wait_older();
-    const uint32_t state = base + W::kState + (i & 1) * kChain * W::kStatePlane;
-    if (chain) {
-      const float2 after[2] = {*reinterpret_cast<const float2*>(m->after + 16 * own + t),
-                               *reinterpret_cast<const float2*>(m->after + 16 * own + 8 + t)};
-      const float total = m->total;
-      const int any = m->any;
-      __syncthreads();   // the state's planes are there; the outputs of the chunk before are read
-      // W^T = U^T - S^T K^^T, this warp's 16 tokens
-      ChainSum<2> acc[MT];
-#pragma unroll
-      for (int n = 0; n < MT; ++n) acc[n].clear();
-#pragma unroll
-      for (int ks = 0; ks < SIDES; ++ks) {
-        uint32_t x[kChain][1][4];
-#pragma unroll
-        for (int k = 0; k < kChain; ++k) load_block(x[k][0], st + W::kKeys, ks * kChain + k, lane);
-#pragma unroll
-        for (int n = 0; n < MT; ++n) {
-          uint32_t s[kChain][4];
-#pragma unroll
-          for (int k = 0; k < kChain; ++k) a_rows<DK>(s[k], state + k * W::kStatePlane, 16 * n, 16 * ks, lane);
-          acc[n].add(s, x);
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < MT; ++n) {
-        float w[2][4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float4 u = *reinterpret_cast<const float4*>(st + W::kU + (2 * n + j) * kBlock + 16 * lane);
-          w[j][0] = u.x - acc[n].get(j, 0); w[j][1] = u.y - acc[n].get(j, 1);
-          w[j][2] = u.z - acc[n].get(j, 2); w[j][3] = u.w - acc[n].get(j, 3);
-          if (KEEP && 16 * (tile0 + n) < p.d)
-            *reinterpret_cast<float4*>(p.im.w + ((bh * p.chunks + i) * SIDES + tile0 + n) * L::kTokens + (2 * own + j) * kBlock + 16 * lane) =
-                make_float4(w[j][0], w[j][1], w[j][2], w[j][3]);
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const int to = unit_at<C>(16 * n + g + 8 * f, 2 * own + j) + 2 * t;
-            if (!KEEP) {
-              uint32_t x[L::kOwn];
-              split<L::kOwn>(w[j][2 * f], w[j][2 * f + 1], x);
-#pragma unroll
-              for (int k = 0; k < L::kOwn; ++k) *reinterpret_cast<uint32_t*>(smem + W::kW + k * W::kTokenPlane + to) = x[k];
-            }
-            uint32_t x[kChain];
-            split<kChain>(w[j][2 * f] * after[j].x, w[j][2 * f + 1] * after[j].y, x);
-#pragma unroll
-            for (int k = 0; k < kChain; ++k) *reinterpret_cast<uint32_t*>(smem + W::kAfter + k * W::kTokenPlane + to) = x[k];
-          }
-        }
-      }
-      load_first(i + 1);
-      __syncthreads();   // W's planes are there
-      wait_older();
-      if (shares) {
-        // S^T <- e^B S^T + (e^{B-b} W)^T K.  The chunk's sum is formed apart and added once, rounded to nearest: a long
-        // sequence must not gather the tensor core's truncation.
-        ChainSum<2 * SHARE> sum[MT];
-#pragma unroll
-        for (int n = 0; n < MT; ++n) sum[n].clear();
-#pragma unroll
-        for (int ks = 0; ks < TILES; ++ks) {
-          uint32_t x[L::kIn][SHARE][4];
-#pragma unroll
-          for (int k = 0; k < L::kIn; ++k)
-#pragma unroll
-            for (int j = 0; j < SHARE; ++j) load_block(x[k][j], st + W::kAdd, (j * TILES + ks) * L::kIn + k, lane);
-#pragma unroll
-          for (int n = 0; n < MT; ++n) {
-            uint32_t w[kChain][4];
-#pragma unroll
-            for (int k = 0; k < kChain; ++k) a_rows<C>(w[k], base + W::kAfter + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
-            sum[n].add(w, x);
-          }
-        }
+    const char* stage = smem + W::kRing + i % STAGES * W::kStage;
+    const char* st = stage + own * W::kPair;
+    const auto* m = marks_at(stage);
+    sync();   // the chunk's operands and the state's planes are there; W's planes of the chunk before are read
+    float w[MT][2][4];
+    {
+      // W^T = U^T - S^T K^^T, this warp's 16 tokens; the next step's operands are asked for in front of a step's products
+      ChainSum<MT, 2> acc;
+      acc.clear();
+      uint32_t x[2][kChain][1][4], s[2][MT][kChain][4];
+      auto fetch = [&](int ks) {
 #pragma unroll
         for (int n = 0; n < MT; ++n)
 #pragma unroll
-          for (int j = 0; j < 2 * SHARE; ++j) {
-            if (KEEP && 16 * (tile0 + n) < p.d)
-              *reinterpret_cast<float4*>(p.im.s + ((bh * p.chunks + i) * SIDES + tile0 + n) * L::kState + (2 * own * SHARE + j) * kBlock +
-                                         16 * lane) = make_float4(S[n][j][0], S[n][j][1], S[n][j][2], S[n][j][3]);
+          for (int k = 0; k < kChain; ++k) a_rows<DK>(s[ks & 1][n][k], state + k * W::kStatePlane, 16 * n, 16 * ks, lane);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[n][j][e] = fmaf(total, S[n][j][e], sum[n].get(j, e));
-          }
-        if (any) {
-#pragma unroll
-          for (int n = 0; n < MT; ++n)
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              const int c = 16 * (tile0 + n) + g + 8 * f;
-              if (c < p.d && m->first[c] < C)
-#pragma unroll
-                for (int j = 0; j < 2 * SHARE; ++j) S[n][j][2 * f] = S[n][j][2 * f + 1] = nan_value();
-            }
-        }
-        publish(i + 1);
-      }
-      load_second(i + 1);
-    } else {
-      // O = scale e^b Q S + scores W, this warp's 16 tokens
-      const float in[2] = {p.scale * m->inside[16 * own + g], p.scale * m->inside[16 * own + g + 8]};
-      const int any = m->any;
-      __syncthreads();
-      Accumulators<2 * MT, L::kApart> o;
-      o.clear();
+        for (int k = 0; k < kChain; ++k) load_block(x[ks & 1][k][0], st, ks * kChain + k, lane);
+      };
+      fetch(0);
 #pragma unroll
       for (int ks = 0; ks < SIDES; ++ks) {
-        uint32_t q[L::kIn][4], x[L::kOwn][MT][4];
-#pragma unroll
-        for (int k = 0; k < L::kIn; ++k) load_block(q[k], st + W::kQ, ks * L::kIn + k, lane);
-#pragma unroll
-        for (int k = 0; k < L::kOwn; ++k)
-#pragma unroll
-          for (int n = 0; n < MT; ++n) b_rows<DK>(x[k][n], state + k * W::kStatePlane, 16 * n, 16 * ks, lane);
-        mma_terms(o, 0, q, x);
+        if (ks + 1 < SIDES) fetch(ks + 1);
+        acc.add(s[ks & 1], x[ks & 1], ks & 1);
       }
 #pragma unroll
-      for (int n = 0; n < 2 * MT; ++n)
+      for (int n = 0; n < MT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          o.main[n][e] = o.get(n, e) * in[e >> 1];
-          if (L::kApart) o.small[L::kApart ? n : 0][e] = 0.0f;
+        for (int j = 0; j < 2; ++j) {
+          const float4 u = *reinterpret_cast<const float4*>(st + W::kU + (2 * n + j) * kBlock + 16 * lane);
+          w[n][j][0] = u.x - acc.get(n, j, 0); w[n][j][1] = u.y - acc.get(n, j, 1);
+          w[n][j][2] = u.z - acc.get(n, j, 2); w[n][j][3] = u.w - acc.get(n, j, 3);
         }
-      load_first(i + 1);
-      __syncthreads();
-      wait_older();
+    }
+    const float2 after[2] = {*reinterpret_cast<const float2*>(m->after + 16 * own + t), *reinterpret_cast<const float2*>(m->after + 16 * own + 8 + t)};
+    const float total = m->total;
+#pragma unroll
+    for (int n = 0; n < MT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int to = unit_at<C>(16 * n + g + 8 * f, 2 * own + j) + 2 * t;
+          if (!KEEP) {
+            uint32_t x[L::kOwn];
+            split<L::kOwn>(w[n][j][2 * f], w[n][j][2 * f + 1], x);
+#pragma unroll
+            for (int k = 0; k < L::kOwn; ++k) *reinterpret_cast<uint32_t*>(smem + W::kW + k * W::kTokenPlane + to) = x[k];
+          }
+          uint32_t x[kChain];
+          split<kChain>(w[n][j][2 * f] * after[j].x, w[n][j][2 * f + 1] * after[j].y, x);
+#pragma unroll
+          for (int k = 0; k < kChain; ++k) *reinterpret_cast<uint32_t*>(smem + W::kAfter + k * W::kTokenPlane + to) = x[k];
+        }
+    sync();   // W's planes are there, the state's are read
+    if (KEEP)
+#pragma unroll
+      for (int n = 0; n < MT; ++n)
+        if (16 * (tile0 + n) < p.d) {
+          float4* to = reinterpret_cast<float4*>(p.im.w + ((bh * p.chunks + i) * SIDES + tile0 + n) * L::kTokens + 2 * own * kBlock) + lane;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) to[32 * j] = make_float4(w[n][j][0], w[n][j][1], w[n][j][2], w[n][j][3]);
+        }
+    if (!shares) continue;
+    // S^T <- e^B S^T + (e^{B-b} W)^T K.  The chunk's sum is formed apart and added once, rounded to nearest: a long
+    // sequence must not gather the tensor core's truncation.
+    ChainSum<MT, 2 * SHARE> sum;
+    sum.clear();
+    {
+      uint32_t x[2][L::kIn][SHARE][4], v[2][MT][kChain][4];
+      auto fetch = [&](int ks) {
+#pragma unroll
+        for (int n = 0; n < MT; ++n)
+#pragma unroll
+          for (int k = 0; k < kChain; ++k) a_rows<C>(v[ks & 1][n][k], base + W::kAfter + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
+#pragma unroll
+        for (int k = 0; k < L::kIn; ++k)
+#pragma unroll
+          for (int j = 0; j < SHARE; ++j) load_block(x[ks & 1][k][j], st + W::kAdd, (j * TILES + ks) * L::kIn + k, lane);
+      };
+      fetch(0);
 #pragma unroll
       for (int ks = 0; ks < TILES; ++ks) {
-        if (ks > own) continue;
-        uint32_t q[L::kScore][4], x[L::kOwn][MT][4];
-#pragma unroll
-        for (int k = 0; k < L::kScore; ++k) load_block(q[k], st + W::kScores, ks * L::kScore + k, lane);
-#pragma unroll
-        for (int k = 0; k < L::kOwn; ++k)
-#pragma unroll
-          for (int n = 0; n < MT; ++n) b_rows<C>(x[k][n], base + W::kW + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
-        mma_terms(o, 0, q, x);
-      }
-      load_second(i + 1);
-      const int64_t t0 = static_cast<int64_t>(i) * C;
-      T* out = static_cast<T*>(a.out.data) + b * a.out.sb + h * a.out.sh;
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const int r = 16 * own + g + 8 * f;
-        if (t0 + r >= p.N) continue;
-#pragma unroll
-        for (int n = 0; n < 2 * MT; ++n) {
-          const int c = 16 * tile0 + 8 * n + t;
-          if (c >= p.d) continue;
-          float y[2] = {o.get(n, 2 * f), o.get(n, 2 * f + 1)};
-          if (any)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (r >= m->first[c + e]) y[e] = nan_value();
-          store_pair<T>(out + (t0 + r) * a.out.sn + c, y[0], y[1], a.out_pairs, c + 1 < p.d);
-        }
+        if (ks + 1 < TILES) fetch(ks + 1);
+        sum.add(v[ks & 1], x[ks & 1], ks & 1);
       }
     }
+#pragma unroll
+    for (int n = 0; n < MT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2 * SHARE; ++j) {
+        if (KEEP && 16 * (tile0 + n) < p.d)
+          *reinterpret_cast<float4*>(p.im.s + ((bh * p.chunks + i) * SIDES + tile0 + n) * L::kState + (2 * own * SHARE + j) * kBlock + 16 * lane) =
+              make_float4(S[n][j][0], S[n][j][1], S[n][j][2], S[n][j][3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[n][j][e] = fmaf(total, S[n][j][e], sum.get(n, j, e));
+      }
+    if (m->any) {
+#pragma unroll
+      for (int n = 0; n < MT; ++n)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int c = 16 * (tile0 + n) + g + 8 * f;
+          if (c < p.d && first_of(i)[c] < C)
+#pragma unroll
+            for (int j = 0; j < 2 * SHARE; ++j) S[n][j][2 * f] = S[n][j][2 * f + 1] = nan_value();
+        }
+    }
+    publish();
   }
   if (shares && a.last) {
     float* last = a.last + bh * p.d * p.d;
@@ -835,7 +870,8 @@ int scan_as(const ScanArgs& a, int64_t BH, cudaStream_t s) {
 
 template <typename T, int DK>
 int scan_for(const ScanArgs& a, int64_t BH, bool keep, cudaStream_t s) {
-  if (two_tiles(BH, a.c.d)) return keep ? scan_as<T, DK, 2, true>(a, BH, s) : scan_as<T, DK, 2, false>(a, BH, s);
+  if constexpr (DK <= 64)
+    if (two_tiles(BH, a.c.d)) return keep ? scan_as<T, DK, 2, true>(a, BH, s) : scan_as<T, DK, 2, false>(a, BH, s);
   return keep ? scan_as<T, DK, 1, true>(a, BH, s) : scan_as<T, DK, 1, false>(a, BH, s);
 }
 
@@ -910,7 +946,7 @@ int64_t delta_chunks(const DeltaProblem& p) {
 
 namespace delta {
 
-bool two_tiles(int64_t BH, int d) { return BH * ((d + 15) / 16) > 2 * kSms; }
+bool two_tiles(int64_t BH, int d) { return BH * ((d + 15) / 16) > kSms; }
 
 int launch_prepare(const Common& c, int64_t BH, int dtype, bool grad, cudaStream_t s) {
   return dtype == MHLA_BF16 ? prepare_type<__nv_bfloat16>(c, BH, grad, s) : prepare_type<float>(c, BH, grad, s);
@@ -1076,5 +1112,9 @@ int launch_delta_step(const DeltaProblem& p, float* state, const Operand& out, v
   if (p.dtype == MHLA_BF16) return vec ? step_as<__nv_bfloat16, 4>(p, state, out, s) : step_as<__nv_bfloat16, 1>(p, state, out, s);
   return vec ? step_as<float, 4>(p, state, out, s) : step_as<float, 1>(p, state, out, s);
 }
+
+int read_and_clear_delta_error(void* stream, uint32_t* flags) { return tc::read_and_clear_word(g_delta_error, stream, flags); }
+
+MHLA_DEFINE_STALL_SETTER(set_stall_delta)
 
 }  // namespace mhla

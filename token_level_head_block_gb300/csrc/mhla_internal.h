@@ -188,6 +188,8 @@ int set_stall_causal(uint32_t warp_plus_1, uint64_t ns);
 int set_stall_module(uint32_t warp_plus_1, uint64_t ns);
 int set_stall_gemm(uint32_t warp_plus_1, uint64_t ns);
 int set_stall_linear(uint32_t warp_plus_1, uint64_t ns);
+int set_stall_delta(uint32_t warp_plus_1, uint64_t ns);
+int set_stall_delta_back(uint32_t warp_plus_1, uint64_t ns);
 int set_stall_gated(uint32_t warp_plus_1, uint64_t ns);
 
 // Brackets one kernel launch with CUDA events on its stream while
@@ -297,6 +299,8 @@ int launch_delta_forward(const DeltaProblem& p, const float* state_in, const Ope
                          void* stream);
 int launch_delta_backward(const DeltaProblem& p, const DeltaBackward& b, void* workspace, void* stream);
 int launch_delta_step(const DeltaProblem& p, float* state, const Operand& out, void* stream);
+int read_and_clear_delta_error(void* stream, uint32_t* flags);
+int read_and_clear_delta_back_error(void* stream, uint32_t* flags);
 
 // Norm and rotation of query and key heads (qk_norm_kernels.cu).
 struct QkNormProblem {
