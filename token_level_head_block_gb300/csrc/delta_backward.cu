@@ -44,10 +44,11 @@ struct BackLay {
   static constexpr int kShare = DK / 16 < kWarps ? 1 : DK / 16 / kWarps;   // blocks of the state's rows a warp
   static constexpr int kHand = MT * (2 + 2 * kShare) * kBlock;           // a warp's part of P^T do and Q^T do
   static constexpr int kStatePlane = 16 * MT * DK * 2, kTokenPlane = 16 * MT * L::C * 2;
-  static constexpr int kState = 0, kW = kState + kChain * kStatePlane, kHands = kW + kChain * kTokenPlane;
+  static constexpr int kState = 0, kW = kState + 2 * kStatePlane, kStateScale = kW + 2 * kTokenPlane;
+  static constexpr int kTokenScale = kStateScale + 16 * MT * L::kSides * 4, kHands = (kTokenScale + 16 * MT * L::kTiles * 4 + 127) / 128 * 128;
   static constexpr int kRing = kHands + 2 * kWarps * kHand;
   // of a chunk, the chain's: blocks of K, of K^
-  static constexpr int kKBytes = L::kSides * L::kIn * kBlock, kKeysBytes = kShare * L::kTiles * kChain * kBlock;
+  static constexpr int kKBytes = L::kSides * L::kHalves * kBlock, kKeysBytes = kShare * L::kTiles * 2 * kBlock;
   static constexpr int kKeys = kKBytes, kPair = kKeys + kKeysBytes;
   static constexpr int kMarkFrom = offsetof(M, after), kMarkBytes = offsetof(M, first) - kMarkFrom;
   static constexpr int kMarks = kWarps * kPair, kStage = kMarks + (kMarkBytes + 127) / 128 * 128;
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
       char* to = stage + own * W::kPair;
       uint64_t* on = bar + (i & 1);
       ptx::mbar_arrive_expect_tx(on, W::kKBytes + (shares ? W::kKeysBytes : 0) + (own == 0 ? W::kMarkBytes : 0));
-      ptx::bulk_load_plain(to, p.im.k_rows + key_chunk_of(i) * L::kInput + own * W::kKBytes, W::kKBytes, on);
+      ptx::bulk_load_plain(to, p.im.k_rows + key_chunk_of(i) * L::kInputHalf + own * W::kKBytes, W::kKBytes, on);
       if (shares) ptx::bulk_load_plain(to + W::kKeys, p.im.keys_add + chunk_of(i) * L::kKeys + own * W::kKeysBytes, W::kKeysBytes, on);
       if (own == 0) ptx::bulk_load_plain(stage + W::kMarks, p.im.marks + chunk_of(i) * L::kMarks + W::kMarkFrom, W::kMarkBytes, on);
     };
@@ -194,14 +195,21 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
 #pragma unroll
     for (int n = 0; n < MT; ++n)
 #pragma unroll
-      for (int j = 0; j < 2 * SHARE; ++j)
+      for (int j = 0; j < SHARE; ++j)
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          uint32_t x[kChain];
-          split<kChain>(D[n][j][2 * f], D[n][j][2 * f + 1], x);
+          const float x[4] = {D[n][2 * j][2 * f], D[n][2 * j][2 * f + 1], D[n][2 * j + 1][2 * f], D[n][2 * j + 1][2 * f + 1]};
+          const Scale by = scale_of(over_row(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])))));
+          const int row = 16 * n + g + 8 * f;
 #pragma unroll
-          for (int k = 0; k < kChain; ++k)
-            *reinterpret_cast<uint32_t*>(smem + W::kState + k * W::kStatePlane + unit_at<DK>(16 * n + g + 8 * f, 2 * own * SHARE + j) + 2 * t) = x[k];
+          for (int e = 0; e < 2; ++e) {
+            uint32_t h[2];
+            halves<2>(x[2 * e] * by.to, x[2 * e + 1] * by.to, h);
+            char* to = smem + W::kState + unit_at<DK>(row, 2 * (own * SHARE + j) + e) + 2 * t;
+            *reinterpret_cast<uint32_t*>(to) = h[0];
+            *reinterpret_cast<uint32_t*>(to + W::kStatePlane) = h[1];
+          }
+          if ((lane & 3) == 0) reinterpret_cast<float*>(smem + W::kStateScale)[row * SIDES + own * SHARE + j] = by.from;
         }
   };
   if (shares) {
@@ -226,45 +234,64 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
     float w[MT][2][4];
     {
       // dW^T = (P^T do)^T + D^T (e^{B-b} K)^T
-      ChainSum<MT, 2> acc;
-      acc.clear();
-      uint32_t x[2][L::kIn][1][4], s[2][MT][kChain][4];
+      float acc[MT][2][4] = {};
+      uint32_t x[2][L::kHalves][4], s[2][MT][2][4];
       auto fetch = [&](int ks) {
 #pragma unroll
         for (int n = 0; n < MT; ++n)
 #pragma unroll
-          for (int k = 0; k < kChain; ++k) a_rows<DK>(s[ks & 1][n][k], base + W::kState + k * W::kStatePlane, 16 * n, 16 * ks, lane);
+          for (int k = 0; k < 2; ++k) a_rows<DK>(s[ks & 1][n][k], base + W::kState + k * W::kStatePlane, 16 * n, 16 * ks, lane);
 #pragma unroll
-        for (int k = 0; k < L::kIn; ++k) load_block(x[ks & 1][k][0], st, ks * L::kIn + k, lane);
+        for (int k = 0; k < L::kHalves; ++k) load_block(x[ks & 1][k], st, ks * L::kHalves + k, lane);
       };
       fetch(0);
 #pragma unroll
       for (int ks = 0; ks < SIDES; ++ks) {
         if (ks + 1 < SIDES) fetch(ks + 1);
-        acc.add(s[ks & 1], x[ks & 1], ks & 1);
+#pragma unroll
+        for (int n = 0; n < MT; ++n) {
+          const float* scale = reinterpret_cast<const float*>(smem + W::kStateScale) + (16 * n + g) * SIDES + ks;
+          const float s0 = scale[0], s1 = scale[8 * SIDES];
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            float c[4];
+            products(c, s[ks & 1][n], x[ks & 1], f);
+            acc[n][f][0] = fmaf(c[0], s0, acc[n][f][0]); acc[n][f][1] = fmaf(c[1], s0, acc[n][f][1]);
+            acc[n][f][2] = fmaf(c[2], s1, acc[n][f][2]); acc[n][f][3] = fmaf(c[3], s1, acc[n][f][3]);
+          }
+        }
       }
+      const float of_key = m->key;
       const float2 after[2] = {*reinterpret_cast<const float2*>(m->after + 16 * own + t), *reinterpret_cast<const float2*>(m->after + 16 * own + 8 + t)};
 #pragma unroll
       for (int n = 0; n < MT; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float4 y = hand[32 * (n * (2 + 2 * SHARE) + j)];
-          w[n][j][0] = fmaf(after[j].x, acc.get(n, j, 0), y.x); w[n][j][1] = fmaf(after[j].y, acc.get(n, j, 1), y.y);
-          w[n][j][2] = fmaf(after[j].x, acc.get(n, j, 2), y.z); w[n][j][3] = fmaf(after[j].y, acc.get(n, j, 3), y.w);
+          const float f0 = after[j].x * of_key, f1 = after[j].y * of_key;
+          w[n][j][0] = fmaf(f0, acc[n][j][0], y.x); w[n][j][1] = fmaf(f1, acc[n][j][1], y.y);
+          w[n][j][2] = fmaf(f0, acc[n][j][2], y.z); w[n][j][3] = fmaf(f1, acc[n][j][3], y.w);
         }
     }
 #pragma unroll
     for (int n = 0; n < MT; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int f = 0; f < 2; ++f) {
+        float most = 0.0f;
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          uint32_t x[kChain];
-          split<kChain>(w[n][j][2 * f], w[n][j][2 * f + 1], x);
+        for (int e = 0; e < 4; ++e) most = fmaxf(most, fabsf(w[n][e >> 1][2 * f + (e & 1)]));
+        const Scale by = scale_of(over_row(most));
+        const int row = 16 * n + g + 8 * f;
 #pragma unroll
-          for (int k = 0; k < kChain; ++k)
-            *reinterpret_cast<uint32_t*>(smem + W::kW + k * W::kTokenPlane + unit_at<C>(16 * n + g + 8 * f, 2 * own + j) + 2 * t) = x[k];
+        for (int j = 0; j < 2; ++j) {
+          uint32_t h[2];
+          halves<2>(w[n][j][2 * f] * by.to, w[n][j][2 * f + 1] * by.to, h);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<uint32_t*>(smem + W::kW + k * W::kTokenPlane + unit_at<C>(row, 2 * own + j) + 2 * t) = h[k];
         }
+        if ((lane & 3) == 0) reinterpret_cast<float*>(smem + W::kTokenScale)[row * TILES + own] = by.from;
+      }
     const float total = m->total;
     sync();   // the planes of dW are there, those of D are read
 #pragma unroll
@@ -276,25 +303,36 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
       }
     if (!shares) continue;
     // D^T <- e^B D^T + (Q^T do)^T - dW^T K^, the chunk's part formed apart
-    ChainSum<MT, 2 * SHARE> sum;
-    sum.clear();
+    float sum[MT][2 * SHARE][4] = {};
     {
-      uint32_t x[2][kChain][SHARE][4], v[2][MT][kChain][4];
+      uint32_t x[2][SHARE][2][4], v[2][MT][2][4];
       auto fetch = [&](int ks) {
 #pragma unroll
         for (int n = 0; n < MT; ++n)
 #pragma unroll
-          for (int k = 0; k < kChain; ++k) a_rows<C>(v[ks & 1][n][k], base + W::kW + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
+          for (int k = 0; k < 2; ++k) a_rows<C>(v[ks & 1][n][k], base + W::kW + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
 #pragma unroll
-        for (int k = 0; k < kChain; ++k)
+        for (int j = 0; j < SHARE; ++j)
 #pragma unroll
-          for (int j = 0; j < SHARE; ++j) load_block(x[ks & 1][k][j], st + W::kKeys, (j * TILES + ks) * kChain + k, lane);
+          for (int k = 0; k < 2; ++k) load_block(x[ks & 1][j][k], st + W::kKeys, (j * TILES + ks) * 2 + k, lane);
       };
       fetch(0);
 #pragma unroll
       for (int ks = 0; ks < TILES; ++ks) {
         if (ks + 1 < TILES) fetch(ks + 1);
-        sum.add(v[ks & 1], x[ks & 1], ks & 1);
+        const float of_keys = m->keys[ks];
+#pragma unroll
+        for (int n = 0; n < MT; ++n) {
+          const float* scale = reinterpret_cast<const float*>(smem + W::kTokenScale) + (16 * n + g) * TILES + ks;
+          const float s0 = scale[0] * of_keys, s1 = scale[8 * TILES] * of_keys;
+#pragma unroll
+          for (int j = 0; j < 2 * SHARE; ++j) {
+            float c[4];
+            products(c, v[ks & 1][n], x[ks & 1][j >> 1], j & 1);
+            sum[n][j][0] = fmaf(c[0], s0, sum[n][j][0]); sum[n][j][1] = fmaf(c[1], s0, sum[n][j][1]);
+            sum[n][j][2] = fmaf(c[2], s1, sum[n][j][2]); sum[n][j][3] = fmaf(c[3], s1, sum[n][j][3]);
+          }
+        }
       }
     }
 #pragma unroll
@@ -307,7 +345,7 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
         const float4 x = hand[32 * (n * (2 + 2 * SHARE) + 2 + j)];
         const float xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) D[n][j][e] = fmaf(total, D[n][j][e], xs[e] - sum.get(n, j, e));
+        for (int e = 0; e < 4; ++e) D[n][j][e] = fmaf(total, D[n][j][e], xs[e] - sum[n][j][e]);
       }
     publish();
   }

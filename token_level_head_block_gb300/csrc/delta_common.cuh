@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -18,31 +19,42 @@ namespace delta {
 
 using namespace gated;
 
-// Terms of bf16 that a value enters the tensor cores with: an input; a value that reaches the float32 state (kChain,
-// 2^-24); a value that reaches outputs alone (kOwn: two leave 2^-16 with bf16 outputs); and a score of the forward pass, whose one
-// rounding (2^-8) stays beside that of bf16 outputs.
+// How values enter the tensor cores.
+//
+// The chain, from chunk to chunk, takes fp16 at a scale: a block's largest value is brought to [1, 2) by a power of two, and
+// a value is then one fp16 (2^-11 of it, or 2^-25 of the largest), or two (2^-22, 2^-25).  What reaches the float32 state
+// (the state, w, K^) takes two; bf16 inputs are exact in one but for that 2^-25; what only feeds bf16 outputs takes one.  Three products
+// of two such terms stand for six of three bf16 ones, and the chain's time is its products.  A scale belongs to 16 columns of
+// a row of the state or of w, to 16 rows of K^, to a row of Q or the scores, to a chunk of K.
+//
+// Elsewhere values are sums of bf16 terms, which need no scale: an input one (bf16) or three (float32), a value that reaches the
+// state three (2^-24), one that reaches outputs alone kOwn: two leave 2^-16 beside bf16 outputs.
 // Tokens a chunk: three planes of float32 rows of 128 channels leave room for 32.
 template <typename T>
 struct Form;
 template <>
 struct Form<__nv_bfloat16> {
-  static constexpr int kIn = 1, kOwn = 2, kScore = 1, kChunk = 64;
+  static constexpr int kIn = 1, kOwn = 2, kHalves = 1, kChunk = 64;
 };
 template <>
 struct Form<float> {
-  static constexpr int kIn = 3, kOwn = 3, kScore = 3, kChunk = 32;
+  static constexpr int kIn = 3, kOwn = 3, kHalves = 2, kChunk = 32;
 };
-constexpr int kChain = 3;
+constexpr int kChain = 3;   // bf16 terms on the way to the state
 
 // A chunk's values a token, then whether any is not finite and each column's first such token.
 template <int C, int DK>
 struct Marks {
   float hi[C], lo[C];      // sum b of the log decays up to the token, in powers of two
   float inside[C];         // e^b
+  float query[C];          // scale e^b and the scale of Q's row
+  float score[C];          // the scale of the scores' row
   float after[C];          // e^(B - b), B that of the whole chunk
   float beta[C];
+  float keys[4];           // the scale of each 16 rows of K^
   float total;             // e^B
-  int32_t any, pad[2];
+  float key;               // the scale of K
+  int32_t any, pad;
   int32_t first[DK];
 };
 
@@ -52,12 +64,12 @@ constexpr int kBlock = 512;
 
 template <typename T, int DK>
 struct Lay {
-  static constexpr int C = Form<T>::kChunk, kIn = Form<T>::kIn, kOwn = Form<T>::kOwn, kScore = Form<T>::kScore;
+  static constexpr int C = Form<T>::kChunk, kIn = Form<T>::kIn, kOwn = Form<T>::kOwn, kHalves = Form<T>::kHalves;
   static constexpr int kTiles = C / 16, kSides = DK / 16;          // blocks of a chunk's tokens, of the channels
   static constexpr bool kApart = kIn > 1;
   static constexpr int kRows = C * DK * 2, kSquare = C * C * 2;   // bytes of a plane
-  static constexpr int kInput = kIn * kRows, kKeys = kChain * kRows, kInverse = kOwn * kSquare;
-  static constexpr int kScores = kScore * kSquare, kScoresBack = kChain * kSquare;
+  static constexpr int kInput = kIn * kRows, kInputHalf = kHalves * kRows, kKeys = 2 * kRows, kInverse = kOwn * kSquare;
+  static constexpr int kScores = kHalves * kSquare, kScoresBack = kChain * kSquare;
   static constexpr int kTokens = C / 8 * kBlock, kState = DK / 8 * kBlock;   // of 16 columns, float32 fragments
   using M = Marks<C, DK>;
   static constexpr int kMarks = sizeof(M);
@@ -65,7 +77,8 @@ struct Lay {
 };
 
 // Where a call's images lie, of every chunk [B][Hk][chunks] (inputs of key heads) or [B][H][chunks].  Blocks of an operand with
-// its terms side by side; k runs fastest, after the terms.  tok: blocks of tokens, ch: of channels.
+// its terms side by side; k runs fastest, after the terms.  tok: blocks of tokens, ch: of channels; fp16 but for q_add,
+// scores_back and dout_cols.
 struct Images {
   char* k_add;          // K as [k = tok][n = ch], blocks [ch][tok]
   char* q_rows;         // Q as [m = tok][k = ch], blocks [tok][ch]
@@ -95,50 +108,48 @@ struct Common {
 };
 enum : uint32_t { kWideQ = 1, kWideK = 2, kWideV = 4, kWideDout = 8 };
 
-// MT x NT tiles of sums of products of terms.  Products of one size have accumulators of their own, the smallest two sets in
-// turn, and follow one another in an order that keeps two additions to one accumulator four MMAs apart: one warp's chain
-// of them is as long as it takes to issue.  Many tiles are apart enough with two sets.
-template <int MT, int NT>
-struct ChainSum {
-  static constexpr int kParts = MT * NT <= 4 ? 4 : 2;
-  float part[kParts][MT][NT][4];
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int s = 0; s < kParts; ++s)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) part[s][m][n][e] = 0.0f;
-  }
-  __device__ __forceinline__ float get(int m, int n, int e) const {
-    if (kParts == 4) return part[0][m][n][e] + (part[1][m][n][e] + (part[kParts - 2][m][n][e] + part[kParts - 1][m][n][e]));
-    return part[0][m][n][e] + part[1][m][n][e];
-  }
-  template <int NB, int P>
-  __device__ __forceinline__ void one(const uint32_t (&a)[MT][kChain][4], const uint32_t (&b)[NB][P][4], int i, int j, int turn) {
-    const int s = i + j == 0 ? 0 : kParts == 2 || i + j == 1 ? 1 : 2 + turn;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) mma(part[s < kParts ? s : 0][m][2 * p + f], a[m][i], b[j][p][2 * f], b[j][p][2 * f + 1]);
-  }
-  template <int NB, int P>
-  __device__ __forceinline__ void add(const uint32_t (&a)[MT][kChain][4], const uint32_t (&b)[NB][P][4], int turn) {
-    static_assert(NB == 1 || NB == kChain, "an input, or three terms");
-    one(a, b, 2, 0, turn);
-    one(a, b, 1, 0, turn);
-    if constexpr (NB > 1) {
-      one(a, b, 1, 1, turn);
-      one(a, b, 0, 1, turn);
-      one(a, b, 0, 2, turn);
-    }
-    one(a, b, 0, 0, turn);
-  }
+// fp16 at a scale: the power of two that brings `most` to [1, 2), and what undoes it.
+struct Scale {
+  float to, from;
 };
+__device__ __forceinline__ Scale scale_of(float most) {
+  const uint32_t e = min(max(__float_as_uint(most) >> 23, 1u), 253u);
+  return Scale{__uint_as_float((254u - e) << 23), __uint_as_float(e << 23)};
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+// A pair as one fp16 each or the sum of two.
+template <int NT>
+__device__ __forceinline__ void halves(float x, float y, uint32_t (&t)[NT]) {
+  t[0] = pack_half(x, y);
+  if constexpr (NT > 1) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&t[0]));
+    t[1] = pack_half(x - f.x, y - f.y);
+  }
+}
+// c = sum over the pairs of terms that matter, small ones first; each tile begins anew.
+template <int NA, int NB>
+__device__ __forceinline__ void products(float (&c)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4], int half) {
+  constexpr bool kMixed = NA > 1 || NB > 1;
+  if constexpr (NA > 1) mma_half_first(c, a[1], b[0][2 * half], b[0][2 * half + 1]);
+  if constexpr (NB > 1) {
+    if constexpr (NA > 1)
+      mma_half(c, a[0], b[1][2 * half], b[1][2 * half + 1]);
+    else
+      mma_half_first(c, a[0], b[1][2 * half], b[1][2 * half + 1]);
+  }
+  if constexpr (kMixed)
+    mma_half(c, a[0], b[0][2 * half], b[0][2 * half + 1]);
+  else
+    mma_half_first(c, a[0], b[0][2 * half], b[0][2 * half + 1]);
+}
+// The largest size among the four lanes of a row.
+__device__ __forceinline__ float over_row(float m) {
+  m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
+  return fmaxf(m, __shfl_xor_sync(~0u, m, 2));
+}
 
 struct ScanArgs {
   Common c;

@@ -35,13 +35,19 @@ namespace {
 // Rows of one operand to planes of terms; zeros behind the last token and channel.
 // WATCH 1: the first row with a value that is not finite to `first`; 2: each column's; such values are left as zeros.
 template <typename T, int DK, int THREADS, int WATCH>
-__device__ __forceinline__ void load_rows(char* dst, const T* src, int64_t sn, int rows, int d, bool wide, int32_t* first) {
+__device__ __forceinline__ void load_rows(char* dst, const T* src, int64_t sn, int rows, int d, bool wide, int32_t* first,
+                                          uint32_t* most = nullptr) {
+  float largest = 0.0f;
   using L = Lay<T, DK>;
   constexpr int C = L::C;
   auto watch = [&](float x, int r, int c) {
-    if (WATCH == 0 || finite(x)) return x;
-    atomicMin(first + (WATCH == 2 ? c : 0), r);
-    return 0.0f;
+    if (WATCH == 0) return x;
+    if (!finite(x)) {
+      atomicMin(first + (WATCH == 2 ? c : 0), r);
+      return 0.0f;
+    }
+    if (WATCH == 1) largest = fmaxf(largest, fabsf(x));
+    return x;
   };
   if (wide) {
     constexpr int E = 16 / sizeof(T), kUnits = C * DK / E, kEach = kUnits / THREADS;
@@ -64,7 +70,7 @@ __device__ __forceinline__ void load_rows(char* dst, const T* src, int64_t sn, i
             const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), __floats2bfloat162_rn(0.0f, 0.0f));
             bad |= *reinterpret_cast<const uint32_t*>(&z);
           }
-          if (bad & 0x7FFF7FFFu)
+          if (WATCH == 1 || (bad & 0x7FFF7FFFu))
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = pack(watch(low(w[e]), r, c + 2 * e), watch(high(w[e]), r, c + 2 * e + 1));
         }
@@ -92,6 +98,22 @@ __device__ __forceinline__ void load_rows(char* dst, const T* src, int64_t sn, i
         *reinterpret_cast<uint32_t*>(dst + n * L::kRows + unit_at<DK>(r, c >> 3) + (c & 7) * 2) = t[n];
     }
   }
+  if (WATCH == 1) {
+    const uint32_t all = __reduce_max_sync(~0u, __float_as_uint(largest));
+    if ((threadIdx.x & 31) == 0) atomicMax(most, all);
+  }
+}
+
+// A pair of values that planes of bf16 terms hold, scaled, as fp16.
+template <int NI, int NH>
+__device__ __forceinline__ void to_halves(const uint32_t (&x)[NI][4], int e, float by, uint32_t (&t)[NH]) {
+  float a = low(x[NI - 1][e]), b = high(x[NI - 1][e]);
+#pragma unroll
+  for (int n = NI - 2; n >= 0; --n) {
+    a += low(x[n][e]);
+    b += high(x[n][e]);
+  }
+  halves<NH>(a * by, b * by, t);
 }
 
 template <typename T, int DK>
@@ -99,7 +121,9 @@ struct Prepare {
   using L = Lay<T, DK>;
   static constexpr int C = L::C, kStrips = L::kTiles, kThreads = 64 * kStrips;
   static constexpr int kPitch = C + 8;   // floats a row of T: a lane's pairs of eight rows meet all banks
-  static constexpr int kK = (C * kPitch * 4 + 127) / 128 * 128, kV = kK + L::kInput, kQ = kV + L::kInput, kBytes = kQ + L::kInput;
+  static constexpr int kK = (C * kPitch * 4 + 127) / 128 * 128, kV = kK + L::kInput, kQ = kV + L::kInput;
+  // K^ on the way, float32: Q's place and what is behind it
+  static constexpr int kKeep = kQ, kBytes = kQ + std::max(L::kInput, C * DK * 4);
 };
 
 // Decays between the tokens of a chunk: D_ij = e^{b_i - b_j} = row_i col_j for j in front of i's block of 16, with
@@ -185,6 +209,7 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
   __shared__ __align__(16) typename L::M m;
   __shared__ __align__(16) Decays<C> w;
   __shared__ int32_t bad_key, bad;
+  __shared__ uint32_t most;   // |k|
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t chunk = blockIdx.x % p.chunks;
   const int64_t bh = blockIdx.x / p.chunks, b = bh / p.H, h = bh % p.H, times = p.H / p.Hk, hk = h / times;
@@ -198,7 +223,10 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
   const bool second = warp >= TILES;
 
   for (int i = threadIdx.x; i < DK; i += THREADS) m.first[i] = C;
-  if (threadIdx.x == 0) bad_key = bad = C;
+  if (threadIdx.x == 0) {
+    bad_key = bad = C;
+    most = 0;
+  }
   __syncthreads();
 
   // gates, E tokens a lane
@@ -215,7 +243,7 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
       if (!finite(g[e]) || !finite(beta[e])) atomicMin(&bad, t);
     }
   }
-  load_rows<T, DK, THREADS, 1>(smem + P::kK, from(p.k, hk), p.k.sn, rows, p.d, p.wide & kWideK, &bad_key);
+  load_rows<T, DK, THREADS, 1>(smem + P::kK, from(p.k, hk), p.k.sn, rows, p.d, p.wide & kWideK, &bad_key, &most);
   load_rows<T, DK, THREADS, 0>(smem + P::kQ, from(p.q, hk), p.q.sn, rows, p.d, p.wide & kWideQ, nullptr);
   load_rows<T, DK, THREADS, 2>(smem + P::kV, from(p.v, h), p.v.sn, rows, p.d, p.wide & kWideV, m.first);
   __syncthreads();
@@ -274,7 +302,10 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
       for (int r = 1; r < TILES; ++r)
         if (r > block) w.col[r][t] = exp2_of(edge[r], s);
     }
-    if (lane == 0) m.total = exp2_of(end, none);
+    if (lane == 0) {
+      m.total = exp2_of(end, none);
+      m.key = scale_of(__uint_as_float(most)).from;
+    }
   }
   __syncthreads();
 
@@ -288,11 +319,6 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
       uint32_t a[L::kIn][4];
 #pragma unroll
       for (int n = 0; n < L::kIn; ++n) a_rows<DK>(a[n], a_base + n * L::kRows, m0, 16 * ks, lane);
-      if (second && !GRAD && h % times == 0)
-#pragma unroll
-        for (int n = 0; n < L::kIn; ++n)
-          *reinterpret_cast<uint4*>(p.im.q_rows + at_key * L::kInput + ((strip * SIDES + ks) * L::kIn + n) * kBlock + 16 * lane) =
-              make_uint4(a[n][0], a[n][1], a[n][2], a[n][3]);
 #pragma unroll
       for (int s = 0; s < TILES; ++s) {
         if (s > strip) continue;
@@ -302,7 +328,40 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
         mma_terms(acc, 2 * s, a, x);
       }
     }
+    if (second && !GRAD) {   // Q's rows, each at its own scale
+      float most_q[2] = {0.0f, 0.0f};
+      for (int ks = 0; ks < SIDES; ++ks) {
+        uint32_t a[4];   // the first terms: the largest is within half a step of theirs
+        a_rows<DK>(a, a_base, m0, 16 * ks, lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most_q[e & 1] = fmaxf(most_q[e & 1], fmaxf(fabsf(low(a[e])), fabsf(high(a[e]))));
+      }
+      const Scale by[2] = {scale_of(over_row(most_q[0])), scale_of(over_row(most_q[1]))};
+      if ((lane & 3) == 0) {
+        m.query[row] = p.scale * m.inside[row] * by[0].from;
+        m.query[row + 8] = p.scale * m.inside[row + 8] * by[1].from;
+      }
+      if (h % times == 0)
+        for (int ks = 0; ks < SIDES; ++ks) {
+          uint32_t a[L::kIn][4], q[L::kHalves][4];
+#pragma unroll
+          for (int n = 0; n < L::kIn; ++n) a_rows<DK>(a[n], a_base + n * L::kRows, m0, 16 * ks, lane);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t t[L::kHalves];
+            to_halves<L::kIn, L::kHalves>(a, e, by[e & 1].to, t);
+#pragma unroll
+            for (int n = 0; n < L::kHalves; ++n) q[n][e] = t[n];
+          }
+#pragma unroll
+          for (int n = 0; n < L::kHalves; ++n)
+            *reinterpret_cast<uint4*>(p.im.q_rows + at_key * L::kInputHalf + ((strip * SIDES + ks) * L::kHalves + n) * kBlock + 16 * lane) =
+                make_uint4(q[n][0], q[n][1], q[n][2], q[n][3]);
+        }
+    }
     const float f[2] = {w.row[row] * (second ? p.scale : m.beta[row]), w.row[row + 8] * (second ? p.scale : m.beta[row + 8])};
+    float most_p[2] = {0.0f, 0.0f};
+    float kept[GRAD ? 1 : TILES][2][4];   // the scores, until the largest of each row is known
 #pragma unroll
     for (int s = 0; s < TILES; ++s) {
       float y[2][4];
@@ -343,19 +402,45 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if (!finite(y[n][e])) atomicMin(&bad, row + 8 * (e >> 1));
-      } else if (s <= strip) {
-        constexpr int NT = GRAD ? kChain : L::kScore;
-        uint32_t a[NT][4];
-        as_rows<NT>(a, y[0], y[1]);
+      } else if (GRAD && s <= strip) {
+        uint32_t a[kChain][4];
+        as_rows<kChain>(a, y[0], y[1]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (GRAD)   // columns in front of rows
-            *reinterpret_cast<uint4*>(p.im.scores_back + at * L::kScoresBack + ((s * TILES + strip) * NT + n) * kBlock + 16 * lane) =
-                make_uint4(turn(a[n][0]), turn(a[n][1]), turn(a[n][2]), turn(a[n][3]));
-          else
-            *reinterpret_cast<uint4*>(p.im.scores + at * L::kScores + ((strip * TILES + s) * NT + n) * kBlock + 16 * lane) =
-                make_uint4(a[n][0], a[n][1], a[n][2], a[n][3]);
+        for (int n = 0; n < kChain; ++n)   // columns in front of rows
+          *reinterpret_cast<uint4*>(p.im.scores_back + at * L::kScoresBack + ((s * TILES + strip) * kChain + n) * kBlock + 16 * lane) =
+              make_uint4(turn(a[n][0]), turn(a[n][1]), turn(a[n][2]), turn(a[n][3]));
+      } else if (!GRAD) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            kept[GRAD ? 0 : s][n][e] = y[n][e];
+            most_p[e >> 1] = fmaxf(most_p[e >> 1], fabsf(y[n][e]));
+          }
+      }
+    }
+    if (second && !GRAD) {
+      const Scale by[2] = {scale_of(over_row(most_p[0])), scale_of(over_row(most_p[1]))};
+      if ((lane & 3) == 0) {
+        m.score[row] = by[0].from;
+        m.score[row + 8] = by[1].from;
+      }
+#pragma unroll
+      for (int s = 0; s < TILES; ++s) {
+        if (s > strip) continue;
+        uint32_t a[L::kHalves][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float(&y)[4] = kept[GRAD ? 0 : s][e >> 1];
+          uint32_t t[L::kHalves];
+          halves<L::kHalves>(y[2 * (e & 1)] * by[e & 1].to, y[2 * (e & 1) + 1] * by[e & 1].to, t);
+#pragma unroll
+          for (int n = 0; n < L::kHalves; ++n) a[n][e] = t[n];
         }
+#pragma unroll
+        for (int n = 0; n < L::kHalves; ++n)
+          *reinterpret_cast<uint4*>(p.im.scores + at * L::kScores + ((strip * TILES + s) * L::kHalves + n) * kBlock + 16 * lane) =
+              make_uint4(a[n][0], a[n][1], a[n][2], a[n][3]);
       }
     }
   }
@@ -384,22 +469,35 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
     for (int r = 0; r < 16; ++r) block[r * PITCH + lane] = x[r];
   }
   if (second && h % times == 0) {   // the key head's images, by its first head
-    char* to = p.im.k_add + at_key * L::kInput;
+    const float by = scale_of(__uint_as_float(most)).to;
+    auto put = [&](char* to, const uint32_t (&x)[L::kIn][4]) {
+      uint32_t k[L::kHalves][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t t[L::kHalves];
+        to_halves<L::kIn, L::kHalves>(x, e, by, t);
+#pragma unroll
+        for (int n = 0; n < L::kHalves; ++n) k[n][e] = t[n];
+      }
+#pragma unroll
+      for (int n = 0; n < L::kHalves; ++n) *reinterpret_cast<uint4*>(to + n * kBlock + 16 * lane) = make_uint4(k[n][0], k[n][1], k[n][2], k[n][3]);
+    };
 #pragma unroll 2
     for (int i = strip; i < SIDES * TILES; i += TILES) {
       const int side = i / TILES, ks = i % TILES;
+      uint32_t x[L::kIn][4];
 #pragma unroll
-      for (int n = 0; n < L::kIn; ++n) {
-        uint32_t x[4];
-        b_cols<DK>(x, base + P::kK + n * L::kRows, 16 * side, 16 * ks, lane);
-        *reinterpret_cast<uint4*>(to + (i * L::kIn + n) * kBlock + 16 * lane) = make_uint4(x[0], x[1], x[2], x[3]);
-        if (GRAD) {
-          b_cols<DK>(x, base + P::kQ + n * L::kRows, 16 * side, 16 * ks, lane);
+      for (int n = 0; n < L::kIn; ++n) b_cols<DK>(x[n], base + P::kK + n * L::kRows, 16 * side, 16 * ks, lane);
+      put(p.im.k_add + at_key * L::kInputHalf + i * L::kHalves * kBlock, x);
+      if (GRAD) {
+#pragma unroll
+        for (int n = 0; n < L::kIn; ++n) b_rows<DK>(x[n], base + P::kK + n * L::kRows, 16 * ks, 16 * side, lane);
+        put(p.im.k_rows + at_key * L::kInputHalf + (ks * SIDES + side) * L::kHalves * kBlock, x);
+#pragma unroll
+        for (int n = 0; n < L::kIn; ++n) {
+          b_cols<DK>(x[n], base + P::kQ + n * L::kRows, 16 * side, 16 * ks, lane);
           *reinterpret_cast<uint4*>(p.im.q_add + at_key * L::kInput + (i * L::kIn + n) * kBlock + 16 * lane) =
-              make_uint4(x[0], x[1], x[2], x[3]);
-          b_rows<DK>(x, base + P::kK + n * L::kRows, 16 * ks, 16 * side, lane);
-          *reinterpret_cast<uint4*>(p.im.k_rows + at_key * L::kInput + ((ks * SIDES + side) * L::kIn + n) * kBlock + 16 * lane) =
-              make_uint4(x[0], x[1], x[2], x[3]);
+              make_uint4(x[n][0], x[n][1], x[n][2], x[n][3]);
         }
       }
     }
@@ -440,9 +538,7 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
       for (int n = 0; n < kChain; ++n) a[ks][n][e] = t[n];
     }
   }
-#pragma unroll 1
-  for (int side = 0; side < SIDES; ++side) {
-    Accumulators<2, true> acc;
+  auto weighed = [&](Accumulators<2, true>& acc, int side) {
     acc.clear();
 #pragma unroll
     for (int ks = 0; ks < TILES; ++ks) {
@@ -471,25 +567,51 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
         mma_terms(acc, 0, a[ks], y);
       }
     }
-    float y[2][4];
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[n][e] = acc.get(n, e);
-    if (second) {
+  };
+  if (second) {
+#pragma unroll 1
+    for (int side = 0; side < SIDES; ++side) {
+      Accumulators<2, true> acc;
+      weighed(acc, side);
       float4* to = reinterpret_cast<float4*>(p.im.u + (at * SIDES + side) * L::kTokens + 2 * strip * kBlock) + lane;
-      to[0] = make_float4(y[0][0], y[0][1], y[0][2], y[0][3]);
-      to[32] = make_float4(y[1][0], y[1][1], y[1][2], y[1][3]);
-    } else {
-      uint32_t t[kChain][4];   // rows of 16 tokens as A would have them; B takes the middle two the other way round
-      as_rows<kChain>(t, y[0], y[1]);
 #pragma unroll
-      for (int n = 0; n < kChain; ++n) {
-        *reinterpret_cast<uint4*>(p.im.keys + at * L::kKeys + ((strip * SIDES + side) * kChain + n) * kBlock + 16 * lane) =
-            make_uint4(t[n][0], t[n][2], t[n][1], t[n][3]);
+      for (int n = 0; n < 2; ++n) to[32 * n] = make_float4(acc.get(n, 0), acc.get(n, 1), acc.get(n, 2), acc.get(n, 3));
+    }
+  } else {   // kept in U's place until the largest of the strip is known: this warp's own bytes
+    float largest = 0.0f;
+    float4* keep = reinterpret_cast<float4*>(smem + P::kKeep) + (strip * SIDES * 64) + lane;
+#pragma unroll 1
+    for (int side = 0; side < SIDES; ++side) {
+      Accumulators<2, true> acc;
+      weighed(acc, side);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const float4 y = make_float4(acc.get(n, 0), acc.get(n, 1), acc.get(n, 2), acc.get(n, 3));
+        largest = fmaxf(largest, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
+        keep[64 * side + 32 * n] = y;
+      }
+    }
+    const Scale by = scale_of(__uint_as_float(__reduce_max_sync(~0u, __float_as_uint(largest))));
+    if (lane == 0) m.keys[strip] = by.from;
+#pragma unroll 1
+    for (int side = 0; side < SIDES; ++side) {
+      uint32_t k[2][4];   // rows of 16 tokens as A would have them; B takes the middle two the other way round
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const float4 y = keep[64 * side + 32 * n];
+        uint32_t t[2];
+        halves<2>(y.x * by.to, y.y * by.to, t);
+        k[0][2 * n] = t[0]; k[1][2 * n] = t[1];
+        halves<2>(y.z * by.to, y.w * by.to, t);
+        k[0][2 * n + 1] = t[0]; k[1][2 * n + 1] = t[1];
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        *reinterpret_cast<uint4*>(p.im.keys + at * L::kKeys + ((strip * SIDES + side) * 2 + n) * kBlock + 16 * lane) =
+            make_uint4(k[n][0], k[n][2], k[n][1], k[n][3]);
         if (GRAD)
-          *reinterpret_cast<uint4*>(p.im.keys_add + at * L::kKeys + ((side * TILES + strip) * kChain + n) * kBlock + 16 * lane) =
-              make_uint4(turn(t[n][0]), turn(t[n][1]), turn(t[n][2]), turn(t[n][3]));
+          *reinterpret_cast<uint4*>(p.im.keys_add + at * L::kKeys + ((side * TILES + strip) * 2 + n) * kBlock + 16 * lane) =
+              make_uint4(turn(k[n][0]), turn(k[n][1]), turn(k[n][2]), turn(k[n][3]));
       }
     }
   }
@@ -542,13 +664,15 @@ struct ScanLay {
   static constexpr int kWarps = L::kTiles, kThreads = 64 * kWarps;
   static constexpr int kShare = DK / 16 < kWarps ? 1 : DK / 16 / kWarps;   // blocks of the state's rows a warp
   static constexpr int kStatePlane = 16 * MT * DK * 2, kTokenPlane = 16 * MT * L::C * 2;
-  static constexpr int kState = 0, kAfter = kState + kChain * kStatePlane, kW = kAfter + kChain * kTokenPlane;
-  static constexpr int kRing = kW + (KEEP ? 0 : L::kOwn * kTokenPlane);
+  // the state, e^{B-b} W and (for the outputs) W, and the scales of their rows
+  static constexpr int kState = 0, kAfter = kState + 2 * kStatePlane, kW = kAfter + 2 * kTokenPlane;
+  static constexpr int kStateScale = kW + (KEEP ? 0 : L::kHalves * kTokenPlane), kTokenScale = kStateScale + 16 * MT * L::kSides * 4;
+  static constexpr int kRing = (kTokenScale + 16 * MT * L::kTiles * 4 + 127) / 128 * 128;
   // of a chunk, a pair of warps': blocks of K^, U, K, and of Q and the scores
-  static constexpr int kKeysBytes = L::kSides * kChain * kBlock, kUBytes = 2 * kBlock, kAddBytes = kShare * L::kTiles * L::kIn * kBlock;
-  static constexpr int kQBytes = KEEP ? 0 : L::kSides * L::kIn * kBlock, kScoreBytes = KEEP ? 0 : L::kTiles * L::kScore * kBlock;
+  static constexpr int kKeysBytes = L::kSides * 2 * kBlock, kUBytes = 2 * kBlock, kAddBytes = kShare * L::kTiles * L::kHalves * kBlock;
+  static constexpr int kQBytes = KEEP ? 0 : L::kSides * L::kHalves * kBlock, kScoreBytes = KEEP ? 0 : L::kTiles * L::kHalves * kBlock;
   static constexpr int kU = kKeysBytes, kAdd = kU + MT * kUBytes, kQ = kAdd + kAddBytes, kScores = kQ + kQBytes, kPair = kScores + kScoreBytes;
-  static constexpr int kMarkFrom = offsetof(M, inside), kMarkBytes = offsetof(M, first) - kMarkFrom;
+  static constexpr int kMarkFrom = offsetof(M, query), kMarkBytes = offsetof(M, first) - kMarkFrom;
   static constexpr int kMarks = kWarps * kPair, kStage = kMarks + (kMarkBytes + 127) / 128 * 128;
   static constexpr int kStages = (227 * 1024 - 1024 - kRing) / kStage < 3 ? 2 : 3;
   static constexpr int kBytes = kRing + kStages * kStage;
@@ -574,7 +698,7 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
   const int g = lane >> 2, t = 2 * (lane & 3);
   const bool shares = own * SHARE < SIDES;   // a warp of the chain has rows of the state
   auto sync = [&]() { ptx::named_bar_sync(1, W::kThreads); };   // of the CTA, from several places in the code
-  // a chunk's marks from `inside` on
+  // a chunk's marks from `query` on
   auto marks_at = [&](const char* stage) { return reinterpret_cast<const typename L::M*>(stage + W::kMarks - W::kMarkFrom); };
   // each column's first token that is not finite, where there is one
   auto first_of = [&](int i) { return reinterpret_cast<const typename L::M*>(p.im.marks + (bh * p.chunks + i) * L::kMarks)->first; };
@@ -590,11 +714,11 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
     bool alive = true;   // no wait has given up
     const char* keys = p.im.keys + bh * p.chunks * L::kKeys + own * W::kKeysBytes;
     const char* u = p.im.u + (bh * p.chunks * SIDES + tile0) * L::kTokens + own * W::kUBytes;
-    const char* add = p.im.k_add + key * p.chunks * L::kInput + own * W::kAddBytes;
-    const char* q_rows = KEEP ? nullptr : p.im.q_rows + key * p.chunks * L::kInput + own * W::kQBytes;
+    const char* add = p.im.k_add + key * p.chunks * L::kInputHalf + own * W::kAddBytes;
+    const char* q_rows = KEEP ? nullptr : p.im.q_rows + key * p.chunks * L::kInputHalf + own * W::kQBytes;
     const char* scores = KEEP ? nullptr : p.im.scores + bh * p.chunks * L::kScores + own * W::kScoreBytes;
     const char* marks = p.im.marks + bh * p.chunks * L::kMarks + W::kMarkFrom;
-    const uint32_t seen = KEEP ? 0 : (own + 1) * L::kScore * kBlock;   // scores up to the diagonal
+    const uint32_t seen = KEEP ? 0 : (own + 1) * L::kHalves * kBlock;   // scores up to the diagonal
     const uint32_t bytes = W::kKeysBytes + MT * W::kUBytes + (shares ? W::kAddBytes : 0) + W::kQBytes + seen + (own == 0 ? W::kMarkBytes : 0);
     auto load = [&](int i) {
       if (lane != 0 || i >= count || !alive) return;
@@ -609,13 +733,13 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
       if (!KEEP) {
         ptx::bulk_load_plain(to + W::kQ, q_rows, W::kQBytes, on);
         ptx::bulk_load_plain(to + W::kScores, scores, seen, on);
-        q_rows += L::kInput;
+        q_rows += L::kInputHalf;
         scores += L::kScores;
       }
       if (own == 0) ptx::bulk_load_plain(stage + W::kMarks, marks, W::kMarkBytes, on);
       keys += L::kKeys;
       u += SIDES * L::kTokens;
-      add += L::kInput;
+      add += L::kInputHalf;
       marks += L::kMarks;
     };
     for (int i = 0; i < STAGES - 1; ++i) load(i);
@@ -631,41 +755,62 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
       } else {
         // O = scale e^b Q S + scores W, this warp's 16 tokens
         const auto* m = marks_at(stage);
-        const float in[2] = {p.scale * m->inside[16 * own + g], p.scale * m->inside[16 * own + g + 8]};
+        const float2 of_q = make_float2(m->query[16 * own + g], m->query[16 * own + g + 8]);
+        const float2 of_p = make_float2(m->score[16 * own + g], m->score[16 * own + g + 8]);
         const int any = m->any;
-        Accumulators<2 * MT, L::kApart> o;
-        o.clear();
+        // a step of 16 of k has its own scale in each column
+        float o[2 * MT][4] = {};
+        auto add_step = [&](const uint32_t (&q)[L::kHalves][4], uint32_t plane, int bytes, const float* scales, int steps, int ks, bool rows_of_state) {
+#pragma unroll
+          for (int n = 0; n < MT; ++n) {
+            uint32_t x[L::kHalves][4];
+#pragma unroll
+            for (int k = 0; k < L::kHalves; ++k) {
+              if (rows_of_state)
+                b_rows<DK>(x[k], plane + k * bytes, 16 * n, 16 * ks, lane);
+              else
+                b_rows<C>(x[k], plane + k * bytes, 16 * n, 16 * ks, lane);
+            }
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              float c[4];
+              products(c, q, x, f);
+              const float s0 = scales[(16 * n + 8 * f + t) * steps + ks], s1 = scales[(16 * n + 8 * f + t + 1) * steps + ks];
+              float(&to)[4] = o[2 * n + f];
+              to[0] = fmaf(c[0], s0, to[0]); to[1] = fmaf(c[1], s1, to[1]);
+              to[2] = fmaf(c[2], s0, to[2]); to[3] = fmaf(c[3], s1, to[3]);
+            }
+          }
+        };
+        const float *state_scale = reinterpret_cast<const float*>(smem + W::kStateScale), *token_scale = reinterpret_cast<const float*>(smem + W::kTokenScale);
 #pragma unroll
         for (int ks = 0; ks < SIDES; ++ks) {
-          uint32_t q[L::kIn][4], x[L::kOwn][MT][4];
+          uint32_t q[L::kHalves][4];
 #pragma unroll
-          for (int k = 0; k < L::kIn; ++k) load_block(q[k], st + W::kQ, ks * L::kIn + k, lane);
-#pragma unroll
-          for (int k = 0; k < L::kOwn; ++k)
-#pragma unroll
-            for (int n = 0; n < MT; ++n) b_rows<DK>(x[k][n], state + k * W::kStatePlane, 16 * n, 16 * ks, lane);
-          mma_terms(o, 0, q, x);
+          for (int k = 0; k < L::kHalves; ++k) load_block(q[k], st + W::kQ, ks * L::kHalves + k, lane);
+          add_step(q, state, W::kStatePlane, state_scale, SIDES, ks, true);
         }
+        float of_state[2 * MT][4];
 #pragma unroll
         for (int n = 0; n < 2 * MT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            o.main[n][e] = o.get(n, e) * in[e >> 1];
-            if (L::kApart) o.small[L::kApart ? n : 0][e] = 0.0f;
+            of_state[n][e] = o[n][e] * (e < 2 ? of_q.x : of_q.y);
+            o[n][e] = 0.0f;
           }
         sync();   // W's planes are there, the state's are read
 #pragma unroll
         for (int ks = 0; ks < TILES; ++ks) {
           if (ks > own) continue;
-          uint32_t q[L::kScore][4], x[L::kOwn][MT][4];
+          uint32_t q[L::kHalves][4];
 #pragma unroll
-          for (int k = 0; k < L::kScore; ++k) load_block(q[k], st + W::kScores, ks * L::kScore + k, lane);
-#pragma unroll
-          for (int k = 0; k < L::kOwn; ++k)
-#pragma unroll
-            for (int n = 0; n < MT; ++n) b_rows<C>(x[k][n], base + W::kW + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
-          mma_terms(o, 0, q, x);
+          for (int k = 0; k < L::kHalves; ++k) load_block(q[k], st + W::kScores, ks * L::kHalves + k, lane);
+          add_step(q, base + W::kW, W::kTokenPlane, token_scale, TILES, ks, false);
         }
+#pragma unroll
+        for (int n = 0; n < 2 * MT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][e] = fmaf(o[n][e], e < 2 ? of_p.x : of_p.y, of_state[n][e]);
         const int64_t t0 = static_cast<int64_t>(i) * C;
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
@@ -675,7 +820,7 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
           for (int n = 0; n < 2 * MT; ++n) {
             const int c = 16 * tile0 + 8 * n + t;
             if (c >= p.d) continue;
-            float y[2] = {o.get(n, 2 * f), o.get(n, 2 * f + 1)};
+            float y[2] = {o[n][2 * f], o[n][2 * f + 1]};
             if (any)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
@@ -690,18 +835,25 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
 
   // S^T: rows the state's columns 16 (tile0 + n) + g, + 8; columns this warp's share of its rows
   float S[MT][2 * SHARE][4];
-  auto publish = [&]() {   // as planes of terms
+  auto publish = [&]() {   // as planes of fp16 pairs, 16 columns of a row at a scale
 #pragma unroll
     for (int n = 0; n < MT; ++n)
 #pragma unroll
-      for (int j = 0; j < 2 * SHARE; ++j)
+      for (int j = 0; j < SHARE; ++j)
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          uint32_t x[kChain];
-          split<kChain>(S[n][j][2 * f], S[n][j][2 * f + 1], x);
+          const float x[4] = {S[n][2 * j][2 * f], S[n][2 * j][2 * f + 1], S[n][2 * j + 1][2 * f], S[n][2 * j + 1][2 * f + 1]};
+          const Scale by = scale_of(over_row(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])))));
+          const int row = 16 * n + g + 8 * f;
 #pragma unroll
-          for (int k = 0; k < kChain; ++k)
-            *reinterpret_cast<uint32_t*>(smem + W::kState + k * W::kStatePlane + unit_at<DK>(16 * n + g + 8 * f, 2 * own * SHARE + j) + 2 * t) = x[k];
+          for (int e = 0; e < 2; ++e) {
+            uint32_t h[2];
+            halves<2>(x[2 * e] * by.to, x[2 * e + 1] * by.to, h);
+            char* to = smem + W::kState + unit_at<DK>(row, 2 * (own * SHARE + j) + e) + 2 * t;
+            *reinterpret_cast<uint32_t*>(to) = h[0];
+            *reinterpret_cast<uint32_t*>(to + W::kStatePlane) = h[1];
+          }
+          if ((lane & 3) == 0) reinterpret_cast<float*>(smem + W::kStateScale)[row * SIDES + own * SHARE + j] = by.from;
         }
   };
   if (shares) {
@@ -724,53 +876,79 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
     sync();   // the chunk's operands and the state's planes are there; W's planes of the chunk before are read
     float w[MT][2][4];
     {
-      // W^T = U^T - S^T K^^T, this warp's 16 tokens; the next step's operands are asked for in front of a step's products
-      ChainSum<MT, 2> acc;
-      acc.clear();
-      uint32_t x[2][kChain][1][4], s[2][MT][kChain][4];
+      // W^T = U^T - S^T K^^T, this warp's 16 tokens; a step of 16 of k has its own scale in each row, and the next step's operands
+      // are asked for in front of a step's products
+      float acc[MT][2][4] = {};
+      uint32_t x[2][2][4], s[2][MT][2][4];
       auto fetch = [&](int ks) {
 #pragma unroll
         for (int n = 0; n < MT; ++n)
 #pragma unroll
-          for (int k = 0; k < kChain; ++k) a_rows<DK>(s[ks & 1][n][k], state + k * W::kStatePlane, 16 * n, 16 * ks, lane);
+          for (int k = 0; k < 2; ++k) a_rows<DK>(s[ks & 1][n][k], state + k * W::kStatePlane, 16 * n, 16 * ks, lane);
 #pragma unroll
-        for (int k = 0; k < kChain; ++k) load_block(x[ks & 1][k][0], st, ks * kChain + k, lane);
+        for (int k = 0; k < 2; ++k) load_block(x[ks & 1][k], st, ks * 2 + k, lane);
       };
       fetch(0);
 #pragma unroll
       for (int ks = 0; ks < SIDES; ++ks) {
         if (ks + 1 < SIDES) fetch(ks + 1);
-        acc.add(s[ks & 1], x[ks & 1], ks & 1);
+#pragma unroll
+        for (int n = 0; n < MT; ++n) {
+          const float* scale = reinterpret_cast<const float*>(smem + W::kStateScale) + (16 * n + g) * SIDES + ks;
+          const float s0 = scale[0], s1 = scale[8 * SIDES];
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            float c[4];
+            products(c, s[ks & 1][n], x[ks & 1], f);
+            acc[n][f][0] = fmaf(c[0], s0, acc[n][f][0]); acc[n][f][1] = fmaf(c[1], s0, acc[n][f][1]);
+            acc[n][f][2] = fmaf(c[2], s1, acc[n][f][2]); acc[n][f][3] = fmaf(c[3], s1, acc[n][f][3]);
+          }
+        }
       }
+      const float of_keys = m->keys[own];
 #pragma unroll
       for (int n = 0; n < MT; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float4 u = *reinterpret_cast<const float4*>(st + W::kU + (2 * n + j) * kBlock + 16 * lane);
-          w[n][j][0] = u.x - acc.get(n, j, 0); w[n][j][1] = u.y - acc.get(n, j, 1);
-          w[n][j][2] = u.z - acc.get(n, j, 2); w[n][j][3] = u.w - acc.get(n, j, 3);
+          w[n][j][0] = fmaf(-of_keys, acc[n][j][0], u.x); w[n][j][1] = fmaf(-of_keys, acc[n][j][1], u.y);
+          w[n][j][2] = fmaf(-of_keys, acc[n][j][2], u.z); w[n][j][3] = fmaf(-of_keys, acc[n][j][3], u.w);
         }
     }
     const float2 after[2] = {*reinterpret_cast<const float2*>(m->after + 16 * own + t), *reinterpret_cast<const float2*>(m->after + 16 * own + 8 + t)};
     const float total = m->total;
+    // W and e^{B-b} W share a scale
 #pragma unroll
     for (int n = 0; n < MT; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int f = 0; f < 2; ++f) {
+        float x[4], z[4];
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const int to = unit_at<C>(16 * n + g + 8 * f, 2 * own + j) + 2 * t;
-          if (!KEEP) {
-            uint32_t x[L::kOwn];
-            split<L::kOwn>(w[n][j][2 * f], w[n][j][2 * f + 1], x);
-#pragma unroll
-            for (int k = 0; k < L::kOwn; ++k) *reinterpret_cast<uint32_t*>(smem + W::kW + k * W::kTokenPlane + to) = x[k];
-          }
-          uint32_t x[kChain];
-          split<kChain>(w[n][j][2 * f] * after[j].x, w[n][j][2 * f + 1] * after[j].y, x);
-#pragma unroll
-          for (int k = 0; k < kChain; ++k) *reinterpret_cast<uint32_t*>(smem + W::kAfter + k * W::kTokenPlane + to) = x[k];
+        for (int e = 0; e < 4; ++e) {
+          x[e] = w[n][e >> 1][2 * f + (e & 1)];
+          z[e] = x[e] * (e & 1 ? after[e >> 1].y : after[e >> 1].x);
         }
+        float most = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most = fmaxf(most, KEEP ? fabsf(z[e]) : fmaxf(fabsf(x[e]), fabsf(z[e])));
+        const Scale by = scale_of(over_row(most));
+        const int row = 16 * n + g + 8 * f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int to = unit_at<C>(row, 2 * own + j) + 2 * t;
+          uint32_t h[2];
+          halves<2>(z[2 * j] * by.to, z[2 * j + 1] * by.to, h);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) *reinterpret_cast<uint32_t*>(smem + W::kAfter + k * W::kTokenPlane + to) = h[k];
+          if (!KEEP) {
+            uint32_t y[L::kHalves];
+            halves<L::kHalves>(x[2 * j] * by.to, x[2 * j + 1] * by.to, y);
+#pragma unroll
+            for (int k = 0; k < L::kHalves; ++k) *reinterpret_cast<uint32_t*>(smem + W::kW + k * W::kTokenPlane + to) = y[k];
+          }
+        }
+        if ((lane & 3) == 0) reinterpret_cast<float*>(smem + W::kTokenScale)[row * TILES + own] = by.from;
+      }
     sync();   // W's planes are there, the state's are read
     if (KEEP)
 #pragma unroll
@@ -781,29 +959,39 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
           for (int j = 0; j < 2; ++j) to[32 * j] = make_float4(w[n][j][0], w[n][j][1], w[n][j][2], w[n][j][3]);
         }
     if (!shares) continue;
-    // S^T <- e^B S^T + (e^{B-b} W)^T K.  The chunk's sum is formed apart and added once, rounded to nearest: a long
-    // sequence must not gather the tensor core's truncation.
-    ChainSum<MT, 2 * SHARE> sum;
-    sum.clear();
+    // S^T <- e^B S^T + (e^{B-b} W)^T K, added outside the tensor core, which truncates what it adds
+    float sum[MT][2 * SHARE][4] = {};
     {
-      uint32_t x[2][L::kIn][SHARE][4], v[2][MT][kChain][4];
+      uint32_t x[2][SHARE][L::kHalves][4], v[2][MT][2][4];
       auto fetch = [&](int ks) {
 #pragma unroll
         for (int n = 0; n < MT; ++n)
 #pragma unroll
-          for (int k = 0; k < kChain; ++k) a_rows<C>(v[ks & 1][n][k], base + W::kAfter + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
+          for (int k = 0; k < 2; ++k) a_rows<C>(v[ks & 1][n][k], base + W::kAfter + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
 #pragma unroll
-        for (int k = 0; k < L::kIn; ++k)
+        for (int j = 0; j < SHARE; ++j)
 #pragma unroll
-          for (int j = 0; j < SHARE; ++j) load_block(x[ks & 1][k][j], st + W::kAdd, (j * TILES + ks) * L::kIn + k, lane);
+          for (int k = 0; k < L::kHalves; ++k) load_block(x[ks & 1][j][k], st + W::kAdd, (j * TILES + ks) * L::kHalves + k, lane);
       };
       fetch(0);
 #pragma unroll
       for (int ks = 0; ks < TILES; ++ks) {
         if (ks + 1 < TILES) fetch(ks + 1);
-        sum.add(v[ks & 1], x[ks & 1], ks & 1);
+#pragma unroll
+        for (int n = 0; n < MT; ++n) {
+          const float* scale = reinterpret_cast<const float*>(smem + W::kTokenScale) + (16 * n + g) * TILES + ks;
+          const float s0 = scale[0], s1 = scale[8 * TILES];
+#pragma unroll
+          for (int j = 0; j < 2 * SHARE; ++j) {
+            float c[4];
+            products(c, v[ks & 1][n], x[ks & 1][j >> 1], j & 1);
+            sum[n][j][0] = fmaf(c[0], s0, sum[n][j][0]); sum[n][j][1] = fmaf(c[1], s0, sum[n][j][1]);
+            sum[n][j][2] = fmaf(c[2], s1, sum[n][j][2]); sum[n][j][3] = fmaf(c[3], s1, sum[n][j][3]);
+          }
+        }
       }
     }
+    const float of_key = m->key;
 #pragma unroll
     for (int n = 0; n < MT; ++n)
 #pragma unroll
@@ -812,7 +1000,7 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
           *reinterpret_cast<float4*>(p.im.s + ((bh * p.chunks + i) * SIDES + tile0 + n) * L::kState + (2 * own * SHARE + j) * kBlock + 16 * lane) =
               make_float4(S[n][j][0], S[n][j][1], S[n][j][2], S[n][j][3]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[n][j][e] = fmaf(total, S[n][j][e], sum.get(n, j, e));
+        for (int e = 0; e < 4; ++e) S[n][j][e] = fmaf(total, S[n][j][e], of_key * sum[n][j][e]);
       }
     if (m->any) {
 #pragma unroll
@@ -902,12 +1090,12 @@ size_t lay_out_as(int64_t heads, int64_t keys, bool grad, char* base, Images* im
     used += align_up(static_cast<size_t>(bytes));
     return at;
   };
-  im->k_add = take(keys * L::kInput);
+  im->k_add = take(keys * L::kInputHalf);
   im->keys = take(heads * L::kKeys);
   im->u = take(heads * L::kSides * L::kTokens);
   im->marks = take(heads * L::kMarks);
   if (!grad) {
-    im->q_rows = take(keys * L::kInput);
+    im->q_rows = take(keys * L::kInputHalf);
     im->scores = take(heads * L::kScores);
     return used;
   }
@@ -915,7 +1103,7 @@ size_t lay_out_as(int64_t heads, int64_t keys, bool grad, char* base, Images* im
   im->q = take(keys * L::kInput);
   im->dout = take(heads * L::kInput);
   im->inverse = take(heads * L::kInverse);
-  im->k_rows = take(keys * L::kInput);
+  im->k_rows = take(keys * L::kInputHalf);
   im->keys_add = take(heads * L::kKeys);
   im->q_add = take(keys * L::kInput);
   im->scores_back = take(heads * L::kScoresBack);
