@@ -235,31 +235,27 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
     {
       // dW^T = (P^T do)^T + D^T (e^{B-b} K)^T
       float acc[MT][2][4] = {};
-      uint32_t x[2][L::kHalves][4], s[2][MT][2][4];
-      auto fetch = [&](int ks) {
+      uint32_t x[2][2][1][L::kHalves][4], s[2][2][MT][2][4];
+      auto fetch = [&](int pair) {
 #pragma unroll
-        for (int n = 0; n < MT; ++n)
+        for (int h = 0; h < 2; ++h) {
+          const int ks = 2 * pair + h;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) a_rows<DK>(s[ks & 1][n][k], base + W::kState + k * W::kStatePlane, 16 * n, 16 * ks, lane);
+          for (int k = 0; k < L::kHalves; ++k) load_block(x[pair & 1][h][0][k], st, ks * L::kHalves + k, lane);
 #pragma unroll
-        for (int k = 0; k < L::kHalves; ++k) load_block(x[ks & 1][k], st, ks * L::kHalves + k, lane);
+          for (int n = 0; n < MT; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) a_rows<DK>(s[pair & 1][h][n][k], base + W::kState + k * W::kStatePlane, 16 * n, 16 * ks, lane);
+        }
       };
+      const float* scales = reinterpret_cast<const float*>(smem + W::kStateScale) + g * SIDES;
       fetch(0);
 #pragma unroll
-      for (int ks = 0; ks < SIDES; ++ks) {
-        if (ks + 1 < SIDES) fetch(ks + 1);
-#pragma unroll
-        for (int n = 0; n < MT; ++n) {
-          const float* scale = reinterpret_cast<const float*>(smem + W::kStateScale) + (16 * n + g) * SIDES + ks;
-          const float s0 = scale[0], s1 = scale[8 * SIDES];
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            float c[4];
-            products(c, s[ks & 1][n], x[ks & 1], f);
-            acc[n][f][0] = fmaf(c[0], s0, acc[n][f][0]); acc[n][f][1] = fmaf(c[1], s0, acc[n][f][1]);
-            acc[n][f][2] = fmaf(c[2], s1, acc[n][f][2]); acc[n][f][3] = fmaf(c[3], s1, acc[n][f][3]);
-          }
-        }
+      for (int pair = 0; pair < SIDES / 2; ++pair) {
+        if (pair + 1 < SIDES / 2) fetch(pair + 1);
+        add_scaled<MT, 2, 2, L::kHalves>(acc, s[pair & 1], x[pair & 1], [&](int k, int n) {
+          return make_float2(scales[16 * n * SIDES + 2 * pair + k], scales[(16 * n + 8) * SIDES + 2 * pair + k]);
+        });
       }
       const float of_key = m->key;
       const float2 after[2] = {*reinterpret_cast<const float2*>(m->after + 16 * own + t), *reinterpret_cast<const float2*>(m->after + 16 * own + 8 + t)};
@@ -305,34 +301,30 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
     // D^T <- e^B D^T + (Q^T do)^T - dW^T K^, the chunk's part formed apart
     float sum[MT][2 * SHARE][4] = {};
     {
-      uint32_t x[2][SHARE][2][4], v[2][MT][2][4];
-      auto fetch = [&](int ks) {
+      uint32_t x[2][2][SHARE][2][4], v[2][2][MT][2][4];
+      auto fetch = [&](int pair) {
 #pragma unroll
-        for (int n = 0; n < MT; ++n)
+        for (int h = 0; h < 2; ++h) {
+          const int ks = 2 * pair + h;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) a_rows<C>(v[ks & 1][n][k], base + W::kW + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
+          for (int n = 0; n < MT; ++n)
 #pragma unroll
-        for (int j = 0; j < SHARE; ++j)
+            for (int k = 0; k < 2; ++k) a_rows<C>(v[pair & 1][h][n][k], base + W::kW + k * W::kTokenPlane, 16 * n, 16 * ks, lane);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) load_block(x[ks & 1][j][k], st + W::kKeys, (j * TILES + ks) * 2 + k, lane);
+          for (int j = 0; j < SHARE; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) load_block(x[pair & 1][h][j][k], st + W::kKeys, (j * TILES + ks) * 2 + k, lane);
+        }
       };
+      const float* scales = reinterpret_cast<const float*>(smem + W::kTokenScale) + g * TILES;
       fetch(0);
 #pragma unroll
-      for (int ks = 0; ks < TILES; ++ks) {
-        if (ks + 1 < TILES) fetch(ks + 1);
-        const float of_keys = m->keys[ks];
-#pragma unroll
-        for (int n = 0; n < MT; ++n) {
-          const float* scale = reinterpret_cast<const float*>(smem + W::kTokenScale) + (16 * n + g) * TILES + ks;
-          const float s0 = scale[0] * of_keys, s1 = scale[8 * TILES] * of_keys;
-#pragma unroll
-          for (int j = 0; j < 2 * SHARE; ++j) {
-            float c[4];
-            products(c, v[ks & 1][n], x[ks & 1][j >> 1], j & 1);
-            sum[n][j][0] = fmaf(c[0], s0, sum[n][j][0]); sum[n][j][1] = fmaf(c[1], s0, sum[n][j][1]);
-            sum[n][j][2] = fmaf(c[2], s1, sum[n][j][2]); sum[n][j][3] = fmaf(c[3], s1, sum[n][j][3]);
-          }
-        }
+      for (int pair = 0; pair < TILES / 2; ++pair) {
+        if (pair + 1 < TILES / 2) fetch(pair + 1);
+        add_scaled<MT, 2 * SHARE, 2, 2>(sum, v[pair & 1], x[pair & 1], [&](int k, int n) {
+          const float of_keys = m->keys[2 * pair + k];
+          return make_float2(of_keys * scales[16 * n * TILES + 2 * pair + k], of_keys * scales[(16 * n + 8) * TILES + 2 * pair + k]);
+        });
       }
     }
 #pragma unroll

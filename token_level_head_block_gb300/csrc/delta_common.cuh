@@ -129,21 +129,48 @@ __device__ __forceinline__ void halves(float x, float y, uint32_t (&t)[NT]) {
     t[1] = pack_half(x - f.x, y - f.y);
   }
 }
-// c = sum over the pairs of terms that matter, small ones first; each tile begins anew.
+// c = sum over the pairs of terms that matter, small ones first; each tile begins anew.  step 0 .. steps - 1 of it.
+template <int NA, int NB>
+__device__ __forceinline__ constexpr int product_steps() { return 1 + (NA > 1) + (NB > 1); }
+template <int NA, int NB>
+__device__ __forceinline__ void product(float (&c)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4], int half, int step) {
+  const int last = product_steps<NA, NB>() - 1;
+  const int i = NA > 1 && step == 0 ? 1 : 0, j = NB > 1 && step == last - 1 ? 1 : 0;
+  if (step == 0)
+    mma_half_first(c, a[i < NA ? i : 0], b[j < NB ? j : 0][2 * half], b[j < NB ? j : 0][2 * half + 1]);
+  else
+    mma_half(c, a[i < NA ? i : 0], b[j < NB ? j : 0][2 * half], b[j < NB ? j : 0][2 * half + 1]);
+}
 template <int NA, int NB>
 __device__ __forceinline__ void products(float (&c)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4], int half) {
-  constexpr bool kMixed = NA > 1 || NB > 1;
-  if constexpr (NA > 1) mma_half_first(c, a[1], b[0][2 * half], b[0][2 * half + 1]);
-  if constexpr (NB > 1) {
-    if constexpr (NA > 1)
-      mma_half(c, a[0], b[1][2 * half], b[1][2 * half + 1]);
-    else
-      mma_half_first(c, a[0], b[1][2 * half], b[1][2 * half + 1]);
-  }
-  if constexpr (kMixed)
-    mma_half(c, a[0], b[0][2 * half], b[0][2 * half + 1]);
-  else
-    mma_half_first(c, a[0], b[0][2 * half], b[0][2 * half + 1]);
+#pragma unroll
+  for (int step = 0; step < product_steps<NA, NB>(); ++step) product(c, a, b, half, step);
+}
+// Two steps of 16 of k of MT x NT tiles, NP of a[k][m] and b[k][n / 2]; the k-th step's sum is added at its rows' scale.  The MMAs of one
+// tile lie 2 MT NT apart, so none waits for the one before.
+template <int MT, int NT, int NA, int NB, typename ScaleOf>
+__device__ __forceinline__ void add_scaled(float (&sum)[MT][NT][4], const uint32_t (&a)[2][MT][NA][4], const uint32_t (&b)[2][NT / 2][NB][4],
+                                           ScaleOf scale) {
+  float c[2][MT][NT][4];
+#pragma unroll
+  for (int step = 0; step < product_steps<NA, NB>(); ++step)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) product(c[k][m][n], a[k][m], b[k][n >> 1], n & 1, step);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const float2 f = scale(k, m);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        sum[m][n][0] = fmaf(c[k][m][n][0], f.x, sum[m][n][0]); sum[m][n][1] = fmaf(c[k][m][n][1], f.x, sum[m][n][1]);
+        sum[m][n][2] = fmaf(c[k][m][n][2], f.y, sum[m][n][2]); sum[m][n][3] = fmaf(c[k][m][n][3], f.y, sum[m][n][3]);
+      }
+    }
 }
 // The largest size among the four lanes of a row.
 __device__ __forceinline__ float over_row(float m) {
