@@ -261,6 +261,16 @@ def kernel_work(wl, name):
         # norm and rotation: q and k in and out; with both output gradients in
         "qk_norm": ("hbm", 4 * io), "qk_norm_backward": ("hbm", 6 * io),
         "qk_norm_weight_grad": ("hbm", 2 * d * 4),
+        # delta rule: q, k, v and what the chain reads of them, written and read; the states of every 64 tokens
+        "delta_prepare": ("hbm", 8 * io), "delta_scan": ("hbm", 6 * io), "delta_step": ("hbm", BH * d * d * 8),
+        "delta_states": ("hbm", 5 * io + BH * max(1, wl.N // 64) * d * d * 4),
+        "delta_back": ("hbm", 6 * io + BH * max(1, wl.N // 64) * d * d * 4),
+        "delta_grads": ("hbm", 12 * io + BH * max(1, wl.N // 64) * d * d * 8), "delta_shared": ("hbm", 6 * io),
+        # linear layer of the model's width
+        "linear_gemm": ("tensor", 2 * wl.tokens * (wl.H * d) ** 2), "linear_gemm_dx": ("tensor", 2 * wl.tokens * (wl.H * d) ** 2),
+        "linear_gemm_dw": ("tensor", 2 * wl.tokens * (wl.H * d) ** 2), "linear_join": ("hbm", 2 * (wl.H * d) ** 2 * 4),
+        "linear_planes": ("hbm", 3 * io), "linear_column_sums": ("hbm", 2 * wl.H * d * 4),
+        "linear_rows": ("hbm", (wl.H * d) ** 2 * wl.elem_bytes),
     }
     return table.get(name, ("hbm", 0))
 

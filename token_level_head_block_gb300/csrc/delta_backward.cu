@@ -358,31 +358,46 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
 struct GradArgs {
   Common c;
   Operand dq, dk, dv, dg, dbeta;   // dq, dk: of every value head when they are shared, float32 then
-  uint32_t pairs;                  // stores of two values: 1 dq, 2 dk, 4 dv
+  uint32_t pairs;                  // stores of two values: 1 dq, 2 dk
 };
 
 template <typename T, int DK>
 struct GradLay {
   using L = Lay<T, DK>;
   static constexpr int C = L::C, kStrips = C / 16, kWarps = 2 * kStrips, kThreads = 32 * kWarps;
+  static constexpr int kHeld = (L::kSides + kWarps - 1) / kWarps;      // tiles of 16 value columns a warp
   static constexpr int kSlice = DK < 64 ? DK : 64;                     // columns of the values of a state at once
-  static constexpr int kTurned = L::kOwn * DK * C * 2;                 // planes [column][token]
-  static constexpr int kSliceBytes = L::kOwn * kSlice * DK * 2, kPairs = C * (C + 1) * 4, kSum = C * DK * 4;
-  static constexpr int kK = 0, kQ = kK + L::kInput, kDout = kQ + L::kInput, kW = kDout + L::kInput, kR = kW + kTurned;
+  static constexpr int kTurnedPlane = DK * C * 2, kTurned = L::kHalves * kTurnedPlane;   // planes [column][token]
+  static constexpr int kSlicePlane = kSlice * DK * 2, kGrid = C + 8, kPairs = C * kGrid * 4, kSum = C * DK * 4;
+  static constexpr int kPitch = DK + 4 / static_cast<int>(sizeof(T)), kValues = C * kPitch * static_cast<int>(sizeof(T));   // V, then dv, [token][column]
+  static constexpr int kK = 0, kQ = kK + L::kInputHalf, kDout = kQ + L::kInputHalf, kW = kDout + L::kInputHalf, kR = kW + kTurned;
   static constexpr int kA = kR + kTurned;                              // T before it is A
   static constexpr int kL = kA + L::kInverse, kState = kL + L::kInverse;
-  static constexpr int kBytes = kState + std::max(kSliceBytes, std::max(kPairs, kSum));
+  static constexpr int kBytes = kState + std::max(L::kHalves * kSlicePlane, std::max(kValues, std::max(kPairs, kSum)));
+  static_assert(kThreads == 4 * C, "four threads a token");
 };
 
+// Two values of row r, column tile n of planes W columns wide.
+template <int W, int NH>
+__device__ __forceinline__ void put(char* smem, int where, int plane, int r, int n, float x, float y) {
+  uint32_t h[NH];
+  halves<NH>(x, y, h);
+#pragma unroll
+  for (int k = 0; k < NH; ++k) *reinterpret_cast<uint32_t*>(smem + where + k * plane + unit_at<W>(r, n) + 4 * (threadIdx.x & 3)) = h[k];
+}
+
 // One chunk of one (b, h).  A pair of warps has 16 rows: one the products with dout (dq, A), the other those with dR (L, dk).
+// Everything enters the tensor cores as one fp16 beside bf16 outputs (2^-11), two beside float32 ones, a whole plane at one scale.
 template <typename T, int DK, typename O>
-__global__ void __launch_bounds__(GradLay<T, DK>::kThreads) delta_grads(const __grid_constant__ GradArgs a) {
+__global__ void __launch_bounds__(GradLay<T, DK>::kThreads, DK < 128 ? 2 : 1) delta_grads(const __grid_constant__ GradArgs a) {
   using G = GradLay<T, DK>;
   using L = Lay<T, DK>;
-  constexpr int C = L::C, THREADS = G::kThreads, STRIPS = G::kStrips, NS = DK / 8, TILES = DK / 16;
+  constexpr int C = L::C, THREADS = G::kThreads, STRIPS = G::kStrips, NS = DK / 8, TILES = L::kSides, NH = L::kHalves, HELD = G::kHeld;
   extern __shared__ __align__(128) char smem[];
   __shared__ __align__(16) typename L::M m;
-  __shared__ float vdot[TILES][C], rows_g[C], zk[C], enters[2][C], leaves[C], crossing[C], both[G::kWarps];
+  __shared__ float vdot[TILES][C], rows_g[C], zk[C], parts[4][C], enters[2][C], leaves[C], crossing[C], both[G::kWarps];
+  enum { kMostW, kMostR, kMostA, kMostL, kMostS, kMostD, kMosts };
+  __shared__ uint32_t most[kMosts];   // the largest of each plane
   const Common& p = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t chunk = blockIdx.x % p.chunks;
@@ -391,152 +406,223 @@ __global__ void __launch_bounds__(GradLay<T, DK>::kThreads) delta_grads(const __
   const int64_t t0 = static_cast<int64_t>(chunk) * C;
   const int rows = static_cast<int>(min(static_cast<int64_t>(C), p.N - t0));
   const uint32_t base = ptx::smem_u32(smem);
-  const int strip = warp % STRIPS, m0 = 16 * strip, row = m0 + (lane >> 2);
+  const int g = lane >> 2, t = 2 * (lane & 3);
+  const int strip = warp % STRIPS, m0 = 16 * strip, row = m0 + g;
   const bool second = warp >= STRIPS;
 
-  copy_async(base + G::kK, p.im.k + at_key * L::kInput, L::kInput, threadIdx.x, THREADS);
-  copy_async(base + G::kQ, p.im.q + at_key * L::kInput, L::kInput, threadIdx.x, THREADS);
-  copy_async(base + G::kDout, p.im.dout + at * L::kInput, L::kInput, threadIdx.x, THREADS);
+  copy_async(base + G::kK, p.im.k + at_key * L::kInputHalf, L::kInputHalf, threadIdx.x, THREADS);
+  copy_async(base + G::kQ, p.im.q + at_key * L::kInputHalf, L::kInputHalf, threadIdx.x, THREADS);
+  copy_async(base + G::kDout, p.im.dout + at * L::kInputHalf, L::kInputHalf, threadIdx.x, THREADS);
   copy_async(base + G::kA, p.im.inverse + at * L::kInverse, L::kInverse, threadIdx.x, THREADS);
   copy_async(ptx::smem_u32(&m), p.im.marks + at * L::kMarks, L::kMarks, threadIdx.x, THREADS);
   commit();
-  // two values of one row of planes W columns wide
-  auto put = [&](int where, int width, int plane, int r, int n, float x, float y) {
-    uint32_t t[L::kOwn];
-    split<L::kOwn>(x, y, t);
-#pragma unroll
-    for (int k = 0; k < L::kOwn; ++k) {
-      const int u = width == C ? unit_at<C>(r, n) : unit_at<DK>(r, n);
-      *reinterpret_cast<uint32_t*>(smem + where + k * plane + u + 4 * (lane & 3)) = t[k];
+  T* values = reinterpret_cast<T*>(smem + G::kState);
+  {
+    const T* v = static_cast<const T*>(p.v.data) + b * p.v.sb + h * p.v.sh + t0 * p.v.sn;
+    const T zero = T(0.0f);
+#pragma unroll 8
+    for (int i = threadIdx.x; i < C * DK; i += THREADS) {
+      const int r = i / DK, c = i % DK;
+      values[r * G::kPitch + c] = r < rows && c < p.d ? v[r * p.v.sn + c] : zero;
     }
+  }
+  if (threadIdx.x < kMosts) most[threadIdx.x] = 0;
+  __syncthreads();
+  auto note = [&](int which, float largest) {
+    const uint32_t all = __reduce_max_sync(~0u, __float_as_uint(largest));
+    if (lane == 0) atomicMax(most + which, all);
   };
-  // W^T from its fragments
-  for (int tile = warp; tile < TILES; tile += G::kWarps) {
-    const float4* from = reinterpret_cast<const float4*>(p.im.w + (at * TILES + tile) * L::kTokens) + lane;
+  auto scale = [&](int which) { return plane_scale(most[which]); };
+  auto size = [](float4 x) { return fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))); };
+  // fragments of W and dW; <S, D> and the largest of both states
+  float4 w[HELD][C / 8], dw[HELD][C / 8];
+  const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float through = 0.0f;
+  {
+    float of_w = 0.0f, of_s = 0.0f, of_d = 0.0f;
 #pragma unroll
-    for (int n = 0; n < C / 8; ++n) {
-      const float4 x = 16 * tile < p.d ? from[32 * n] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      put(G::kW, C, DK * C * 2, 16 * tile + (lane >> 2), n, x.x, x.y);
-      put(G::kW, C, DK * C * 2, 16 * tile + (lane >> 2) + 8, n, x.z, x.w);
+    for (int i = 0; i < HELD; ++i) {
+      const int tile = warp + i * G::kWarps;
+      const bool in = 16 * tile < p.d;
+      const float4 *from = reinterpret_cast<const float4*>(p.im.w + (at * TILES + tile) * L::kTokens) + lane,
+                   *from_d = reinterpret_cast<const float4*>(p.im.dw + (at * TILES + tile) * L::kTokens) + lane;
+#pragma unroll
+      for (int n = 0; n < C / 8; ++n) {
+        w[i][n] = in ? from[32 * n] : none;
+        dw[i][n] = in ? from_d[32 * n] : none;
+      }
     }
+    const int64_t off = at * TILES * L::kState;
+    const int used = (p.d + 15) / 16 * NS * 32;   // float4 of either state
+#pragma unroll 4
+    for (int i = threadIdx.x; i < used; i += THREADS) {
+      const float4 x = reinterpret_cast<const float4*>(p.im.s + off)[i], y = reinterpret_cast<const float4*>(p.im.ds + off)[i];
+      of_s = fmaxf(of_s, size(x));
+      of_d = fmaxf(of_d, size(y));
+      through = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, through))));
+    }
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+#pragma unroll
+      for (int n = 0; n < C / 8; ++n) of_w = fmaxf(of_w, size(w[i][n]));
+    note(kMostW, of_w);
+    note(kMostS, of_s);
+    note(kMostD, of_d);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) through += __shfl_xor_sync(~0u, through, o);
+    if (lane == 0) both[warp] = through;
   }
   wait_all();
   __syncthreads();
 
-  // dR^T = dW^T T; dv; dR . V
-  for (int tile = warp; tile < TILES; tile += G::kWarps) {
-    Accumulators<C / 8, L::kApart> acc;
-    acc.clear();
-    if (16 * tile < p.d) {
-      const float4* from = reinterpret_cast<const float4*>(p.im.dw + (at * TILES + tile) * L::kTokens) + lane;
+  // W's planes; dR^T = dW^T T, each row of dW^T at its own scale; dv; dR . V
+  {
+    const Scale by_w = scale(kMostW);
+    float of_r = 0.0f;
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      const int tile = warp + i * G::kWarps;
+      if (tile >= TILES) break;
+      float largest[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int n = 0; n < C / 8; ++n) {
+        const float4 x = w[i][n], y = dw[i][n];
+        put<C, NH>(smem, G::kW, G::kTurnedPlane, 16 * tile + g, n, x.x * by_w.to, x.y * by_w.to);
+        put<C, NH>(smem, G::kW, G::kTurnedPlane, 16 * tile + g + 8, n, x.z * by_w.to, x.w * by_w.to);
+        largest[0] = fmaxf(largest[0], fmaxf(fabsf(y.x), fabsf(y.y)));
+        largest[1] = fmaxf(largest[1], fmaxf(fabsf(y.z), fabsf(y.w)));
+      }
+      const Scale by[2] = {scale_of(over_row(largest[0])), scale_of(over_row(largest[1]))};
+      float acc[C / 8][4] = {};
 #pragma unroll
       for (int ks = 0; ks < STRIPS; ++ks) {
-        const float4 x = from[64 * ks], y = from[64 * ks + 32];
-        const float lo[4] = {x.x, x.y, x.z, x.w}, hi[4] = {y.x, y.y, y.z, y.w};
-        uint32_t wa[L::kOwn][4];
-        as_rows<L::kOwn>(wa, lo, hi);
+        uint32_t x[NH][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float4 y = dw[i][2 * ks + n];
+          uint32_t h2[NH];
+          halves<NH>(y.x * by[0].to, y.y * by[0].to, h2);
+#pragma unroll
+          for (int k = 0; k < NH; ++k) x[k][2 * n] = h2[k];
+          halves<NH>(y.z * by[1].to, y.w * by[1].to, h2);
+#pragma unroll
+          for (int k = 0; k < NH; ++k) x[k][2 * n + 1] = h2[k];
+        }
 #pragma unroll
         for (int s = 0; s <= ks; ++s) {
-          uint32_t t[L::kOwn][1][4];
+          uint32_t y[NH][4];
 #pragma unroll
-          for (int n = 0; n < L::kOwn; ++n) b_cols<C>(t[n][0], base + G::kA + n * L::kSquare, 16 * s, 16 * ks, lane);
-          mma_terms(acc, 2 * s, wa, t);
+          for (int k = 0; k < NH; ++k) b_cols<C>(y[k], base + G::kA + k * L::kSquare, 16 * s, 16 * ks, lane);
+#pragma unroll
+          for (int f = 0; f < 2; ++f) add_products(acc[2 * s + f], x, y, f);
+        }
+      }
+      const float f0 = by[0].from * m.inverse, f1 = by[1].from * m.inverse;
+#pragma unroll
+      for (int n = 0; n < C / 8; ++n) {
+        const float4 x = make_float4(acc[n][0] * f0, acc[n][1] * f0, acc[n][2] * f1, acc[n][3] * f1);
+        dw[i][n] = x;
+        of_r = fmaxf(of_r, size(x));
+        const float xs[4] = {x.x, x.y, x.z, x.w};
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int token = 8 * n + t + (e & 1);
+          T* v = values + token * G::kPitch + 16 * tile + g + 8 * (e >> 1);
+          sum[e & 1] = fmaf(xs[e], to_f(*v), sum[e & 1]);
+          from_f(v, m.beta[token] * xs[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sum[e] += __shfl_xor_sync(~0u, sum[e], 4);
+          sum[e] += __shfl_xor_sync(~0u, sum[e], 8);
+          sum[e] += __shfl_xor_sync(~0u, sum[e], 16);
+          if (lane < 4) vdot[tile][8 * n + t + e] = sum[e];
         }
       }
     }
-    const T* v = static_cast<const T*>(p.v.data) + b * p.v.sb + h * p.v.sh + t0 * p.v.sn;
+    note(kMostR, of_r);
+  }
+  __syncthreads();
+  {
     T* dv = static_cast<T*>(a.dv.data) + b * a.dv.sb + h * a.dv.sh + t0 * a.dv.sn;
+    for (int i = threadIdx.x; i < C * DK; i += THREADS) {
+      const int r = i / DK, c = i % DK;
+      if (r < rows && c < p.d) dv[r * a.dv.sn + c] = values[r * G::kPitch + c];
+    }
+    const float by = scale(kMostR).to;
 #pragma unroll
-    for (int n = 0; n < C / 8; ++n) {
-      float sum[2] = {0.0f, 0.0f};
+    for (int i = 0; i < HELD; ++i) {
+      const int tile = warp + i * G::kWarps;
+      if (tile >= TILES) break;
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const int c = 16 * tile + (lane >> 2) + 8 * f;
-        put(G::kR, C, DK * C * 2, c, n, acc.get(n, 2 * f), acc.get(n, 2 * f + 1));
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int t = 8 * n + 2 * (lane & 3) + e;
-          if (t < rows && c < p.d) {
-            const float x = acc.get(n, 2 * f + e);
-            sum[e] = fmaf(x, to_f(v[t * p.v.sn + c]), sum[e]);
-            from_f(dv + t * a.dv.sn + c, m.beta[t] * x);
-          }
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        sum[e] += __shfl_xor_sync(~0u, sum[e], 4);
-        sum[e] += __shfl_xor_sync(~0u, sum[e], 8);
-        sum[e] += __shfl_xor_sync(~0u, sum[e], 16);
-        if (lane < 4) vdot[tile][8 * n + 2 * lane + e] = sum[e];
+      for (int n = 0; n < C / 8; ++n) {
+        const float4 x = dw[i][n];
+        put<C, NH>(smem, G::kR, G::kTurnedPlane, 16 * tile + g, n, x.x * by, x.y * by);
+        put<C, NH>(smem, G::kR, G::kTurnedPlane, 16 * tile + g + 8, n, x.z * by, x.w * by);
       }
     }
   }
   __syncthreads();
 
   // do W^T and Q K^T (first), dR W^T and K K^T (second), up to the diagonal: A and L, and the pairs of the gates
-  float pairs[2 * STRIPS][4];
+  const float of_w = scale(kMostW).from, of_r = scale(kMostR).from;
+  float kept[2 * STRIPS][4], pairs[2 * STRIPS][4];
   {
-    Accumulators<2 * STRIPS, L::kApart> x, y;
-    x.clear();
-    y.clear();
+    float x[2 * STRIPS][4] = {}, y[2 * STRIPS][4] = {};
 #pragma unroll 1
     for (int ks = 0; ks < TILES; ++ks) {
-      uint32_t l[L::kIn][4], r[L::kOwn][4];
-      uint32_t key[L::kIn][4];
+      uint32_t l[NH][4], key[NH][4];
 #pragma unroll
-      for (int n = 0; n < L::kIn; ++n) a_rows<DK>(key[n], base + (second ? G::kK : G::kQ) + n * L::kRows, m0, 16 * ks, lane);
-      if (second)
-#pragma unroll
-        for (int n = 0; n < L::kOwn; ++n) a_cols<C>(r[n], base + G::kR + n * DK * C * 2, m0, 16 * ks, lane);
-      else
-#pragma unroll
-        for (int n = 0; n < L::kIn; ++n) a_rows<DK>(l[n], base + G::kDout + n * L::kRows, m0, 16 * ks, lane);
+      for (int n = 0; n < NH; ++n) {
+        a_rows<DK>(key[n], base + (second ? G::kK : G::kQ) + n * L::kRows, m0, 16 * ks, lane);
+        if (second)
+          a_cols<C>(l[n], base + G::kR + n * G::kTurnedPlane, m0, 16 * ks, lane);
+        else
+          a_rows<DK>(l[n], base + G::kDout + n * L::kRows, m0, 16 * ks, lane);
+      }
 #pragma unroll
       for (int s = 0; s < STRIPS; ++s) {
         if (s > strip) continue;
-        uint32_t w[L::kOwn][1][4], k[L::kIn][1][4];
+        uint32_t u[NH][4], k[NH][4];
 #pragma unroll
-        for (int n = 0; n < L::kOwn; ++n) b_cols<C>(w[n][0], base + G::kW + n * DK * C * 2, 16 * s, 16 * ks, lane);
+        for (int n = 0; n < NH; ++n) {
+          b_cols<C>(u[n], base + G::kW + n * G::kTurnedPlane, 16 * s, 16 * ks, lane);
+          b_rows<DK>(k[n], base + G::kK + n * L::kRows, 16 * s, 16 * ks, lane);
+        }
 #pragma unroll
-        for (int n = 0; n < L::kIn; ++n) b_rows<DK>(k[n][0], base + G::kK + n * L::kRows, 16 * s, 16 * ks, lane);
-        if (second)
-          mma_terms(x, 2 * s, r, w);
-        else
-          mma_terms(x, 2 * s, l, w);
-        mma_terms(y, 2 * s, key, k);
+        for (int f = 0; f < 2; ++f) {
+          add_products(x[2 * s + f], l, u, f);
+          add_products(y[2 * s + f], key, k, f);
+        }
       }
     }
+    const float of_x = of_w * (second ? of_r : m.douts), of_y = m.key * (second ? m.key : m.queries);
     const Sum br[2] = {{m.hi[row], m.lo[row]}, {m.hi[row + 8], m.lo[row + 8]}};
     const float beta_r[2] = {m.beta[row], m.beta[row + 8]};
-    float sum[2] = {0.0f, 0.0f};
-    // T's planes, where A goes, were last read in front of the barrier
+    float sum[2] = {0.0f, 0.0f}, largest = 0.0f;
 #pragma unroll
     for (int n = 0; n < 2 * STRIPS; ++n) {
-      if (n >= 2 * strip + 2) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) pairs[n][e] = 0.0f;
-        continue;
-      }
-      const int c = 8 * n + 2 * (lane & 3);
-      float f[4];
+      const int c = 8 * n + t;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = row + 8 * (e >> 1), s = c + (e & 1);
+        kept[n][e] = pairs[n][e] = 0.0f;
+        if (n >= 2 * strip + 2) continue;
         const Sum bc = {m.hi[s], m.lo[s]};
         const float decay = s <= r ? exp2_of(br[e >> 1], bc) : 0.0f;
-        const float g = s <= r ? x.get(n, e) * decay : 0.0f, k = y.get(n, e);
+        const float d = s <= r ? x[n][e] * of_x * decay : 0.0f, k = y[n][e] * of_y;
         if (second) {
-          f[e] = s < r ? -beta_r[e >> 1] * g : 0.0f;
-          if (s < r) sum[e >> 1] = fmaf(g, k, sum[e >> 1]);
+          kept[n][e] = s < r ? -beta_r[e >> 1] * d : 0.0f;
+          if (s < r) sum[e >> 1] = fmaf(d, k, sum[e >> 1]);
         } else {
-          f[e] = p.scale * g;
+          kept[n][e] = p.scale * d;
         }
-        pairs[n][e] = s < r ? f[e] * k : 0.0f;
+        pairs[n][e] = s < r ? kept[n][e] * k : 0.0f;
+        largest = fmaxf(largest, fabsf(kept[n][e]));
       }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) put(second ? G::kL : G::kA, C, L::kSquare, row + 8 * e, n, f[2 * e], f[2 * e + 1]);
     }
+    note(second ? kMostL : kMostA, largest);
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
       sum[f] += __shfl_xor_sync(~0u, sum[f], 1);
@@ -552,121 +638,143 @@ __global__ void __launch_bounds__(GradLay<T, DK>::kThreads) delta_grads(const __
 #pragma unroll
       for (int n = 0; n < 2 * STRIPS; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float* to = grid + (row + 8 * (e >> 1)) * (C + 1) + 8 * n + 2 * (lane & 3) + (e & 1);
-          *to = turn ? *to + pairs[n][e] : pairs[n][e];
+        for (int f = 0; f < 2; ++f) {
+          float2* to = reinterpret_cast<float2*>(grid + (row + 8 * f) * G::kGrid + 8 * n + t);
+          float2 x = make_float2(pairs[n][2 * f], pairs[n][2 * f + 1]);
+          if (turn) x = make_float2(to->x + x.x, to->y + x.y);
+          *to = x;
         }
+    if (turn == 1) {   // every warp's largest is noted; T's planes, where A goes, were last read long ago
+      const float by = scale(second ? kMostL : kMostA).to;
+#pragma unroll
+      for (int n = 0; n < 2 * STRIPS; ++n) {
+        if (n >= 2 * strip + 2) continue;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) put<C, NH>(smem, second ? G::kL : G::kA, L::kSquare, row + 8 * e, n, kept[n][2 * e] * by, kept[n][2 * e + 1] * by);
+      }
+    }
     __syncthreads();
   }
-  if (threadIdx.x < C) {
-    float run = 0.0f;
-    for (int t = C - 1; t >= 0; --t) {
-      run += grid[t * (C + 1) + threadIdx.x];
-      grid[t * (C + 1) + threadIdx.x] = run;
+  {
+    constexpr int PART = C / 4;   // a thread's rows of a column, then columns of a row
+    const int c = threadIdx.x % C, r0 = threadIdx.x / C * PART;
+    float run[PART];
+#pragma unroll
+    for (int i = 0; i < PART; ++i) run[i] = grid[(r0 + i) * G::kGrid + c];
+#pragma unroll
+    for (int i = PART - 2; i >= 0; --i) run[i] += run[i + 1];
+    parts[threadIdx.x / C][c] = run[0];
+    __syncthreads();
+    float behind = 0.0f;
+#pragma unroll
+    for (int j = 3; j > 0; --j)
+      if (j * PART > r0) behind += parts[j][c];
+#pragma unroll
+    for (int i = 0; i < PART; ++i) grid[(r0 + i) * G::kGrid + c] = run[i] + behind;
+    __syncthreads();
+    const int r = threadIdx.x / 4, c0 = (threadIdx.x & 3) * PART;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PART; ++i) {   // each row from another column on: the lanes at other banks
+      const int s = c0 + ((i + r) & (PART - 1));
+      sum += s < r ? grid[r * G::kGrid + s] : 0.0f;
     }
-  }
-  __syncthreads();
-  if (threadIdx.x < C) {
-    float run = 0.0f;
-    for (int s = 0; s < static_cast<int>(threadIdx.x); ++s) run += grid[threadIdx.x * (C + 1) + s];
-    crossing[threadIdx.x] = run;
+    sum += __shfl_xor_sync(~0u, sum, 1);
+    sum += __shfl_xor_sync(~0u, sum, 2);
+    if ((threadIdx.x & 3) == 0) crossing[r] = sum;
   }
   __syncthreads();
 
-  float through = 0.0f;   // <S, D>
+  const float of_a = scale(kMostA).from, of_l = scale(kMostL).from;
+  float acc[NS][4] = {};
   // rows of S^T or D^T of a slice of the values' columns
-  auto fill = [&](const char* from, int slice, bool dot) {
+  auto fill = [&](const char* from, int slice, float by) {
     for (int j = warp; j < G::kSlice / 16 * NS; j += G::kWarps) {
       const int tile = slice * (G::kSlice / 16) + j / NS, n = j % NS;
-      const bool in = 16 * tile < p.d;
-      const int64_t off = (at * TILES + tile) * L::kState;
-      const float4 x = in ? reinterpret_cast<const float4*>(from + off)[32 * n + lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      const int r = 16 * (j / NS) + (lane >> 2);
-      put(G::kState, DK, G::kSlice * DK * 2, r, n, x.x, x.y);
-      put(G::kState, DK, G::kSlice * DK * 2, r + 8, n, x.z, x.w);
-      if (dot && in) {
-        const float4 y = reinterpret_cast<const float4*>(p.im.s + off)[32 * n + lane];
-        through = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, through))));
-      }
+      const float4 x = 16 * tile < p.d ? reinterpret_cast<const float4*>(from + (at * TILES + tile) * L::kState)[32 * n + lane] : none;
+      const int r = 16 * (j / NS) + g;
+      put<DK, NH>(smem, G::kState, G::kSlicePlane, r, n, x.x * by, x.y * by);
+      put<DK, NH>(smem, G::kState, G::kSlicePlane, r + 8, n, x.z * by, x.w * by);
     }
   };
   // a row's sum of acc times the rows of a plane
-  auto dot_rows = [&](const Accumulators<NS, L::kApart>& acc, int where, float (&sum)[2]) {
+  auto dot_rows = [&](int where, float of_plane, float (&sum)[2]) {
     sum[0] = sum[1] = 0.0f;
 #pragma unroll
     for (int n = 0; n < NS; ++n)
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        float x = 0.0f, y = 0.0f;
+        float2 x = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int k = L::kIn - 1; k >= 0; --k) {
-          const uint32_t t = *reinterpret_cast<const uint32_t*>(smem + where + k * L::kRows + unit_at<DK>(row + 8 * f, n) + 4 * (lane & 3));
-          x += low(t);
-          y += high(t);
+        for (int k = NH - 1; k >= 0; --k) {
+          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(smem + where + k * L::kRows + unit_at<DK>(row + 8 * f, n) + 2 * t));
+          x.x += y.x;
+          x.y += y.y;
         }
-        sum[f] = fmaf(acc.get(n, 2 * f), x, fmaf(acc.get(n, 2 * f + 1), y, sum[f]));
+        sum[f] = fmaf(acc[n][2 * f], x.x, fmaf(acc[n][2 * f + 1], x.y, sum[f]));
       }
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
       sum[f] += __shfl_xor_sync(~0u, sum[f], 1);
       sum[f] += __shfl_xor_sync(~0u, sum[f], 2);
+      sum[f] *= of_plane;
     }
   };
-  auto weigh = [&](Accumulators<NS, L::kApart>& acc, float f0, float f1) {
+  // acc += (f0, f1 of the rows) times 16 rows of KS steps of k, those from `from` up to `to`, with planes [k][channel]
+  auto add_rows = [&](const auto& l, int from, int to, int where, int plane, float f0, float f1) {
+    constexpr int STEPS = sizeof(l) / (NH * 16);
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
+    for (int j = 0; j < NS / 2; ++j) {
+      float c[2][4] = {};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc.main[n][e] = acc.get(n, e) * (e < 2 ? f0 : f1);
-        if (L::kApart) acc.small[L::kApart ? n : 0][e] = 0.0f;
+      for (int ks = 0; ks < STEPS; ++ks) {
+        if (ks < from || ks >= to) continue;
+        uint32_t x[NH][4];
+#pragma unroll
+        for (int n = 0; n < NH; ++n) b_cols<DK>(x[n], base + where + n * plane, 16 * j, 16 * ks, lane);
+#pragma unroll
+        for (int f = 0; f < 2; ++f) add_products(c[f], l[ks], x, f);
       }
-  };
-  // acc += rows of a square plane, or of its transpose, times the rows of an input
-  auto add_square = [&](Accumulators<NS, L::kApart>& acc, int square, bool turned, int where) {
-#pragma unroll 1
-    for (int ks = turned ? strip : 0; ks < (turned ? STRIPS : strip + 1); ++ks) {
-      uint32_t l[L::kOwn][4];
 #pragma unroll
-      for (int n = 0; n < L::kOwn; ++n) {
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[2 * j + f][e] = fmaf(c[f][e], e < 2 ? f0 : f1, acc[2 * j + f][e]);
+    }
+  };
+  // rows of a square plane, or of its transpose, times the rows of an input
+  auto add_square = [&](int square, bool turned, int where, float by) {
+    uint32_t l[STRIPS][NH][4];
+#pragma unroll
+    for (int ks = 0; ks < STRIPS; ++ks) {
+      if (turned ? ks < strip : ks > strip) continue;
+#pragma unroll
+      for (int n = 0; n < NH; ++n) {
         if (turned)
-          a_cols<C>(l[n], base + square + n * L::kSquare, m0, 16 * ks, lane);
+          a_cols<C>(l[ks][n], base + square + n * L::kSquare, m0, 16 * ks, lane);
         else
-          a_rows<C>(l[n], base + square + n * L::kSquare, m0, 16 * ks, lane);
-      }
-#pragma unroll
-      for (int j = 0; j < NS / 2; ++j) {
-        uint32_t x[L::kIn][1][4];
-#pragma unroll
-        for (int n = 0; n < L::kIn; ++n) b_cols<DK>(x[n][0], base + where + n * L::kRows, 16 * j, 16 * ks, lane);
-        mma_terms(acc, 2 * j, l, x);
+          a_rows<C>(l[ks][n], base + square + n * L::kSquare, m0, 16 * ks, lane);
       }
     }
+    add_rows(l, turned ? strip : 0, turned ? STRIPS : strip + 1, where, L::kRows, by, by);
   };
-  // acc += rows of dout (of inputs) or of the transposes of dR, W, times the state's slice
-  auto add_state = [&](Accumulators<NS, L::kApart>& acc, int slice, int turned) {
-#pragma unroll 1
-    for (int ks = 0; ks < G::kSlice / 16; ++ks) {
-      uint32_t in[L::kIn][4], l[L::kOwn][4];
+  // rows of dout, or of the transposes of dR, W, times the state's slice
+  auto add_state = [&](int slice, int turned, float f0, float f1) {
+    constexpr int STEPS = G::kSlice / 16;
+    uint32_t l[STEPS][NH][4];
+#pragma unroll
+    for (int ks = 0; ks < STEPS; ++ks) {
       const int k0 = slice * G::kSlice + 16 * ks;
-      if (turned)
 #pragma unroll
-        for (int n = 0; n < L::kOwn; ++n) a_cols<C>(l[n], base + turned + n * DK * C * 2, m0, k0, lane);
-      else
-#pragma unroll
-        for (int n = 0; n < L::kIn; ++n) a_rows<DK>(in[n], base + G::kDout + n * L::kRows, m0, k0, lane);
-#pragma unroll
-      for (int j = 0; j < NS / 2; ++j) {
-        uint32_t x[L::kOwn][1][4];
-#pragma unroll
-        for (int n = 0; n < L::kOwn; ++n) b_cols<DK>(x[n][0], base + G::kState + n * G::kSlice * DK * 2, 16 * j, 16 * ks, lane);
+      for (int n = 0; n < NH; ++n) {
         if (turned)
-          mma_terms(acc, 2 * j, l, x);
+          a_cols<C>(l[ks][n], base + turned + n * G::kTurnedPlane, m0, k0, lane);
         else
-          mma_terms(acc, 2 * j, in, x);
+          a_rows<DK>(l[ks][n], base + G::kDout + n * L::kRows, m0, k0, lane);
       }
     }
+    add_rows(l, 0, STEPS, G::kState, G::kSlicePlane, f0, f1);
   };
-  auto store = [&](const Accumulators<NS, L::kApart>& acc, const Operand& to, bool two) {
+  auto store = [&](const Operand& to, bool two) {
     O* out = static_cast<O*>(to.data) + b * to.sb + h * to.sh + t0 * to.sn;
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
@@ -674,96 +782,98 @@ __global__ void __launch_bounds__(GradLay<T, DK>::kThreads) delta_grads(const __
       if (r >= rows) continue;
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
-        const int c = 8 * n + 2 * (lane & 3);
-        if (c < p.d) store_pair<O>(out + r * to.sn + c, acc.get(n, 2 * f), acc.get(n, 2 * f + 1), two, c + 1 < p.d);
+        const int c = 8 * n + t;
+        if (c < p.d) store_pair<O>(out + r * to.sn + c, acc[n][2 * f], acc[n][2 * f + 1], two, c + 1 < p.d);
       }
     }
   };
 
-  Accumulators<NS, L::kApart> acc;
-  acc.clear();
+  const float in0 = m.inside[row], in1 = m.inside[row + 8];
+  const Scale by_s = scale(kMostS), by_d = scale(kMostD);
   for (int slice = 0; slice < DK / G::kSlice; ++slice) {
-    fill(p.im.s, slice, false);
+    fill(p.im.s, slice, by_s.to);
     __syncthreads();
-    add_state(acc, slice, second ? G::kR : 0);
+    if (second)
+      add_state(slice, G::kR, of_r * by_s.from, of_r * by_s.from);
+    else
+      add_state(slice, 0, p.scale * in0 * m.douts * by_s.from, p.scale * in1 * m.douts * by_s.from);
     __syncthreads();
   }
   {
-    const float in0 = m.inside[row], in1 = m.inside[row + 8];
     float sum[2];
     if (second) {
-      dot_rows(acc, G::kK, sum);
-      weigh(acc, -m.beta[row] * in0, -m.beta[row + 8] * in1);
+      dot_rows(G::kK, m.key, sum);
+      const float b0 = -m.beta[row] * in0, b1 = -m.beta[row + 8] * in1;
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][e] *= e < 2 ? b0 : b1;
       if ((lane & 3) == 0) {
         zk[row] = in0 * sum[0];
         zk[row + 8] = in1 * sum[1];
-        enters[1][row] = -m.beta[row] * in0 * sum[0];
-        enters[1][row + 8] = -m.beta[row + 8] * in1 * sum[1];
+        enters[1][row] = b0 * sum[0];
+        enters[1][row + 8] = b1 * sum[1];
       }
-      add_square(acc, G::kL, false, G::kK);
-      add_square(acc, G::kL, true, G::kK);
+      add_square(G::kL, false, G::kK, of_l * m.key);
+      add_square(G::kL, true, G::kK, of_l * m.key);
     } else {
-      weigh(acc, p.scale * in0, p.scale * in1);
-      dot_rows(acc, G::kQ, sum);
+      dot_rows(G::kQ, m.queries, sum);
       if ((lane & 3) == 0) {
         enters[0][row] = sum[0];
         enters[0][row + 8] = sum[1];
       }
-      add_square(acc, G::kA, false, G::kK);
-      store(acc, a.dq, a.pairs & 1);
-      acc.clear();
+      add_square(G::kA, false, G::kK, of_a * m.key);
+      store(a.dq, a.pairs & 1);
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
     }
   }
   for (int slice = 0; slice < DK / G::kSlice; ++slice) {
-    fill(p.im.ds, slice, true);
+    fill(p.im.ds, slice, by_d.to);
     __syncthreads();
-    if (!second) add_state(acc, slice, G::kW);
+    if (!second) add_state(slice, G::kW, m.after[row] * of_w * by_d.from, m.after[row + 8] * of_w * by_d.from);
     __syncthreads();
   }
-  through += __shfl_xor_sync(~0u, through, 16);
-  through += __shfl_xor_sync(~0u, through, 8);
-  through += __shfl_xor_sync(~0u, through, 4);
-  through += __shfl_xor_sync(~0u, through, 2);
-  through += __shfl_xor_sync(~0u, through, 1);
-  if (lane == 0) both[warp] = through;
   float4* half = reinterpret_cast<float4*>(smem + G::kState) + strip * NS * 32 + lane;
   if (!second) {
-    weigh(acc, m.after[row], m.after[row + 8]);
     float sum[2];
-    dot_rows(acc, G::kK, sum);
+    dot_rows(G::kK, m.key, sum);
     if ((lane & 3) == 0) {
       leaves[row] = sum[0];
       leaves[row + 8] = sum[1];
     }
-    add_square(acc, G::kA, true, G::kQ);
+    add_square(G::kA, true, G::kQ, of_a * m.queries);
 #pragma unroll
-    for (int n = 0; n < NS; ++n) half[32 * n] = make_float4(acc.get(n, 0), acc.get(n, 1), acc.get(n, 2), acc.get(n, 3));
+    for (int n = 0; n < NS; ++n) half[32 * n] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
   }
   __syncthreads();
   if (second) {
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
       const float4 x = half[32 * n];
-      acc.main[n][0] += x.x; acc.main[n][1] += x.y; acc.main[n][2] += x.z; acc.main[n][3] += x.w;
+      acc[n][0] += x.x; acc[n][1] += x.y; acc[n][2] += x.z; acc[n][3] += x.w;
     }
-    store(acc, a.dk, a.pairs & 2);
-  } else if (threadIdx.x < C && static_cast<int>(threadIdx.x) < rows) {
-    const int t = threadIdx.x;
-    float dbeta = 0.0f, dg = crossing[t], all = 0.0f;
+    store(a.dk, a.pairs & 2);
+  }
+  constexpr int PART = C / 4;
+  const int token = threadIdx.x / 4, s0 = (threadIdx.x & 3) * PART;
+  float sum = 0.0f;
 #pragma unroll
-    for (int n = 0; n < TILES; ++n) dbeta += vdot[n][t];
-    dbeta -= zk[t] + rows_g[t];
-    float sum = 0.0f;
-    for (int s = C - 1; s >= t; --s) sum += enters[0][s] + enters[1][s];
-    dg += sum;
-    sum = 0.0f;
-    for (int s = 0; s < t; ++s) sum += leaves[s];
-    dg += sum;
+  for (int i = 0; i < PART; ++i) sum += s0 + i >= token ? enters[0][s0 + i] + enters[1][s0 + i] : leaves[s0 + i];
+  sum += __shfl_xor_sync(~0u, sum, 1);
+  sum += __shfl_xor_sync(~0u, sum, 2);
+  if ((threadIdx.x & 3) == 0 && token < rows) {
+    float dbeta = 0.0f, all = 0.0f;
+#pragma unroll
+    for (int n = 0; n < TILES; ++n) dbeta += vdot[n][token];
+    dbeta -= zk[token] + rows_g[token];
 #pragma unroll
     for (int n = 0; n < G::kWarps; ++n) all += both[n];
-    dg = fmaf(m.total, all, dg);
-    from_f(static_cast<T*>(a.dg.data) + b * a.dg.sb + h * a.dg.sh + (t0 + t) * a.dg.sn, dg);
-    from_f(static_cast<T*>(a.dbeta.data) + b * a.dbeta.sb + h * a.dbeta.sh + (t0 + t) * a.dbeta.sn, dbeta);
+    const float dg = fmaf(m.total, all, crossing[token] + sum);
+    from_f(static_cast<T*>(a.dg.data) + b * a.dg.sb + h * a.dg.sh + (t0 + token) * a.dg.sn, dg);
+    from_f(static_cast<T*>(a.dbeta.data) + b * a.dbeta.sb + h * a.dbeta.sh + (t0 + token) * a.dbeta.sn, dbeta);
   }
 }
 

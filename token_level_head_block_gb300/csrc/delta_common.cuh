@@ -54,7 +54,8 @@ struct Marks {
   float keys[4];           // the scale of each 16 rows of K^
   float total;             // e^B
   float key;               // the scale of K
-  int32_t any, pad;
+  int32_t any;
+  float inverse, queries, douts, pad[2];   // gradients: the scales of T, Q and dout
   int32_t first[DK];
 };
 
@@ -68,7 +69,7 @@ struct Lay {
   static constexpr int kTiles = C / 16, kSides = DK / 16;          // blocks of a chunk's tokens, of the channels
   static constexpr bool kApart = kIn > 1;
   static constexpr int kRows = C * DK * 2, kSquare = C * C * 2;   // bytes of a plane
-  static constexpr int kInput = kIn * kRows, kInputHalf = kHalves * kRows, kKeys = 2 * kRows, kInverse = kOwn * kSquare;
+  static constexpr int kInput = kIn * kRows, kInputHalf = kHalves * kRows, kKeys = 2 * kRows, kInverse = kHalves * kSquare;
   static constexpr int kScores = kHalves * kSquare, kScoresBack = kChain * kSquare;
   static constexpr int kTokens = C / 8 * kBlock, kState = DK / 8 * kBlock;   // of 16 columns, float32 fragments
   using M = Marks<C, DK>;
@@ -87,7 +88,7 @@ struct Images {
   char* u;              // (T beta V)^T, float32 fragments [ch][C / 8][32]
   char* marks;
   // gradients
-  char *k, *q, *dout, *inverse;   // planes of rows; T
+  char *k, *q, *dout, *inverse;   // planes of rows at a scale each; T
   char* k_rows;         // K as [n = tok][k = ch], blocks [tok][ch]
   char* keys_add;       // T beta e^b K as [k = tok][n = ch], blocks [ch][tok]
   char* q_add;          // Q as [k = tok][n = ch], blocks [ch][tok]
@@ -115,6 +116,11 @@ struct Scale {
 __device__ __forceinline__ Scale scale_of(float most) {
   const uint32_t e = min(max(__float_as_uint(most) >> 23, 1u), 253u);
   return Scale{__uint_as_float((254u - e) << 23), __uint_as_float(e << 23)};
+}
+// The scale of a whole plane of a chunk, from the bits of its largest; with an infinity in it all of it becomes NaN, not zero.
+__device__ __forceinline__ Scale plane_scale(uint32_t most) {
+  const Scale by = scale_of(__uint_as_float(most));
+  return most < 0x7F800000u ? by : Scale{__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u)};
 }
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 p = __floats2half2_rn(lo, hi);
@@ -171,6 +177,13 @@ __device__ __forceinline__ void add_scaled(float (&sum)[MT][NT][4], const uint32
         sum[m][n][2] = fmaf(c[k][m][n][2], f.y, sum[m][n][2]); sum[m][n][3] = fmaf(c[k][m][n][3], f.y, sum[m][n][3]);
       }
     }
+}
+// The same, added to c.
+template <int NA, int NB>
+__device__ __forceinline__ void add_products(float (&c)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4], int half) {
+  if constexpr (NA > 1) mma_half(c, a[1], b[0][2 * half], b[0][2 * half + 1]);
+  if constexpr (NB > 1) mma_half(c, a[0], b[1][2 * half], b[1][2 * half + 1]);
+  mma_half(c, a[0], b[0][2 * half], b[0][2 * half + 1]);
 }
 // The largest size among the four lanes of a row.
 __device__ __forceinline__ float over_row(float m) {

@@ -34,19 +34,19 @@ namespace {
 
 // Rows of one operand to planes of terms; zeros behind the last token and channel.
 // WATCH 1: the first row with a value that is not finite to `first`; 2: each column's; such values are left as zeros.
-template <typename T, int DK, int THREADS, int WATCH>
+// MOST: the largest size to *most.
+template <typename T, int DK, int THREADS, int WATCH, bool MOST = (WATCH == 1)>
 __device__ __forceinline__ void load_rows(char* dst, const T* src, int64_t sn, int rows, int d, bool wide, int32_t* first,
                                           uint32_t* most = nullptr) {
   float largest = 0.0f;
   using L = Lay<T, DK>;
   constexpr int C = L::C;
   auto watch = [&](float x, int r, int c) {
-    if (WATCH == 0) return x;
-    if (!finite(x)) {
+    if (WATCH != 0 && !finite(x)) {
       atomicMin(first + (WATCH == 2 ? c : 0), r);
       return 0.0f;
     }
-    if (WATCH == 1) largest = fmaxf(largest, fabsf(x));
+    if (MOST) largest = fmaxf(largest, fabsf(x));
     return x;
   };
   if (wide) {
@@ -63,14 +63,14 @@ __device__ __forceinline__ void load_rows(char* dst, const T* src, int64_t sn, i
       const int i = threadIdx.x + THREADS * j, r = i / (DK / E), c = E * (i % (DK / E));
       uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
       if constexpr (sizeof(T) == 2) {
-        if (WATCH != 0) {
+        if (WATCH != 0 || MOST) {
           uint32_t bad = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {   // 0 times what is not finite is NaN
             const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), __floats2bfloat162_rn(0.0f, 0.0f));
             bad |= *reinterpret_cast<const uint32_t*>(&z);
           }
-          if (WATCH == 1 || (bad & 0x7FFF7FFFu))
+          if (MOST || (bad & 0x7FFF7FFFu))
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = pack(watch(low(w[e]), r, c + 2 * e), watch(high(w[e]), r, c + 2 * e + 1));
         }
@@ -98,7 +98,7 @@ __device__ __forceinline__ void load_rows(char* dst, const T* src, int64_t sn, i
         *reinterpret_cast<uint32_t*>(dst + n * L::kRows + unit_at<DK>(r, c >> 3) + (c & 7) * 2) = t[n];
     }
   }
-  if (WATCH == 1) {
+  if (MOST) {
     const uint32_t all = __reduce_max_sync(~0u, __float_as_uint(largest));
     if ((threadIdx.x & 31) == 0) atomicMax(most, all);
   }
@@ -125,6 +125,29 @@ struct Prepare {
   // K^ on the way, float32: Q's place and what is behind it
   static constexpr int kKeep = kQ, kBytes = kQ + std::max(L::kInput, C * DK * 4);
 };
+
+// Planes of terms, scaled, as planes of fp16.
+template <typename T, int DK>
+__device__ __forceinline__ void plane_halves(char* to, const char* from, float by, int thread, int threads) {
+  using L = Lay<T, DK>;
+  for (int i = 16 * thread; i < L::kRows; i += 16 * threads) {
+    uint32_t x[L::kIn][4], y[L::kHalves][4];
+#pragma unroll
+    for (int n = 0; n < L::kIn; ++n) {
+      const uint4 q = *reinterpret_cast<const uint4*>(from + n * L::kRows + i);
+      x[n][0] = q.x; x[n][1] = q.y; x[n][2] = q.z; x[n][3] = q.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t t[L::kHalves];
+      to_halves<L::kIn, L::kHalves>(x, e, by, t);
+#pragma unroll
+      for (int n = 0; n < L::kHalves; ++n) y[n][e] = t[n];
+    }
+#pragma unroll
+    for (int n = 0; n < L::kHalves; ++n) *reinterpret_cast<uint4*>(to + n * L::kRows + i) = make_uint4(y[n][0], y[n][1], y[n][2], y[n][3]);
+  }
+}
 
 // Decays between the tokens of a chunk: D_ij = e^{b_i - b_j} = row_i col_j for j in front of i's block of 16, with
 // row_i = e^{b_i - m}, col_j = e^{m - b_j}, m the sum in front of the block; neither exceeds 1.
@@ -209,7 +232,7 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
   __shared__ __align__(16) typename L::M m;
   __shared__ __align__(16) Decays<C> w;
   __shared__ int32_t bad_key, bad;
-  __shared__ uint32_t most;   // |k|
+  __shared__ uint32_t most, most_q, most_o, most_t;   // |k|, and for the gradients |q|, |dout|, |T|
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t chunk = blockIdx.x % p.chunks;
   const int64_t bh = blockIdx.x / p.chunks, b = bh / p.H, h = bh % p.H, times = p.H / p.Hk, hk = h / times;
@@ -225,7 +248,7 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
   for (int i = threadIdx.x; i < DK; i += THREADS) m.first[i] = C;
   if (threadIdx.x == 0) {
     bad_key = bad = C;
-    most = 0;
+    most = most_q = most_o = most_t = 0;
   }
   __syncthreads();
 
@@ -244,7 +267,7 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
     }
   }
   load_rows<T, DK, THREADS, 1>(smem + P::kK, from(p.k, hk), p.k.sn, rows, p.d, p.wide & kWideK, &bad_key, &most);
-  load_rows<T, DK, THREADS, 0>(smem + P::kQ, from(p.q, hk), p.q.sn, rows, p.d, p.wide & kWideQ, nullptr);
+  load_rows<T, DK, THREADS, 0, GRAD>(smem + P::kQ, from(p.q, hk), p.q.sn, rows, p.d, p.wide & kWideQ, nullptr, &most_q);
   load_rows<T, DK, THREADS, 2>(smem + P::kV, from(p.v, h), p.v.sn, rows, p.d, p.wide & kWideV, m.first);
   __syncthreads();
   if (warp == 0) {
@@ -501,11 +524,10 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
         }
       }
     }
-    if (GRAD)
-      for (int i = 16 * (threadIdx.x - THREADS / 2); i < L::kInput; i += 8 * THREADS) {
-        *reinterpret_cast<uint4*>(p.im.k + at_key * L::kInput + i) = *reinterpret_cast<const uint4*>(smem + P::kK + i);
-        *reinterpret_cast<uint4*>(p.im.q + at_key * L::kInput + i) = *reinterpret_cast<const uint4*>(smem + P::kQ + i);
-      }
+    if (GRAD) {
+      plane_halves<T, DK>(p.im.k + at_key * L::kInputHalf, smem + P::kK, by, threadIdx.x - THREADS / 2, THREADS / 2);
+      plane_halves<T, DK>(p.im.q + at_key * L::kInputHalf, smem + P::kQ, plane_scale(most_q).to, threadIdx.x - THREADS / 2, THREADS / 2);
+    }
   }
   __syncthreads();
   {
@@ -616,21 +638,34 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
     }
   }
   if (GRAD) {   // T, and the rows of dout in V's place
-    for (int i = threadIdx.x; i < C * C / 2; i += THREADS) {
-      const int r = i / (C / 2), c = 2 * (i % (C / 2));
-      if (c > (r | 15)) continue;
-      const float2 x = pair_at<PITCH>(inv, r, c);
-      uint32_t t[L::kOwn];
-      split<L::kOwn>(x.x, x.y, t);
+    float largest = 0.0f;
+    auto each = [&](auto use) {
+      for (int i = threadIdx.x; i < C * C / 2; i += THREADS) {
+        const int r = i / (C / 2), c = 2 * (i % (C / 2));
+        if (c <= (r | 15)) use(r, c, pair_at<PITCH>(inv, r, c));
+      }
+    };
+    each([&](int, int, float2 x) { largest = fmaxf(largest, fmaxf(fabsf(x.x), fabsf(x.y))); });
+    largest = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(largest)));
+    if (lane == 0) atomicMax(&most_t, __float_as_uint(largest));
+    __syncthreads();
+    load_rows<T, DK, THREADS, 0, true>(smem + P::kV, from(p.dout, h), p.dout.sn, rows, p.d, p.wide & kWideDout, nullptr, &most_o);
+    const Scale by = plane_scale(most_t);
+    each([&](int r, int c, float2 x) {
+      uint32_t t[L::kHalves];
+      halves<L::kHalves>(x.x * by.to, x.y * by.to, t);
 #pragma unroll
-      for (int n = 0; n < L::kOwn; ++n)
+      for (int n = 0; n < L::kHalves; ++n)
         *reinterpret_cast<uint32_t*>(p.im.inverse + at * L::kInverse + n * L::kSquare + unit_at<C>(r, c >> 3) + (c & 7) * 2) = t[n];
+    });
+    __syncthreads();
+    const Scale by_o = plane_scale(most_o);
+    if (threadIdx.x == 0) {
+      m.inverse = by.from;
+      m.queries = plane_scale(most_q).from;
+      m.douts = by_o.from;
     }
-    __syncthreads();
-    load_rows<T, DK, THREADS, 0>(smem + P::kV, from(p.dout, h), p.dout.sn, rows, p.d, p.wide & kWideDout, nullptr);
-    __syncthreads();
-    for (int i = 16 * threadIdx.x; i < L::kInput; i += 16 * THREADS)
-      *reinterpret_cast<uint4*>(p.im.dout + at * L::kInput + i) = *reinterpret_cast<const uint4*>(smem + P::kV + i);
+    plane_halves<T, DK>(p.im.dout + at * L::kInputHalf, smem + P::kV, by_o.to, threadIdx.x, THREADS);
     for (int i = warp; i < SIDES * TILES; i += 2 * TILES)
 #pragma unroll
       for (int n = 0; n < L::kIn; ++n) {
@@ -1091,9 +1126,9 @@ size_t lay_out_as(int64_t heads, int64_t keys, bool grad, char* base, Images* im
     im->scores = take(heads * L::kScores);
     return used;
   }
-  im->k = take(keys * L::kInput);
-  im->q = take(keys * L::kInput);
-  im->dout = take(heads * L::kInput);
+  im->k = take(keys * L::kInputHalf);
+  im->q = take(keys * L::kInputHalf);
+  im->dout = take(heads * L::kInputHalf);
   im->inverse = take(heads * L::kInverse);
   im->k_rows = take(keys * L::kInputHalf);
   im->keys_add = take(heads * L::kKeys);
