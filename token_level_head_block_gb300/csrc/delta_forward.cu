@@ -32,12 +32,28 @@ using namespace delta;
 
 namespace {
 
+// A thread's share of one operand's rows, where they are 16-byte units: asked for together, before the first is waited for.
+template <typename T, int DK, int THREADS>
+struct Rows {
+  static constexpr int C = Lay<T, DK>::C, E = 16 / sizeof(T), kUnits = C * DK / E, kEach = kUnits / THREADS;
+  static_assert(kUnits % THREADS == 0, "whole passes");
+  uint4 x[kEach];
+  __device__ __forceinline__ void fetch(const T* src, int64_t sn, int rows, int d, bool wide) {
+    if (!wide) return;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int i = threadIdx.x + THREADS * j, r = i / (DK / E), c = E * (i % (DK / E));
+      x[j] = r < rows && c < d ? *reinterpret_cast<const uint4*>(src + r * sn + c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+};
+
 // Rows of one operand to planes of terms; zeros behind the last token and channel.
 // WATCH 1: the first row with a value that is not finite to `first`; 2: each column's; such values are left as zeros.
 // MOST: the largest size to *most.
 template <typename T, int DK, int THREADS, int WATCH, bool MOST = (WATCH == 1)>
-__device__ __forceinline__ void load_rows(char* dst, const T* src, int64_t sn, int rows, int d, bool wide, int32_t* first,
-                                          uint32_t* most = nullptr) {
+__device__ __forceinline__ void load_rows(char* dst, const Rows<T, DK, THREADS>& units, const T* src, int64_t sn, int rows, int d,
+                                          bool wide, int32_t* first, uint32_t* most = nullptr) {
   float largest = 0.0f;
   using L = Lay<T, DK>;
   constexpr int C = L::C;
@@ -50,18 +66,11 @@ __device__ __forceinline__ void load_rows(char* dst, const T* src, int64_t sn, i
     return x;
   };
   if (wide) {
-    constexpr int E = 16 / sizeof(T), kUnits = C * DK / E, kEach = kUnits / THREADS;
-    static_assert(kUnits % THREADS == 0, "whole passes");
-    uint4 x[kEach];
+    using R = Rows<T, DK, THREADS>;
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const int i = threadIdx.x + THREADS * j, r = i / (DK / E), c = E * (i % (DK / E));
-      x[j] = r < rows && c < d ? *reinterpret_cast<const uint4*>(src + r * sn + c) : make_uint4(0u, 0u, 0u, 0u);
-    }
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const int i = threadIdx.x + THREADS * j, r = i / (DK / E), c = E * (i % (DK / E));
-      uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+    for (int j = 0; j < R::kEach; ++j) {
+      const int i = threadIdx.x + THREADS * j, r = i / (DK / R::E), c = R::E * (i % (DK / R::E));
+      uint32_t w[4] = {units.x[j].x, units.x[j].y, units.x[j].z, units.x[j].w};
       if constexpr (sizeof(T) == 2) {
         if (WATCH != 0 || MOST) {
           uint32_t bad = 0;
@@ -245,6 +254,10 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
   const int strip = warp % TILES, m0 = 16 * strip, row = m0 + (lane >> 2);
   const bool second = warp >= TILES;
 
+  Rows<T, DK, THREADS> k_units, q_units, v_units;
+  k_units.fetch(from(p.k, hk), p.k.sn, rows, p.d, p.wide & kWideK);
+  q_units.fetch(from(p.q, hk), p.q.sn, rows, p.d, p.wide & kWideQ);
+  v_units.fetch(from(p.v, h), p.v.sn, rows, p.d, p.wide & kWideV);
   for (int i = threadIdx.x; i < DK; i += THREADS) m.first[i] = C;
   if (threadIdx.x == 0) {
     bad_key = bad = C;
@@ -266,9 +279,9 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
       if (!finite(g[e]) || !finite(beta[e])) atomicMin(&bad, t);
     }
   }
-  load_rows<T, DK, THREADS, 1>(smem + P::kK, from(p.k, hk), p.k.sn, rows, p.d, p.wide & kWideK, &bad_key, &most);
-  load_rows<T, DK, THREADS, 0, GRAD>(smem + P::kQ, from(p.q, hk), p.q.sn, rows, p.d, p.wide & kWideQ, nullptr, &most_q);
-  load_rows<T, DK, THREADS, 2>(smem + P::kV, from(p.v, h), p.v.sn, rows, p.d, p.wide & kWideV, m.first);
+  load_rows<T, DK, THREADS, 1>(smem + P::kK, k_units, from(p.k, hk), p.k.sn, rows, p.d, p.wide & kWideK, &bad_key, &most);
+  load_rows<T, DK, THREADS, 0, GRAD>(smem + P::kQ, q_units, from(p.q, hk), p.q.sn, rows, p.d, p.wide & kWideQ, nullptr, &most_q);
+  load_rows<T, DK, THREADS, 2>(smem + P::kV, v_units, from(p.v, h), p.v.sn, rows, p.d, p.wide & kWideV, m.first);
   __syncthreads();
   if (warp == 0) {
     const int stop = min(bad, bad_key);
@@ -638,6 +651,8 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
     }
   }
   if (GRAD) {   // T, and the rows of dout in V's place
+    Rows<T, DK, THREADS> units;
+    units.fetch(from(p.dout, h), p.dout.sn, rows, p.d, p.wide & kWideDout);
     float largest = 0.0f;
     auto each = [&](auto use) {
       for (int i = threadIdx.x; i < C * C / 2; i += THREADS) {
@@ -649,7 +664,7 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
     largest = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(largest)));
     if (lane == 0) atomicMax(&most_t, __float_as_uint(largest));
     __syncthreads();
-    load_rows<T, DK, THREADS, 0, true>(smem + P::kV, from(p.dout, h), p.dout.sn, rows, p.d, p.wide & kWideDout, nullptr, &most_o);
+    load_rows<T, DK, THREADS, 0, true>(smem + P::kV, units, from(p.dout, h), p.dout.sn, rows, p.d, p.wide & kWideDout, nullptr, &most_o);
     const Scale by = plane_scale(most_t);
     each([&](int r, int c, float2 x) {
       uint32_t t[L::kHalves];
