@@ -170,16 +170,23 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
     };
     load_ahead(0);
     load(0);
-    alive = wait_copies(bar + 2, 0, &g_delta_back_error);
+    if (stall_this_warp()) wait_copies_long(bar, 0, &g_delta_back_error);   // a test's
+    // the chain's copies of chunk i and, ahead, those of chunk j: waited for once more when a wait has given up
+    auto give_up = [&](int i, int j) {
+      alive = false;
+      if (i < count) wait_copies_long(bar + (i & 1), i >> 1 & 1, &g_delta_back_error);
+      if (j < count) wait_copies_long(bar + 2, j & 1, &g_delta_back_error);
+    };
+    if (!wait_copies(bar + 2, 0, &g_delta_back_error)) give_up(0, 0);
     ahead(0);
     __syncwarp();
     load_ahead(1);
     for (int i = 0; i < count; ++i) {
-      alive = alive && wait_copies(bar + (i & 1), i >> 1 & 1, &g_delta_back_error);
+      if (alive && !wait_copies(bar + (i & 1), i >> 1 & 1, &g_delta_back_error)) give_up(i, i + 1);
       sync();   // the chunk's operands, what was formed ahead and the planes of D are there; the chunk before is done with
       load(i + 1);
       if (i + 1 < count) {
-        alive = alive && wait_copies(bar + 2, i + 1 & 1, &g_delta_back_error);
+        if (alive && !wait_copies(bar + 2, i + 1 & 1, &g_delta_back_error)) give_up(i + 1, i + 1);
         ahead(i + 1);
         __syncwarp();
         load_ahead(i + 2);

@@ -232,7 +232,7 @@ __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;"
 __device__ __forceinline__ void wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 // Waits for a phase of a barrier that copies complete on.  Bounded: one that gives up is reported in *error and false for the
-// whole warp, which then asks for no more.
+// whole warp, which then waits (again for so long at most) for the copies that are still in flight and asks for no more.
 static __device__ __noinline__ bool wait_copies_long(uint64_t* bar, uint32_t parity, unsigned int* error) {
   if (stall_this_warp()) {   // a test's: it gives up, and the copies in flight are waited for behind it
     volatile uint32_t none = 0;

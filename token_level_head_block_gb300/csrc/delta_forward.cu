@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
       ptx::fence_mbar_init();
     }
     __syncwarp();
-    bool alive = true;   // no wait has given up
+    int alive = count;   // chunks; -1 - i once the wait for chunk i has given up
     const char* keys = p.im.keys + bh * p.chunks * L::kKeys + own * W::kKeysBytes;
     const char* u = p.im.u + (bh * p.chunks * SIDES + tile0) * L::kTokens + own * W::kUBytes;
     const char* add = p.im.k_add + key * p.chunks * L::kInputHalf + own * W::kAddBytes;
@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
     const uint32_t seen = KEEP ? 0 : (own + 1) * L::kHalves * kBlock;   // scores up to the diagonal
     const uint32_t bytes = W::kKeysBytes + MT * W::kUBytes + (shares ? W::kAddBytes : 0) + W::kQBytes + seen + (own == 0 ? W::kMarkBytes : 0);
     auto load = [&](int i) {
-      if (lane != 0 || i >= count || !alive) return;
+      if (lane != 0 || i >= alive) return;
       char* stage = smem + W::kRing + i % STAGES * W::kStage;
       char* to = stage + own * W::kPair;
       uint64_t* on = bar + i % STAGES;
@@ -793,11 +793,12 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
       marks += L::kMarks;
     };
     for (int i = 0; i < STAGES - 1; ++i) load(i);
+    if (stall_this_warp()) wait_copies_long(bar, 0, &g_delta_error);   // a test's
     T* const out = static_cast<T*>(a.out.data) + b * a.out.sb + h * a.out.sh;
     for (int i = 0; i < count; ++i) {
       const char* stage = smem + W::kRing + i % STAGES * W::kStage;
       const char* st = stage + own * W::kPair;
-      alive = alive && wait_copies(bar + i % STAGES, i / STAGES & 1, &g_delta_error);
+      if (alive >= 0 && !wait_copies(bar + i % STAGES, i / STAGES & 1, &g_delta_error)) alive = -1 - i;
       sync();   // the chunk's operands and the state's planes are there; the chunk before is done with
       load(i + STAGES - 1);
       if constexpr (KEEP) {
@@ -880,6 +881,9 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
         }
       }
     }
+#pragma unroll 1
+    for (int j = -1 - alive; alive < 0 && j < min(-alive - 2 + STAGES, count); ++j)
+      wait_copies_long(bar + j % STAGES, j / STAGES & 1, &g_delta_error);
     return;
   }
 
