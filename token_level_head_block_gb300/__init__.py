@@ -517,14 +517,16 @@ def _heads(x):
     sb, sn, sh, sd = x.stride()
     if sd != 1 and d > 1:
         raise ValueError("the d dimension must be contiguous")
-    return _PACK_TENSOR(x.data_ptr(), _dtype_code(x), 0, B, N, H, d, sb, sn, sh)
+    code = _CODES.get(x.dtype)
+    return _PACK_TENSOR(x.data_ptr(), _dtype_code(x) if code is None else code, 0, B, N, H, d, sb, sn, sh)
 
 
 def _gates(x):
     """mhla_tensor_t of a [B, N, H] tensor of one value per token and head."""
     B, N, H = x.shape
     sb, sn, sh = x.stride()
-    return _PACK_TENSOR(x.data_ptr(), _dtype_code(x), 0, B, N, H, 1, sb, sn, sh)
+    code = _CODES.get(x.dtype)
+    return _PACK_TENSOR(x.data_ptr(), _dtype_code(x) if code is None else code, 0, B, N, H, 1, sb, sn, sh)
 
 
 def _float_array(name, x, shape, like):
@@ -776,14 +778,14 @@ def linear_act_backward_workspace_size(rows, k, n, dtype, activation="none"):
     return n_bytes.value
 
 
-def _dense(name, x, shape, like, code):
-    """Address of a contiguous tensor of this shape, of like's type and device; None for None."""
+def _dense(name, x, shape, dtype, index):
+    """Address of a contiguous tensor of this shape and type on this device; None for None."""
     if x is None:
         return None
-    if tuple(x.shape) != shape or not x.is_contiguous() or _dtype_code(x) != code:
-        raise ValueError(f"{name} must be a contiguous {like.dtype} tensor of shape {list(shape)}")
-    if x.get_device() != like.get_device():
-        raise ValueError(f"{name} is on {x.device}, not on {like.device}")
+    if x.shape != shape or x.dtype != dtype or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+    if x.get_device() != index:
+        raise ValueError(f"{name} is on {x.device}, not on cuda:{index}")
     return x.data_ptr()
 
 
@@ -792,10 +794,11 @@ def _linear_sizes(x, w, activation):
         raise ValueError(f"unknown activation {activation!r}")
     if w.dim() != 2 or x.dim() < 1 or x.shape[-1] != w.shape[1]:
         raise ValueError(f"x {list(x.shape)} does not meet w {list(w.shape)}")
-    if x.get_device() < 0:
+    index = x.get_device()
+    if index < 0:
         raise ValueError("expected CUDA tensors")
     n, k = w.shape
-    return x.numel() // k if k else 0, k, n, _dtype_code(x)
+    return x.numel() // k if k else 0, k, n, _dtype_code(x), x.dtype, index
 
 
 def linear_act(x, w, bias=None, activation="none", residual=None, out=None, pre=None, workspace=None, stream=None):
@@ -803,17 +806,17 @@ def linear_act(x, w, bias=None, activation="none", residual=None, out=None, pre=
     w [n, k], bias [n], residual [..., n] of its type.  ``activation``: none, relu, gelu, gelu_tanh
     or silu.  ``pre`` ([..., n]), when given, receives x w^T + bias.  Returns ``out``, which may be
     residual.  ``stream`` as for ``gated_forward``."""
-    import torch
     if stream is not None:
         with _on(stream, x):
             return linear_act(x, w, bias, activation, residual, out, pre, workspace)
-    rows, k, n, code = _linear_sizes(x, w, activation)
+    rows, k, n, code, dtype, index = _linear_sizes(x, w, activation)
     shape = (*x.shape[:-1], n)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
-    args = (_dense("x", x, tuple(x.shape), x, code), _dense("w", w, (n, k), x, code), _dense("bias", bias, (n,), x, code),
-            ACTIVATIONS[activation], _dense("residual", residual, shape, x, code), _dense("pre", pre, shape, x, code),
-            _dense("out", out, shape, x, code), rows, k, n, code)
+        import torch
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+    args = (_dense("x", x, x.shape, dtype, index), _dense("w", w, (n, k), dtype, index), _dense("bias", bias, (n,), dtype, index),
+            ACTIVATIONS[activation], _dense("residual", residual, shape, dtype, index), _dense("pre", pre, shape, dtype, index),
+            _dense("out", out, shape, dtype, index), rows, k, n, code)
     L = lib()
     _launch("mhla_linear_act", L.mhla_linear_act, args, x, workspace,
             lambda: _size(L.mhla_linear_act_workspace_size, "mhla_linear_act_workspace_size", rows, k, n, code))
@@ -829,20 +832,21 @@ def linear_act_backward(x, w, dout, activation="none", pre=None, bias=True, dx=N
     if stream is not None:
         with _on(stream, x):
             return linear_act_backward(x, w, dout, activation, pre, bias, dx, dw, dbias, workspace)
-    rows, k, n, code = _linear_sizes(x, w, activation)
+    rows, k, n, code, dtype, index = _linear_sizes(x, w, activation)
     shape = (*x.shape[:-1], n)
     if activation == "none":
         pre = None
     elif pre is None:
         raise ValueError(f"{activation} needs pre")
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx
-    dw = torch.empty(w.shape, dtype=w.dtype, device=x.device) if dw is None else dw
-    if bias and dbias is None:
-        dbias = torch.empty((n,), dtype=x.dtype, device=x.device)
     act = ACTIVATIONS[activation]
-    args = (_dense("x", x, tuple(x.shape), x, code), _dense("w", w, (n, k), x, code), _dense("dout", dout, shape, x, code),
-            _dense("pre", pre, shape, x, code), act, _dense("dx", dx, tuple(x.shape), x, code), _dense("dw", dw, (n, k), x, code),
-            _dense("dbias", dbias, (n,), x, code) if bias else None, rows, k, n, code)
+    args = (_dense("x", x, x.shape, dtype, index), _dense("w", w, (n, k), dtype, index), _dense("dout", dout, shape, dtype, index),
+            _dense("pre", pre, shape, dtype, index), act)
+    dx = torch.empty_like(x) if dx is None else dx
+    dw = torch.empty_like(w) if dw is None else dw
+    if bias and dbias is None:
+        dbias = torch.empty(n, dtype=dtype, device=x.device)
+    args += (_dense("dx", dx, x.shape, dtype, index), _dense("dw", dw, (n, k), dtype, index),
+             _dense("dbias", dbias, (n,), dtype, index) if bias else None, rows, k, n, code)
     L = lib()
     _launch("mhla_linear_act_backward", L.mhla_linear_act_backward, args, x, workspace,
             lambda: _size(L.mhla_linear_act_backward_workspace_size, "mhla_linear_act_backward_workspace_size", rows, k, n,
