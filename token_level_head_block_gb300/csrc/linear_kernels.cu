@@ -582,10 +582,17 @@ struct Planes {
   int32_t act;
 };
 
+// Up to three matrices at once: a launch costs more than a small one of them.
+struct PlaneSet {
+  Planes of[3];
+};
+
 // A thread has VEC columns; 32 threads side by side, eight rows at once.
 template <int TERMS, int VEC>
-__global__ void __launch_bounds__(256) linear_planes(const __grid_constant__ Planes p) {
+__global__ void __launch_bounds__(256) linear_planes(const __grid_constant__ PlaneSet set) {
   __shared__ float part[8][32 * VEC];
+  const Planes& p = set.of[blockIdx.z];
+  if (static_cast<int64_t>(blockIdx.x) * 32 * VEC >= p.cols || blockIdx.y * p.block_rows >= p.rows) return;
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + x) * VEC;
   const int64_t first = blockIdx.y * p.block_rows, last = min(p.rows, first + p.block_rows);
@@ -889,23 +896,33 @@ int run_product(const char* name, const Matrix& a, bool a_major, const Matrix& b
 // Columns a thread of the planes' kernel has: 16 bytes where rows are a multiple of that.
 int plane_vec(int64_t cols, int dtype) { return dtype == MHLA_BF16 ? (cols % 8 == 0 ? 8 : 1) : cols % 4 == 0 ? 4 : 1; }
 
-int run_planes(Planes p, int dtype, int64_t row_blocks, cudaStream_t s) {
-  p.block_rows = (p.rows + row_blocks - 1) / row_blocks;
-  const int vec = plane_vec(p.cols, dtype);
-  const int64_t wide = 32 * vec;
-  const dim3 grid(static_cast<unsigned>((p.cols + wide - 1) / wide), static_cast<unsigned>(row_blocks));
-  KernelTimer timer("linear_planes", s);
-  if (dtype == MHLA_BF16) {
-    if (vec > 1) linear_planes<1, 8><<<grid, 256, 0, s>>>(p);
-    else linear_planes<1, 1><<<grid, 256, 0, s>>>(p);
-  } else {
-    if (vec > 1) linear_planes<3, 4><<<grid, 256, 0, s>>>(p);
-    else linear_planes<3, 1><<<grid, 256, 0, s>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
-}
+int64_t plane_columns(const Planes& p, int vec) { return (p.cols + 32 * vec - 1) / (32 * vec); }
 
-// Blocks of rows of the planes' kernel: enough CTAs for the machine, 32 rows each at least.
+// n matrices; those that take their columns the same way in one launch.
+int run_planes(const Planes* jobs, int n, int dtype, cudaStream_t s) {
+  const int wide = dtype == MHLA_BF16 ? 8 : 4;
+  for (int vec : {wide, 1}) {
+    PlaneSet set = {};
+    dim3 grid(0, 0, 0);
+    for (int i = 0; i < n; ++i) {
+      if (plane_vec(jobs[i].cols, dtype) != vec) continue;
+      set.of[grid.z++] = jobs[i];
+      grid.x = std::max(grid.x, static_cast<unsigned>(plane_columns(jobs[i], vec)));
+      grid.y = std::max(grid.y, static_cast<unsigned>((jobs[i].rows + jobs[i].block_rows - 1) / jobs[i].block_rows));
+    }
+    if (grid.z == 0) continue;
+    KernelTimer timer("linear_planes", s);
+    if (dtype == MHLA_BF16) {
+      if (vec > 1) linear_planes<1, 8><<<grid, 256, 0, s>>>(set);
+      else linear_planes<1, 1><<<grid, 256, 0, s>>>(set);
+    } else {
+      if (vec > 1) linear_planes<3, 4><<<grid, 256, 0, s>>>(set);
+      else linear_planes<3, 1><<<grid, 256, 0, s>>>(set);
+    }
+    if (cudaGetLastError() != cudaSuccess) return MHLA_ERR_CUDA;
+  }
+  return MHLA_OK;
+}
 int64_t blocks_of_rows(int64_t rows, int64_t cols, int dtype) {
   const int64_t wide = 32 * plane_vec(cols, dtype), across = (cols + wide - 1) / wide;
   int64_t n = std::max<int64_t>(1, std::min<int64_t>((rows + 31) / 32, (8 * kSms + across - 1) / across));
@@ -914,18 +931,18 @@ int64_t blocks_of_rows(int64_t rows, int64_t cols, int dtype) {
 }
 
 // The matrix as the product reads it: as it lies, or laid out at *ws.
-int lay_matrix(const void* x, int64_t rows, int64_t cols, int dtype, char** ws, Matrix* m, cudaStream_t s) {
-  if (direct(cols, dtype)) {
-    *m = Matrix{x, rows, cols, cols};
-    return MHLA_OK;
-  }
-  Planes p = {};
+// A matrix as it lies, or one more of the n to be laid out.
+Matrix lay_matrix(const void* x, int64_t rows, int64_t cols, int dtype, char** ws, Planes* jobs, int* n) {
+  if (direct(cols, dtype)) return Matrix{x, rows, cols, cols};
+  Planes& p = jobs[(*n)++];
+  p = Planes{};
   p.src = x;
   p.dst = reinterpret_cast<__nv_bfloat16*>(*ws);
   p.rows = rows; p.cols = cols; p.pitch = plane_pitch(cols);
-  *m = Matrix{*ws, rows, cols, p.pitch};
+  const int64_t blocks = blocks_of_rows(rows, cols, dtype);
+  p.block_rows = (rows + blocks - 1) / blocks;
   *ws += plane_bytes(rows, cols, dtype);
-  return run_planes(p, dtype, blocks_of_rows(rows, cols, dtype), s);
+  return Matrix{p.dst, rows, cols, p.pitch};
 }
 size_t lay_bytes(int64_t rows, int64_t cols, int dtype) { return direct(cols, dtype) ? 0 : plane_bytes(rows, cols, dtype); }
 
@@ -969,9 +986,10 @@ int launch_linear_act(const LinearProblem& p, const void* bias, const void* resi
     return cudaGetLastError() == cudaSuccess ? MHLA_OK : MHLA_ERR_CUDA;
   }
   char* ws = static_cast<char*>(workspace);
-  Matrix x, w;
-  int rc = lay_matrix(p.x, p.rows, p.k, p.dtype, &ws, &x, s);
-  if (rc == MHLA_OK) rc = lay_matrix(p.w, p.n, p.k, p.dtype, &ws, &w, s);
+  Planes jobs[2];
+  int n = 0;
+  const Matrix x = lay_matrix(p.x, p.rows, p.k, p.dtype, &ws, jobs, &n), w = lay_matrix(p.w, p.n, p.k, p.dtype, &ws, jobs, &n);
+  const int rc = run_planes(jobs, n, p.dtype, s);
   return rc == MHLA_OK ? run_product("linear_gemm", x, false, w, false, p.rows, p.n, p.k, p.dtype, f, ws, s) : rc;
 }
 
@@ -989,13 +1007,15 @@ int launch_linear_act_backward(const LinearProblem& p, const void* dout, const v
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool f32 = p.dtype != MHLA_BF16, plain = p.act == MHLA_ACT_NONE && direct(p.n, p.dtype);
   char* ws = static_cast<char*>(workspace);
-  Matrix dz = {dout, p.rows, p.n, p.n}, x, w;
+  Matrix dz = {dout, p.rows, p.n, p.n}, x = {}, w = {};
+  Planes jobs[3];
+  int n = 0;
   const int64_t blocks = blocks_of_rows(p.rows, p.n, p.dtype);
   float* sums = reinterpret_cast<float*>(ws);
   ws += align_up(static_cast<size_t>(blocks * p.n) * 4);
-  int rc = MHLA_OK;
   if (!plain || dbias) {
-    Planes z = {};
+    Planes& z = jobs[n++];
+    z = Planes{};
     z.src = dout;
     z.pre = p.act == MHLA_ACT_NONE ? nullptr : pre;
     z.act = p.act;
@@ -1006,19 +1026,20 @@ int launch_linear_act_backward(const LinearProblem& p, const void* dout, const v
       dz = Matrix{ws, p.rows, p.n, z.pitch};
       ws += plane_bytes(p.rows, p.n, p.dtype);
     }
-    rc = run_planes(z, p.dtype, blocks, s);
-    if (rc == MHLA_OK && dbias) {
-      KernelTimer timer("linear_column_sums", s);
-      const unsigned grid = static_cast<unsigned>((p.n + 7) / 8);
-      if (f32)
-        linear_column_sums<true><<<grid, 256, 0, s>>>(sums, dbias, p.n, static_cast<int32_t>(blocks));
-      else
-        linear_column_sums<false><<<grid, 256, 0, s>>>(sums, dbias, p.n, static_cast<int32_t>(blocks));
-      if (cudaGetLastError() != cudaSuccess) rc = MHLA_ERR_CUDA;
-    }
+    z.block_rows = (p.rows + blocks - 1) / blocks;
   }
-  if (rc == MHLA_OK && dw) rc = lay_matrix(p.x, p.rows, p.k, p.dtype, &ws, &x, s);
-  if (rc == MHLA_OK && dx) rc = lay_matrix(p.w, p.n, p.k, p.dtype, &ws, &w, s);
+  if (dw) x = lay_matrix(p.x, p.rows, p.k, p.dtype, &ws, jobs, &n);
+  if (dx) w = lay_matrix(p.w, p.n, p.k, p.dtype, &ws, jobs, &n);
+  int rc = run_planes(jobs, n, p.dtype, s);
+  if (rc == MHLA_OK && dbias) {
+    KernelTimer timer("linear_column_sums", s);
+    const unsigned grid = static_cast<unsigned>((p.n + 7) / 8);
+    if (f32)
+      linear_column_sums<true><<<grid, 256, 0, s>>>(sums, dbias, p.n, static_cast<int32_t>(blocks));
+    else
+      linear_column_sums<false><<<grid, 256, 0, s>>>(sums, dbias, p.n, static_cast<int32_t>(blocks));
+    if (cudaGetLastError() != cudaSuccess) rc = MHLA_ERR_CUDA;
+  }
   Finish f = {};
   f.act = MHLA_ACT_NONE;
   f.quads = p.k % 4 == 0;
