@@ -155,6 +155,15 @@ def test_backward(B, N, Hk, times, d, dtype, state):
     check_backward(x, dtype, d ** -0.5, run_backward(x, d ** -0.5))
 
 
+# more tiles of 16 columns than SMs (twice as many in the last): a CTA takes two tiles, the last one of 48 channels a half
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,N,Hk,times,d", [(3, 150, 7, 2, 64), (4, 70, 13, 1, 48), (5, 70, 4, 4, 60), (2, 90, 40, 1, 32)])
+def test_many_heads(B, N, Hk, times, d, dtype):
+    x = draw(N + d, B, N, Hk, times, d, dtype)
+    check_forward(x, dtype, d ** -0.5, *run_forward(x, d ** -0.5))
+    check_backward(x, dtype, d ** -0.5, run_backward(x, d ** -0.5))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,Hk,times,d", [(1, 1, 1, 64), (3, 2, 2, 64), (2, 3, 1, 48), (1, 2, 1, 7), (2, 1, 3, 128), (1, 1, 1, 1),
                                           (2, 2, 1, 30)])

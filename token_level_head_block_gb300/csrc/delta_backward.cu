@@ -932,8 +932,8 @@ int grads_as(const GradArgs& a, int64_t BH, cudaStream_t s) {
 template <typename T, int DK>
 int run_as(const BackArgs& b, const GradArgs& g, int64_t BH, bool shared, cudaStream_t s) {
   int rc;
-  if constexpr (DK <= 64)
-    rc = two_tiles(BH, b.c.d) ? back_as<T, DK, 2>(b, BH, s) : back_as<T, DK, 1>(b, BH, s);
+  if constexpr (DK == 64)
+    rc = two_tiles(BH, b.c.d, sizeof(T) == 2 ? kSms : 2 * kSms) ? back_as<T, DK, 2>(b, BH, s) : back_as<T, DK, 1>(b, BH, s);
   else
     rc = back_as<T, DK, 1>(b, BH, s);
   if (rc != MHLA_OK) return rc;

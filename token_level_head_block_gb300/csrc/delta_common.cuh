@@ -279,8 +279,8 @@ int launch_prepare(const Common& c, int64_t BH, int dtype, bool grad, cudaStream
 int launch_scan(const ScanArgs& a, int64_t BH, int dtype, bool keep, cudaStream_t s);
 size_t lay_out(const DeltaProblem& p, bool grad, char* base, Images* im);
 Common common(const DeltaProblem& p, const Operand* dout);
-// Whether a scan's CTA takes 32 columns of the state or 16 (wider heads always do): 16 where all of them run at once.
-bool two_tiles(int64_t BH, int d);
+// Whether a chain's CTA takes 32 columns of the state (heads of 33 to 64 channels) or 16, as the others always do.
+bool two_tiles(int64_t BH, int d, int64_t most);
 bool pairs_fit(const Operand& o, int d, int dtype);
 
 }  // namespace delta

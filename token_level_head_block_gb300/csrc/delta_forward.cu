@@ -1104,8 +1104,8 @@ int scan_as(const ScanArgs& a, int64_t BH, cudaStream_t s) {
 
 template <typename T, int DK>
 int scan_for(const ScanArgs& a, int64_t BH, bool keep, cudaStream_t s) {
-  if constexpr (DK <= 64)
-    if (two_tiles(BH, a.c.d)) return keep ? scan_as<T, DK, 2, true>(a, BH, s) : scan_as<T, DK, 2, false>(a, BH, s);
+  if constexpr (DK == 64 && sizeof(T) == 2)
+    if (two_tiles(BH, a.c.d, kSms)) return keep ? scan_as<T, DK, 2, true>(a, BH, s) : scan_as<T, DK, 2, false>(a, BH, s);
   return keep ? scan_as<T, DK, 1, true>(a, BH, s) : scan_as<T, DK, 1, false>(a, BH, s);
 }
 
@@ -1180,7 +1180,12 @@ int64_t delta_chunks(const DeltaProblem& p) {
 
 namespace delta {
 
-bool two_tiles(int64_t BH, int d) { return BH * ((d + 15) / 16) > kSms; }
+// Measured, bf16 at 4096 tokens (scan / gradients' chain, us, one tile against two): 192 tiles of d = 64 149 / 186 against 106 /
+// 142, 384 of them 222 / 277 against 205 / 278, but 128 of them, which all run at once, 78 / 97 against 104 / 143; d = 32, where
+// several CTAs of one tile fit on an SM, 192 tiles 87 / 131 against 85 / 152, 384 of 2048 tokens 78 / 117 against 86 / 154.  float32 at 2048
+// tokens, d = 64: 192 tiles 78 / 109 against 88 / 136, 384 of them 148 / 211 against 168 / 166.  So the scan takes two for bf16 alone, and
+// the gradients' chain from `most` = as many tiles as there are SMs on for bf16, twice as many for float32.
+bool two_tiles(int64_t BH, int d, int64_t most) { return d > 32 && BH * ((d + 15) / 16) > most; }
 
 int launch_prepare(const Common& c, int64_t BH, int dtype, bool grad, cudaStream_t s) {
   return dtype == MHLA_BF16 ? prepare_type<__nv_bfloat16>(c, BH, grad, s) : prepare_type<float>(c, BH, grad, s);

@@ -946,9 +946,15 @@ Matrix lay_matrix(const void* x, int64_t rows, int64_t cols, int dtype, char** w
 }
 size_t lay_bytes(int64_t rows, int64_t cols, int dtype) { return direct(cols, dtype) ? 0 : plane_bytes(rows, cols, dtype); }
 
-// Rows that linear_rows and linear_dots take.
-constexpr int64_t kFewRows = 64, kFewDots = 8;
-bool few_rows(const LinearProblem& p) { return p.rows <= (direct(p.k, p.dtype) ? kFewRows : kFewDots); }
+// Whether linear_rows (or linear_dots) takes the call: w is read once either way, but linear_gemm is at 8 to 14 us whatever the
+// rows, and linear_rows grows with rows x k.  Measured, bf16, us, linear_rows against linear_gemm for k x n: 8 rows 768 x 2304 3.2 and 9.3,
+// 2304 x 768 4.3 and 8.6, 4096 x 4096 6.5 and 12.9; 16 rows 3.4 and 9.4, 5.7 and 8.6, 9.5 and 13.0; 32 rows 4.7 and 9.4, 9.1 and 8.3, 15.8 and
+// 13.5; 64 rows 5.2 and 9.4, 9.2 and 8.3, 29.5 and 13.6.  linear_dots, float32, against laying out and linear_gemm, 768 x 2304 and 333 x 201: 1 row
+// 7.2 and 17.2, 4.4 and 10.9; 8 rows 15.8 and 16.0, 7.5 and 10.9; 32 rows 30.3 and 16.0, 7.5 and 11.4.
+constexpr int64_t kFewRows = 64, kFewProducts = 65536, kFewDots = 8;
+bool few_rows(const LinearProblem& p) {
+  return p.rows <= kFewDots || (direct(p.k, p.dtype) && p.rows <= kFewRows && p.rows * p.k <= kFewProducts);
+}
 
 template <int GROUPS>
 int run_rows(const LinearProblem& p, const Finish& f, cudaStream_t s) {
