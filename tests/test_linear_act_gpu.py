@@ -120,6 +120,32 @@ def test_backward(shape, dtype, act, bias):
     check_backward(x, dtype, act, pre, got, bias)
 
 
+# what the small ones above do not reach: pairs of CTAs on tiles of 256 rows, each width of tile, the long axis in parts
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(300, 768, 8192), (700, 200, 4096), (300, 200, 8192), (129, 65536, 200), (129, 65536, 192),
+                                   (129, 65536, 100), (65, 65536, 384), (65, 65536, 1000), (65, 65536, 192)], ids=str)
+def test_forward_of_every_cutting(shape, dtype):
+    x = draw(sum(shape), *shape, dtype)
+    g = {n: t.to(DEV) for n, t in x.items()}
+    pre = torch.empty(shape[0], shape[2], dtype=DT[dtype], device=DEV)
+    out = mhla.linear_act(g["x"], g["w"], g["bias"], "silu", g["residual"], pre=pre)
+    torch.cuda.synchronize()
+    assert mhla.device_status() == 0
+    check(x, dtype, "silu", True, True, out, pre)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(300, 8192, 768), (129, 8192, 8), (768, 8192, 300), (129, 192, 65536), (65536, 192, 129),
+                                   (65536, 100, 129)], ids=str)
+def test_backward_of_every_cutting(shape, dtype):
+    x = draw(sum(shape) + 1, *shape, dtype)
+    g = {n: t.to(DEV) for n, t in x.items()}
+    got = mhla.linear_act_backward(g["x"], g["w"], g["dout"])
+    torch.cuda.synchronize()
+    assert mhla.device_status() == 0
+    check_backward(x, dtype, "none", None, got)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("act", ["relu", "gelu_tanh"])
 def test_slopes(act, dtype):
