@@ -577,14 +577,17 @@ mhla_status_t mhla_gated_step(const mhla_tensor_t* q, const mhla_tensor_t* k, co
  *   the state as it is.
  * The states and every sum are float32 or wider; bf16 results are rounded once.
  * Chunks of 64 tokens (float32: 32) on the tensor cores.  A chunk is a
- * triangular solve and products, and enters the tensor cores as sums of bf16 terms:
- * bf16 calls use two (2^-16) and one for the scores within a chunk, which reach
- * bf16 outputs alone; float32 calls three (2^-24).  The same call gives the same bits.
+ * triangular solve and products.  What reaches the state enters the tensor cores as
+ * three bf16 terms (2^-24) or as two of fp16 at the scale of its block (2^-22 of a
+ * value, 2^-25 of the block's largest); what only reaches bf16 outputs as one (2^-11).
+ * The same call gives the same bits.
  * From the first token whose k, g or beta is not finite (g: but for -infinity),
  * out and the state are NaN; one in v does this to its channel alone, one in q to
- * its token's out.  Earlier tokens are as they would be without it.
- * The workspace holds about 0.9 KB a token and head in bf16 with d = 64
- * (proportional to d), twice to three times that in float32. */
+ * its token's out.  Earlier tokens are as they would be without it, but for
+ * the rounding of what shares a block's scale with it.
+ * The waits are bounded (mhla_device_status).  The workspace holds about 1 KB a
+ * token and head in bf16 with d = 64 (about proportional to d), 1.6 times that in
+ * float32; mhla_delta_backward's is three to four times the forward's. */
 mhla_status_t mhla_delta_workspace_size(const mhla_tensor_t* q, const mhla_tensor_t* v, size_t* bytes);
 mhla_status_t mhla_delta_forward(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v,
                                  const mhla_tensor_t* g, const mhla_tensor_t* beta, float scale,

@@ -10,6 +10,11 @@
 //   dv = beta dR,   dbeta = dR . (V - e^b K S) - rows of (dR W^T . G)
 // and the gates', a sum over what has the gate between its two tokens (pairs A (q k) + L (k k), what reads the state behind
 // it, what writes D in front of it, and e^B <S, D>; nothing cancels), every chunk does by itself: delta_grads.
+//
+// Measured, bf16 [4, 4096, 12, 64]: delta_prepare 132 us, delta_states (delta_scan with its states and W kept) 77, delta_back 142 (2.2 us a
+// chunk: the chain's two products, and beside it the warps that form a chunk's parts ahead), delta_grads 221: 160 KB read and written a chunk
+// (75 us of HBM's time), 40,000 cycles a chunk, two of them on an SM at once, of which 10,000 wait for what it reads.  Values and
+// their gradients element by element from memory took 315 us, sums of bf16 terms 351.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

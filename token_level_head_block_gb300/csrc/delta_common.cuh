@@ -27,18 +27,18 @@ using namespace gated;
 // of two such terms stand for six of three bf16 ones, and the chain's time is its products.  A scale belongs to 16 columns of
 // a row of the state or of w, to 16 rows of K^, to a row of Q or the scores, to a chunk of K.
 //
-// Elsewhere values are sums of bf16 terms, which need no scale: an input one (bf16) or three (float32), a value that reaches the
-// state three (2^-24), one that reaches outputs alone kOwn: two leave 2^-16 beside bf16 outputs.
+// In delta_prepare, and in what delta_back forms ahead, values are sums of bf16 terms, which need no scale: an input one (bf16) or three
+// (float32), a value that reaches the state three (2^-24).  delta_grads takes every plane of a chunk as fp16 at one scale.
 // Tokens a chunk: three planes of float32 rows of 128 channels leave room for 32.
 template <typename T>
 struct Form;
 template <>
 struct Form<__nv_bfloat16> {
-  static constexpr int kIn = 1, kOwn = 2, kHalves = 1, kChunk = 64;
+  static constexpr int kIn = 1, kHalves = 1, kChunk = 64;
 };
 template <>
 struct Form<float> {
-  static constexpr int kIn = 3, kOwn = 3, kHalves = 2, kChunk = 32;
+  static constexpr int kIn = 3, kHalves = 2, kChunk = 32;
 };
 constexpr int kChain = 3;   // bf16 terms on the way to the state
 
@@ -65,7 +65,7 @@ constexpr int kBlock = 512;
 
 template <typename T, int DK>
 struct Lay {
-  static constexpr int C = Form<T>::kChunk, kIn = Form<T>::kIn, kOwn = Form<T>::kOwn, kHalves = Form<T>::kHalves;
+  static constexpr int C = Form<T>::kChunk, kIn = Form<T>::kIn, kHalves = Form<T>::kHalves;
   static constexpr int kTiles = C / 16, kSides = DK / 16;          // blocks of a chunk's tokens, of the channels
   static constexpr bool kApart = kIn > 1;
   static constexpr int kRows = C * DK * 2, kSquare = C * C * 2;   // bytes of a plane
