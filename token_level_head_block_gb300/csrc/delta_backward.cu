@@ -45,7 +45,7 @@ template <typename T, int DK, int MT>
 struct BackLay {
   using L = Lay<T, DK>;
   using M = typename L::M;
-  static constexpr int kWarps = L::kTiles, kThreads = 64 * kWarps;
+  static constexpr int kWarps = L::kTiles, kThreads = 96 * kWarps;   // the chain's; with those beside it
   static constexpr int kShare = DK / 16 < kWarps ? 1 : DK / 16 / kWarps;   // blocks of the state's rows a warp
   static constexpr int kHand = MT * (2 + 2 * kShare) * kBlock;           // a warp's part of P^T do and Q^T do
   static constexpr int kStatePlane = 16 * MT * DK * 2, kTokenPlane = 16 * MT * L::C * 2;
@@ -60,11 +60,12 @@ struct BackLay {
   // and of the next chunk, what is formed ahead: of dout, of the scores, of Q, e^b
   static constexpr int kDoutBytes = MT * L::kTiles * L::kIn * kBlock, kScoreBytes = L::kTiles * kChain * kBlock;
   static constexpr int kQBytes = kShare * L::kTiles * L::kIn * kBlock, kInsideBytes = L::C * 4;
-  static constexpr int kScores = kDoutBytes, kQ = kScores + kScoreBytes, kInside = kQ + kQBytes, kAhead = kInside + kInsideBytes;
-  static constexpr int kAheads = kRing + 2 * kStage;   // one a warp
-  static constexpr int kBytes = kAheads + kWarps * kAhead;
+  static constexpr int kScores = kDoutBytes, kFirst = kScores + kScoreBytes;                             // a warp that forms P^T do
+  static constexpr int kQ = kDoutBytes, kInside = kQ + kQBytes, kSecond = kInside + kInsideBytes;        // and one that forms Q^T do
+  static constexpr int kFirsts = kRing + 2 * kStage, kSeconds = kFirsts + kWarps * kFirst;
+  static constexpr int kBytes = kSeconds + kWarps * kSecond;
   static_assert(kBytes <= 226 * 1024, "shared memory");
-  static_assert(kMarkFrom % 16 == 0 && kMarkBytes % 16 == 0 && kPair % 128 == 0 && kAhead % 128 == 0, "copied in units of 16 bytes");
+  static_assert(kMarkFrom % 16 == 0 && kMarkBytes % 16 == 0 && kPair % 128 == 0 && kFirst % 128 == 0 && kSecond % 128 == 0, "copied in units of 16 bytes");
 };
 
 template <typename T, int DK, int MT>
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
   using L = Lay<T, DK>;
   constexpr int C = L::C, TILES = L::kTiles, SIDES = L::kSides, SHARE = W::kShare;
   extern __shared__ __align__(128) char smem[];
-  __shared__ uint64_t bars[TILES][3];   // of either stage of the chain's operands, of what is formed ahead
+  __shared__ uint64_t bars[TILES][4];   // of either stage of the chain's operands, of what either warp beside it forms ahead
   const Common& p = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = (p.d + 16 * MT - 1) / (16 * MT);
@@ -88,18 +89,24 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
   auto chunk_of = [&](int i) { return bh * p.chunks + (count - 1 - i); };
   auto key_chunk_of = [&](int i) { return key * p.chunks + (count - 1 - i); };
 
+  // The warps beside the chain: the first of 16 tokens (a share of the state's rows) fetches for the chain and forms (P^T do)^T, the
+  // second ((scale e^b Q)^T do)^T.
   if (warp >= TILES) {
-    uint64_t* bar = bars[own];
+    const bool first = warp < 2 * TILES;
+    uint64_t *bar = bars[own], *bar_ahead = bar + (first ? 2 : 3);
     if (lane == 0) {
-#pragma unroll
-      for (int n = 0; n < 3; ++n) ptx::mbar_init(bar + n, 1);
+      if (first) {
+        ptx::mbar_init(bar, 1);
+        ptx::mbar_init(bar + 1, 1);
+      }
+      ptx::mbar_init(bar_ahead, 1);
       ptx::fence_mbar_init();
     }
     __syncwarp();
-    bool alive = true;   // no wait has given up
-    char* const st = smem + W::kAheads + own * W::kAhead;
+    bool alive = first || shares;   // and no wait has given up
+    char* const st = smem + (first ? W::kFirsts + own * W::kFirst : W::kSeconds + own * W::kSecond);
     auto load = [&](int i) {   // the chain's
-      if (lane != 0 || i >= count || !alive) return;
+      if (!first || lane != 0 || i >= count || !alive) return;
       char* stage = smem + W::kRing + (i & 1) * W::kStage;
       char* to = stage + own * W::kPair;
       uint64_t* on = bar + (i & 1);
@@ -111,63 +118,73 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
     const uint32_t seen = (TILES - own) * kChain * kBlock;   // scores from the diagonal on
     auto load_ahead = [&](int i) {
       if (lane != 0 || i >= count || !alive) return;
-      uint64_t* on = bar + 2;
-      ptx::mbar_arrive_expect_tx(on, W::kDoutBytes + seen + (shares ? W::kQBytes : 0) + W::kInsideBytes);
-      ptx::bulk_load_plain(st, p.im.dout_cols + chunk_of(i) * L::kInput + tile0 * TILES * L::kIn * kBlock, W::kDoutBytes, on);
-      ptx::bulk_load_plain(st + W::kScores + own * kChain * kBlock,
-                           p.im.scores_back + chunk_of(i) * L::kScoresBack + own * (TILES + 1) * kChain * kBlock, seen, on);
-      if (shares) ptx::bulk_load_plain(st + W::kQ, p.im.q_add + key_chunk_of(i) * L::kInput + own * W::kQBytes, W::kQBytes, on);
-      ptx::bulk_load_plain(st + W::kInside, p.im.marks + chunk_of(i) * L::kMarks + offsetof(typename L::M, inside), W::kInsideBytes, on);
+      ptx::mbar_arrive_expect_tx(bar_ahead, W::kDoutBytes + (first ? seen : W::kQBytes + W::kInsideBytes));
+      ptx::bulk_load_plain(st, p.im.dout_cols + chunk_of(i) * L::kInput + tile0 * TILES * L::kIn * kBlock, W::kDoutBytes, bar_ahead);
+      if (first) {
+        ptx::bulk_load_plain(st + W::kScores + own * kChain * kBlock,
+                             p.im.scores_back + chunk_of(i) * L::kScoresBack + own * (TILES + 1) * kChain * kBlock, seen, bar_ahead);
+        return;
+      }
+      ptx::bulk_load_plain(st + W::kQ, p.im.q_add + key_chunk_of(i) * L::kInput + own * W::kQBytes, W::kQBytes, bar_ahead);
+      ptx::bulk_load_plain(st + W::kInside, p.im.marks + chunk_of(i) * L::kMarks + offsetof(typename L::M, inside), W::kInsideBytes, bar_ahead);
     };
-    // (P^T do)^T of 16 tokens and ((scale e^b Q)^T do)^T of a share of the state's rows
     auto ahead = [&](int i) {
       float4* hand = reinterpret_cast<float4*>(smem + W::kHands + ((i & 1) * TILES + own) * W::kHand) + lane;
-      const float* inside = reinterpret_cast<const float*>(st + W::kInside);
+      if (first) {
 #pragma unroll
-      for (int n = 0; n < MT; ++n) {
-        Accumulators<2, true> y;
-        Accumulators<2 * SHARE, true> x;
-        y.clear();
-        x.clear();
+        for (int n = 0; n < MT; ++n) {
+          Accumulators<2, true> y;
+          y.clear();
 #pragma unroll
-        for (int ks = 0; ks < TILES; ++ks) {
-          uint32_t o[L::kIn][4];
-          float f[4][2];
+          for (int ks = 0; ks < TILES; ++ks) {
+            if (ks < own) continue;
+            uint32_t o[L::kIn][4], s[kChain][1][4];
 #pragma unroll
-          for (int k = 0; k < L::kIn; ++k) {
-            load_block(o[k], st, (n * TILES + ks) * L::kIn + k, lane);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              f[e][0] = k == 0 ? low(o[k][e]) : f[e][0] + low(o[k][e]);
-              f[e][1] = k == 0 ? high(o[k][e]) : f[e][1] + high(o[k][e]);
-            }
-          }
-          if (ks >= own) {
-            uint32_t s[kChain][1][4];
+            for (int k = 0; k < L::kIn; ++k) load_block(o[k], st, (n * TILES + ks) * L::kIn + k, lane);
 #pragma unroll
             for (int k = 0; k < kChain; ++k) load_block(s[k][0], st + W::kScores, ks * kChain + k, lane);
             mma_terms(y, 0, o, s);
           }
-          if (shares) {
-            uint32_t oa[kChain][4], q[L::kIn][SHARE][4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            hand[32 * (n * (2 + 2 * SHARE) + j)] = make_float4(y.get(j, 0), y.get(j, 1), y.get(j, 2), y.get(j, 3));
+        }
+        return;
+      }
+      if (!shares) return;
+      const float* inside = reinterpret_cast<const float*>(st + W::kInside);
+#pragma unroll
+      for (int n = 0; n < MT; ++n) {
+        Accumulators<2 * SHARE, true> x;
+        x.clear();
+#pragma unroll
+        for (int ks = 0; ks < TILES; ++ks) {
+          float f[4][2];
+#pragma unroll
+          for (int k = 0; k < L::kIn; ++k) {
+            uint32_t o[4];
+            load_block(o, st, (n * TILES + ks) * L::kIn + k, lane);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 in = *reinterpret_cast<const float2*>(inside + 16 * ks + 8 * (e >> 1) + t);
-              uint32_t z[kChain];
-              split<kChain>(f[e][0] * (p.scale * in.x), f[e][1] * (p.scale * in.y), z);
-#pragma unroll
-              for (int k = 0; k < kChain; ++k) oa[k][e] = z[k];
+              f[e][0] = k == 0 ? low(o[e]) : f[e][0] + low(o[e]);
+              f[e][1] = k == 0 ? high(o[e]) : f[e][1] + high(o[e]);
             }
-#pragma unroll
-            for (int k = 0; k < L::kIn; ++k)
-#pragma unroll
-              for (int j = 0; j < SHARE; ++j) load_block(q[k][j], st + W::kQ, (j * TILES + ks) * L::kIn + k, lane);
-            mma_terms(x, 0, oa, q);
           }
-        }
+          uint32_t oa[kChain][4], q[L::kIn][SHARE][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          hand[32 * (n * (2 + 2 * SHARE) + j)] = make_float4(y.get(j, 0), y.get(j, 1), y.get(j, 2), y.get(j, 3));
+          for (int e = 0; e < 4; ++e) {
+            const float2 in = *reinterpret_cast<const float2*>(inside + 16 * ks + 8 * (e >> 1) + t);
+            uint32_t z[kChain];
+            split<kChain>(f[e][0] * (p.scale * in.x), f[e][1] * (p.scale * in.y), z);
+#pragma unroll
+            for (int k = 0; k < kChain; ++k) oa[k][e] = z[k];
+          }
+#pragma unroll
+          for (int k = 0; k < L::kIn; ++k)
+#pragma unroll
+            for (int j = 0; j < SHARE; ++j) load_block(q[k][j], st + W::kQ, (j * TILES + ks) * L::kIn + k, lane);
+          mma_terms(x, 0, oa, q);
+        }
 #pragma unroll
         for (int j = 0; j < 2 * SHARE; ++j)
           hand[32 * (n * (2 + 2 * SHARE) + 2 + j)] = make_float4(x.get(j, 0), x.get(j, 1), x.get(j, 2), x.get(j, 3));
@@ -175,23 +192,23 @@ __global__ void __launch_bounds__(BackLay<T, DK, MT>::kThreads) delta_back(const
     };
     load_ahead(0);
     load(0);
-    if (stall_this_warp()) wait_copies_long(bar, 0, &g_delta_back_error);   // a test's
+    if (alive && stall_this_warp()) wait_copies_long(bar_ahead, 0, &g_delta_back_error);   // a test's
     // the chain's copies of chunk i and, ahead, those of chunk j: waited for once more when a wait has given up
     auto give_up = [&](int i, int j) {
       alive = false;
-      if (i < count) wait_copies_long(bar + (i & 1), i >> 1 & 1, &g_delta_back_error);
-      if (j < count) wait_copies_long(bar + 2, j & 1, &g_delta_back_error);
+      if (first && i < count) wait_copies_long(bar + (i & 1), i >> 1 & 1, &g_delta_back_error);
+      if (j < count) wait_copies_long(bar_ahead, j & 1, &g_delta_back_error);
     };
-    if (!wait_copies(bar + 2, 0, &g_delta_back_error)) give_up(0, 0);
+    if (alive && !wait_copies(bar_ahead, 0, &g_delta_back_error)) give_up(0, 0);
     ahead(0);
     __syncwarp();
     load_ahead(1);
     for (int i = 0; i < count; ++i) {
-      if (alive && !wait_copies(bar + (i & 1), i >> 1 & 1, &g_delta_back_error)) give_up(i, i + 1);
+      if (first && alive && !wait_copies(bar + (i & 1), i >> 1 & 1, &g_delta_back_error)) give_up(i, i + 1);
       sync();   // the chunk's operands, what was formed ahead and the planes of D are there; the chunk before is done with
       load(i + 1);
       if (i + 1 < count) {
-        if (alive && !wait_copies(bar + 2, i + 1 & 1, &g_delta_back_error)) give_up(i + 1, i + 1);
+        if (alive && !wait_copies(bar_ahead, i + 1 & 1, &g_delta_back_error)) give_up(i + 1, i + 1);
         ahead(i + 1);
         __syncwarp();
         load_ahead(i + 2);

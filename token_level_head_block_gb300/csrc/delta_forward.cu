@@ -721,7 +721,7 @@ template <typename T, int DK, int MT, bool KEEP>
 struct ScanLay {
   using L = Lay<T, DK>;
   using M = typename L::M;
-  static constexpr int kWarps = L::kTiles, kThreads = 64 * kWarps;
+  static constexpr int kWarps = L::kTiles, kThreads = (KEEP ? 64 : 96) * kWarps;   // the chain's; with those beside it
   static constexpr int kShare = DK / 16 < kWarps ? 1 : DK / 16 / kWarps;   // blocks of the state's rows a warp
   static constexpr int kStatePlane = 16 * MT * DK * 2, kTokenPlane = 16 * MT * L::C * 2;
   // the state, e^{B-b} W and (for the outputs) W, and the scales of their rows
@@ -764,8 +764,9 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
   auto first_of = [&](int i) { return reinterpret_cast<const typename L::M*>(p.im.marks + (bh * p.chunks + i) * L::kMarks)->first; };
 
   if (warp >= TILES) {
+    const int part = warp / TILES - 1;   // half of the outputs' columns; the first also fetches
     uint64_t* bar = bars[own];
-    if (lane == 0) {
+    if (part == 0 && lane == 0) {
 #pragma unroll
       for (int n = 0; n < STAGES; ++n) ptx::mbar_init(bar + n, 1);
       ptx::fence_mbar_init();
@@ -781,7 +782,7 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
     const uint32_t seen = KEEP ? 0 : (own + 1) * L::kHalves * kBlock;   // scores up to the diagonal
     const uint32_t bytes = W::kKeysBytes + MT * W::kUBytes + (shares ? W::kAddBytes : 0) + W::kQBytes + seen + (own == 0 ? W::kMarkBytes : 0);
     auto load = [&](int i) {
-      if (lane != 0 || i >= alive) return;
+      if (part != 0 || lane != 0 || i >= alive) return;
       char* stage = smem + W::kRing + i % STAGES * W::kStage;
       char* to = stage + own * W::kPair;
       uint64_t* on = bar + i % STAGES;
@@ -803,44 +804,45 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
       marks += L::kMarks;
     };
     for (int i = 0; i < STAGES - 1; ++i) load(i);
-    if (stall_this_warp()) wait_copies_long(bar, 0, &g_delta_error);   // a test's
+    if (part == 0 && stall_this_warp()) wait_copies_long(bar, 0, &g_delta_error);   // a test's
     T* const out = static_cast<T*>(a.out.data) + b * a.out.sb + h * a.out.sh;
     for (int i = 0; i < count; ++i) {
       const char* stage = smem + W::kRing + i % STAGES * W::kStage;
       const char* st = stage + own * W::kPair;
-      if (alive >= 0 && !wait_copies(bar + i % STAGES, i / STAGES & 1, &g_delta_error)) alive = -1 - i;
+      if (part == 0 && alive >= 0 && !wait_copies(bar + i % STAGES, i / STAGES & 1, &g_delta_error)) alive = -1 - i;
       sync();   // the chunk's operands and the state's planes are there; the chunk before is done with
       load(i + STAGES - 1);
       if constexpr (KEEP) {
         sync();
       } else {
-        // O = scale e^b Q S + scores W, this warp's 16 tokens
+        // O = scale e^b Q S + scores W, this warp's 16 tokens and 8 MT columns
+        const int col0 = 8 * MT * part;
         const auto* m = marks_at(stage);
         const float2 of_q = make_float2(m->query[16 * own + g], m->query[16 * own + g + 8]);
         const float2 of_p = make_float2(m->score[16 * own + g], m->score[16 * own + g + 8]);
         const int any = m->any;
         // a step of 16 of k has its own scale in each column
-        float o[2 * MT][4] = {};
+        float o[MT][4] = {};
         auto add_step = [&](const uint32_t (&q)[L::kHalves][4], uint32_t plane, int bytes, const float* scales, int steps, int ks, bool rows_of_state) {
+          uint32_t x[L::kHalves][4];
 #pragma unroll
-          for (int n = 0; n < MT; ++n) {
-            uint32_t x[L::kHalves][4];
-#pragma unroll
-            for (int k = 0; k < L::kHalves; ++k) {
-              if (rows_of_state)
-                b_rows<DK>(x[k], plane + k * bytes, 16 * n, 16 * ks, lane);
-              else
-                b_rows<C>(x[k], plane + k * bytes, 16 * n, 16 * ks, lane);
+          for (int k = 0; k < L::kHalves; ++k) {
+            if (rows_of_state)
+              b_rows<DK>(x[k], plane + k * bytes, 16 * (MT - 1) * part, 16 * ks, lane);
+            else
+              b_rows<C>(x[k], plane + k * bytes, 16 * (MT - 1) * part, 16 * ks, lane);
+            if (MT == 1 && part) {
+              x[k][0] = x[k][2];
+              x[k][1] = x[k][3];
             }
+          }
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              float c[4];
-              products(c, q, x, f);
-              const float s0 = scales[(16 * n + 8 * f + t) * steps + ks], s1 = scales[(16 * n + 8 * f + t + 1) * steps + ks];
-              float(&to)[4] = o[2 * n + f];
-              to[0] = fmaf(c[0], s0, to[0]); to[1] = fmaf(c[1], s1, to[1]);
-              to[2] = fmaf(c[2], s0, to[2]); to[3] = fmaf(c[3], s1, to[3]);
-            }
+          for (int f = 0; f < MT; ++f) {
+            float c[4];
+            products(c, q, x, f);
+            const float s0 = scales[(col0 + 8 * f + t) * steps + ks], s1 = scales[(col0 + 8 * f + t + 1) * steps + ks];
+            o[f][0] = fmaf(c[0], s0, o[f][0]); o[f][1] = fmaf(c[1], s1, o[f][1]);
+            o[f][2] = fmaf(c[2], s0, o[f][2]); o[f][3] = fmaf(c[3], s1, o[f][3]);
           }
         };
         const float *state_scale = reinterpret_cast<const float*>(smem + W::kStateScale), *token_scale = reinterpret_cast<const float*>(smem + W::kTokenScale);
@@ -851,9 +853,9 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
           for (int k = 0; k < L::kHalves; ++k) load_block(q[k], st + W::kQ, ks * L::kHalves + k, lane);
           add_step(q, state, W::kStatePlane, state_scale, SIDES, ks, true);
         }
-        float of_state[2 * MT][4];
+        float of_state[MT][4];
 #pragma unroll
-        for (int n = 0; n < 2 * MT; ++n)
+        for (int n = 0; n < MT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             of_state[n][e] = o[n][e] * (e < 2 ? of_q.x : of_q.y);
@@ -869,7 +871,7 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
           add_step(q, base + W::kW, W::kTokenPlane, token_scale, TILES, ks, false);
         }
 #pragma unroll
-        for (int n = 0; n < 2 * MT; ++n)
+        for (int n = 0; n < MT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[n][e] = fmaf(o[n][e], e < 2 ? of_p.x : of_p.y, of_state[n][e]);
         const int64_t t0 = static_cast<int64_t>(i) * C;
@@ -878,8 +880,8 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
           const int r = 16 * own + g + 8 * f;
           if (t0 + r >= p.N) continue;
 #pragma unroll
-          for (int n = 0; n < 2 * MT; ++n) {
-            const int c = 16 * tile0 + 8 * n + t;
+          for (int n = 0; n < MT; ++n) {
+            const int c = 16 * tile0 + col0 + 8 * n + t;
             if (c >= p.d) continue;
             float y[2] = {o[n][2 * f], o[n][2 * f + 1]};
             if (any)
@@ -892,7 +894,7 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
       }
     }
 #pragma unroll 1
-    for (int j = -1 - alive; alive < 0 && j < min(-alive - 2 + STAGES, count); ++j)
+    for (int j = -1 - alive; part == 0 && alive < 0 && j < min(-alive - 2 + STAGES, count); ++j)
       wait_copies_long(bar + j % STAGES, j / STAGES & 1, &g_delta_error);
     return;
   }
