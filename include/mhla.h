@@ -606,9 +606,12 @@ mhla_status_t mhla_delta_forward(const mhla_tensor_t* q, const mhla_tensor_t* k,
  *                heads that share them, in float32);  dg, dbeta  like g.
  *   dstate_in    device float32 [B][H][d][d], or NULL when not wanted.
  * dg_t is summed from what has the gate between its two tokens, as in
- * mhla_gated_backward.  The states are recomputed.  The written tensors share no
- * element with one another or with an input (views interleaved in a token's row
- * are fine).  workspace, stream, statuses and empty calls as for the forward. */
+ * mhla_gated_backward.  Within a chunk a factor is known to 2^-11 of itself and
+ * 2^-25 of the chunk's largest (float32: 2^-22 and 2^-25): rows far smaller than
+ * others of their chunk have their gradients to that.  The states are recomputed.
+ * The written tensors share no element with one another or with an input (views
+ * interleaved in a token's row are fine).  workspace, stream, statuses and empty
+ * calls as for the forward. */
 mhla_status_t mhla_delta_backward_workspace_size(const mhla_tensor_t* q, const mhla_tensor_t* v, size_t* bytes);
 mhla_status_t mhla_delta_backward(const mhla_tensor_t* q, const mhla_tensor_t* k, const mhla_tensor_t* v,
                                   const mhla_tensor_t* g, const mhla_tensor_t* beta, const mhla_tensor_t* dout,

@@ -3,7 +3,7 @@
 //   dW = P^T do + (e^{B-b} K) D          dR = T^T dW
 //   D' = e^B D + (scale e^b Q)^T do - K^^T dW      of the state that enters
 // so the gradient of the state runs backwards through a chunk in two products, as the state itself runs forwards: delta_back is
-// delta_scan's chain turned round, its second warps a chunk ahead with P^T do and Q^T do.  What is left,
+// delta_scan's chain turned round, the warps beside it a chunk ahead with P^T do and Q^T do.  What is left,
 //   A = scale (do W^T) . D_ij  (i >= j),   L = -beta (dR W^T) . D_ij  (i > j)
 //   dq = scale e^b do S^T + A K
 //   dk = A^T Q + L K + L^T K - beta e^b dR S^T + e^{B-b} W D^T
@@ -11,10 +11,13 @@
 // and the gates', a sum over what has the gate between its two tokens (pairs A (q k) + L (k k), what reads the state behind
 // it, what writes D in front of it, and e^B <S, D>; nothing cancels), every chunk does by itself: delta_grads.
 //
-// Measured, bf16 [4, 4096, 12, 64]: delta_prepare 132 us, delta_states (delta_scan with its states and W kept) 77, delta_back 142 (2.2 us a
-// chunk: the chain's two products, and beside it the warps that form a chunk's parts ahead), delta_grads 221: 160 KB read and written a chunk
-// (75 us of HBM's time), 40,000 cycles a chunk, two of them on an SM at once, of which 10,000 wait for what it reads.  Values and
-// their gradients element by element from memory took 315 us, sums of bf16 terms 351.
+// Measured, bf16 [4, 4096, 12, 64]:
+//   delta_prepare 132 us, delta_states (delta_scan with its states and W kept) 77
+//   delta_back    126 us, 2.0 us a chunk: the chain's two products, which share an SM's issue slots with the warps beside it; one such warp
+//                 for two took 142
+//   delta_grads   221 us: 160 KB read and written a chunk (75 us of HBM's time), 40,000 cycles a chunk, two of them on an SM at once, of which
+//                 10,000 wait for what it reads.  Values and their gradients element by element from memory took 315 us, sums of bf16
+//                 terms for fp16 351.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

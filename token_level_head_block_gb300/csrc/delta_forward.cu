@@ -11,18 +11,19 @@
 //
 // The scan is a chain of two products a chunk, so latency bounds it.  It runs transposed (S^T, W^T), a CTA with 16 or 32 columns of the
 // state.  A warp of the chain forms the W of 16 tokens and then its share of the state's rows; W and the state pass between the
-// warps as planes of fp16 pairs in shared memory, two barriers a chunk.  As many warps beside the chain's fetch what both read with bulk
-// copies, up to two chunks ahead, and form the outputs from the same planes.  What the scan reads lies as its fragments do, so that
-// a lane takes 16 bytes of an operand at once.
+// warps as planes of fp16 pairs in shared memory, two barriers a chunk.  Two warps beside each of the chain's form its tokens' outputs
+// from the same planes, half of the columns each; one of them fetches what all read with bulk copies, up to two chunks ahead.  What the scan
+// reads lies as its fragments do, so that a lane takes 16 bytes of an operand at once.
 //
 // Measured, bf16 [4, 4096, 12, 64] and [4, 65536, 6, 64]:
 //   delta_prepare  103 and 773 us, 92 KB read and written a chunk (42 and 340 us of HBM's time).  A chunk takes 25,000 cycles, three of
 //     them on an SM at once: 4,000 until its rows are there, 5,000 for T's blocks, 4,500 in the products of K^ and U, the rest in gates,
 //     scores and images; issue slots are 45% full, and the instruction cache misses one time in eight.  Scores formed while the other
 //     warps invert took 111 us for 107.
-//   delta_scan  105 and 1142 us: 96 CTAs of two tiles, 1.6 us a chunk, and 96 of one tile, 1.1 us: 2,100 cycles, 700 of them W's products,
-//     400 its splitting, 500 the state's products, 250 its splitting.  Asking L2 for a chunk's operands ahead of the copies took 1875 us for
-//     1426.
+//   delta_scan  107 and 1103 us: 96 CTAs of two tiles, 1.65 us a chunk, and 96 of one tile, 1.08 us: of 2,400 cycles (clocks read in
+//     between) 700 W's products, 400 its splitting, 550 the state's products, 450 its splitting, 250 at the barriers.  The chain alone, without
+//     outputs, takes 76 us for 107: the warps beside it share its issue slots and tensor cores.  One such warp for two took 105 and 1142.
+//     Asking L2 for a chunk's operands ahead of the copies took 1875 us for 1426.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -714,9 +715,9 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
 }
 
 // A CTA walks the chunks with 16 MT columns of the state.  TILES warps make the chain: each forms the W of 16 tokens, and then its
-// share of the state's rows.  As many warps beside them fetch what both read, chunks ahead, and (unless KEEP) read 16 tokens'
-// outputs, so nothing stands between the chain's products: it waits for two barriers a chunk.  KEEP leaves the states and the
-// w of every chunk for the gradients instead of outputs.
+// share of the state's rows.  The warps beside them fetch what all read, chunks ahead, and form 16 tokens' outputs, so nothing else
+// stands between the chain's products: it waits for two barriers a chunk.  KEEP leaves the states and the w of every chunk for the
+// gradients instead of outputs, with one warp beside each of the chain's.
 template <typename T, int DK, int MT, bool KEEP>
 struct ScanLay {
   using L = Lay<T, DK>;
@@ -1192,11 +1193,11 @@ int64_t delta_chunks(const DeltaProblem& p) {
 
 namespace delta {
 
-// Measured, bf16 at 4096 tokens (scan / gradients' chain, us, one tile against two): 192 tiles of d = 64 149 / 186 against 106 /
-// 142, 384 of them 222 / 277 against 205 / 278, but 128 of them, which all run at once, 78 / 97 against 104 / 143; d = 32, where
-// several CTAs of one tile fit on an SM, 192 tiles 87 / 131 against 85 / 152, 384 of 2048 tokens 78 / 117 against 86 / 154.  float32 at 2048
-// tokens, d = 64: 192 tiles 78 / 109 against 88 / 136, 384 of them 148 / 211 against 168 / 166.  So the scan takes two for bf16 alone, and
-// the gradients' chain from `most` = as many tiles as there are SMs on for bf16, twice as many for float32.
+// Measured, bf16 at 4096 tokens (scan / gradients' chain, us, one tile against two): 192 tiles of d = 64 147 / 178 against 107 /
+// 126, 384 of them 218 / 264 against 207 / 247, but 128 of them, which all run at once, 76 / 92 against 107 / 126; d = 32, where
+// several CTAs of one tile fit on an SM, 384 of 2048 tokens 78 / 117 against 86 / 154 (when one warp stood beside each of the chain's).  float32
+// at 2048 tokens, d = 64: 192 tiles 85 / 96 against 99 / 125, 384 of them 161 / 186 against 193 / 148.  So the scan takes two for bf16
+// alone, and the gradients' chain beyond `most`, as many tiles as there are SMs for bf16 and twice as many for float32.
 bool two_tiles(int64_t BH, int d, int64_t most) { return d > 32 && BH * ((d + 15) / 16) > most; }
 
 int launch_prepare(const Common& c, int64_t BH, int dtype, bool grad, cudaStream_t s) {
