@@ -292,6 +292,30 @@ def test_padding_leaves_the_state():
     assert torch.equal(last, short) or (np.sqrt((f64(last - short) ** 2).sum((-1, -2))) <= 2 * reference(cut, "f32", 0.1)[3]).all()
 
 
+def test_offsets_beyond_32_bits():
+    """Tokens 2^23 elements apart, the last ones behind 2^31: every tensor a view of rows of one array, the same bits as
+    with its own."""
+    B, N, H, d = 1, 300, 2, 64
+    x = draw(41, B, N, H, 1, d, "bf16")
+    want = run_forward(x, 0.125) + tuple(run_backward(x, 0.125))
+    rows = torch.empty(N, 1 << 23, dtype=torch.bfloat16, device=DEV)
+    assert (N - 1) * rows.stride(0) > 1 << 31
+    views, at = {}, 0
+    for name, width in [(n, H * d) for n in ("q", "k", "v", "dout", "out", "dq", "dk", "dv")] + [(n, H) for n in ("g", "beta", "dg", "dbeta")]:
+        part = rows[:, at:at + width]
+        views[name] = part.view(1, N, H, d) if width == H * d else part.view(1, N, H)
+        at += width + 8
+        if name in x:
+            views[name].copy_(x[name])
+    args = [views[n] for n in INPUTS]
+    out, last = mhla.delta_forward(*args, scale=0.125, state=gpu(x["state"]), out=views["out"])
+    grads = mhla.delta_backward(*args, views["dout"], scale=0.125, state=gpu(x["state"]), dstate_out=gpu(x["dstate_out"]),
+                                **{n: views[n] for n in ("dq", "dk", "dv", "dg", "dbeta")})
+    torch.cuda.synchronize()
+    assert mhla.device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip((out, last) + tuple(grads), want))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("what", ["k", "g", "beta", "v", "q"])
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])

@@ -248,6 +248,31 @@ def test_gradients_by_differences():
         assert abs((f64(grad) * f64(way)).sum() - want) <= 2.0 ** -20 * size / h + 4 * h * h * float(grad.norm())
 
 
+def test_offsets_beyond_32_bits():
+    """Results and gradients of more than 2^31 elements: their last rows, and sums over all rows (of ones: exact in float32)."""
+    rows, k, n = (1 << 20) + 77, 24, 2056
+    x = torch.ones(rows, k, dtype=torch.bfloat16, device=DEV)
+    w = draw(3, 1, k, n, "bf16")["w"].to(DEV)
+    assert rows * n > 1 << 31
+    tail = draw(4, 500, k, n, "bf16")
+    x[-500:] = tail["x"].to(DEV)
+    pre = torch.empty(rows, n, dtype=torch.bfloat16, device=DEV)
+    out = mhla.linear_act(x, w, activation="silu", pre=pre)
+    torch.cuda.synchronize()
+    assert mhla.device_status() == 0
+    check({"x": tail["x"], "w": w.cpu()}, "bf16", "silu", False, False, out[-500:], pre[-500:])
+    x[-500:] = 1
+    pre.fill_(1.0)                                                       # where the slope of relu is one
+    dx, dw, db = mhla.linear_act_backward(x, w, pre, "relu", pre)
+    torch.cuda.synchronize()
+    assert mhla.device_status() == 0
+    # rows ones added exactly or each partial sum rounded (2^-24 of it, 2 rows / 64 additions); bf16 rounds the result
+    for got in (dw, db):
+        assert (got.double() - rows).abs().max() <= (2.0 ** -8 + rows / 32 * 2.0 ** -24) * rows
+    want = f64(w).sum(0)
+    assert (np.abs(f64(dx[-500:]) - want) <= 2.0 ** -8 * np.abs(want) + 2 * (n + 4) * 2.0 ** -23 * np.abs(f64(w)).sum(0)).all()
+
+
 def test_no_rows():
     x, w = torch.empty(0, 16, device=DEV), torch.ones(8, 16, device=DEV)
     assert mhla.linear_act(x, w).shape == (0, 8)
