@@ -606,9 +606,10 @@ mhla_status_t mhla_delta_forward(const mhla_tensor_t* q, const mhla_tensor_t* k,
  *                heads that share them, in float32);  dg, dbeta  like g.
  *   dstate_in    device float32 [B][H][d][d], or NULL when not wanted.
  * dg_t is summed from what has the gate between its two tokens, as in
- * mhla_gated_backward.  Within a chunk a factor is known to 2^-11 of itself and
- * 2^-25 of the chunk's largest (float32: 2^-22 and 2^-25): rows far smaller than
- * others of their chunk have their gradients to that.  The states are recomputed.
+ * mhla_gated_backward.  A factor of a chunk is known to 2^-11 of itself and 2^-25
+ * of the largest it is summed with (float32: 2^-22, 2^-25); dout counts token by
+ * token, so dq is right for the size of its own token's dout.  The states are
+ * recomputed.
  * The written tensors share no element with one another or with an input (views
  * interleaved in a token's row are fine).  workspace, stream, statuses and empty
  * calls as for the forward. */

@@ -292,6 +292,30 @@ def test_padding_leaves_the_state():
     assert torch.equal(last, short) or (np.sqrt((f64(last - short) ** 2).sum((-1, -2))) <= 2 * reference(cut, "f32", 0.1)[3]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tokens_of_very_different_sizes(dtype):
+    """Output gradients, queries and values over six decades from token to token: a token's dq is right for its own size.
+    dq_t = scale S_t dout_t, so with dout_t exact and S_t known to a share r of X its error is below r scale X |dout_t|.  bf16
+    calls: one rounding of the result, 2^-12 of the largest for each of a sum of d = 64 values of the state or of a chunk's w and k,
+    of random sign: sqrt(64) 2^-12 = 2^-9 for either, r = 2^-8.  float32: E of the forward, with two fp16 (2^-22) a factor."""
+    x = draw(51, 1, 200, 2, 1, 64, dtype)
+    r = np.random.default_rng(52)
+    for name in ("q", "v", "dout"):
+        x[name] = (x[name].double() * torch.from_numpy(10.0 ** (-6 * r.random((1, 200, 2, 1))))).to(DT[dtype])
+    out, last = run_forward(x, 0.125)
+    check_forward(x, dtype, 0.125, out, last)
+    got = run_backward(x, 0.125)
+    check_backward(x, dtype, 0.125, got)
+    q, k, v, g, beta, do, S, dS = (f64(x[n]) for n in INPUTS + ("dout", "state", "dstate_out"))
+    ref = oracle.delta_backward(q, k, v, g, beta, do, 0.125, S, dS)[0]
+    _, _, all_S, w = oracle.delta(q, k, v, g, beta, 0.125, S, steps=True)
+    X = float(np.linalg.norm(all_S, axis=(-2, -1)).max()) + float(np.linalg.norm(w, axis=-1).max()) * CHUNK[dtype] ** 0.5
+    share = 2.0 ** -8 if dtype == "bf16" else 16 * 2.0 ** -22 * 7
+    each = np.linalg.norm(f64(got[0]) - ref, axis=-1)
+    allowed = HALF[dtype] * np.linalg.norm(ref, axis=-1) + share * 0.125 * X * np.linalg.norm(do, axis=-1)
+    assert (each <= allowed).all(), (each / allowed).max()
+
+
 def test_offsets_beyond_32_bits():
     """Tokens 2^23 elements apart, the last ones behind 2^31: every tensor a view of rows of one array, the same bits as
     with its own."""

@@ -15,7 +15,7 @@
 //   delta_prepare 132 us, delta_states (delta_scan with its states and W kept) 77
 //   delta_back    126 us, 2.0 us a chunk: the chain's two products, which share an SM's issue slots with the warps beside it; one such warp
 //                 for two took 142
-//   delta_grads   221 us: 160 KB read and written a chunk (75 us of HBM's time), 40,000 cycles a chunk, two of them on an SM at once, of which
+//   delta_grads   213 us: 160 KB read and written a chunk (75 us of HBM's time), 40,000 cycles a chunk, two of them on an SM at once, of which
 //                 10,000 wait for what it reads.  Values and their gradients element by element from memory took 315 us, sums of bf16
 //                 terms for fp16 351.
 #include <cuda_bf16.h>
@@ -404,7 +404,7 @@ struct GradLay {
   static constexpr int kPitch = DK + 4 / static_cast<int>(sizeof(T)), kValues = C * kPitch * static_cast<int>(sizeof(T));   // V, then dv, [token][column]
   static constexpr int kK = 0, kQ = kK + L::kInputHalf, kDout = kQ + L::kInputHalf, kW = kDout + L::kInputHalf, kR = kW + kTurned;
   static constexpr int kA = kR + kTurned;                              // T before it is A
-  static constexpr int kL = kA + L::kInverse, kState = kL + L::kInverse;
+  static constexpr int kL = kA + L::kInverse, kTurn = kL + L::kInverse, kState = kTurn + L::kInverse;   // A at its rows' scales, L, A at one scale
   static constexpr int kBytes = kState + std::max(L::kHalves * kSlicePlane, std::max(kValues, std::max(kPairs, kSum)));
   static_assert(kThreads == 4 * C, "four threads a token");
 };
@@ -600,6 +600,7 @@ __global__ void __launch_bounds__(GradLay<T, DK>::kThreads, DK < 128 ? 2 : 1) de
   // do W^T and Q K^T (first), dR W^T and K K^T (second), up to the diagonal: A and L, and the pairs of the gates
   const float of_w = scale(kMostW).from, of_r = scale(kMostR).from;
   float kept[2 * STRIPS][4], pairs[2 * STRIPS][4];
+  Scale of_row[2] = {};
   {
     float x[2 * STRIPS][4] = {}, y[2 * STRIPS][4] = {};
 #pragma unroll 1
@@ -629,10 +630,10 @@ __global__ void __launch_bounds__(GradLay<T, DK>::kThreads, DK < 128 ? 2 : 1) de
         }
       }
     }
-    const float of_x = of_w * (second ? of_r : m.douts), of_y = m.key * (second ? m.key : m.queries);
+    const float of_x[2] = {of_w * (second ? of_r : m.douts[row]), of_w * (second ? of_r : m.douts[row + 8])}, of_y = m.key * (second ? m.key : m.queries);
     const Sum br[2] = {{m.hi[row], m.lo[row]}, {m.hi[row + 8], m.lo[row + 8]}};
     const float beta_r[2] = {m.beta[row], m.beta[row + 8]};
-    float sum[2] = {0.0f, 0.0f}, largest = 0.0f;
+    float sum[2] = {0.0f, 0.0f}, largest[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int n = 0; n < 2 * STRIPS; ++n) {
       const int c = 8 * n + t;
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(GradLay<T, DK>::kThreads, DK < 128 ? 2 : 1) de
         if (n >= 2 * strip + 2) continue;
         const Sum bc = {m.hi[s], m.lo[s]};
         const float decay = s <= r ? exp2_of(br[e >> 1], bc) : 0.0f;
-        const float d = s <= r ? x[n][e] * of_x * decay : 0.0f, k = y[n][e] * of_y;
+        const float d = s <= r ? x[n][e] * of_x[e >> 1] * decay : 0.0f, k = y[n][e] * of_y;
         if (second) {
           kept[n][e] = s < r ? -beta_r[e >> 1] * d : 0.0f;
           if (s < r) sum[e >> 1] = fmaf(d, k, sum[e >> 1]);
@@ -651,10 +652,12 @@ __global__ void __launch_bounds__(GradLay<T, DK>::kThreads, DK < 128 ? 2 : 1) de
           kept[n][e] = p.scale * d;
         }
         pairs[n][e] = s < r ? kept[n][e] * k : 0.0f;
-        largest = fmaxf(largest, fabsf(kept[n][e]));
+        largest[e >> 1] = fmaxf(largest[e >> 1], fabsf(kept[n][e]));
       }
     }
-    note(second ? kMostL : kMostA, largest);
+    note(second ? kMostL : kMostA, fmaxf(largest[0], largest[1]));
+#pragma unroll
+    for (int f = 0; f < 2; ++f) of_row[f] = plane_scale(__float_as_uint(over_row(largest[f])));
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
       sum[f] += __shfl_xor_sync(~0u, sum[f], 1);
@@ -682,7 +685,10 @@ __global__ void __launch_bounds__(GradLay<T, DK>::kThreads, DK < 128 ? 2 : 1) de
       for (int n = 0; n < 2 * STRIPS; ++n) {
         if (n >= 2 * strip + 2) continue;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) put<C, NH>(smem, second ? G::kL : G::kA, L::kSquare, row + 8 * e, n, kept[n][2 * e] * by, kept[n][2 * e + 1] * by);
+        for (int e = 0; e < 2; ++e) {
+          put<C, NH>(smem, second ? G::kL : G::kTurn, L::kSquare, row + 8 * e, n, kept[n][2 * e] * by, kept[n][2 * e + 1] * by);
+          if (!second) put<C, NH>(smem, G::kA, L::kSquare, row + 8 * e, n, kept[n][2 * e] * of_row[e].to, kept[n][2 * e + 1] * of_row[e].to);
+        }
       }
     }
     __syncthreads();
@@ -774,7 +780,7 @@ __global__ void __launch_bounds__(GradLay<T, DK>::kThreads, DK < 128 ? 2 : 1) de
     }
   };
   // rows of a square plane, or of its transpose, times the rows of an input
-  auto add_square = [&](int square, bool turned, int where, float by) {
+  auto add_square = [&](int square, bool turned, int where, float f0, float f1) {
     uint32_t l[STRIPS][NH][4];
 #pragma unroll
     for (int ks = 0; ks < STRIPS; ++ks) {
@@ -787,7 +793,7 @@ __global__ void __launch_bounds__(GradLay<T, DK>::kThreads, DK < 128 ? 2 : 1) de
           a_rows<C>(l[ks][n], base + square + n * L::kSquare, m0, 16 * ks, lane);
       }
     }
-    add_rows(l, turned ? strip : 0, turned ? STRIPS : strip + 1, where, L::kRows, by, by);
+    add_rows(l, turned ? strip : 0, turned ? STRIPS : strip + 1, where, L::kRows, f0, f1);
   };
   // rows of dout, or of the transposes of dR, W, times the state's slice
   auto add_state = [&](int slice, int turned, float f0, float f1) {
@@ -828,7 +834,7 @@ __global__ void __launch_bounds__(GradLay<T, DK>::kThreads, DK < 128 ? 2 : 1) de
     if (second)
       add_state(slice, G::kR, of_r * by_s.from, of_r * by_s.from);
     else
-      add_state(slice, 0, p.scale * in0 * m.douts * by_s.from, p.scale * in1 * m.douts * by_s.from);
+      add_state(slice, 0, p.scale * in0 * m.douts[row] * by_s.from, p.scale * in1 * m.douts[row + 8] * by_s.from);
     __syncthreads();
   }
   {
@@ -846,15 +852,15 @@ __global__ void __launch_bounds__(GradLay<T, DK>::kThreads, DK < 128 ? 2 : 1) de
         enters[1][row] = b0 * sum[0];
         enters[1][row + 8] = b1 * sum[1];
       }
-      add_square(G::kL, false, G::kK, of_l * m.key);
-      add_square(G::kL, true, G::kK, of_l * m.key);
+      add_square(G::kL, false, G::kK, of_l * m.key, of_l * m.key);
+      add_square(G::kL, true, G::kK, of_l * m.key, of_l * m.key);
     } else {
       dot_rows(G::kQ, m.queries, sum);
       if ((lane & 3) == 0) {
         enters[0][row] = sum[0];
         enters[0][row + 8] = sum[1];
       }
-      add_square(G::kA, false, G::kK, of_a * m.key);
+      add_square(G::kA, false, G::kK, of_row[0].from * m.key, of_row[1].from * m.key);
       store(a.dq, a.pairs & 1);
 #pragma unroll
       for (int n = 0; n < NS; ++n)
@@ -876,7 +882,7 @@ __global__ void __launch_bounds__(GradLay<T, DK>::kThreads, DK < 128 ? 2 : 1) de
       leaves[row] = sum[0];
       leaves[row + 8] = sum[1];
     }
-    add_square(G::kA, true, G::kQ, of_a * m.queries);
+    add_square(G::kTurn, true, G::kQ, of_a * m.queries, of_a * m.queries);
 #pragma unroll
     for (int n = 0; n < NS; ++n) half[32 * n] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
   }

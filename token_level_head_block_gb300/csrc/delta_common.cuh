@@ -28,7 +28,8 @@ using namespace gated;
 // a row of the state or of w, to 16 rows of K^, to a row of Q or the scores, to a chunk of K.
 //
 // In delta_prepare, and in what delta_back forms ahead, values are sums of bf16 terms, which need no scale: an input one (bf16) or three
-// (float32), a value that reaches the state three (2^-24).  delta_grads takes every plane of a chunk as fp16 at one scale.
+// (float32), a value that reaches the state three (2^-24).  delta_grads takes every plane of a chunk as fp16 at one scale,
+// but dout and A in dq's products, whose rows stand for a token's own gradient, at a row's.
 // Tokens a chunk: three planes of float32 rows of 128 channels leave room for 32.
 template <typename T>
 struct Form;
@@ -45,6 +46,7 @@ constexpr int kChain = 3;   // bf16 terms on the way to the state
 // A chunk's values a token, then whether any is not finite and each column's first such token.
 template <int C, int DK>
 struct Marks {
+  float douts[C];          // gradients: the scale of dout's row
   float hi[C], lo[C];      // sum b of the log decays up to the token, in powers of two
   float inside[C];         // e^b
   float query[C];          // scale e^b and the scale of Q's row
@@ -55,7 +57,7 @@ struct Marks {
   float total;             // e^B
   float key;               // the scale of K
   int32_t any;
-  float inverse, queries, douts, pad[2];   // gradients: the scales of T, Q and dout
+  float inverse, queries, pad[3];   // gradients: the scales of T and Q
   int32_t first[DK];
 };
 

@@ -146,9 +146,9 @@ struct Prepare {
   static constexpr int kKeep = kQ, kBytes = kQ + std::max(L::kInput, C * DK * 4);
 };
 
-// Planes of terms, scaled, as planes of fp16.
-template <typename T, int DK>
-__device__ __forceinline__ void plane_halves(char* to, const char* from, float by, int thread, int threads) {
+// Planes of terms as planes of fp16, scaled by `by`, or (ROWS) each row at its own scale, which `scales` receives.
+template <typename T, int DK, bool ROWS = false>
+__device__ __forceinline__ void plane_halves(char* to, const char* from, float by, int thread, int threads, float* scales = nullptr) {
   using L = Lay<T, DK>;
   for (int i = 16 * thread; i < L::kRows; i += 16 * threads) {
     uint32_t x[L::kIn][4], y[L::kHalves][4];
@@ -156,6 +156,16 @@ __device__ __forceinline__ void plane_halves(char* to, const char* from, float b
     for (int n = 0; n < L::kIn; ++n) {
       const uint4 q = *reinterpret_cast<const uint4*>(from + n * L::kRows + i);
       x[n][0] = q.x; x[n][1] = q.y; x[n][2] = q.z; x[n][3] = q.w;
+    }
+    if (ROWS) {   // the largest of the first terms is within half a step of the row's; DK / 8 lanes have a row
+      uint32_t most = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) most = max(most, max(x[0][e] << 16 & 0x7FFF0000u, x[0][e] & 0x7FFF0000u));
+#pragma unroll
+      for (int o = 1; o < DK / 8; o <<= 1) most = max(most, __shfl_xor_sync(~0u, most, o));
+      const Scale row = plane_scale(most);
+      by = row.to;
+      scales[i / (2 * DK)] = row.from;
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -252,7 +262,7 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
   __shared__ __align__(16) typename L::M m;
   __shared__ __align__(16) Decays<C> w;
   __shared__ int32_t bad_key, bad;
-  __shared__ uint32_t most, most_q, most_o, most_t;   // |k|, and for the gradients |q|, |dout|, |T|
+  __shared__ uint32_t most, most_q, most_t;   // |k|, and for the gradients |q|, |T|
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t chunk = blockIdx.x % p.chunks;
   const int64_t bh = blockIdx.x / p.chunks, b = bh / p.H, h = bh % p.H, times = p.H / p.Hk, hk = h / times;
@@ -272,7 +282,7 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
   for (int i = threadIdx.x; i < DK; i += THREADS) m.first[i] = C;
   if (threadIdx.x == 0) {
     bad_key = bad = C;
-    most = most_q = most_o = most_t = 0;
+    most = most_q = most_t = 0;
   }
   __syncthreads();
 
@@ -675,7 +685,7 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
     largest = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(largest)));
     if (lane == 0) atomicMax(&most_t, __float_as_uint(largest));
     __syncthreads();
-    load_rows<T, DK, THREADS, 0, true>(smem + P::kV, units, from(p.dout, h), p.dout.sn, rows, p.d, p.wide & kWideDout, nullptr, &most_o);
+    load_rows<T, DK, THREADS, 0>(smem + P::kV, units, from(p.dout, h), p.dout.sn, rows, p.d, p.wide & kWideDout, nullptr);
     const Scale by = plane_scale(most_t);
     each([&](int r, int c, float2 x) {
       uint32_t t[L::kHalves];
@@ -685,13 +695,11 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
         *reinterpret_cast<uint32_t*>(p.im.inverse + at * L::kInverse + n * L::kSquare + unit_at<C>(r, c >> 3) + (c & 7) * 2) = t[n];
     });
     __syncthreads();
-    const Scale by_o = plane_scale(most_o);
     if (threadIdx.x == 0) {
       m.inverse = by.from;
       m.queries = plane_scale(most_q).from;
-      m.douts = by_o.from;
     }
-    plane_halves<T, DK>(p.im.dout + at * L::kInputHalf, smem + P::kV, by_o.to, threadIdx.x, THREADS);
+    plane_halves<T, DK, true>(p.im.dout + at * L::kInputHalf, smem + P::kV, 0.0f, threadIdx.x, THREADS, m.douts);
     for (int i = warp; i < SIDES * TILES; i += 2 * TILES)
 #pragma unroll
       for (int n = 0; n < L::kIn; ++n) {
