@@ -466,6 +466,13 @@ __global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(
             if (i < rows) residual[i].fetch(p.f.residual, i0 + STEP * i * p.f.N + GROUP * gi);
       };
       fetch(side);
+      if (whole && p.f.residual && u + stride < p.units) {   // the next tile's, as far as L2
+        const Unit next = unit_of<PAIR>(p, u + stride, rank);
+        const int64_t row = next.m0 + 32 * q4 + lane;
+        if (row < p.f.M)
+          for (int64_t c = next.n0 + GROUP * side; c < min(p.f.N, next.n0 + static_cast<int64_t>(p.BN)); c += GROUP * L::SIDE)
+            prefetch_l2(static_cast<const char*>(p.f.residual) + (row * p.f.N + c) * (F32 ? 4 : 2));
+      }
       if (!warp_wait(tfull + acc, aph, abortf)) break;
       tc_fence_after();
       const uint32_t tb = tmem + acc * 256 + (static_cast<uint32_t>(32 * q4) << 16);
