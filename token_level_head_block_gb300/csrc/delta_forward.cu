@@ -19,7 +19,7 @@
 //   delta_prepare  103 and 773 us, 92 KB read and written a chunk (42 and 340 us of HBM's time).  A chunk takes 25,000 cycles, three of
 //     them on an SM at once: 4,000 until its rows are there, 5,000 for T's blocks, 4,500 in the products of K^ and U, the rest in gates,
 //     scores and images; issue slots are 45% full, and the instruction cache misses one time in eight.  Scores formed while the other
-//     warps invert took 111 us for 107.
+//     warps invert took 111 us for 107; the rows of the CTA that follows asked for as far as L2, 141 for 132 (with the gradients' images).
 //   delta_scan  107 and 1103 us: 96 CTAs of two tiles, 1.65 us a chunk, and 96 of one tile, 1.08 us: of 2,400 cycles (clocks read in
 //     between) 700 W's products, 400 its splitting, 550 the state's products, 450 its splitting, 250 at the barriers.  The chain alone, without
 //     outputs, takes 76 us for 107: the warps beside it share its issue slots and tensor cores.  One such warp for two took 105 and 1142.

@@ -13,8 +13,10 @@
 // A persistent CTA (or a pair of them with one tile of 256 rows, cta_group::2) loads with TMA, multiplies and finishes the tile before
 // at once.  Measured, bf16, against the measured 1947 TFLOP/s and 6.7 TB/s: 16384 x 768 by 2304 with bias, SiLU and z kept 66 us (30 us of
 // products, 25 of HBM's time; without any of these 57, and with 4096 for 768 216 us: 0.38 us a chunk of 64, of which the products need
-// 0.28, what an SM takes in from L2 being the bound); 262144 x 384 by 384 with residual 126 us (91 of HBM's time).  Its tiles of 256
-// columns finish in 4.3 us beside 4.6 us of products.  Six stages for five, and single CTAs (163 and 89 us for 126 and 66), were no faster.
+// 0.28, what an SM takes in from L2 being the bound); 262144 x 384 by 384 with residual 113 us (91 of HBM's time; 126 when the
+// next tile's residual is not asked for as far as L2, 117 for the one after it).  Its tiles of 256
+// columns finish in 4.3 us beside 4.6 us of products.  Six stages for five were no faster; single CTAs took 163 us for 140,
+// before the finish was 32 columns wide.
 //
 // Few rows (serving) read w once and compute next to nothing: linear_rows gives every CTA 16 of w's rows and
 // its warps a part of K each.
