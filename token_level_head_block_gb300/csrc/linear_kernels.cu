@@ -265,7 +265,7 @@ struct GemmLay {
 };
 
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  return wait_bounded_on(bar, parity, abort_flag, &g_linear_error);
+  return mbar_try_wait(bar, parity) || wait_bounded_on(bar, parity, abort_flag, &g_linear_error);   // the first look without a call
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
   return warp_wait_on(bar, parity, abort_flag, &g_linear_error);
@@ -394,8 +394,11 @@ __global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(
     if (lane == 0 && rank == 0) {
       const uint32_t idesc = idesc_bf16_f32(PAIR ? 256 : 128, p.BN, p.a_major != 0, p.b_major != 0);
       // steps of 16 of K: 32 bytes along swizzled rows, or 16 rows of 128 bytes
-      const uint32_t a_step = p.a_major ? 2048 : 32, b_step = p.b_major ? 2048 : 32;
-      const uint32_t a_lbo = p.a_major ? 8192 : 16, b_lbo = p.b_major ? 8192 : 16;
+      // One thread issues everything, so what it computes in between is kept short: descriptors of the first stage, to whose address
+      // fields (units of 16 bytes, below 2^14 over all of shared memory) the rest is added.
+      const uint32_t a_step = (p.a_major ? 2048 : 32) / 16, b_step = (p.b_major ? 2048 : 32) / 16;
+      const uint64_t a_first = smem_desc(smem_u32(smem), p.a_major ? 8192 : 16, 1024, 2);
+      const uint64_t b_first = smem_desc(smem_u32(smem) + TERMS * L::A_BYTES, p.b_major ? 8192 : 16, 1024, 2);
       auto commit = [&](uint64_t* bar) {
         if (PAIR)
           mma_commit_pair(bar);
@@ -414,10 +417,10 @@ __global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(
         for (int kc = 0; kc < un.count; ++kc) {
           if (!wait_bounded(full + s, ph, abortf)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a_base = smem_u32(smem + s * L::STAGE), b_base = a_base + TERMS * L::A_BYTES;
+          const uint64_t a_stage = a_first + s * (L::STAGE / 16), b_stage = b_first + s * (L::STAGE / 16);
           // the accumulator of this part of K, and whether it is empty yet
-          const int main = L::MAINS * kc / un.count;
-          const bool opens = kc == (main * un.count + L::MAINS - 1) / L::MAINS;
+          const int main = L::MAINS == 1 ? 0 : L::MAINS * kc / un.count;
+          const bool opens = L::MAINS == 1 ? kc == 0 : kc == (main * un.count + L::MAINS - 1) / L::MAINS;
 #pragma unroll
           for (int ks = 0; ks < L::BK / 16; ++ks)
 #pragma unroll
@@ -425,8 +428,7 @@ __global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(
 #pragma unroll
               for (int j = TERMS - 1 - i; j >= 0; --j) {
                 const bool large = i + j == 0;
-                const uint64_t a = smem_desc(a_base + i * L::A_BYTES + ks * a_step, a_lbo, 1024, 2);
-                const uint64_t b = smem_desc(b_base + j * L::B_BYTES + ks * b_step, b_lbo, 1024, 2);
+                const uint64_t a = a_stage + (i * (L::A_BYTES / 16) + ks * a_step), b = b_stage + (j * (L::B_BYTES / 16) + ks * b_step);
                 const bool first = large ? opens && ks == 0 : kc == 0 && ks == 0 && i == TERMS - 1;
                 const uint32_t to = dt + (large ? 128 * main : 128 * L::MAINS);
                 if (PAIR)
