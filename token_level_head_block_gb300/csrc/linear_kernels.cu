@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull + a, 1);
-      mbar_init(tempty + a, (PAIR ? 64 : 32) * L::WARPS);
+      mbar_init(tempty + a, (PAIR ? 2 : 1) * L::WARPS);   // one arrival a warp
     }
     mbar_init(fin, 1);
     *abortf = 0u;
@@ -543,10 +543,13 @@ __global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(
         __syncwarp();
       }
       tc_fence_before();
-      if (PAIR)
-        mbar_arrive_at(tempty + acc, 0);   // the sums are read out
-      else
-        mbar_arrive(tempty + acc);
+      __syncwarp();
+      if (lane == 0) {   // the sums are read out
+        if (PAIR)
+          mbar_arrive_at(tempty + acc, 0);
+        else
+          mbar_arrive(tempty + acc);
+      }
     }
   }
   tc_fence_before();
