@@ -239,7 +239,7 @@ __device__ __forceinline__ void finish_quad(const Finish& f, int64_t r, int64_t 
 // ----------------------------------------------------------------- product
 
 struct Product {
-  CUtensorMap a, b;
+  CUtensorMap a, b, out, pre;   // out, pre: of bulk stores
   Finish f;
   float* parts;          // [splits][M][pitch] sums of parts of K, or null
   int64_t pitch, units;
@@ -262,6 +262,7 @@ struct GemmLay {
   static constexpr int WARPS = 4 * SIDE, THREADS = 64 + 32 * WARPS;
   static constexpr size_t SMEM = static_cast<size_t>(NS) * STAGE + WARPS * STAGING + 1024 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(!PAIR || (GROUP == 32 && STAGING % 512 == 0 && STAGING >= 4096), "bulk stores' staging");
 };
 
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
@@ -291,7 +292,8 @@ __device__ __forceinline__ Unit unit_of(const Product& p, int64_t u, uint32_t ra
 // Persistent CTAs walk the units, neighbours sharing A's rows in L2.  Warp 0 loads K chunks of 64 (a ring of
 // stages), warp 1 issues the MMAs, eight warps turn the sums round through shared memory, so that a row's columns lie in
 // neighbouring lanes, and finish them.
-template <int TERMS, bool PAIR>
+// BULK: finished rows leave through the copy engine.
+template <int TERMS, bool PAIR, bool BULK>
 __global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(const __grid_constant__ Product p) {
   using L = GemmLay<TERMS, PAIR>;
   extern __shared__ uint8_t smem_raw[];
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(
       // what the finish reads of memory: the first group's while the products run, then a group ahead
       Quad<F32> residual[ROWS] = {}, bias = {};
       auto fetch = [&](int gi) {
-        if (!whole || c0 + GROUP * gi >= p.f.N) return;
+        if (BULK || !whole || c0 + GROUP * gi >= p.f.N) return;
         if (p.f.bias) bias.fetch(p.f.bias, c0 + GROUP * gi);
         if (p.f.residual)
 #pragma unroll
@@ -506,41 +508,79 @@ __global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(
             tmem_ld_x16(tb + 16 * gi, v);
           tmem_ld_wait();
         }
-        // a row of the group a lane becomes four columns of ROWS rows
-#pragma unroll
-        for (int e = 0; e < LANES; ++e)
-          *reinterpret_cast<uint4*>(stage + lane * L::PITCH + 4 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-        __syncwarp();
         float z[4 * ROWS];
-        const float4 add = p.f.bias ? bias.value() : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if constexpr (BULK) {
+          // a lane keeps its row of the group: bf16 rows staged as the copies take them, 16-byte units changing places with the row
+          const int64_t c = un.n0 + GROUP * gi;
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-          const float4 x = *reinterpret_cast<const float4*>(stage + (STEP * i + lane_row) * L::PITCH + lane_col);
-          z[4 * i] = x.x; z[4 * i + 1] = x.y; z[4 * i + 2] = x.z; z[4 * i + 3] = x.w;
-        }
-        __syncwarp();
-        const int64_t c = c0 + GROUP * gi;
-        if (whole) {
-          Quad<F32> now[ROWS];
+          for (int j = 0; j < GROUP / 8; ++j) {
+            uint4 add = make_uint4(0u, 0u, 0u, 0u);
+            if (p.f.bias && c + 8 * j < p.f.N) add = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.f.bias) + c + 8 * j));
+            const uint32_t adds[4] = {add.x, add.y, add.z, add.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              z[8 * j + 2 * i] = __uint_as_float(v[8 * j + 2 * i]) + low(adds[i]);
+              z[8 * j + 2 * i + 1] = __uint_as_float(v[8 * j + 2 * i + 1]) + high(adds[i]);
+            }
+          }
+          if (lane == 0) bulk_wait_group_read0();   // what the copies before read
+          __syncwarp();
+          auto put = [&](int where) {
+#pragma unroll
+            for (int j = 0; j < GROUP / 8; ++j)
+              *reinterpret_cast<uint4*>(reinterpret_cast<char*>(stage) + where + 64 * lane + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(gated::pack(z[8 * j], z[8 * j + 1]), gated::pack(z[8 * j + 2], z[8 * j + 3]), gated::pack(z[8 * j + 4], z[8 * j + 5]),
+                             gated::pack(z[8 * j + 6], z[8 * j + 7]));
+          };
+          if (p.f.pre) put(2048);
+          activate_all<true>(z, p.f.act);
+          put(0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const int32_t row = un.m0 + 32 * q4;
+            if (row < p.f.M) {
+              tma_store_2d(&p.out, stage, static_cast<int32_t>(c), row);
+              if (p.f.pre) tma_store_2d(&p.pre, reinterpret_cast<char*>(stage) + 2048, static_cast<int32_t>(c), row);
+              bulk_commit_group();
+            }
+          }
+        } else {
+          // a row of the group a lane becomes four columns of ROWS rows
+#pragma unroll
+          for (int e = 0; e < LANES; ++e)
+            *reinterpret_cast<uint4*>(stage + lane * L::PITCH + 4 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          __syncwarp();
+          const float4 add = p.f.bias ? bias.value() : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
           for (int i = 0; i < ROWS; ++i) {
-            now[i] = residual[i];
-            z[4 * i] += add.x; z[4 * i + 1] += add.y; z[4 * i + 2] += add.z; z[4 * i + 3] += add.w;
+            const float4 x = *reinterpret_cast<const float4*>(stage + (STEP * i + lane_row) * L::PITCH + lane_col);
+            z[4 * i] = x.x; z[4 * i + 1] = x.y; z[4 * i + 2] = x.z; z[4 * i + 3] = x.w;
           }
-          if (gi + L::SIDE < used) fetch(gi + L::SIDE);
-          if (c < p.f.N) finish_quads<F32, ROWS>(p.f, i0 + GROUP * gi, STEP * p.f.N, rows, z, now);
-        } else if (c < p.f.N) {
+          __syncwarp();
+          const int64_t c = c0 + GROUP * gi;
+          if (whole) {
+            Quad<F32> now[ROWS];
 #pragma unroll
-          for (int i = 0; i < ROWS; ++i) {
-            if (i >= rows) break;
-            const float4 x = make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
-            if (p.parts)
-              *reinterpret_cast<float4*>(p.parts + (un.split * p.f.M + row0 + STEP * i) * p.pitch + c) = x;
-            else
-              finish_quad<F32>(p.f, row0 + STEP * i, c, x);
+            for (int i = 0; i < ROWS; ++i) {
+              now[i] = residual[i];
+              z[4 * i] += add.x; z[4 * i + 1] += add.y; z[4 * i + 2] += add.z; z[4 * i + 3] += add.w;
+            }
+            if (gi + L::SIDE < used) fetch(gi + L::SIDE);
+            if (c < p.f.N) finish_quads<F32, ROWS>(p.f, i0 + GROUP * gi, STEP * p.f.N, rows, z, now);
+          } else if (c < p.f.N) {
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+              if (i >= rows) break;
+              const float4 x = make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
+              if (p.parts)
+                *reinterpret_cast<float4*>(p.parts + (un.split * p.f.M + row0 + STEP * i) * p.pitch + c) = x;
+              else
+                finish_quad<F32>(p.f, row0 + STEP * i, c, x);
+            }
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
@@ -552,6 +592,7 @@ __global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(
       }
     }
   }
+  if (BULK && warp > 1 && lane == 0) bulk_wait_group0();
   tc_fence_before();
   // neither CTA leaves while the other's MMAs read its shared memory or their commits arrive there
   __syncthreads();
@@ -852,10 +893,10 @@ size_t part_bytes(int64_t M, int64_t N, const Cutting& c) {
   return c.splits < 2 ? 0 : align_up(static_cast<size_t>(c.splits) * M * ((N + 3) / 4 * 4) * 4);
 }
 
-template <int TERMS, bool PAIR>
+template <int TERMS, bool PAIR, bool BULK = false>
 int launch_product(const char* name, const Product& p, cudaStream_t s) {
   using L = GemmLay<TERMS, PAIR>;
-  auto kernel = linear_gemm<TERMS, PAIR>;
+  auto kernel = linear_gemm<TERMS, PAIR, BULK>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L::SMEM)) != cudaSuccess)
     return MHLA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -899,8 +940,20 @@ int run_product(const char* name, const Matrix& a, bool a_major, const Matrix& b
   p.pitch = (N + 3) / 4 * 4;
   p.units = c.tiles * c.splits;
   p.a_major = a_major; p.b_major = b_major;
+  // 32 x 32 values a warp, 64 bytes a row
+  const bool bulk = c.pair && c.splits < 2 && !f.residual && N % 8 == 0;
+  if (bulk) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)}, strides[1] = {static_cast<cuuint64_t>(2 * N)};
+    const cuuint32_t box[2] = {32, 32};
+    if (!encode_tensor_map(&p.out, 2, f.out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        (f.pre && !encode_tensor_map(&p.pre, 2, f.pre, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B)))
+      return MHLA_ERR_CUDA;
+  }
   p.BN = c.BN; p.tiles_n = c.tiles_n; p.chunks = c.chunks; p.splits = c.splits; p.split_chunks = c.split_chunks;
-  const int rc = terms > 1 ? launch_product<3, false>(name, p, s) : c.pair ? launch_product<1, true>(name, p, s) : launch_product<1, false>(name, p, s);
+  const int rc = terms > 1  ? launch_product<3, false>(name, p, s)
+                 : bulk     ? launch_product<1, true, true>(name, p, s)
+                 : c.pair   ? launch_product<1, true>(name, p, s)
+                            : launch_product<1, false>(name, p, s);
   if (rc != MHLA_OK) return rc;
   if (c.splits < 2) return MHLA_OK;
   const Join j = {f, p.parts, p.pitch, c.splits};
