@@ -244,6 +244,7 @@ struct Product {
   float* parts;          // [splits][M][pitch] sums of parts of K, or null
   int64_t pitch, units;
   int32_t a_major, b_major;   // 1: the operand lies [K][M] ([K][N])
+  int32_t a_blocks, b_blocks; // and one copy takes all its blocks of 64 columns
   int32_t BN, tiles_n, chunks, splits, split_chunks;
 };
 
@@ -369,14 +370,18 @@ __global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(
 #pragma unroll
           for (int t = 0; t < TERMS; ++t) {
             uint8_t* at = st + t * L::A_BYTES;
-            if (p.a_major) {
+            if (TERMS == 1 && p.a_blocks) {
+              load(at, &p.a, s, 0, k0, un.m0 / 64);
+            } else if (p.a_major) {
               load(at, &p.a, s, un.m0, k0, t);
               load(at + 8192, &p.a, s, un.m0 + 64, k0, t);
             } else {
               load(at, &p.a, s, k0, un.m0, t);
             }
             at = st + TERMS * L::A_BYTES + t * L::B_BYTES;
-            if (p.b_major) {
+            if (TERMS == 1 && p.b_blocks) {
+              load(at, &p.b, s, 0, k0, n0 / 64);
+            } else if (p.b_major) {
               for (int j = 0; j < b_rows / 64; ++j) load(at + 8192 * j, &p.b, s, n0 + 64 * j, k0, t);
             } else {
               load(at, &p.b, s, k0, n0, t);
@@ -847,6 +852,14 @@ bool encode_planes(CUtensorMap* m, const Matrix& x, int terms, int box_cols, int
   return encode_tensor_map(m, 3, const_cast<void*>(x.data), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Columns as blocks of 64 (a whole number of them), `count` a box: where a matrix is read N-major, one copy takes a chunk's.
+bool encode_blocks(CUtensorMap* m, const Matrix& x, int count) {
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(x.rows), static_cast<cuuint64_t>(x.cols / 64)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(x.pitch * 2), 128};
+  const cuuint32_t box[3] = {64, 64, static_cast<cuuint32_t>(count)};
+  return encode_tensor_map(m, 3, const_cast<void*>(x.data), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 // How C [M][N] over K is cut.  Time of a unit: its chunks, by the operand bytes that an SM takes in (a chunk of 128 + 256 rows is
 // about 0.55 us under full load), and what its finish leaves uncovered.  K is split where there are few tiles.
 struct Cutting {
@@ -932,8 +945,11 @@ int run_product(const char* name, const Matrix& a, bool a_major, const Matrix& b
   const int terms = dtype == MHLA_BF16 ? 1 : 3;
   const Cutting c = cut_product(M, N, K, dtype, b_major);
   Product p = {};
-  if (!encode_planes(&p.a, a, terms, 64, a_major ? 64 : 128) ||
-      !encode_planes(&p.b, b, terms, 64, b_major ? 64 : c.pair ? c.BN / 2 : c.BN))
+  const int b_rows = c.pair ? c.BN / 2 : c.BN;
+  p.a_blocks = a_major && terms == 1 && a.cols % 64 == 0;
+  p.b_blocks = b_major && terms == 1 && b.cols % 64 == 0;
+  if (!(p.a_blocks ? encode_blocks(&p.a, a, 2) : encode_planes(&p.a, a, terms, 64, a_major ? 64 : 128)) ||
+      !(p.b_blocks ? encode_blocks(&p.b, b, b_rows / 64) : encode_planes(&p.b, b, terms, 64, b_major ? 64 : b_rows)))
     return MHLA_ERR_CUDA;
   p.f = f;
   p.parts = c.splits > 1 ? reinterpret_cast<float*>(parts) : nullptr;
