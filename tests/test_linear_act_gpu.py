@@ -123,7 +123,7 @@ def test_backward(shape, dtype, act, bias):
 # what the small ones above do not reach: pairs of CTAs on tiles of 256 rows, each width of tile, the long axis in parts
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shape", [(300, 768, 8192), (700, 200, 4096), (300, 200, 8192), (129, 65536, 200), (129, 65536, 192),
-                                   (129, 65536, 100), (65, 65536, 384), (65, 65536, 1000), (65, 65536, 192)], ids=str)
+                                   (129, 65536, 100), (257, 65536, 256), (65, 65536, 384), (65, 65536, 1000), (65, 65536, 192)], ids=str)
 def test_forward_of_every_cutting(shape, dtype):
     x = draw(sum(shape), *shape, dtype)
     g = {n: t.to(DEV) for n, t in x.items()}
@@ -136,7 +136,7 @@ def test_forward_of_every_cutting(shape, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shape", [(300, 8192, 768), (129, 8192, 8), (768, 8192, 300), (129, 192, 65536), (65536, 192, 129),
-                                   (65536, 100, 129)], ids=str)
+                                   (65536, 100, 129), (65536, 256, 257)], ids=str)
 def test_backward_of_every_cutting(shape, dtype):
     x = draw(sum(shape) + 1, *shape, dtype)
     g = {n: t.to(DEV) for n, t in x.items()}

@@ -11,12 +11,14 @@
 // its small products apart and its large ones in three accumulators, a third of K each, added in the epilogue.
 //
 // A persistent CTA (or a pair of them with one tile of 256 rows, cta_group::2) loads with TMA, multiplies and finishes the tile before
-// at once.  Measured, bf16, against the measured 1947 TFLOP/s and 6.7 TB/s: 16384 x 768 by 2304 with bias, SiLU and z kept 66 us (30 us of
-// products, 25 of HBM's time; without any of these 57, and with 4096 for 768 216 us: 0.38 us a chunk of 64, of which the products need
-// 0.28, what an SM takes in from L2 being the bound); 262144 x 384 by 384 with residual 113 us (91 of HBM's time; 126 when the
-// next tile's residual is not asked for as far as L2, 117 for the one after it).  Its tiles of 256
-// columns finish in 4.3 us beside 4.6 us of products.  Six stages for five were no faster; single CTAs took 163 us for 140,
-// before the finish was 32 columns wide.
+// at once.  Measured, bf16, against the measured 1947 TFLOP/s and 6.7 TB/s:
+//   16384 x 768 by 2304: 44 us, with bias, SiLU and z kept 56 (30 us of products; 27 of HBM's time); 4096 for 768: 168 (159 of products), 0.30 us a
+//     chunk of 64 where the products need 0.27; 64 for 768: 24, the finish and HBM (12).  One thread issues a chunk's copies, another its
+//     products: with descriptors formed anew for each product it took 0.38 us a chunk whatever the tile (57 us), with two copies a chunk
+//     for N-major operands dx and dw took 49 and 60 us for 46 and 53.  Six stages for five were no faster.
+//   The finish: rows staged as bf16 and copied out asynchronously; through float32 and ordinary stores 60 us for 56, 35 for 24.
+//   262144 x 384 by 384 with residual: 114 us (91 of HBM's time); 126 when the next tile's residual is not asked for as far as L2, 117 for the
+//     one after it; ordinary stores, since the residual is read as it lies.
 //
 // Few rows (serving) read w once and compute next to nothing: linear_rows gives every CTA 16 of w's rows and
 // its warps a part of K each.
@@ -861,7 +863,7 @@ bool encode_blocks(CUtensorMap* m, const Matrix& x, int count) {
 }
 
 // How C [M][N] over K is cut.  Time of a unit: its chunks, by the operand bytes that an SM takes in (a chunk of 128 + 256 rows is
-// about 0.55 us under full load), and what its finish leaves uncovered.  K is split where there are few tiles.
+// about 0.45 us under full load), and what its finish leaves uncovered.  K is split where there are few tiles.
 struct Cutting {
   int BN, tiles_n, chunks, splits, split_chunks;
   int64_t tiles;
@@ -884,7 +886,7 @@ Cutting cut_product(int64_t M, int64_t N, int64_t K, int dtype, bool b_major) {
       const int64_t m = pair ? 256 : 128;
       c.tiles = (M + m - 1) / m * c.tiles_n;
       const int64_t machine = pair ? kSms / 2 : kSms;
-      const double chunk_us = (f32 ? 3.0 : 1.0) * 0.55 * (128 + (pair ? BN / 2 : BN)) / 384, tail_us = 1.5 + 0.01 * BN;
+      const double chunk_us = (f32 ? 3.0 : 1.0) * 0.45 * (128 + (pair ? BN / 2 : BN)) / 384, tail_us = 1.5 + 0.01 * BN;
       for (int splits = 1; splits <= 64; splits = splits < 8 ? splits + 1 : 2 * splits) {
         if (splits > 1 && (splits > chunks || c.tiles * (splits - 1) >= 2 * machine)) break;
         const int each = (chunks + splits - 1) / splits, used = (chunks + each - 1) / each;
