@@ -383,7 +383,8 @@ typedef enum mhla_activation {
  * Any k >= 1 and n >= 1 up to 2^20, rows < 2^31; every pointer 16-byte aligned
  * (MHLA_ERR_INVALID_ARG otherwise).  out and pre overlap neither one another nor
  * an input (out as residual aside).  float32 accumulation, results rounded once;
- * float32 operands enter the tensor cores as three bf16 terms (2^-24).  Few rows (8;
+ * float32 operands enter the tensor cores as three bf16 terms (2^-24), with which an
+ * infinity among them may give NaN for an infinite result.  Few rows (8;
  * in bf16 with k % 8 == 0 up to 64, while rows * k <= 65536) run in a kernel of
  * their own that reads w once.  Operands that TMA does not take as they lie (float32, k % 8 != 0) are laid
  * out in the workspace.  workspace as for mhla_forward.  Asynchronous on stream;

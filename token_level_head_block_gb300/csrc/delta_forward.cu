@@ -525,6 +525,7 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
 #pragma unroll
     for (int r = 0; r < 16; ++r) block[r * PITCH + lane] = x[r];
   }
+  if (!second) ptx::named_bar_sync(1, THREADS / 2);   // the diagonal blocks are inverted; the other warps have the images meanwhile
   if (second && h % times == 0) {   // the key head's images, by its first head
     const float by = scale_of(__uint_as_float(most)).to;
     auto put = [&](char* to, const uint32_t (&x)[L::kIn][4]) {
@@ -563,7 +564,6 @@ __global__ void __launch_bounds__(Prepare<T, DK>::kThreads, DK < 128 ? 3 : 1) de
       plane_halves<T, DK>(p.im.q + at_key * L::kInputHalf, smem + P::kQ, plane_scale(most_q).to, threadIdx.x - THREADS / 2, THREADS / 2);
     }
   }
-  __syncthreads();
   {
     float Z[TILES][2][4];
     if (!second) invert_column<TILES, PITCH>(inv, Z, strip, lane);
