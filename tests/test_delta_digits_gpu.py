@@ -1,0 +1,149 @@
+"""The delta rule's digits: results against bounds made of the very terms that are summed for them (delta_bounds.py), so that a token, a
+state or a head is held to its own size and not to the largest of the call."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import token_level_head_block_gb300 as mhla
+
+from . import delta_bounds as db
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+INPUTS = ("q", "k", "v", "g", "beta")
+GRADS = ("dq", "dk", "dv", "dg", "dbeta", "dstate")
+
+
+def draw(seed, B, N, Hk, times, d, dtype, state=True, remember=3.0):
+    r = np.random.default_rng(seed)
+    H = Hk * times
+    f = lambda *s: torch.from_numpy(r.standard_normal(s).astype(np.float32))
+    x = {"q": f(B, N, Hk, d), "k": f(B, N, Hk, d), "v": f(B, N, H, d), "dout": f(B, N, H, d)}
+    x["k"] = x["k"] / x["k"].norm(dim=-1, keepdim=True) * 0.99
+    x["g"] = torch.nn.functional.logsigmoid(f(B, N, H) + remember)
+    x["beta"] = f(B, N, H).sigmoid()
+    x = {n: t.to(DT[dtype]) for n, t in x.items()}
+    x["state"] = f(B, H, d, d) if state else None
+    x["dstate_out"] = f(B, H, d, d) if state else None
+    return x
+
+
+def f64(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+def gpu(t):
+    return None if t is None else t.to(DEV)
+
+
+def doubles(x):
+    return {n: f64(t) for n, t in x.items()}
+
+
+def forward(x, scale):
+    out, last = mhla.delta_forward(*(gpu(x[n]) for n in INPUTS), scale=scale, state=gpu(x["state"]))
+    torch.cuda.synchronize()
+    assert mhla.device_status() == 0
+    return out, last
+
+
+def check_forward(x, dtype, scale, out, last):
+    want, end = db.chunk_form(doubles(x), dtype, scale)
+    off, bound = db.over_axes(f64(out) - want.x, -1), db.out_bound(want, dtype)
+    assert (off <= bound).all(), f"out: {(off / bound).max():.2f} of what is allowed"
+    off, bound = db.over_axes(f64(last) - end.x, (-2, -1)), db.state_bound(end)
+    assert (off <= bound).all(), f"state: {(off / bound).max():.2f} of what is allowed"
+    return want, end
+
+
+def check_backward(x, dtype, scale, got):
+    for name, y, a in zip(GRADS, db.chunk_form(doubles(x), dtype, scale, back=True), got):
+        bound, axes = db.grad_bound(name, y, dtype)
+        off = db.over_axes(f64(a) - y.x, axes)
+        assert np.isfinite(off).all() and (off <= bound).all(), f"{name}: {(off / bound).max():.2f} of what is allowed"
+
+
+def backward(x, scale):
+    got = mhla.delta_backward(*(gpu(x[n]) for n in INPUTS), gpu(x["dout"]), scale=scale, state=gpu(x["state"]),
+                              dstate_out=gpu(x["dstate_out"]))
+    torch.cuda.synchronize()
+    assert mhla.device_status() == 0
+    return got
+
+
+# around the chunks of 32 and 64 tokens, several of them, head sizes on and off the tiles, shared keys, two tiles a CTA (24 heads
+# and more of 64 channels)
+SHAPES = [(1, 1, 1, 1, 64), (2, 64, 1, 2, 64), (1, 65, 1, 1, 128), (2, 129, 1, 3, 64), (1, 200, 2, 1, 48), (1, 130, 2, 1, 7),
+          (2, 300, 1, 2, 100), (1, 700, 2, 1, 64), (1, 33, 1, 2, 32), (1, 260, 1, 2, 128), (3, 150, 7, 2, 64), (2, 70, 20, 1, 48)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("state", [True, False], ids=["state", "empty"])
+def test_forward(shape, state, dtype):
+    x = draw(sum(shape), *shape, dtype, state)
+    check_forward(x, dtype, shape[4] ** -0.5, *forward(x, shape[4] ** -0.5))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("state", [True, False], ids=["state", "empty"])
+def test_backward(shape, state, dtype):
+    x = draw(sum(shape) + 1, *shape, dtype, state)
+    check_backward(x, dtype, shape[4] ** -0.5, backward(x, shape[4] ** -0.5))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1e-12, 1e-6, 1e6])
+def test_gradients_of_every_size(size, dtype):
+    """Gradients are linear in what comes back: dout and dstate_out a power of two times others give that times the bits, as long as
+    no result leaves the type's normal range."""
+    x = draw(9, 1, 150, 2, 2, 64, dtype)
+    by = 2.0 ** round(np.log2(size))
+    one = backward(x, 0.125)
+    many = backward({**x, "dout": x["dout"] * by, "dstate_out": x["dstate_out"] * by}, 0.125)
+    assert all(torch.equal(a.double() * by, b.double()) for a, b in zip(one, many))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_what_lies_around_the_results_stays(dtype):
+    """Odd sizes and rows of their own length: nothing is written in front of, between or behind the results."""
+    for B, N, Hk, times, d in [(2, 67, 1, 2, 33), (1, 1, 1, 1, 1), (1, 64, 2, 1, 7), (2, 130, 1, 3, 100)]:
+        H = Hk * times
+        x = draw(d, B, N, Hk, times, d, dtype)
+        rooms = []
+
+        def room(heads, width=None):
+            """[B, N, heads(, width)] inside a larger array of sevens, and what is not of it."""
+            shape = (B + 2, N + 2, heads + 1) + ((width + 3,) if width else ())
+            whole = torch.full(shape, 7.0, dtype=DT[dtype], device=DEV)
+            part = whole[1:B + 1, 1:N + 1, :heads, 1:width + 1] if width else whole[1:B + 1, 1:N + 1, :heads]
+            mask = torch.ones(shape, dtype=torch.bool, device=DEV)
+            (mask[1:B + 1, 1:N + 1, :heads, 1:width + 1] if width else mask[1:B + 1, 1:N + 1, :heads]).fill_(False)
+            rooms.append((whole, mask))
+            return part
+
+        def square():
+            whole = torch.full((B * H * d * d + 200,), 7.0, device=DEV)
+            mask = torch.ones_like(whole, dtype=torch.bool)
+            mask[100:-100] = False
+            rooms.append((whole, mask))
+            return whole[100:-100].view(B, H, d, d)
+
+        args = [gpu(x[n]) for n in INPUTS]
+        got = mhla.delta_forward(*args, scale=0.2, state=gpu(x["state"]), out=room(H, d), state_out=square())
+        grads = mhla.delta_backward(*args, gpu(x["dout"]), scale=0.2, state=gpu(x["state"]), dstate_out=gpu(x["dstate_out"]),
+                                    dq=room(Hk, d), dk=room(Hk, d), dv=room(H, d), dg=room(H), dbeta=room(H), dstate=square())
+        state = square()
+        state.copy_(gpu(x["state"]))
+        one = mhla.delta_step(*(t[:, :1] for t in args), state, scale=0.2, out=room(H, d)[:, :1])
+        torch.cuda.synchronize()
+        assert all((whole[mask] == 7).all() for whole, mask in rooms)
+        check_forward(x, dtype, 0.2, *got)
+        check_backward(x, dtype, 0.2, grads)
+        first, after = oracle.delta(*(f64(x[n][:, :1]) for n in INPUTS), 0.2, f64(x["state"]))
+        assert np.abs(f64(one) - first).max() <= 2 * db.HALF[dtype] * np.abs(first).max() + 1e-5
+        assert np.abs(f64(state) - after).max() <= 1e-5 * np.abs(after).max()
