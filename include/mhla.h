@@ -580,7 +580,7 @@ mhla_status_t mhla_gated_step(const mhla_tensor_t* q, const mhla_tensor_t* k, co
  * Chunks of 64 tokens (float32: 32) on the tensor cores.  A chunk is a
  * triangular solve and products.  What reaches the state enters the tensor cores as
  * three bf16 terms (2^-24) or as two of fp16 at the scale of its block (2^-22 of a
- * value, 2^-25 of the block's largest); what only reaches bf16 outputs as one (2^-11).
+ * value, 2^-39 of the block's largest); what only reaches bf16 outputs as one (2^-11, 2^-39).
  * The same call gives the same bits.
  * From the first token whose k, g or beta is not finite (g: but for -infinity),
  * out and the state are NaN; one in v does this to its channel alone, one in q to
@@ -607,8 +607,8 @@ mhla_status_t mhla_delta_forward(const mhla_tensor_t* q, const mhla_tensor_t* k,
  *                heads that share them, in float32);  dg, dbeta  like g.
  *   dstate_in    device float32 [B][H][d][d], or NULL when not wanted.
  * dg_t is summed from what has the gate between its two tokens, as in
- * mhla_gated_backward.  A factor of a chunk is known to 2^-11 of itself and 2^-25
- * of the largest it is summed with (float32: 2^-22, 2^-25); dout counts token by
+ * mhla_gated_backward.  A factor of a chunk is known to 2^-11 of itself and 2^-39
+ * of the largest it is summed with (float32: 2^-22, 2^-39); dout counts token by
  * token, so dq is right for the size of its own token's dout.  The states are
  * recomputed.
  * The written tensors share no element with one another or with an input (views

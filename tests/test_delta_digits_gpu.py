@@ -97,6 +97,37 @@ def test_backward(shape, state, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what", [("v",), ("q", "v", "dout")], ids=["values", "all"])
+def test_values_over_six_decades(what, dtype):
+    """From token to token: each token's output is right for what that token and those before it put into it."""
+    x = draw(5, 1, 200, 2, 1, 64, dtype, False)
+    r = np.random.default_rng(6)
+    for name in what:
+        x[name] = (x[name].double() * torch.from_numpy(10.0 ** (-6 * r.random((1, 200, 2, 1))))).to(DT[dtype])
+    check_forward(x, dtype, 0.125, *forward(x, 0.125))
+    check_backward(x, dtype, 0.125, backward(x, 0.125))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_small_token_in_front_of_a_large_one(dtype):
+    """The first token of a sequence, its value 1e-6 of the next one's: its output is w_0 (q . k) scale of its own value alone."""
+    x = draw(7, 1, 16, 1, 1, 64, dtype, False)
+    x["v"][:, 0] = (x["v"][:, 0].float() * 1e-6).to(DT[dtype])
+    x["beta"][:, 0] = 1.0
+    out, _ = forward(x, 0.125)
+    y = doubles(x)
+    score = 0.125 * (y["q"][0, 0, 0] @ y["k"][0, 0, 0])
+    want = score * y["v"][0, 0, 0]
+    # bf16: its score and its w as one fp16 each, the result's rounding; float32: three factors of 2^-22.  A channel of 16 tokens' w has one
+    # scale: fp16's last bit, 2^-24 where the largest is at least 2^14, rounds by half of it, so 2^-39 of that largest
+    share = 2 * 2.0 ** -11 + 2.0 ** -8 if dtype == "bf16" else 2.0 ** -17
+    w = oracle.delta(*(y[n] for n in INPUTS), 0.125, steps=True)[3][0, :, 0]
+    allowed = share * np.abs(want) + abs(score) * 2.0 ** -39 * np.abs(w).max(0)
+    assert (np.abs(f64(out)[0, 0, 0] - want) <= allowed).all()
+    assert np.linalg.norm(allowed) <= 0.01 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("size", [1e-12, 1e-6, 1e6])
 def test_gradients_of_every_size(size, dtype):
     """Gradients are linear in what comes back: dout and dstate_out a power of two times others give that times the bits, as long as

@@ -21,9 +21,11 @@ using namespace gated;
 
 // How values enter the tensor cores.
 //
-// The chain, from chunk to chunk, takes fp16 at a scale: a block's largest value is brought to [1, 2) by a power of two, and
-// a value is then one fp16 (2^-11 of it, or 2^-25 of the largest), or two (2^-22, 2^-25).  What reaches the float32 state
-// (the state, w, K^) takes two; bf16 inputs are exact in one but for that 2^-25; what only feeds bf16 outputs takes one.  Three products
+// The chain, from chunk to chunk, takes fp16 at a scale: a block's largest value is brought to [2^14, 2^15) by a power of two, near
+// fp16's end, so that its last bit, 2^-24, lies as far below as it can; sums of 128 products of two such values stay below 2^37.
+// A value is then one fp16 (2^-11 of it, or 2^-39 of the largest), or two (2^-22, 2^-39).  Brought to [1, 2) a token's value of 1e-6 of a
+// later one's in its block was 2% off, which a causal result may not be.  What reaches the float32 state
+// (the state, w, K^) takes two; bf16 inputs are exact in one but for that 2^-39; what only feeds bf16 outputs takes one.  Three products
 // of two such terms stand for six of three bf16 ones, and the chain's time is its products.  A scale belongs to 16 columns of
 // a row of the state or of w, to 16 rows of K^, to a row of Q or the scores, to a chunk of K.
 //
@@ -111,13 +113,14 @@ struct Common {
 };
 enum : uint32_t { kWideQ = 1, kWideK = 2, kWideV = 4, kWideDout = 8 };
 
-// fp16 at a scale: the power of two that brings `most` to [1, 2), and what undoes it.
+// fp16 at a scale: the power of two that brings `most` to [2^14, 2^15), and what undoes it; both are normal.
 struct Scale {
   float to, from;
 };
 __device__ __forceinline__ Scale scale_of(float most) {
-  const uint32_t e = min(max(__float_as_uint(most) >> 23, 1u), 253u);
-  return Scale{__uint_as_float((254u - e) << 23), __uint_as_float(e << 23)};
+  constexpr uint32_t kUp = 14;
+  const uint32_t e = min(max(__float_as_uint(most) >> 23, kUp + 1), 254u);
+  return Scale{__uint_as_float((254u + kUp - e) << 23), __uint_as_float((e - kUp) << 23)};
 }
 // The scale of a whole plane of a chunk, from the bits of its largest; with an infinity in it all of it becomes NaN, not zero.
 __device__ __forceinline__ Scale plane_scale(uint32_t most) {
