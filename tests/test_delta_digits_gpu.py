@@ -50,6 +50,16 @@ def forward(x, scale):
     return out, last
 
 
+def steps(x, scale):
+    """The same tokens one call each, from the same state."""
+    B, N, H, d = x["v"].shape
+    args = [gpu(x[n]) for n in INPUTS]
+    state = torch.zeros(B, H, d, d, device=DEV) if x["state"] is None else gpu(x["state"])
+    rows = [mhla.delta_step(*(t[:, i:i + 1] for t in args), state, scale=scale) for i in range(N)]
+    torch.cuda.synchronize()
+    return torch.cat(rows, 1), state
+
+
 def check_forward(x, dtype, scale, out, last):
     want, end = db.chunk_form(doubles(x), dtype, scale)
     off, bound = db.over_axes(f64(out) - want.x, -1), db.out_bound(want, dtype)
@@ -94,6 +104,42 @@ def test_forward(shape, state, dtype):
 def test_backward(shape, state, dtype):
     x = draw(sum(shape) + 1, *shape, dtype, state)
     check_backward(x, dtype, shape[4] ** -0.5, backward(x, shape[4] ** -0.5))
+
+
+def fading(tokens, last, g, beta, dtype, d=64, state=False):
+    """A chunk's tokens of full strength, then `last` ones that fade and write little."""
+    x = draw(tokens + last, 1, tokens, 2, 1, d, dtype, state)
+    x["g"][:, -last:] = g
+    x["beta"][:, -last:] = beta
+    return x
+
+
+# a whole chunk of either type and a ragged one behind another; powers of two, so that a type's rounding does not matter
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens", [32, 64, 90])
+@pytest.mark.parametrize("last,g,beta", [(8, -0.5, 0.0), (8, -1.0, 0.0), (12, -1.0, 0.0), (12, -1.0, 2.0 ** -13), (16, -1.0, 0.0),
+                                         (16, -1.0, 2.0 ** -13), (16, -2.0, 0.0)])
+def test_state_of_a_chunk_that_fades(last, g, beta, tokens, dtype):
+    """What is left of a chunk's writes at its end is right for its own size, and the states that the gradients are formed
+    with are those of the forward."""
+    x = fading(tokens, last, g, beta, dtype)
+    out, end = forward(x, 0.125)
+    want, ref = check_forward(x, dtype, 0.125, out, end)
+    assert (db.state_bound(ref) <= 1e-5 * db.over_axes(ref.x, (-2, -1))).all()
+    _, one = steps(x, 0.125)
+    assert (db.over_axes(f64(one) - f64(end), (-2, -1)) <= 2 * db.state_bound(ref)).all()
+    check_backward(x, dtype, 0.125, backward(x, 0.125))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tokens_behind_a_fading_chunk_read_what_is_left(dtype):
+    """Chunks that end in fading, each read by tokens whose queries lift what is left to ordinary size."""
+    x = draw(3, 1, 200, 2, 1, 64, dtype, False)
+    for t in range(0, 200, 64):
+        x["g"][:, t + 48:t + 64] = -1.0
+        x["beta"][:, t + 48:t + 64] = 0.0
+    check_forward(x, dtype, 0.125, *forward(x, 0.125))
+    check_backward(x, dtype, 0.125, backward(x, 0.125))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

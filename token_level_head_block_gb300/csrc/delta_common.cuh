@@ -27,7 +27,7 @@ using namespace gated;
 // later one's in its block was 2% off, which a causal result may not be.  What reaches the float32 state
 // (the state, w, K^) takes two; bf16 inputs are exact in one but for that 2^-39; what only feeds bf16 outputs takes one.  Three products
 // of two such terms stand for six of three bf16 ones, and the chain's time is its products.  A scale belongs to 16 columns of
-// a row of the state or of w, to 16 rows of K^, to a row of Q or the scores, to a chunk of K.
+// a row of the state, of w or of e^{B-b} w, to 16 rows of K^, to a row of Q or the scores, to a chunk of K.
 //
 // In delta_prepare, and in what delta_back forms ahead, values are sums of bf16 terms, which need no scale: an input one (bf16) or three
 // (float32), a value that reaches the state three (2^-24).  delta_grads takes every plane of a chunk as fp16 at one scale,

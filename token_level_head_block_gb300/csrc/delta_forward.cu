@@ -735,8 +735,9 @@ struct ScanLay {
   static constexpr int kStatePlane = 16 * MT * DK * 2, kTokenPlane = 16 * MT * L::C * 2;
   // the state, e^{B-b} W and (for the outputs) W, and the scales of their rows
   static constexpr int kState = 0, kAfter = kState + 2 * kStatePlane, kW = kAfter + 2 * kTokenPlane;
-  static constexpr int kStateScale = kW + (KEEP ? 0 : L::kHalves * kTokenPlane), kTokenScale = kStateScale + 16 * MT * L::kSides * 4;
-  static constexpr int kRing = (kTokenScale + 16 * MT * L::kTiles * 4 + 127) / 128 * 128;
+  static constexpr int kStateScale = kW + (KEEP ? 0 : L::kHalves * kTokenPlane), kAfterScale = kStateScale + 16 * MT * L::kSides * 4;
+  static constexpr int kTokenScales = 16 * MT * L::kTiles * 4, kWScale = kAfterScale + kTokenScales;
+  static constexpr int kRing = (kWScale + (KEEP ? 0 : kTokenScales) + 127) / 128 * 128;
   // of a chunk, a pair of warps': blocks of K^, U, K, and of Q and the scores
   static constexpr int kKeysBytes = L::kSides * 2 * kBlock, kUBytes = 2 * kBlock, kAddBytes = kShare * L::kTiles * L::kHalves * kBlock;
   static constexpr int kQBytes = KEEP ? 0 : L::kSides * L::kHalves * kBlock, kScoreBytes = KEEP ? 0 : L::kTiles * L::kHalves * kBlock;
@@ -854,7 +855,7 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
             o[f][2] = fmaf(c[2], s0, o[f][2]); o[f][3] = fmaf(c[3], s1, o[f][3]);
           }
         };
-        const float *state_scale = reinterpret_cast<const float*>(smem + W::kStateScale), *token_scale = reinterpret_cast<const float*>(smem + W::kTokenScale);
+        const float *state_scale = reinterpret_cast<const float*>(smem + W::kStateScale), *token_scale = reinterpret_cast<const float*>(smem + W::kWScale);
 #pragma unroll
         for (int ks = 0; ks < SIDES; ++ks) {
           uint32_t q[L::kHalves][4];
@@ -988,27 +989,27 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
     }
     const float2 after[2] = {*reinterpret_cast<const float2*>(m->after + 16 * own + t), *reinterpret_cast<const float2*>(m->after + 16 * own + 8 + t)};
     const float total = m->total;
-    // W and e^{B-b} W share a scale
+    // e^{B-b} W, which reaches the state, and W each at its own scale: where a chunk fades towards its end the first is far below the
+    // second, and at W's scale would end below fp16's last bit
 #pragma unroll
     for (int n = 0; n < MT; ++n)
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        float x[4], z[4];
+        float x[4], z[4], most = 0.0f, most_z = 0.0f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           x[e] = w[n][e >> 1][2 * f + (e & 1)];
           z[e] = x[e] * (e & 1 ? after[e >> 1].y : after[e >> 1].x);
+          most = fmaxf(most, fabsf(x[e]));
+          most_z = fmaxf(most_z, fabsf(z[e]));
         }
-        float most = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) most = fmaxf(most, KEEP ? fabsf(z[e]) : fmaxf(fabsf(x[e]), fabsf(z[e])));
-        const Scale by = scale_of(over_row(most));
+        const Scale by_z = scale_of(over_row(most_z)), by = KEEP ? by_z : scale_of(over_row(most));
         const int row = 16 * n + g + 8 * f;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int to = unit_at<C>(row, 2 * own + j) + 2 * t;
           uint32_t h[2];
-          halves<2>(z[2 * j] * by.to, z[2 * j + 1] * by.to, h);
+          halves<2>(z[2 * j] * by_z.to, z[2 * j + 1] * by_z.to, h);
 #pragma unroll
           for (int k = 0; k < 2; ++k) *reinterpret_cast<uint32_t*>(smem + W::kAfter + k * W::kTokenPlane + to) = h[k];
           if (!KEEP) {
@@ -1018,7 +1019,10 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
             for (int k = 0; k < L::kHalves; ++k) *reinterpret_cast<uint32_t*>(smem + W::kW + k * W::kTokenPlane + to) = y[k];
           }
         }
-        if ((lane & 3) == 0) reinterpret_cast<float*>(smem + W::kTokenScale)[row * TILES + own] = by.from;
+        if ((lane & 3) == 0) {
+          reinterpret_cast<float*>(smem + W::kAfterScale)[row * TILES + own] = by_z.from;
+          if (!KEEP) reinterpret_cast<float*>(smem + W::kWScale)[row * TILES + own] = by.from;
+        }
       }
     sync();   // W's planes are there, the state's are read
     if (KEEP)
@@ -1048,7 +1052,7 @@ __global__ void __launch_bounds__(ScanLay<T, DK, MT, KEEP>::kThreads) delta_scan
             for (int k = 0; k < L::kHalves; ++k) load_block(x[pair & 1][h][j][k], st + W::kAdd, (j * TILES + ks) * L::kHalves + k, lane);
         }
       };
-      const float* scales = reinterpret_cast<const float*>(smem + W::kTokenScale) + g * TILES;
+      const float* scales = reinterpret_cast<const float*>(smem + W::kAfterScale) + g * TILES;
       fetch(0);
 #pragma unroll
       for (int pair = 0; pair < TILES / 2; ++pair) {
