@@ -60,10 +60,32 @@ __device__ __forceinline__ float over_sigmoid(float z) { return 1.0f + (FAST ? _
 
 constexpr float kTanhScale = 0.7978845608028654f, kTanhCube = 0.044715f;   // sqrt(2 / pi)
 
+// Phi(z) = erfc(-z / sqrt 2) / 2; (1 + erf(z / sqrt 2)) / 2 cancels for z < 0, 4% off at -5.  FAST: Phi(-s) = e^(-s^2 / 2) P(t), t = 1 / (1 +
+// 0.265 s), P a polynomial without a constant term fitted to the quotient over [0, 15] for the least relative error (Remez's criterion by reweighted
+// least squares in 64 bits), 2^-20; behind that the exponential is 0.  `e` receives e^(-z^2 / 2).  [16384, 768] x 2304, z kept, and
+// its gradients, called: erff 70 and 173 us, erfcf 97 and 200, this 71 and 161; float32 erff 315 and 700, erfcf 348 and 722.
+template <bool FAST>
+__device__ __forceinline__ float normal_below(float z, float& e) {
+  e = FAST ? __expf(-0.5f * z * z) : expf(-0.5f * z * z);
+  if (!FAST) return 0.5f * erfcf(z * -0.7071067811865476f);
+  const float t = __fdividef(1.0f, fmaf(0.265f, fabsf(z), 1.0f));
+  float p = fmaf(-0.067709036f, t, 0.195002005f);
+  p = fmaf(p, t, -0.065985590f);
+  p = fmaf(p, t, 0.142225206f);
+  p = fmaf(p, t, 0.083048776f);
+  p = fmaf(p, t, 0.107817046f);
+  p = fmaf(p, t, 0.105601341f);
+  const float q = p * t * e;
+  return z < 0.0f ? q : 1.0f - q;
+}
+
 template <bool FAST, int ACT>
 __device__ __forceinline__ float activate(float z) {
   if (ACT == MHLA_ACT_RELU) return z < 0.0f ? 0.0f : z;   // NaN stays
-  if (ACT == MHLA_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
+  if (ACT == MHLA_ACT_GELU) {
+    float e;
+    return z * normal_below<FAST>(z, e);
+  }
   if (ACT == MHLA_ACT_GELU_TANH) {   // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
     const float u = kTanhScale * fmaf(kTanhCube * z * z, z, z);
     return FAST ? __fdividef(z, over_sigmoid<true>(2.0f * u)) : z / over_sigmoid<false>(2.0f * u);
@@ -94,9 +116,11 @@ __device__ __forceinline__ float sigmoid(float z) { return FAST ? __fdividef(1.0
 template <bool FAST, int ACT>
 __device__ __forceinline__ float slope(float z) {
   if (ACT == MHLA_ACT_RELU) return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
-  if (ACT == MHLA_ACT_GELU)
-    return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) +
-           z * 0.3989422804014327f * (FAST ? __expf(-0.5f * z * z) : expf(-0.5f * z * z));
+  if (ACT == MHLA_ACT_GELU) {
+    float e;
+    const float below = normal_below<FAST>(z, e);
+    return fmaf(z * 0.3989422804014327f, e, below);
+  }
   if (ACT == MHLA_ACT_GELU_TANH) {
     z = z > 30.0f ? 30.0f : z < -30.0f ? -30.0f : z;   // 1 and 0 there; the cube stays finite
     const float u = kTanhScale * fmaf(kTanhCube * z * z, z, z), p = sigmoid<FAST>(2.0f * u);
