@@ -604,7 +604,8 @@ mhla_status_t mhla_delta_forward(const mhla_tensor_t* q, const mhla_tensor_t* k,
  *   q, k, v, g, beta, scale, state_in   those of the forward, finite (g: or -infinity);
  *   what is not leaves the gradients of its sequence and head without a meaning.
  *   dout, dv     device tensors shaped like v;  dq, dk  like q (summed over the
- *                heads that share them, in float32);  dg, dbeta  like g.
+ *                heads that share them, in float32; MHLA_ERR_SHAPE where H is 0
+ *                and Hk is not);  dg, dbeta  like g.
  *   dstate_in    device float32 [B][H][d][d], or NULL when not wanted.
  * dg_t is summed from what has the gate between its two tokens, as in
  * mhla_gated_backward.  A factor of a chunk is known to 2^-11 of itself and 2^-39
