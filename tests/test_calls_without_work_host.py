@@ -30,3 +30,13 @@ def test_gradients_of_keys_that_no_value_head_reads_are_refused(L):
     assert L.mhla_delta_forward(*args, 1.0, None, none(5), None, None, 0, None) == OK
     assert L.mhla_delta_backward(*args, none(5), 1.0, None, None, keys(6), keys(7), none(8), none(9, 1), none(10, 1), None, None, 0,
                                  None) == SHAPE
+
+
+def test_pre_is_not_looked_at_without_an_activation(L):
+    """With MHLA_ACT_NONE it may be anything, the place of a result too: the checks end at the workspace, made too small here."""
+    n = ctypes.c_size_t()
+    assert L.mhla_linear_act_backward_workspace_size(300, 64, 96, 0, 0, ctypes.byref(n)) == OK and n.value > 0
+    for pre in (None, at(3), at(3, 8), at(4), at(5), at(6)):
+        got = L.mhla_linear_act_backward(at(0), at(1), at(2), pre, 0, at(4), at(5), at(6), 300, 64, 96, 0, at(9), n.value - 1, None)
+        assert got == WORKSPACE
+    assert L.mhla_linear_act_backward(at(0), at(1), at(2), at(4), 4, at(4), at(5), at(6), 300, 64, 96, 0, at(9), 16, None) == INVALID

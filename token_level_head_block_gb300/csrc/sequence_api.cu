@@ -533,6 +533,7 @@ extern "C" mhla_status_t mhla_linear_act_backward(const void* x, const void* w, 
                                                   void* stream) {
   const int rc = check_linear(rows, k, n, dtype, activation);
   if (rc != MHLA_OK) return static_cast<mhla_status_t>(rc);
+  if (activation == MHLA_ACT_NONE) pre = nullptr;   // unused, whatever it is
   if (!all_aligned({x, w, dout, pre, dx, dw, dbias})) return MHLA_ERR_INVALID_ARG;
   const int64_t e = elem_bytes(dtype);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
