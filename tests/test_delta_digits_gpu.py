@@ -224,3 +224,41 @@ def test_what_lies_around_the_results_stays(dtype):
         first, after = oracle.delta(*(f64(x[n][:, :1]) for n in INPUTS), 0.2, f64(x["state"]))
         assert np.abs(f64(one) - first).max() <= 2 * db.HALF[dtype] * np.abs(first).max() + 1e-5
         assert np.abs(f64(state) - after).max() <= 1e-5 * np.abs(after).max()
+
+
+# two tiles of 16 columns a CTA, the widest heads, the narrowest, shared keys
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,Hk,times,d", [(3, 7, 2, 64), (4, 13, 1, 48), (1, 1, 2, 128), (1, 2, 1, 32), (2, 1, 3, 7)])
+def test_fading_in_every_form_of_the_scan(B, Hk, times, d, dtype):
+    x = draw(d, B, 100, Hk, times, d, dtype, False)
+    for t in (20, 52, 88):                             # inside chunks of both types, the last one at the end
+        x["g"][:, t:t + 12] = -1.0
+        x["beta"][:, t:t + 12] = 0.0
+    check_forward(x, dtype, d ** -0.5, *forward(x, d ** -0.5))
+    check_backward(x, dtype, d ** -0.5, backward(x, d ** -0.5))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("beta", [1.0, 2.0])
+def test_strengths_at_their_end(beta, dtype):
+    """Unit keys written at full strength, and reflected (2): the state stays bounded, the triangular solve does not decay."""
+    x = draw(31, 1, 150, 2, 1, 64, dtype)
+    x["beta"][:] = beta
+    check_forward(x, dtype, 0.125, *forward(x, 0.125))
+    check_backward(x, dtype, 0.125, backward(x, 0.125))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what,value", [(w, float(x)) for w in ("k", "g", "beta", "v", "q") for x in ("nan", "inf")] + [("q", 1e30)])
+def test_tokens_in_front_of_one_that_is_not_finite(what, value, dtype):
+    """They keep their own digits, whatever stands behind them in their block of 16 or their chunk; so do other heads."""
+    x = draw(33, 1, 70, 2, 1, 48, dtype)
+    at, head = 21, 1
+    want, _ = db.chunk_form(doubles(x), dtype, 0.2)
+    if what in ("g", "beta"):
+        x[what][0, at, head] = value
+    else:
+        x[what][0, at, head, 5] = value
+    out, _ = forward(x, 0.2)
+    off, bound = db.over_axes(f64(out) - want.x, -1), db.out_bound(want, dtype)
+    assert (off <= bound)[:, :at].all() and (off <= bound)[:, :, 0].all()
