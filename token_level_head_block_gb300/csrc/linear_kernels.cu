@@ -378,9 +378,10 @@ __global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(
       bool ok = true;
       const int b_rows = PAIR ? p.BN / 2 : p.BN;
       const uint32_t bytes = TERMS * (L::A_BYTES + b_rows * L::BK * 2);
+      const uint32_t full_of_0 = PAIR ? address_at(full, 0) : 0u;   // rank 0's barriers count both CTAs' bytes
       auto load = [&](uint8_t* at, const CUtensorMap* map, int st, int32_t x, int32_t y, int32_t z) {
         if (PAIR)
-          tma_load_3d_pair(at, map, full + st, x, y, z, policy);
+          tma_load_3d_pair(at, map, full_of_0 + 8 * st, x, y, z, policy);
         else
           tma_load_3d(at, map, full + st, x, y, z, policy);
       };
@@ -389,7 +390,6 @@ __global__ void __launch_bounds__(GemmLay<TERMS, PAIR>::THREADS, 1) linear_gemm(
         const int32_t n0 = un.n0 + static_cast<int32_t>(rank) * b_rows;
         for (int kc = 0; kc < un.count; ++kc) {
           if (!wait_bounded(empty + s, ph ^ 1u, abortf)) { ok = false; break; }
-          // rank 0's barrier counts both CTAs' bytes
           if (rank == 0) mbar_arrive_expect_tx(full + s, (PAIR ? 2 : 1) * bytes);
           uint8_t* st = smem + s * L::STAGE;
           const int32_t k0 = (un.first + kc) * L::BK;
