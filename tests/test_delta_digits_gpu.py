@@ -262,3 +262,35 @@ def test_tokens_in_front_of_one_that_is_not_finite(what, value, dtype):
     out, _ = forward(x, 0.2)
     off, bound = db.over_axes(f64(out) - want.x, -1), db.out_bound(want, dtype)
     assert (off <= bound)[:, :at].all() and (off <= bound)[:, :, 0].all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what", ["k", "beta"])
+def test_keys_and_strengths_over_six_decades(what, dtype):
+    """Tokens that write a millionth of what others do, and read as little of the state for it."""
+    x = draw(41, 1, 200, 2, 1, 64, dtype)
+    r = np.random.default_rng(42)
+    by = torch.from_numpy(10.0 ** (-6 * r.random((1, 200, 2))))
+    x[what] = (x[what].double() * (by[..., None] if what == "k" else by)).to(DT[dtype])
+    check_forward(x, dtype, 0.125, *forward(x, 0.125))
+    check_backward(x, dtype, 0.125, backward(x, 0.125))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_padding_of_ordinary_size(dtype):
+    """Rows padded in front and behind by tokens that are there but write nothing (beta = 0, g = 0), with any k of the others' size: out and
+    state as without them; and the gradients of the tokens between."""
+    N, front, behind, d = 90, 37, 21, 64
+    x = draw(43, 1, front + N + behind, 2, 1, d, dtype)
+    for cut in (slice(0, front), slice(front + N, None)):
+        x["beta"][:, cut] = 0
+        x["g"][:, cut] = 0
+        x["dout"][:, cut] = 0
+    mid = slice(front, front + N)
+    short = {n: (t[:, mid].contiguous() if n in INPUTS + ("dout",) else t) for n, t in x.items()}
+    out, last = forward(x, 0.125)
+    check_forward(short, dtype, 0.125, out[:, mid], last)
+    dq, dk, dv, dg, dbeta, dstate = backward(x, 0.125)
+    check_backward(short, dtype, 0.125, (dq[:, mid], dk[:, mid], dv[:, mid], dg[:, mid], dbeta[:, mid], dstate))
+    for cut in (slice(0, front), slice(front + N, None)):
+        assert (dv[:, cut] == 0).all() and (dq[:, cut] == 0).all()
