@@ -575,12 +575,15 @@ mhla_status_t mhla_gated_step(const mhla_tensor_t* q, const mhla_tensor_t* k, co
  *               mhla_gated_forward.
  *   state_in, state_out, scale, workspace, stream, statuses and empty calls as
  *   for mhla_gated_forward.  A padding token with beta = 0 and g = 0 leaves
- *   the state as it is.
+ *   the state as it is; its k is finite and no larger than others (zeros, say):
+ *   the keys of a chunk share a scale, below.
  * The states and every sum are float32 or wider; bf16 results are rounded once.
  * Chunks of 64 tokens (float32: 32) on the tensor cores.  A chunk is a
  * triangular solve and products.  What reaches the state enters the tensor cores as
  * three bf16 terms (2^-24) or as two of fp16 at the scale of its block (2^-22 of a
  * value, 2^-39 of the block's largest); what only reaches bf16 outputs as one (2^-11, 2^-39).
+ * A block is 16 tokens of a channel of w, 16 rows of a column of the state, a row of q or of
+ * the scores, or the keys of a chunk.
  * The same call gives the same bits.
  * From the first token whose k, g or beta is not finite (g: but for -infinity),
  * out and the state are NaN; one in v does this to its channel alone, one in q to

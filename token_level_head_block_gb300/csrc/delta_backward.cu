@@ -12,7 +12,7 @@
 // it, what writes D in front of it, and e^B <S, D>; nothing cancels), every chunk does by itself: delta_grads.
 //
 // Measured, bf16 [4, 4096, 12, 64]:
-//   delta_prepare 132 us, delta_states (delta_scan with its states and W kept) 77
+//   delta_prepare 131 us, delta_states (delta_scan with its states and W kept) 74
 //   delta_back    126 us, 2.0 us a chunk: the chain's two products, which share an SM's issue slots with the warps beside it; one such warp
 //                 for two took 142
 //   delta_grads   213 us: 160 KB read and written a chunk (75 us of HBM's time), 40,000 cycles a chunk, two of them on an SM at once, of which

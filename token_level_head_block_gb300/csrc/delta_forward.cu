@@ -20,10 +20,11 @@
 //     them on an SM at once: 4,000 until its rows are there, 5,000 for T's blocks, 4,500 in the products of K^ and U, the rest in gates,
 //     scores and images; issue slots are 45% full, and the instruction cache misses one time in eight.  Scores formed while the other
 //     warps invert took 111 us for 107; the rows of the CTA that follows asked for as far as L2, 141 for 132 (with the gradients' images).
-//   delta_scan  107 and 1103 us: 96 CTAs of two tiles, 1.65 us a chunk, and 96 of one tile, 1.08 us: of 2,400 cycles (clocks read in
-//     between) 700 W's products, 400 its splitting, 550 the state's products, 450 its splitting, 250 at the barriers.  The chain alone, without
-//     outputs, takes 76 us for 107: the warps beside it share its issue slots and tensor cores.  One such warp for two took 105 and 1142.
-//     Asking L2 for a chunk's operands ahead of the copies took 1875 us for 1426.
+//   delta_scan  107 and 1180 us: 96 CTAs of two tiles, 1.65 us a chunk, and 96 of one tile, 1.15 us.  With W and e^{B-b} W at one
+//     scale the long scan took 1103, and the state lost its digits where a chunk fades; their two maxima through one pair of shuffles took
+//     1190.  Before that, of 2,400 cycles a chunk (clocks read in between) 700 W's products, 400 its splitting, 550 the state's products, 450 its
+//     splitting, 250 at the barriers; the chain alone, without outputs, 76 us for 105: the warps beside it share its issue slots and
+//     tensor cores; one such warp for two 1142 us for 1103.  Asking L2 for a chunk's operands ahead of the copies took 1875 us for 1426.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -1209,7 +1210,8 @@ namespace delta {
 // 126, 384 of them 218 / 264 against 207 / 247, but 128 of them, which all run at once, 76 / 92 against 107 / 126; d = 32, where
 // several CTAs of one tile fit on an SM, 384 of 2048 tokens 78 / 117 against 86 / 154 (when one warp stood beside each of the chain's).  float32
 // at 2048 tokens, d = 64: 192 tiles 85 / 96 against 99 / 125, 384 of them 161 / 186 against 193 / 148.  So the scan takes two for bf16
-// alone, and the gradients' chain beyond `most`, as many tiles as there are SMs for bf16 and twice as many for float32.
+// alone, and the gradients' chain beyond `most`, as many tiles as there are SMs for bf16 and twice as many for float32.  Heads of
+// 65 to 128 channels take one: two were not measured.
 bool two_tiles(int64_t BH, int d, int64_t most) { return d > 32 && BH * ((d + 15) / 16) > most; }
 
 int launch_prepare(const Common& c, int64_t BH, int dtype, bool grad, cudaStream_t s) {

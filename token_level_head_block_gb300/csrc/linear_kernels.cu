@@ -54,7 +54,8 @@ using gated::to_f;
 
 // ----------------------------------------------------------------- activations
 
-// 1 / (1 + e^-z); FAST for results that are rounded to bf16 (2^-8; ex2 and the reciprocal are good to 2^-21).
+// 1 + e^-z; FAST for results that are rounded to bf16 (2^-8; ex2 and the reciprocal are good to 2^-21; a quotient by 2^126 or
+// more is 0).
 template <bool FAST>
 __device__ __forceinline__ float over_sigmoid(float z) { return 1.0f + (FAST ? __expf(-z) : expf(-z)); }
 
