@@ -32,6 +32,13 @@ def test_gradients_of_keys_that_no_value_head_reads_are_refused(L):
                                  None) == SHAPE
 
 
+def test_gradients_of_no_sequences_have_nothing_to_write(L):
+    """B = 0: dq and dk have no elements whatever the heads."""
+    t = lambda heads, d=64: ctypes.byref(mhla.tensor_desc(0, "bf16", (0, 5, heads, d), (1, 1, 1)))
+    args = (t(2), t(2), t(0), t(0, 1), t(0, 1))
+    assert L.mhla_delta_backward(*args, t(0), 1.0, None, None, t(2), t(2), t(0), t(0, 1), t(0, 1), None, None, 0, None) == OK
+
+
 def test_pre_is_not_looked_at_without_an_activation(L):
     """With MHLA_ACT_NONE it may be anything, the place of a result too: the checks end at the workspace, made too small here."""
     n = ctypes.c_size_t()

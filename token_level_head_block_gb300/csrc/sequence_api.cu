@@ -298,7 +298,7 @@ extern "C" mhla_status_t mhla_delta_backward(const mhla_tensor_t* q, const mhla_
   if (!same_shape(v, dout) || !same_shape(v, dv) || !same_shape(q, dq) || !same_shape(q, dk) || !gate_shape(v, dg) ||
       !gate_shape(v, dbeta))
     return MHLA_ERR_SHAPE;
-  if (v->H == 0 && q->H > 0) return MHLA_ERR_SHAPE;   // nothing would write the elements of dq and dk
+  if (v->H == 0 && !empty(q)) return MHLA_ERR_SHAPE;   // nothing would write the elements of dq and dk
   if (empty(v)) return MHLA_OK;
   const mhla_tensor_t* all[] = {q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta};
   constexpr int kInputs = 6, kAll = 11;
