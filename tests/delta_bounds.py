@@ -197,3 +197,9 @@ def grad_bound(name, y, dtype):
     axes = (-2, -1) if name == "dstate" else (1, 3) if y.x.ndim == 4 else (1,)
     own = 2.0 ** -24 if name == "dstate" else HALF[dtype]
     return MARGIN * over_axes(y.e, axes) + own * over_axes(y.x, axes) + 1e-30, axes
+
+
+def token_bound(y, dtype):
+    """Of each token's own gradient, a row or a value."""
+    size = lambda z: over_axes(z, -1) if z.ndim == 4 else np.abs(z)
+    return MARGIN * size(y.e) + HALF[dtype] * size(y.x) + 1e-30, size

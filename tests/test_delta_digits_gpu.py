@@ -294,3 +294,21 @@ def test_padding_of_ordinary_size(dtype):
     check_backward(short, dtype, 0.125, (dq[:, mid], dk[:, mid], dv[:, mid], dg[:, mid], dbeta[:, mid], dstate))
     for cut in (slice(0, front), slice(front + N, None)):
         assert (dv[:, cut] == 0).all() and (dq[:, cut] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what", [(), ("v",), ("q", "v", "dout"), ("dout",), ("k",), ("beta",)], ids=lambda w: "_".join(w) or "alike")
+@pytest.mark.parametrize("shape", [(1, 200, 2, 1, 64), (1, 150, 1, 2, 100)], ids=str)
+def test_gradients_token_by_token(shape, what, dtype):
+    """Inputs alike or over six decades: every token's own gradients are right for their own size (shared heads: dq and dk in sum)."""
+    x = draw(51, *shape, dtype)
+    r = np.random.default_rng(52)
+    for name in what:
+        by = torch.from_numpy(10.0 ** (-6 * r.random(x[name].shape[:3])))
+        x[name] = (x[name].double() * (by if name == "beta" else by[..., None])).to(DT[dtype])
+    got = backward(x, 0.125)
+    for name, y, a in zip(GRADS[:5], db.chunk_form(doubles(x), dtype, 0.125, back=True), got):
+        bound, size = db.token_bound(y, dtype)
+        off = size(f64(a) - y.x)
+        assert (off <= bound).all(), f"{name}: {(off / bound).max():.2f} of what is allowed"
+        assert np.median(bound / size(y.x)) <= 0.05, name
